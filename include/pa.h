@@ -50,7 +50,8 @@ typedef enum pa_status {
 
 typedef enum pa_dtype {
   PA_DTYPE_F32 = 0,
-  PA_DTYPE_BF16 = 1
+  PA_DTYPE_BF16 = 1,
+  PA_DTYPE_FP4 = 2 /* a cache held in 4 bits (see below): copy and compaction calls */
 } pa_dtype;
 
 /* Human-readable name of a status code (static string). */
@@ -101,7 +102,8 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, int32_t num_t
  * check them on the host: a pair naming a block outside the pool is skipped,
  * and overlapping pairs give an undefined result for the blocks involved.
  * pa_copy_blocks_checked reports invalid pairs instead.  num_pairs == 0 is
- * a no-op.
+ * a no-op.  dtype PA_DTYPE_FP4: the pools of the 4-bit cache (also in the
+ * checked and multi-layer calls; a layer stride then counts bytes).
  * ---------------------------------------------------------------------- */
 pa_status pa_copy_blocks(void* k_cache, void* v_cache,
                          int32_t num_blocks, int32_t block_size,
@@ -395,6 +397,129 @@ pa_status pa_prefill(void* out, pa_dtype out_dtype, const void* q, int32_t num_t
                      float scale, int32_t* status, void* stream);
 
 /* ------------------------------------------------------------------------
+ * A K/V cache held in 4 bits -- [PA] "KV Cache 为什么难管理": the cache grows
+ * with every token of every layer and its reads bound decode.  The calls
+ * below keep the block tables, slots and allocator as they are and hold K and
+ * V as e2m1 codes with one e4m3 scale for every 16 values: 4.5 bits a value
+ * against 16, so 3.56 times as many tokens fit and a decode step reads that
+ * much less.
+ *
+ * k_cache and v_cache are byte arrays [num_blocks][num_kv_heads][tile] with
+ * tile = pa_fp4_tile_bytes(block_size, head_dim): block_size rows of
+ * head_dim / 2 code bytes (element 2i in the low nibble of byte i), then
+ * block_size rows of head_dim / 16 scale bytes, then padding to a multiple of
+ * 16 bytes.  With a = max |x| / k over a group of 16 values,
+ *   s    = a / 6 rounded to e4m3 (nearest, ties to even, at most 448)
+ *   code = x / k / s rounded to e2m1 (nearest, ties to even, at most 6)
+ * and the cache stands for code * s * k (exact in bf16); -0 is stored as 0.  k_scale and v_scale,
+ * the k of the K and of the V cache, are powers of two from 2^-32 to 2^32 and
+ * the same in every call on a cache; a group whose largest magnitude lies
+ * between 2^-4 * k and 2688 * k keeps the scale's full precision.  A group
+ * with an infinity or NaN reads back as NaN.
+ *
+ * block_size: a power of two from 1 to 256; head_dim 64, 128 or 256.
+ * ---------------------------------------------------------------------- */
+/* Bytes of one (block, kv head) tile; 0 for unsupported sizes. */
+size_t pa_fp4_tile_bytes(int32_t block_size, int32_t head_dim);
+
+/* pa_reshape_and_cache into a 4-bit cache: key and value are
+ * [num_tokens][num_kv_heads][head_dim] of src_dtype (F32 or BF16).  status
+ * (device int32, caller-zeroed, or NULL) receives PA_ERR_INVALID_ARG if a
+ * slot lies past the pool; such a token is not written, negative slots are
+ * padding. */
+pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, pa_dtype src_dtype,
+                                   int32_t num_tokens, const int64_t* slot_mapping,
+                                   void* k_cache, void* v_cache,
+                                   int32_t num_blocks, int32_t block_size,
+                                   int32_t num_kv_heads, int32_t head_dim,
+                                   float k_scale, float v_scale, int32_t* status, void* stream);
+
+/* The reverse: row t of key and value receives the values held in slot
+ * slot_mapping[t] (F32 or BF16, both exact).  Rows of negative slots, and of
+ * slots past the pool (reported as above), are left as they were. */
+pa_status pa_gather_cache_fp4(void* key, void* value, pa_dtype dst_dtype,
+                              int32_t num_tokens, const int64_t* slot_mapping,
+                              const void* k_cache, const void* v_cache,
+                              int32_t num_blocks, int32_t block_size,
+                              int32_t num_kv_heads, int32_t head_dim,
+                              float k_scale, float v_scale, int32_t* status, void* stream);
+
+/* pa_decode over a 4-bit cache: the attention of bf16 queries over exactly
+ * the values the cache stands for, out F32 or BF16.  Scores, softmax
+ * statistics and the output are accumulated in fp32; the probabilities enter
+ * the second product as f16 (11 bits).  Tables, lengths, zero output for
+ * length 0, workspace rules (256-byte aligned, zero-filled before its first
+ * use, pa_workspace_error for table entries outside the pool and lengths
+ * outside [0, max_context_len]) as for pa_decode.  num_q_heads / num_kv_heads
+ * in {1, 2, 4, 8, 16}. */
+size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t head_dim, int32_t block_size,
+                                    int32_t max_context_len);
+pa_status pa_decode_fp4(void* out, pa_dtype out_dtype,
+                        const void* q, int32_t num_seqs, int32_t num_q_heads,
+                        const void* k_cache, const void* v_cache,
+                        int32_t num_blocks, int32_t block_size,
+                        int32_t num_kv_heads, int32_t head_dim,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* context_lens, int32_t max_context_len,
+                        float scale, float k_scale, float v_scale,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* pa_prefill over a 4-bit cache (head_dim 128, any block size): causal
+ * attention of each sequence's chunk of bf16 queries, rounded as in
+ * pa_decode_fp4.  max_context_len: host, >= every q_start[i] + chunk length
+ * (a longer one is reported in *status and its rows are not written).  The
+ * workspace (256-byte aligned, zero-filled before its first use) holds the
+ * partial results of a long history that is split over CTAs; calls that
+ * overlap on the GPU need workspaces of their own. */
+size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                     int32_t max_context_len);
+pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t num_tokens,
+                         const int32_t* cu_q, const int32_t* q_start, int32_t num_seqs,
+                         int32_t max_q_len, int32_t max_context_len, int32_t num_q_heads,
+                         const void* k_cache, const void* v_cache, int32_t num_blocks,
+                         int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, float scale,
+                         float k_scale, float v_scale, int32_t* status,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Token compaction -- [PA] "Block Table 如何工作": a token's place is its
+ * sequence's block and an offset, so dropping tokens from the middle of a
+ * sequence (rejected drafts, evicted history) means moving the kept ones
+ * forward before the emptied blocks can return to the pool.
+ *
+ * For sequence i and j < cu_keep[i+1] - cu_keep[i], in every layer and head of
+ * both caches, the token at position dst_start[i] + j of the sequence becomes
+ * the one that was at position keep[cu_keep[i] + j].  The kept positions of a
+ * sequence ascend strictly and keep[cu_keep[i] + j] >= dst_start[i] + j
+ * (positions before dst_start[i] stay).  Nothing behind the last kept token
+ * is written.
+ *   dtype              F32, BF16 or FP4; layers as in pa_copy_blocks_layers
+ *                      (FP4: cache_layer_stride counts bytes)
+ *   block_tables       device, int32 [num_seqs][max_blocks_per_seq]
+ *   dst_start          device, int32 [num_seqs]
+ *   keep, cu_keep      device, int32 [cu_keep[num_seqs]], [num_seqs + 1]
+ *   max_keep           host, >= every sequence's count
+ *   status             device int32, caller-zeroed, or NULL: receives
+ *                      PA_ERR_INVALID_ARG for positions that do not ascend,
+ *                      lie before their destination or past the table, for a
+ *                      table entry outside the pool (such a token is not
+ *                      moved) and for a count outside [0, max_keep] (such a
+ *                      sequence is left alone)
+ * Blocks that are written must belong to one sequence only
+ * (pa_alloc_make_writable); afterwards pa_alloc_truncate frees the rest.
+ * ---------------------------------------------------------------------- */
+pa_status pa_compact_tokens(void* k_cache, void* v_cache, int64_t cache_layer_stride,
+                            int32_t num_layers, int32_t num_blocks, int32_t block_size,
+                            int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* dst_start, const int32_t* keep,
+                            const int32_t* cu_keep, int32_t num_seqs, int32_t max_keep,
+                            int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------
  * Host block allocator -- [vLLM2] block-table section and [KV02] section 2:
  * fixed-size blocks handed out on demand from anywhere in the pool; [PA]
  * "Block Table 如何工作": full blocks trigger a new allocation, freed blocks
@@ -446,6 +571,21 @@ pa_status pa_alloc_append_slots(pa_allocator* a, const int32_t* seqs, int32_t n,
  * fill); slots[0..n) receive the slots.  PA_ERR_INVALID_ARG if a copy would
  * be needed.  On PA_ERR_OOM nothing changes. */
 pa_status pa_alloc_append_tokens(pa_allocator* a, int32_t seq, int32_t n, int64_t* slots);
+/* Make positions [from, upto) of `seq` writable in place: every block of that
+ * range that is shared (count > 1) is replaced in the table by a fresh one and
+ * (old, new) is appended to cow_pairs ([cap][2], int64), counted in *num_cow;
+ * the caller copies those blocks before writing.  With prefix caching the
+ * range's blocks give up their keys and the sequence is no longer keyed (its
+ * contents will no longer be those of its token ids).  PA_ERR_INVALID_ARG for
+ * a range outside [0, length] or cap below the pairs needed, PA_ERR_OOM without
+ * enough free blocks; either leaves the state unchanged. */
+pa_status pa_alloc_make_writable(pa_allocator* a, int32_t seq, int32_t from, int32_t upto,
+                                 int64_t* cow_pairs, int32_t cap, int32_t* num_cow);
+/* Shorten `seq` to its first new_len tokens and release the blocks behind
+ * them (in table order; last block first when prefix caching is on).  A
+ * tracked sequence stays tracked.  PA_ERR_INVALID_ARG unless
+ * 0 <= new_len <= length. */
+pa_status pa_alloc_truncate(pa_allocator* a, int32_t seq, int32_t new_len);
 /* Release every block of `seq` in table order (last block first when
  * prefix caching is on); the id becomes invalid. */
 pa_status pa_alloc_free_seq(pa_allocator* a, int32_t seq);

@@ -22,9 +22,11 @@ PA_ERR_DEVICE_TIMEOUT = 6
 
 PA_DTYPE_F32 = 0
 PA_DTYPE_BF16 = 1
+PA_DTYPE_FP4 = 2
 
 i32 = C.c_int32
 i64 = C.c_int64
+f32 = C.c_float
 vp = C.c_void_p
 P_i32 = C.POINTER(C.c_int32)
 P_i64 = C.POINTER(C.c_int64)
@@ -56,6 +58,17 @@ SIGNATURES = {
     "pa_workspace_init": (i32, [vp, C.c_size_t, vp]),
     "pa_test_stall_decode": (None, [C.c_uint64]),
     "pa_workspace_error": (i32, [vp, vp, P_i32]),
+    "pa_fp4_tile_bytes": (C.c_size_t, [i32, i32]),
+    "pa_reshape_and_cache_fp4": (i32, [vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp]),
+    "pa_gather_cache_fp4": (i32, [vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp]),
+    "pa_decode_fp4_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32]),
+    "pa_decode_fp4": (i32, [vp, i32, vp, i32, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, f32, f32, f32,
+                            vp, C.c_size_t, vp]),
+    "pa_prefill_fp4_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+    "pa_prefill_fp4": (i32, [vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, i32,
+                             f32, f32, f32, vp, vp, C.c_size_t, vp]),
+    "pa_compact_tokens": (i32, [vp, vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, i32, vp,
+                                vp]),
     "pa_alloc_create": (i32, [i32, i32, P_i32, C.POINTER(vp)]),
     "pa_alloc_destroy": (None, [vp]),
     "pa_alloc_num_blocks": (i32, [vp]),
@@ -70,6 +83,8 @@ SIGNATURES = {
     "pa_alloc_append_slot": (i32, [vp, i32, P_i64, P_i32, P_i32]),
     "pa_alloc_append_slots": (i32, [vp, P_i32, i32, P_i64, P_i64, P_i32, P_i32]),
     "pa_alloc_append_tokens": (i32, [vp, i32, i32, P_i64]),
+    "pa_alloc_make_writable": (i32, [vp, i32, i32, i32, P_i64, i32, P_i32]),
+    "pa_alloc_truncate": (i32, [vp, i32, i32]),
     "pa_alloc_free_seq": (i32, [vp, i32]),
     "pa_alloc_seq_len": (i32, [vp, i32]),
     "pa_alloc_num_seqs": (i32, [vp]),

@@ -410,18 +410,22 @@ pa_status copy_blocks_impl(void* k_cache, void* v_cache, int64_t cache_layer_str
                                 int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
                                 const int64_t* block_pairs, int32_t num_pairs, int32_t* status,
                                 void* stream) {
-  pa_status st = check_cache_shape(num_blocks, block_size, num_kv_heads, head_dim, dtype);
+  const bool fp4 = dtype == PA_DTYPE_FP4;  // 4-bit pools: tiles of bytes
+  pa_status st = check_cache_shape(num_blocks, block_size, num_kv_heads, head_dim, fp4 ? PA_DTYPE_BF16 : dtype);
+  if (st == PA_OK && fp4 && pa_fp4_tile_bytes(block_size, head_dim) == 0) st = PA_ERR_UNSUPPORTED;
   if (st != PA_OK) return st;
   if (num_pairs < 0 || num_layers < 1 || num_layers > kMaxLayers) return PA_ERR_INVALID_ARG;
-  const int64_t e = dtype_bytes(dtype);
-  const int64_t cache_layer = static_cast<int64_t>(num_blocks) * num_kv_heads * block_size * head_dim;
+  const int64_t e = fp4 ? 1 : dtype_bytes(dtype);
+  const int64_t tile = fp4 ? static_cast<int64_t>(pa_fp4_tile_bytes(block_size, head_dim))
+                           : static_cast<int64_t>(block_size) * head_dim;  // elements, 4-bit: bytes
+  const int64_t cache_layer = static_cast<int64_t>(num_blocks) * num_kv_heads * tile;
   if (num_layers > 1 && (cache_layer_stride < cache_layer || (cache_layer_stride * e) % 16 != 0))
     return PA_ERR_INVALID_ARG;
   if (num_pairs == 0) return PA_OK;
   if (!k_cache || !v_cache || !block_pairs) return PA_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
   if (status && !aligned4(status)) return PA_ERR_INVALID_ARG;
-  const int64_t block_bytes = static_cast<int64_t>(num_kv_heads) * block_size * head_dim * e;
+  const int64_t block_bytes = static_cast<int64_t>(num_kv_heads) * tile * e;
   cudaError_t err = pa::launch_copy_blocks(k_cache, v_cache,
                                            num_layers > 1 ? cache_layer_stride * e : 0, num_layers,
                                            num_blocks, block_bytes, block_pairs, num_pairs, status,

@@ -194,6 +194,64 @@ class BlockAllocator {
     return PA_OK;
   }
 
+  // Fresh blocks in the place of the shared ones that hold positions
+  // [from, upto) (see pa_alloc_make_writable).
+  pa_status make_writable(int32_t s, int32_t from, int32_t upto, int64_t* pairs, int32_t cap, int32_t* n) {
+    Seq* q = find(s);
+    if (!q || from < 0 || upto < from || upto > q->len) return PA_ERR_INVALID_ARG;
+    if (from == upto) return PA_OK;
+    const int32_t first = from / block_size_, last = (upto - 1) / block_size_;
+    int32_t shared = 0;
+    for (int32_t j = first; j <= last; ++j) shared += ref_[q->table[j]] > 1;
+    if (shared > cap || (shared > 0 && !pairs)) return PA_ERR_INVALID_ARG;
+    if (shared > static_cast<int32_t>(free_.size())) return PA_ERR_OOM;
+    for (int32_t j = first; j <= last; ++j) {
+      const int32_t b = q->table[j];
+      if (ref_[b] > 1) {
+        const int32_t nb = allocate();
+        --ref_[b];
+        q->table[j] = nb;
+        pairs[2 * static_cast<int64_t>(*n)] = b;
+        pairs[2 * static_cast<int64_t>(*n) + 1] = nb;
+        ++*n;
+      } else if (pc_) {
+        drop_key(b);
+      }
+    }
+    q->track = false;
+    q->tokens.clear();
+    return PA_OK;
+  }
+
+  pa_status truncate(int32_t s, int32_t new_len) {
+    Seq* q = find(s);
+    if (!q || new_len < 0 || new_len > q->len) return PA_ERR_INVALID_ARG;
+    const size_t keep = (static_cast<size_t>(new_len) + block_size_ - 1) / block_size_;
+    if (pc_) {
+      for (size_t j = q->table.size(); j > keep; --j)
+        if (--ref_[q->table[j - 1]] == 0) push_free(q->table[j - 1]);
+    } else {
+      for (size_t j = keep; j < q->table.size(); ++j)
+        if (--ref_[q->table[j]] == 0) push_free(q->table[j]);
+    }
+    q->table.resize(keep);
+    q->len = new_len;
+    if (q->track) {
+      q->tokens.resize(static_cast<size_t>(new_len));
+      const int32_t full = new_len / block_size_;
+      if (q->keyed > full) {  // the last key is that of the new last full block
+        q->keyed = full;
+        for (int32_t j = 0; j < full; ++j)
+          q->last_key = key_of(j ? &q->last_key : nullptr,
+                               q->tokens.data() + static_cast<int64_t>(j) * block_size_, q->extra);
+      }
+    }
+    // a block that is no longer full will be filled with other tokens: no key
+    // may go on standing for it
+    if (pc_ && new_len % block_size_ != 0) drop_key(q->table[keep - 1]);
+    return PA_OK;
+  }
+
   // ---- prefix caching ----
   pa_status enable_prefix_cache() {
     if (pc_) return PA_OK;
@@ -282,6 +340,11 @@ class BlockAllocator {
     free_.push_back(b);
     where_[b] = std::prev(free_.end());
     in_free_[b] = 1;
+  }
+  void drop_key(int32_t b) {
+    if (!keyed_[b]) return;
+    cached_.erase(key_[b]);
+    keyed_[b] = 0;
   }
   void take_free(int32_t b) {
     free_.erase(where_[b]);
@@ -442,6 +505,17 @@ pa_status pa_alloc_append_slots(pa_allocator* a, const int32_t* seqs, int32_t n,
 pa_status pa_alloc_append_tokens(pa_allocator* a, int32_t seq, int32_t n, int64_t* slots) {
   if (!a || n < 0 || (n > 0 && !slots)) return PA_ERR_INVALID_ARG;
   return a->impl.append_tokens(seq, n, slots);
+}
+
+pa_status pa_alloc_make_writable(pa_allocator* a, int32_t seq, int32_t from, int32_t upto,
+                                 int64_t* cow_pairs, int32_t cap, int32_t* num_cow) {
+  if (num_cow) *num_cow = 0;
+  if (!a || !num_cow || cap < 0) return PA_ERR_INVALID_ARG;
+  return a->impl.make_writable(seq, from, upto, cow_pairs, cap, num_cow);
+}
+
+pa_status pa_alloc_truncate(pa_allocator* a, int32_t seq, int32_t new_len) {
+  return a ? a->impl.truncate(seq, new_len) : PA_ERR_INVALID_ARG;
 }
 
 pa_status pa_alloc_free_seq(pa_allocator* a, int32_t seq) {

@@ -1,0 +1,165 @@
+// The 4-bit K/V page format and the internal interface of its kernels.
+//
+// A row of head_dim values is cut into groups of 16.  With k the call's global
+// scale (a power of two) and a = max |x| / k over a group,
+//   s    = a / 6 rounded to e4m3 (nearest even, at most 448)    one byte
+//   code = x / k / s rounded to e2m1 (nearest even, at most 6)  four bits
+//   the value read back is code * s * k.
+// code has 2 significant bits and s has 4, so code * s has at most 6: it is
+// exact in bf16 and in f16 (at most 6 * 448, at least 2^-10), and the
+// attention kernels multiply exactly the stored values.  A group with a
+// non-finite element gets the NaN scale: it reads back as NaN.
+//
+// A (block, kv head) tile is one run of bytes: block_size rows of D / 2 code
+// bytes (element 2i in the low nibble of byte i), block_size rows of D / 16
+// scale bytes, padding up to a multiple of 16 bytes.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace pa {
+
+constexpr int kFp4Group = 16;
+
+inline __host__ __device__ int64_t fp4_tile_bytes(int bs, int d) {
+  return (static_cast<int64_t>(bs) * (d / 2 + d / kFp4Group) + 15) & ~static_cast<int64_t>(15);
+}
+
+struct Fp4AttnParams {
+  void* out;
+  const void* q;  // bf16
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;  // decode
+  const int32_t* cu_q;          // prefill
+  const int32_t* q_start;
+  int32_t num_seqs, num_q_heads, num_kv_heads, num_blocks, block_size, max_blocks_per_seq;
+  int32_t max_context_len;
+  int32_t num_tokens, max_q_len;  // prefill
+  int32_t out_bf16;
+  float scale_log2;  // softmax scale * log2(e) * k_scale
+  float v_scale;
+  int32_t* err;      // device error word (may be null in prefill)
+  unsigned char* ws;
+};
+
+cudaError_t launch_fp4_append(const void* key, const void* value, bool src_bf16, int32_t num_tokens,
+                              const int64_t* slots, void* k_cache, void* v_cache, int32_t num_blocks,
+                              int32_t block_size, int32_t num_kv_heads, int32_t head_dim, float k_scale,
+                              float v_scale, int32_t* status, cudaStream_t stream);
+cudaError_t launch_fp4_gather(void* key, void* value, bool dst_bf16, int32_t num_tokens, const int64_t* slots,
+                              const void* k_cache, const void* v_cache, int32_t num_blocks, int32_t block_size,
+                              int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale, int32_t* status,
+                              cudaStream_t stream);
+cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream);
+
+struct CompactParams {
+  unsigned char* k_cache;
+  unsigned char* v_cache;
+  int64_t layer_bytes;
+  const int32_t* block_tables;
+  const int32_t* dst_start;
+  const int32_t* keep;
+  const int32_t* cu_keep;
+  int32_t* status;
+  int32_t num_layers, num_blocks, block_size, num_kv_heads, max_blocks_per_seq, num_seqs, max_keep;
+  int32_t row_bytes;    // one token's row of one head (4-bit pages: its codes)
+  int32_t scale_bytes;  // 4-bit pages: its scales, else 0
+  int64_t tile_bytes;
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+#ifdef __CUDACC__
+namespace fp4 {
+
+// 8 codes of a word -> four f16 pairs (element 2i in the low half)
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// two e4m3 scales -> f16 pair (low byte in the low half)
+__device__ __forceinline__ uint32_t scales_to_f16(uint32_t two) {
+  uint32_t r;
+  const uint16_t v = static_cast<uint16_t>(two);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// both halves of a f16 pair as floats
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t v) {
+  float2 r;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float scale_to_f32(uint32_t byte) { return f16x2_to_f32(scales_to_f16(byte)).x; }
+
+// x (>= 0) to the nearest e4m3, ties to even, at most 448
+__device__ __forceinline__ uint32_t to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  return r & 0xffu;
+}
+// (lo, hi) to the nearest e2m1, ties to even, at most 6: lo in the low nibble
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 fp32 values, already divided by the global scale -> 8 code bytes and
+// the scale byte.  `top` is the largest |x| bit pattern before that division.
+__device__ __forceinline__ void quantise16(const float (&x)[16], uint32_t top, uint2& codes, uint32_t& scale) {
+  if (top >= 0x7f800000u) {  // infinity or NaN among them: the group reads back as NaN
+    codes = make_uint2(0, 0);
+    scale = 0x7fu;
+    return;
+  }
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]));
+  // the correctly rounded quotient cannot cross a rounding border of the
+  // target: 6 * border has few bits, so a / 6 != border differs from it by
+  // more than half an fp32 step
+  scale = to_e4m3(__fdiv_rn(a, 6.f));
+  const float s = scale_to_f32(scale);
+  const float r = scale ? __frcp_rn(s) : 0.f;
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // x / s, correctly rounded (the product by the rounded reciprocal and
+      // one exact-remainder step); past 1e6 the scale is at its largest and
+      // the code at 6, whatever the value
+      const float v = fminf(fmaxf(x[2 * i + e], -1e6f), 1e6f);
+      const float q = v * r;
+      t[e] = fmaf(fmaf(-q, s, v), r, q);
+    }
+    b[i] = to_e2m1x2(t[0], t[1]);
+  }
+  codes.x = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+  codes.y = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+}
+
+}  // namespace fp4
+#endif
+
+}  // namespace pa

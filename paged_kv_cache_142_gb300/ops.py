@@ -19,6 +19,7 @@ _LIB = L.load()
 
 PA_DTYPE_F32 = L.PA_DTYPE_F32
 PA_DTYPE_BF16 = L.PA_DTYPE_BF16
+PA_DTYPE_FP4 = L.PA_DTYPE_FP4
 PAError = L.PAError
 
 
@@ -59,6 +60,36 @@ def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor):
     return k_cache.shape
 
 
+def _fp4_dims(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size, head_dim):
+    """(NB, Hkv) of 4-bit caches [NB, Hkv, tile]."""
+    _need(block_size is not None and head_dim is not None, "4-bit caches need block_size and head_dim")
+    tile = fp4_tile_bytes(block_size, head_dim)
+    for c in (k_cache, v_cache):
+        _need(c.dtype == torch.uint8 and c.is_cuda, "4-bit caches must be CUDA uint8 tensors")
+        _need(c.dim() == 3 and c.shape[2] == tile and c.is_contiguous(),
+              f"4-bit caches must be contiguous [NB, Hkv, {tile}] for block_size {block_size}, head_dim {head_dim}")
+    _need(k_cache.shape == v_cache.shape, "K and V caches must share a shape")
+    _on_current_device(k_cache, v_cache)
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def _any_cache_dims(k_cache, v_cache, block_size, head_dim):
+    """(NB, Hkv, bs, D, dtype code) of caches of any dtype."""
+    if k_cache.dtype == torch.uint8:
+        return (*_fp4_dims(k_cache, v_cache, block_size, head_dim), int(block_size), int(head_dim), PA_DTYPE_FP4)
+    return (*_cache_dims(k_cache, v_cache), dtype_code(k_cache.dtype))
+
+
+def _any_layer_cache_dims(k_cache, v_cache, block_size, head_dim):
+    """(L, NB, Hkv, bs, D, dtype code) of multi-layer caches of any dtype."""
+    if k_cache.dtype == torch.uint8:
+        _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.stride(0) == v_cache.stride(0),
+              "4-bit caches must be [L, NB, Hkv, tile] with one layer stride for K and V")
+        nb, hkv = _fp4_dims(k_cache[0], v_cache[0], block_size, head_dim)
+        return k_cache.shape[0], nb, hkv, int(block_size), int(head_dim), PA_DTYPE_FP4
+    return (*_layer_cache_dims(k_cache, v_cache), dtype_code(k_cache.dtype))
+
+
 # --------------------------------------------------------------------------
 # device calls
 # --------------------------------------------------------------------------
@@ -88,12 +119,14 @@ def pa_reshape_and_cache(key, value, slot_mapping, k_cache, v_cache, stream=None
             "pa_reshape_and_cache")
 
 
-def pa_copy_blocks(k_cache, v_cache, block_pairs, stream=None, status=None) -> None:
+def pa_copy_blocks(k_cache, v_cache, block_pairs, stream=None, status=None, block_size=None,
+                   head_dim=None) -> None:
     """cache[dst] = cache[src] for every row (src, dst) of ``block_pairs``.
     ``status`` (a zeroed CUDA int32 tensor): the checked call, which validates
     the pairs first and copies nothing if any is invalid
-    (pa_copy_blocks_checked)."""
-    NB, Hkv, bs, D = _cache_dims(k_cache, v_cache)
+    (pa_copy_blocks_checked).  4-bit caches (uint8): give ``block_size`` and
+    ``head_dim``."""
+    NB, Hkv, bs, D, dt = _any_cache_dims(k_cache, v_cache, block_size, head_dim)
     _on_current_device(block_pairs, status)
     n = block_pairs.shape[0] if block_pairs.numel() else 0
     if n:
@@ -103,12 +136,12 @@ def pa_copy_blocks(k_cache, v_cache, block_pairs, stream=None, status=None) -> N
         _need(status.dtype == torch.int32 and status.is_cuda and status.numel() >= 1,
               "status must be a CUDA int32 tensor")
         L.check(_LIB.pa_copy_blocks_checked(k_cache.data_ptr(), v_cache.data_ptr(), NB, bs, Hkv, D,
-                                            dtype_code(k_cache.dtype), block_pairs.data_ptr() if n else None,
+                                            dt, block_pairs.data_ptr() if n else None,
                                             n, status.data_ptr(), _stream(stream)),
                 "pa_copy_blocks_checked")
         return
     L.check(_LIB.pa_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), NB, bs, Hkv, D,
-                                dtype_code(k_cache.dtype), block_pairs.data_ptr() if n else None, n,
+                                dt, block_pairs.data_ptr() if n else None, n,
                                 _stream(stream)),
             "pa_copy_blocks")
 
@@ -141,16 +174,18 @@ def pa_reshape_and_cache_layers(key, value, slot_mapping, k_cache, v_cache, stre
         dtype_code(k_cache.dtype), _stream(stream)), "pa_reshape_and_cache_layers")
 
 
-def pa_copy_blocks_layers(k_cache, v_cache, block_pairs, stream=None) -> None:
-    """cache[l, dst] = cache[l, src] for every layer l and row (src, dst) of ``block_pairs``."""
-    Lyr, NB, Hkv, bs, D = _layer_cache_dims(k_cache, v_cache)
+def pa_copy_blocks_layers(k_cache, v_cache, block_pairs, stream=None, block_size=None, head_dim=None) -> None:
+    """cache[l, dst] = cache[l, src] for every layer l and row (src, dst) of
+    ``block_pairs``.  4-bit caches ``[L, NB, Hkv, tile]``: give ``block_size``
+    and ``head_dim``."""
+    Lyr, NB, Hkv, bs, D, dt = _any_layer_cache_dims(k_cache, v_cache, block_size, head_dim)
     _on_current_device(k_cache, v_cache, block_pairs)
     n = block_pairs.shape[0] if block_pairs.numel() else 0
     if n:
         _need(block_pairs.dtype == torch.int64 and block_pairs.is_cuda and block_pairs.is_contiguous()
               and block_pairs.shape == (n, 2), "block_pairs must be a contiguous CUDA int64 [n, 2]")
     L.check(_LIB.pa_copy_blocks_layers(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), Lyr,
-                                       NB, bs, Hkv, D, dtype_code(k_cache.dtype),
+                                       NB, bs, Hkv, D, dt,
                                        block_pairs.data_ptr() if n else None, n, _stream(stream)),
             "pa_copy_blocks_layers")
 
@@ -309,6 +344,170 @@ def pa_workspace_error(workspace, stream=None) -> int:
 
 
 # --------------------------------------------------------------------------
+# a cache held in 4 bits, and token compaction
+# --------------------------------------------------------------------------
+def _i32(t, numel, what):
+    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == numel,
+          f"{what} must be a contiguous CUDA int32 tensor of {numel} entries")
+
+
+def _status_ptr(status):
+    if status is None:
+        return None
+    _need(status.dtype == torch.int32 and status.is_cuda and status.numel() >= 1, "status must be a CUDA int32 tensor")
+    return status.data_ptr()
+
+
+def fp4_tile_bytes(block_size, head_dim) -> int:
+    """Bytes of one (block, kv head) tile of a 4-bit cache."""
+    n = _LIB.pa_fp4_tile_bytes(int(block_size), int(head_dim))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_fp4_tile_bytes")
+    return int(n)
+
+
+def make_cache_fp4(num_blocks, num_kv_heads, block_size, head_dim, num_layers=None, device="cuda") -> torch.Tensor:
+    """A zeroed 4-bit K or V cache ``[NB, Hkv, tile]`` (``[L, NB, Hkv, tile]`` with layers)."""
+    shape = (num_blocks, num_kv_heads, fp4_tile_bytes(block_size, head_dim))
+    return torch.zeros(shape if num_layers is None else (num_layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size):
+    _need(key.dim() == 3 and value.shape == key.shape and value.dtype == key.dtype, "key/value must be [T, Hkv, D]")
+    T, Hkv, D = key.shape
+    NB, cache_heads = _fp4_dims(k_cache, v_cache, block_size, D)
+    _need(Hkv == cache_heads, "num_kv_heads does not match the cache")
+    _need(key.is_cuda and value.is_cuda and key.is_contiguous() and value.is_contiguous(),
+          "key/value must be contiguous CUDA tensors")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T and slot_mapping.is_cuda
+          and slot_mapping.is_contiguous(), "slot_mapping must be a contiguous CUDA int64 tensor of num_tokens entries")
+    _on_current_device(key, value, slot_mapping)
+    return T, NB, Hkv, D
+
+
+def pa_reshape_and_cache_fp4(key, value, slot_mapping, k_cache, v_cache, block_size, k_scale=1.0, v_scale=1.0,
+                             stream=None, status=None) -> None:
+    """Quantise key/value ``[T, Hkv, D]`` (fp32 or bf16) into the slots
+    ``slot_mapping[T]`` of the 4-bit caches."""
+    T, NB, Hkv, D = _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size)
+    _on_current_device(status)
+    L.check(_LIB.pa_reshape_and_cache_fp4(
+        key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
+        _stream(stream)), "pa_reshape_and_cache_fp4")
+
+
+def pa_gather_cache_fp4(key, value, slot_mapping, k_cache, v_cache, block_size, k_scale=1.0, v_scale=1.0,
+                        stream=None, status=None) -> None:
+    """Fill key/value ``[T, Hkv, D]`` (fp32 or bf16) with the values held in
+    the slots ``slot_mapping[T]``; rows of negative slots stay as they are."""
+    T, NB, Hkv, D = _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size)
+    _on_current_device(status)
+    L.check(_LIB.pa_gather_cache_fp4(
+        key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
+        _stream(stream)), "pa_gather_cache_fp4")
+
+
+def pa_decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
+    n = _LIB.pa_decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                          int(max_context_len))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_decode_fp4_workspace_size")
+    return int(n)
+
+
+def make_workspace_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                       device="cuda") -> torch.Tensor:
+    """A zero-filled pa_decode_fp4 workspace of the required size."""
+    n = pa_decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _fp4_queries(out, q, k_cache, v_cache, block_tables, num_seqs, num_kv_heads, block_size, workspace):
+    _need(q.dim() == 3 and q.dtype == torch.bfloat16 and q.is_cuda and q.is_contiguous(),
+          "q must be a contiguous CUDA bf16 tensor [rows, H, D]")
+    NB, Hkv = _fp4_dims(k_cache, v_cache, block_size, q.shape[2])
+    _need(Hkv == num_kv_heads, "num_kv_heads does not match the cache")
+    _need(out.shape == q.shape and out.is_cuda and out.is_contiguous()
+          and out.dtype in (torch.float32, torch.bfloat16), "out must be a contiguous fp32 or bf16 tensor of q's shape")
+    _need(block_tables.dtype == torch.int32 and block_tables.is_cuda and block_tables.dim() == 2
+          and block_tables.shape[0] == num_seqs and block_tables.is_contiguous(),
+          "block_tables must be contiguous int32 [num_seqs, max_blocks]")
+    _need(workspace.dtype == torch.uint8 and workspace.is_cuda, "workspace must be a CUDA uint8 tensor")
+    _on_current_device(out, q, block_tables, workspace)
+    return NB
+
+
+def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, block_size,
+                  max_context_len, workspace, k_scale=1.0, v_scale=1.0, stream=None) -> None:
+    """out[B, H, D] = paged decode attention of q[B, H, D] (bf16) over the 4-bit caches."""
+    B, H, D = q.shape
+    NB = _fp4_queries(out, q, k_cache, v_cache, block_tables, B, num_kv_heads, block_size, workspace)
+    _i32(context_lens, B, "context_lens")
+    _on_current_device(context_lens)
+    L.check(_LIB.pa_decode_fp4(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), B, H, k_cache.data_ptr(), v_cache.data_ptr(), NB,
+        int(block_size), num_kv_heads, D, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+        int(max_context_len), float(scale), float(k_scale), float(v_scale), workspace.data_ptr(), workspace.numel(),
+        _stream(stream)), "pa_decode_fp4")
+
+
+def make_prefill_workspace_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
+                               max_context_len, device="cuda") -> torch.Tensor:
+    """A zero-filled pa_prefill_fp4 workspace of the required size."""
+    n = _LIB.pa_prefill_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, int(max_q_len),
+                                           int(max_context_len))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_prefill_fp4_workspace_size")
+    return torch.zeros(int(n), dtype=torch.uint8, device=device)
+
+
+def pa_prefill_fp4(out, q, k_cache, v_cache, cu_q, q_start, block_tables, scale, num_kv_heads, block_size,
+                   max_q_len, max_context_len, workspace, k_scale=1.0, v_scale=1.0, status=None, stream=None) -> None:
+    """Causal paged attention of each sequence's chunk ``q[cu_q[i]:cu_q[i+1]]``
+    (bf16, positions from ``q_start[i]``) over the 4-bit caches."""
+    T, H, D = q.shape
+    S = cu_q.numel() - 1
+    _i32(cu_q, S + 1, "cu_q")
+    _i32(q_start, S, "q_start")
+    NB = _fp4_queries(out, q, k_cache, v_cache, block_tables, S, num_kv_heads, block_size, workspace)
+    _on_current_device(cu_q, q_start, status)
+    L.check(_LIB.pa_prefill_fp4(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), T, cu_q.data_ptr(), q_start.data_ptr(), S,
+        int(max_q_len), int(max_context_len), H, k_cache.data_ptr(), v_cache.data_ptr(), NB, int(block_size),
+        num_kv_heads, D, block_tables.data_ptr(), block_tables.shape[1], float(scale), float(k_scale),
+        float(v_scale), _status_ptr(status), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        "pa_prefill_fp4")
+
+
+def pa_compact_tokens(k_cache, v_cache, block_tables, dst_start, keep, cu_keep, max_keep, block_size=None,
+                      head_dim=None, status=None, stream=None) -> None:
+    """Move each sequence's kept tokens ``keep[cu_keep[i]:cu_keep[i+1]]``
+    (ascending positions) to positions ``dst_start[i]``, ``dst_start[i] + 1``,
+    ...  Caches of one layer or with a leading layer dimension; 4-bit caches
+    (uint8): give ``block_size`` and ``head_dim``."""
+    layered = k_cache.dim() == (4 if k_cache.dtype == torch.uint8 else 5)
+    if layered:
+        Lyr, NB, Hkv, bs, D, dt = _any_layer_cache_dims(k_cache, v_cache, block_size, head_dim)
+    else:
+        Lyr = 1
+        NB, Hkv, bs, D, dt = _any_cache_dims(k_cache, v_cache, block_size, head_dim)
+    S = dst_start.numel()
+    _i32(dst_start, S, "dst_start")
+    _i32(cu_keep, S + 1, "cu_keep")
+    _i32(keep, keep.numel(), "keep")
+    _need(block_tables.dtype == torch.int32 and block_tables.is_cuda and block_tables.dim() == 2
+          and block_tables.shape[0] == S and block_tables.is_contiguous(),
+          "block_tables must be contiguous int32 [num_seqs, max_blocks]")
+    _on_current_device(k_cache, v_cache, block_tables, dst_start, keep, cu_keep, status)
+    L.check(_LIB.pa_compact_tokens(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0) if layered else 0, Lyr, NB, bs, Hkv, D, dt,
+        block_tables.data_ptr(), block_tables.shape[1], dst_start.data_ptr(), keep.data_ptr(), cu_keep.data_ptr(), S,
+        min(int(max_keep), keep.numel()), _status_ptr(status), _stream(stream)), "pa_compact_tokens")
+
+
+# --------------------------------------------------------------------------
 # host allocator
 # --------------------------------------------------------------------------
 def _p32(a: np.ndarray):
@@ -421,6 +620,20 @@ class BlockAllocator:
         slots = np.empty(max(n, 1), dtype=np.int64)
         _acheck(_LIB.pa_alloc_append_tokens(self._h, seq, n, _p64(slots)), "pa_alloc_append_tokens")
         return slots[:n]
+
+    def make_writable(self, seq: int, start: int, stop: int) -> np.ndarray:
+        """Positions [start, stop) of ``seq`` made writable in place; returns the
+        copy-on-write pairs int64 [k, 2] to copy before they are written."""
+        cap = max(0, int(stop) - int(start)) // max(1, self.block_size) + 2
+        pairs = np.empty((cap, 2), dtype=np.int64)
+        n = C.c_int32(0)
+        _acheck(_LIB.pa_alloc_make_writable(self._h, seq, int(start), int(stop), _p64(pairs), cap, C.byref(n)),
+                "pa_alloc_make_writable")
+        return pairs[:n.value].copy()
+
+    def truncate(self, seq: int, new_len: int) -> None:
+        """Keep the first ``new_len`` tokens of ``seq`` and release the blocks behind them."""
+        L.check(_LIB.pa_alloc_truncate(self._h, seq, int(new_len)), "pa_alloc_truncate")
 
     def free_seq(self, seq: int) -> None:
         L.check(_LIB.pa_alloc_free_seq(self._h, seq), "pa_alloc_free_seq")
