@@ -88,7 +88,7 @@ size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32
       check_pool(1, block_size, num_kv_heads, head_dim) != PA_OK || num_q_heads % num_kv_heads ||
       !group_ok(num_q_heads, num_kv_heads))
     return 0;
-  return 256;
+  return pa::fp4_decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim);
 }
 
 pa_status pa_decode_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t num_seqs, int32_t num_q_heads,

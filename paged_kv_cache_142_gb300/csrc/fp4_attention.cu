@@ -112,17 +112,6 @@ __device__ void attend(const Fp4AttnParams& p, int64_t row, int head, const int3
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) fp4_decode_kernel(const Fp4AttnParams p) {
-  const int seq = blockIdx.x / p.num_q_heads, head = blockIdx.x % p.num_q_heads;
-  int len = p.context_lens[seq];
-  if (len < 0 || len > p.max_context_len) {
-    if (threadIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
-    len = len < 0 ? 0 : p.max_context_len;
-  }
-  attend<D>(p, seq, head, p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq, len);
-}
-
 __global__ void __launch_bounds__(kThreads) fp4_prefill_kernel(const Fp4AttnParams p) {
   const int head = blockIdx.x % p.num_q_heads;
   const int j = blockIdx.x / p.num_q_heads, seq = blockIdx.y;
@@ -138,14 +127,6 @@ __global__ void __launch_bounds__(kThreads) fp4_prefill_kernel(const Fp4AttnPara
 }
 
 }  // namespace
-
-cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(p.num_seqs) * static_cast<unsigned>(p.num_q_heads);
-  if (head_dim == 64) fp4_decode_kernel<64><<<grid, kThreads, 0, stream>>>(p);
-  else if (head_dim == 128) fp4_decode_kernel<128><<<grid, kThreads, 0, stream>>>(p);
-  else fp4_decode_kernel<256><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.max_q_len) * static_cast<unsigned>(p.num_q_heads),

@@ -1,0 +1,801 @@
+// Decode attention over the 4-bit K/V pages (the format: fp4.cuh).
+//
+// For every (sequence, kv head), with its G query heads,
+//   S[t][h] = scale q[h].K[t],  O[h] = sum_t softmax_t(S)[t][h] V[t].
+// A token costs 9/16 byte an element where bf16 costs 2, so the memory leaves
+// an SM about 780 clocks for 128 tokens of one kv head (K and V, D = 128), and
+// what bounds the kernel next is the instructions that turn codes into
+// operands: 2 per 2 elements (cvt e2m1x2 -> f16x2, times the scale).  Hence:
+//  * the products run on mma.sync m16n8k16 (f16 in, fp32 out), whose operands
+//    come from registers: a converted value goes straight into the instruction
+//    that uses it, and never to shared or tensor memory.  Both products put
+//    the cache on the 16-row side and the heads on the 8-column side,
+//      S^T[16 tokens x 8 heads]  = K[16 x D] . Q^T
+//      O^T[16 dims x 8 heads]   += V^T[16 x 16 tokens] . P^T,
+//    so with G = 4 half of the columns are idle, not three quarters;
+//  * the indices a product sums over may come in any order.  In Q.K^T a thread
+//    takes D / 4 consecutive dims of a token (one 16-byte load for D = 128);
+//    in P.V it takes D / 8 consecutive dims of four tokens, and two tokens'
+//    nibbles are interleaved before the conversion, which then yields the
+//    (token, token') pairs that the instruction wants;
+//  * codes * scale is exact in f16.  The queries are scaled by a power of two
+//    per head (their largest magnitude to 2^14) and are exact in f16 down to
+//    2^-28 of it.  The probabilities, times 2^10, are rounded to f16: 2^-12
+//    each, against 2^-9 in bf16, and none is lost before 2^-34 of the largest;
+//  * every warp streams its own 32-token units, K and V, through a ring of its
+//    own with cp.async.bulk (a page's tile of one head is one run of bytes),
+//    with the table entries of the next unit loaded one unit ahead.  Warps
+//    meet only at the end of a (sequence, kv head), to add up their sums;
+//  * the work is cut into equal runs of units, one for each CTA, across the
+//    borders of heads and sequences.  A (sequence, kv head) that several CTAs
+//    share is joined by the last of them, in the order of its tokens, so
+//    results do not depend on which CTA is last.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "decode.cuh"
+#include "fp4.cuh"
+#include "ptx.cuh"
+
+namespace pa {
+namespace fp4_decode_detail {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnit = 32;    // tokens a warp takes at a time
+constexpr int kMaxStages = 4;  // units in a warp's ring, at most
+constexpr float kPShift = 10.f;  // probabilities enter P.V times 2^10
+
+// Sequences of one launch: their lengths and unit counts live in shared memory.
+constexpr int kMaxSeqs = 4096;
+
+struct Launch {
+  Fp4AttnParams p;
+  int seq0, nseq;          // this launch's sequences
+  int stages;              // units in a warp's ring
+  int hkv, group, cache_heads, per_cache_head;  // (virtual) kv heads, their query heads; see launch_fp4_decode
+  int eff_log;             // log2 of the tokens of a piece (a page's, at most a unit's)
+  int bs_log;
+  int piece_bytes;         // of one piece in shared memory
+  int kv_bytes;            // of one unit's K (or V) in shared memory
+  int off_merge, off_stat, off_q, off_prefix, off_lens, off_bar;
+  int64_t tile_bytes;
+  int32_t* counters;       // [nseq * num_kv_heads], zero between launches
+  float* part;             // [2 * CTAs][G * (D + 2)]
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// the 8 x 8 matrix of 16-bit elements spread over the warp, transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int BYTES>
+struct Words;  // BYTES consecutive bytes of shared memory as 32-bit words
+template <>
+struct Words<4> {
+  uint32_t w[1];
+  __device__ __forceinline__ void load(const unsigned char* p) { w[0] = *reinterpret_cast<const uint32_t*>(p); }
+};
+template <>
+struct Words<8> {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+};
+template <>
+struct Words<16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+};
+template <>
+struct Words<32> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 16);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+};
+
+// A unit of the launch: 32 tokens of a (sequence, kv head).
+struct Cursor {
+  int seq, head, st, nst;  // st of the nst units of this (sequence, kv head)
+};
+
+}  // namespace fp4_decode_detail
+
+// D: head_dim; NT: columns of heads in eights (G <= 8 * NT)
+template <int D, int NT>
+__global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT == 1) ? 2 : 1)
+    fp4_decode_kernel(const __grid_constant__ fp4_decode_detail::Launch L) {
+  using namespace fp4_decode_detail;
+  constexpr int kMma = D / 16;        // instructions of Q.K^T a slice of 16 tokens, and of P.V
+  constexpr int kKWords = D / 32;     // words of codes of a thread's dims in Q.K^T (D / 4)
+  constexpr int kVWords = D / 64;     // and in P.V (D / 8)
+  const Fp4AttnParams& p = L.p;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, tig = lane & 3;  // the thread's row and column group in an instruction's operands
+  const int hkv = L.hkv, G = L.group;
+  unsigned char* ring = smem + warp * (L.stages * 2 * L.kv_bytes);
+  float* merge = reinterpret_cast<float*>(smem + L.off_merge);     // [warp][G][D + pad]
+  float2* stat = reinterpret_cast<float2*>(smem + L.off_stat);     // [warp][8]: maximum, sum
+  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + L.off_q);  // [2][G * D]
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.off_prefix);       // [nseq + 1] units before a sequence
+  int32_t* lens = reinterpret_cast<int32_t*>(smem + L.off_lens);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.off_bar) + warp * kMaxStages;
+  __shared__ int warp_sums[kWarps];
+  __shared__ int last_flag;
+
+  ptx::griddep_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < L.stages; ++s) ptx::mbar_init(&full[s], 1);
+    ptx::mbar_init_fence();
+  }
+  ptx::griddep_wait();
+
+  // ---- units before every sequence (an empty one has a unit of no tokens) ----
+  {
+    const int per = (L.nseq + kThreads - 1) / kThreads;
+    const int beg = min(L.nseq, tid * per), end = min(L.nseq, beg + per);
+    int local = 0;
+    for (int i = beg; i < end; ++i) {
+      int n = p.context_lens[L.seq0 + i];
+      if (n < 0 || n > p.max_context_len) {
+        if (blockIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
+        n = n < 0 ? 0 : p.max_context_len;
+      }
+      lens[i] = n;
+      local += max(1, (n + kUnit - 1) / kUnit) * hkv;
+    }
+    int x = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int run = x - local;
+    for (int w = 0; w < warp; ++w) run += warp_sums[w];
+    for (int i = beg; i < end; ++i) {
+      prefix[i] = run;
+      run += max(1, (lens[i] + kUnit - 1) / kUnit) * hkv;
+    }
+    if (tid == kThreads - 1) prefix[L.nseq] = run;
+    __syncthreads();
+  }
+  const int total = prefix[L.nseq];
+  // CTA c takes units [c * share + min(c, extra), ...): share or share + 1 of them
+  const int share = total / gridDim.x, extra = total - share * gridDim.x;
+  auto cta_begin = [&](int c) { return c * share + min(c, extra); };
+  auto cta_of = [&](int u) {
+    const int wide = extra * (share + 1);
+    return u < wide ? u / (share + 1) : extra + (u - wide) / share;
+  };
+  const int c_begin = cta_begin(blockIdx.x), c_end = cta_begin(blockIdx.x + 1);
+  if (c_begin >= c_end) return;
+
+  auto locate = [&](int u, Cursor& c) {
+    int lo = 0, hi = L.nseq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    c.seq = lo;
+    c.nst = (prefix[lo + 1] - prefix[lo]) / hkv;
+    const int r = u - prefix[lo];
+    c.head = r / c.nst;
+    c.st = r - c.head * c.nst;
+  };
+  auto advance = [&](Cursor& c, int by) {
+    c.st += by;
+    while (c.st >= c.nst) {
+      c.st -= c.nst;
+      if (++c.head == hkv) {
+        c.head = 0;
+        if (++c.seq >= L.nseq) return;
+        c.nst = (prefix[c.seq + 1] - prefix[c.seq]) / hkv;
+      }
+    }
+  };
+
+  // ---- this warp's stream of units: c_begin + warp, + kWarps, ... ----
+  const int eff = 1 << L.eff_log, npieces = kUnit >> L.eff_log;
+  const int bs = 1 << L.bs_log;
+  const bool whole = bs <= kUnit;  // a piece is a whole tile, else rows of one
+  Cursor ic{};                     // the next unit to be fetched
+  int iu = c_begin + warp;
+  int32_t phys = 0;                // its page, this lane's piece
+  auto fetch_table = [&]() {
+    const int tok = ic.st * kUnit + (lane << L.eff_log);
+    phys = 0;
+    if (lane < npieces && tok < lens[ic.seq]) {
+      phys = __ldg(p.block_tables + static_cast<int64_t>(L.seq0 + ic.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+    }
+  };
+  const uint64_t policy = ptx::policy_evict_first();
+  int issue_slot = 0, use_slot = 0, in_flight = 0;
+  uint32_t use_parity = 0;
+  auto issue = [&]() {
+    const int slot = issue_slot;
+    const int left = lens[ic.seq] - ic.st * kUnit;
+    const int nv = min(npieces, (left + eff - 1) >> L.eff_log);
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(2 * nv * L.piece_bytes));
+    __syncwarp();
+    if (lane < nv) {
+      if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
+        atomicExch(p.err, kDevErrInvalidArg);
+        phys = 0;
+      }
+      const int64_t tile = (static_cast<int64_t>(phys) * L.cache_heads + ic.head / L.per_cache_head) * L.tile_bytes;
+      unsigned char* dk = ring + slot * 2 * L.kv_bytes + lane * L.piece_bytes;
+      unsigned char* dv = dk + L.kv_bytes;
+      if (whole) {
+        ptx::bulk_g2s(dk, p.k_cache + tile, L.piece_bytes, &full[slot], policy);
+        ptx::bulk_g2s(dv, p.v_cache + tile, L.piece_bytes, &full[slot], policy);
+      } else {
+        const int row = (ic.st * kUnit) & (bs - 1);
+        const int64_t codes = tile + row * (D / 2), scales = tile + bs * (D / 2) + row * (D / 16);
+        ptx::bulk_g2s(dk, p.k_cache + codes, kUnit * (D / 2), &full[slot], policy);
+        ptx::bulk_g2s(dk + kUnit * (D / 2), p.k_cache + scales, kUnit * (D / 16), &full[slot], policy);
+        ptx::bulk_g2s(dv, p.v_cache + codes, kUnit * (D / 2), &full[slot], policy);
+        ptx::bulk_g2s(dv + kUnit * (D / 2), p.v_cache + scales, kUnit * (D / 16), &full[slot], policy);
+      }
+    }
+    if (++issue_slot == L.stages) issue_slot = 0;
+    ++in_flight;
+    iu += kWarps;
+    if (iu < c_end) {
+      advance(ic, kWarps);
+      fetch_table();
+    }
+  };
+  if (iu < c_end) {
+    locate(iu, ic);
+    fetch_table();
+  }
+  for (int s = 0; s < L.stages && iu < c_end; ++s) issue();
+
+  // ---- where this thread's tokens lie in a unit ----
+  // Row r of a slice (and index r of the sum in P.V) is token 2a + (e ^ (a & 1))
+  // for r = 2a + e: of the rows 0, 2, 4, 6 that a load of V touches together
+  // two then lie in even and two in odd 64-byte rows (D = 128).
+  auto row_token = [](int r) { return (r & ~1) + ((r & 1) ^ ((r >> 1) & 1)); };
+  auto place = [&](int t, int& codes, int& scales) {
+    const int piece = t >> L.eff_log, o = t & (eff - 1);
+    codes = piece * L.piece_bytes + o * (D / 2);
+    scales = piece * L.piece_bytes + eff * (D / 2) + o * (D / 16);
+  };
+  int k_c0, k_s0, v_c0, v_s0, v_c1, v_s1, c8, s8, c16, s16;
+  place(row_token(g), k_c0, k_s0);
+  place(row_token(2 * tig), v_c0, v_s0);
+  place(row_token(2 * tig + 1), v_c1, v_s1);
+  {
+    int z0, z1;
+    place(0, z0, z1);
+    place(8, c8, s8);
+    place(16, c16, s16);
+    s8 -= z1;
+    s16 -= z1;
+  }
+  k_c0 += tig * (D / 8);
+  k_s0 += tig * (D / 64);
+  v_c0 += g * (D / 16);
+  v_c1 += g * (D / 16);
+  v_s0 += g * D / 128;
+  v_s1 += g * D / 128;
+
+  // ---- queries: a (sequence, kv head)'s rows, fetched one segment ahead ----
+  const int q_chunks = G * D / 8;  // of 16 bytes
+  auto fetch_q = [&](const Cursor& c, int b) {
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                               (static_cast<int64_t>(L.seq0 + c.seq) * p.num_q_heads + c.head * G) * D;
+    for (int i = tid; i < q_chunks; i += kThreads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(qbuf + b * G * D + i * 8)),
+                   "l"(src + i * 8)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  Cursor sc;  // the segment: this CTA's units of one (sequence, kv head)
+  locate(c_begin, sc);
+  fetch_q(sc, 0);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  bool aborted = false;
+  int qb = 0;
+  for (int sb = c_begin; sb < c_end;) {
+    const int item_b = sb - sc.st;                    // the item's first unit
+    const int se = min(c_end, item_b + sc.nst);       // the segment's end
+    Cursor next = sc;
+    if (se < c_end) {
+      next.st = sc.nst - 1;
+      advance(next, 1);
+      fetch_q(next, qb ^ 1);
+    }
+    const int len = lens[sc.seq];
+
+    // this thread's part of the queries: head g (and g + 8), dims tig * D / 4 ..
+    uint32_t qf[NT][kMma][2];
+    float fac[NT][2];  // score factor of the thread's columns, heads 2 tig and 2 tig + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + g;
+      uint32_t w[D / 8];
+      uint32_t top = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(qbuf + qb * G * D + h * D + tig * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 v = h < G ? src[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // exponent that takes the largest magnitude to [2^14, 2^15); 0 for a
+      // zero, subnormal or non-finite row
+      const int ex = static_cast<int>(top >> 7);
+      const int shift = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 14 - (ex - 127)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      const float f = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+      for (int j = 0; j < kMma; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = w[2 * j + e];
+          qf[nt][j][e] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+        }
+      fac[nt][0] = __shfl_sync(0xffffffffu, f, tig * 8);
+      fac[nt][1] = __shfl_sync(0xffffffffu, f, tig * 8 + 4);
+    }
+
+    float o[NT][kMma][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = -CUDART_INF_F, l[nt][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kMma; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+    }
+
+    // the warp's units of the segment
+    const int first = sb + ((c_begin + warp - sb) % kWarps + kWarps) % kWarps;
+    for (int u = first; u < se; u += kWarps) {
+      if (!aborted && !ptx::mbar_wait(&full[use_slot], use_parity, kWaitLimitNs)) {
+        aborted = true;
+        atomicExch(p.err, kDevErrTimeout);
+      }
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) continue;
+      const int slot = use_slot;
+      if (++use_slot == L.stages) use_slot = 0, use_parity ^= 1u;
+      --in_flight;
+      const unsigned char* kb = ring + slot * 2 * L.kv_bytes;
+      const unsigned char* vb = kb + L.kv_bytes;
+      const int left = len - (u - item_b) * kUnit;  // tokens from this unit on
+
+      // S^T of two slices of 16 tokens
+      float s[2][NT][4];
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[sl][nt][e] = 0.f;
+        Words<D / 8> ka, kc;  // codes of rows g and g + 8
+        ka.load(kb + k_c0 + sl * c16);
+        kc.load(kb + k_c0 + sl * c16 + c8);
+        uint32_t sa = 0, sc8 = 0;  // their scales: D / 64 bytes
+        const unsigned char* ps = kb + k_s0 + sl * s16;
+        if (D == 64) {
+          sa = ps[0], sc8 = ps[s8];
+        } else if (D == 128) {
+          sa = *reinterpret_cast<const uint16_t*>(ps), sc8 = *reinterpret_cast<const uint16_t*>(ps + s8);
+        } else {
+          sa = *reinterpret_cast<const uint32_t*>(ps), sc8 = *reinterpret_cast<const uint32_t*>(ps + s8);
+        }
+#pragma unroll
+        for (int w = 0; w < kKWords; ++w) {
+          // words 2i and 2i + 1 are group i of the thread's dims
+          const uint32_t pa = fp4::scales_to_f16(sa >> (16 * (w >> 2))), pc = fp4::scales_to_f16(sc8 >> (16 * (w >> 2)));
+          const uint32_t ma = (w & 2) ? __byte_perm(pa, 0, 0x3232) : __byte_perm(pa, 0, 0x1010);
+          const uint32_t mc = (w & 2) ? __byte_perm(pc, 0, 0x3232) : __byte_perm(pc, 0, 0x1010);
+          uint32_t ha[4], hc[4];
+          fp4::codes_to_f16(ka.w[w], ha);
+          fp4::codes_to_f16(kc.w[w], hc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ha[e] = fp4::mul_f16x2(ha[e], ma), hc[e] = fp4::mul_f16x2(hc[e], mc);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(s[sl][nt], ha[0], hc[0], ha[1], hc[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+            mma(s[sl][nt], ha[2], hc[2], ha[3], hc[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          }
+        }
+      }
+      // scaled scores (log2), tokens past the end masked
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[sl][nt][e] *= fac[nt][e & 1];
+      if (left < kUnit) {
+        const int t = row_token(g);
+#pragma unroll
+        for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (sl * 16 + (e >> 1) * 8 + t >= left) s[sl][nt][e] = -CUDART_INF_F;
+      }
+      // running maximum, probabilities, running sum (a thread's own rows)
+      uint32_t pb[2][NT][2];
+      bool raised = false;
+      float corr[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[nt][c], mx);
+          const float ref = mn == -CUDART_INF_F ? 0.f : mn;
+          raised |= mn > m[nt][c];
+          corr[nt][c] = fast_exp2(m[nt][c] - ref);
+          m[nt][c] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float e = fast_exp2(s[sl][nt][c + 2 * r] - ref + kPShift);
+              s[sl][nt][c + 2 * r] = e;
+              sum += e;
+            }
+          l[nt][c] = fmaf(l[nt][c], corr[nt][c], sum);
+        }
+      if (__any_sync(0xffffffffu, raised)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < kMma; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][j][e] *= corr[nt][e & 1];
+      }
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            pb[sl][nt][r] = transpose8x8(pack_f16(s[sl][nt][2 * r], s[sl][nt][2 * r + 1]));
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl) {
+        Words<D / 16> v[4];  // tokens of indices 2 tig, 2 tig + 1, and + 8
+        uint32_t vs[4][D == 256 ? 2 : 1];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int co = ((t & 1) ? v_c1 : v_c0) + sl * c16 + (t >> 1) * c8;
+          const int so = ((t & 1) ? v_s1 : v_s0) + sl * s16 + (t >> 1) * s8;
+          v[t].load(vb + co);
+          vs[t][0] = vb[so];
+          if (D == 256) vs[t][D == 256 ? 1 : 0] = vb[so + 1];
+        }
+        if (left < kUnit) {  // the scales of what lies past the end may be NaN: 0 * NaN must not reach the sums
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (sl * 16 + (t >> 1) * 8 + row_token(2 * tig + (t & 1)) >= left) {
+              vs[t][0] = 0;
+              if (D == 256) vs[t][D == 256 ? 1 : 0] = 0;
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) {
+          const int sg = D == 256 ? (w >> 1) : 0;
+          const uint32_t m0 = fp4::scales_to_f16(vs[0][sg] | (vs[1][sg] << 8));
+          const uint32_t m1 = fp4::scales_to_f16(vs[2][sg] | (vs[3][sg] << 8));
+          uint32_t a0[4], a1[4], a2[4], a3[4];  // even dims, odd dims of tokens 0, 1; the same of tokens 2, 3
+          const uint32_t x0 = v[0].w[w], x1 = v[1].w[w], x2 = v[2].w[w], x3 = v[3].w[w];
+          fp4::codes_to_f16((x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u), a0);
+          fp4::codes_to_f16(((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u), a1);
+          fp4::codes_to_f16((x2 & 0x0f0f0f0fu) | ((x3 << 4) & 0xf0f0f0f0u), a2);
+          fp4::codes_to_f16(((x2 >> 4) & 0x0f0f0f0fu) | (x3 & 0xf0f0f0f0u), a3);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b0 = fp4::mul_f16x2(a0[e], m0), b1 = fp4::mul_f16x2(a1[e], m0);
+            const uint32_t b2 = fp4::mul_f16x2(a2[e], m1), b3 = fp4::mul_f16x2(a3[e], m1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(o[nt][4 * w + e], b0, b1, b2, b3, pb[sl][nt][0], pb[sl][nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (iu < c_end) issue();
+    }
+
+    // ---- the warps' sums of the segment joined, eight heads at a time ----
+    // Head pair tig at a distance of 2 D + 2 floats, and the float pairs of
+    // row group g turned by 8 or more, so that a store touches every bank once.
+    constexpr int kPair = 2 * D + 2, kRow = D / 8;
+    const int gpairs = (min(G, 8) + 1) / 2;
+    const int turn = D == 64 ? 0 : (D == 128 ? 8 * ((g >> 1) & 1) : 8 * (g & 3));
+    const bool active = first < se;
+    const bool complete = item_b >= sb && item_b + sc.nst <= se;
+    const int64_t out_row = static_cast<int64_t>(L.seq0 + sc.seq) * p.num_q_heads + sc.head * G;
+    const int part_slot = sb == c_begin ? 0 : 1;
+    float* part = L.part + (static_cast<int64_t>(blockIdx.x) * 2 + part_slot) * (G * (D + 2));
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // the next segment's queries
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) __syncthreads();
+      const int heads = min(8, G - nt * 8);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 4);
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 8);
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 16);
+        const int h = 2 * tig + c;
+        if (g == 0) stat[warp * 8 + h] = active ? make_float2(m[nt][c], l[nt][c]) : make_float2(-CUDART_INF_F, 0.f);
+        if (active && h < heads) {
+          float* row = merge + warp * (gpairs * kPair) + tig * kPair + c * D + g * kRow;
+#pragma unroll
+          for (int j = 0; j < kMma; ++j)
+            *reinterpret_cast<float2*>(row + ((2 * j + turn) & (kRow - 1))) = make_float2(o[nt][j][c], o[nt][j][c + 2]);
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < heads * D / 2; i += kThreads) {
+        const int h = i / (D / 2), d = (i - h * (D / 2)) * 2;
+        float M = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w * 8 + h].x);
+        const float ref = M == -CUDART_INF_F ? 0.f : M;
+        const int rg = d / kRow;
+        const int rt = D == 64 ? 0 : (D == 128 ? 8 * ((rg >> 1) & 1) : 8 * (rg & 3));
+        const int at = (h >> 1) * kPair + (h & 1) * D + rg * kRow + ((d - rg * kRow + rt) & (kRow - 1));
+        float lsum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 st = stat[w * 8 + h];
+          if (st.y != 0.f) {  // a warp without tokens wrote nothing
+            const float f = fast_exp2(st.x - ref);
+            const float2 v = *reinterpret_cast<const float2*>(merge + w * (gpairs * kPair) + at);
+            lsum = fmaf(f, st.y, lsum);
+            x = fmaf(f, v.x, x);
+            y = fmaf(f, v.y, y);
+          }
+        }
+        const int head = nt * 8 + h;
+        if (complete) {
+          const float inv = lsum != 0.f ? p.v_scale / lsum : 0.f;
+          const int64_t at_out = (out_row + head) * D + d;
+          if (p.out_bf16)
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at_out) =
+                __floats2bfloat162_rn(x * inv, y * inv);
+          else
+            *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at_out) = make_float2(x * inv, y * inv);
+        } else {
+          *reinterpret_cast<float2*>(part + 2 * G + head * D + d) = make_float2(x, y);
+          if (d == 0) *reinterpret_cast<float2*>(part + 2 * head) = make_float2(M, lsum);
+        }
+      }
+    }
+    if (!complete) {
+      // the last CTA of the item joins the CTAs' parts, in the order of the tokens
+      __threadfence();
+      __syncthreads();
+      const int c0 = cta_of(item_b), c1 = cta_of(item_b + sc.nst - 1);
+      if (tid == 0) {
+        int32_t* counter = L.counters + sc.seq * hkv + sc.head;
+        const int before = atomicAdd(counter, 1);
+        last_flag = before == c1 - c0;
+        if (before == c1 - c0) *counter = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (last_flag) {
+        const int n = c1 - c0 + 1;
+        const float* base = L.part;
+        auto part_of = [&](int k) {
+          const int c = c0 + k;
+          return base + (static_cast<int64_t>(c) * 2 + (cta_begin(c) >= item_b ? 0 : 1)) * (G * (D + 2));
+        };
+        // groups of threads take every ngroups-th part; then the groups are added
+        const int width = min(kThreads, G * D / 4);  // threads that cover the item's outputs, 4 each
+        const int ngroups = kThreads / width, grp = tid / width;
+        for (int i0 = 0; i0 < G * D / 4; i0 += width) {
+          const int i = i0 + tid % width;
+          const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+          float M = -CUDART_INF_F;
+#pragma unroll 8
+          for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(part_of(k) + 2 * h));
+          const float ref = M == -CUDART_INF_F ? 0.f : M;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float lsum = 0.f;
+#pragma unroll 4
+          for (int k = grp; k < n; k += ngroups) {
+            const float* q = part_of(k);
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(q + 2 * h));
+            const float2 v0 = __ldcg(reinterpret_cast<const float2*>(q + 2 * G + h * D + d));
+            const float2 v1 = __ldcg(reinterpret_cast<const float2*>(q + 2 * G + h * D + d + 2));
+            const float f = st.y != 0.f ? fast_exp2(st.x - ref) : 0.f;
+            lsum = fmaf(f, st.y, lsum);
+            acc.x = fmaf(f, v0.x, acc.x);
+            acc.y = fmaf(f, v0.y, acc.y);
+            acc.z = fmaf(f, v1.x, acc.z);
+            acc.w = fmaf(f, v1.y, acc.w);
+          }
+          if (ngroups > 1) {
+            float* red = merge + tid * 5;  // 5 floats a thread
+            red[0] = acc.x, red[1] = acc.y, red[2] = acc.z, red[3] = acc.w, red[4] = lsum;
+            __syncthreads();
+            if (grp == 0) {
+              for (int r = 1; r < ngroups; ++r) {
+                const float* o2 = merge + (tid + r * width) * 5;
+                acc.x += o2[0], acc.y += o2[1], acc.z += o2[2], acc.w += o2[3], lsum += o2[4];
+              }
+            }
+          }
+          if (grp == 0) {
+            const float inv = lsum != 0.f ? p.v_scale / lsum : 0.f;
+            const int64_t at_out = (out_row + h) * D + d;
+            if (p.out_bf16) {
+              __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at_out);
+              dst[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+              dst[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            } else {
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at_out) =
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();  // the merge area and the flag are free again
+    sb = se;
+    sc = next;
+    qb ^= 1;
+  }
+  // a wait that gave up: what is in flight still has to land before the CTA ends
+  for (; in_flight > 0; --in_flight) {
+    (void)ptx::mbar_wait(&full[use_slot], use_parity, kWaitLimitNs);
+    if (++use_slot == L.stages) use_slot = 0, use_parity ^= 1u;
+  }
+}
+
+namespace {
+
+using fp4_decode_detail::Launch;
+
+const void* kernel_for(int head_dim, int group) {
+  if (head_dim == 64)
+    return group <= 8 ? reinterpret_cast<const void*>(&fp4_decode_kernel<64, 1>)
+                      : reinterpret_cast<const void*>(&fp4_decode_kernel<64, 2>);
+  if (head_dim == 128)
+    return group <= 8 ? reinterpret_cast<const void*>(&fp4_decode_kernel<128, 1>)
+                      : reinterpret_cast<const void*>(&fp4_decode_kernel<128, 2>);
+  return reinterpret_cast<const void*>(&fp4_decode_kernel<256, 1>);
+}
+
+// CTAs that a launch has at most: what its part slots are sized for.
+int64_t max_ctas(int head_dim, int group) { return device_sm_count() * (head_dim <= 128 && group <= 8 ? 2 : 1); }
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+}  // namespace
+
+// 16 query heads of 256 dims would need more registers than a thread has:
+// they are taken as two kv heads of 8 that share their pages.
+int per_cache_head(int head_dim, int group) { return head_dim == 256 && group == 16 ? 2 : 1; }
+
+size_t fp4_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
+  using namespace fp4_decode_detail;
+  const int split = per_cache_head(head_dim, num_q_heads / num_kv_heads);
+  const int G = num_q_heads / num_kv_heads / split;
+  const int64_t seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
+  return static_cast<size_t>(256 + round_up(seqs * num_kv_heads * split * 4, 256) +
+                             max_ctas(head_dim, G) * 2 * G * (head_dim + 2) * 4);
+}
+
+cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t stream) {
+  using namespace fp4_decode_detail;
+  const int split = per_cache_head(head_dim, p.num_q_heads / p.num_kv_heads);
+  const int hkv = p.num_kv_heads * split;
+  const int G = p.num_q_heads / hkv;
+  const void* fn = kernel_for(head_dim, G);
+  for (int seq0 = 0; seq0 < p.num_seqs; seq0 += kMaxSeqs) {
+    Launch L{};
+    L.p = p;
+    L.seq0 = seq0;
+    L.nseq = p.num_seqs - seq0 < kMaxSeqs ? p.num_seqs - seq0 : kMaxSeqs;
+    L.hkv = hkv;
+    L.group = G;
+    L.cache_heads = p.num_kv_heads;
+    L.per_cache_head = split;
+    L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
+    const int eff = p.block_size < kUnit ? p.block_size : kUnit;
+    L.eff_log = __builtin_ctz(static_cast<unsigned>(eff));
+    L.tile_bytes = fp4_tile_bytes(p.block_size, head_dim);
+    L.piece_bytes = static_cast<int>(fp4_tile_bytes(eff, head_dim));
+    L.kv_bytes = (kUnit / eff) * L.piece_bytes;
+    // as deep a ring as leaves room for the CTAs of an SM
+    const int64_t unit = static_cast<int64_t>(kWarps) * 2 * L.kv_bytes;
+    const int64_t merge = static_cast<int64_t>(kWarps) * ((G < 8 ? G : 8) + 1) / 2 * (2 * head_dim + 2) * 4;
+    const int64_t fixed = (merge > kThreads * 20 ? merge : kThreads * 20) + 2 * G * head_dim * 2 + 8 * L.nseq + 2048;
+    const int64_t room = (head_dim <= 128 && G <= 8 ? 113 : 226) * 1024 - fixed;
+    L.stages = static_cast<int>(room / unit);
+    L.stages = L.stages < 2 ? (2 * unit + fixed <= 226 * 1024 ? 2 : 1) : (L.stages > kMaxStages ? kMaxStages : L.stages);
+    int64_t off = L.stages * unit;
+    auto take = [&](int64_t bytes) {
+      const int64_t at = off;
+      off += round_up(bytes, 16);
+      return static_cast<int>(at);
+    };
+    L.off_merge = take(merge > kThreads * 20 ? merge : kThreads * 20);
+    L.off_stat = take(kWarps * 8 * 8);
+    L.off_q = take(2 * G * head_dim * 2);
+    L.off_prefix = take((L.nseq + 1) * 4);
+    L.off_lens = take(L.nseq * 4);
+    L.off_bar = take(kWarps * kMaxStages * 8);
+    L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
+    const int64_t seqs = p.num_seqs < kMaxSeqs ? p.num_seqs : kMaxSeqs;
+    L.part = reinterpret_cast<float*>(p.ws + 256 + round_up(seqs * hkv * 4, 256));
+    // at least a unit for every warp, as far as the longest context allows
+    const int64_t most = static_cast<int64_t>(L.nseq) * hkv * ((p.max_context_len + kUnit - 1) / kUnit + 1);
+    int64_t ctas = (most + kWarps - 1) / kWarps;
+    const int64_t items = static_cast<int64_t>(L.nseq) * hkv;
+    if (ctas < items) ctas = items;
+    const int64_t cap = max_ctas(head_dim, G);
+    if (ctas > cap) ctas = cap;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(off));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(off);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&L};
+    e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace pa
