@@ -33,6 +33,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <mutex>
+
 #include "decode.cuh"
 #include "fp4.cuh"
 #include "ptx.cuh"
@@ -40,25 +42,34 @@
 namespace pa {
 namespace fp4_decode_detail {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 32;    // tokens a warp takes at a time
-constexpr int kMaxStages = 4;  // units in a warp's ring, at most
+// Units in a warp's ring: what an SM's shared memory holds for 16 warps (8
+// with 16 heads or 256 dims), so that a warp has the next one or three in
+// flight while it works on one.
+__host__ __device__ constexpr int ring_stages(int D, int NT) { return D == 64 || (D == 128 && NT == 2) ? 4 : 2; }
+constexpr int kMergeHeads = 4;  // heads whose sums are joined at a time
+// What starting and joining a (sequence, kv head) costs a CTA, in units: the
+// shares of the CTAs count it, as places before the first unit.
+constexpr int kLead = 4;
 constexpr float kPShift = 10.f;  // probabilities enter P.V times 2^10
+// The reference of the probabilities is raised only when a score passes it by
+// more than 2^4: they stay below 2^14 in f16, and most units leave O alone.
+constexpr float kSlack = 4.f;
 
 // Sequences of one launch: their lengths and unit counts live in shared memory.
-constexpr int kMaxSeqs = 4096;
+constexpr int kMaxSeqs = 1024;
 
 struct Launch {
   Fp4AttnParams p;
   int seq0, nseq;          // this launch's sequences
-  int stages;              // units in a warp's ring
   int hkv, group, cache_heads, per_cache_head;  // (virtual) kv heads, their query heads; see launch_fp4_decode
   int eff_log;             // log2 of the tokens of a piece (a page's, at most a unit's)
   int bs_log;
   int piece_bytes;         // of one piece in shared memory
   int kv_bytes;            // of one unit's K (or V) in shared memory
-  int off_merge, off_stat, off_q, off_prefix, off_lens, off_bar;
+  int off_merge, off_stat, off_q, off_qfac, off_prefix, off_lens, off_bar;
   int64_t tile_bytes;
   int32_t* counters;       // [nseq * num_kv_heads], zero between launches
   float* part;             // [2 * CTAs][G * (D + 2)]
@@ -85,6 +96,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// four outputs, times inv
+__device__ __forceinline__ void store4(const Fp4AttnParams& p, int64_t at, const float4& v, float inv) {
+  if (p.out_bf16) {
+    __nv_bfloat162 r[2] = {__floats2bfloat162_rn(v.x * inv, v.y * inv), __floats2bfloat162_rn(v.z * inv, v.w * inv)};
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) = *reinterpret_cast<const uint2*>(r);
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  }
 }
 template <int BYTES>
 struct Words;  // BYTES consecutive bytes of shared memory as 32-bit words
@@ -118,18 +138,26 @@ struct Words<32> {
   }
 };
 
-// A unit of the launch: 32 tokens of a (sequence, kv head).
+// A place of the launch: a unit, 32 tokens of a (sequence, kv head), or one of
+// the kLead places before its first unit (st < 0), which hold no work.
 struct Cursor {
   int seq, head, st, nst;  // st of the nst units of this (sequence, kv head)
 };
 
 }  // namespace fp4_decode_detail
 
-// D: head_dim; NT: columns of heads in eights (G <= 8 * NT)
-template <int D, int NT>
-__global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT == 1) ? 2 : 1)
+// D: head_dim; NT: columns of heads in eights (G <= 8 * NT); EL: log2 of the
+// tokens of a piece (blocks of 16 tokens: 4, of 32 and more: 5), or -1 for
+// blocks of fewer than 16 tokens, whose layout is then read from L
+template <int D, int NT, int EL>
+__global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT == 1) ? 4 : 2)
     fp4_decode_kernel(const __grid_constant__ fp4_decode_detail::Launch L) {
   using namespace fp4_decode_detail;
+  constexpr int kStages = ring_stages(D, NT);
+  const int eff_log = EL >= 0 ? EL : L.eff_log;
+  const int eff = 1 << eff_log, npieces = kUnit >> eff_log;
+  const int piece_bytes = EL >= 0 ? (1 << (EL >= 0 ? EL : 0)) * (D / 2 + D / 16) : L.piece_bytes;
+  const int kv_bytes = EL >= 0 ? kUnit * (D / 2 + D / 16) : L.kv_bytes;
   constexpr int kMma = D / 16;        // instructions of Q.K^T a slice of 16 tokens, and of P.V
   constexpr int kKWords = D / 32;     // words of codes of a thread's dims in Q.K^T (D / 4)
   constexpr int kVWords = D / 64;     // and in P.V (D / 8)
@@ -138,24 +166,27 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, tig = lane & 3;  // the thread's row and column group in an instruction's operands
   const int hkv = L.hkv, G = L.group;
-  unsigned char* ring = smem + warp * (L.stages * 2 * L.kv_bytes);
+  unsigned char* ring = smem + warp * (kStages * 2 * kv_bytes);
   float* merge = reinterpret_cast<float*>(smem + L.off_merge);     // [warp][G][D + pad]
   float2* stat = reinterpret_cast<float2*>(smem + L.off_stat);     // [warp][8]: maximum, sum
   __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + L.off_q);  // [2][G * D]
-  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.off_prefix);       // [nseq + 1] units before a sequence
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.off_prefix);       // [nseq + 1] places before a sequence
   int32_t* lens = reinterpret_cast<int32_t*>(smem + L.off_lens);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.off_bar) + warp * kMaxStages;
+  float* qfac = reinterpret_cast<float*>(smem + L.off_qfac);               // [2][16] score factors
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L.off_bar);         // [2]
   __shared__ int warp_sums[kWarps];
   __shared__ int last_flag;
 
   ptx::griddep_launch_dependents();
-  if (lane == 0) {
-    for (int s = 0; s < L.stages; ++s) ptx::mbar_init(&full[s], 1);
+  if (tid == 0) {
+    ptx::mbar_init(&q_full[0], 1);
+    ptx::mbar_init(&q_full[1], 1);
     ptx::mbar_init_fence();
   }
   ptx::griddep_wait();
 
-  // ---- units before every sequence (an empty one has a unit of no tokens) ----
+  // ---- places before every sequence: kLead and one for every unit of each of
+  // its kv heads (an empty sequence has a unit of no tokens) ----
   {
     const int per = (L.nseq + kThreads - 1) / kThreads;
     const int beg = min(L.nseq, tid * per), end = min(L.nseq, beg + per);
@@ -167,7 +198,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
         n = n < 0 ? 0 : p.max_context_len;
       }
       lens[i] = n;
-      local += max(1, (n + kUnit - 1) / kUnit) * hkv;
+      local += (kLead + max(1, (n + kUnit - 1) / kUnit)) * hkv;
     }
     int x = local;
 #pragma unroll
@@ -181,13 +212,13 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
     for (int w = 0; w < warp; ++w) run += warp_sums[w];
     for (int i = beg; i < end; ++i) {
       prefix[i] = run;
-      run += max(1, (lens[i] + kUnit - 1) / kUnit) * hkv;
+      run += (kLead + max(1, (lens[i] + kUnit - 1) / kUnit)) * hkv;
     }
     if (tid == kThreads - 1) prefix[L.nseq] = run;
     __syncthreads();
   }
   const int total = prefix[L.nseq];
-  // CTA c takes units [c * share + min(c, extra), ...): share or share + 1 of them
+  // CTA c takes places [c * share + min(c, extra), ...): share or share + 1 of them
   const int share = total / gridDim.x, extra = total - share * gridDim.x;
   auto cta_begin = [&](int c) { return c * share + min(c, extra); };
   auto cta_of = [&](int u) {
@@ -205,79 +236,109 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       else hi = mid - 1;
     }
     c.seq = lo;
-    c.nst = (prefix[lo + 1] - prefix[lo]) / hkv;
+    const int places = (prefix[lo + 1] - prefix[lo]) / hkv;
     const int r = u - prefix[lo];
-    c.head = r / c.nst;
-    c.st = r - c.head * c.nst;
+    c.nst = places - kLead;
+    c.head = r / places;
+    c.st = r - c.head * places - kLead;
   };
   auto advance = [&](Cursor& c, int by) {
     c.st += by;
     while (c.st >= c.nst) {
-      c.st -= c.nst;
+      c.st -= c.nst + kLead;
       if (++c.head == hkv) {
         c.head = 0;
         if (++c.seq >= L.nseq) return;
-        c.nst = (prefix[c.seq + 1] - prefix[c.seq]) / hkv;
+        c.nst = (prefix[c.seq + 1] - prefix[c.seq]) / hkv - kLead;
       }
     }
   };
 
   // ---- this warp's stream of units: c_begin + warp, + kWarps, ... ----
-  const int eff = 1 << L.eff_log, npieces = kUnit >> L.eff_log;
   const int bs = 1 << L.bs_log;
-  const bool whole = bs <= kUnit;  // a piece is a whole tile, else rows of one
   Cursor ic{};                     // the next unit to be fetched
   int iu = c_begin + warp;
   int32_t phys = 0;                // its page, this lane's piece
   auto fetch_table = [&]() {
-    const int tok = ic.st * kUnit + (lane << L.eff_log);
+    const int tok = ic.st * kUnit + (lane << eff_log);
     phys = 0;
     if (lane < npieces && tok < lens[ic.seq]) {
       phys = __ldg(p.block_tables + static_cast<int64_t>(L.seq0 + ic.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
     }
   };
-  const uint64_t policy = ptx::policy_evict_first();
-  int issue_slot = 0, use_slot = 0, in_flight = 0;
-  uint32_t use_parity = 0;
+  auto copy16 = [](uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  };
+  auto next_unit = [&]() {
+    do {
+      iu += kWarps;
+      if (iu >= c_end) return;
+      advance(ic, kWarps);
+    } while (ic.st < 0);
+    fetch_table();
+  };
+  int issue_slot = 0, use_slot = 0;
+  // fetches the next unit, or nothing at the end: one group of copies each time
   auto issue = [&]() {
-    const int slot = issue_slot;
-    const int left = lens[ic.seq] - ic.st * kUnit;
-    const int nv = min(npieces, (left + eff - 1) >> L.eff_log);
-    if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(2 * nv * L.piece_bytes));
-    __syncwarp();
-    if (lane < nv) {
-      if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
+    if (iu < c_end) {
+      const int left = lens[ic.seq] - ic.st * kUnit;
+      const int nv = min(npieces, (left + eff - 1) >> eff_log);
+      if (lane < nv && (phys < 0 || phys >= p.num_blocks)) {  // never read outside the pool
         atomicExch(p.err, kDevErrInvalidArg);
         phys = 0;
       }
-      const int64_t tile = (static_cast<int64_t>(phys) * L.cache_heads + ic.head / L.per_cache_head) * L.tile_bytes;
-      unsigned char* dk = ring + slot * 2 * L.kv_bytes + lane * L.piece_bytes;
-      unsigned char* dv = dk + L.kv_bytes;
-      if (whole) {
-        ptx::bulk_g2s(dk, p.k_cache + tile, L.piece_bytes, &full[slot], policy);
-        ptx::bulk_g2s(dv, p.v_cache + tile, L.piece_bytes, &full[slot], policy);
+      const uint32_t dst = ptx::smem_addr(ring + issue_slot * 2 * kv_bytes);
+      const int cache_head = L.per_cache_head == 1 ? ic.head : ic.head / L.per_cache_head;
+      auto tile_of = [&](int page) { return (static_cast<int64_t>(page) * L.cache_heads + cache_head) * L.tile_bytes; };
+      if (EL >= 0) {
+        // 16-byte chunks: kCodes a lane of a unit's codes, piece after piece,
+        // then one of its scales in the first kScales lanes
+        constexpr int kCodes = kUnit * (D / 2) / 512, kScales = kUnit * (D / 16) / 16;
+        constexpr int kPieces = EL == 4 ? 2 : 1, kPerPiece = kCodes / kPieces;
+        constexpr int kEff = kUnit / kPieces;
+        const int row = EL == 5 ? (ic.st * kUnit) & (bs - 1) : 0;  // of the piece in its tile
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          if (j < nv) {
+            const int64_t at = tile_of(__shfl_sync(0xffffffffu, phys, j)) + row * (D / 2) + lane * 16;
+            const uint32_t d = dst + j * (kEff * (D / 2 + D / 16)) + lane * 16;
+#pragma unroll
+            for (int i = 0; i < kPerPiece; ++i) {
+              copy16(d + i * 512, p.k_cache + at + i * 512);
+              copy16(d + kv_bytes + i * 512, p.v_cache + at + i * 512);
+            }
+          }
+        }
+        const int j = kPieces == 1 ? 0 : lane / (kScales / kPieces);  // the piece of this lane's scales
+        const int page = __shfl_sync(0xffffffffu, phys, j & 1);
+        if (lane < kScales && j < nv) {
+          const int c = (kPieces == 1 ? lane : lane % (kScales / kPieces)) * 16;
+          const int64_t at = tile_of(page) + static_cast<int64_t>(bs) * (D / 2) + row * (D / 16) + c;
+          const uint32_t d = dst + j * (kEff * (D / 2 + D / 16)) + kEff * (D / 2) + c;
+          copy16(d, p.k_cache + at);
+          copy16(d + kv_bytes, p.v_cache + at);
+        }
       } else {
-        const int row = (ic.st * kUnit) & (bs - 1);
-        const int64_t codes = tile + row * (D / 2), scales = tile + bs * (D / 2) + row * (D / 16);
-        ptx::bulk_g2s(dk, p.k_cache + codes, kUnit * (D / 2), &full[slot], policy);
-        ptx::bulk_g2s(dk + kUnit * (D / 2), p.k_cache + scales, kUnit * (D / 16), &full[slot], policy);
-        ptx::bulk_g2s(dv, p.v_cache + codes, kUnit * (D / 2), &full[slot], policy);
-        ptx::bulk_g2s(dv + kUnit * (D / 2), p.v_cache + scales, kUnit * (D / 16), &full[slot], policy);
+#pragma unroll 1
+        for (int j = 0; j < nv; ++j) {  // whole tiles of a few hundred bytes
+          const int64_t at = tile_of(__shfl_sync(0xffffffffu, phys, j));
+          for (int c = lane * 16; c < piece_bytes; c += 512) {
+            copy16(dst + j * piece_bytes + c, p.k_cache + at + c);
+            copy16(dst + kv_bytes + j * piece_bytes + c, p.v_cache + at + c);
+          }
+        }
       }
+      if (++issue_slot == kStages) issue_slot = 0;
+      next_unit();
     }
-    if (++issue_slot == L.stages) issue_slot = 0;
-    ++in_flight;
-    iu += kWarps;
-    if (iu < c_end) {
-      advance(ic, kWarps);
-      fetch_table();
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if (iu < c_end) {
     locate(iu, ic);
-    fetch_table();
+    if (ic.st < 0) next_unit();
+    else fetch_table();
   }
-  for (int s = 0; s < L.stages && iu < c_end; ++s) issue();
+  for (int s = 0; s < kStages; ++s) issue();
 
   // ---- where this thread's tokens lie in a unit ----
   // Row r of a slice (and index r of the sum in P.V) is token 2a + (e ^ (a & 1))
@@ -285,9 +346,9 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   // two then lie in even and two in odd 64-byte rows (D = 128).
   auto row_token = [](int r) { return (r & ~1) + ((r & 1) ^ ((r >> 1) & 1)); };
   auto place = [&](int t, int& codes, int& scales) {
-    const int piece = t >> L.eff_log, o = t & (eff - 1);
-    codes = piece * L.piece_bytes + o * (D / 2);
-    scales = piece * L.piece_bytes + eff * (D / 2) + o * (D / 16);
+    const int piece = t >> eff_log, o = t & (eff - 1);
+    codes = piece * piece_bytes + o * (D / 2);
+    scales = piece * piece_bytes + eff * (D / 2) + o * (D / 16);
   };
   int k_c0, k_s0, v_c0, v_s0, v_c1, v_s1, c8, s8, c16, s16;
   place(row_token(g), k_c0, k_s0);
@@ -309,31 +370,72 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   v_s1 += g * D / 128;
 
   // ---- queries: a (sequence, kv head)'s rows, fetched one segment ahead ----
-  const int q_chunks = G * D / 8;  // of 16 bytes
-  auto fetch_q = [&](const Cursor& c, int b) {
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                               (static_cast<int64_t>(L.seq0 + c.seq) * p.num_q_heads + c.head * G) * D;
-    for (int i = tid; i < q_chunks; i += kThreads)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(qbuf + b * G * D + i * 8)),
-                   "l"(src + i * 8)
-                   : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  // They are turned into f16 in place once the segment before is done.
+  const int q_chunks = G * D / 8;
+  auto fetch_q = [&](const Cursor& c, int b) {  // one run of bytes
+    if (tid == 0) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                 (static_cast<int64_t>(L.seq0 + c.seq) * p.num_q_heads + c.head * G) * D;
+      ptx::fence_proxy_async_smem();  // the buffer was written by ordinary stores before
+      ptx::mbar_arrive_expect_tx(&q_full[b], G * D * 2);
+      ptx::bulk_g2s(qbuf + b * G * D, src, G * D * 2, &q_full[b], ptx::policy_evict_first());
+    }
+  };
+  bool aborted = false;
+  uint32_t q_parity = 0;  // one bit for each buffer
+  auto convert_q = [&](int b) {
+    if (!ptx::mbar_wait(&q_full[b], (q_parity >> b) & 1u, kWaitLimitNs)) {
+      aborted = true;  // the output is then undefined
+      atomicExch(p.err, kDevErrTimeout);
+    }
+    q_parity ^= 1u << b;
+    for (int i0 = 0; i0 < q_chunks; i0 += kThreads) {
+      const int i = i0 + tid;
+      uint4* at = reinterpret_cast<uint4*>(qbuf + b * G * D + i * 8);
+      const uint4 v = i < q_chunks ? *at : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int x = 1; x < D / 8; x *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+      // exponent that takes the head's largest magnitude to [2^14, 2^15); 0
+      // for a zero, subnormal or non-finite row.  A negative softmax scale
+      // goes into the sign of the query: the score factor is not negative.
+      const int ex = static_cast<int>(top >> 7);
+      const int shift = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 14 - (ex - 127)));
+      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), p.scale_log2);
+      uint32_t r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        r[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+      if (i < q_chunks) {
+        *at = make_uint4(r[0], r[1], r[2], r[3]);
+        if (i % (D / 8) == 0)
+          // (not zero: a masked -inf times it stays -inf)
+          qfac[b * 16 + i / (D / 8)] =
+              fmaxf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 1.2e-38f);
+      }
+    }
   };
 
   Cursor sc;  // the segment: this CTA's units of one (sequence, kv head)
   locate(c_begin, sc);
+  const int s_begin = sc.st < 0 ? c_begin - sc.st : c_begin;  // its first unit
+  if (sc.st < 0) sc.st = 0;
+  if (s_begin >= c_end) return;
   fetch_q(sc, 0);
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  convert_q(0);
   __syncthreads();
-  bool aborted = false;
   int qb = 0;
-  for (int sb = c_begin; sb < c_end;) {
+  for (int sb = s_begin; sb < c_end;) {
     const int item_b = sb - sc.st;                    // the item's first unit
     const int se = min(c_end, item_b + sc.nst);       // the segment's end
     Cursor next = sc;
-    if (se < c_end) {
+    const bool more = se + kLead < c_end;             // another segment with a unit follows
+    if (more) {
       next.st = sc.nst - 1;
-      advance(next, 1);
+      advance(next, 1 + kLead);
       fetch_q(next, qb ^ 1);
     }
     const int len = lens[sc.seq];
@@ -344,33 +446,14 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = nt * 8 + g;
-      uint32_t w[D / 8];
-      uint32_t top = 0;
       const uint4* src = reinterpret_cast<const uint4*>(qbuf + qb * G * D + h * D + tig * (D / 4));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 v = h < G ? src[i] : make_uint4(0, 0, 0, 0);
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        qf[nt][2 * i][0] = v.x, qf[nt][2 * i][1] = v.y, qf[nt][2 * i + 1][0] = v.z, qf[nt][2 * i + 1][1] = v.w;
       }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // exponent that takes the largest magnitude to [2^14, 2^15); 0 for a
-      // zero, subnormal or non-finite row
-      const int ex = static_cast<int>(top >> 7);
-      const int shift = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 14 - (ex - 127)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      const float f = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-#pragma unroll
-      for (int j = 0; j < kMma; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t v = w[2 * j + e];
-          qf[nt][j][e] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
-        }
-      fac[nt][0] = __shfl_sync(0xffffffffu, f, tig * 8);
-      fac[nt][1] = __shfl_sync(0xffffffffu, f, tig * 8 + 4);
+      for (int c = 0; c < 2; ++c) fac[nt][c] = nt * 8 + 2 * tig + c < G ? qfac[qb * 16 + nt * 8 + 2 * tig + c] : 1.f;
     }
 
     float o[NT][kMma][4];
@@ -388,17 +471,12 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
     // the warp's units of the segment
     const int first = sb + ((c_begin + warp - sb) % kWarps + kWarps) % kWarps;
     for (int u = first; u < se; u += kWarps) {
-      if (!aborted && !ptx::mbar_wait(&full[use_slot], use_parity, kWaitLimitNs)) {
-        aborted = true;
-        atomicExch(p.err, kDevErrTimeout);
-      }
-      aborted = __any_sync(0xffffffffu, aborted);
-      if (aborted) continue;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
       const int slot = use_slot;
-      if (++use_slot == L.stages) use_slot = 0, use_parity ^= 1u;
-      --in_flight;
-      const unsigned char* kb = ring + slot * 2 * L.kv_bytes;
-      const unsigned char* vb = kb + L.kv_bytes;
+      if (++use_slot == kStages) use_slot = 0;
+      const unsigned char* kb = ring + slot * 2 * kv_bytes;
+      const unsigned char* vb = kb + kv_bytes;
       const int left = len - (u - item_b) * kUnit;  // tokens from this unit on
 
       // S^T of two slices of 16 tokens
@@ -439,14 +517,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
           }
         }
       }
-      // scaled scores (log2), tokens past the end masked
-#pragma unroll
-      for (int sl = 0; sl < 2; ++sl)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[sl][nt][e] *= fac[nt][e & 1];
-      if (left < kUnit) {
+      if (left < kUnit) {  // tokens past the end
         const int t = row_token(g);
 #pragma unroll
         for (int sl = 0; sl < 2; ++sl)
@@ -456,42 +527,50 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
             for (int e = 0; e < 4; ++e)
               if (sl * 16 + (e >> 1) * 8 + t >= left) s[sl][nt][e] = -CUDART_INF_F;
       }
-      // running maximum, probabilities, running sum (a thread's own rows)
-      uint32_t pb[2][NT][2];
-      bool raised = false;
-      float corr[NT][2];
+      // m: the reference of the probabilities (log2), the same in the four
+      // lanes' column of a head; l: the sum of this thread's own rows
+      float mx[NT][2];
+      bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m[nt][c], mx);
-          const float ref = mn == -CUDART_INF_F ? 0.f : mn;
-          raised |= mn > m[nt][c];
-          corr[nt][c] = fast_exp2(m[nt][c] - ref);
-          m[nt][c] = mn;
-          float sum = 0.f;
+          mx[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+          mx[nt][c] *= fac[nt][c];
+          over |= mx[nt][c] > m[nt][c] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v = mx[nt][c];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float mn = fmaxf(m[nt][c], v);
+            const float corr = mn == -CUDART_INF_F ? 1.f : fast_exp2(m[nt][c] - mn);
+            m[nt][c] = mn;
+            l[nt][c] *= corr;
+#pragma unroll
+            for (int j = 0; j < kMma; ++j) o[nt][j][c] *= corr, o[nt][j][c + 2] *= corr;
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float bias = m[nt][c] == -CUDART_INF_F ? 0.f : kPShift - m[nt][c];
 #pragma unroll
           for (int sl = 0; sl < 2; ++sl)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float e = fast_exp2(s[sl][nt][c + 2 * r] - ref + kPShift);
+              const float e = fast_exp2(fmaf(s[sl][nt][c + 2 * r], fac[nt][c], bias));
               s[sl][nt][c + 2 * r] = e;
-              sum += e;
+              l[nt][c] += e;
             }
-          l[nt][c] = fmaf(l[nt][c], corr[nt][c], sum);
         }
-      if (__any_sync(0xffffffffu, raised)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < kMma; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][j][e] *= corr[nt][e & 1];
-      }
+      uint32_t pb[2][NT][2];
 #pragma unroll
       for (int sl = 0; sl < 2; ++sl)
 #pragma unroll
@@ -542,73 +621,85 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
         }
       }
       __syncwarp();
-      if (iu < c_end) issue();
+      issue();
     }
 
-    // ---- the warps' sums of the segment joined, eight heads at a time ----
-    // Head pair tig at a distance of 2 D + 2 floats, and the float pairs of
-    // row group g turned by 8 or more, so that a store touches every bank once.
-    constexpr int kPair = 2 * D + 2, kRow = D / 8;
-    const int gpairs = (min(G, 8) + 1) / 2;
+    // ---- the warps' sums of the segment joined, a few heads at a time ----
+    // Head pairs at a distance of 2 D + 4 floats, and the floats of row group g
+    // turned by a multiple of 8, so that a store touches every bank once.
+    constexpr int kPair = 2 * D + 4, kRow = D / 8, kHeads = kMergeHeads;
+    const int gpairs = (min(G, kHeads) + 1) / 2;
     const int turn = D == 64 ? 0 : (D == 128 ? 8 * ((g >> 1) & 1) : 8 * (g & 3));
     const bool active = first < se;
     const bool complete = item_b >= sb && item_b + sc.nst <= se;
     const int64_t out_row = static_cast<int64_t>(L.seq0 + sc.seq) * p.num_q_heads + sc.head * G;
-    const int part_slot = sb == c_begin ? 0 : 1;
+    const int part_slot = sb == s_begin ? 0 : 1;
     float* part = L.part + (static_cast<int64_t>(blockIdx.x) * 2 + part_slot) * (G * (D + 2));
-    asm volatile("cp.async.wait_group 0;" ::: "memory");  // the next segment's queries
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0) __syncthreads();
-      const int heads = min(8, G - nt * 8);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 4);
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 8);
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 16);
-        const int h = 2 * tig + c;
-        if (g == 0) stat[warp * 8 + h] = active ? make_float2(m[nt][c], l[nt][c]) : make_float2(-CUDART_INF_F, 0.f);
-        if (active && h < heads) {
-          float* row = merge + warp * (gpairs * kPair) + tig * kPair + c * D + g * kRow;
-#pragma unroll
-          for (int j = 0; j < kMma; ++j)
-            *reinterpret_cast<float2*>(row + ((2 * j + turn) & (kRow - 1))) = make_float2(o[nt][j][c], o[nt][j][c + 2]);
-        }
       }
-      __syncthreads();
-      for (int i = tid; i < heads * D / 2; i += kThreads) {
-        const int h = i / (D / 2), d = (i - h * (D / 2)) * 2;
-        float M = -CUDART_INF_F;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w * 8 + h].x);
-        const float ref = M == -CUDART_INF_F ? 0.f : M;
-        const int rg = d / kRow;
-        const int rt = D == 64 ? 0 : (D == 128 ? 8 * ((rg >> 1) & 1) : 8 * (rg & 3));
-        const int at = (h >> 1) * kPair + (h & 1) * D + rg * kRow + ((d - rg * kRow + rt) & (kRow - 1));
-        float lsum = 0.f, x = 0.f, y = 0.f;
+      for (int h0 = 0; h0 < 8; h0 += kHeads) {
+        const int heads = min(kHeads, G - nt * 8 - h0);  // of this round
+        if (heads <= 0) break;
+        if (nt > 0 || h0 > 0) __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 st = stat[w * 8 + h];
-          if (st.y != 0.f) {  // a warp without tokens wrote nothing
-            const float f = fast_exp2(st.x - ref);
-            const float2 v = *reinterpret_cast<const float2*>(merge + w * (gpairs * kPair) + at);
-            lsum = fmaf(f, st.y, lsum);
-            x = fmaf(f, v.x, x);
-            y = fmaf(f, v.y, y);
+        for (int c = 0; c < 2; ++c) {
+          const int h = 2 * tig + c - h0;
+          if (h >= 0 && h < kHeads) {
+            if (g == 0) stat[warp * 8 + h] = active ? make_float2(m[nt][c], l[nt][c]) : make_float2(-CUDART_INF_F, 0.f);
+            if (active && h < heads) {
+              float* row = merge + warp * (gpairs * kPair) + (h >> 1) * kPair + c * D + g * kRow;
+#pragma unroll
+              for (int j = 0; j < kMma; ++j)
+                *reinterpret_cast<float2*>(row + ((2 * j + turn) & (kRow - 1))) =
+                    make_float2(o[nt][j][c], o[nt][j][c + 2]);
+            }
           }
         }
-        const int head = nt * 8 + h;
-        if (complete) {
-          const float inv = lsum != 0.f ? p.v_scale / lsum : 0.f;
-          const int64_t at_out = (out_row + head) * D + d;
-          if (p.out_bf16)
-            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at_out) =
-                __floats2bfloat162_rn(x * inv, y * inv);
-          else
-            *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at_out) = make_float2(x * inv, y * inv);
-        } else {
-          *reinterpret_cast<float2*>(part + 2 * G + head * D + d) = make_float2(x, y);
-          if (d == 0) *reinterpret_cast<float2*>(part + 2 * head) = make_float2(M, lsum);
+        __syncthreads();
+        for (int i = tid; i < heads * D / 4; i += kThreads) {
+          const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+          float2 st[kWarps];
+          float M = -CUDART_INF_F;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            st[w] = stat[w * 8 + h];
+            M = fmaxf(M, st[w].x);
+          }
+          const float ref = M == -CUDART_INF_F ? 0.f : M;
+          const int rg = d / kRow;
+          const int rt = D == 64 ? 0 : (D == 128 ? 8 * ((rg >> 1) & 1) : 8 * (rg & 3));
+          const float* at = merge + (h >> 1) * kPair + (h & 1) * D + rg * kRow + ((d - rg * kRow + rt) & (kRow - 1));
+          float lsum = 0.f;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            if (st[w].y != 0.f) {  // a warp without tokens wrote nothing
+              const float f = fast_exp2(st[w].x - ref);
+              const float4 v = *reinterpret_cast<const float4*>(at + w * (gpairs * kPair));
+              lsum = fmaf(f, st[w].y, lsum);
+              x.x = fmaf(f, v.x, x.x);
+              x.y = fmaf(f, v.y, x.y);
+              x.z = fmaf(f, v.z, x.z);
+              x.w = fmaf(f, v.w, x.w);
+            }
+          }
+          const int head = nt * 8 + h0 + h;
+          if (complete) {
+            const float inv = lsum != 0.f ? p.v_scale / lsum : 0.f;
+            store4(p, (out_row + head) * D + d, x, inv);
+          } else {
+            float* q = part + 2 * G + head * D + d;
+            *reinterpret_cast<float2*>(q) = make_float2(x.x, x.y);
+            *reinterpret_cast<float2*>(q + 2) = make_float2(x.z, x.w);
+            if (d == 0) *reinterpret_cast<float2*>(part + 2 * head) = make_float2(M, lsum);
+          }
         }
       }
     }
@@ -630,7 +721,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
         const float* base = L.part;
         auto part_of = [&](int k) {
           const int c = c0 + k;
-          return base + (static_cast<int64_t>(c) * 2 + (cta_begin(c) >= item_b ? 0 : 1)) * (G * (D + 2));
+          return base + (static_cast<int64_t>(c) * 2 + (cta_begin(c) >= item_b - kLead ? 0 : 1)) * (G * (D + 2));
         };
         // groups of threads take every ngroups-th part; then the groups are added
         const int width = min(kThreads, G * D / 4);  // threads that cover the item's outputs, 4 each
@@ -670,28 +761,23 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
           }
           if (grp == 0) {
             const float inv = lsum != 0.f ? p.v_scale / lsum : 0.f;
-            const int64_t at_out = (out_row + h) * D + d;
-            if (p.out_bf16) {
-              __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at_out);
-              dst[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-              dst[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            } else {
-              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at_out) =
-                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            }
+            store4(p, (out_row + h) * D + d, acc, inv);
           }
         }
       }
     }
+    if (!more) break;
+    convert_q(qb ^ 1);
     __syncthreads();  // the merge area and the flag are free again
-    sb = se;
+    sb = se + kLead;
     sc = next;
     qb ^= 1;
   }
-  // a wait that gave up: what is in flight still has to land before the CTA ends
-  for (; in_flight > 0; --in_flight) {
-    (void)ptx::mbar_wait(&full[use_slot], use_parity, kWaitLimitNs);
-    if (++use_slot == L.stages) use_slot = 0, use_parity ^= 1u;
+  // (every query copy has landed unless a wait of 2 s gave up; such a copy is given another 2 s)
+  if (__syncthreads_or(aborted)) {
+    if (tid == 0)
+      for (int b = 0; b < 2; ++b) (void)ptx::mbar_wait(&q_full[b], ((q_parity >> b) & 1u) ^ 1u, kWaitLimitNs);
+    __syncthreads();
   }
 }
 
@@ -699,18 +785,20 @@ namespace {
 
 using fp4_decode_detail::Launch;
 
-const void* kernel_for(int head_dim, int group) {
-  if (head_dim == 64)
-    return group <= 8 ? reinterpret_cast<const void*>(&fp4_decode_kernel<64, 1>)
-                      : reinterpret_cast<const void*>(&fp4_decode_kernel<64, 2>);
-  if (head_dim == 128)
-    return group <= 8 ? reinterpret_cast<const void*>(&fp4_decode_kernel<128, 1>)
-                      : reinterpret_cast<const void*>(&fp4_decode_kernel<128, 2>);
-  return reinterpret_cast<const void*>(&fp4_decode_kernel<256, 1>);
+template <int D, int NT>
+const void* kernel_of(int eff_log) {
+  if (eff_log == 5) return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, 5>);
+  if (eff_log == 4) return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, 4>);
+  return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, -1>);
+}
+const void* kernel_for(int head_dim, int group, int eff_log) {
+  if (head_dim == 64) return group <= 8 ? kernel_of<64, 1>(eff_log) : kernel_of<64, 2>(eff_log);
+  if (head_dim == 128) return group <= 8 ? kernel_of<128, 1>(eff_log) : kernel_of<128, 2>(eff_log);
+  return kernel_of<256, 1>(eff_log);
 }
 
 // CTAs that a launch has at most: what its part slots are sized for.
-int64_t max_ctas(int head_dim, int group) { return device_sm_count() * (head_dim <= 128 && group <= 8 ? 2 : 1); }
+int64_t max_ctas(int head_dim, int group) { return device_sm_count() * (head_dim <= 128 && group <= 8 ? 4 : 2); }
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -719,6 +807,39 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // 16 query heads of 256 dims would need more registers than a thread has:
 // they are taken as two kv heads of 8 that share their pages.
 int per_cache_head(int head_dim, int group) { return head_dim == 256 && group == 16 ? 2 : 1; }
+
+// CTAs of a kernel that an SM holds with this much dynamic shared memory, the
+// answers kept for the devices and sizes that come by.
+cudaError_t fp4_occupancy(const void* fn, int threads, int smem, int* per_sm) {
+  struct Entry {
+    const void* fn;
+    int device, smem, per_sm;
+  };
+  static std::mutex mu;
+  static Entry kept[64];
+  static int n = 0, next = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  for (int i = 0; i < n; ++i)
+    if (kept[i].fn == fn && kept[i].device == dev && kept[i].smem == smem) {
+      *per_sm = kept[i].per_sm;
+      return cudaSuccess;
+    }
+  // the attribute only ever grows: another thread's launch may count on it
+  cudaFuncAttributes at{};
+  if ((e = cudaFuncGetAttributes(&at, fn)) != cudaSuccess) return e;
+  if (smem > at.maxDynamicSharedSizeBytes &&
+      (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+    return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, fn, threads, smem)) != cudaSuccess) return e;
+  if (*per_sm < 1) return cudaErrorInvalidConfiguration;
+  kept[next] = Entry{fn, dev, smem, *per_sm};
+  next = (next + 1) % 64;
+  if (n < 64) ++n;
+  return cudaSuccess;
+}
 
 size_t fp4_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
   using namespace fp4_decode_detail;
@@ -734,7 +855,9 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
   const int split = per_cache_head(head_dim, p.num_q_heads / p.num_kv_heads);
   const int hkv = p.num_kv_heads * split;
   const int G = p.num_q_heads / hkv;
-  const void* fn = kernel_for(head_dim, G);
+  const int eff = p.block_size < kUnit ? p.block_size : kUnit;
+  const int eff_log = __builtin_ctz(static_cast<unsigned>(eff));
+  const void* fn = kernel_for(head_dim, G, eff_log);
   for (int seq0 = 0; seq0 < p.num_seqs; seq0 += kMaxSeqs) {
     Launch L{};
     L.p = p;
@@ -745,19 +868,13 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     L.cache_heads = p.num_kv_heads;
     L.per_cache_head = split;
     L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
-    const int eff = p.block_size < kUnit ? p.block_size : kUnit;
-    L.eff_log = __builtin_ctz(static_cast<unsigned>(eff));
+    L.eff_log = eff_log;
     L.tile_bytes = fp4_tile_bytes(p.block_size, head_dim);
     L.piece_bytes = static_cast<int>(fp4_tile_bytes(eff, head_dim));
     L.kv_bytes = (kUnit / eff) * L.piece_bytes;
-    // as deep a ring as leaves room for the CTAs of an SM
-    const int64_t unit = static_cast<int64_t>(kWarps) * 2 * L.kv_bytes;
-    const int64_t merge = static_cast<int64_t>(kWarps) * ((G < 8 ? G : 8) + 1) / 2 * (2 * head_dim + 2) * 4;
-    const int64_t fixed = (merge > kThreads * 20 ? merge : kThreads * 20) + 2 * G * head_dim * 2 + 8 * L.nseq + 2048;
-    const int64_t room = (head_dim <= 128 && G <= 8 ? 113 : 226) * 1024 - fixed;
-    L.stages = static_cast<int>(room / unit);
-    L.stages = L.stages < 2 ? (2 * unit + fixed <= 226 * 1024 ? 2 : 1) : (L.stages > kMaxStages ? kMaxStages : L.stages);
-    int64_t off = L.stages * unit;
+    const int64_t merge =
+        static_cast<int64_t>(kWarps) * (((G < kMergeHeads ? G : kMergeHeads) + 1) / 2) * (2 * head_dim + 4) * 4;
+    int64_t off = static_cast<int64_t>(kWarps) * ring_stages(head_dim, G <= 8 ? 1 : 2) * 2 * L.kv_bytes;
     auto take = [&](int64_t bytes) {
       const int64_t at = off;
       off += round_up(bytes, 16);
@@ -766,21 +883,24 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     L.off_merge = take(merge > kThreads * 20 ? merge : kThreads * 20);
     L.off_stat = take(kWarps * 8 * 8);
     L.off_q = take(2 * G * head_dim * 2);
+    L.off_qfac = take(2 * 16 * 4);
     L.off_prefix = take((L.nseq + 1) * 4);
     L.off_lens = take(L.nseq * 4);
-    L.off_bar = take(kWarps * kMaxStages * 8);
+    L.off_bar = take(2 * 8);
     L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
     const int64_t seqs = p.num_seqs < kMaxSeqs ? p.num_seqs : kMaxSeqs;
     L.part = reinterpret_cast<float*>(p.ws + 256 + round_up(seqs * hkv * 4, 256));
     // at least a unit for every warp, as far as the longest context allows
-    const int64_t most = static_cast<int64_t>(L.nseq) * hkv * ((p.max_context_len + kUnit - 1) / kUnit + 1);
+    const int64_t most = static_cast<int64_t>(L.nseq) * hkv * ((p.max_context_len + kUnit - 1) / kUnit);
     int64_t ctas = (most + kWarps - 1) / kWarps;
     const int64_t items = static_cast<int64_t>(L.nseq) * hkv;
     if (ctas < items) ctas = items;
-    const int64_t cap = max_ctas(head_dim, G);
-    if (ctas > cap) ctas = cap;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(off));
+    int per_sm = 0;
+    cudaError_t e = fp4_occupancy(fn, kThreads, static_cast<int>(off), &per_sm);
     if (e != cudaSuccess) return e;
+    int64_t cap = device_sm_count() * per_sm;  // all of them at work at once: their shares are equal
+    if (cap > max_ctas(head_dim, G)) cap = max_ctas(head_dim, G);
+    if (ctas > cap) ctas = cap;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);
