@@ -21,6 +21,8 @@ pa_status check_pool(int32_t num_blocks, int32_t block_size, int32_t num_kv_head
   if (num_blocks <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0) return PA_ERR_INVALID_ARG;
   if ((block_size & (block_size - 1)) != 0 || block_size > 256) return PA_ERR_UNSUPPORTED;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return PA_ERR_UNSUPPORTED;
+  // tiles are numbered in 32 bits by the attention kernels
+  if (static_cast<int64_t>(num_blocks) * num_kv_heads >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 

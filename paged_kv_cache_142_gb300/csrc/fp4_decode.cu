@@ -69,8 +69,8 @@ struct Launch {
   int bs_log;
   int piece_bytes;         // of one piece in shared memory
   int kv_bytes;            // of one unit's K (or V) in shared memory
-  int off_merge, off_stat, off_q, off_qfac, off_prefix, off_lens, off_bar;
-  int64_t tile_bytes;
+  int off_merge, off_stat, off_qraw, off_q, off_qfac, off_prefix, off_lens, off_bar;
+  uint32_t tile_bytes;
   int32_t* counters;       // [nseq * num_kv_heads], zero between launches
   float* part;             // [2 * CTAs][G * (D + 2)]
 };
@@ -169,20 +169,21 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   unsigned char* ring = smem + warp * (kStages * 2 * kv_bytes);
   float* merge = reinterpret_cast<float*>(smem + L.off_merge);     // [warp][G][D + pad]
   float2* stat = reinterpret_cast<float2*>(smem + L.off_stat);     // [warp][8]: maximum, sum
-  __nv_bfloat16* qbuf = reinterpret_cast<__nv_bfloat16*>(smem + L.off_q);  // [2][G * D]
+  __nv_bfloat16* qraw = reinterpret_cast<__nv_bfloat16*>(smem + L.off_qraw);  // [G * D], the next segment's
+  uint4* qf16 = reinterpret_cast<uint4*>(smem + L.off_q);  // [NT][D / 32][32 lanes]: operands of Q.K^T
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.off_prefix);       // [nseq + 1] places before a sequence
   int32_t* lens = reinterpret_cast<int32_t*>(smem + L.off_lens);
-  float* qfac = reinterpret_cast<float*>(smem + L.off_qfac);               // [2][16] score factors
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L.off_bar);         // [2]
+  float* qfac = reinterpret_cast<float*>(smem + L.off_qfac);               // [16] score factors
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L.off_bar);         // the next segment's queries
   __shared__ int warp_sums[kWarps];
   __shared__ int last_flag;
 
   ptx::griddep_launch_dependents();
   if (tid == 0) {
-    ptx::mbar_init(&q_full[0], 1);
-    ptx::mbar_init(&q_full[1], 1);
+    ptx::mbar_init(q_full, 1);
     ptx::mbar_init_fence();
   }
+  for (int i = tid; i < NT * (D / 32) * 32; i += kThreads) qf16[i] = make_uint4(0, 0, 0, 0);  // heads past G
   ptx::griddep_wait();
 
   // ---- places before every sequence: kLead and one for every unit of each of
@@ -256,87 +257,110 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
 
   // ---- this warp's stream of units: c_begin + warp, + kWarps, ... ----
   const int bs = 1 << L.bs_log;
-  Cursor ic{};                     // the next unit to be fetched
-  int iu = c_begin + warp;
-  int32_t phys = 0;                // its page, this lane's piece
+  Cursor ic{};              // the next unit to be fetched
+  int iu = c_begin + warp;  // its place
+  int ilen = 0;             // its sequence's length
+  const int32_t* itable = nullptr;
+  int32_t phys = 0;         // its page, this lane's piece
   auto fetch_table = [&]() {
     const int tok = ic.st * kUnit + (lane << eff_log);
-    phys = 0;
-    if (lane < npieces && tok < lens[ic.seq]) {
-      phys = __ldg(p.block_tables + static_cast<int64_t>(L.seq0 + ic.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+    if (lane < npieces && tok < ilen) phys = __ldg(itable + (tok >> L.bs_log));
+  };
+  auto enter = [&]() {  // ic is in another sequence
+    ilen = lens[ic.seq];
+    itable = p.block_tables + static_cast<int64_t>(L.seq0 + ic.seq) * p.max_blocks_per_seq;
+  };
+  auto next_unit = [&]() {
+    iu += kWarps;
+    if (iu >= c_end) return;
+    ic.st += kWarps;
+    if (ic.st >= ic.nst) {  // into the next (sequence, kv head), past its lead
+      ic.st -= kWarps;
+      advance(ic, kWarps);
+      while (ic.st < 0) {
+        iu += kWarps;
+        if (iu >= c_end) return;
+        advance(ic, kWarps);
+      }
+      enter();
     }
+    fetch_table();
   };
   auto copy16 = [](uint32_t dst, const uint8_t* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   };
-  auto next_unit = [&]() {
-    do {
-      iu += kWarps;
-      if (iu >= c_end) return;
-      advance(ic, kWarps);
-    } while (ic.st < 0);
-    fetch_table();
-  };
-  int issue_slot = 0, use_slot = 0;
+  const uint32_t ring_lane = ptx::smem_addr(ring) + lane * 16;
+  const uint8_t* const k_lane = p.k_cache + lane * 16;
+  const uint8_t* const v_lane = p.v_cache + lane * 16;
+  const uint32_t tile_bytes = L.tile_bytes;
+  uint32_t issue_at = 0;  // the ring place to be filled
+  int use_slot = 0;
   // fetches the next unit, or nothing at the end: one group of copies each time
   auto issue = [&]() {
     if (iu < c_end) {
-      const int left = lens[ic.seq] - ic.st * kUnit;
-      const int nv = min(npieces, (left + eff - 1) >> eff_log);
-      if (lane < nv && (phys < 0 || phys >= p.num_blocks)) {  // never read outside the pool
-        atomicExch(p.err, kDevErrInvalidArg);
+      const int nv = (ilen - ic.st * kUnit + eff - 1) >> eff_log;  // pieces that hold tokens, or more
+      if (lane < min(nv, npieces) && static_cast<uint32_t>(phys) >= static_cast<uint32_t>(p.num_blocks)) {
+        atomicExch(p.err, kDevErrInvalidArg);  // never read outside the pool
         phys = 0;
       }
-      const uint32_t dst = ptx::smem_addr(ring + issue_slot * 2 * kv_bytes);
-      const int cache_head = L.per_cache_head == 1 ? ic.head : ic.head / L.per_cache_head;
-      auto tile_of = [&](int page) { return (static_cast<int64_t>(page) * L.cache_heads + cache_head) * L.tile_bytes; };
+      const uint32_t dst = ring_lane + issue_at;
+      const uint32_t cache_head = L.per_cache_head == 1 ? ic.head : ic.head / L.per_cache_head;
+      // this lane's piece's tile (fewer than 2^31 of them in a pool)
+      const uint32_t mine = static_cast<uint32_t>(phys) * L.cache_heads + cache_head;
       if (EL >= 0) {
         // 16-byte chunks: kCodes a lane of a unit's codes, piece after piece,
         // then one of its scales in the first kScales lanes
         constexpr int kCodes = kUnit * (D / 2) / 512, kScales = kUnit * (D / 16) / 16;
         constexpr int kPieces = EL == 4 ? 2 : 1, kPerPiece = kCodes / kPieces;
-        constexpr int kEff = kUnit / kPieces;
+        constexpr int kEff = kUnit / kPieces, kPieceBytes = kEff * (D / 2 + D / 16);
         const int row = EL == 5 ? (ic.st * kUnit) & (bs - 1) : 0;  // of the piece in its tile
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, mine, j)) * tile_bytes + row * (D / 2);
           if (j < nv) {
-            const int64_t at = tile_of(__shfl_sync(0xffffffffu, phys, j)) + row * (D / 2) + lane * 16;
-            const uint32_t d = dst + j * (kEff * (D / 2 + D / 16)) + lane * 16;
 #pragma unroll
             for (int i = 0; i < kPerPiece; ++i) {
-              copy16(d + i * 512, p.k_cache + at + i * 512);
-              copy16(d + kv_bytes + i * 512, p.v_cache + at + i * 512);
+              copy16(dst + j * kPieceBytes + i * 512, k_lane + at + i * 512);
+              copy16(dst + j * kPieceBytes + kv_bytes + i * 512, v_lane + at + i * 512);
             }
           }
         }
-        const int j = kPieces == 1 ? 0 : lane / (kScales / kPieces);  // the piece of this lane's scales
-        const int page = __shfl_sync(0xffffffffu, phys, j & 1);
+        // a piece's scale chunks: lanes c of kScales / kPieces
+        constexpr int kSc = kScales / kPieces;
+        const int j = kPieces == 1 ? 0 : (lane / kSc) & 1;
+        const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, mine, j)) * tile_bytes + bs * (D / 2) +
+                            row * (D / 16) - j * (kSc * 16);
         if (lane < kScales && j < nv) {
-          const int c = (kPieces == 1 ? lane : lane % (kScales / kPieces)) * 16;
-          const int64_t at = tile_of(page) + static_cast<int64_t>(bs) * (D / 2) + row * (D / 16) + c;
-          const uint32_t d = dst + j * (kEff * (D / 2 + D / 16)) + kEff * (D / 2) + c;
-          copy16(d, p.k_cache + at);
-          copy16(d + kv_bytes, p.v_cache + at);
+          const uint32_t d = dst + j * (kPieceBytes - kSc * 16) + kEff * (D / 2);
+          copy16(d, k_lane + at);
+          copy16(d + kv_bytes, v_lane + at);
         }
       } else {
+        const int n = min(nv, npieces);
 #pragma unroll 1
-        for (int j = 0; j < nv; ++j) {  // whole tiles of a few hundred bytes
-          const int64_t at = tile_of(__shfl_sync(0xffffffffu, phys, j));
-          for (int c = lane * 16; c < piece_bytes; c += 512) {
-            copy16(dst + j * piece_bytes + c, p.k_cache + at + c);
-            copy16(dst + kv_bytes + j * piece_bytes + c, p.v_cache + at + c);
+        for (int j = 0; j < n; ++j) {  // whole tiles of a few hundred bytes
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, mine, j)) * tile_bytes;
+          for (int c = 0; c + lane * 16 < piece_bytes; c += 512) {
+            copy16(dst + j * piece_bytes + c, k_lane + at + c);
+            copy16(dst + j * piece_bytes + kv_bytes + c, v_lane + at + c);
           }
         }
       }
-      if (++issue_slot == kStages) issue_slot = 0;
+      issue_at = issue_at + 2 * kv_bytes == kStages * 2 * kv_bytes ? 0 : issue_at + 2 * kv_bytes;
       next_unit();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if (iu < c_end) {
     locate(iu, ic);
-    if (ic.st < 0) next_unit();
-    else fetch_table();
+    while (ic.st < 0 && iu < c_end) {
+      iu += kWarps;
+      if (iu < c_end) advance(ic, kWarps);
+    }
+    if (iu < c_end) {
+      enter();
+      fetch_table();
+    }
   }
   for (int s = 0; s < kStages; ++s) issue();
 
@@ -370,29 +394,28 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   v_s1 += g * D / 128;
 
   // ---- queries: a (sequence, kv head)'s rows, fetched one segment ahead ----
-  // They are turned into f16 in place once the segment before is done.
+  // They are turned into f16, in the order of the operands, once the segment
+  // before is done.
   const int q_chunks = G * D / 8;
-  auto fetch_q = [&](const Cursor& c, int b) {  // one run of bytes
+  auto fetch_q = [&](const Cursor& c) {  // one run of bytes
     if (tid == 0) {
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
                                  (static_cast<int64_t>(L.seq0 + c.seq) * p.num_q_heads + c.head * G) * D;
-      ptx::fence_proxy_async_smem();  // the buffer was written by ordinary stores before
-      ptx::mbar_arrive_expect_tx(&q_full[b], G * D * 2);
-      ptx::bulk_g2s(qbuf + b * G * D, src, G * D * 2, &q_full[b], ptx::policy_evict_first());
+      ptx::mbar_arrive_expect_tx(q_full, G * D * 2);
+      ptx::bulk_g2s(qraw, src, G * D * 2, q_full, ptx::policy_evict_first());
     }
   };
   bool aborted = false;
-  uint32_t q_parity = 0;  // one bit for each buffer
-  auto convert_q = [&](int b) {
-    if (!ptx::mbar_wait(&q_full[b], (q_parity >> b) & 1u, kWaitLimitNs)) {
+  uint32_t q_parity = 0;
+  auto convert_q = [&]() {
+    if (!ptx::mbar_wait(q_full, q_parity, kWaitLimitNs)) {
       aborted = true;  // the output is then undefined
       atomicExch(p.err, kDevErrTimeout);
     }
-    q_parity ^= 1u << b;
+    q_parity ^= 1u;
     for (int i0 = 0; i0 < q_chunks; i0 += kThreads) {
       const int i = i0 + tid;
-      uint4* at = reinterpret_cast<uint4*>(qbuf + b * G * D + i * 8);
-      const uint4 v = i < q_chunks ? *at : make_uint4(0, 0, 0, 0);
+      const uint4 v = i < q_chunks ? *reinterpret_cast<const uint4*>(qraw + i * 8) : make_uint4(0, 0, 0, 0);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t top = 0;
 #pragma unroll
@@ -410,10 +433,11 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       for (int e = 0; e < 4; ++e)
         r[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
       if (i < q_chunks) {
-        *at = make_uint4(r[0], r[1], r[2], r[3]);
-        if (i % (D / 8) == 0)
+        const int h = i / (D / 8), c = i % (D / 8);  // head, eight dims of it
+        qf16[((h >> 3) * (D / 32) + c % (D / 32)) * 32 + (h & 7) * 4 + c / (D / 32)] = make_uint4(r[0], r[1], r[2], r[3]);
+        if (c == 0)
           // (not zero: a masked -inf times it stays -inf)
-          qfac[b * 16 + i / (D / 8)] =
+          qfac[h] =
               fmaxf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 1.2e-38f);
       }
     }
@@ -424,10 +448,9 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   const int s_begin = sc.st < 0 ? c_begin - sc.st : c_begin;  // its first unit
   if (sc.st < 0) sc.st = 0;
   if (s_begin >= c_end) return;
-  fetch_q(sc, 0);
-  convert_q(0);
+  fetch_q(sc);
+  convert_q();
   __syncthreads();
-  int qb = 0;
   for (int sb = s_begin; sb < c_end;) {
     const int item_b = sb - sc.st;                    // the item's first unit
     const int se = min(c_end, item_b + sc.nst);       // the segment's end
@@ -436,25 +459,15 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
     if (more) {
       next.st = sc.nst - 1;
       advance(next, 1 + kLead);
-      fetch_q(next, qb ^ 1);
+      fetch_q(next);
     }
     const int len = lens[sc.seq];
 
-    // this thread's part of the queries: head g (and g + 8), dims tig * D / 4 ..
-    uint32_t qf[NT][kMma][2];
     float fac[NT][2];  // score factor of the thread's columns, heads 2 tig and 2 tig + 1
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + g;
-      const uint4* src = reinterpret_cast<const uint4*>(qbuf + qb * G * D + h * D + tig * (D / 4));
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 v = h < G ? src[i] : make_uint4(0, 0, 0, 0);
-        qf[nt][2 * i][0] = v.x, qf[nt][2 * i][1] = v.y, qf[nt][2 * i + 1][0] = v.z, qf[nt][2 * i + 1][1] = v.w;
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) fac[nt][c] = nt * 8 + 2 * tig + c < G ? qfac[qb * 16 + nt * 8 + 2 * tig + c] : 1.f;
-    }
+      for (int c = 0; c < 2; ++c) fac[nt][c] = nt * 8 + 2 * tig + c < G ? qfac[nt * 8 + 2 * tig + c] : 1.f;
 
     float o[NT][kMma][4];
     float m[NT][2], l[NT][2];
@@ -479,41 +492,47 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       const unsigned char* vb = kb + kv_bytes;
       const int left = len - (u - item_b) * kUnit;  // tokens from this unit on
 
-      // S^T of two slices of 16 tokens
+      // S^T of two slices of 16 tokens, side by side
       float s[2][NT][4];
+      Words<D / 8> kw[2][2];  // [slice][rows g, g + 8]: the codes of the thread's dims
+      uint32_t ks[2][2];      // their scales: D / 64 bytes
 #pragma unroll
-      for (int sl = 0; sl < 2; ++sl) {
+      for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          kw[sl][r].load(kb + k_c0 + sl * c16 + r * c8);
+          const unsigned char* ps = kb + k_s0 + sl * s16 + r * s8;
+          if (D == 64) ks[sl][r] = ps[0];
+          else if (D == 128) ks[sl][r] = *reinterpret_cast<const uint16_t*>(ps);
+          else ks[sl][r] = *reinterpret_cast<const uint32_t*>(ps);
+        }
+#pragma unroll
+      for (int sl = 0; sl < 2; ++sl)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[sl][nt][e] = 0.f;
-        Words<D / 8> ka, kc;  // codes of rows g and g + 8
-        ka.load(kb + k_c0 + sl * c16);
-        kc.load(kb + k_c0 + sl * c16 + c8);
-        uint32_t sa = 0, sc8 = 0;  // their scales: D / 64 bytes
-        const unsigned char* ps = kb + k_s0 + sl * s16;
-        if (D == 64) {
-          sa = ps[0], sc8 = ps[s8];
-        } else if (D == 128) {
-          sa = *reinterpret_cast<const uint16_t*>(ps), sc8 = *reinterpret_cast<const uint16_t*>(ps + s8);
-        } else {
-          sa = *reinterpret_cast<const uint32_t*>(ps), sc8 = *reinterpret_cast<const uint32_t*>(ps + s8);
-        }
 #pragma unroll
-        for (int w = 0; w < kKWords; ++w) {
-          // words 2i and 2i + 1 are group i of the thread's dims
-          const uint32_t pa = fp4::scales_to_f16(sa >> (16 * (w >> 2))), pc = fp4::scales_to_f16(sc8 >> (16 * (w >> 2)));
-          const uint32_t ma = (w & 2) ? __byte_perm(pa, 0, 0x3232) : __byte_perm(pa, 0, 0x1010);
-          const uint32_t mc = (w & 2) ? __byte_perm(pc, 0, 0x3232) : __byte_perm(pc, 0, 0x1010);
-          uint32_t ha[4], hc[4];
-          fp4::codes_to_f16(ka.w[w], ha);
-          fp4::codes_to_f16(kc.w[w], hc);
+      for (int w = 0; w < kKWords; ++w) {
+        uint4 q[NT];  // head g (and g + 8), eight dims
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ha[e] = fp4::mul_f16x2(ha[e], ma), hc[e] = fp4::mul_f16x2(hc[e], mc);
+        for (int nt = 0; nt < NT; ++nt) q[nt] = qf16[(nt * (D / 32) + w) * 32 + lane];
+#pragma unroll
+        for (int sl = 0; sl < 2; ++sl) {
+          uint32_t h[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            // words 2i and 2i + 1 are group i of the thread's dims
+            const uint32_t pair = fp4::scales_to_f16(ks[sl][r] >> (16 * (w >> 2)));
+            const uint32_t sc2 = (w & 2) ? __byte_perm(pair, 0, 0x3232) : __byte_perm(pair, 0, 0x1010);
+            fp4::codes_to_f16(kw[sl][r].w[w], h[r]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[r][e] = fp4::mul_f16x2(h[r][e], sc2);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma(s[sl][nt], ha[0], hc[0], ha[1], hc[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-            mma(s[sl][nt], ha[2], hc[2], ha[3], hc[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+            mma(s[sl][nt], h[0][0], h[1][0], h[0][1], h[1][1], q[nt].x, q[nt].y);
+            mma(s[sl][nt], h[0][2], h[1][2], h[0][3], h[1][3], q[nt].z, q[nt].w);
           }
         }
       }
@@ -767,16 +786,14 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       }
     }
     if (!more) break;
-    convert_q(qb ^ 1);
+    convert_q();
     __syncthreads();  // the merge area and the flag are free again
     sb = se + kLead;
     sc = next;
-    qb ^= 1;
   }
-  // (every query copy has landed unless a wait of 2 s gave up; such a copy is given another 2 s)
+  // a query copy whose wait of 2 s gave up is given another 2 s to land
   if (__syncthreads_or(aborted)) {
-    if (tid == 0)
-      for (int b = 0; b < 2; ++b) (void)ptx::mbar_wait(&q_full[b], ((q_parity >> b) & 1u) ^ 1u, kWaitLimitNs);
+    if (tid == 0) (void)ptx::mbar_wait(q_full, q_parity ^ 1u, kWaitLimitNs);
     __syncthreads();
   }
 }
@@ -869,7 +886,7 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     L.per_cache_head = split;
     L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
     L.eff_log = eff_log;
-    L.tile_bytes = fp4_tile_bytes(p.block_size, head_dim);
+    L.tile_bytes = static_cast<uint32_t>(fp4_tile_bytes(p.block_size, head_dim));
     L.piece_bytes = static_cast<int>(fp4_tile_bytes(eff, head_dim));
     L.kv_bytes = (kUnit / eff) * L.piece_bytes;
     const int64_t merge =
@@ -882,11 +899,12 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     };
     L.off_merge = take(merge > kThreads * 20 ? merge : kThreads * 20);
     L.off_stat = take(kWarps * 8 * 8);
-    L.off_q = take(2 * G * head_dim * 2);
-    L.off_qfac = take(2 * 16 * 4);
+    L.off_qraw = take(G * head_dim * 2);
+    L.off_q = take((G <= 8 ? 8 : 16) * head_dim * 2);
+    L.off_qfac = take(16 * 4);
     L.off_prefix = take((L.nseq + 1) * 4);
     L.off_lens = take(L.nseq * 4);
-    L.off_bar = take(2 * 8);
+    L.off_bar = take(8);
     L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
     const int64_t seqs = p.num_seqs < kMaxSeqs ? p.num_seqs : kMaxSeqs;
     L.part = reinterpret_cast<float*>(p.ws + 256 + round_up(seqs * hkv * 4, 256));
