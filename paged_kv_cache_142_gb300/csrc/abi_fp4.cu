@@ -141,7 +141,7 @@ size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int3
       check_pool(1, block_size, num_kv_heads, head_dim) != PA_OK || num_q_heads % num_kv_heads || head_dim != 128 ||
       !group_ok(num_q_heads, num_kv_heads))
     return 0;
-  return 256;
+  return pa::fp4_prefill_workspace(num_seqs, num_q_heads, num_kv_heads, max_q_len, max_context_len);
 }
 
 pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t num_tokens, const int32_t* cu_q,

@@ -1,0 +1,694 @@
+// Causal attention of chunks of queries over the 4-bit K/V pages (the format:
+// fp4.cuh) on the 5th-generation tensor cores; head_dim 128.
+//
+//   S[128 rows x 128 keys]  = Q K^T,   P = 2^(S f - m),   O[128 x 128] += P V
+// A row is one query head of one token; a CTA takes two tiles of 128 rows
+// (TQ = 128 / G tokens x the G heads of a kv head, each), so every key and
+// value that it restores from 4 bits serves 256 rows.  All operands are f16:
+// code * scale is exact there, the queries are scaled by a power of two per row
+// (their largest magnitude to 2^14, exact down to 2^-28 of it), and the
+// probabilities are rounded to 11 bits (2^-12 each, where bf16 would leave
+// 2^-9); accumulators are fp32 in tensor memory: S of both tiles, O of both.
+// P is written over its S and read from there as the A operand.
+//
+// One CTA per SM, 13 warps, persistent over (tile pair, sequence, kv head,
+// part of the keys):
+//  * warps 8-11 restore: a thread owns one key of a tile.  It reads the key's
+//    64 code bytes and 8 scales through the block table, one tile ahead, and
+//    writes the 128 f16 values in the 128-byte-swizzled layout that the
+//    tensor core reads; then the same for the value row.  They load the
+//    queries too, and the power of two of each row;
+//  * warp 12 issues every product.  Q.K^T of a tile's next step is issued
+//    right behind P.V of its last one, which read P from the same columns, so
+//    while one tile's softmax runs the tensor core works for the other;
+//  * warps 0-3 and 4-7 run the softmax of the first and the second tile, one
+//    row a thread: maximum, exponentials and sum in fp32 (log2 domain).  The
+//    reference of a row is raised only when its maximum passes it by 2^8.
+// What bounds it: the tensor core needs about 2150 clocks for a step's four
+// products, the exponentials and their conversions about 1700 of the SM's
+// issue slots, the restoring about 400.
+//
+// With fewer tile pairs than SMs the keys are cut into parts; a part's rows go
+// to the workspace unnormalised with their maximum and sum, and a second
+// launch adds the parts up in order.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "decode.cuh"
+#include "fp4.cuh"
+#include "ptx.cuh"
+
+namespace pa {
+namespace fp4_prefill_detail {
+
+constexpr int kThreads = 13 * 32;
+constexpr int kTileBytes = 32768;  // 128 rows x 128 f16
+constexpr int kOffQ = 0;           // two tiles: [half of the dims][128 rows][128 bytes]
+constexpr int kOffK = 2 * kTileBytes;
+constexpr int kOffV = kOffK + 2 * kTileBytes;
+constexpr int kOffFac = kOffV + 2 * kTileBytes;   // [2 items][256] row factors
+constexpr int kOffBar = kOffFac + 2 * 256 * 4;
+constexpr int kSmemBytes = kOffBar + 256 + 1024;  // then slack to align the base
+constexpr float kSlack = 8.f;     // the reference is raised past 2^8
+constexpr float kPShift = 6.f;    // probabilities enter P.V times 2^6: below 2^14, none lost before 2^-30
+
+// barriers ([2] each where they have a number)
+enum : int {
+  kQFull = 0, kQFree = 1, kKFull = 2, kKFree = 4, kVFull = 6, kVFree = 8,
+  kSFull = 10, kPFull = 12, kODone = 14, kOFree = 16, kDrain = 18, kNumBars = 19
+};
+static_assert(kNumBars * 8 + 16 <= 256, "barrier area");
+constexpr uint32_t kColO = 256;  // tensor memory: S of the tiles at 0 and 128, then O of the tiles
+
+struct Launch {
+  Fp4AttnParams p;
+  int pairs;       // tile pairs of the longest chunk
+  int parts;       // parts of the keys
+  uint32_t tile_bytes;
+  int bs_log;
+  // parts > 1, rows (sequence * max_q_len + token of the chunk) * heads + head:
+  float* ml;       // [parts][rows][2] maximum (log2), sum
+  float* o;        // [parts][rows][128]
+};
+
+struct Item {
+  int seq, kvh, tok0, qb, pos0;  // first token: in the chunk, in q; position of tok0
+  int ntok;                      // tokens of the pair's two tiles
+  int part, t0, t1;              // tiles of keys
+  int kend;                      // keys that the last token sees
+  int n[2];                      // steps of each tile
+};
+
+template <int G>
+__device__ __forceinline__ bool item_at(const Launch& L, int w, Item& it) {
+  constexpr int TQ = 128 / G;
+  const Fp4AttnParams& p = L.p;
+  const int npairs = p.num_seqs * p.num_kv_heads;
+  // later (longer) tiles first; sequences and heads, then parts, fastest
+  const int per = npairs * L.parts;
+  const int tile = L.pairs - 1 - w / per;
+  int r = w % per;
+  it.part = r / npairs;
+  r -= it.part * npairs;
+  it.seq = r / p.num_kv_heads;
+  it.kvh = r - it.seq * p.num_kv_heads;
+  const int b = p.cu_q[it.seq], n = p.cu_q[it.seq + 1] - b, q0 = p.q_start[it.seq];
+  it.tok0 = tile * 2 * TQ;
+  if (n <= 0 || it.tok0 >= n) return false;
+  const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) << L.bs_log;
+  const int64_t last = static_cast<int64_t>(q0) + n;
+  if (b < 0 || static_cast<int64_t>(b) + n > p.num_tokens || q0 < 0 || n > p.max_q_len || last > table_tokens ||
+      last > p.max_context_len) {
+    if (p.err) atomicExch(p.err, kDevErrInvalidArg);
+    return false;
+  }
+  it.qb = b;
+  it.ntok = min(2 * TQ, n - it.tok0);
+  it.pos0 = q0 + it.tok0;
+  it.kend = it.pos0 + it.ntok;
+  const int tiles = (it.kend + 127) / 128;
+  it.t0 = static_cast<int>(static_cast<int64_t>(tiles) * it.part / L.parts);
+  it.t1 = static_cast<int>(static_cast<int64_t>(tiles) * (it.part + 1) / L.parts);
+  // the first tile's last token may see fewer keys than the second's
+  const int seen0 = (it.pos0 + min(TQ, it.ntok) + 127) / 128;
+  it.n[0] = max(0, min(it.t1, seen0) - it.t0);
+  it.n[1] = it.ntok > TQ ? it.t1 - it.t0 : 0;
+  return true;
+}
+
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
+  if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// kind::f16, f16 operands, fp32 accumulator, M = N = 128; b_mn: B is N-major
+__host__ __device__ constexpr uint32_t idesc_f16(int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (16u << 17) | (8u << 24);
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// A key's or value's row: 64 code bytes and 8 scales.
+struct Row {
+  uint4 c[4];
+  uint2 s;
+};
+
+}  // namespace fp4_prefill_detail
+
+template <int G>
+__global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
+    fp4_prefill_kernel(const __grid_constant__ fp4_prefill_detail::Launch L) {
+  using namespace fp4_prefill_detail;
+  constexpr int TQ = 128 / G;
+  const Fp4AttnParams& p = L.p;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* fac = reinterpret_cast<float*>(smem + kOffFac);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int items = p.num_seqs * p.num_kv_heads * L.pairs * L.parts;
+
+  ptx::griddep_launch_dependents();
+  if (tid == 0) {
+    ptx::mbar_init(&bars[kQFull], 4);
+    ptx::mbar_init(&bars[kQFree], 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kKFull + i], 4);
+      ptx::mbar_init(&bars[kKFree + i], 1);
+      ptx::mbar_init(&bars[kVFull + i], 4);
+      ptx::mbar_init(&bars[kVFree + i], 1);
+      ptx::mbar_init(&bars[kSFull + i], 1);
+      ptx::mbar_init(&bars[kPFull + i], 4);
+      ptx::mbar_init(&bars[kODone + i], 1);
+      ptx::mbar_init(&bars[kOFree + i], 4);
+    }
+    ptx::mbar_init(&bars[kDrain], 1);
+    *gave_up = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == 12) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool aborted = false;
+  ptx::griddep_wait();
+
+  if (warp >= 8 && warp < 12) {
+    // ======================= restoring, queries =======================
+    const int r = tid - 256;  // this thread's key of a tile, and query row of both
+    const int bs = 1 << L.bs_log;
+    const uint32_t sw = r & 7;
+    uint32_t ic = 0, kc = 0;
+    auto locate = [&](const Item& it, const int32_t* table, int t) -> int64_t {
+      const int key = t * 128 + r;
+      if (key >= it.kend) return -1;
+      const int lb = key >> L.bs_log;
+      int phys = __ldg(table + lb);
+      if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
+        if (p.err) atomicExch(p.err, kDevErrInvalidArg);
+        phys = 0;
+      }
+      return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(phys) * p.num_kv_heads + it.kvh) *
+                                  L.tile_bytes);
+    };
+    auto load = [&](Row& x, const uint8_t* cache, int64_t at, int t) {
+      if (at < 0) {  // past the last key: zeros
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.c[i] = make_uint4(0, 0, 0, 0);
+        x.s = make_uint2(0, 0);
+        return;
+      }
+      const int off = (t * 128 + r) & (bs - 1);
+      const uint4* c = reinterpret_cast<const uint4*>(cache + at + off * 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.c[i] = __ldg(c + i);
+      x.s = __ldg(reinterpret_cast<const uint2*>(cache + at + bs * 64 + off * 8));
+    };
+    auto store = [&](unsigned char* tile, const Row& x) {
+      unsigned char* row = tile + (r >> 3) * 2048 + sw * 128;
+      const uint32_t w[16] = {x.c[0].x, x.c[0].y, x.c[0].z, x.c[0].w, x.c[1].x, x.c[1].y, x.c[1].z, x.c[1].w,
+                              x.c[2].x, x.c[2].y, x.c[2].z, x.c[2].w, x.c[3].x, x.c[3].y, x.c[3].z, x.c[3].w};
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {  // scale groups: 16 dims, two 16-byte chunks
+        const uint32_t two = fp4::scales_to_f16((g < 4 ? x.s.x : x.s.y) >> (16 * ((g >> 1) & 1)));
+        const uint32_t sc = (g & 1) ? __byte_perm(two, 0, 0x3232) : __byte_perm(two, 0, 0x1010);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t h[4];
+          fp4::codes_to_f16(w[2 * g + e], h);
+          const int chunk = 2 * g + e;  // of 8 dims
+          *reinterpret_cast<uint4*>(row + (chunk >> 3) * 1024 + (((chunk & 7) ^ sw) << 4)) =
+              make_uint4(fp4::mul_f16x2(h[0], sc), fp4::mul_f16x2(h[1], sc), fp4::mul_f16x2(h[2], sc),
+                         fp4::mul_f16x2(h[3], sc));
+        }
+      }
+    };
+    for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
+      Item it;
+      if (!item_at<G>(L, w, it)) continue;
+      const int n = max(it.n[0], it.n[1]);
+      const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
+      Row kx, vx;
+      int64_t at = -1;
+      if (n > 0) {
+        at = locate(it, table, it.t0);
+        load(kx, p.k_cache, at, it.t0);
+        load(vx, p.v_cache, at, it.t0);
+      }
+      // the queries of the item: row r of both tiles
+      wait(&bars[kQFree], (ic & 1u) ^ 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) break;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int tok = i * TQ + r % TQ;
+        const bool valid = tok < it.ntok;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.q) +
+            (static_cast<int64_t>(it.qb + it.tok0 + tok) * p.num_q_heads + it.kvh * G + r / TQ) * 128);
+        uint32_t top = 0;
+        if (valid) {
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 v = __ldg(src + c);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
+          }
+        }
+        // the power of two that takes the row's largest magnitude to [2^14, 2^15);
+        // 1 for a zero, subnormal or non-finite row
+        const int ex = static_cast<int>(top >> 7);
+        const int shift = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 14 - (ex - 127)));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+        fac[(ic & 1u) * 256 + i * 128 + r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+        unsigned char* row = smem + kOffQ + i * kTileBytes + r * 128;
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = pack_f16(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+          *reinterpret_cast<uint4*>(row + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
+      ++ic;
+      for (int t = 0; t < n; ++t, ++kc) {
+        const int slot = kc & 1u;
+        const uint32_t ph = (kc >> 1) & 1u;
+        const bool more = t + 1 < n;
+        if (more) at = locate(it, table, it.t0 + t + 1);
+        wait(&bars[kKFree + slot], ph ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        store(smem + kOffK + slot * kTileBytes, kx);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kKFull + slot]);
+        if (more) load(kx, p.k_cache, at, it.t0 + t + 1);
+        wait(&bars[kVFree + slot], ph ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        store(smem + kOffV + slot * kTileBytes, vx);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kVFull + slot]);
+        if (more) load(vx, p.v_cache, at, it.t0 + t + 1);
+      }
+    }
+  } else if (warp == 12) {
+    // ============================ products ============================
+    if (lane == 0) {
+      constexpr uint32_t kIdQK = idesc_f16(0), kIdPV = idesc_f16(1);
+      uint32_t ic = 0, kc = 0;
+      uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};  // steps and items of each tile
+      auto qk = [&](int i, int slot) {
+        const unsigned char* qt = smem + kOffQ + i * kTileBytes;
+        const unsigned char* kt = smem + kOffK + slot * kTileBytes;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const int h = k >> 2, k4 = k & 3;
+          ptx::umma_bf16(tmem + i * 128, ptx::smem_desc(qt + h * 16384 + k4 * 32, 16, 1024, ptx::kLayoutSw128),
+                         ptx::smem_desc(kt + h * 1024 + k4 * 32, 16, 2048, ptx::kLayoutSw128), kIdQK, k > 0);
+        }
+        ptx::umma_commit(&bars[kSFull + i]);
+      };
+      auto pv = [&](int i, int slot, bool first) {
+        const unsigned char* vt = smem + kOffV + slot * kTileBytes;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k)
+          umma_ts(tmem + kColO + i * 128, tmem + i * 128 + k * 8,
+                  ptx::smem_desc(vt + k * 4096, 1024, 2048, ptx::kLayoutSw128), kIdPV, !first || k > 0);
+        ptx::umma_commit(&bars[kODone + i]);
+      };
+      for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
+        Item it;
+        if (!item_at<G>(L, w, it)) continue;
+        const int n = max(it.n[0], it.n[1]);
+        wait(&bars[kQFull], ic & 1u, aborted);
+        for (int t = -1; t < n && !aborted; ++t) {
+          // P.V of step t (none before the first), Q.K^T of step t + 1
+          const int vslot = (kc + t) & 1u, kslot = (kc + t + 1) & 1u;
+          const bool next = t + 1 < n;
+          if (t >= 0) wait(&bars[kVFull + vslot], ((kc + t) >> 1) & 1u, aborted);
+          if (next) wait(&bars[kKFull + kslot], ((kc + t + 1) >> 1) & 1u, aborted);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (t >= 0 && t < it.n[i]) {
+              if (t == 0) wait(&bars[kOFree + i], (oc[i]++ & 1u) ^ 1u, aborted);
+              wait(&bars[kPFull + i], pc[i]++ & 1u, aborted);
+              if (aborted) break;
+              ptx::tc_fence_after();
+              pv(i, vslot, t == 0);
+            }
+            if (aborted) break;
+            if (t + 1 < it.n[i]) {
+              ptx::tc_fence_after();
+              qk(i, kslot);
+            }
+          }
+          if (aborted) break;
+          if (t >= 0) ptx::umma_commit(&bars[kVFree + vslot]);
+          if (next) ptx::umma_commit(&bars[kKFree + kslot]);
+          if (t == n - 2 || n == 0) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
+        }
+        kc += n;
+        ++ic;
+      }
+      // nothing may be in flight when tensor memory is freed
+      ptx::umma_commit(&bars[kDrain]);
+      bool drain = false;
+      wait(&bars[kDrain], 0, drain);
+      if (aborted || drain) *gave_up = 1;
+    }
+    __syncwarp();
+  } else {
+    // ============ softmax and output: one query row per thread ============
+    const int i = warp >> 2;  // tile
+    const int quarter = warp & 3;
+    const int r = 32 * quarter + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + kColO + i * 128;
+    const int g = r / TQ, trow = i * TQ + r % TQ;
+    uint32_t sc = 0, ic = 0;  // steps of the tile, items
+    for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
+      Item it;
+      if (!item_at<G>(L, w, it)) continue;
+      const uint32_t item_no = ic++;
+      const int64_t row = static_cast<int64_t>(it.qb + it.tok0 + trow) * p.num_q_heads + it.kvh * G + g;
+      const bool valid = trow < it.ntok;
+      const int limit = valid ? it.pos0 + trow + 1 : 0;  // keys that this row sees
+      float m = -CUDART_INF_F, l = 0.f, f = 0.f;
+      for (int t = 0; t < it.n[i]; ++t, ++sc) {
+        wait(&bars[kSFull + i], sc & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        ptx::tc_fence_after();
+        if (t == 0) {
+          wait(&bars[kQFull], item_no & 1u, aborted);  // long complete: orders the factor's read
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) break;
+          f = fac[(item_no & 1u) * 256 + i * 128 + r];
+        }
+        const int nvis = limit - (it.t0 + t) * 128;
+        float mx = -CUDART_INF_F;
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t a[32], b[32];
+          ptx::TmemLd<32>::run(s_at + c * 32, a);
+          ptx::TmemLd<32>::run(s_at + c * 32 + 32, b);
+          ptx::tmem_wait_ld();
+          float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
+          if (nvis >= 128) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              m0 = fmaxf(m0, __uint_as_float(a[j]));
+              m1 = fmaxf(m1, __uint_as_float(a[j + 1]));
+              m2 = fmaxf(m2, __uint_as_float(b[j]));
+              m3 = fmaxf(m3, __uint_as_float(b[j + 1]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (c * 32 + j < nvis) m0 = fmaxf(m0, __uint_as_float(a[j]));
+              if (c * 32 + 32 + j < nvis) m1 = fmaxf(m1, __uint_as_float(b[j]));
+            }
+          }
+          mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+        }
+        mx *= f;  // f > 0 for rows that see a key
+        if (nvis <= 0) mx = -CUDART_INF_F;
+        const bool raise = mx > m + kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? fast_exp2(m - mx) : 1.f;
+          if (raise) m = mx;
+          l *= alpha;
+          if (t > 0) {  // O, once P.V of the step before is in it
+            wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
+            aborted = __any_sync(0xffffffffu, aborted);
+            if (aborted) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              ptx::TmemLd<32>::run(o_at + c * 32, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+              ptx::tmem_st32(o_at + c * 32, v);
+            }
+          }
+        }
+        const float bias = m == -CUDART_INF_F ? 0.f : kPShift - m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], pk[16];
+          ptx::TmemLd<32>::run(s_at + c * 32, v);
+          ptx::tmem_wait_ld();
+          if (nvis >= 128) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(v[j]), f, bias));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(v[j + 1]), f, bias));
+              ls[j & 3] += p0;
+              ls[(j + 1) & 3] += p1;
+              pk[j >> 1] = pack_f16(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float p0 = c * 32 + j < nvis ? fast_exp2(fmaf(__uint_as_float(v[j]), f, bias)) : 0.f;
+              const float p1 = c * 32 + j + 1 < nvis ? fast_exp2(fmaf(__uint_as_float(v[j + 1]), f, bias)) : 0.f;
+              ls[j & 3] += p0;
+              ls[(j + 1) & 3] += p1;
+              pk[j >> 1] = pack_f16(p0, p1);
+            }
+          }
+          tmem_st16(s_at + c * 16, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kPFull + i]);
+      }
+      if (aborted) break;
+      const int64_t prow =
+          ((static_cast<int64_t>(it.part) * p.num_seqs + it.seq) * p.max_q_len + it.tok0 + trow) * p.num_q_heads +
+          it.kvh * G + g;
+      if (it.n[i] > 0) {
+        wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        ptx::tc_fence_after();
+        const float inv = l != 0.f ? p.v_scale / l : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          ptx::TmemLd<32>::run(o_at + c * 32, v);
+          ptx::tmem_wait_ld();
+          if (c == 3) {  // O is read: the next item's P.V may write it
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars[kOFree + i]);
+          }
+          if (!valid) continue;
+          if (L.parts > 1) {
+            float4* dst = reinterpret_cast<float4*>(L.o + prow * 128 + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+          } else if (p.out_bf16) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * 128 + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * e]) * inv,
+                                                               __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+                h[e] = *reinterpret_cast<const uint32_t*>(&x);
+              }
+              dst[q] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * 128 + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                   __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+          }
+        }
+      }
+      if (L.parts > 1 && valid) *reinterpret_cast<float2*>(L.ml + prow * 2) = make_float2(m, l);
+    }
+  }
+
+  if (aborted) *gave_up = 1;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 12) ptx::tmem_dealloc(tmem, 512);
+  if (tid == 0 && *gave_up && p.err) atomicExch(p.err, kDevErrTimeout);
+}
+
+// The parts of every (token, head) of a chunk added up, in order; a warp a row.
+__global__ void __launch_bounds__(256) fp4_prefill_merge_kernel(const __grid_constant__ fp4_prefill_detail::Launch L) {
+  using namespace fp4_prefill_detail;
+  const Fp4AttnParams& p = L.p;
+  ptx::griddep_wait();
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_q_heads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
+  // rows of no chunk, or of a chunk that was refused, are left as they were
+  const int tok = static_cast<int>(row / p.num_q_heads);
+  int lo = 0, hi = p.num_seqs - 1;
+  while (lo < hi) {  // the last sequence that starts at or before the token
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.cu_q[mid] <= tok) lo = mid;
+    else hi = mid - 1;
+  }
+  const int b = p.cu_q[lo], n = p.cu_q[lo + 1] - b, q0 = p.q_start[lo];
+  const int64_t last = static_cast<int64_t>(q0) + n;
+  if (b < 0 || tok < b || tok >= b + n || static_cast<int64_t>(b) + n > p.num_tokens || q0 < 0 || n > p.max_q_len ||
+      last > (static_cast<int64_t>(p.max_blocks_per_seq) << L.bs_log) || last > p.max_context_len)
+    return;
+  const int64_t prows = static_cast<int64_t>(p.num_seqs) * p.max_q_len * p.num_q_heads;
+  const int64_t prow = (static_cast<int64_t>(lo) * p.max_q_len + tok - b) * p.num_q_heads + row % p.num_q_heads;
+  float M = -CUDART_INF_F;
+  for (int k = 0; k < L.parts; ++k) M = fmaxf(M, L.ml[(k * prows + prow) * 2]);
+  const float ref = M == -CUDART_INF_F ? 0.f : M;
+  float l = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < L.parts; ++k) {
+    const float2 ml = *reinterpret_cast<const float2*>(L.ml + (k * prows + prow) * 2);
+    if (ml.y == 0.f) continue;  // a part that this row sees nothing of: its O is not written
+    const float4 v = *reinterpret_cast<const float4*>(L.o + (k * prows + prow) * 128 + lane * 4);
+    const float f = fast_exp2(ml.x - ref);
+    l = fmaf(f, ml.y, l);
+    a.x = fmaf(f, v.x, a.x);
+    a.y = fmaf(f, v.y, a.y);
+    a.z = fmaf(f, v.z, a.z);
+    a.w = fmaf(f, v.w, a.w);
+  }
+  const float inv = l != 0.f ? p.v_scale / l : 0.f;
+  const int64_t at = row * 128 + lane * 4;
+  if (p.out_bf16) {
+    __nv_bfloat162 r[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv), __floats2bfloat162_rn(a.z * inv, a.w * inv)};
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) = *reinterpret_cast<const uint2*>(r);
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  }
+}
+
+namespace {
+
+const void* kernel_for(int group) {
+  switch (group) {
+    case 1: return reinterpret_cast<const void*>(&fp4_prefill_kernel<1>);
+    case 2: return reinterpret_cast<const void*>(&fp4_prefill_kernel<2>);
+    case 4: return reinterpret_cast<const void*>(&fp4_prefill_kernel<4>);
+    case 8: return reinterpret_cast<const void*>(&fp4_prefill_kernel<8>);
+    default: return reinterpret_cast<const void*>(&fp4_prefill_kernel<16>);
+  }
+}
+
+// Parts of the keys: with fewer tile pairs than three for every SM, enough
+// parts to come near that, of four tiles of keys or more.
+int parts_for(int64_t pairs, int max_context_len) {
+  const int64_t want = 3 * device_sm_count() / (pairs > 0 ? pairs : 1);
+  const int64_t most = (static_cast<int64_t>(max_context_len) + 511) / 512;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : (n > 64 ? 64 : n));
+}
+int64_t pairs_of(int num_seqs, int num_q_heads, int num_kv_heads, int max_q_len, int* per_chunk) {
+  const int tq2 = 256 / (num_q_heads / num_kv_heads);
+  *per_chunk = (max_q_len + tq2 - 1) / tq2;
+  return static_cast<int64_t>(num_seqs) * num_kv_heads * *per_chunk;
+}
+
+}  // namespace
+
+size_t fp4_prefill_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int max_q_len, int max_context_len) {
+  int per_chunk = 0;
+  const int parts = parts_for(pairs_of(num_seqs, num_q_heads, num_kv_heads, max_q_len, &per_chunk), max_context_len);
+  if (parts == 1) return 256;
+  const int64_t rows = static_cast<int64_t>(num_seqs) * max_q_len * num_q_heads;
+  return static_cast<size_t>(256 + parts * rows * (128 + 2) * 4 + 256);
+}
+
+cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
+  using namespace fp4_prefill_detail;
+  Launch L{};
+  L.p = p;
+  const int64_t pairs = pairs_of(p.num_seqs, p.num_q_heads, p.num_kv_heads, p.max_q_len, &L.pairs);
+  L.parts = parts_for(pairs, p.max_context_len);
+  L.tile_bytes = static_cast<uint32_t>(fp4_tile_bytes(p.block_size, 128));
+  L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_q_heads;
+  if (L.parts > 1) {
+    L.o = reinterpret_cast<float*>(p.ws + 256);
+    L.ml = L.o + static_cast<int64_t>(L.parts) * p.num_seqs * p.max_q_len * p.num_q_heads * 128;
+  }
+  const void* fn = kernel_for(p.num_q_heads / p.num_kv_heads);
+  int per_sm = 0;
+  cudaError_t e = fp4_occupancy(fn, kThreads, kSmemBytes, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t items = pairs * L.parts;
+  if (items >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  const int64_t sms = device_sm_count();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? items : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&L};
+  e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e != cudaSuccess || L.parts == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&fp4_prefill_merge_kernel), args);
+}
+
+}  // namespace pa
