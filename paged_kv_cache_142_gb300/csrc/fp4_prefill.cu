@@ -119,6 +119,17 @@ __device__ __forceinline__ bool item_at(const Launch& L, int w, Item& it) {
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
   if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
 }
+// by a whole warp: it gives up together
+__device__ __forceinline__ void wait_all(uint64_t* bar, uint32_t parity, bool& aborted) {
+  wait(bar, parity, aborted);
+  aborted = __any_sync(0xffffffffu, aborted);
+}
+// one lane of the warp, the same each time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -329,45 +340,52 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     }
   } else if (warp == 12) {
     // ============================ products ============================
-    if (lane == 0) {
+    // The whole warp runs this, so that descriptors and addresses stay in
+    // uniform registers; one elected lane issues.  The eight instructions of a
+    // product are unrolled: a rolled loop of one lane took 130 clocks each.
+    {
+      const bool leader = elect_one();
+      const uint64_t desc_q = ptx::smem_desc(smem + kOffQ, 16, 1024, ptx::kLayoutSw128);
+      const uint64_t desc_k = ptx::smem_desc(smem + kOffK, 16, 2048, ptx::kLayoutSw128);
+      const uint64_t desc_v = ptx::smem_desc(smem + kOffV, 1024, 2048, ptx::kLayoutSw128);
       constexpr uint32_t kIdQK = idesc_f16(0), kIdPV = idesc_f16(1);
       uint32_t ic = 0, kc = 0;
       uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};  // steps and items of each tile
-      auto qk = [&](int i, int slot) {
-        const unsigned char* qt = smem + kOffQ + i * kTileBytes;
-        const unsigned char* kt = smem + kOffK + slot * kTileBytes;
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-          const int h = k >> 2, k4 = k & 3;
-          ptx::umma_bf16(tmem + i * 128, ptx::smem_desc(qt + h * 16384 + k4 * 32, 16, 1024, ptx::kLayoutSw128),
-                         ptx::smem_desc(kt + h * 1024 + k4 * 32, 16, 2048, ptx::kLayoutSw128), kIdQK, k > 0);
+      auto qk = [&](int i, uint32_t slot) {
+        const uint64_t dq = desc_q + i * (kTileBytes >> 4), dk = desc_k + slot * (kTileBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // halves of 64 dims, 16 dims (32 bytes) each
+            ptx::umma_bf16(tmem + i * 128, dq + (k >> 2) * (16384 >> 4) + (k & 3) * 2,
+                           dk + (k >> 2) * (1024 >> 4) + (k & 3) * 2, kIdQK, k > 0);
+          ptx::umma_commit(&bars[kSFull + i]);
         }
-        ptx::umma_commit(&bars[kSFull + i]);
       };
-      auto pv = [&](int i, int slot, bool first) {
-        const unsigned char* vt = smem + kOffV + slot * kTileBytes;
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          umma_ts(tmem + kColO + i * 128, tmem + i * 128 + k * 8,
-                  ptx::smem_desc(vt + k * 4096, 1024, 2048, ptx::kLayoutSw128), kIdPV, !first || k > 0);
-        ptx::umma_commit(&bars[kODone + i]);
+      auto pv = [&](int i, uint32_t slot, bool first) {
+        const uint64_t dv = desc_v + slot * (kTileBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 keys (4096 bytes) each
+            umma_ts(tmem + kColO + i * 128, tmem + i * 128 + k * 8, dv + k * (4096 >> 4), kIdPV, k > 0 ? 1u : !first);
+          ptx::umma_commit(&bars[kODone + i]);
+        }
       };
       for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
         Item it;
         if (!item_at<G>(L, w, it)) continue;
         const int n = max(it.n[0], it.n[1]);
-        wait(&bars[kQFull], ic & 1u, aborted);
+        wait_all(&bars[kQFull], ic & 1u, aborted);
         for (int t = -1; t < n && !aborted; ++t) {
           // P.V of step t (none before the first), Q.K^T of step t + 1
           const int vslot = (kc + t) & 1u, kslot = (kc + t + 1) & 1u;
           const bool next = t + 1 < n;
-          if (t >= 0) wait(&bars[kVFull + vslot], ((kc + t) >> 1) & 1u, aborted);
-          if (next) wait(&bars[kKFull + kslot], ((kc + t + 1) >> 1) & 1u, aborted);
+          if (t >= 0) wait_all(&bars[kVFull + vslot], ((kc + t) >> 1) & 1u, aborted);
+          if (next) wait_all(&bars[kKFull + kslot], ((kc + t + 1) >> 1) & 1u, aborted);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (t >= 0 && t < it.n[i]) {
-              if (t == 0) wait(&bars[kOFree + i], (oc[i]++ & 1u) ^ 1u, aborted);
-              wait(&bars[kPFull + i], pc[i]++ & 1u, aborted);
+              if (t == 0) wait_all(&bars[kOFree + i], (oc[i]++ & 1u) ^ 1u, aborted);
+              wait_all(&bars[kPFull + i], pc[i]++ & 1u, aborted);
               if (aborted) break;
               ptx::tc_fence_after();
               pv(i, vslot, t == 0);
@@ -379,18 +397,23 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
             }
           }
           if (aborted) break;
-          if (t >= 0) ptx::umma_commit(&bars[kVFree + vslot]);
-          if (next) ptx::umma_commit(&bars[kKFree + kslot]);
-          if (t == n - 2 || n == 0) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
+          if (leader) {
+            if (t >= 0) ptx::umma_commit(&bars[kVFree + vslot]);
+            if (next) ptx::umma_commit(&bars[kKFree + kslot]);
+            if (t == n - 2 || n == 0) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
+          }
+          __syncwarp();
         }
         kc += n;
         ++ic;
       }
       // nothing may be in flight when tensor memory is freed
-      ptx::umma_commit(&bars[kDrain]);
-      bool drain = false;
-      wait(&bars[kDrain], 0, drain);
-      if (aborted || drain) *gave_up = 1;
+      if (leader) {
+        ptx::umma_commit(&bars[kDrain]);
+        bool drain = false;
+        wait(&bars[kDrain], 0, drain);
+        if (aborted || drain) *gave_up = 1;
+      }
     }
     __syncwarp();
   } else {
