@@ -150,12 +150,92 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b,
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// waits for this warp's tensor-memory loads; what uses v comes after it
+__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
+// A row's probabilities 2^(s f + bias) of a step's 128 keys as 64 f16 pairs,
+// their sum, and the largest s; MASK: keys from nvis on do not count.  The
+// next 16 scores load while 16 are worked on.
+template <bool MASK>
+__device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&pk)[64],
+                                              float& top, float& sum) {
+  const uint64_t ff = pack2(f, f), bb = pack2(bias, bias);
+  uint64_t s0 = 0, s1 = 0;
+  float m0 = -CUDART_INF_F, m1 = m0;
+  uint32_t v[2][16];
+  ptx::TmemLd<16>::run(s_at, v[0]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    wait_ld16(v[c & 1]);
+    if (c < 7) ptx::TmemLd<16>::run(s_at + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(v[c & 1][j + e]);
+        if (MASK && c * 16 + j + e >= nvis) x[e] = -CUDART_INF_F;
+      }
+      m0 = max3(m0, x[0], x[1]);
+      m1 = max3(m1, x[2], x[3]);
+      const float2 a = unpack2(fma2(pack2(x[0], x[1]), ff, bb)), b = unpack2(fma2(pack2(x[2], x[3]), ff, bb));
+      const float e0 = fast_exp2(a.x), e1 = fast_exp2(a.y), e2 = fast_exp2(b.x), e3 = fast_exp2(b.y);
+      s0 = add2(s0, pack2(e0, e1));
+      s1 = add2(s1, pack2(e2, e3));
+      pk[(c * 16 + j) / 2] = pack_f16(e0, e1);
+      pk[(c * 16 + j) / 2 + 1] = pack_f16(e2, e3);
+    }
+  }
+  top = fmaxf(m0, m1);
+  const float2 t = unpack2(add2(s0, s1));
+  sum = t.x + t.y;
+}
+// the largest of a row's first nvis scores of a step
+__device__ __forceinline__ float row_max(uint32_t s_at, int nvis) {
+  float m0 = -CUDART_INF_F, m1 = m0;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    uint32_t v[16];
+    ptx::TmemLd<16>::run(s_at + c * 16, v);
+    wait_ld16(v);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      if (c * 16 + j < nvis) m0 = fmaxf(m0, __uint_as_float(v[j]));
+      if (c * 16 + j + 1 < nvis) m1 = fmaxf(m1, __uint_as_float(v[j + 1]));
+    }
+  }
+  return fmaxf(m0, m1);
 }
 
 // A key's or value's row: 64 code bytes and 8 scales.
@@ -298,7 +378,9 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         const int ex = static_cast<int>(top >> 7);
         const int shift = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 14 - (ex - 127)));
         const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-        fac[(ic & 1u) * 256 + i * 128 + r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+        // (not zero: a masked -inf times it stays -inf)
+        fac[(ic & 1u) * 256 + i * 128 + r] =
+            fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 1.2e-38f);
         unsigned char* row = smem + kOffQ + i * kTileBytes + r * 128;
 #pragma unroll 4
         for (int c = 0; c < 16; ++c) {
@@ -445,37 +527,26 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
           f = fac[(item_no & 1u) * 256 + i * 128 + r];
         }
         const int nvis = limit - (it.t0 + t) * 128;
-        float mx = -CUDART_INF_F;
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t a[32], b[32];
-          ptx::TmemLd<32>::run(s_at + c * 32, a);
-          ptx::TmemLd<32>::run(s_at + c * 32 + 32, b);
-          ptx::tmem_wait_ld();
-          float m0 = -CUDART_INF_F, m1 = m0, m2 = m0, m3 = m0;
-          if (nvis >= 128) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              m0 = fmaxf(m0, __uint_as_float(a[j]));
-              m1 = fmaxf(m1, __uint_as_float(a[j + 1]));
-              m2 = fmaxf(m2, __uint_as_float(b[j]));
-              m3 = fmaxf(m3, __uint_as_float(b[j + 1]));
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (c * 32 + j < nvis) m0 = fmaxf(m0, __uint_as_float(a[j]));
-              if (c * 32 + 32 + j < nvis) m1 = fmaxf(m1, __uint_as_float(b[j]));
-            }
-          }
-          mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+        // The probabilities are formed on the reference as it is; a row whose
+        // maximum turns out to pass it by more than 2^8 raises it, and the step
+        // is formed again (its scores are still there).  The first step starts
+        // from its own maximum.
+        if (t == 0) {
+          const float mx = row_max(s_at, nvis) * f;
+          if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
         }
-        mx *= f;  // f > 0 for rows that see a key
-        if (nvis <= 0) mx = -CUDART_INF_F;
-        const bool raise = mx > m + kSlack;
+        uint32_t pk[64];
+        float top, sum;
+        auto form = [&]() {
+          const float bias = m == -CUDART_INF_F ? 0.f : kPShift - m;
+          if (__all_sync(0xffffffffu, nvis >= 128)) probabilities<false>(s_at, nvis, f, bias, pk, top, sum);
+          else probabilities<true>(s_at, nvis, f, bias, pk, top, sum);
+        };
+        form();
+        const bool raise = top * f > m + kSlack;
         if (__any_sync(0xffffffffu, raise)) {
-          const float alpha = raise ? fast_exp2(m - mx) : 1.f;
-          if (raise) m = mx;
+          const float alpha = raise ? fast_exp2(m - top * f) : 1.f;
+          if (raise) m = top * f;
           l *= alpha;
           if (t > 0) {  // O, once P.V of the step before is in it
             wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
@@ -492,36 +563,11 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
               ptx::tmem_st32(o_at + c * 32, v);
             }
           }
+          form();
         }
-        const float bias = m == -CUDART_INF_F ? 0.f : kPShift - m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], pk[16];
-          ptx::TmemLd<32>::run(s_at + c * 32, v);
-          ptx::tmem_wait_ld();
-          if (nvis >= 128) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(v[j]), f, bias));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(v[j + 1]), f, bias));
-              ls[j & 3] += p0;
-              ls[(j + 1) & 3] += p1;
-              pk[j >> 1] = pack_f16(p0, p1);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float p0 = c * 32 + j < nvis ? fast_exp2(fmaf(__uint_as_float(v[j]), f, bias)) : 0.f;
-              const float p1 = c * 32 + j + 1 < nvis ? fast_exp2(fmaf(__uint_as_float(v[j + 1]), f, bias)) : 0.f;
-              ls[j & 3] += p0;
-              ls[(j + 1) & 3] += p1;
-              pk[j >> 1] = pack_f16(p0, p1);
-            }
-          }
-          tmem_st16(s_at + c * 16, pk);
-        }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += sum;
+        ptx::tmem_st32(s_at, *reinterpret_cast<uint32_t(*)[32]>(pk));
+        ptx::tmem_st32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
