@@ -11,16 +11,18 @@
 // 2^-9); accumulators are fp32 in tensor memory: S of both tiles, O of both.
 // P is written over its S and read from there as the A operand.
 //
-// One CTA per SM, 13 warps, persistent over (tile pair, sequence, kv head,
+// One CTA per SM, 14 warps, persistent over (tile pair, sequence, kv head,
 // part of the keys):
 //  * warps 8-11 restore: a thread owns one key of a tile.  It reads the key's
 //    64 code bytes and 8 scales through the block table, one tile ahead, and
 //    writes the 128 f16 values in the 128-byte-swizzled layout that the
 //    tensor core reads; then the same for the value row.  They load the
 //    queries too, and the power of two of each row;
-//  * warp 12 issues every product.  Q.K^T of a tile's next step is issued
-//    right behind P.V of its last one, which read P from the same columns, so
-//    while one tile's softmax runs the tensor core works for the other;
+//  * warps 12 and 13 issue the products of the first and the second tile.
+//    Q.K^T of a tile's next step is issued right behind P.V of its last one,
+//    which read P from the same columns (the tensor core runs a thread's
+//    products in order); while one tile's softmax runs the tensor core works
+//    for the other;
 //  * warps 0-3 and 4-7 run the softmax of the first and the second tile, one
 //    row a thread: maximum, exponentials and sum in fp32 (log2 domain).  The
 //    reference of a row is raised only when its maximum passes it by 2^8.
@@ -41,7 +43,7 @@
 namespace pa {
 namespace fp4_prefill_detail {
 
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr int kTileBytes = 32768;  // 128 rows x 128 f16
 constexpr int kOffQ = 0;           // two tiles: [half of the dims][128 rows][128 bytes]
 constexpr int kOffK = 2 * kTileBytes;
@@ -118,11 +120,6 @@ __device__ __forceinline__ bool item_at(const Launch& L, int w, Item& it) {
 
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
   if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
-}
-// by a whole warp: it gives up together
-__device__ __forceinline__ void wait_all(uint64_t* bar, uint32_t parity, bool& aborted) {
-  wait(bar, parity, aborted);
-  aborted = __any_sync(0xffffffffu, aborted);
 }
 // one lane of the warp, the same each time
 __device__ __forceinline__ bool elect_one() {
@@ -265,18 +262,18 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
   ptx::griddep_launch_dependents();
   if (tid == 0) {
     ptx::mbar_init(&bars[kQFull], 4);
-    ptx::mbar_init(&bars[kQFree], 1);
+    ptx::mbar_init(&bars[kQFree], 2);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars[kKFull + i], 4);
-      ptx::mbar_init(&bars[kKFree + i], 1);
+      ptx::mbar_init(&bars[kKFree + i], 2);
       ptx::mbar_init(&bars[kVFull + i], 4);
-      ptx::mbar_init(&bars[kVFree + i], 1);
+      ptx::mbar_init(&bars[kVFree + i], 2);
       ptx::mbar_init(&bars[kSFull + i], 1);
       ptx::mbar_init(&bars[kPFull + i], 4);
       ptx::mbar_init(&bars[kODone + i], 1);
       ptx::mbar_init(&bars[kOFree + i], 4);
     }
-    ptx::mbar_init(&bars[kDrain], 1);
+    ptx::mbar_init(&bars[kDrain], 2);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
@@ -420,82 +417,93 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         if (more) load(vx, p.v_cache, at, it.t0 + t + 1);
       }
     }
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
     // ============================ products ============================
-    // The whole warp runs this, so that descriptors and addresses stay in
-    // uniform registers; one elected lane issues.  The eight instructions of a
-    // product are unrolled: a rolled loop of one lane took 130 clocks each.
-    {
-      const bool leader = elect_one();
-      const uint64_t desc_q = ptx::smem_desc(smem + kOffQ, 16, 1024, ptx::kLayoutSw128);
-      const uint64_t desc_k = ptx::smem_desc(smem + kOffK, 16, 2048, ptx::kLayoutSw128);
-      const uint64_t desc_v = ptx::smem_desc(smem + kOffV, 1024, 2048, ptx::kLayoutSw128);
-      constexpr uint32_t kIdQK = idesc_f16(0), kIdPV = idesc_f16(1);
-      uint32_t ic = 0, kc = 0;
-      uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};  // steps and items of each tile
-      auto qk = [&](int i, uint32_t slot) {
-        const uint64_t dq = desc_q + i * (kTileBytes >> 4), dk = desc_k + slot * (kTileBytes >> 4);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)  // halves of 64 dims, 16 dims (32 bytes) each
-            ptx::umma_bf16(tmem + i * 128, dq + (k >> 2) * (16384 >> 4) + (k & 3) * 2,
-                           dk + (k >> 2) * (1024 >> 4) + (k & 3) * 2, kIdQK, k > 0);
-          ptx::umma_commit(&bars[kSFull + i]);
-        }
-      };
-      auto pv = [&](int i, uint32_t slot, bool first) {
-        const uint64_t dv = desc_v + slot * (kTileBytes >> 4);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 keys (4096 bytes) each
-            umma_ts(tmem + kColO + i * 128, tmem + i * 128 + k * 8, dv + k * (4096 >> 4), kIdPV, k > 0 ? 1u : !first);
-          ptx::umma_commit(&bars[kODone + i]);
-        }
-      };
-      for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
-        Item it;
-        if (!item_at<G>(L, w, it)) continue;
-        const int n = max(it.n[0], it.n[1]);
-        wait_all(&bars[kQFull], ic & 1u, aborted);
-        for (int t = -1; t < n && !aborted; ++t) {
-          // P.V of step t (none before the first), Q.K^T of step t + 1
-          const int vslot = (kc + t) & 1u, kslot = (kc + t + 1) & 1u;
-          const bool next = t + 1 < n;
-          if (t >= 0) wait_all(&bars[kVFull + vslot], ((kc + t) >> 1) & 1u, aborted);
-          if (next) wait_all(&bars[kKFull + kslot], ((kc + t + 1) >> 1) & 1u, aborted);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (t >= 0 && t < it.n[i]) {
-              if (t == 0) wait_all(&bars[kOFree + i], (oc[i]++ & 1u) ^ 1u, aborted);
-              wait_all(&bars[kPFull + i], pc[i]++ & 1u, aborted);
-              if (aborted) break;
-              ptx::tc_fence_after();
-              pv(i, vslot, t == 0);
-            }
-            if (aborted) break;
-            if (t + 1 < it.n[i]) {
-              ptx::tc_fence_after();
-              qk(i, kslot);
-            }
-          }
-          if (aborted) break;
-          if (leader) {
-            if (t >= 0) ptx::umma_commit(&bars[kVFree + vslot]);
-            if (next) ptx::umma_commit(&bars[kKFree + kslot]);
-            if (t == n - 2 || n == 0) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
-          }
-          __syncwarp();
-        }
-        kc += n;
-        ++ic;
-      }
-      // nothing may be in flight when tensor memory is freed
+    // A warp for each tile, so that one's waits pass while the other's products
+    // run.  The whole warp runs this and descriptors stay in uniform registers;
+    // one elected lane issues.  The eight instructions of a product are
+    // unrolled: a rolled loop of one lane took 130 clocks each.
+    const int i = warp - 12;
+    const bool leader = elect_one();
+    constexpr uint32_t kIdQK = idesc_f16(0), kIdPV = idesc_f16(1);
+    const uint64_t desc_q = ptx::smem_desc(smem + kOffQ + i * kTileBytes, 16, 1024, ptx::kLayoutSw128);
+    const uint64_t desc_k = ptx::smem_desc(smem + kOffK, 16, 2048, ptx::kLayoutSw128);
+    const uint64_t desc_v = ptx::smem_desc(smem + kOffV, 1024, 2048, ptx::kLayoutSw128);
+    const uint32_t s_at = tmem + i * 128, o_at = tmem + kColO + i * 128;
+    uint32_t ic = 0, kc = 0, pc = 0, oc = 0;  // items; steps of keys; steps and items of the tile
+    auto qk = [&](uint32_t slot) {
+      const uint64_t dk = desc_k + slot * (kTileBytes >> 4);
       if (leader) {
-        ptx::umma_commit(&bars[kDrain]);
-        bool drain = false;
-        wait(&bars[kDrain], 0, drain);
-        if (aborted || drain) *gave_up = 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)  // halves of 64 dims, 16 dims (32 bytes) each
+          ptx::umma_bf16(s_at, desc_q + (k >> 2) * (16384 >> 4) + (k & 3) * 2,
+                         dk + (k >> 2) * (1024 >> 4) + (k & 3) * 2, kIdQK, k > 0);
+        ptx::umma_commit(&bars[kSFull + i]);
+        ptx::umma_commit(&bars[kKFree + slot]);
       }
+    };
+    auto pv = [&](uint32_t slot, bool first) {
+      const uint64_t dv = desc_v + slot * (kTileBytes >> 4);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)  // 16 keys (4096 bytes) each
+          umma_ts(o_at, s_at + k * 8, dv + k * (4096 >> 4), kIdPV, k > 0 ? 1u : !first);
+        ptx::umma_commit(&bars[kODone + i]);
+        ptx::umma_commit(&bars[kVFree + slot]);
+      }
+    };
+    uint32_t turns = 0;
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      Item it;
+      if (!item_at<G>(L, w, it)) continue;
+      const int n = max(it.n[0], it.n[1]), mine = i ? it.n[1] : it.n[0];
+      for (int t = -1; t < n; ++t) {
+        // P.V of step t (none before the first), Q.K^T of step t + 1; a lane
+        // polls each of the barriers that this needs
+        const uint32_t vslot = (kc + t) & 1u, kslot = (kc + t + 1) & 1u;
+        const bool do_pv = t >= 0 && t < mine, next = t + 1 < n, do_qk = t + 1 < mine;
+        uint64_t* bar = nullptr;
+        uint32_t parity = 0;
+        if (lane == 0 && do_pv) bar = &bars[kPFull + i], parity = pc & 1u;
+        if (lane == 1 && t >= 0) bar = &bars[kVFull + vslot], parity = ((kc + t) >> 1) & 1u;
+        if (lane == 2 && next) bar = &bars[kKFull + kslot], parity = ((kc + t + 1) >> 1) & 1u;
+        if (lane == 3 && do_pv && t == 0) bar = &bars[kOFree + i], parity = (oc & 1u) ^ 1u;
+        if (lane == 4 && t == -1) bar = &bars[kQFull], parity = ic & 1u;
+        if (bar) wait(bar, parity, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        // the tiles' turns: whole steps alternate, so that the tiles' softmaxes
+        // and products do too (a warp that gave up goes on taking turns)
+        if (i) ptx::bar_sync(1, 64);
+        else if (turns++) ptx::bar_sync(2, 64);
+        ptx::tc_fence_after();
+        if (aborted) {
+        } else if (do_pv) {
+          pv(vslot, t == 0);
+          ++pc;
+          oc += t == 0;
+        } else if (t >= 0 && leader) {
+          ptx::mbar_arrive(&bars[kVFree + vslot]);  // a step of the other tile alone
+        }
+        if (aborted) {
+        } else if (do_qk) {
+          qk(kslot);
+        } else if (next && leader) {
+          ptx::mbar_arrive(&bars[kKFree + kslot]);
+        }
+        if (!aborted && leader && (t == n - 2 || n == 0)) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
+        __syncwarp();
+        asm volatile("bar.arrive %0, 64;" ::"r"(i ? 2 : 1) : "memory");
+      }
+      kc += n;
+      ++ic;
+    }
+    if (i == 0 && turns) ptx::bar_sync(2, 64);
+    // nothing may be in flight when tensor memory is freed
+    if (leader) {
+      ptx::umma_commit(&bars[kDrain]);
+      bool drain = false;
+      wait(&bars[kDrain], 0, drain);
+      if (aborted || drain) *gave_up = 1;
     }
     __syncwarp();
   } else {
