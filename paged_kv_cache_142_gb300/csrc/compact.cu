@@ -8,95 +8,131 @@
 // written.  keep ascends, so every later source lies at or behind its own
 // destination and so behind every destination written so far: nothing is
 // overwritten before it is read, and the next chunk may be read before this
-// one is written.  Bound by the bytes moved.
+// one is written.
+//
+// What bounds it is the chain keep -> block table -> row, three dependent
+// loads a chunk, far more than the bytes: so a chunk is as long as the CTA's
+// registers allow (four pieces a thread; 1024 threads for long lists), the
+// positions and table entries of the next chunk load during this one, and few
+// kept tokens (accepted drafts) take all heads in one CTA.
 #include "decode.cuh"
 #include "fp4.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kUnroll = 4;       // pieces a thread holds
+constexpr int kMaxThreads = 1024;
 
-// VEC: the unit of a move (16 bytes; 4-bit pages with head_dim 64: 4 bytes,
-// their scale rows' size).
-template <typename VEC>
-__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p, int heads_per_cta, int units_per_row,
-                                                           int code_units) {
+struct Piece {
+  uint32_t w[4];
+};
+__device__ __forceinline__ void load_piece(Piece& v, const unsigned char* p, int bytes) {
+  if (bytes == 16) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    v.w[0] = r.x, v.w[1] = r.y, v.w[2] = r.z, v.w[3] = r.w;
+  } else if (bytes == 8) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    v.w[0] = r.x, v.w[1] = r.y;
+  } else {
+    v.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+__device__ __forceinline__ void store_piece(const Piece& v, unsigned char* p, int bytes) {
+  if (bytes == 16) *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+  else if (bytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
+  else *reinterpret_cast<uint32_t*>(p) = v.w[0];
+}
+
+__global__ void __launch_bounds__(kMaxThreads)
+    compact_kernel(const CompactParams p, int heads_per_cta, int units) {
   const int seq = blockIdx.x;
-  const int h0 = blockIdx.y * heads_per_cta;
   const int64_t layer = blockIdx.z >> 1;
   unsigned char* cache = ((blockIdx.z & 1) ? p.v_cache : p.k_cache) + layer * p.layer_bytes;
   const int b = p.cu_keep[seq], n = p.cu_keep[seq + 1] - b;
   const int dst0 = p.dst_start[seq];
   const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
   const bool report = p.status && blockIdx.y == 0 && blockIdx.z == 0;
-  if (n <= 0) {
-    if (n < 0 && report && threadIdx.x == 0) atomicExch(p.status, kDevErrInvalidArg);
-    return;
-  }
-  if (b < 0 || n > p.max_keep || dst0 < 0 || dst0 + static_cast<int64_t>(n) > table_tokens) {
+  if (n == 0) return;
+  if (b < 0 || n < 0 || n > p.max_keep || dst0 < 0 || dst0 + static_cast<int64_t>(n) > table_tokens) {
     if (report && threadIdx.x == 0) atomicExch(p.status, kDevErrInvalidArg);
     return;
   }
   const int32_t* table = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq;
-  const int per_token = heads_per_cta * units_per_row;
-  const int64_t total = static_cast<int64_t>(n) * per_token;
-  const int bs = p.block_size;
-  for (int64_t i0 = 0; i0 < total; i0 += kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    VEC v;
-    VEC* dst = nullptr;
-    if (i < total) {
-      const int j = static_cast<int>(i / per_token);
-      const int r = static_cast<int>(i - static_cast<int64_t>(j) * per_token);
-      const int h = h0 + r / units_per_row, u = r % units_per_row;
-      const int src_pos = p.keep[b + j], dst_pos = dst0 + j;
-      const bool ok = src_pos >= dst_pos && src_pos < table_tokens && (j == 0 || src_pos > p.keep[b + j - 1]);
+  const int bs_log = __ffs(p.block_size) - 1, bs_mask = p.block_size - 1;
+  // this thread's piece: token `tok` of every step of `tokens` tokens, unit u of head h.
+  // Units of a row: 16-byte pieces (4-bit pages: of its codes, then its scales)
+  const int per_token = heads_per_cta * units;
+  const int tokens = blockDim.x / per_token;
+  const int tok = threadIdx.x / per_token;
+  const int r = threadIdx.x - tok * per_token;
+  const int h = blockIdx.y * heads_per_cta + r / units, u = r % units;
+  const bool scales = p.scale_bytes && u == units - 1;
+  const int bytes = scales ? p.scale_bytes : 16;
+  const int stride = scales ? p.scale_bytes : p.row_bytes;  // from row to row of a tile
+  const int64_t first = h * p.tile_bytes + (scales ? static_cast<int64_t>(p.row_bytes) << bs_log : u * 16);
+  const bool mine = tok < tokens && h < p.num_kv_heads;
+  const int64_t block_bytes = p.tile_bytes * p.num_kv_heads;
+  const int chunk = tokens * kUnroll;
+
+  // where a chunk's pieces come from and go to (src < 0: nothing to move)
+  int64_t src[kUnroll], dst[kUnroll];
+  auto locate = [&](int j0) {
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e) {
+      const int j = j0 + e * tokens + tok;
+      src[e] = -1;
+      if (!mine || j >= n) continue;
+      const int sp = p.keep[b + j], dp = dst0 + j;
       int sb = -1, db = -1;
-      if (ok) {
-        sb = table[src_pos / bs];
-        db = table[dst_pos / bs];
+      if (sp >= dp && sp < table_tokens && (j == 0 || sp > p.keep[b + j - 1])) {
+        sb = table[sp >> bs_log];
+        db = table[dp >> bs_log];
       }
       if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
         if (report && r == 0) atomicExch(p.status, kDevErrInvalidArg);
-      } else if (src_pos != dst_pos && h < p.num_kv_heads) {
-        const int64_t st = (static_cast<int64_t>(sb) * p.num_kv_heads + h) * p.tile_bytes;
-        const int64_t dt = (static_cast<int64_t>(db) * p.num_kv_heads + h) * p.tile_bytes;
-        const int so = src_pos % bs, dof = dst_pos % bs;
-        int64_t in_s, in_d;
-        if (u < code_units) {
-          in_s = static_cast<int64_t>(so) * p.row_bytes + u * static_cast<int>(sizeof(VEC));
-          in_d = static_cast<int64_t>(dof) * p.row_bytes + u * static_cast<int>(sizeof(VEC));
-        } else {
-          const int64_t base = static_cast<int64_t>(bs) * p.row_bytes + (u - code_units) * static_cast<int>(sizeof(VEC));
-          in_s = base + static_cast<int64_t>(so) * p.scale_bytes;
-          in_d = base + static_cast<int64_t>(dof) * p.scale_bytes;
-        }
-        v = *reinterpret_cast<const VEC*>(cache + st + in_s);
-        dst = reinterpret_cast<VEC*>(cache + dt + in_d);
+        continue;
+      }
+      if (sp == dp) continue;
+      src[e] = sb * block_bytes + first + static_cast<int64_t>(sp & bs_mask) * stride;
+      dst[e] = db * block_bytes + first + static_cast<int64_t>(dp & bs_mask) * stride;
+    }
+  };
+  locate(0);
+  for (int j0 = 0; j0 < n; j0 += chunk) {
+    Piece v[kUnroll];
+    int64_t to[kUnroll];
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e) {
+      to[e] = -1;
+      if (src[e] >= 0) {
+        load_piece(v[e], cache + src[e], bytes);
+        to[e] = dst[e];
       }
     }
+    if (j0 + chunk < n) locate(j0 + chunk);
     __syncthreads();
-    if (dst) *dst = v;
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e)
+      if (to[e] >= 0) store_piece(v[e], cache + to[e], bytes);
   }
-}
-
-template <typename VEC>
-cudaError_t launch(const CompactParams& p, cudaStream_t stream) {
-  const int code_units = p.row_bytes / static_cast<int>(sizeof(VEC));
-  const int units = code_units + p.scale_bytes / static_cast<int>(sizeof(VEC));
-  const int hpc = 1;
-  const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>((p.num_kv_heads + hpc - 1) / hpc),
-                  static_cast<unsigned>(2 * p.num_layers));
-  compact_kernel<VEC><<<grid, kThreads, 0, stream>>>(p, hpc, units, code_units);
-  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  if (p.scale_bytes == 0 || p.scale_bytes % 16 == 0) return launch<uint4>(p, stream);
-  return p.scale_bytes % 8 == 0 ? launch<uint2>(p, stream) : launch<uint32_t>(p, stream);
+  const int units = p.row_bytes / 16 + (p.scale_bytes ? 1 : 0);
+  // few kept tokens: as many heads a CTA as one chunk of 256 threads moves at once
+  int heads = 1;
+  for (int h = 2; h <= p.num_kv_heads; ++h)
+    if (h * units <= 256 && static_cast<int64_t>(p.max_keep) * h * units <= 256 * kUnroll) heads = h;
+  int threads = 256;
+  while (threads < kMaxThreads && (threads < units || static_cast<int64_t>(p.max_keep) * heads * units > threads * kUnroll))
+    threads *= 2;
+  const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>((p.num_kv_heads + heads - 1) / heads),
+                  static_cast<unsigned>(2 * p.num_layers));
+  compact_kernel<<<grid, threads, 0, stream>>>(p, heads, units);
+  return cudaGetLastError();
 }
 
 }  // namespace pa

@@ -126,37 +126,33 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   return r;
 }
 
-// 16 fp32 values, already divided by the global scale -> 8 code bytes and
-// the scale byte.  `top` is the largest |x| bit pattern before that division.
-__device__ __forceinline__ void quantise16(const float (&x)[16], uint32_t top, uint2& codes, uint32_t& scale) {
+// 16 fp32 values -> 8 code bytes and the scale byte, under the global scale k
+// (a power of two).  `top`: the bits of their largest magnitude.
+__device__ __forceinline__ void quantise16(float (&x)[16], uint32_t top, float k, uint2& codes, uint32_t& scale) {
   if (top >= 0x7f800000u) {  // infinity or NaN among them: the group reads back as NaN
     codes = make_uint2(0, 0);
     scale = 0x7fu;
     return;
   }
-  float a = 0.f;
+  const float inv = 1.f / k;  // exact
+  const float a = __uint_as_float(top) * inv;
+  if (a > 1e6f) {  // the scale is at its largest, and past 2688 so is the code: no overflow below
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]));
+    for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -1e6f * k), 1e6f * k);
+  }
   // the correctly rounded quotient cannot cross a rounding border of the
   // target: 6 * border has few bits, so a / 6 != border differs from it by
   // more than half an fp32 step
   scale = to_e4m3(__fdiv_rn(a, 6.f));
   const float s = scale_to_f32(scale);
-  const float r = scale ? __frcp_rn(s) : 0.f;
+  // x / (s k), correctly rounded: the product by the rounded reciprocal and one
+  // step with the exact remainder (k scales exactly); the same argument holds
+  const float sk = s * k, r = scale ? __frcp_rn(s) * inv : 0.f;
   uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float t[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      // x / s, correctly rounded (the product by the rounded reciprocal and
-      // one exact-remainder step); past 1e6 the scale is at its largest and
-      // the code at 6, whatever the value
-      const float v = fminf(fmaxf(x[2 * i + e], -1e6f), 1e6f);
-      const float q = v * r;
-      t[e] = fmaf(fmaf(-q, s, v), r, q);
-    }
-    b[i] = to_e2m1x2(t[0], t[1]);
+    const float q0 = x[2 * i] * r, q1 = x[2 * i + 1] * r;
+    b[i] = to_e2m1x2(fmaf(fmaf(-q0, sk, x[2 * i]), r, q0), fmaf(fmaf(-q1, sk, x[2 * i + 1]), r, q1));
   }
   codes.x = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
   codes.y = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);

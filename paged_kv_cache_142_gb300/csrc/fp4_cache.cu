@@ -1,7 +1,8 @@
 // Write to and read back from the pages of the 4-bit K/V cache (the format:
-// fp4.cuh).  One thread quantises, or restores, one 16-value group of one
-// token's row of one head; blockIdx.y picks K or V.  Both are bound by the
-// bytes they move.
+// fp4.cuh).  One thread quantises, or restores, the 16 values of one group of
+// one token's row of one head; blockIdx.y picks K or V.  The bytes moved bound
+// both, once each thread keeps the loads of several tokens in flight and no
+// index costs a division: a thread's place in a token's row is found once.
 #include <cuda_bf16.h>
 
 #include "decode.cuh"
@@ -11,124 +12,144 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 2;  // tokens a thread works on at a time
 
 struct Fp4RowParams {
   const int64_t* slots;
   int64_t num_slots, tile_bytes;
-  int32_t num_tokens, bs_log, hkv, groups;  // groups: head_dim / 16
+  int32_t num_tokens, bs_log, hkv, groups_log, groups;  // groups of a token's row of all heads
   int32_t* status;
 };
 
-// The group of work item i: its tile's offset in the pool, its row's place,
-// or false for padding and for slots past the pool.
-__device__ __forceinline__ bool locate(const Fp4RowParams& p, int64_t i, int64_t& codes, int64_t& scales) {
-  const int64_t row = i / p.groups;  // token * hkv + head
-  const int g = static_cast<int>(i - row * p.groups);
-  const int64_t t = row / p.hkv;
-  const int h = static_cast<int>(row - t * p.hkv);
-  const int64_t slot = p.slots[t];
-  if (slot < 0) return false;
-  if (slot >= p.num_slots) {
-    if (p.status && g == 0 && h == 0 && blockIdx.y == 0) atomicExch(p.status, kDevErrInvalidArg);
-    return false;
+// 32 bytes of global memory
+__device__ __forceinline__ void load32(uint32_t (&w)[8], const void* p) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Calls body(e, row, codes, scales) for this thread's groups: `row` is the
+// group's number in the tensors of rows, the others its places in the pool.
+// kUnroll tokens at a time: `head` for each of them first, then `body`.
+template <bool BF16, typename HEAD, typename BODY>
+__device__ __forceinline__ void each_group(const Fp4RowParams& p, HEAD head, BODY body) {
+  const int per_block = p.groups < kThreads ? kThreads / p.groups : 1;  // tokens
+  const int tok = p.groups < kThreads ? threadIdx.x / p.groups : 0;
+  const int first = p.groups < kThreads ? threadIdx.x - tok * p.groups : threadIdx.x;
+  if (tok >= per_block) return;
+  const int group_mask = (1 << p.groups_log) - 1;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  for (int r = first; r < p.groups; r += kThreads) {  // once, unless a token has more groups than the block threads
+    const int h = r >> p.groups_log, g = r & group_mask;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_block + tok; t0 < p.num_tokens; t0 += step * kUnroll) {
+      int64_t codes[kUnroll], scales[kUnroll];
+      bool on[kUnroll];
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) {
+        const int64_t t = t0 + e * step;
+        const int64_t slot = t < p.num_tokens ? p.slots[t] : -1;
+        on[e] = slot >= 0 && slot < p.num_slots;
+        if (slot >= p.num_slots && p.status && r == 0 && blockIdx.y == 0) atomicExch(p.status, kDevErrInvalidArg);
+        const int64_t blk = slot >> p.bs_log;
+        const int64_t off = slot - (blk << p.bs_log);
+        const int64_t tile = (blk * p.hkv + h) * p.tile_bytes;
+        codes[e] = tile + (((off << p.groups_log) + g) << 3);
+        scales[e] = tile + (int64_t(8) << (p.groups_log + p.bs_log)) + (off << p.groups_log) + g;
+        if (on[e]) head(e, t * p.groups + r, codes[e], scales[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e)
+        if (on[e]) body(e, (t0 + e * step) * p.groups + r, codes[e], scales[e]);
+    }
   }
-  const int64_t blk = slot >> p.bs_log;
-  const int off = static_cast<int>(slot - (blk << p.bs_log));
-  const int64_t tile = (blk * p.hkv + h) * p.tile_bytes;
-  codes = tile + (static_cast<int64_t>(off) * p.groups + g) * 8;
-  scales = tile + (static_cast<int64_t>(p.groups * 8) << p.bs_log) + static_cast<int64_t>(off) * p.groups + g;
-  return true;
 }
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    fp4_append_kernel(Fp4RowParams p, const void* __restrict__ key, const void* __restrict__ value,
-                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, float k_inv, float v_inv) {
-  const void* src = blockIdx.y ? value : key;
+    fp4_append_kernel(const Fp4RowParams p, const void* __restrict__ key, const void* __restrict__ value,
+                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, float k_scale, float v_scale) {
+  const unsigned char* src = static_cast<const unsigned char*>(blockIdx.y ? value : key);
   uint8_t* cache = blockIdx.y ? v_cache : k_cache;
-  const float inv = blockIdx.y ? v_inv : k_inv;
-  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.hkv * p.groups;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    int64_t codes, scales;
-    if (!locate(p, i, codes, scales)) continue;
-    uint32_t w[16];  // the values' fp32 bits
-    if (BF16) {
-      const uint4* s = static_cast<const uint4*>(src) + i * 2;
+  const float k = blockIdx.y ? v_scale : k_scale;
+  constexpr int kWords = BF16 ? 1 : 2;  // in eights
+  uint32_t w[kUnroll][kWords][8];
+  each_group<BF16>(
+      p,
+      [&](int e, int64_t row, int64_t, int64_t) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint4 r = s[v];
-        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+        for (int i = 0; i < kWords; ++i) load32(w[e][i], src + (row * kWords + i) * 32);
+      },
+      [&](int e, int64_t, int64_t codes, int64_t scales) {
+        float x[16];
+        uint32_t top = 0;  // largest magnitude's bits
+        if (BF16) {
+          uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[v * 8 + 2 * e] = u[e] << 16;
-          w[v * 8 + 2 * e + 1] = u[e] & 0xffff0000u;
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t u = w[e][0][i];
+            m = __vmaxu2(m, u & 0x7fff7fffu);
+            x[2 * i] = __uint_as_float(u << 16);
+            x[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
+          }
+          top = max(m << 16, m & 0xffff0000u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t u = w[e][BF16 ? 0 : i >> 3][i & 7];
+            top = max(top, u & 0x7fffffffu);
+            x[i] = __uint_as_float(u);
+          }
         }
-      }
-    } else {
-      const uint4* s = static_cast<const uint4*>(src) + i * 4;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint4 r = s[v];
-        w[4 * v] = r.x;
-        w[4 * v + 1] = r.y;
-        w[4 * v + 2] = r.z;
-        w[4 * v + 3] = r.w;
-      }
-    }
-    uint32_t top = 0;
-    float x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      top = max(top, w[e] & 0x7fffffffu);
-      x[e] = __uint_as_float(w[e]) * inv;
-    }
-    uint2 c;
-    uint32_t sc;
-    fp4::quantise16(x, top, c, sc);
-    *reinterpret_cast<uint2*>(cache + codes) = c;
-    cache[scales] = static_cast<uint8_t>(sc);
-  }
+        uint2 c;
+        uint32_t sc;
+        fp4::quantise16(x, top, k, c, sc);
+        *reinterpret_cast<uint2*>(cache + codes) = c;
+        cache[scales] = static_cast<uint8_t>(sc);
+      });
 }
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    fp4_gather_kernel(Fp4RowParams p, void* __restrict__ key, void* __restrict__ value,
+    fp4_gather_kernel(const Fp4RowParams p, void* __restrict__ key, void* __restrict__ value,
                       const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache, float k_scale,
                       float v_scale) {
-  void* dst = blockIdx.y ? value : key;
+  unsigned char* dst = static_cast<unsigned char*>(blockIdx.y ? value : key);
   const uint8_t* cache = blockIdx.y ? v_cache : k_cache;
-  const float gs = blockIdx.y ? v_scale : k_scale;
-  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.hkv * p.groups;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    int64_t codes, scales;
-    if (!locate(p, i, codes, scales)) continue;
-    const uint2 c = *reinterpret_cast<const uint2*>(cache + codes);
-    const float s = fp4::scale_to_f32(cache[scales]) * gs;
-    uint32_t h[8];
-    fp4::codes_to_f16(c.x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
-    fp4::codes_to_f16(c.y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
-    uint32_t w[16];
+  const float k = blockIdx.y ? v_scale : k_scale;
+  uint2 c[kUnroll];
+  uint32_t sc[kUnroll];
+  each_group<BF16>(
+      p,
+      [&](int e, int64_t, int64_t codes, int64_t scales) {
+        c[e] = *reinterpret_cast<const uint2*>(cache + codes);
+        sc[e] = cache[scales];
+      },
+      [&](int e, int64_t row, int64_t, int64_t) {
+        const float s = fp4::scale_to_f32(sc[e]) * k;
+        uint32_t h[8], w[16];
+        fp4::codes_to_f16(c[e].x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
+        fp4::codes_to_f16(c[e].y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 f = fp4::f16x2_to_f32(h[e]);
-      w[2 * e] = __float_as_uint(f.x * s);
-      w[2 * e + 1] = __float_as_uint(f.y * s);
-    }
-    if (BF16) {  // exact: the values' low 16 bits are zero (NaN keeps its high bits)
-      uint4* d = static_cast<uint4*>(dst) + i * 2;
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = fp4::f16x2_to_f32(h[i]);
+          w[2 * i] = __float_as_uint(f.x * s);
+          w[2 * i + 1] = __float_as_uint(f.y * s);
+        }
+        if (BF16) {  // exact: the values' low 16 bits are zero (NaN keeps its high bits)
+          uint32_t o[8];
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        d[v] = make_uint4(__byte_perm(w[8 * v], w[8 * v + 1], 0x7632), __byte_perm(w[8 * v + 2], w[8 * v + 3], 0x7632),
-                          __byte_perm(w[8 * v + 4], w[8 * v + 5], 0x7632),
-                          __byte_perm(w[8 * v + 6], w[8 * v + 7], 0x7632));
-    } else {
-      uint4* d = static_cast<uint4*>(dst) + i * 4;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) d[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-    }
-  }
+          for (int i = 0; i < 8; ++i) o[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+          store32(dst + row * 32, o);
+        } else {
+          store32(dst + row * 64, reinterpret_cast<uint32_t(&)[8]>(w[0]));
+          store32(dst + row * 64 + 32, reinterpret_cast<uint32_t(&)[8]>(w[8]));
+        }
+      });
 }
 
 Fp4RowParams row_params(const int64_t* slots, int32_t num_tokens, int32_t num_blocks, int32_t block_size,
@@ -140,15 +161,19 @@ Fp4RowParams row_params(const int64_t* slots, int32_t num_tokens, int32_t num_bl
   p.num_tokens = num_tokens;
   p.bs_log = __builtin_ctz(static_cast<unsigned>(block_size));
   p.hkv = num_kv_heads;
-  p.groups = head_dim / kFp4Group;
+  p.groups_log = __builtin_ctz(static_cast<unsigned>(head_dim / kFp4Group));
+  p.groups = num_kv_heads * (head_dim / kFp4Group);
   p.status = status;
   return p;
 }
 
 dim3 row_grid(const Fp4RowParams& p) {
-  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.hkv * p.groups;
-  int64_t blocks = (total + kThreads - 1) / kThreads;
-  const int64_t cap = device_sm_count() * 32;
+  const int64_t per_block = p.groups < kThreads ? kThreads / p.groups : 1;
+  // every token its own block while that fills the card; then kUnroll and more
+  int64_t blocks = (p.num_tokens + per_block - 1) / per_block;
+  const int64_t few = device_sm_count() * 8;
+  if (blocks > few) blocks = (blocks + kUnroll - 1) / kUnroll > few ? (blocks + kUnroll - 1) / kUnroll : few;
+  const int64_t cap = device_sm_count() * 64;
   return dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 2);
 }
 
@@ -161,9 +186,9 @@ cudaError_t launch_fp4_append(const void* key, const void* value, bool src_bf16,
   const Fp4RowParams p = row_params(slots, num_tokens, num_blocks, block_size, num_kv_heads, head_dim, status);
   auto kc = static_cast<uint8_t*>(k_cache), vc = static_cast<uint8_t*>(v_cache);
   if (src_bf16)
-    fp4_append_kernel<true><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, 1.f / k_scale, 1.f / v_scale);
+    fp4_append_kernel<true><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
   else
-    fp4_append_kernel<false><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, 1.f / k_scale, 1.f / v_scale);
+    fp4_append_kernel<false><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
   return cudaGetLastError();
 }
 
