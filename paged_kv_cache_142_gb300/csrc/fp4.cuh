@@ -117,45 +117,85 @@ __device__ __forceinline__ uint32_t to_e4m3(float x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
   return r & 0xffu;
 }
-// (lo, hi) to the nearest e2m1, ties to even, at most 6: lo in the low nibble
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+// eight values to the nearest e2m1, ties to even, at most 6: their codes, the first in the lowest nibble
+__device__ __forceinline__ uint32_t to_e2m1x8(const uint64_t (&t)[4]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .f32 l, h;\n\t"
+      "mov.b64 {l, h}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 a, h, l;\n\t"
+      "mov.b64 {l, h}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b, h, l;\n\t"
+      "mov.b64 {l, h}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, h, l;\n\t"
+      "mov.b64 {l, h}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 d, h, l;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "l"(t[0]), "l"(t[1]), "l"(t[2]), "l"(t[3]));
+  return r;
+}
+// pairs of fp32
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
 // 16 fp32 values -> 8 code bytes and the scale byte, under the global scale k
-// (a power of two).  `top`: the bits of their largest magnitude.
-__device__ __forceinline__ void quantise16(float (&x)[16], uint32_t top, float k, uint2& codes, uint32_t& scale) {
+// (a power of two) with 1 / k = inv.  `top`: the bits of their largest magnitude.
+//
+// Both roundings are those of the exact quotients.  A quotient x / y is formed
+// as q + (x - q y) r, with q = x r and r an approximate 1 / y: the remainder is
+// exact, so the result is x / y to within 2^-40 of it, rounded once to fp32.
+// A border between two targets is representable, so a quotient that equals one
+// comes out equal.  One that does not is off by more than half an fp32 step: the
+// border times y has at most 7 significant bits, x differs from it by an fp32
+// step at least, and divided by y (below 2^(e+1) by 1/16 or more) that is 0.53
+// of a step of the border or more.  So it cannot round onto the border either.
+__device__ __forceinline__ void quantise16(float (&x)[16], uint32_t top, float k, float inv, uint2& codes,
+                                           uint32_t& scale) {
   if (top >= 0x7f800000u) {  // infinity or NaN among them: the group reads back as NaN
     codes = make_uint2(0, 0);
     scale = 0x7fu;
     return;
   }
-  const float inv = 1.f / k;  // exact
   const float a = __uint_as_float(top) * inv;
   if (a > 1e6f) {  // the scale is at its largest, and past 2688 so is the code: no overflow below
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -1e6f * k), 1e6f * k);
   }
-  // the correctly rounded quotient cannot cross a rounding border of the
-  // target: 6 * border has few bits, so a / 6 != border differs from it by
-  // more than half an fp32 step
-  scale = to_e4m3(__fdiv_rn(a, 6.f));
+  const float a6 = fminf(a, 1e6f), q6 = a6 * (1.f / 6.f);
+  scale = to_e4m3(fmaf(fmaf(-q6, 6.f, a6), 1.f / 6.f, q6));
   const float s = scale_to_f32(scale);
-  // x / (s k), correctly rounded: the product by the rounded reciprocal and one
-  // step with the exact remainder (k scales exactly); the same argument holds
-  const float sk = s * k, r = scale ? __frcp_rn(s) * inv : 0.f;
-  uint32_t b[8];
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = scale ? r * inv : 0.f;  // k scales exactly
+  const uint64_t r2 = pair(r, r), nsk = pair(-s * k, -s * k);
+  uint64_t t[2][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q0 = x[2 * i] * r, q1 = x[2 * i + 1] * r;
-    b[i] = to_e2m1x2(fmaf(fmaf(-q0, sk, x[2 * i]), r, q0), fmaf(fmaf(-q1, sk, x[2 * i + 1]), r, q1));
+    const uint64_t v = pair(x[2 * i], x[2 * i + 1]);
+    const uint64_t q = mul2(v, r2);
+    t[i >> 2][i & 3] = fma2(fma2(q, nsk, v), r2, q);
   }
-  codes.x = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-  codes.y = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+  codes.x = to_e2m1x8(t[0]);
+  codes.y = to_e2m1x8(t[1]);
 }
 
 }  // namespace fp4

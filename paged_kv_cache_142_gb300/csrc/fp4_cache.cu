@@ -12,7 +12,7 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;  // tokens a thread works on at a time
+constexpr int kAppendUnroll = 2, kGatherUnroll = 4;  // tokens a thread works on at a time
 
 struct Fp4RowParams {
   const int64_t* slots;
@@ -33,11 +33,12 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// Calls body(e, row, codes, scales) for this thread's groups: `row` is the
-// group's number in the tensors of rows, the others its places in the pool.
-// kUnroll tokens at a time: `head` for each of them first, then `body`.
-template <bool BF16, typename HEAD, typename BODY>
-__device__ __forceinline__ void each_group(const Fp4RowParams& p, HEAD head, BODY body) {
+// Walks this thread's groups, kUnroll tokens at a time: early(e, row) for
+// each, then early2(e, codes, scales) and last(e, row, codes, scales) for those
+// whose slot is in the pool.  `row` is the group's number in the tensors of
+// rows, codes and scales are its places in the pool.
+template <int kUnroll, typename EARLY, typename EARLY2, typename LAST>
+__device__ __forceinline__ void each_group(const Fp4RowParams& p, EARLY early, EARLY2 early2, LAST last) {
   const int per_block = p.groups < kThreads ? kThreads / p.groups : 1;  // tokens
   const int tok = p.groups < kThreads ? threadIdx.x / p.groups : 0;
   const int first = p.groups < kThreads ? threadIdx.x - tok * p.groups : threadIdx.x;
@@ -47,43 +48,53 @@ __device__ __forceinline__ void each_group(const Fp4RowParams& p, HEAD head, BOD
   for (int r = first; r < p.groups; r += kThreads) {  // once, unless a token has more groups than the block threads
     const int h = r >> p.groups_log, g = r & group_mask;
     for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_block + tok; t0 < p.num_tokens; t0 += step * kUnroll) {
-      int64_t codes[kUnroll], scales[kUnroll];
-      bool on[kUnroll];
+      int64_t slot[kUnroll], codes[kUnroll], scales[kUnroll];
 #pragma unroll
       for (int e = 0; e < kUnroll; ++e) {
         const int64_t t = t0 + e * step;
-        const int64_t slot = t < p.num_tokens ? p.slots[t] : -1;
-        on[e] = slot >= 0 && slot < p.num_slots;
-        if (slot >= p.num_slots && p.status && r == 0 && blockIdx.y == 0) atomicExch(p.status, kDevErrInvalidArg);
-        const int64_t blk = slot >> p.bs_log;
-        const int64_t off = slot - (blk << p.bs_log);
+        slot[e] = -1;
+        if (t < p.num_tokens) {
+          slot[e] = p.slots[t];
+          early(e, t * p.groups + r);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) {
+        if (slot[e] >= p.num_slots) {  // past the pool: reported, neither written nor read
+          if (p.status && r == 0 && blockIdx.y == 0) atomicExch(p.status, kDevErrInvalidArg);
+          slot[e] = -1;
+        }
+        const int64_t blk = slot[e] >> p.bs_log;
+        const int64_t off = slot[e] - (blk << p.bs_log);
         const int64_t tile = (blk * p.hkv + h) * p.tile_bytes;
         codes[e] = tile + (((off << p.groups_log) + g) << 3);
         scales[e] = tile + (int64_t(8) << (p.groups_log + p.bs_log)) + (off << p.groups_log) + g;
-        if (on[e]) head(e, t * p.groups + r, codes[e], scales[e]);
+        if (slot[e] >= 0) early2(e, codes[e], scales[e]);
       }
 #pragma unroll
       for (int e = 0; e < kUnroll; ++e)
-        if (on[e]) body(e, (t0 + e * step) * p.groups + r, codes[e], scales[e]);
+        if (slot[e] >= 0) last(e, (t0 + e * step) * p.groups + r, codes[e], scales[e]);
     }
   }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3)
     fp4_append_kernel(const Fp4RowParams p, const void* __restrict__ key, const void* __restrict__ value,
-                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, float k_scale, float v_scale) {
+                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, float k_scale, float v_scale,
+                      float k_inv, float v_inv) {
   const unsigned char* src = static_cast<const unsigned char*>(blockIdx.y ? value : key);
   uint8_t* cache = blockIdx.y ? v_cache : k_cache;
-  const float k = blockIdx.y ? v_scale : k_scale;
+  const float k = blockIdx.y ? v_scale : k_scale, inv = blockIdx.y ? v_inv : k_inv;
   constexpr int kWords = BF16 ? 1 : 2;  // in eights
-  uint32_t w[kUnroll][kWords][8];
-  each_group<BF16>(
+  uint32_t w[kAppendUnroll][kWords][8];
+  each_group<kAppendUnroll>(
       p,
-      [&](int e, int64_t row, int64_t, int64_t) {
+      [&](int e, int64_t row) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) load32(w[e][i], src + (row * kWords + i) * 32);
       },
+      [](int, int64_t, int64_t) {},
       [&](int e, int64_t, int64_t codes, int64_t scales) {
         float x[16];
         uint32_t top = 0;  // largest magnitude's bits
@@ -107,7 +118,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         uint2 c;
         uint32_t sc;
-        fp4::quantise16(x, top, k, c, sc);
+        fp4::quantise16(x, top, k, inv, c, sc);
         *reinterpret_cast<uint2*>(cache + codes) = c;
         cache[scales] = static_cast<uint8_t>(sc);
       });
@@ -121,11 +132,11 @@ __global__ void __launch_bounds__(kThreads)
   unsigned char* dst = static_cast<unsigned char*>(blockIdx.y ? value : key);
   const uint8_t* cache = blockIdx.y ? v_cache : k_cache;
   const float k = blockIdx.y ? v_scale : k_scale;
-  uint2 c[kUnroll];
-  uint32_t sc[kUnroll];
-  each_group<BF16>(
-      p,
-      [&](int e, int64_t, int64_t codes, int64_t scales) {
+  uint2 c[kGatherUnroll];
+  uint32_t sc[kGatherUnroll];
+  each_group<kGatherUnroll>(
+      p, [](int, int64_t) {},
+      [&](int e, int64_t codes, int64_t scales) {
         c[e] = *reinterpret_cast<const uint2*>(cache + codes);
         sc[e] = cache[scales];
       },
@@ -167,12 +178,12 @@ Fp4RowParams row_params(const int64_t* slots, int32_t num_tokens, int32_t num_bl
   return p;
 }
 
-dim3 row_grid(const Fp4RowParams& p) {
+dim3 row_grid(const Fp4RowParams& p, int unroll) {
   const int64_t per_block = p.groups < kThreads ? kThreads / p.groups : 1;
-  // every token its own block while that fills the card; then kUnroll and more
+  // every token its own block while that fills the card; then unroll and more
   int64_t blocks = (p.num_tokens + per_block - 1) / per_block;
   const int64_t few = device_sm_count() * 8;
-  if (blocks > few) blocks = (blocks + kUnroll - 1) / kUnroll > few ? (blocks + kUnroll - 1) / kUnroll : few;
+  if (blocks > few) blocks = (blocks + unroll - 1) / unroll > few ? (blocks + unroll - 1) / unroll : few;
   const int64_t cap = device_sm_count() * 64;
   return dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 2);
 }
@@ -186,9 +197,11 @@ cudaError_t launch_fp4_append(const void* key, const void* value, bool src_bf16,
   const Fp4RowParams p = row_params(slots, num_tokens, num_blocks, block_size, num_kv_heads, head_dim, status);
   auto kc = static_cast<uint8_t*>(k_cache), vc = static_cast<uint8_t*>(v_cache);
   if (src_bf16)
-    fp4_append_kernel<true><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
+    fp4_append_kernel<true><<<row_grid(p, kAppendUnroll), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale,
+                                                                                1.f / k_scale, 1.f / v_scale);
   else
-    fp4_append_kernel<false><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
+    fp4_append_kernel<false><<<row_grid(p, kAppendUnroll), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale,
+                                                                                 1.f / k_scale, 1.f / v_scale);
   return cudaGetLastError();
 }
 
@@ -199,9 +212,9 @@ cudaError_t launch_fp4_gather(void* key, void* value, bool dst_bf16, int32_t num
   const Fp4RowParams p = row_params(slots, num_tokens, num_blocks, block_size, num_kv_heads, head_dim, status);
   auto kc = static_cast<const uint8_t*>(k_cache), vc = static_cast<const uint8_t*>(v_cache);
   if (dst_bf16)
-    fp4_gather_kernel<true><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
+    fp4_gather_kernel<true><<<row_grid(p, kGatherUnroll), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
   else
-    fp4_gather_kernel<false><<<row_grid(p), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
+    fp4_gather_kernel<false><<<row_grid(p, kGatherUnroll), kThreads, 0, stream>>>(p, key, value, kc, vc, k_scale, v_scale);
   return cudaGetLastError();
 }
 

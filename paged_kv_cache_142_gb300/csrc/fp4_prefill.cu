@@ -152,26 +152,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // waits for this warp's tensor-memory loads; what uses v comes after it
 __device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -187,7 +167,7 @@ __device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
 template <bool MASK>
 __device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&pk)[64],
                                               float& top, float& sum) {
-  const uint64_t ff = pack2(f, f), bb = pack2(bias, bias);
+  const uint64_t ff = fp4::pair(f, f), bb = fp4::pair(bias, bias);
   uint64_t s0 = 0, s1 = 0;
   float m0 = -CUDART_INF_F, m1 = m0;
   uint32_t v[2][16];
@@ -206,16 +186,16 @@ __device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, 
       }
       m0 = max3(m0, x[0], x[1]);
       m1 = max3(m1, x[2], x[3]);
-      const float2 a = unpack2(fma2(pack2(x[0], x[1]), ff, bb)), b = unpack2(fma2(pack2(x[2], x[3]), ff, bb));
+      const float2 a = fp4::unpair(fp4::fma2(fp4::pair(x[0], x[1]), ff, bb)), b = fp4::unpair(fp4::fma2(fp4::pair(x[2], x[3]), ff, bb));
       const float e0 = fast_exp2(a.x), e1 = fast_exp2(a.y), e2 = fast_exp2(b.x), e3 = fast_exp2(b.y);
-      s0 = add2(s0, pack2(e0, e1));
-      s1 = add2(s1, pack2(e2, e3));
+      s0 = fp4::add2(s0, fp4::pair(e0, e1));
+      s1 = fp4::add2(s1, fp4::pair(e2, e3));
       pk[(c * 16 + j) / 2] = pack_f16(e0, e1);
       pk[(c * 16 + j) / 2 + 1] = pack_f16(e2, e3);
     }
   }
   top = fmaxf(m0, m1);
-  const float2 t = unpack2(add2(s0, s1));
+  const float2 t = fp4::unpair(fp4::add2(s0, s1));
   sum = t.x + t.y;
 }
 // the largest of a row's first nvis scores of a step
