@@ -9,6 +9,7 @@ missing.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import numpy as np
 import torch
@@ -32,8 +33,9 @@ def dtype_code(dt) -> int:
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream)
 
 
 def _need(cond: bool, msg: str) -> None:
@@ -46,9 +48,9 @@ def _on_current_device(*tensors) -> None:
     so every tensor handed to it must live there."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda:
-            _need(t.device.index == dev, f"tensor on cuda:{t.device.index} but the current device is "
-                  f"cuda:{dev}: call inside torch.cuda.device(...) of the tensors' device")
+        if t is not None and t.get_device() not in (dev, -1):
+            raise ValueError(f"tensor on cuda:{t.get_device()} but the current device is "
+                             f"cuda:{dev}: call inside torch.cuda.device(...) of the tensors' device")
 
 
 def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor):
@@ -60,29 +62,38 @@ def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor):
     return k_cache.shape
 
 
+@functools.lru_cache(maxsize=None)
+def fp4_tile_bytes(block_size, head_dim) -> int:
+    """Bytes of one (block, kv head) tile of a 4-bit cache."""
+    n = _LIB.pa_fp4_tile_bytes(int(block_size), int(head_dim))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_fp4_tile_bytes")
+    return int(n)
+
+
 def _fp4_dims(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size, head_dim):
     """(NB, Hkv) of 4-bit caches [NB, Hkv, tile]."""
     _need(block_size is not None and head_dim is not None, "4-bit caches need block_size and head_dim")
     tile = fp4_tile_bytes(block_size, head_dim)
-    for c in (k_cache, v_cache):
-        _need(c.dtype == torch.uint8 and c.is_cuda, "4-bit caches must be CUDA uint8 tensors")
-        _need(c.dim() == 3 and c.shape[2] == tile and c.is_contiguous(),
-              f"4-bit caches must be contiguous [NB, Hkv, {tile}] for block_size {block_size}, head_dim {head_dim}")
-    _need(k_cache.shape == v_cache.shape, "K and V caches must share a shape")
-    _on_current_device(k_cache, v_cache)
-    return k_cache.shape[0], k_cache.shape[1]
+    shape = k_cache.shape
+    if len(shape) != 3 or shape[2] != tile or v_cache.shape != shape:
+        raise ValueError(f"4-bit caches must be [NB, Hkv, {tile}] both, for block_size {block_size}, "
+                         f"head_dim {head_dim}")
+    _need(k_cache.dtype is torch.uint8 and v_cache.dtype is torch.uint8 and k_cache.is_cuda and v_cache.is_cuda
+          and k_cache.is_contiguous() and v_cache.is_contiguous(), "4-bit caches must be contiguous CUDA uint8 tensors")
+    return shape[0], shape[1]
 
 
 def _any_cache_dims(k_cache, v_cache, block_size, head_dim):
     """(NB, Hkv, bs, D, dtype code) of caches of any dtype."""
-    if k_cache.dtype == torch.uint8:
+    if k_cache.dtype is torch.uint8:
         return (*_fp4_dims(k_cache, v_cache, block_size, head_dim), int(block_size), int(head_dim), PA_DTYPE_FP4)
     return (*_cache_dims(k_cache, v_cache), dtype_code(k_cache.dtype))
 
 
 def _any_layer_cache_dims(k_cache, v_cache, block_size, head_dim):
     """(L, NB, Hkv, bs, D, dtype code) of multi-layer caches of any dtype."""
-    if k_cache.dtype == torch.uint8:
+    if k_cache.dtype is torch.uint8:
         _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.stride(0) == v_cache.stride(0),
               "4-bit caches must be [L, NB, Hkv, tile] with one layer stride for K and V")
         nb, hkv = _fp4_dims(k_cache[0], v_cache[0], block_size, head_dim)
@@ -127,7 +138,7 @@ def pa_copy_blocks(k_cache, v_cache, block_pairs, stream=None, status=None, bloc
     (pa_copy_blocks_checked).  4-bit caches (uint8): give ``block_size`` and
     ``head_dim``."""
     NB, Hkv, bs, D, dt = _any_cache_dims(k_cache, v_cache, block_size, head_dim)
-    _on_current_device(block_pairs, status)
+    _on_current_device(k_cache, v_cache, block_pairs, status)
     n = block_pairs.shape[0] if block_pairs.numel() else 0
     if n:
         _need(block_pairs.dtype == torch.int64 and block_pairs.is_cuda and block_pairs.is_contiguous()
@@ -347,8 +358,8 @@ def pa_workspace_error(workspace, stream=None) -> int:
 # a cache held in 4 bits, and token compaction
 # --------------------------------------------------------------------------
 def _i32(t, numel, what):
-    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == numel,
-          f"{what} must be a contiguous CUDA int32 tensor of {numel} entries")
+    if not (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == numel):
+        raise ValueError(f"{what} must be a contiguous CUDA int32 tensor of {numel} entries")
 
 
 def _status_ptr(status):
@@ -356,14 +367,6 @@ def _status_ptr(status):
         return None
     _need(status.dtype == torch.int32 and status.is_cuda and status.numel() >= 1, "status must be a CUDA int32 tensor")
     return status.data_ptr()
-
-
-def fp4_tile_bytes(block_size, head_dim) -> int:
-    """Bytes of one (block, kv head) tile of a 4-bit cache."""
-    n = _LIB.pa_fp4_tile_bytes(int(block_size), int(head_dim))
-    if n == 0:
-        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_fp4_tile_bytes")
-    return int(n)
 
 
 def make_cache_fp4(num_blocks, num_kv_heads, block_size, head_dim, num_layers=None, device="cuda") -> torch.Tensor:
@@ -381,7 +384,6 @@ def _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size):
           "key/value must be contiguous CUDA tensors")
     _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T and slot_mapping.is_cuda
           and slot_mapping.is_contiguous(), "slot_mapping must be a contiguous CUDA int64 tensor of num_tokens entries")
-    _on_current_device(key, value, slot_mapping)
     return T, NB, Hkv, D
 
 
@@ -390,7 +392,7 @@ def pa_reshape_and_cache_fp4(key, value, slot_mapping, k_cache, v_cache, block_s
     """Quantise key/value ``[T, Hkv, D]`` (fp32 or bf16) into the slots
     ``slot_mapping[T]`` of the 4-bit caches."""
     T, NB, Hkv, D = _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size)
-    _on_current_device(status)
+    _on_current_device(key, value, slot_mapping, k_cache, v_cache, status)
     L.check(_LIB.pa_reshape_and_cache_fp4(
         key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
@@ -402,7 +404,7 @@ def pa_gather_cache_fp4(key, value, slot_mapping, k_cache, v_cache, block_size, 
     """Fill key/value ``[T, Hkv, D]`` (fp32 or bf16) with the values held in
     the slots ``slot_mapping[T]``; rows of negative slots stay as they are."""
     T, NB, Hkv, D = _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size)
-    _on_current_device(status)
+    _on_current_device(key, value, slot_mapping, k_cache, v_cache, status)
     L.check(_LIB.pa_gather_cache_fp4(
         key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
@@ -434,8 +436,7 @@ def _fp4_queries(out, q, k_cache, v_cache, block_tables, num_seqs, num_kv_heads,
     _need(block_tables.dtype == torch.int32 and block_tables.is_cuda and block_tables.dim() == 2
           and block_tables.shape[0] == num_seqs and block_tables.is_contiguous(),
           "block_tables must be contiguous int32 [num_seqs, max_blocks]")
-    _need(workspace.dtype == torch.uint8 and workspace.is_cuda, "workspace must be a CUDA uint8 tensor")
-    _on_current_device(out, q, block_tables, workspace)
+    _need(workspace.dtype is torch.uint8 and workspace.is_cuda, "workspace must be a CUDA uint8 tensor")
     return NB
 
 
@@ -445,7 +446,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, context_lens, scale, n
     B, H, D = q.shape
     NB = _fp4_queries(out, q, k_cache, v_cache, block_tables, B, num_kv_heads, block_size, workspace)
     _i32(context_lens, B, "context_lens")
-    _on_current_device(context_lens)
+    _on_current_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
     L.check(_LIB.pa_decode_fp4(
         out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), B, H, k_cache.data_ptr(), v_cache.data_ptr(), NB,
         int(block_size), num_kv_heads, D, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
@@ -472,7 +473,7 @@ def pa_prefill_fp4(out, q, k_cache, v_cache, cu_q, q_start, block_tables, scale,
     _i32(cu_q, S + 1, "cu_q")
     _i32(q_start, S, "q_start")
     NB = _fp4_queries(out, q, k_cache, v_cache, block_tables, S, num_kv_heads, block_size, workspace)
-    _on_current_device(cu_q, q_start, status)
+    _on_current_device(out, q, k_cache, v_cache, block_tables, cu_q, q_start, status, workspace)
     L.check(_LIB.pa_prefill_fp4(
         out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), T, cu_q.data_ptr(), q_start.data_ptr(), S,
         int(max_q_len), int(max_context_len), H, k_cache.data_ptr(), v_cache.data_ptr(), NB, int(block_size),
