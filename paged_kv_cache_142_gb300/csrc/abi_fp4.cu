@@ -90,7 +90,7 @@ size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32
       check_pool(1, block_size, num_kv_heads, head_dim) != PA_OK || num_q_heads % num_kv_heads ||
       !group_ok(num_q_heads, num_kv_heads))
     return 0;
-  return pa::fp4_decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim);
+  return pa::fp4_decode_workspace(num_q_heads, num_kv_heads, head_dim);
 }
 
 pa_status pa_decode_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t num_seqs, int32_t num_q_heads,
@@ -165,6 +165,7 @@ pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t n
     return PA_ERR_INVALID_ARG;
   const size_t need = pa_prefill_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                                     max_q_len, max_context_len);
+  if (need == 0) return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return PA_ERR_WORKSPACE;
   pa::Fp4AttnParams p{};
   p.out = out;

@@ -54,7 +54,8 @@ cudaError_t launch_fp4_gather(void* key, void* value, bool dst_bf16, int32_t num
                               int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale, int32_t* status,
                               cudaStream_t stream);
 cudaError_t fp4_occupancy(const void* fn, int threads, int smem, int* per_sm);
-size_t fp4_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim);
+int64_t fp4_counter_bytes();
+size_t fp4_decode_workspace(int num_q_heads, int num_kv_heads, int head_dim);
 cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t stream);
 size_t fp4_prefill_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int max_q_len, int max_context_len);
 cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream);

@@ -71,7 +71,7 @@ struct Launch {
   int kv_bytes;            // of one unit's K (or V) in shared memory
   int off_merge, off_stat, off_qraw, off_q, off_qfac, off_prefix, off_lens, off_bar;
   uint32_t tile_bytes;
-  int32_t* counters;       // [nseq * num_kv_heads], zero between launches
+  int32_t* counters;       // [CTAs], zero between launches: of the head that CTA is the first of several to work on
   float* part;             // [2 * CTAs][G * (D + 2)]
 };
 
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       __syncthreads();
       const int c0 = cta_of(item_b), c1 = cta_of(item_b + sc.nst - 1);
       if (tid == 0) {
-        int32_t* counter = L.counters + sc.seq * hkv + sc.head;
+        int32_t* counter = L.counters + c0;
         const int before = atomicAdd(counter, 1);
         last_flag = before == c1 - c0;
         if (before == c1 - c0) *counter = 0;
@@ -825,6 +825,8 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // they are taken as two kv heads of 8 that share their pages.
 int per_cache_head(int head_dim, int group) { return head_dim == 256 && group == 16 ? 2 : 1; }
 
+int64_t fp4_counter_bytes() { return round_up(4 * device_sm_count() * 4, 256); }
+
 // CTAs of a kernel that an SM holds with this much dynamic shared memory, the
 // answers kept for the devices and sizes that come by.
 cudaError_t fp4_occupancy(const void* fn, int threads, int smem, int* per_sm) {
@@ -858,13 +860,12 @@ cudaError_t fp4_occupancy(const void* fn, int threads, int smem, int* per_sm) {
   return cudaSuccess;
 }
 
-size_t fp4_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
+size_t fp4_decode_workspace(int num_q_heads, int num_kv_heads, int head_dim) {
   using namespace fp4_decode_detail;
   const int split = per_cache_head(head_dim, num_q_heads / num_kv_heads);
   const int G = num_q_heads / num_kv_heads / split;
-  const int64_t seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
-  return static_cast<size_t>(256 + round_up(seqs * num_kv_heads * split * 4, 256) +
-                             max_ctas(head_dim, G) * 2 * G * (head_dim + 2) * 4);
+  // header | counters | parts: the first two lie where they lie for every shape
+  return static_cast<size_t>(256 + fp4_counter_bytes() + max_ctas(head_dim, G) * 2 * G * (head_dim + 2) * 4);
 }
 
 cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t stream) {
@@ -875,11 +876,16 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
   const int eff = p.block_size < kUnit ? p.block_size : kUnit;
   const int eff_log = __builtin_ctz(static_cast<unsigned>(eff));
   const void* fn = kernel_for(head_dim, G, eff_log);
-  for (int seq0 = 0; seq0 < p.num_seqs; seq0 += kMaxSeqs) {
+  // sequences of one launch: their places fit an int
+  const int64_t places = (static_cast<int64_t>(p.max_context_len) + kUnit - 1) / kUnit + 1 + kLead;
+  const int64_t fit = ((int64_t(1) << 31) - 1) / (places * hkv);
+  const int seqs = static_cast<int>(fit < kMaxSeqs ? fit : kMaxSeqs);
+  if (seqs < 1) return cudaErrorInvalidValue;
+  for (int seq0 = 0; seq0 < p.num_seqs; seq0 += seqs) {
     Launch L{};
     L.p = p;
     L.seq0 = seq0;
-    L.nseq = p.num_seqs - seq0 < kMaxSeqs ? p.num_seqs - seq0 : kMaxSeqs;
+    L.nseq = p.num_seqs - seq0 < seqs ? p.num_seqs - seq0 : seqs;
     L.hkv = hkv;
     L.group = G;
     L.cache_heads = p.num_kv_heads;
@@ -906,8 +912,7 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     L.off_lens = take(L.nseq * 4);
     L.off_bar = take(8);
     L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
-    const int64_t seqs = p.num_seqs < kMaxSeqs ? p.num_seqs : kMaxSeqs;
-    L.part = reinterpret_cast<float*>(p.ws + 256 + round_up(seqs * hkv * 4, 256));
+    L.part = reinterpret_cast<float*>(p.ws + 256 + fp4_counter_bytes());
     // at least a unit for every warp, as far as the longest context allows
     const int64_t most = static_cast<int64_t>(L.nseq) * hkv * ((p.max_context_len + kUnit - 1) / kUnit);
     int64_t ctas = (most + kWarps - 1) / kWarps;

@@ -4,20 +4,26 @@
 //   S[128 rows x 128 keys]  = Q K^T,   P = 2^(S f - m),   O[128 x 128] += P V
 // A row is one query head of one token; a CTA takes two tiles of 128 rows
 // (TQ = 128 / G tokens x the G heads of a kv head, each), so every key and
-// value that it restores from 4 bits serves 256 rows.  All operands are f16:
-// code * scale is exact there, the queries are scaled by a power of two per row
-// (their largest magnitude to 2^14, exact down to 2^-28 of it), and the
-// probabilities are rounded to 11 bits (2^-12 each, where bf16 would leave
-// 2^-9); accumulators are fp32 in tensor memory: S of both tiles, O of both.
-// P is written over its S and read from there as the A operand.
+// value that it restores from 4 bits serves 256 rows.  code * scale is exact in
+// bf16 and in f16.  Keys become bf16, so that the queries enter as they are, by
+// TMA; values become f16, so that the probabilities are rounded to 11 bits
+// (2^-12 each, where bf16 would leave 2^-9).  Accumulators are fp32 in tensor
+// memory: S of both tiles, O of both.  P is written over its S and read from
+// there as the A operand.
 //
-// One CTA per SM, 14 warps, persistent over (tile pair, sequence, kv head,
-// part of the keys):
+// The work is cut into equal runs of steps (128 keys of a tile pair), one for
+// each CTA, across the borders of heads, tile pairs and sequences; an item is
+// a (sequence, tile pair, kv head).  A CTA that takes part of an item's keys
+// leaves its rows unnormalised in the workspace with their maximum and sum, and
+// the last CTA of the item adds the parts up in the order of the keys.
+//
+// One CTA per SM, 14 warps, each role walking the same items:
 //  * warps 8-11 restore: a thread owns one key of a tile.  It reads the key's
 //    64 code bytes and 8 scales through the block table, one tile ahead, and
-//    writes the 128 f16 values in the 128-byte-swizzled layout that the
-//    tensor core reads; then the same for the value row.  They load the
-//    queries too, and the power of two of each row;
+//    writes the 128 values in the 128-byte-swizzled layout that the tensor core
+//    reads; then the same for the value row.  Warp 8 loads the queries too
+//    (turning them to f16 here instead, with a power of two for each row, cost
+//    12000 clocks an item: four warps of long dependent chains);
 //  * warps 12 and 13 issue the products of the first and the second tile.
 //    Q.K^T of a tile's next step is issued right behind P.V of its last one,
 //    which read P from the same columns (the tensor core runs a thread's
@@ -29,12 +35,11 @@
 // What bounds it: the tensor core needs about 2150 clocks for a step's four
 // products, the exponentials and their conversions about 1700 of the SM's
 // issue slots, the restoring about 400.
-//
-// With fewer tile pairs than SMs the keys are cut into parts; a part's rows go
-// to the workspace unnormalised with their maximum and sum, and a second
-// launch adds the parts up in order.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "decode.cuh"
 #include "fp4.cuh"
@@ -48,9 +53,9 @@ constexpr int kTileBytes = 32768;  // 128 rows x 128 f16
 constexpr int kOffQ = 0;           // two tiles: [half of the dims][128 rows][128 bytes]
 constexpr int kOffK = 2 * kTileBytes;
 constexpr int kOffV = kOffK + 2 * kTileBytes;
-constexpr int kOffFac = kOffV + 2 * kTileBytes;   // [2 items][256] row factors
-constexpr int kOffBar = kOffFac + 2 * 256 * 4;
-constexpr int kSmemBytes = kOffBar + 256 + 1024;  // then slack to align the base
+constexpr int kOffBar = kOffV + 2 * kTileBytes;
+constexpr int kOffPrefix = kOffBar + 256;         // [sequences + 1] places before a sequence
+constexpr int kSmemBytes = kOffPrefix + 1024;     // with slack to align the base, then the places
 constexpr float kSlack = 8.f;     // the reference is raised past 2^8
 constexpr float kPShift = 6.f;    // probabilities enter P.V times 2^6: below 2^14, none lost before 2^-30
 
@@ -62,60 +67,107 @@ enum : int {
 static_assert(kNumBars * 8 + 16 <= 256, "barrier area");
 constexpr uint32_t kColO = 256;  // tensor memory: S of the tiles at 0 and 128, then O of the tiles
 
+// What starting and ending an item costs a CTA, in steps: the shares count it,
+// as places before the item's first step.
+constexpr int kLead = 1;
+constexpr int kMaxSeqs = 4096;   // of one launch: their places lie in shared memory
+constexpr int kMostParts = 32;   // CTAs of an item
+
 struct Launch {
-  Fp4AttnParams p;
-  int pairs;       // tile pairs of the longest chunk
-  int parts;       // parts of the keys
+  Fp4AttnParams p;      // of this launch's sequences
+  int rows;             // of a part: the most that a tile pair has
   uint32_t tile_bytes;
   int bs_log;
-  // parts > 1, rows (sequence * max_q_len + token of the chunk) * heads + head:
-  float* ml;       // [parts][rows][2] maximum (log2), sum
-  float* o;        // [parts][rows][128]
+  int32_t* counters;    // [CTAs], zero between launches: of the item that CTA is the first of several to work on
+  float* ml;            // [2 * CTAs][rows][2] maximum (log2), sum
+  float* o;             // [2 * CTAs][rows][128]
 };
 
 struct Item {
-  int seq, kvh, tok0, qb, pos0;  // first token: in the chunk, in q; position of tok0
-  int ntok;                      // tokens of the pair's two tiles
-  int part, t0, t1;              // tiles of keys
-  int kend;                      // keys that the last token sees
-  int n[2];                      // steps of each tile
+  int seq, pair, kvh, tok0, qb, pos0;  // first token: in the chunk, in q; position of tok0
+  int ntok;                            // tokens of the pair's two tiles
+  int start, end;                      // places: kLead, then the steps
+  int t0, t1;                          // this CTA's steps
+  int kend;                            // keys that the last token sees
+  int n[2];                            // this CTA's steps of each tile
+  bool whole;                          // all steps are this CTA's
+};
+
+// A sequence's items, pair after pair with the kv heads inside.  Pair j has
+// kLead + ceil((q0 + tokens up to its end) / 128) places for each head.
+template <int G>
+struct Chunk {
+  static constexpr int S = 256 / G;  // tokens of a pair
+  int b, n, q0;
+  __device__ __forceinline__ int pairs() const { return (n + S - 1) / S; }
+  __device__ __forceinline__ int tiles(int j) const { return (q0 + min(n, (j + 1) * S) + 127) / 128; }
+  // places of pairs 0 .. j - 1, all whole, for one head
+  __device__ __forceinline__ int before(int j) const {
+    if (S > 128) return j * (kLead + (q0 + 127) / 128) + j * (j + 1);  // two more tiles for every pair
+    // sum of ceil((a + t) / per) over t = 1 .. j, with q0 rounded up to pairs a
+    constexpr int per = S > 128 ? 1 : 128 / S;
+    const int a = (q0 + S - 1) / S;
+    auto f = [](int x) {
+      const int k = x / per, r = x % per;
+      return per * (k * (k + 1) / 2) + r * (k + 1);
+    };
+    return j * kLead + f(a + j) - f(a);
+  }
+  __device__ __forceinline__ int places() const {  // of one head
+    if (n <= 0) return 0;
+    const int j = pairs() - 1;
+    return before(j) + kLead + tiles(j);
+  }
 };
 
 template <int G>
-__device__ __forceinline__ bool item_at(const Launch& L, int w, Item& it) {
+__device__ __forceinline__ Chunk<G> chunk_of(const Launch& L, int seq) {
+  Chunk<G> c;
+  c.b = L.p.cu_q[seq];
+  c.n = L.p.cu_q[seq + 1] - c.b;
+  c.q0 = L.p.q_start[seq];
+  return c;
+}
+
+// The item at place `pos` of the launch, and what of it lies before `c_end`.
+template <int G>
+__device__ __forceinline__ void item_at(const Launch& L, const int* prefix, int pos, int c_end, Item& it) {
   constexpr int TQ = 128 / G;
-  const Fp4AttnParams& p = L.p;
-  const int npairs = p.num_seqs * p.num_kv_heads;
-  // later (longer) tiles first; sequences and heads, then parts, fastest
-  const int per = npairs * L.parts;
-  const int tile = L.pairs - 1 - w / per;
-  int r = w % per;
-  it.part = r / npairs;
-  r -= it.part * npairs;
-  it.seq = r / p.num_kv_heads;
-  it.kvh = r - it.seq * p.num_kv_heads;
-  const int b = p.cu_q[it.seq], n = p.cu_q[it.seq + 1] - b, q0 = p.q_start[it.seq];
-  it.tok0 = tile * 2 * TQ;
-  if (n <= 0 || it.tok0 >= n) return false;
-  const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) << L.bs_log;
-  const int64_t last = static_cast<int64_t>(q0) + n;
-  if (b < 0 || static_cast<int64_t>(b) + n > p.num_tokens || q0 < 0 || n > p.max_q_len || last > table_tokens ||
-      last > p.max_context_len) {
-    if (p.err) atomicExch(p.err, kDevErrInvalidArg);
-    return false;
+  const int hkv = L.p.num_kv_heads;
+  int lo = 0, hi = L.p.num_seqs - 1;
+  while (lo < hi) {  // the last sequence that starts at or before pos (none of no places after it)
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= pos) lo = mid;
+    else hi = mid - 1;
   }
-  it.qb = b;
-  it.ntok = min(2 * TQ, n - it.tok0);
-  it.pos0 = q0 + it.tok0;
+  it.seq = lo;
+  const Chunk<G> c = chunk_of<G>(L, lo);
+  int r = pos - prefix[lo];
+  int a = 0, b = c.pairs() - 1;
+  while (a < b) {
+    const int mid = (a + b + 1) >> 1;
+    if (hkv * c.before(mid) <= r) a = mid;
+    else b = mid - 1;
+  }
+  it.pair = a;
+  r -= hkv * c.before(a);
+  const int tiles = c.tiles(a), places = kLead + tiles;
+  it.kvh = r / places;
+  it.start = pos - (r - it.kvh * places);
+  it.end = it.start + places;
+  it.tok0 = a * 2 * TQ;
+  it.qb = c.b;
+  it.ntok = min(2 * TQ, c.n - it.tok0);
+  it.pos0 = c.q0 + it.tok0;
   it.kend = it.pos0 + it.ntok;
-  const int tiles = (it.kend + 127) / 128;
-  it.t0 = static_cast<int>(static_cast<int64_t>(tiles) * it.part / L.parts);
-  it.t1 = static_cast<int>(static_cast<int64_t>(tiles) * (it.part + 1) / L.parts);
+  const int first = it.start + kLead;
+  it.t0 = max(pos, first) - first;
+  it.t1 = min(c_end, it.end) - first;
+  it.whole = it.t0 == 0 && it.t1 == tiles;
   // the first tile's last token may see fewer keys than the second's
   const int seen0 = (it.pos0 + min(TQ, it.ntok) + 127) / 128;
   it.n[0] = max(0, min(it.t1, seen0) - it.t0);
-  it.n[1] = it.ntok > TQ ? it.t1 - it.t0 : 0;
-  return true;
+  it.n[1] = it.ntok > TQ ? max(0, it.t1 - it.t0) : 0;
 }
 
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
@@ -223,25 +275,52 @@ struct Row {
 
 }  // namespace fp4_prefill_detail
 
+namespace fp4_prefill_detail {
+// 32 outputs of a row, times inv
+__device__ __forceinline__ void store_out(const Fp4AttnParams& p, int64_t at, const uint32_t (&v)[32], float inv) {
+  if (p.out_bf16) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * e]) * inv,
+                                                       __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+        h[e] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      dst[q] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                           __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+  }
+}
+}  // namespace fp4_prefill_detail
+
 template <int G>
 __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
-    fp4_prefill_kernel(const __grid_constant__ fp4_prefill_detail::Launch L) {
+    fp4_prefill_kernel(const __grid_constant__ fp4_prefill_detail::Launch L, const __grid_constant__ CUtensorMap tm_q) {
   using namespace fp4_prefill_detail;
   constexpr int TQ = 128 / G;
   const Fp4AttnParams& p = L.p;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* fac = reinterpret_cast<float*>(smem + kOffFac);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int items = p.num_seqs * p.num_kv_heads * L.pairs * L.parts;
+  int* prefix = reinterpret_cast<int*>(smem + kOffPrefix);
+  __shared__ int warp_sums[kThreads / 32];
+  __shared__ int last_flag;
 
   ptx::griddep_launch_dependents();
   if (tid == 0) {
-    ptx::mbar_init(&bars[kQFull], 4);
+    ptx::mbar_init(&bars[kQFull], 1);
     ptx::mbar_init(&bars[kQFree], 2);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars[kKFull + i], 4);
@@ -266,6 +345,43 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   bool aborted = false;
   ptx::griddep_wait();
+
+  // ---- places before every sequence; a chunk that is refused has none ----
+  {
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int beg = min(p.num_seqs, tid * per), end = min(p.num_seqs, beg + per);
+    const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) << L.bs_log;
+    int local = 0;
+    for (int s = beg; s < end; ++s) {
+      const Chunk<G> c = chunk_of<G>(L, s);
+      const int64_t last = static_cast<int64_t>(c.q0) + c.n;
+      int places = 0;
+      if (c.n > 0 && c.b >= 0 && static_cast<int64_t>(c.b) + c.n <= p.num_tokens && c.q0 >= 0 && c.n <= p.max_q_len &&
+          last <= table_tokens && last <= p.max_context_len)
+        places = c.places() * p.num_kv_heads;
+      else if (c.n != 0 && blockIdx.x == 0 && p.err)
+        atomicExch(p.err, kDevErrInvalidArg);
+      prefix[s + 1] = places;
+      local += places;
+    }
+    int x = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int run = x - local;
+    for (int w = 0; w < warp; ++w) run += warp_sums[w];
+    if (tid == 0) prefix[0] = 0;
+    for (int s = beg; s < end; ++s) prefix[s + 1] = run += prefix[s + 1];
+    __syncthreads();
+  }
+  const int total = prefix[p.num_seqs];
+  const int share = total / gridDim.x, extra = total - share * gridDim.x;
+  auto cta_begin = [&](int c) { return c * share + min(c, extra); };
+  const int c_begin = cta_begin(blockIdx.x), c_end = cta_begin(blockIdx.x + 1);
 
   if (warp >= 8 && warp < 12) {
     // ======================= restoring, queries =======================
@@ -298,28 +414,39 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       for (int i = 0; i < 4; ++i) x.c[i] = __ldg(c + i);
       x.s = __ldg(reinterpret_cast<const uint2*>(cache + at + bs * 64 + off * 8));
     };
-    auto store = [&](unsigned char* tile, const Row& x) {
+    // a row restored, K to bf16 and V to f16, in 16-byte chunks of 8 dims
+    auto store = [&](unsigned char* tile, const Row& x, auto bf16) {
       unsigned char* row = tile + (r >> 3) * 2048 + sw * 128;
       const uint32_t w[16] = {x.c[0].x, x.c[0].y, x.c[0].z, x.c[0].w, x.c[1].x, x.c[1].y, x.c[1].z, x.c[1].w,
                               x.c[2].x, x.c[2].y, x.c[2].z, x.c[2].w, x.c[3].x, x.c[3].y, x.c[3].z, x.c[3].w};
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {  // scale groups: 16 dims, two 16-byte chunks
+      for (int g = 0; g < 8; ++g) {  // scale groups: 16 dims
         const uint32_t two = fp4::scales_to_f16((g < 4 ? x.s.x : x.s.y) >> (16 * ((g >> 1) & 1)));
         const uint32_t sc = (g & 1) ? __byte_perm(two, 0, 0x3232) : __byte_perm(two, 0, 0x1010);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t h[4];
           fp4::codes_to_f16(w[2 * g + e], h);
-          const int chunk = 2 * g + e;  // of 8 dims
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[k] = fp4::mul_f16x2(h[k], sc);
+            if (decltype(bf16)::value) {  // exact: 6 significant bits, so the fp32 value's low half is zero
+              const float2 f = fp4::f16x2_to_f32(h[k]);
+              h[k] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+            }
+          }
+          const int chunk = 2 * g + e;
           *reinterpret_cast<uint4*>(row + (chunk >> 3) * 1024 + (((chunk & 7) ^ sw) << 4)) =
-              make_uint4(fp4::mul_f16x2(h[0], sc), fp4::mul_f16x2(h[1], sc), fp4::mul_f16x2(h[2], sc),
-                         fp4::mul_f16x2(h[3], sc));
+              make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
     };
-    for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
+    if (warp == 8 && lane == 0) ptx::prefetch_tensormap(&tm_q);
+    for (int pos = c_begin; pos < c_end && !aborted;) {
       Item it;
-      if (!item_at<G>(L, w, it)) continue;
+      item_at<G>(L, prefix, pos, c_end, it);
+      pos = it.end;
+      if (it.t1 <= it.t0) continue;  // its first step is the next CTA's
       const int n = max(it.n[0], it.n[1]);
       const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
       Row kx, vx;
@@ -329,52 +456,24 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         load(kx, p.k_cache, at, it.t0);
         load(vx, p.v_cache, at, it.t0);
       }
-      // the queries of the item: row r of both tiles
-      wait(&bars[kQFree], (ic & 1u) ^ 1u, aborted);
-      aborted = __any_sync(0xffffffffu, aborted);
-      if (aborted) break;
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const int tok = i * TQ + r % TQ;
-        const bool valid = tok < it.ntok;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(p.q) +
-            (static_cast<int64_t>(it.qb + it.tok0 + tok) * p.num_q_heads + it.kvh * G + r / TQ) * 128);
-        uint32_t top = 0;
-        if (valid) {
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 v = __ldg(src + c);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
-          }
-        }
-        // the power of two that takes the row's largest magnitude to [2^14, 2^15);
-        // 1 for a zero, subnormal or non-finite row
-        const int ex = static_cast<int>(top >> 7);
-        const int shift = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 14 - (ex - 127)));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-        // (not zero: a masked -inf times it stays -inf)
-        fac[(ic & 1u) * 256 + i * 128 + r] =
-            fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 1.2e-38f);
-        unsigned char* row = smem + kOffQ + i * kTileBytes + r * 128;
-#pragma unroll 4
-        for (int c = 0; c < 16; ++c) {
-          const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[e] = pack_f16(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
-          *reinterpret_cast<uint4*>(row + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      // the queries of the item, a box for every head and half of the dims;
+      // rows past the chunk are other rows' or zeros, and nobody's
+      if (warp == 8 && lane == 0) {
+        wait(&bars[kQFree], (ic & 1u) ^ 1u, aborted);
+        if (!aborted) {
+          const int tiles = it.ntok > TQ ? 2 : 1;
+          ptx::mbar_arrive_expect_tx(&bars[kQFull], static_cast<uint32_t>(tiles * kTileBytes));
+          for (int i = 0; i < tiles; ++i)
+            for (int g = 0; g < G; ++g)
+              for (int h = 0; h < 2; ++h)
+                ptx::tma_load_2d(smem + kOffQ + i * kTileBytes + h * 16384 + g * TQ * 128, &tm_q,
+                                 (it.kvh * G + g) * 128 + h * 64, it.qb + it.tok0 + i * TQ, &bars[kQFull],
+                                 ptx::policy_evict_first());
         }
       }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
+      aborted = __any_sync(0xffffffffu, aborted);
       ++ic;
-      for (int t = 0; t < n; ++t, ++kc) {
+      for (int t = 0; t < n && !aborted; ++t, ++kc) {
         const int slot = kc & 1u;
         const uint32_t ph = (kc >> 1) & 1u;
         const bool more = t + 1 < n;
@@ -382,7 +481,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         wait(&bars[kKFree + slot], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
-        store(smem + kOffK + slot * kTileBytes, kx);
+        store(smem + kOffK + slot * kTileBytes, kx, std::true_type{});
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kKFull + slot]);
@@ -390,7 +489,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         wait(&bars[kVFree + slot], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
-        store(smem + kOffV + slot * kTileBytes, vx);
+        store(smem + kOffV + slot * kTileBytes, vx, std::false_type{});
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kVFull + slot]);
@@ -405,7 +504,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     // unrolled: a rolled loop of one lane took 130 clocks each.
     const int i = warp - 12;
     const bool leader = elect_one();
-    constexpr uint32_t kIdQK = idesc_f16(0), kIdPV = idesc_f16(1);
+    constexpr uint32_t kIdQK = ptx::idesc_bf16_f32(128, 128, 0, 0), kIdPV = idesc_f16(1);
     const uint64_t desc_q = ptx::smem_desc(smem + kOffQ + i * kTileBytes, 16, 1024, ptx::kLayoutSw128);
     const uint64_t desc_k = ptx::smem_desc(smem + kOffK, 16, 2048, ptx::kLayoutSw128);
     const uint64_t desc_v = ptx::smem_desc(smem + kOffV, 1024, 2048, ptx::kLayoutSw128);
@@ -433,9 +532,11 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       }
     };
     uint32_t turns = 0;
-    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    for (int pos = c_begin; pos < c_end;) {
       Item it;
-      if (!item_at<G>(L, w, it)) continue;
+      item_at<G>(L, prefix, pos, c_end, it);
+      pos = it.end;
+      if (it.t1 <= it.t0) continue;
       const int n = max(it.n[0], it.n[1]), mine = i ? it.n[1] : it.n[0];
       for (int t = -1; t < n; ++t) {
         // P.V of step t (none before the first), Q.K^T of step t + 1; a lane
@@ -494,26 +595,22 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + kColO + i * 128;
     const int g = r / TQ, trow = i * TQ + r % TQ;
-    uint32_t sc = 0, ic = 0;  // steps of the tile, items
-    for (int w = blockIdx.x; w < items && !aborted; w += gridDim.x) {
+    uint32_t sc = 0;  // steps of the tile
+    const float f = fmaxf(p.scale_log2, 1.2e-38f);  // not zero: a masked -inf times it stays -inf
+    for (int pos = c_begin; pos < c_end;) {  // a warp that gave up still meets the others below
       Item it;
-      if (!item_at<G>(L, w, it)) continue;
-      const uint32_t item_no = ic++;
+      item_at<G>(L, prefix, pos, c_end, it);
+      pos = it.end;
+      if (it.t1 <= it.t0) continue;  // its first step is the next CTA's
       const int64_t row = static_cast<int64_t>(it.qb + it.tok0 + trow) * p.num_q_heads + it.kvh * G + g;
       const bool valid = trow < it.ntok;
       const int limit = valid ? it.pos0 + trow + 1 : 0;  // keys that this row sees
-      float m = -CUDART_INF_F, l = 0.f, f = 0.f;
-      for (int t = 0; t < it.n[i]; ++t, ++sc) {
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int t = 0; t < it.n[i] && !aborted; ++t, ++sc) {
         wait(&bars[kSFull + i], sc & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
         ptx::tc_fence_after();
-        if (t == 0) {
-          wait(&bars[kQFull], item_no & 1u, aborted);  // long complete: orders the factor's read
-          aborted = __any_sync(0xffffffffu, aborted);
-          if (aborted) break;
-          f = fac[(item_no & 1u) * 256 + i * 128 + r];
-        }
         const int nvis = limit - (it.t0 + t) * 128;
         // The probabilities are formed on the reference as it is; a row whose
         // maximum turns out to pass it by more than 2^8 raises it, and the step
@@ -561,14 +658,14 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kPFull + i]);
       }
-      if (aborted) break;
-      const int64_t prow =
-          ((static_cast<int64_t>(it.part) * p.num_seqs + it.seq) * p.max_q_len + it.tok0 + trow) * p.num_q_heads +
-          it.kvh * G + g;
-      if (it.n[i] > 0) {
+      // a part's place; its row: token of the pair, then head
+      auto part_of = [&](int c) { return (c * 2 + (cta_begin(c) >= it.start ? 0 : 1)) * L.rows + trow * G + g; };
+      const int64_t prow = part_of(blockIdx.x);
+      if (it.n[i] > 0 && !aborted) {
         wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted) break;
+      }
+      if (it.n[i] > 0 && !aborted) {
         ptx::tc_fence_after();
         const float inv = l != 0.f ? p.v_scale / l : 0.f;
 #pragma unroll 1
@@ -582,35 +679,66 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(&bars[kOFree + i]);
           }
           if (!valid) continue;
-          if (L.parts > 1) {
+          if (it.whole) {
+            store_out(p, row * 128 + c * 32, v, inv);
+          } else {
             float4* dst = reinterpret_cast<float4*>(L.o + prow * 128 + c * 32);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
                                    __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-          } else if (p.out_bf16) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * 128 + c * 32);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * e]) * inv,
-                                                               __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
-                h[e] = *reinterpret_cast<const uint32_t*>(&x);
-              }
-              dst[q] = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          } else {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * 128 + c * 32);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
-                                   __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
           }
         }
       }
-      if (L.parts > 1 && valid) *reinterpret_cast<float2*>(L.ml + prow * 2) = make_float2(m, l);
+      if (!it.whole) {
+        // the last CTA of the item adds its parts up
+        if (valid && !aborted) *reinterpret_cast<float2*>(L.ml + prow * 2) = make_float2(m, l);
+        auto cta_of = [&](int u) {
+          const int wide = extra * (share + 1);
+          return u < wide ? u / (share + 1) : extra + (u - wide) / share;
+        };
+        const int c0 = cta_of(it.start + kLead), c1 = cta_of(it.end - 1);
+        __threadfence();
+        ptx::bar_sync(3, 256);
+        if (tid == 0) {
+          int32_t* counter = L.counters + c0;
+          const int before = atomicAdd(counter, 1);
+          last_flag = before == c1 - c0;
+          if (before == c1 - c0) *counter = 0;
+          __threadfence();
+        }
+        ptx::bar_sync(3, 256);
+        if (last_flag && valid) {
+          float M = -CUDART_INF_F;
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(L.ml + static_cast<int64_t>(part_of(c)) * 2));
+          const float ref = M == -CUDART_INF_F ? 0.f : M;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float acc[32], sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+#pragma unroll 1
+            for (int c = c0; c <= c1; ++c) {
+              const int64_t at = part_of(c);
+              const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + at * 2));
+              if (e.y == 0.f) continue;  // a part that this row sees nothing of: its O may not be written
+              const float f2 = fast_exp2(e.x - ref);
+              sum = fmaf(f2, e.y, sum);
+              const float4* src = reinterpret_cast<const float4*>(L.o + at * 128 + q * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 x = __ldcg(src + j);
+                acc[4 * j] = fmaf(f2, x.x, acc[4 * j]);
+                acc[4 * j + 1] = fmaf(f2, x.y, acc[4 * j + 1]);
+                acc[4 * j + 2] = fmaf(f2, x.z, acc[4 * j + 2]);
+                acc[4 * j + 3] = fmaf(f2, x.w, acc[4 * j + 3]);
+              }
+            }
+            store_out(p, row * 128 + q * 32, reinterpret_cast<uint32_t(&)[32]>(acc), sum != 0.f ? p.v_scale / sum : 0.f);
+          }
+        }
+        ptx::bar_sync(3, 256);  // the flag is free again
+      }
     }
   }
 
@@ -622,57 +750,11 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
   if (tid == 0 && *gave_up && p.err) atomicExch(p.err, kDevErrTimeout);
 }
 
-// The parts of every (token, head) of a chunk added up, in order; a warp a row.
-__global__ void __launch_bounds__(256) fp4_prefill_merge_kernel(const __grid_constant__ fp4_prefill_detail::Launch L) {
-  using namespace fp4_prefill_detail;
-  const Fp4AttnParams& p = L.p;
-  ptx::griddep_wait();
-  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_q_heads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int lane = threadIdx.x & 31;
-  // rows of no chunk, or of a chunk that was refused, are left as they were
-  const int tok = static_cast<int>(row / p.num_q_heads);
-  int lo = 0, hi = p.num_seqs - 1;
-  while (lo < hi) {  // the last sequence that starts at or before the token
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.cu_q[mid] <= tok) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = p.cu_q[lo], n = p.cu_q[lo + 1] - b, q0 = p.q_start[lo];
-  const int64_t last = static_cast<int64_t>(q0) + n;
-  if (b < 0 || tok < b || tok >= b + n || static_cast<int64_t>(b) + n > p.num_tokens || q0 < 0 || n > p.max_q_len ||
-      last > (static_cast<int64_t>(p.max_blocks_per_seq) << L.bs_log) || last > p.max_context_len)
-    return;
-  const int64_t prows = static_cast<int64_t>(p.num_seqs) * p.max_q_len * p.num_q_heads;
-  const int64_t prow = (static_cast<int64_t>(lo) * p.max_q_len + tok - b) * p.num_q_heads + row % p.num_q_heads;
-  float M = -CUDART_INF_F;
-  for (int k = 0; k < L.parts; ++k) M = fmaxf(M, L.ml[(k * prows + prow) * 2]);
-  const float ref = M == -CUDART_INF_F ? 0.f : M;
-  float l = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < L.parts; ++k) {
-    const float2 ml = *reinterpret_cast<const float2*>(L.ml + (k * prows + prow) * 2);
-    if (ml.y == 0.f) continue;  // a part that this row sees nothing of: its O is not written
-    const float4 v = *reinterpret_cast<const float4*>(L.o + (k * prows + prow) * 128 + lane * 4);
-    const float f = fast_exp2(ml.x - ref);
-    l = fmaf(f, ml.y, l);
-    a.x = fmaf(f, v.x, a.x);
-    a.y = fmaf(f, v.y, a.y);
-    a.z = fmaf(f, v.z, a.z);
-    a.w = fmaf(f, v.w, a.w);
-  }
-  const float inv = l != 0.f ? p.v_scale / l : 0.f;
-  const int64_t at = row * 128 + lane * 4;
-  if (p.out_bf16) {
-    __nv_bfloat162 r[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv), __floats2bfloat162_rn(a.z * inv, a.w * inv)};
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) = *reinterpret_cast<const uint2*>(r);
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-  }
-}
+}  // namespace pa
 
+extern "C" bool encode_q_tokens(CUtensorMap* m, const void* base, uint64_t tokens, uint64_t row_elems, uint32_t box_rows);
+
+namespace pa {
 namespace {
 
 const void* kernel_for(int group) {
@@ -685,67 +767,74 @@ const void* kernel_for(int group) {
   }
 }
 
-// Parts of the keys: with fewer tile pairs than three for every SM, enough
-// parts to come near that, of four tiles of keys or more.
-int parts_for(int64_t pairs, int max_context_len) {
-  const int64_t want = 3 * device_sm_count() / (pairs > 0 ? pairs : 1);
-  const int64_t most = (static_cast<int64_t>(max_context_len) + 511) / 512;
-  const int64_t n = want < most ? want : most;
-  return static_cast<int>(n < 1 ? 1 : (n > 64 ? 64 : n));
-}
-int64_t pairs_of(int num_seqs, int num_q_heads, int num_kv_heads, int max_q_len, int* per_chunk) {
-  const int tq2 = 256 / (num_q_heads / num_kv_heads);
-  *per_chunk = (max_q_len + tq2 - 1) / tq2;
-  return static_cast<int64_t>(num_seqs) * num_kv_heads * *per_chunk;
+int pairs_of(int group, int max_q_len) { return (max_q_len + 256 / group - 1) / (256 / group); }
+int rows_of(int group, int max_q_len) { return max_q_len * group < 256 ? max_q_len * group : 256; }
+
+// Sequences of one launch: their places fit an int.  0: not even one's do.
+int seqs_of(int num_seqs, int num_kv_heads, int group, int max_q_len, int max_context_len) {
+  using namespace fp4_prefill_detail;
+  const int64_t places = (kLead + (static_cast<int64_t>(max_context_len) + 127) / 128) * pairs_of(group, max_q_len) *
+                         num_kv_heads;
+  const int64_t fit = ((int64_t(1) << 31) - 1) / (places > 0 ? places : 1);
+  const int64_t most = fit < kMaxSeqs ? fit : kMaxSeqs;
+  return static_cast<int>(num_seqs < most ? num_seqs : most);
 }
 
 }  // namespace
 
 size_t fp4_prefill_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int max_q_len, int max_context_len) {
-  int per_chunk = 0;
-  const int parts = parts_for(pairs_of(num_seqs, num_q_heads, num_kv_heads, max_q_len, &per_chunk), max_context_len);
-  if (parts == 1) return 256;
-  const int64_t rows = static_cast<int64_t>(num_seqs) * max_q_len * num_q_heads;
-  return static_cast<size_t>(256 + parts * rows * (128 + 2) * 4 + 256);
+  const int G = num_q_heads / num_kv_heads;
+  const int seqs = seqs_of(num_seqs, num_kv_heads, G, max_q_len, max_context_len);
+  if (num_seqs > 0 && max_q_len > 0 && seqs == 0) return 0;
+  // header | counters | parts: the first two lie where they lie for every shape
+  return static_cast<size_t>(256 + fp4_counter_bytes() + 2 * device_sm_count() * rows_of(G, max_q_len) * (128 + 2) * 4);
 }
 
 cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
   using namespace fp4_prefill_detail;
-  Launch L{};
-  L.p = p;
-  const int64_t pairs = pairs_of(p.num_seqs, p.num_q_heads, p.num_kv_heads, p.max_q_len, &L.pairs);
-  L.parts = parts_for(pairs, p.max_context_len);
-  L.tile_bytes = static_cast<uint32_t>(fp4_tile_bytes(p.block_size, 128));
-  L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
-  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_q_heads;
-  if (L.parts > 1) {
-    L.o = reinterpret_cast<float*>(p.ws + 256);
-    L.ml = L.o + static_cast<int64_t>(L.parts) * p.num_seqs * p.max_q_len * p.num_q_heads * 128;
-  }
-  const void* fn = kernel_for(p.num_q_heads / p.num_kv_heads);
-  int per_sm = 0;
-  cudaError_t e = fp4_occupancy(fn, kThreads, kSmemBytes, &per_sm);
-  if (e != cudaSuccess) return e;
-  const int64_t items = pairs * L.parts;
-  if (items >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  const int G = p.num_q_heads / p.num_kv_heads;
+  const int seqs = seqs_of(p.num_seqs, p.num_kv_heads, G, p.max_q_len, p.max_context_len);
   const int64_t sms = device_sm_count();
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? items : sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {&L};
-  e = cudaLaunchKernelExC(&cfg, fn, args);
-  if (e != cudaSuccess || L.parts == 1) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&fp4_prefill_merge_kernel), args);
+  CUtensorMap tm_q;
+  if (!encode_q_tokens(&tm_q, p.q, static_cast<uint64_t>(p.num_tokens), static_cast<uint64_t>(p.num_q_heads) * 128,
+                       static_cast<uint32_t>(128 / G)))
+    return cudaErrorInvalidValue;
+  for (int seq0 = 0; seq0 < p.num_seqs; seq0 += seqs) {
+    Launch L{};
+    L.p = p;
+    L.p.num_seqs = p.num_seqs - seq0 < seqs ? p.num_seqs - seq0 : seqs;
+    L.p.cu_q += seq0;
+    L.p.q_start += seq0;
+    L.p.block_tables += static_cast<int64_t>(seq0) * p.max_blocks_per_seq;
+    L.rows = rows_of(G, p.max_q_len);
+    L.tile_bytes = static_cast<uint32_t>(fp4_tile_bytes(p.block_size, 128));
+    L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
+    L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
+    L.o = reinterpret_cast<float*>(p.ws + 256 + fp4_counter_bytes());
+    L.ml = L.o + 2 * sms * L.rows * 128;
+    const void* fn = kernel_for(G);
+    const int smem = kSmemBytes + (L.p.num_seqs + 1) * 4;
+    int per_sm = 0;
+    cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    // every SM, while an item is not cut into too many parts to add up
+    const int64_t items = static_cast<int64_t>(L.p.num_seqs) * pairs_of(G, p.max_q_len) * p.num_kv_heads;
+    const int64_t ctas = items * kMostParts < sms ? items * kMostParts : sms;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&L, &tm_q};
+    e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pa
