@@ -423,7 +423,8 @@ pa_status pa_prefill(void* out, pa_dtype out_dtype, const void* q, int32_t num_t
 size_t pa_fp4_tile_bytes(int32_t block_size, int32_t head_dim);
 
 /* pa_reshape_and_cache into a 4-bit cache: key and value are
- * [num_tokens][num_kv_heads][head_dim] of src_dtype (F32 or BF16).  status
+ * [num_tokens][num_kv_heads][head_dim] of src_dtype (F32 or BF16), 32-byte
+ * aligned (PA_ERR_INVALID_ARG otherwise; also in the gather).  status
  * (device int32, caller-zeroed, or NULL) receives PA_ERR_INVALID_ARG if a
  * slot lies past the pool; such a token is not written, negative slots are
  * padding. */
@@ -467,7 +468,7 @@ pa_status pa_decode_fp4(void* out, pa_dtype out_dtype,
 
 /* pa_prefill over a 4-bit cache (head_dim 128, any block size): causal
  * attention of each sequence's chunk of bf16 queries, rounded as in
- * pa_decode_fp4.  max_context_len: host, >= every q_start[i] + chunk length
+ * pa_decode_fp4; out is 32-byte aligned.  max_context_len: host, >= every q_start[i] + chunk length
  * (a longer one is reported in *status and its rows are not written).  The
  * workspace (256-byte aligned, zero-filled before its first use) holds the
  * partial results of a long history that is split over CTAs; calls that

@@ -36,7 +36,7 @@ pa_status check_rows(const void* key, const void* value, pa_dtype dtype, int32_t
     return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
   if (!key || !value || !slot_mapping || !k_cache || !v_cache) return PA_ERR_INVALID_ARG;
-  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+  if (!aligned(key, 32) || !aligned(value, 32) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(slot_mapping, 8) || !aligned(status, 4))
     return PA_ERR_INVALID_ARG;
   return PA_OK;
@@ -160,7 +160,7 @@ pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t n
   if (head_dim != 128 || !group_ok(num_q_heads, num_kv_heads)) return PA_ERR_UNSUPPORTED;
   if (num_tokens == 0 || num_seqs == 0 || max_q_len == 0) return PA_OK;
   if (!out || !q || !cu_q || !q_start || !k_cache || !v_cache || !block_tables) return PA_ERR_INVALID_ARG;
-  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(cu_q, 4) ||
+  if (!aligned(out, 32) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(cu_q, 4) ||
       !aligned(q_start, 4) || !aligned(block_tables, 4) || !aligned(status, 4))
     return PA_ERR_INVALID_ARG;
   const size_t need = pa_prefill_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,

@@ -83,16 +83,6 @@ struct Launch {
   float* o;             // [2 * CTAs][rows][128]
 };
 
-struct Item {
-  int seq, pair, kvh, tok0, qb, pos0;  // first token: in the chunk, in q; position of tok0
-  int ntok;                            // tokens of the pair's two tiles
-  int start, end;                      // places: kLead, then the steps
-  int t0, t1;                          // this CTA's steps
-  int kend;                            // keys that the last token sees
-  int n[2];                            // this CTA's steps of each tile
-  bool whole;                          // all steps are this CTA's
-};
-
 // A sequence's items, pair after pair with the kv heads inside.  Pair j has
 // kLead + ceil((q0 + tokens up to its end) / 128) places for each head.
 template <int G>
@@ -129,46 +119,76 @@ __device__ __forceinline__ Chunk<G> chunk_of(const Launch& L, int seq) {
   return c;
 }
 
-// The item at place `pos` of the launch, and what of it lies before `c_end`.
+// An item and this CTA's part of it.
 template <int G>
-__device__ __forceinline__ void item_at(const Launch& L, const int* prefix, int pos, int c_end, Item& it) {
-  constexpr int TQ = 128 / G;
-  const int hkv = L.p.num_kv_heads;
-  int lo = 0, hi = L.p.num_seqs - 1;
-  while (lo < hi) {  // the last sequence that starts at or before pos (none of no places after it)
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= pos) lo = mid;
-    else hi = mid - 1;
+struct Item {
+  static constexpr int TQ = 128 / G;
+  Chunk<G> c;
+  int seq, pair, kvh;
+  int start, end;  // places: kLead, then the steps
+  // derived: first token in the chunk; position of tok0; tokens of the two tiles
+  int tok0, pos0, ntok;
+  int t0, t1;      // this CTA's steps
+  int n0, n1;      // this CTA's steps of each tile
+  bool whole;      // all steps are this CTA's
+  __device__ __forceinline__ int kend() const { return pos0 + ntok; }  // keys that the last token sees
+  __device__ __forceinline__ int steps_of(int tile) const { return tile ? n1 : n0; }
+
+  __device__ __forceinline__ void derive(int c_begin, int c_end) {
+    const int tiles = c.tiles(pair);
+    end = start + kLead + tiles;
+    tok0 = pair * 2 * TQ;
+    ntok = min(2 * TQ, c.n - tok0);
+    pos0 = c.q0 + tok0;
+    const int first = start + kLead;
+    t0 = max(c_begin, first) - first;
+    t1 = min(c_end, end) - first;
+    whole = t0 == 0 && t1 == tiles;
+    // the first tile's last token may see fewer keys than the second's
+    const int seen0 = (pos0 + min(TQ, ntok) + 127) / 128;
+    n0 = max(0, min(t1, seen0) - t0);
+    n1 = ntok > TQ ? max(0, t1 - t0) : 0;
   }
-  it.seq = lo;
-  const Chunk<G> c = chunk_of<G>(L, lo);
-  int r = pos - prefix[lo];
-  int a = 0, b = c.pairs() - 1;
-  while (a < b) {
-    const int mid = (a + b + 1) >> 1;
-    if (hkv * c.before(mid) <= r) a = mid;
-    else b = mid - 1;
+  // the item at place c_begin
+  __device__ __forceinline__ void find(const Launch& L, const int* prefix, int c_begin, int c_end) {
+    const int hkv = L.p.num_kv_heads;
+    int lo = 0, hi = L.p.num_seqs - 1;
+    while (lo < hi) {  // the last sequence that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= c_begin) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo;
+    c = chunk_of<G>(L, lo);
+    int r = c_begin - prefix[lo];
+    int a = 0, b = c.pairs() - 1;
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (hkv * c.before(mid) <= r) a = mid;
+      else b = mid - 1;
+    }
+    pair = a;
+    r -= hkv * c.before(a);
+    const int places = kLead + c.tiles(a);
+    kvh = r / places;
+    start = c_begin - (r - kvh * places);
+    derive(c_begin, c_end);
   }
-  it.pair = a;
-  r -= hkv * c.before(a);
-  const int tiles = c.tiles(a), places = kLead + tiles;
-  it.kvh = r / places;
-  it.start = pos - (r - it.kvh * places);
-  it.end = it.start + places;
-  it.tok0 = a * 2 * TQ;
-  it.qb = c.b;
-  it.ntok = min(2 * TQ, c.n - it.tok0);
-  it.pos0 = c.q0 + it.tok0;
-  it.kend = it.pos0 + it.ntok;
-  const int first = it.start + kLead;
-  it.t0 = max(pos, first) - first;
-  it.t1 = min(c_end, it.end) - first;
-  it.whole = it.t0 == 0 && it.t1 == tiles;
-  // the first tile's last token may see fewer keys than the second's
-  const int seen0 = (it.pos0 + min(TQ, it.ntok) + 127) / 128;
-  it.n[0] = max(0, min(it.t1, seen0) - it.t0);
-  it.n[1] = it.ntok > TQ ? max(0, it.t1 - it.t0) : 0;
-}
+  // the next one (there is one before c_end)
+  __device__ __forceinline__ void next(const Launch& L, const int* prefix, int c_begin, int c_end) {
+    start = end;
+    if (++kvh == L.p.num_kv_heads) {
+      kvh = 0;
+      if (++pair * 2 * TQ >= c.n) {
+        pair = 0;
+        do ++seq;
+        while (prefix[seq + 1] == start);  // sequences without places
+        c = chunk_of<G>(L, seq);
+      }
+    }
+    derive(c_begin, c_end);
+  }
+};
 
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
   if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
@@ -253,16 +273,25 @@ __device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, 
 // the largest of a row's first nvis scores of a step
 __device__ __forceinline__ float row_max(uint32_t s_at, int nvis) {
   float m0 = -CUDART_INF_F, m1 = m0;
+  const bool all = __all_sync(0xffffffffu, nvis >= 128);
 #pragma unroll 1
-  for (int c = 0; c < 8; ++c) {
-    uint32_t v[16];
-    ptx::TmemLd<16>::run(s_at + c * 16, v);
-    wait_ld16(v);
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t v[2][16];
+    ptx::TmemLd<16>::run(s_at + c, v[0]);
+    ptx::TmemLd<16>::run(s_at + c + 16, v[1]);
+    wait_ld16(v[0]);
+    wait_ld16(v[1]);
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      if (c * 16 + j < nvis) m0 = fmaxf(m0, __uint_as_float(v[j]));
-      if (c * 16 + j + 1 < nvis) m1 = fmaxf(m1, __uint_as_float(v[j + 1]));
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = all || c + h * 16 + j + e < nvis ? __uint_as_float(v[h][j + e]) : -CUDART_INF_F;
+        m0 = max3(m0, x[0], x[1]);
+        m1 = max3(m1, x[2], x[3]);
+      }
   }
   return fmaxf(m0, m1);
 }
@@ -276,27 +305,33 @@ struct Row {
 }  // namespace fp4_prefill_detail
 
 namespace fp4_prefill_detail {
-// 32 outputs of a row, times inv
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// 32 outputs of a row, times inv, in whole 32-byte sectors
 __device__ __forceinline__ void store_out(const Fp4AttnParams& p, int64_t at, const uint32_t (&v)[32], float inv) {
   if (p.out_bf16) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t h[4];
+    for (int q = 0; q < 2; ++q) {
+      uint32_t h[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * q + 2 * e]) * inv,
-                                                       __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+      for (int e = 0; e < 8; ++e) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[16 * q + 2 * e]) * inv,
+                                                       __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
         h[e] = *reinterpret_cast<const uint32_t*>(&x);
       }
-      dst[q] = make_uint4(h[0], h[1], h[2], h[3]);
+      store32(static_cast<__nv_bfloat16*>(p.out) + at + 16 * q, h);
     }
   } else {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
-                           __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(__uint_as_float(v[8 * q + e]) * inv);
+      store32(static_cast<float*>(p.out) + at + 8 * q, h);
+    }
   }
 }
 }  // namespace fp4_prefill_detail
@@ -389,9 +424,9 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     const int bs = 1 << L.bs_log;
     const uint32_t sw = r & 7;
     uint32_t ic = 0, kc = 0;
-    auto locate = [&](const Item& it, const int32_t* table, int t) -> int64_t {
+    auto locate = [&](const Item<G>& it, const int32_t* table, int t) -> int64_t {
       const int key = t * 128 + r;
-      if (key >= it.kend) return -1;
+      if (key >= it.kend()) return -1;
       const int lb = key >> L.bs_log;
       int phys = __ldg(table + lb);
       if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
@@ -442,12 +477,14 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       }
     };
     if (warp == 8 && lane == 0) ptx::prefetch_tensormap(&tm_q);
-    for (int pos = c_begin; pos < c_end && !aborted;) {
-      Item it;
-      item_at<G>(L, prefix, pos, c_end, it);
-      pos = it.end;
+    Item<G> it;
+    it.end = c_begin;
+    for (bool more = c_begin < c_end; more && !aborted;) {
+      if (it.end == c_begin) it.find(L, prefix, c_begin, c_end);
+      else it.next(L, prefix, c_begin, c_end);
+      more = it.end < c_end;
       if (it.t1 <= it.t0) continue;  // its first step is the next CTA's
-      const int n = max(it.n[0], it.n[1]);
+      const int n = max(it.n0, it.n1);
       const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
       Row kx, vx;
       int64_t at = -1;
@@ -467,7 +504,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
             for (int g = 0; g < G; ++g)
               for (int h = 0; h < 2; ++h)
                 ptx::tma_load_2d(smem + kOffQ + i * kTileBytes + h * 16384 + g * TQ * 128, &tm_q,
-                                 (it.kvh * G + g) * 128 + h * 64, it.qb + it.tok0 + i * TQ, &bars[kQFull],
+                                 (it.kvh * G + g) * 128 + h * 64, it.c.b + it.tok0 + i * TQ, &bars[kQFull],
                                  ptx::policy_evict_first());
         }
       }
@@ -532,12 +569,14 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       }
     };
     uint32_t turns = 0;
-    for (int pos = c_begin; pos < c_end;) {
-      Item it;
-      item_at<G>(L, prefix, pos, c_end, it);
-      pos = it.end;
+    Item<G> it;
+    it.end = c_begin;
+    for (bool more = c_begin < c_end; more;) {
+      if (it.end == c_begin) it.find(L, prefix, c_begin, c_end);
+      else it.next(L, prefix, c_begin, c_end);
+      more = it.end < c_end;
       if (it.t1 <= it.t0) continue;
-      const int n = max(it.n[0], it.n[1]), mine = i ? it.n[1] : it.n[0];
+      const int n = max(it.n0, it.n1), mine = it.steps_of(i);
       for (int t = -1; t < n; ++t) {
         // P.V of step t (none before the first), Q.K^T of step t + 1; a lane
         // polls each of the barriers that this needs
@@ -597,16 +636,19 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     const int g = r / TQ, trow = i * TQ + r % TQ;
     uint32_t sc = 0;  // steps of the tile
     const float f = fmaxf(p.scale_log2, 1.2e-38f);  // not zero: a masked -inf times it stays -inf
-    for (int pos = c_begin; pos < c_end;) {  // a warp that gave up still meets the others below
-      Item it;
-      item_at<G>(L, prefix, pos, c_end, it);
-      pos = it.end;
+    Item<G> it;
+    it.end = c_begin;
+    for (bool more = c_begin < c_end; more;) {  // a warp that gave up still meets the others below
+      if (it.end == c_begin) it.find(L, prefix, c_begin, c_end);
+      else it.next(L, prefix, c_begin, c_end);
+      more = it.end < c_end;
       if (it.t1 <= it.t0) continue;  // its first step is the next CTA's
-      const int64_t row = static_cast<int64_t>(it.qb + it.tok0 + trow) * p.num_q_heads + it.kvh * G + g;
+      const int64_t row = static_cast<int64_t>(it.c.b + it.tok0 + trow) * p.num_q_heads + it.kvh * G + g;
       const bool valid = trow < it.ntok;
+      const int steps = it.steps_of(i);
       const int limit = valid ? it.pos0 + trow + 1 : 0;  // keys that this row sees
       float m = -CUDART_INF_F, l = 0.f;
-      for (int t = 0; t < it.n[i] && !aborted; ++t, ++sc) {
+      for (int t = 0; t < steps && !aborted; ++t, ++sc) {
         wait(&bars[kSFull + i], sc & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
@@ -661,11 +703,11 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       // a part's place; its row: token of the pair, then head
       auto part_of = [&](int c) { return (c * 2 + (cta_begin(c) >= it.start ? 0 : 1)) * L.rows + trow * G + g; };
       const int64_t prow = part_of(blockIdx.x);
-      if (it.n[i] > 0 && !aborted) {
+      if (steps > 0 && !aborted) {
         wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
       }
-      if (it.n[i] > 0 && !aborted) {
+      if (steps > 0 && !aborted) {
         ptx::tc_fence_after();
         const float inv = l != 0.f ? p.v_scale / l : 0.f;
 #pragma unroll 1

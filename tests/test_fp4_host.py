@@ -71,7 +71,7 @@ def test_append_and_gather_refusals(lib):
         for s in (0.0, -1.0, 3.0, 0.1, float("inf"), float("nan"), 2.0 ** 33, 2.0 ** -33):
             assert call(ks=s) == BAD and call(vs=s) == BAD
         assert call(key=None) == BAD and call(slots=None) == BAD and call(kc=None) == BAD
-        assert call(key=P + 8) == BAD and call(kc=P + 4) == BAD and call(slots=P + 4) == BAD and call(status=P + 2) == BAD
+        assert call(key=P + 16) == BAD and call(kc=P + 4) == BAD and call(slots=P + 4) == BAD and call(status=P + 2) == BAD
         assert call(t=0, key=None, slots=None, kc=None) == L.PA_OK
 
 
@@ -104,6 +104,7 @@ def test_prefill_refusals(lib):
     assert call(ks=5.0) == BAD and call(vs=-2.0) == BAD and call(h=7) == BAD
     for name in ("out", "q", "cu", "qs", "kc", "tab"):
         assert call(**{name: None}) == BAD
+    assert call(out=P + 16) == BAD and call(q=P + 8) == BAD and call(status=P + 2) == BAD
     assert call(ws=None) == WS and call(wb=8) == WS and call(ws=P + 8) == WS
     assert call(t=0, q=None, ws=None) == L.PA_OK and call(mq=0, q=None) == L.PA_OK
     assert lib.pa_prefill_fp4_workspace_size(2, 8, 2, 64, 16, 5, 64) == 0
