@@ -497,7 +497,7 @@ pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t n
  * sequence ascend strictly and keep[cu_keep[i] + j] >= dst_start[i] + j
  * (positions before dst_start[i] stay).  Nothing behind the last kept token
  * is written.
- *   dtype              F32, BF16 (rows of at most 16384 bytes) or FP4; layers
+ *   dtype              F32, BF16 (rows of at most 8192 bytes) or FP4; layers
  *                      as in pa_copy_blocks_layers (FP4: cache_layer_stride
  *                      counts bytes)
  *   block_tables       device, int32 [num_seqs][max_blocks_per_seq]

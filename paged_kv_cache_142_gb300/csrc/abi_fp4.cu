@@ -205,7 +205,7 @@ pa_status pa_compact_tokens(void* k_cache, void* v_cache, int64_t cache_layer_st
     return PA_ERR_UNSUPPORTED;
   const int64_t e = dtype == PA_DTYPE_F32 ? 4 : (dtype == PA_DTYPE_BF16 ? 2 : 1);
   const int64_t row = dtype == PA_DTYPE_FP4 ? head_dim / 2 : head_dim * e;
-  if (dtype != PA_DTYPE_FP4 && (row % 16 != 0 || row > 16384)) return PA_ERR_UNSUPPORTED;
+  if (dtype != PA_DTYPE_FP4 && (row % 16 != 0 || row > 8192)) return PA_ERR_UNSUPPORTED;
   const int64_t tile = dtype == PA_DTYPE_FP4 ? pa::fp4_tile_bytes(block_size, head_dim) : row * block_size;
   const int64_t layer = tile * num_kv_heads * num_blocks;
   if (num_seqs < 0 || max_keep < 0 || max_blocks_per_seq <= 0 || num_layers < 1 || num_layers > 32767)

@@ -2,19 +2,19 @@
 // kept tokens behind position dst_start move to the front, in order:
 //   position dst_start + j  :=  position keep[j],   keep[j] >= dst_start + j.
 //
-// One CTA owns the rows of one (sequence, head group, layer, K or V), so no
-// other CTA reads or writes them.  It walks the kept tokens in chunks: all of
-// a chunk's rows are read into registers, the CTA synchronises, then they are
-// written.  keep ascends, so every later source lies at or behind its own
-// destination and so behind every destination written so far: nothing is
-// overwritten before it is read, and the next chunk may be read before this
-// one is written.
+// One CTA owns the rows of one (sequence, head group) in a few planes (a plane:
+// the K or V cache of a layer), so no other CTA reads or writes them.  It walks
+// the kept tokens in chunks, and a chunk plane by plane: all of its rows are
+// read into registers, the CTA synchronises, then they are written.  keep
+// ascends, so every later source lies at or behind its own destination and so
+// behind every destination written so far: nothing is overwritten before it is
+// read, and the next chunk, or plane, may be read before this one is written.
 //
 // What bounds it is the chain keep -> block table -> row, three dependent
-// loads a chunk, far more than the bytes: so a chunk is as long as the CTA's
-// registers allow (four pieces a thread; 1024 threads for long lists), the
-// positions and table entries of the next chunk load during this one, and few
-// kept tokens (accepted drafts) take all heads in one CTA.
+// loads a chunk, more than the bytes: so a chunk is as long as the CTA's
+// registers allow (four pieces a thread, 512 threads for long lists), its
+// places serve several planes, the next plane's rows load before this one's
+// are written, and few kept tokens (accepted drafts) take all heads in one CTA.
 #include "decode.cuh"
 #include "fp4.cuh"
 
@@ -22,7 +22,7 @@ namespace pa {
 namespace {
 
 constexpr int kUnroll = 4;       // pieces a thread holds
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 
 struct Piece {
   uint32_t w[4];
@@ -44,11 +44,16 @@ __device__ __forceinline__ void store_piece(const Piece& v, unsigned char* p, in
   else *reinterpret_cast<uint32_t*>(p) = v.w[0];
 }
 
-__global__ void __launch_bounds__(kMaxThreads)
-    compact_kernel(const CompactParams p, int heads_per_cta, int units) {
+// MANY: several planes, each loaded while the one before is written; else one,
+// with the next chunk's places found meanwhile.
+template <bool MANY>
+__global__ void __launch_bounds__(kMaxThreads, 2)
+    compact_kernel(const CompactParams p, int heads_per_cta, int units, int planes) {
   const int seq = blockIdx.x;
-  const int64_t layer = blockIdx.z >> 1;
-  unsigned char* cache = ((blockIdx.z & 1) ? p.v_cache : p.k_cache) + layer * p.layer_bytes;
+  const int plane0 = blockIdx.z * planes, plane1 = min(2 * p.num_layers, plane0 + planes);
+  auto cache_of = [&](int plane) {
+    return ((plane & 1) ? p.v_cache : p.k_cache) + (plane >> 1) * p.layer_bytes;
+  };
   const int b = p.cu_keep[seq], n = p.cu_keep[seq + 1] - b;
   const int dst0 = p.dst_start[seq];
   const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
@@ -98,23 +103,45 @@ __global__ void __launch_bounds__(kMaxThreads)
       dst[e] = db * block_bytes + first + static_cast<int64_t>(dp & bs_mask) * stride;
     }
   };
-  locate(0);
-  for (int j0 = 0; j0 < n; j0 += chunk) {
-    Piece v[kUnroll];
-    int64_t to[kUnroll];
-#pragma unroll
-    for (int e = 0; e < kUnroll; ++e) {
-      to[e] = -1;
-      if (src[e] >= 0) {
-        load_piece(v[e], cache + src[e], bytes);
-        to[e] = dst[e];
-      }
-    }
-    if (j0 + chunk < n) locate(j0 + chunk);
-    __syncthreads();
+  auto load = [&](Piece (&x)[kUnroll], const unsigned char* cache) {
 #pragma unroll
     for (int e = 0; e < kUnroll; ++e)
-      if (to[e] >= 0) store_piece(v[e], cache + to[e], bytes);
+      if (src[e] >= 0) load_piece(x[e], cache + src[e], bytes);
+  };
+  if (MANY) {
+    Piece v[2][kUnroll];
+    auto store = [&](const Piece (&x)[kUnroll], unsigned char* cache) {
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e)
+        if (src[e] >= 0) store_piece(x[e], cache + dst[e], bytes);
+    };
+    for (int j0 = 0; j0 < n; j0 += chunk) {
+      locate(j0);
+      load(v[0], cache_of(plane0));
+      for (int plane = plane0; plane < plane1; plane += 2) {
+        if (plane + 1 < plane1) load(v[1], cache_of(plane + 1));
+        __syncthreads();
+        store(v[0], cache_of(plane));
+        if (plane + 2 < plane1) load(v[0], cache_of(plane + 2));
+        __syncthreads();
+        if (plane + 1 < plane1) store(v[1], cache_of(plane + 1));
+      }
+    }
+  } else {
+    unsigned char* cache = cache_of(plane0);
+    locate(0);
+    for (int j0 = 0; j0 < n; j0 += chunk) {
+      Piece v[kUnroll];
+      int64_t to[kUnroll];
+      load(v, cache);
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) to[e] = src[e] >= 0 ? dst[e] : -1;
+      if (j0 + chunk < n) locate(j0 + chunk);
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e)
+        if (to[e] >= 0) store_piece(v[e], cache + to[e], bytes);
+    }
   }
 }
 
@@ -129,9 +156,15 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   int threads = 256;
   while (threads < kMaxThreads && (threads < units || static_cast<int64_t>(p.max_keep) * heads * units > threads * kUnroll))
     threads *= 2;
-  const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>((p.num_kv_heads + heads - 1) / heads),
-                  static_cast<unsigned>(2 * p.num_layers));
-  compact_kernel<<<grid, threads, 0, stream>>>(p, heads, units);
+  const int64_t groups = (p.num_kv_heads + heads - 1) / heads;
+  // as few planes a CTA as let all CTAs run at once (an SM holds 1024 threads of them)
+  const int64_t room = device_sm_count() * (1024 / threads), per_plane = static_cast<int64_t>(p.num_seqs) * groups;
+  int planes = 1;
+  while (planes < 2 * p.num_layers && per_plane * ((2 * p.num_layers + planes - 1) / planes) > room) ++planes;
+  const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(groups),
+                  static_cast<unsigned>((2 * p.num_layers + planes - 1) / planes));
+  if (planes > 1) compact_kernel<true><<<grid, threads, 0, stream>>>(p, heads, units, planes);
+  else compact_kernel<false><<<grid, threads, 0, stream>>>(p, heads, units, 1);
   return cudaGetLastError();
 }
 
