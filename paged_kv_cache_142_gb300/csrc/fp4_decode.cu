@@ -170,20 +170,22 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   float* merge = reinterpret_cast<float*>(smem + L.off_merge);     // [warp][G][D + pad]
   float2* stat = reinterpret_cast<float2*>(smem + L.off_stat);     // [warp][8]: maximum, sum
   __nv_bfloat16* qraw = reinterpret_cast<__nv_bfloat16*>(smem + L.off_qraw);  // [G * D], the next segment's
-  uint4* qf16 = reinterpret_cast<uint4*>(smem + L.off_q);  // [NT][D / 32][32 lanes]: operands of Q.K^T
+  uint4* qf16 = reinterpret_cast<uint4*>(smem + L.off_q);  // [2][NT][D / 32][32 lanes]: operands of Q.K^T
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.off_prefix);       // [nseq + 1] places before a sequence
   int32_t* lens = reinterpret_cast<int32_t*>(smem + L.off_lens);
-  float* qfac = reinterpret_cast<float*>(smem + L.off_qfac);               // [16] score factors
+  float* qfac = reinterpret_cast<float*>(smem + L.off_qfac);               // [2][16] score factors
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L.off_bar);         // the next segment's queries
+  uint64_t* merge_free = q_full + 1;  // the merge area and stat have been read
   __shared__ int warp_sums[kWarps];
   __shared__ int last_flag;
 
   ptx::griddep_launch_dependents();
   if (tid == 0) {
     ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(merge_free, kWarps);
     ptx::mbar_init_fence();
   }
-  for (int i = tid; i < NT * (D / 32) * 32; i += kThreads) qf16[i] = make_uint4(0, 0, 0, 0);  // heads past G
+  for (int i = tid; i < 2 * NT * (D / 32) * 32; i += kThreads) qf16[i] = make_uint4(0, 0, 0, 0);  // heads past G
   ptx::griddep_wait();
 
   // ---- places before every sequence: kLead and one for every unit of each of
@@ -394,8 +396,8 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   v_s1 += g * D / 128;
 
   // ---- queries: a (sequence, kv head)'s rows, fetched one segment ahead ----
-  // They are turned into f16, in the order of the operands, once the segment
-  // before is done.
+  // They are turned into f16, in the order of the operands, before the segment
+  // before is joined (its own are in the other buffer).
   const int q_chunks = G * D / 8;
   auto fetch_q = [&](const Cursor& c) {  // one run of bytes
     if (tid == 0) {
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   };
   bool aborted = false;
   uint32_t q_parity = 0;
-  auto convert_q = [&]() {
+  auto convert_q = [&](int b) {
     if (!ptx::mbar_wait(q_full, q_parity, kWaitLimitNs)) {
       aborted = true;  // the output is then undefined
       atomicExch(p.err, kDevErrTimeout);
@@ -434,10 +436,10 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
         r[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
       if (i < q_chunks) {
         const int h = i / (D / 8), c = i % (D / 8);  // head, eight dims of it
-        qf16[((h >> 3) * (D / 32) + c % (D / 32)) * 32 + (h & 7) * 4 + c / (D / 32)] = make_uint4(r[0], r[1], r[2], r[3]);
+        qf16[((b * NT + (h >> 3)) * (D / 32) + c % (D / 32)) * 32 + (h & 7) * 4 + c / (D / 32)] = make_uint4(r[0], r[1], r[2], r[3]);
         if (c == 0)
           // (not zero: a masked -inf times it stays -inf)
-          qfac[h] =
+          qfac[b * 16 + h] =
               fmaxf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23), 1.2e-38f);
       }
     }
@@ -449,8 +451,10 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   if (sc.st < 0) sc.st = 0;
   if (s_begin >= c_end) return;
   fetch_q(sc);
-  convert_q();
+  convert_q(0);
   __syncthreads();
+  int qb = 0;
+  uint32_t merge_parity = 1;  // free at the start
   for (int sb = s_begin; sb < c_end;) {
     const int item_b = sb - sc.st;                    // the item's first unit
     const int se = min(c_end, item_b + sc.nst);       // the segment's end
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) fac[nt][c] = nt * 8 + 2 * tig + c < G ? qfac[nt * 8 + 2 * tig + c] : 1.f;
+      for (int c = 0; c < 2; ++c) fac[nt][c] = nt * 8 + 2 * tig + c < G ? qfac[qb * 16 + nt * 8 + 2 * tig + c] : 1.f;
 
     float o[NT][kMma][4];
     float m[NT][2], l[NT][2];
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       for (int w = 0; w < kKWords; ++w) {
         uint4 q[NT];  // head g (and g + 8), eight dims
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) q[nt] = qf16[(nt * (D / 32) + w) * 32 + lane];
+        for (int nt = 0; nt < NT; ++nt) q[nt] = qf16[((qb * NT + nt) * (D / 32) + w) * 32 + lane];
 #pragma unroll
         for (int sl = 0; sl < 2; ++sl) {
           uint32_t h[2][4];
@@ -654,6 +658,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
     const int64_t out_row = static_cast<int64_t>(L.seq0 + sc.seq) * p.num_q_heads + sc.head * G;
     const int part_slot = sb == s_begin ? 0 : 1;
     float* part = L.part + (static_cast<int64_t>(blockIdx.x) * 2 + part_slot) * (G * (D + 2));
+    if (more) convert_q(qb ^ 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -666,7 +671,9 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       for (int h0 = 0; h0 < 8; h0 += kHeads) {
         const int heads = min(kHeads, G - nt * 8 - h0);  // of this round
         if (heads <= 0) break;
-        if (nt > 0 || h0 > 0) __syncthreads();
+        // the round before, of this segment or the last, is read
+        if (!ptx::mbar_wait(merge_free, merge_parity, kWaitLimitNs)) aborted = true;
+        merge_parity ^= 1u;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int h = 2 * tig + c - h0;
@@ -720,12 +727,14 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
             if (d == 0) *reinterpret_cast<float2*>(part + 2 * head) = make_float2(M, lsum);
           }
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(merge_free);
       }
     }
     if (!complete) {
       // the last CTA of the item joins the CTAs' parts, in the order of the tokens
       __threadfence();
-      __syncthreads();
+      __syncthreads();  // and nobody reads the merge area any more
       const int c0 = cta_of(item_b), c1 = cta_of(item_b + sc.nst - 1);
       if (tid == 0) {
         int32_t* counter = L.counters + c0;
@@ -784,12 +793,12 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
           }
         }
       }
+      __syncthreads();  // the merge area and the flag are free again
     }
     if (!more) break;
-    convert_q();
-    __syncthreads();  // the merge area and the flag are free again
     sb = se + kLead;
     sc = next;
+    qb ^= 1;
   }
   // a query copy whose wait of 2 s gave up is given another 2 s to land
   if (__syncthreads_or(aborted)) {
@@ -906,11 +915,11 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     L.off_merge = take(merge > kThreads * 20 ? merge : kThreads * 20);
     L.off_stat = take(kWarps * 8 * 8);
     L.off_qraw = take(G * head_dim * 2);
-    L.off_q = take((G <= 8 ? 8 : 16) * head_dim * 2);
-    L.off_qfac = take(16 * 4);
+    L.off_q = take(2 * (G <= 8 ? 8 : 16) * head_dim * 2);
+    L.off_qfac = take(2 * 16 * 4);
     L.off_prefix = take((L.nseq + 1) * 4);
     L.off_lens = take(L.nseq * 4);
-    L.off_bar = take(8);
+    L.off_bar = take(2 * 8);
     L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
     L.part = reinterpret_cast<float*>(p.ws + 256 + fp4_counter_bytes());
     // at least a unit for every warp, as far as the longest context allows
