@@ -52,7 +52,7 @@ __host__ __device__ constexpr int ring_stages(int D, int NT) { return D == 64 ||
 constexpr int kMergeHeads = 4;  // heads whose sums are joined at a time
 // What starting and joining a (sequence, kv head) costs a CTA, in units: the
 // shares of the CTAs count it, as places before the first unit.
-constexpr int kLead = 4;
+constexpr int kLead = 6;
 constexpr float kPShift = 10.f;  // probabilities enter P.V times 2^10
 // The reference of the probabilities is raised only when a score passes it by
 // more than 2^4: they stay below 2^14 in f16, and most units leave O alone.

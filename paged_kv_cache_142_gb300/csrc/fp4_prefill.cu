@@ -69,7 +69,7 @@ constexpr uint32_t kColO = 256;  // tensor memory: S of the tiles at 0 and 128, 
 
 // What starting and ending an item costs a CTA, in steps: the shares count it,
 // as places before the item's first step.
-constexpr int kLead = 1;
+constexpr int kLead = 2;
 constexpr int kMaxSeqs = 4096;   // of one launch: their places lie in shared memory
 constexpr int kMostParts = 32;   // CTAs of an item
 
