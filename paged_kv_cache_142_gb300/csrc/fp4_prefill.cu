@@ -271,24 +271,24 @@ __device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, 
   sum = t.x + t.y;
 }
 // the largest of a row's first nvis scores of a step
+template <bool MASK>
 __device__ __forceinline__ float row_max(uint32_t s_at, int nvis) {
   float m0 = -CUDART_INF_F, m1 = m0;
-  const bool all = __all_sync(0xffffffffu, nvis >= 128);
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
-    uint32_t v[2][16];
-    ptx::TmemLd<16>::run(s_at + c, v[0]);
-    ptx::TmemLd<16>::run(s_at + c + 16, v[1]);
-    wait_ld16(v[0]);
-    wait_ld16(v[1]);
+  for (int c = 0; c < 128; c += 64) {
+    uint32_t v[4][16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 4; ++h) ptx::TmemLd<16>::run(s_at + c + h * 16, v[h]);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) wait_ld16(v[h]);
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          x[e] = all || c + h * 16 + j + e < nvis ? __uint_as_float(v[h][j + e]) : -CUDART_INF_F;
+          x[e] = MASK && c + h * 16 + j + e >= nvis ? -CUDART_INF_F : __uint_as_float(v[h][j + e]);
         m0 = max3(m0, x[0], x[1]);
         m1 = max3(m1, x[2], x[3]);
       }
@@ -310,24 +310,20 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-// 32 outputs of a row, times inv, in whole 32-byte sectors
-__device__ __forceinline__ void store_out(const Fp4AttnParams& p, int64_t at, const uint32_t (&v)[32], float inv) {
+// 16 outputs of a row, times inv, in whole 32-byte sectors
+__device__ __forceinline__ void store_out(const Fp4AttnParams& p, int64_t at, const uint32_t (&v)[16], float inv) {
+  uint32_t h[8];
   if (p.out_bf16) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t h[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[16 * q + 2 * e]) * inv,
-                                                       __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
-        h[e] = *reinterpret_cast<const uint32_t*>(&x);
-      }
-      store32(static_cast<__nv_bfloat16*>(p.out) + at + 16 * q, h);
+    for (int e = 0; e < 8; ++e) {
+      const __nv_bfloat162 x =
+          __floats2bfloat162_rn(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+      h[e] = *reinterpret_cast<const uint32_t*>(&x);
     }
+    store32(static_cast<__nv_bfloat16*>(p.out) + at, h);
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t h[8];
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(__uint_as_float(v[8 * q + e]) * inv);
       store32(static_cast<float*>(p.out) + at + 8 * q, h);
@@ -659,7 +655,8 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         // is formed again (its scores are still there).  The first step starts
         // from its own maximum.
         if (t == 0) {
-          const float mx = row_max(s_at, nvis) * f;
+          const float mx =
+              (__all_sync(0xffffffffu, nvis >= 128) ? row_max<false>(s_at, nvis) : row_max<true>(s_at, nvis)) * f;
           if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
         }
         uint32_t pk[64];
@@ -711,24 +708,29 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         ptx::tc_fence_after();
         const float inv = l != 0.f ? p.v_scale / l : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          ptx::TmemLd<32>::run(o_at + c * 32, v);
-          ptx::tmem_wait_ld();
-          if (c == 3) {  // O is read: the next item's P.V may write it
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t v[4][16];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) ptx::TmemLd<16>::run(o_at + c + h * 16, v[h]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) wait_ld16(v[h]);
+          if (c == 64) {  // O is read: the next item's P.V may write it
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars[kOFree + i]);
           }
           if (!valid) continue;
-          if (it.whole) {
-            store_out(p, row * 128 + c * 32, v, inv);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(L.o + prow * 128 + c * 32);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+          for (int h = 0; h < 4; ++h) {
+            if (it.whole) {
+              store_out(p, row * 128 + c + h * 16, v[h], inv);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(L.o + prow * 128 + c + h * 16);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                dst[q] = make_float4(__uint_as_float(v[h][4 * q]), __uint_as_float(v[h][4 * q + 1]),
+                                     __uint_as_float(v[h][4 * q + 2]), __uint_as_float(v[h][4 * q + 3]));
+            }
           }
         }
       }
@@ -776,7 +778,9 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
                 acc[4 * j + 3] = fmaf(f2, x.w, acc[4 * j + 3]);
               }
             }
-            store_out(p, row * 128 + q * 32, reinterpret_cast<uint32_t(&)[32]>(acc), sum != 0.f ? p.v_scale / sum : 0.f);
+            const float inv = sum != 0.f ? p.v_scale / sum : 0.f;
+            store_out(p, row * 128 + q * 32, reinterpret_cast<uint32_t(&)[16]>(acc[0]), inv);
+            store_out(p, row * 128 + q * 32 + 16, reinterpret_cast<uint32_t(&)[16]>(acc[16]), inv);
           }
         }
         ptx::bar_sync(3, 256);  // the flag is free again
