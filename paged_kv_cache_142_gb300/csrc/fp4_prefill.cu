@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       const int64_t row = static_cast<int64_t>(it.c.b + it.tok0 + trow) * p.num_q_heads + it.kvh * G + g;
       const bool valid = trow < it.ntok;
       const int steps = it.steps_of(i);
-      const int limit = valid ? it.pos0 + trow + 1 : 0;  // keys that this row sees
+      // keys that this row sees (one that is nobody's: as the last, so that it needs no mask of its own)
+      const int limit = valid ? it.pos0 + trow + 1 : it.kend();
       float m = -CUDART_INF_F, l = 0.f;
       for (int t = 0; t < steps && !aborted; ++t, ++sc) {
         wait(&bars[kSFull + i], sc & 1u, aborted);
@@ -698,8 +699,8 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&bars[kPFull + i]);
       }
       // a part's place; its row: token of the pair, then head
-      auto part_of = [&](int c) { return (c * 2 + (cta_begin(c) >= it.start ? 0 : 1)) * L.rows + trow * G + g; };
-      const int64_t prow = part_of(blockIdx.x);
+      auto part_of = [&](int c) { return static_cast<int64_t>(c * 2 + (cta_begin(c) >= it.start ? 0 : 1)) * L.rows; };
+      const int64_t prow = part_of(blockIdx.x) + trow * G + g;
       if (steps > 0 && !aborted) {
         wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
@@ -752,35 +753,38 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
           __threadfence();
         }
         ptx::bar_sync(3, 256);
-        if (last_flag && valid) {
-          float M = -CUDART_INF_F;
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(L.ml + static_cast<int64_t>(part_of(c)) * 2));
-          const float ref = M == -CUDART_INF_F ? 0.f : M;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float acc[32], sum = 0.f;
+        if (last_flag) {
+          // 16 outputs a thread, eight threads a row: a warp reads whole rows
+          for (int k = tid; k < it.ntok * G * 8; k += 256) {
+            const int pr = k >> 3, d = (k & 7) * 16;  // token of the pair * G + head
+            float M = -CUDART_INF_F;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(L.ml + (part_of(c) + pr) * 2));
+            const float ref = M == -CUDART_INF_F ? 0.f : M;
+            float acc[16], sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[j] = 0.f;
-#pragma unroll 1
+            for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+#pragma unroll 2
             for (int c = c0; c <= c1; ++c) {
-              const int64_t at = part_of(c);
+              const int64_t at = part_of(c) + pr;
               const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + at * 2));
-              if (e.y == 0.f) continue;  // a part that this row sees nothing of: its O may not be written
-              const float f2 = fast_exp2(e.x - ref);
-              sum = fmaf(f2, e.y, sum);
-              const float4* src = reinterpret_cast<const float4*>(L.o + at * 128 + q * 32);
+              const float4* src = reinterpret_cast<const float4*>(L.o + at * 128 + d);
+              float4 x[4];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 x = __ldcg(src + j);
-                acc[4 * j] = fmaf(f2, x.x, acc[4 * j]);
-                acc[4 * j + 1] = fmaf(f2, x.y, acc[4 * j + 1]);
-                acc[4 * j + 2] = fmaf(f2, x.z, acc[4 * j + 2]);
-                acc[4 * j + 3] = fmaf(f2, x.w, acc[4 * j + 3]);
+              for (int j = 0; j < 4; ++j) x[j] = __ldcg(src + j);
+              if (e.y == 0.f) continue;  // a part that this row sees nothing of: its O may be anything
+              const float w = fast_exp2(e.x - ref);
+              sum = fmaf(w, e.y, sum);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                acc[4 * j] = fmaf(w, x[j].x, acc[4 * j]);
+                acc[4 * j + 1] = fmaf(w, x[j].y, acc[4 * j + 1]);
+                acc[4 * j + 2] = fmaf(w, x[j].z, acc[4 * j + 2]);
+                acc[4 * j + 3] = fmaf(w, x[j].w, acc[4 * j + 3]);
               }
             }
-            const float inv = sum != 0.f ? p.v_scale / sum : 0.f;
-            store_out(p, row * 128 + q * 32, reinterpret_cast<uint32_t(&)[16]>(acc[0]), inv);
-            store_out(p, row * 128 + q * 32 + 16, reinterpret_cast<uint32_t(&)[16]>(acc[16]), inv);
+            const int64_t orow = static_cast<int64_t>(it.c.b + it.tok0 + pr / G) * p.num_q_heads + it.kvh * G + pr % G;
+            store_out(p, orow * 128 + d, reinterpret_cast<uint32_t(&)[16]>(acc), sum != 0.f ? p.v_scale / sum : 0.f);
           }
         }
         ptx::bar_sync(3, 256);  // the flag is free again
