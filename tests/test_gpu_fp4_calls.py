@@ -1,0 +1,249 @@
+"""Calls of the 4-bit cache that its documentation allows around the plain
+ones: one workspace for calls of many shapes, captured graphs beside eager
+calls, other streams, pools past 2^31 bytes, batches past one launch, softmax
+scales of any sign, rows behind the last chunk."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import fp4
+from fp4_case import attention_bound, bf16, pool
+from paged_case import to_device, to_f64
+from test_gpu_fp4 import KS, VS, _attention_case, _check, _decode, _dev, _reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops(lib):
+    import importlib
+    return importlib.import_module("paged_kv_cache_142_gb300.ops")
+
+
+def test_one_workspace_for_many_shapes(ops):
+    """Batches, lengths, groups and chunk sizes change from call to call over a
+    workspace that was zeroed once."""
+    rng = np.random.default_rng(1)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    shapes = [(4, 8, 128, 16, [700] * 6), (1, 2, 64, 8, [3000, 5]), (16, 1, 128, 32, [2500]), (4, 8, 128, 16, [9, 4000]),
+              (2, 1, 256, 16, [1900]), (4, 8, 128, 16, [700] * 6)]
+    for G, hkv, d, bs, lens in shapes:
+        tables, kc, vc = _attention_case(rng, lens, G, hkv, d, bs)
+        q = bf16(rng.standard_normal((len(lens), G * hkv, d)))
+        ref, tol = _reference(q.f32, tables, kc, vc, bs, d, 0.1, range(len(lens)), lens)
+        _check(_decode(ops, q, tables, lens, _dev(kc), _dev(vc), bs, 0.1, hkv, ws=ws), ref, tol)
+        if d != 128:
+            continue
+        for n in (1, 70):  # the same sequences' last tokens as a chunk, through the same workspace
+            n = min(n, min(lens))
+            chunks = [(x - n, n) for x in lens]
+            qp = bf16(rng.standard_normal((n * len(lens), G * hkv, d)))
+            cu = np.arange(0, n * len(lens) + 1, n, dtype=np.int32)
+            out = torch.full(qp.shape, float("nan"), device="cuda")
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            ops.pa_prefill_fp4(out, to_device(qp), _dev(kc), _dev(vc), _dev(cu),
+                               _dev(np.array([s for s, _ in chunks], np.int32)), _dev(tables), 0.1, hkv, bs, n, max(lens),
+                               ws, KS, VS, status=st)
+            rows = [(i, s + j + 1) for i, (s, c) in enumerate(chunks) for j in range(c)]
+            pick = sorted({0, len(rows) - 1, *rng.integers(0, len(rows), 12).tolist()})
+            ref, tol = _reference(qp.f32[pick], tables, kc, vc, bs, d, 0.1, [rows[r][0] for r in pick],
+                                  [rows[r][1] for r in pick])
+            assert int(st.item()) == 0
+            _check(out[torch.tensor(pick, device="cuda")], ref, tol)
+    assert ops.pa_workspace_error(ws) == 0
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30, 3.0])
+def test_decode_with_any_softmax_scale(ops, scale):
+    rng = np.random.default_rng(2)
+    lens, d, bs = [100, 1, 70], 128, 16
+    tables, kc, vc = _attention_case(rng, lens, 4, 2, d, bs)
+    q = bf16(rng.standard_normal((3, 8, d)))
+    ref, tol = _reference(q.f32, tables, kc, vc, bs, d, scale, range(3), lens)
+    _check(_decode(ops, q, tables, lens, _dev(kc), _dev(vc), bs, scale, 2), ref, tol)
+
+
+def test_pool_past_2_to_the_31_bytes(ops):
+    """Blocks at the far end of pools of more than 2^31 bytes: append, gather,
+    decode, prefill, copy and compaction."""
+    rng = np.random.default_rng(3)
+    hkv, bs, d, G, n = 8, 16, 128, 4, 75
+    tile = fp4.tile_bytes(bs, d)
+    nb = (1 << 31) // (hkv * tile) + 100
+    kc, vc = ops.make_cache_fp4(nb, hkv, bs, d), ops.make_cache_fp4(nb, hkv, bs, d)
+    table = np.array([[nb - 1, 3, nb - 7, nb - 2, nb - 50]], dtype=np.int32)
+    k, v = (bf16(rng.standard_normal((n, hkv, d))) for _ in range(2))
+    pos = np.arange(n)
+    slots = table[0, pos // bs].astype(np.int64) * bs + pos % bs
+    ops.pa_reshape_and_cache_fp4(to_device(k), to_device(v), _dev(slots), kc, vc, bs, KS, VS)
+    K, V = fp4.dequantise(*fp4.quantise(k.f32, KS), KS), fp4.dequantise(*fp4.quantise(v.f32, VS), VS)
+    ko, vo = (torch.zeros(n, hkv, d, device="cuda") for _ in range(2))
+    ops.pa_gather_cache_fp4(ko, vo, _dev(slots), kc, vc, bs, KS, VS)
+    assert np.array_equal(to_f64(ko), K) and np.array_equal(to_f64(vo), V)
+    q = bf16(rng.standard_normal((n, G * hkv, d)))
+    got = _decode(ops, q[n - 1:], table, [n], kc, vc, bs, 0.1, hkv)
+    ref = oracle.contiguous_attention(q.f32[n - 1], K, V, 0.1)
+    tol = attention_bound(q.f32[n - 1].astype(np.float64), K, V, 0.1)[:, None]
+    _check(got[0], ref, tol)
+    ws = ops.make_prefill_workspace_fp4(1, G * hkv, hkv, d, bs, n, n)
+    out = torch.zeros(n, G * hkv, d, device="cuda")
+    ops.pa_prefill_fp4(out, to_device(q), kc, vc, _dev(np.array([0, n], np.int32)), _dev(np.array([0], np.int32)),
+                       _dev(table), 0.1, hkv, bs, n, n, ws, KS, VS)
+    _check(out[n - 1], ref, tol)
+    ops.pa_copy_blocks(kc, vc, _dev(np.array([[nb - 1, nb - 3]], np.int64)), block_size=bs, head_dim=d)
+    table2 = table.copy()
+    table2[0, 0] = nb - 3
+    _check(_decode(ops, q[n - 1:], table2, [n], kc, vc, bs, 0.1, hkv)[0], ref, tol)
+    keep = [9, 20, 40, 70]
+    ops.pa_compact_tokens(kc, vc, _dev(table2), _dev(np.array([2], np.int32)), _dev(np.array(keep, np.int32)),
+                          _dev(np.array([0, 4], np.int32)), 4, bs, d)
+    kept = [0, 1] + keep
+    ref = oracle.contiguous_attention(q.f32[0], K[kept], V[kept], 0.1)
+    tol = attention_bound(q.f32[0].astype(np.float64), K[kept], V[kept], 0.1)[:, None]
+    _check(_decode(ops, q[:1], table2, [6], kc, vc, bs, 0.1, hkv)[0], ref, tol)
+
+
+def test_prefill_batches_past_one_launch(ops):
+    """More sequences than one launch takes, empty ones at both ends and between."""
+    rng = np.random.default_rng(4)
+    S, hkv, G, bs, d = 5000, 1, 2, 16, 128
+    n = rng.integers(0, 3, size=S)
+    n[[0, 1, 4095, 4096, 4097, S - 1]] = 0
+    start = rng.integers(0, 20, size=S)
+    need = -(-(start + n) // bs)
+    m = int(need.max())
+    nb = 64
+    tables = rng.integers(0, nb, size=(S, m)).astype(np.int32)  # sequences share blocks freely: only read
+    kc, vc = pool(rng, nb, hkv, bs, d, KS), pool(rng, nb, hkv, bs, d, VS)
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    q = bf16(rng.standard_normal((int(cu[-1]) + 3, G * hkv, d)))
+    ws = ops.make_prefill_workspace_fp4(S, G * hkv, hkv, d, bs, 2, 22)
+    out = torch.full(q.shape, 5.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.pa_prefill_fp4(out, to_device(q), _dev(kc), _dev(vc), _dev(cu), _dev(start.astype(np.int32)), _dev(tables), 0.1,
+                       hkv, bs, 2, 22, ws, KS, VS, status=st)
+    assert int(st.item()) == 0 and bool((out[cu[-1]:] == 5.0).all())  # rows behind the last chunk stay
+    rows = [(i, start[i] + j + 1) for i in range(S) for j in range(n[i])]
+    pick = sorted({0, len(rows) - 1, *rng.integers(0, len(rows), 300).tolist()})
+    ref, tol = _reference(q.f32[pick], tables, kc, vc, bs, d, 0.1, [rows[r][0] for r in pick], [rows[r][1] for r in pick])
+    _check(out[torch.tensor(pick, device="cuda")], ref, tol)
+
+
+def test_two_streams_and_captured_prefill(ops):
+    """Decode and prefill at the same time on two streams with workspaces of
+    their own; the prefill captured and replayed with other chunk lengths."""
+    rng = np.random.default_rng(5)
+    lens, G, hkv, bs, d = [900, 40, 333], 4, 8, 16, 128
+    tables, kc, vc = _attention_case(rng, lens, G, hkv, d, bs)
+    H = G * hkv
+    k, v, t = _dev(kc), _dev(vc), _dev(tables)
+    q1, q2 = bf16(rng.standard_normal((3, H, d))), bf16(rng.standard_normal((60, H, d)))
+    d1, d2, n1 = to_device(q1), to_device(q2), _dev(np.array(lens, np.int32))
+    o1, o2 = torch.zeros(3, H, d, device="cuda"), torch.zeros(60, H, d, device="cuda")
+    w1 = ops.make_workspace_fp4(3, H, hkv, d, bs, 900)
+    w2 = ops.make_prefill_workspace_fp4(3, H, hkv, d, bs, 40, 900)
+    chunks = [(860, 40), (35, 5), (318, 15)]
+    cu = _dev(np.array([0, 40, 45, 60], np.int32))
+    start = _dev(np.array([s for s, _ in chunks], np.int32))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pre = lambda: ops.pa_prefill_fp4(o2, d2, k, v, cu, start, t, 0.1, hkv, bs, 40, 900, w2, KS, VS, status=st)
+    dec = lambda: ops.pa_decode_fp4(o1, d1, k, v, t, n1, 0.1, hkv, bs, 900, w1, KS, VS)
+    pre()
+    dec()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pre()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(s1):
+            dec()
+        with torch.cuda.stream(s2):
+            g.replay()
+    torch.cuda.synchronize()
+
+    def check_prefill(chunks):
+        rows = [(i, s + j + 1) for i, (s, c) in enumerate(chunks) for j in range(c)]
+        ref, tol = _reference(q2.f32[:len(rows)], tables, kc, vc, bs, d, 0.1, [r[0] for r in rows], [r[1] for r in rows])
+        _check(o2[:len(rows)], ref, tol)
+
+    check_prefill(chunks)
+    ref, tol = _reference(q1.f32, tables, kc, vc, bs, d, 0.1, range(3), lens)
+    _check(o1, ref, tol)
+    chunks = [(0, 3), (0, 40), (200, 0)]
+    cu.copy_(torch.tensor([0, 3, 43, 43], dtype=torch.int32))
+    start.copy_(torch.tensor([0, 0, 200], dtype=torch.int32))
+    o2.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    check_prefill(chunks)
+    assert int(st.item()) == 0 and bool(torch.isnan(o2[43:]).all())
+
+
+@pytest.mark.parametrize("ks,vs", [(2.0 ** -32, 2.0 ** 32), (1.0, 1.0), (2.0 ** 10, 2.0 ** -20)])
+def test_extreme_global_scales(ops, ks, vs):
+    rng = np.random.default_rng(6)
+    n, hkv, bs, d, G = 40, 2, 16, 64, 2
+    k, v = (rng.standard_normal((n, hkv, d)) * ks * 8).astype(np.float32), (rng.standard_normal((n, hkv, d)) * vs * 8).astype(
+        np.float32)
+    kc, vc = ops.make_cache_fp4(3, hkv, bs, d), ops.make_cache_fp4(3, hkv, bs, d)
+    slots = np.arange(n, dtype=np.int64)
+    ops.pa_reshape_and_cache_fp4(_dev(k), _dev(v), _dev(slots), kc, vc, bs, ks, vs)
+    K, V = fp4.dequantise(*fp4.quantise(k, ks), ks), fp4.dequantise(*fp4.quantise(v, vs), vs)
+    ko, vo = (torch.zeros(n, hkv, d, device="cuda") for _ in range(2))
+    ops.pa_gather_cache_fp4(ko, vo, _dev(slots), kc, vc, bs, ks, vs)
+    assert np.array_equal(to_f64(ko), K) and np.array_equal(to_f64(vo), V)
+    q = bf16(rng.standard_normal((1, G * hkv, d)) / 8)
+    scale = 0.25 / ks if ks < 1 else 0.25 / ks
+    ws = ops.make_workspace_fp4(1, G * hkv, hkv, d, bs, n)
+    out = torch.zeros(1, G * hkv, d, device="cuda")
+    ops.pa_decode_fp4(out, to_device(q), kc, vc, _dev(np.array([[0, 1, 2]], np.int32)), _dev(np.array([n], np.int32)),
+                      scale, hkv, bs, n, ws, ks, vs)
+    ref = oracle.contiguous_attention(q.f32[0], K, V, scale)
+    tol = attention_bound(q.f32[0].astype(np.float64), K, V, scale)[:, None]
+    _check(out[0], ref, tol)
+
+
+def test_tables_wider_than_the_lengths(ops):
+    """max_context_len is a bound: the tables and it may be far larger than any
+    length, and the entries behind a sequence's pages are never read."""
+    rng = np.random.default_rng(7)
+    lens, d, bs, hkv, G = [33, 0, 129, 16], 128, 16, 2, 4
+    tables, kc, vc = _attention_case(rng, lens, G, hkv, d, bs)
+    wide = np.full((4, 2048), 1 << 30, dtype=np.int32)
+    wide[:, :tables.shape[1]] = np.where(tables < 0, 1 << 30, tables)
+    q = bf16(rng.standard_normal((4, G * hkv, d)))
+    ref, tol = _reference(q.f32, tables, kc, vc, bs, d, 0.1, range(4), lens)
+    _check(_decode(ops, q, wide, lens, _dev(kc), _dev(vc), bs, 0.1, hkv, max_len=32768), ref, tol)
+
+
+def test_refusals_of_the_binding(ops):
+    hkv, bs, d, G = 2, 16, 128, 4
+    kc, vc = ops.make_cache_fp4(4, hkv, bs, d), ops.make_cache_fp4(4, hkv, bs, d)
+    q = torch.zeros(2, G * hkv, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    t, n = torch.zeros(2, 2, dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    ws = ops.make_workspace_fp4(2, G * hkv, hkv, d, bs, 32)
+    good = dict(out=out, q=q, k_cache=kc, v_cache=vc, block_tables=t, context_lens=n, scale=0.1, num_kv_heads=hkv,
+                block_size=bs, max_context_len=32, workspace=ws)
+    ops.pa_decode_fp4(**good)
+    for change in (dict(q=q.float()), dict(out=out[:1]), dict(out=out.half()), dict(k_cache=kc[:, :1]), dict(block_size=8),
+                   dict(num_kv_heads=1), dict(block_tables=t.long()), dict(block_tables=t[:1]), dict(context_lens=n[:1]),
+                   dict(context_lens=n.cpu()), dict(workspace=ws.float()), dict(q=q.transpose(0, 1)),
+                   dict(k_cache=kc.cpu()), dict(v_cache=kc.to(torch.int8))):
+        with pytest.raises(ValueError):
+            ops.pa_decode_fp4(**{**good, **change})
+    for change in (dict(max_context_len=33), dict(workspace=ws[:300]), dict(k_scale=0.3), dict(scale=float("inf"))):
+        with pytest.raises(ops.PAError):
+            ops.pa_decode_fp4(**{**good, **change})
+    x = torch.zeros(3, hkv, d, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    for bad in ((x.half(), x.half(), slots), (x, x[:2], slots), (x, x, slots.int()), (x, x, slots[:2]),
+                (x.transpose(0, 1), x.transpose(0, 1), slots[:2])):
+        with pytest.raises(ValueError):
+            ops.pa_reshape_and_cache_fp4(*bad, kc, vc, bs)
+    pad = torch.zeros(3 * hkv * d + 4, device="cuda")[4:].view(3, hkv, d)  # 16-byte aligned only
+    with pytest.raises(ops.PAError):
+        ops.pa_reshape_and_cache_fp4(pad, x, slots, kc, vc, bs)
+    torch.cuda.synchronize()
