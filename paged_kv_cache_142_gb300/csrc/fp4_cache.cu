@@ -7,6 +7,7 @@
 
 #include "decode.cuh"
 #include "fp4.cuh"
+#include "ptx.cuh"
 
 namespace pa {
 namespace {
@@ -83,6 +84,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3)
     fp4_append_kernel(const Fp4RowParams p, const void* __restrict__ key, const void* __restrict__ value,
                       uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, float k_scale, float v_scale,
                       float k_inv, float v_inv) {
+  // an attention call launched behind this one may begin its set-up; it waits
+  // for this grid's writes before it reads the cache
+  ptx::griddep_launch_dependents();
   const unsigned char* src = static_cast<const unsigned char*>(blockIdx.y ? value : key);
   uint8_t* cache = blockIdx.y ? v_cache : k_cache;
   const float k = blockIdx.y ? v_scale : k_scale, inv = blockIdx.y ? v_inv : k_inv;

@@ -32,15 +32,24 @@ def dtype_code(dt) -> int:
     raise ValueError(f"unsupported dtype {dt}")
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev=None) -> int:
     if stream is None:  # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     return int(stream.cuda_stream)
 
 
 def _need(cond: bool, msg: str) -> None:
     if not cond:
         raise ValueError(msg)
+
+
+def _all_on(dev, *tensors) -> None:
+    """Every tensor given is on CUDA device ``dev``, the current one."""
+    for t in tensors:
+        if t.get_device() != dev:
+            if t.get_device() < 0:
+                raise ValueError("host tensor where a CUDA tensor is needed")
+            _on_current_device(t)
 
 
 def _on_current_device(*tensors) -> None:
@@ -79,8 +88,9 @@ def _fp4_dims(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size, head_dim
     if len(shape) != 3 or shape[2] != tile or v_cache.shape != shape:
         raise ValueError(f"4-bit caches must be [NB, Hkv, {tile}] both, for block_size {block_size}, "
                          f"head_dim {head_dim}")
-    _need(k_cache.dtype is torch.uint8 and v_cache.dtype is torch.uint8 and k_cache.is_cuda and v_cache.is_cuda
-          and k_cache.is_contiguous() and v_cache.is_contiguous(), "4-bit caches must be contiguous CUDA uint8 tensors")
+    if not (k_cache.dtype is torch.uint8 and v_cache.dtype is torch.uint8 and k_cache.is_cuda and v_cache.is_cuda
+            and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("4-bit caches must be contiguous CUDA uint8 tensors")
     return shape[0], shape[1]
 
 
@@ -375,40 +385,41 @@ def make_cache_fp4(num_blocks, num_kv_heads, block_size, head_dim, num_layers=No
     return torch.zeros(shape if num_layers is None else (num_layers, *shape), dtype=torch.uint8, device=device)
 
 
-def _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size):
-    _need(key.dim() == 3 and value.shape == key.shape and value.dtype == key.dtype, "key/value must be [T, Hkv, D]")
-    T, Hkv, D = key.shape
+def _fp4_rows(name, key, value, slot_mapping, k_cache, v_cache, block_size, k_scale, v_scale, stream, status):
+    shape = key.shape
+    if len(shape) != 3 or value.shape != shape or value.dtype is not key.dtype or not (
+            key.is_contiguous() and value.is_contiguous()):
+        raise ValueError("key/value must be contiguous [T, Hkv, D] of one dtype")
+    T, Hkv, D = shape
     NB, cache_heads = _fp4_dims(k_cache, v_cache, block_size, D)
-    _need(Hkv == cache_heads, "num_kv_heads does not match the cache")
-    _need(key.is_cuda and value.is_cuda and key.is_contiguous() and value.is_contiguous(),
-          "key/value must be contiguous CUDA tensors")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T and slot_mapping.is_cuda
-          and slot_mapping.is_contiguous(), "slot_mapping must be a contiguous CUDA int64 tensor of num_tokens entries")
-    return T, NB, Hkv, D
+    if Hkv != cache_heads:
+        raise ValueError("num_kv_heads does not match the cache")
+    if not (slot_mapping.dtype is torch.int64 and slot_mapping.numel() == T and slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping must be a contiguous CUDA int64 tensor of num_tokens entries")
+    dev = torch.cuda.current_device()
+    _all_on(dev, key, value, slot_mapping, k_cache, v_cache)
+    if status is not None:
+        _all_on(dev, status)
+    L.check(getattr(_LIB, name)(
+        key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
+        _stream(stream, dev)), name)
 
 
 def pa_reshape_and_cache_fp4(key, value, slot_mapping, k_cache, v_cache, block_size, k_scale=1.0, v_scale=1.0,
                              stream=None, status=None) -> None:
     """Quantise key/value ``[T, Hkv, D]`` (fp32 or bf16) into the slots
     ``slot_mapping[T]`` of the 4-bit caches."""
-    T, NB, Hkv, D = _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size)
-    _on_current_device(key, value, slot_mapping, k_cache, v_cache, status)
-    L.check(_LIB.pa_reshape_and_cache_fp4(
-        key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
-        _stream(stream)), "pa_reshape_and_cache_fp4")
+    _fp4_rows("pa_reshape_and_cache_fp4", key, value, slot_mapping, k_cache, v_cache, block_size, k_scale, v_scale,
+              stream, status)
 
 
 def pa_gather_cache_fp4(key, value, slot_mapping, k_cache, v_cache, block_size, k_scale=1.0, v_scale=1.0,
                         stream=None, status=None) -> None:
     """Fill key/value ``[T, Hkv, D]`` (fp32 or bf16) with the values held in
     the slots ``slot_mapping[T]``; rows of negative slots stay as they are."""
-    T, NB, Hkv, D = _fp4_rows(key, value, slot_mapping, k_cache, v_cache, block_size)
-    _on_current_device(key, value, slot_mapping, k_cache, v_cache, status)
-    L.check(_LIB.pa_gather_cache_fp4(
-        key.data_ptr(), value.data_ptr(), dtype_code(key.dtype), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), NB, int(block_size), Hkv, D, float(k_scale), float(v_scale), _status_ptr(status),
-        _stream(stream)), "pa_gather_cache_fp4")
+    _fp4_rows("pa_gather_cache_fp4", key, value, slot_mapping, k_cache, v_cache, block_size, k_scale, v_scale,
+              stream, status)
 
 
 def pa_decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
@@ -427,16 +438,18 @@ def make_workspace_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size
 
 
 def _fp4_queries(out, q, k_cache, v_cache, block_tables, num_seqs, num_kv_heads, block_size, workspace):
-    _need(q.dim() == 3 and q.dtype == torch.bfloat16 and q.is_cuda and q.is_contiguous(),
-          "q must be a contiguous CUDA bf16 tensor [rows, H, D]")
+    if q.dim() != 3 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA bf16 tensor [rows, H, D]")
     NB, Hkv = _fp4_dims(k_cache, v_cache, block_size, q.shape[2])
-    _need(Hkv == num_kv_heads, "num_kv_heads does not match the cache")
-    _need(out.shape == q.shape and out.is_cuda and out.is_contiguous()
-          and out.dtype in (torch.float32, torch.bfloat16), "out must be a contiguous fp32 or bf16 tensor of q's shape")
-    _need(block_tables.dtype == torch.int32 and block_tables.is_cuda and block_tables.dim() == 2
-          and block_tables.shape[0] == num_seqs and block_tables.is_contiguous(),
-          "block_tables must be contiguous int32 [num_seqs, max_blocks]")
-    _need(workspace.dtype is torch.uint8 and workspace.is_cuda, "workspace must be a CUDA uint8 tensor")
+    if Hkv != num_kv_heads:
+        raise ValueError("num_kv_heads does not match the cache")
+    if out.shape != q.shape or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be a contiguous fp32 or bf16 tensor of q's shape")
+    if not (block_tables.dtype is torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == num_seqs
+            and block_tables.is_contiguous()):
+        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks]")
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
     return NB
 
 
@@ -446,12 +459,13 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, context_lens, scale, n
     B, H, D = q.shape
     NB = _fp4_queries(out, q, k_cache, v_cache, block_tables, B, num_kv_heads, block_size, workspace)
     _i32(context_lens, B, "context_lens")
-    _on_current_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    dev = torch.cuda.current_device()
+    _all_on(dev, out, q, k_cache, v_cache, block_tables, context_lens, workspace)
     L.check(_LIB.pa_decode_fp4(
         out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), B, H, k_cache.data_ptr(), v_cache.data_ptr(), NB,
         int(block_size), num_kv_heads, D, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
         int(max_context_len), float(scale), float(k_scale), float(v_scale), workspace.data_ptr(), workspace.numel(),
-        _stream(stream)), "pa_decode_fp4")
+        _stream(stream, dev)), "pa_decode_fp4")
 
 
 def make_prefill_workspace_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
@@ -473,12 +487,15 @@ def pa_prefill_fp4(out, q, k_cache, v_cache, cu_q, q_start, block_tables, scale,
     _i32(cu_q, S + 1, "cu_q")
     _i32(q_start, S, "q_start")
     NB = _fp4_queries(out, q, k_cache, v_cache, block_tables, S, num_kv_heads, block_size, workspace)
-    _on_current_device(out, q, k_cache, v_cache, block_tables, cu_q, q_start, status, workspace)
+    dev = torch.cuda.current_device()
+    _all_on(dev, out, q, k_cache, v_cache, block_tables, cu_q, q_start, workspace)
+    if status is not None:
+        _all_on(dev, status)
     L.check(_LIB.pa_prefill_fp4(
         out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), T, cu_q.data_ptr(), q_start.data_ptr(), S,
         int(max_q_len), int(max_context_len), H, k_cache.data_ptr(), v_cache.data_ptr(), NB, int(block_size),
         num_kv_heads, D, block_tables.data_ptr(), block_tables.shape[1], float(scale), float(k_scale),
-        float(v_scale), _status_ptr(status), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        float(v_scale), _status_ptr(status), workspace.data_ptr(), workspace.numel(), _stream(stream, dev)),
         "pa_prefill_fp4")
 
 
