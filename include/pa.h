@@ -427,7 +427,7 @@ size_t pa_fp4_tile_bytes(int32_t block_size, int32_t head_dim);
  * aligned (PA_ERR_INVALID_ARG otherwise; also in the gather).  status
  * (device int32, caller-zeroed, or NULL) receives PA_ERR_INVALID_ARG if a
  * slot lies past the pool; such a token is not written, negative slots are
- * padding. */
+ * padding.  Two tokens of one call in the same slot leave it undefined. */
 pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, pa_dtype src_dtype,
                                    int32_t num_tokens, const int64_t* slot_mapping,
                                    void* k_cache, void* v_cache,

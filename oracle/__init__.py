@@ -23,6 +23,8 @@ Modules:
   allocator   block pool with a free list, reference counts, fork and COW
   prefix_cache  automatic prefix caching on the pool (chained SHA-256 block
               keys over full blocks, LRU eviction of freed cached blocks)
+  fp4         the K/V cache held in 4 bits: quantisation by search among the
+              codes' values, page layout, token compaction
 
 Every function here is pinned by ``tests/test_oracle_pins.py`` against values
 the pages print, closed forms and brute force; none is "parity unpinned".

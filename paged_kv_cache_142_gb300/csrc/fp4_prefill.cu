@@ -21,7 +21,10 @@
 //  * warps 8-11 restore: a thread owns one key of a tile.  It reads the key's
 //    64 code bytes and 8 scales through the block table, one tile ahead, and
 //    writes the 128 values in the 128-byte-swizzled layout that the tensor core
-//    reads; then the same for the value row.  Warp 8 loads the queries too
+//    reads; then the same for the value row.  A value group that stands for NaN
+//    enters the product as zero, and its key's place is noted: rows that see
+//    the key put NaN out, while 0 * NaN must not reach the others.  Warp 8 loads
+//    the queries too
 //    (turning them to f16 here instead, with a power of two for each row, cost
 //    12000 clocks an item: four warps of long dependent chains);
 //  * warps 12 and 13 issue the products of the first and the second tile.
@@ -32,9 +35,17 @@
 //  * warps 0-3 and 4-7 run the softmax of the first and the second tile, one
 //    row a thread: maximum, exponentials and sum in fp32 (log2 domain).  The
 //    reference of a row is raised only when its maximum passes it by 2^8.
-// What bounds it: the tensor core needs about 2150 clocks for a step's four
-// products, the exponentials and their conversions about 1700 of the SM's
-// issue slots, the restoring about 400.
+// What bounds it is a tile's chain: 128 rows' exponentials (1000 clocks; 512 of
+// them the exponential unit's), P.V and Q.K^T (550 each), and 900 of barriers and
+// tensor-memory waits, 3150 a step in all; the other tile's products fill its
+// gaps, 2250 of the 3150 clocks.  16 prompts of 2048 tokens, 32 q / 8 kv heads:
+// 530 us, 1040 TFLOP/s, 53% of the measured bf16 rate; a chunk of 512 tokens over
+// 16000: 1210 TFLOP/s.  What it took: one elected lane of a uniform warp issues
+// unrolled products (a rolled loop of one lane: 130 clocks an instruction, 987 us
+// instead of 730), one pass over the scores on the reference as it is, a warp for
+// each tile's products taking turns (720 to 692 us), equal runs and TMA queries
+// (678), items walked instead of searched and whole-sector stores (592), and
+// kLead of 2 (530).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -54,7 +65,8 @@ constexpr int kOffQ = 0;           // two tiles: [half of the dims][128 rows][12
 constexpr int kOffK = 2 * kTileBytes;
 constexpr int kOffV = kOffK + 2 * kTileBytes;
 constexpr int kOffBar = kOffV + 2 * kTileBytes;
-constexpr int kOffPrefix = kOffBar + 256;         // [sequences + 1] places before a sequence
+constexpr int kOffNan = kOffBar + 256;            // [8 items][8 groups] the first key whose value is NaN
+constexpr int kOffPrefix = kOffNan + 256;         // [sequences + 1] places before a sequence
 constexpr int kSmemBytes = kOffPrefix + 1024;     // with slack to align the base, then the places
 constexpr float kSlack = 8.f;     // the reference is raised past 2^8
 constexpr float kPShift = 6.f;    // probabilities enter P.V times 2^6: below 2^14, none lost before 2^-30
@@ -346,6 +358,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* prefix = reinterpret_cast<int*>(smem + kOffPrefix);
+  int* first_nan = reinterpret_cast<int*>(smem + kOffNan);
   __shared__ int warp_sums[kThreads / 32];
   __shared__ int last_flag;
 
@@ -367,6 +380,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
+  if (tid < 64) first_nan[tid] = 0x7fffffff;
   if (warp == 12) {
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tc_fence_before();
@@ -431,6 +445,18 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       }
       return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(phys) * p.num_kv_heads + it.kvh) *
                                   L.tile_bytes);
+    };
+    // NaN scales of a value row out of it, and noted
+    auto take_nan = [&](Row& x, int key, int* noted) {
+      uint32_t w[2] = {x.s.x, x.s.y};
+      if ((((w[0] & 0x7f7f7f7fu) + 0x01010101u) | ((w[1] & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) {
+        for (int g = 0; g < 8; ++g)
+          if (((w[g >> 2] >> (8 * (g & 3))) & 0x7fu) == 0x7fu) {
+            atomicMin(&noted[g], key);
+            w[g >> 2] &= ~(0xffu << (8 * (g & 3)));
+          }
+        x.s = make_uint2(w[0], w[1]);
+      }
     };
     auto load = [&](Row& x, const uint8_t* cache, int64_t at, int t) {
       if (at < 0) {  // past the last key: zeros
@@ -505,7 +531,12 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         }
       }
       aborted = __any_sync(0xffffffffu, aborted);
-      ++ic;
+      const uint32_t item_no = ic++;
+      // Three items ahead the notes start afresh: a warp gets no further than two
+      // steps ahead of another, and the output of five items ago is read (the
+      // values stored by now waited for the products of two steps ago, and those
+      // for the output of the item before).
+      if (tid >= 256 && tid < 264) first_nan[((item_no + 3) & 7u) * 8 + tid - 256] = 0x7fffffff;
       for (int t = 0; t < n && !aborted; ++t, ++kc) {
         const int slot = kc & 1u;
         const uint32_t ph = (kc >> 1) & 1u;
@@ -522,6 +553,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         wait(&bars[kVFree + slot], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
+        take_nan(vx, (it.t0 + t) * 128 + r, first_nan + (item_no & 7u) * 8);
         store(smem + kOffV + slot * kTileBytes, vx, std::false_type{});
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -630,7 +662,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + kColO + i * 128;
     const int g = r / TQ, trow = i * TQ + r % TQ;
-    uint32_t sc = 0;  // steps of the tile
+    uint32_t sc = 0, ic = 0;  // steps of the tile, items
     const float f = fmaxf(p.scale_log2, 1.2e-38f);  // not zero: a masked -inf times it stays -inf
     Item<G> it;
     it.end = c_begin;
@@ -642,6 +674,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       const int64_t row = static_cast<int64_t>(it.c.b + it.tok0 + trow) * p.num_q_heads + it.kvh * G + g;
       const bool valid = trow < it.ntok;
       const int steps = it.steps_of(i);
+      const uint32_t item_no = ic++;
       // keys that this row sees (one that is nobody's: as the last, so that it needs no mask of its own)
       const int limit = valid ? it.pos0 + trow + 1 : it.kend();
       float m = -CUDART_INF_F, l = 0.f;
@@ -708,6 +741,8 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       if (steps > 0 && !aborted) {
         ptx::tc_fence_after();
         const float inv = l != 0.f ? p.v_scale / l : 0.f;
+        // the first key with a NaN in this lane's group (read before O is handed on)
+        const int nan_key = first_nan[(item_no & 7u) * 8 + (lane & 7)];
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {
           uint32_t v[4][16];
@@ -731,6 +766,20 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
               for (int q = 0; q < 4; ++q)
                 dst[q] = make_float4(__uint_as_float(v[h][4 * q]), __uint_as_float(v[h][4 * q + 1]),
                                      __uint_as_float(v[h][4 * q + 2]), __uint_as_float(v[h][4 * q + 3]));
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, nan_key != 0x7fffffff)) {  // groups of which the row sees a NaN, over what was stored
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            if (__shfl_sync(0xffffffffu, nan_key, k) >= limit || !valid) continue;
+            if (it.whole) {
+              uint32_t v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
+              store_out(p, row * 128 + k * 16, v, 1.f);
+            } else {
+              for (int j = 0; j < 16; ++j) L.o[prow * 128 + k * 16 + j] = __uint_as_float(0x7fffffffu);
             }
           }
         }
@@ -863,7 +912,7 @@ cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
     L.o = reinterpret_cast<float*>(p.ws + 256 + fp4_counter_bytes());
     L.ml = L.o + 2 * sms * L.rows * 128;
     const void* fn = kernel_for(G);
-    const int smem = kSmemBytes + (L.p.num_seqs + 1) * 4;
+    const int smem = kSmemBytes + (L.p.num_seqs + 64) / 64 * 256;  // few different sizes
     int per_sm = 0;
     cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
     if (e != cudaSuccess) return e;

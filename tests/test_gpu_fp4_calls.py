@@ -247,3 +247,67 @@ def test_refusals_of_the_binding(ops):
     with pytest.raises(ops.PAError):
         ops.pa_reshape_and_cache_fp4(pad, x, slots, kc, vc, bs)
     torch.cuda.synchronize()
+
+
+def test_prefill_nan_reaches_the_rows_that_see_it(ops):
+    """NaN groups of keys and of values inside the chunk and before it: rows in
+    front of the token are finite, rows behind it are NaN, in all dims for a
+    key and in the group's 16 for a value; also where an item is split."""
+    rng = np.random.default_rng(8)
+    G, hkv, bs, d = 4, 2, 16, 128
+    for start, n, at_k, at_v in ((0, 150, 40, 100), (5000, 90, 5050, 5003), (0, 300, 299, 0)):
+        tables, kc, vc = _attention_case(rng, [start + n], G, hkv, d, bs)
+
+        def spoil(c, pos, head, group):
+            c[tables[0, pos // bs], head, bs * 64 + (pos % bs) * 8 + group] = 0x7f
+
+        spoil(kc, at_k, 0, 3)
+        spoil(vc, at_v, 1, 5)
+        spoil(vc, at_v, 1, 0)
+        q = bf16(rng.standard_normal((n, G * hkv, d)))
+        ws = ops.make_prefill_workspace_fp4(1, G * hkv, hkv, d, bs, n, start + n)
+        out = torch.zeros(n, G * hkv, d, device="cuda")
+        ops.pa_prefill_fp4(out, to_device(q), _dev(kc), _dev(vc), _dev(np.array([0, n], np.int32)),
+                           _dev(np.array([start], np.int32)), _dev(tables), 0.1, hkv, bs, n, start + n, ws, KS, VS)
+        want = np.zeros(out.shape, dtype=bool)
+        rows = np.arange(start, start + n)
+        want[rows >= at_k, :G] = True
+        for g in (0, 5):
+            want[rows >= at_v, G:, 16 * g:16 * g + 16] = True
+        got = to_f64(out)
+        assert np.array_equal(np.isnan(got), want)
+        pick = [r for r in sorted({0, n - 1, n // 2}) if start + r < min(at_k, at_v)]
+        if pick:
+            ref, tol = _reference(q.f32[pick], tables, kc, vc, bs, d, 0.1, [0] * len(pick), [start + r + 1 for r in pick])
+            _check(out[torch.tensor(pick, device="cuda")], ref, tol)
+
+
+def test_many_short_items(ops):
+    """Items of a single step, several hundred for every CTA, NaN values in some."""
+    rng = np.random.default_rng(9)
+    S, G, hkv, bs, d = 3000, 1, 16, 8, 128
+    nb = 40
+    tables = rng.integers(0, nb, size=(S, 1)).astype(np.int32)
+    kc, vc = pool(rng, nb, hkv, bs, d, KS), pool(rng, nb, hkv, bs, d, VS)
+    bad, clean = [3, 17], vc.copy()
+    for b in bad:
+        vc[b, 5, bs * 64 + 6 * 8 + 2] = 0x7f  # token 6 of the block, head 5, group 2
+    n = rng.integers(1, 9, size=S)
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    q = bf16(rng.standard_normal((int(cu[-1]), G * hkv, d)))
+    ws = ops.make_prefill_workspace_fp4(S, G * hkv, hkv, d, bs, 8, 8)
+    out = torch.zeros(q.shape, device="cuda")
+    ops.pa_prefill_fp4(out, to_device(q), _dev(kc), _dev(vc), _dev(cu), _dev(np.zeros(S, np.int32)), _dev(tables), 0.1,
+                       hkv, bs, 8, 8, ws, KS, VS)
+    got = to_f64(out)
+    want = np.zeros(got.shape, dtype=bool)
+    for i in range(S):
+        if tables[i, 0] in bad and n[i] > 6:
+            want[cu[i] + 6:cu[i + 1], 5, 32:48] = True
+    assert np.array_equal(np.isnan(got), want)
+    rows = [(i, j + 1) for i in range(S) for j in range(n[i])]
+    pick = [r for r in sorted({0, len(rows) - 1, *rng.integers(0, len(rows), 200).tolist()}) if not want[r].any()]
+    ref, tol = _reference(q.f32[pick], tables, kc, clean, bs, d, 0.1, [rows[r][0] for r in pick],
+                          [rows[r][1] for r in pick])
+    keep = [k for k, r in enumerate(pick) if tables[rows[r][0], 0] not in bad]
+    _check(out[torch.tensor([pick[k] for k in keep], device="cuda")], ref[keep], tol[keep])
