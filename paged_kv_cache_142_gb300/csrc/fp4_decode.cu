@@ -25,10 +25,14 @@
 //  * every warp streams its own 32-token units, K and V, through a ring of its
 //    own with cp.async, the table entries of the next unit loaded one unit
 //    ahead.  (Bulk copies of the pages' tiles were right too, but the hardware
-//    takes them lane by lane: 25 instructions each, four a unit.)  Blocks of 16
-//    and of 32 and more tokens have kernels with their layout as constants:
-//    700 instructions a unit instead of 900.  Warps meet only at the end of a
-//    (sequence, kv head), to add up their sums;
+//    takes them lane by lane: 25 instructions each, four a unit.)  Blocks of 8 (from
+//    128 dims on), of 16 and of 32 and more tokens have kernels with their layout
+//    as constants: 700 instructions a unit instead of 900 (32 sequences of 4096
+//    tokens in blocks of 8: 55.7 us, 69 without; in blocks of 4, which have none,
+//    84).  Warps meet only at the end of a (sequence, kv head), to add up their
+//    sums.  Units of 64 tokens, which halve what a unit costs besides its tokens,
+//    gave 70.3 / 76.8 / 65.0 us against 65.2 / 72.2 / 69.7 (the three sizes below):
+//    too few units for the warps of a short sequence;
 //  * the work is cut into equal runs of units, one for each CTA, across the
 //    borders of heads and sequences, counting what a head's start and end cost
 //    (kLead).  A (sequence, kv head) that several CTAs share is joined by the
@@ -158,8 +162,8 @@ struct Cursor {
 }  // namespace fp4_decode_detail
 
 // D: head_dim; NT: columns of heads in eights (G <= 8 * NT); EL: log2 of the
-// tokens of a piece (blocks of 16 tokens: 4, of 32 and more: 5), or -1 for
-// blocks of fewer than 16 tokens, whose layout is then read from L
+// tokens of a piece (blocks of 8 tokens: 3, of 16: 4, of 32 and more: 5), or -1
+// for smaller blocks, whose layout is then read from L
 template <int D, int NT, int EL>
 __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT == 1) ? 4 : 2)
     fp4_decode_kernel(const __grid_constant__ fp4_decode_detail::Launch L) {
@@ -320,12 +324,12 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       const uint32_t cache_head = L.per_cache_head == 1 ? ic.head : ic.head / L.per_cache_head;
       // this lane's piece's tile (fewer than 2^31 of them in a pool)
       const uint32_t mine = static_cast<uint32_t>(phys) * L.cache_heads + cache_head;
-      if (EL >= 0) {
-        // 16-byte chunks: kCodes a lane of a unit's codes, piece after piece,
-        // then one of its scales in the first kScales lanes
-        constexpr int kCodes = kUnit * (D / 2) / 512, kScales = kUnit * (D / 16) / 16;
-        constexpr int kPieces = EL == 4 ? 2 : 1, kPerPiece = kCodes / kPieces;
-        constexpr int kEff = kUnit / kPieces, kPieceBytes = kEff * (D / 2 + D / 16);
+      if constexpr (EL >= 0) {
+        // 16-byte chunks: kPerPiece a lane of a piece's codes, then one of the
+        // unit's scales in the first kScales lanes
+        constexpr int kEff = 1 << EL, kPieces = kUnit / kEff, kPieceBytes = kEff * (D / 2 + D / 16);
+        constexpr int kPerPiece = kEff * (D / 2) / 512, kScales = kUnit * (D / 16) / 16;
+        static_assert(kPerPiece > 0 && kPerPiece * 512 == kEff * (D / 2), "whole rounds of the lanes");
         const int row = EL == 5 ? (ic.st * kUnit) & (bs - 1) : 0;  // of the piece in its tile
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
         }
         // a piece's scale chunks: lanes c of kScales / kPieces
         constexpr int kSc = kScales / kPieces;
-        const int j = kPieces == 1 ? 0 : (lane / kSc) & 1;
+        const int j = (lane / kSc) & (kPieces - 1);
         const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, mine, j)) * tile_bytes + bs * (D / 2) +
                             row * (D / 16) - j * (kSc * 16);
         if (lane < kScales && j < nv) {
@@ -826,6 +830,8 @@ template <int D, int NT>
 const void* kernel_of(int eff_log) {
   if (eff_log == 5) return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, 5>);
   if (eff_log == 4) return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, 4>);
+  if constexpr (D >= 128)  // a round of the lanes copies 512 bytes: 8 rows of codes
+    if (eff_log == 3) return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, 3>);
   return reinterpret_cast<const void*>(&fp4_decode_kernel<D, NT, -1>);
 }
 const void* kernel_for(int head_dim, int group, int eff_log) {
