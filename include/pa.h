@@ -452,7 +452,8 @@ pa_status pa_gather_cache_fp4(void* key, void* value, pa_dtype dst_dtype,
  * length 0, workspace rules (256-byte aligned, zero-filled before its first
  * use, pa_workspace_error for table entries outside the pool and lengths
  * outside [0, max_context_len]) as for pa_decode.  num_q_heads / num_kv_heads
- * in {1, 2, 4, 8, 16}. */
+ * in {1, 2, 4, 8, 16}; max_context_len at most 2^30 (PA_ERR_UNSUPPORTED), also
+ * in the prefill. */
 size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                     int32_t head_dim, int32_t block_size,
                                     int32_t max_context_len);

@@ -42,6 +42,9 @@ pa_status check_rows(const void* key, const void* value, pa_dtype dtype, int32_t
   return PA_OK;
 }
 
+// Positions, and what the kernels round up from them, fit 32 bits.
+constexpr int32_t kMaxContext = 1 << 30;
+
 bool group_ok(int32_t num_q_heads, int32_t num_kv_heads) {
   const int g = num_q_heads / num_kv_heads;
   return g == 1 || g == 2 || g == 4 || g == 8 || g == 16;
@@ -88,7 +91,7 @@ size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32
                                     int32_t block_size, int32_t max_context_len) {
   if (num_seqs < 0 || num_q_heads <= 0 || max_context_len < 0 ||
       check_pool(1, block_size, num_kv_heads, head_dim) != PA_OK || num_q_heads % num_kv_heads ||
-      !group_ok(num_q_heads, num_kv_heads))
+      !group_ok(num_q_heads, num_kv_heads) || max_context_len > kMaxContext)
     return 0;
   return pa::fp4_decode_workspace(num_q_heads, num_kv_heads, head_dim);
 }
@@ -102,9 +105,10 @@ pa_status pa_decode_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t nu
   if (st != PA_OK) return st;
   if (!is_float(out_dtype) || !std::isfinite(scale) || !global_scale_ok(k_scale) || !global_scale_ok(v_scale) ||
       num_seqs < 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || max_blocks_per_seq <= 0 ||
-      max_context_len < 0 || static_cast<int64_t>(max_blocks_per_seq) * block_size < max_context_len)
+      max_context_len < 0 || static_cast<int64_t>(max_blocks_per_seq) * block_size < max_context_len ||
+      !std::isfinite(scale * 1.4426950408889634f * k_scale))
     return PA_ERR_INVALID_ARG;
-  if (!group_ok(num_q_heads, num_kv_heads)) return PA_ERR_UNSUPPORTED;
+  if (!group_ok(num_q_heads, num_kv_heads) || max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
@@ -139,7 +143,7 @@ size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int3
                                      int32_t block_size, int32_t max_q_len, int32_t max_context_len) {
   if (num_seqs < 0 || num_q_heads <= 0 || max_q_len < 0 || max_context_len < 0 ||
       check_pool(1, block_size, num_kv_heads, head_dim) != PA_OK || num_q_heads % num_kv_heads || head_dim != 128 ||
-      !group_ok(num_q_heads, num_kv_heads))
+      !group_ok(num_q_heads, num_kv_heads) || max_context_len > kMaxContext)
     return 0;
   return pa::fp4_prefill_workspace(num_seqs, num_q_heads, num_kv_heads, max_q_len, max_context_len);
 }
@@ -155,9 +159,11 @@ pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t n
   if (!is_float(out_dtype) || !(scale > 0.f) || !std::isfinite(scale) || !global_scale_ok(k_scale) ||
       !global_scale_ok(v_scale) || num_tokens < 0 || num_seqs < 0 || max_q_len < 0 || num_q_heads <= 0 ||
       num_q_heads % num_kv_heads || max_blocks_per_seq <= 0 || max_context_len < 0 ||
-      static_cast<int64_t>(max_blocks_per_seq) * block_size < max_context_len)
+      static_cast<int64_t>(max_blocks_per_seq) * block_size < max_context_len ||
+      !std::isfinite(scale * 1.4426950408889634f * k_scale))
     return PA_ERR_INVALID_ARG;
-  if (head_dim != 128 || !group_ok(num_q_heads, num_kv_heads)) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 128 || !group_ok(num_q_heads, num_kv_heads) || max_context_len > kMaxContext)
+    return PA_ERR_UNSUPPORTED;
   if (num_tokens == 0 || num_seqs == 0 || max_q_len == 0) return PA_OK;
   if (!out || !q || !cu_q || !q_start || !k_cache || !v_cache || !block_tables) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 32) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(cu_q, 4) ||

@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   };
   const int b = p.cu_keep[seq], n = p.cu_keep[seq + 1] - b;
   const int dst0 = p.dst_start[seq];
-  const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+  // positions are 32-bit numbers
+  const int64_t table_tokens = min(static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size, int64_t(0x7fffffff));
   const bool report = p.status && blockIdx.y == 0 && blockIdx.z == 0;
   if (n == 0) return;
   if (b < 0 || n < 0 || n > p.max_keep || dst0 < 0 || dst0 + static_cast<int64_t>(n) > table_tokens) {

@@ -109,11 +109,11 @@ struct Chunk {
     // sum of ceil((a + t) / per) over t = 1 .. j, with q0 rounded up to pairs a
     constexpr int per = S > 128 ? 1 : 128 / S;
     const int a = (q0 + S - 1) / S;
-    auto f = [](int x) {
-      const int k = x / per, r = x % per;
+    auto f = [](int64_t x) {  // passes 2^31 where the difference does not
+      const int64_t k = x / per, r = x % per;
       return per * (k * (k + 1) / 2) + r * (k + 1);
     };
-    return j * kLead + f(a + j) - f(a);
+    return static_cast<int>(j * kLead + f(static_cast<int64_t>(a) + j) - f(a));
   }
   __device__ __forceinline__ int places() const {  // of one head
     if (n <= 0) return 0;

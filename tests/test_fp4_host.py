@@ -88,6 +88,8 @@ def test_decode_refusals(lib):
     assert call(q=P + 2) == BAD and call(out=P + 4) == BAD
     assert call(ws=None) == WS and call(ws=P + 4) == WS and call(wb=16) == WS
     assert call(n=0, out=None, ws=None) == L.PA_OK
+    assert call(m=1 << 27, ml=(1 << 30) + 1) == UNSUP    # positions are 32-bit numbers
+    assert call(scale=1e38, ks=2.0 ** 32) == BAD         # the product is not finite
     size = lib.pa_decode_fp4_workspace_size
     assert size(2, 8, 2, 128, 16, 64) > 0
     assert size(2, 6, 2, 128, 16, 64) == 0 and size(2, 8, 2, 96, 16, 64) == 0 and size(-1, 8, 2, 128, 16, 64) == 0
@@ -107,6 +109,7 @@ def test_prefill_refusals(lib):
     assert call(out=P + 16) == BAD and call(q=P + 8) == BAD and call(status=P + 2) == BAD
     assert call(ws=None) == WS and call(wb=8) == WS and call(ws=P + 8) == WS
     assert call(t=0, q=None, ws=None) == L.PA_OK and call(mq=0, q=None) == L.PA_OK
+    assert call(m=1 << 27, ml=(1 << 30) + 1) == UNSUP and call(scale=1e38, ks=2.0 ** 32) == BAD
     assert lib.pa_prefill_fp4_workspace_size(2, 8, 2, 64, 16, 5, 64) == 0
 
 

@@ -311,3 +311,44 @@ def test_many_short_items(ops):
                           [rows[r][1] for r in pick])
     keep = [k for k, r in enumerate(pick) if tables[rows[r][0], 0] not in bad]
     _check(out[torch.tensor([pick[k] for k in keep], device="cuda")], ref[keep], tol[keep])
+
+
+def test_contexts_of_millions_of_tokens(ops):
+    """Positions around 6 million (their pages repeat, so a key's weight is the
+    number of times that a row sees it): decode, and a chunk of several tiles."""
+    rng = np.random.default_rng(8)
+    nb, bs, d, G, n, start, scale = 64, 256, 128, 16, 40, 6_000_037, 0.1
+    period = nb * bs
+    kc, vc = pool(rng, nb, 1, bs, d, KS), pool(rng, nb, 1, bs, d, VS)
+    order = rng.permutation(nb).astype(np.int32)
+    end = start + n
+    m = -(-end // bs)
+    tables = np.resize(order, (1, m)).astype(np.int32)
+    K = oracle.gather_sequence(fp4.values(kc, bs, d, KS), order, period)[:, 0]
+    V = oracle.gather_sequence(fp4.values(vc, bs, d, VS), order, period)[:, 0]
+
+    def reference(q, pos):
+        s = scale * (q.astype(np.float64) @ K.T)
+        count = (pos - np.arange(period)) // period + 1
+        w = count * np.exp(s - s.max(axis=1, keepdims=True))
+        return (w / w.sum(axis=1, keepdims=True)) @ V
+
+    # attention_bound counts one period's keys.  An accumulator takes those of
+    # a CTA's share: at least 100 CTAs share 3 tiles' rows of `end` keys.
+    more = 3 * end / 100 * 2.0 ** -23 * float(np.abs(V).max())
+
+    def check(out, q, pos):
+        tol = attention_bound(q.astype(np.float64), K[:, None], V[:, None], scale) + more
+        _check(out, reference(q, pos), tol[:, None])
+
+    q = bf16(rng.standard_normal((n, G, d)))
+    ws = ops.make_prefill_workspace_fp4(1, G, 1, d, bs, n, end)
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.pa_prefill_fp4(out, to_device(q), _dev(kc), _dev(vc), _dev(np.array([0, n], np.int32)),
+                       _dev(np.array([start], np.int32)), _dev(tables), scale, 1, bs, n, end, ws, KS, VS, status=st)
+    assert int(st.item()) == 0
+    for t in (0, 15, 16, 31, 32, n - 1):
+        check(out[t], q.f32[t], start + t)
+    got = _decode(ops, bf16(q.f32[:1]), tables, [end], _dev(kc), _dev(vc), bs, scale, 1)
+    check(got[0], q.f32[0], end - 1)
