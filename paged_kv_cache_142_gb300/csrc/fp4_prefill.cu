@@ -39,13 +39,13 @@
 // them the exponential unit's), P.V and Q.K^T (550 each), and 900 of barriers and
 // tensor-memory waits, 3150 a step in all; the other tile's products fill its
 // gaps, 2250 of the 3150 clocks.  16 prompts of 2048 tokens, 32 q / 8 kv heads:
-// 530 us, 1040 TFLOP/s, 53% of the measured bf16 rate; a chunk of 512 tokens over
-// 16000: 1210 TFLOP/s.  What it took: one elected lane of a uniform warp issues
+// 548 us, 1003 TFLOP/s, 52% of the measured bf16 rate; chunks of 200 to 512 tokens
+// over 8000 to 16000: 179 us, 1196 TFLOP/s.  What it took: one elected lane of a uniform warp issues
 // unrolled products (a rolled loop of one lane: 130 clocks an instruction, 987 us
 // instead of 730), one pass over the scores on the reference as it is, a warp for
 // each tile's products taking turns (720 to 692 us), equal runs and TMA queries
-// (678), items walked instead of searched and whole-sector stores (592), and
-// kLead of 2 (530).
+// (678), items walked instead of searched and whole-sector stores (592), kLead
+// of 2 (530), and NaN values kept from the rows that do not see them (548).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
