@@ -15,11 +15,12 @@
 // registers allow (four pieces a thread, 512 threads for long lists), its
 // places serve several planes, the next plane's rows load before this one's
 // are written, and few kept tokens (accepted drafts) take all heads in one CTA.
-// 64 sequences x up to 8 tokens in 32 layers (81 MB): 24.7 us; 16 sequences x
+// 64 sequences x up to 8 tokens in 32 layers (81 MB): 23.4 us; 16 sequences x
 // 2000 of 4096 tokens in 4 bits (75 MB): 33 us (one piece a thread and a CTA a
 // plane and head: 49 and 104 us).
 #include "decode.cuh"
 #include "fp4.cuh"
+#include "ptx.cuh"
 
 namespace pa {
 namespace {
@@ -52,6 +53,8 @@ __device__ __forceinline__ void store_piece(const Piece& v, unsigned char* p, in
 template <bool MANY>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     compact_kernel(const CompactParams p, int heads_per_cta, int units, int planes) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int seq = blockIdx.x;
   const int plane0 = blockIdx.z * planes, plane1 = min(2 * p.num_layers, plane0 + planes);
   auto cache_of = [&](int plane) {
@@ -167,9 +170,8 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   while (planes < 2 * p.num_layers && per_plane * ((2 * p.num_layers + planes - 1) / planes) > room) ++planes;
   const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(groups),
                   static_cast<unsigned>((2 * p.num_layers + planes - 1) / planes));
-  if (planes > 1) compact_kernel<true><<<grid, threads, 0, stream>>>(p, heads, units, planes);
-  else compact_kernel<false><<<grid, threads, 0, stream>>>(p, heads, units, 1);
-  return cudaGetLastError();
+  return launch_early(planes > 1 ? compact_kernel<true> : compact_kernel<false>, grid, threads, stream, p, heads, units,
+                      planes);
 }
 
 }  // namespace pa

@@ -45,6 +45,22 @@ struct Fp4AttnParams {
   unsigned char* ws;
 };
 
+// Launches a kernel whose CTAs may start while the one before still drains: it
+// calls griddep_wait before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 cudaError_t launch_fp4_append(const void* key, const void* value, bool src_bf16, int32_t num_tokens,
                               const int64_t* slots, void* k_cache, void* v_cache, int32_t num_blocks,
                               int32_t block_size, int32_t num_kv_heads, int32_t head_dim, float k_scale,

@@ -352,3 +352,53 @@ def test_contexts_of_millions_of_tokens(ops):
         check(out[t], q.f32[t], start + t)
     got = _decode(ops, bf16(q.f32[:1]), tables, [end], _dev(kc), _dev(vc), bs, scale, 1)
     check(got[0], q.f32[0], end - 1)
+
+
+def test_calls_behind_one_another(ops):
+    """Each call of a chain reads what the one before it writes, without a
+    synchronisation between them; eager, then captured and replayed."""
+    rng = np.random.default_rng(9)
+    S, n, hkv, bs, d = 8, 600, 4, 16, 128
+    m = -(-n // bs)
+    tables = rng.permutation(S * m).reshape(S, m).astype(np.int32)
+    keep = [np.sort(rng.permutation(n)[:n // 2]) for _ in range(S)]
+    t = np.arange(n)
+    slots = np.concatenate([tables[i][t // bs].astype(np.int64) * bs + t % bs for i in range(S)])
+    kept = np.concatenate([slots[i * n:(i + 1) * n][:n // 2] for i in range(S)])
+    rounds = 6
+    keys = [bf16(rng.standard_normal((S * n, hkv, d)) * 2.0 ** r) for r in range(rounds)]
+    dev = [to_device(x) for x in keys]
+    kc, vc = (ops.make_cache_fp4(S * m, hkv, bs, d) for _ in range(2))
+    outs = [[torch.zeros((S * n // 2, hkv, d), device="cuda") for _ in range(2)] for _ in range(rounds)]
+    args = (_dev(tables), torch.zeros(S, dtype=torch.int32, device="cuda"),
+            _dev(np.concatenate(keep).astype(np.int32)), _dev(np.arange(S + 1, dtype=np.int32) * (n // 2)))
+    slots_dev, kept_dev = _dev(slots), _dev(kept)
+
+    def chain():
+        for r in range(rounds):
+            ops.pa_reshape_and_cache_fp4(dev[r], dev[-1 - r], slots_dev, kc, vc, bs)
+            ops.pa_compact_tokens(kc, vc, *args, n // 2, bs, d)
+            ops.pa_gather_cache_fp4(*outs[r], kept_dev, kc, vc, bs)
+
+    moved = np.concatenate([i * n + keep[i] for i in range(S)])
+
+    def check():
+        for r in range(rounds):
+            for out, x in zip(outs[r], (keys[r], keys[-1 - r])):
+                codes, scales = fp4.quantise(x.f32[moved], 1.0)
+                assert np.array_equal(to_f64(out), fp4.dequantise(codes, scales, 1.0))
+
+    chain()
+    check()
+    for pair in outs:
+        for out in pair:
+            out.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        chain()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    check()
