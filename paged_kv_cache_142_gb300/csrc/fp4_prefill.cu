@@ -39,13 +39,16 @@
 // them the exponential unit's), P.V and Q.K^T (550 each), and 900 of barriers and
 // tensor-memory waits, 3150 a step in all; the other tile's products fill its
 // gaps, 2250 of the 3150 clocks.  16 prompts of 2048 tokens, 32 q / 8 kv heads:
-// 548 us, 1003 TFLOP/s, 52% of the measured bf16 rate; chunks of 200 to 512 tokens
-// over 8000 to 16000: 179 us, 1196 TFLOP/s.  What it took: one elected lane of a uniform warp issues
+// 519 us, 1060 TFLOP/s, 55% of the measured bf16 rate; chunks of 200 to 512 tokens
+// over 8000 to 16000: 177 us, 1208 TFLOP/s.  What it took: one elected lane of a uniform warp issues
 // unrolled products (a rolled loop of one lane: 130 clocks an instruction, 987 us
 // instead of 730), one pass over the scores on the reference as it is, a warp for
 // each tile's products taking turns (720 to 692 us), equal runs and TMA queries
 // (678), items walked instead of searched and whole-sector stores (592), kLead
-// of 2 (530), and NaN values kept from the rows that do not see them (548).
+// of 2 (530), NaN values kept from the rows that do not see them (548), and the
+// search for the first item out of line (519).  P.V in two halves, one beside the
+// other half's softmax, took 612 us, and one copy of the probabilities' code for
+// first and second tries 526.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -109,11 +112,12 @@ struct Chunk {
     // sum of ceil((a + t) / per) over t = 1 .. j, with q0 rounded up to pairs a
     constexpr int per = S > 128 ? 1 : 128 / S;
     const int a = (q0 + S - 1) / S;
-    auto f = [](int64_t x) {  // passes 2^31 where the difference does not
-      const int64_t k = x / per, r = x % per;
-      return per * (k * (k + 1) / 2) + r * (k + 1);
+    // (modulo 2^32: the sums may pass it where their difference does not)
+    auto f = [](uint32_t x) {
+      const uint32_t k = x / per, r = x % per;
+      return per * ((k & 1) ? k * ((k + 1) / 2) : k / 2 * (k + 1)) + r * (k + 1);
     };
-    return static_cast<int>(j * kLead + f(static_cast<int64_t>(a) + j) - f(a));
+    return static_cast<int>(static_cast<uint32_t>(j * kLead) + f(a + j) - f(a));
   }
   __device__ __forceinline__ int places() const {  // of one head
     if (n <= 0) return 0;
@@ -129,6 +133,31 @@ __device__ __forceinline__ Chunk<G> chunk_of(const Launch& L, int seq) {
   c.n = L.p.cu_q[seq + 1] - c.b;
   c.q0 = L.p.q_start[seq];
   return c;
+}
+
+// The item at a place: its sequence, pair, kv head and first place.  One copy
+// for the three kinds of warps, once each: inlined in each of them it pushed
+// code that runs out of the instruction cache (16 x 2048 prompts 549 us, so 519).
+template <int G>
+__device__ __noinline__ int4 item_at(const Launch& L, const int* prefix, int u) {
+  const int hkv = L.p.num_kv_heads;
+  int lo = 0, hi = L.p.num_seqs - 1;
+  while (lo < hi) {  // the last sequence that starts at or before it
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const Chunk<G> c = chunk_of<G>(L, lo);
+  int r = u - prefix[lo];
+  int a = 0, b = c.pairs() - 1;
+  while (a < b) {
+    const int mid = (a + b + 1) >> 1;
+    if (hkv * c.before(mid) <= r) a = mid;
+    else b = mid - 1;
+  }
+  r -= hkv * c.before(a);
+  const int places = kLead + c.tiles(a);
+  return make_int4(lo, a, r / places, u - r % places);
 }
 
 // An item and this CTA's part of it.
@@ -163,27 +192,9 @@ struct Item {
   }
   // the item at place c_begin
   __device__ __forceinline__ void find(const Launch& L, const int* prefix, int c_begin, int c_end) {
-    const int hkv = L.p.num_kv_heads;
-    int lo = 0, hi = L.p.num_seqs - 1;
-    while (lo < hi) {  // the last sequence that starts at or before it
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= c_begin) lo = mid;
-      else hi = mid - 1;
-    }
-    seq = lo;
-    c = chunk_of<G>(L, lo);
-    int r = c_begin - prefix[lo];
-    int a = 0, b = c.pairs() - 1;
-    while (a < b) {
-      const int mid = (a + b + 1) >> 1;
-      if (hkv * c.before(mid) <= r) a = mid;
-      else b = mid - 1;
-    }
-    pair = a;
-    r -= hkv * c.before(a);
-    const int places = kLead + c.tiles(a);
-    kvh = r / places;
-    start = c_begin - (r - kvh * places);
+    const int4 x = item_at<G>(L, prefix, c_begin);
+    seq = x.x, pair = x.y, kvh = x.z, start = x.w;
+    c = chunk_of<G>(L, seq);
     derive(c_begin, c_end);
   }
   // the next one (there is one before c_end)
