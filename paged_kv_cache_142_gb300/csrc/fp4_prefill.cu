@@ -877,15 +877,25 @@ const void* kernel_for(int group) {
   }
 }
 
-int pairs_of(int group, int max_q_len) { return (max_q_len + 256 / group - 1) / (256 / group); }
-int rows_of(int group, int max_q_len) { return max_q_len * group < 256 ? max_q_len * group : 256; }
+// A chunk is no longer than the context that it ends in, however loose the
+// caller's bound (and one token at least, so that a launch has a CTA to report
+// what it refuses).
+int longest_of(int max_q_len, int max_context_len) {
+  const int n = max_q_len < max_context_len ? max_q_len : max_context_len;
+  return n > 1 ? n : 1;
+}
+// Of chunks of up to n tokens: a chunk's tile pairs, and the rows of a pair (a
+// pair has 256 / group tokens).  Neither forms a product that could pass 32 bits.
+int64_t pairs_of(int group, int n) { return (static_cast<int64_t>(n) + 256 / group - 1) / (256 / group); }
+int rows_of(int group, int n) { return n < 256 / group ? n * group : 256; }
 
 // Sequences of one launch: their places fit an int.  0: not even one's do.
-int seqs_of(int num_seqs, int num_kv_heads, int group, int max_q_len, int max_context_len) {
+int seqs_of(int num_seqs, int num_kv_heads, int group, int longest, int max_context_len) {
   using namespace fp4_prefill_detail;
-  const int64_t places = (kLead + (static_cast<int64_t>(max_context_len) + 127) / 128) * pairs_of(group, max_q_len) *
-                         num_kv_heads;
-  const int64_t fit = ((int64_t(1) << 31) - 1) / (places > 0 ? places : 1);
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+  // of one head: below 2^50, as a context has at most 2^30 tokens
+  const int64_t places = (kLead + (static_cast<int64_t>(max_context_len) + 127) / 128) * pairs_of(group, longest);
+  const int64_t fit = kMost / places / num_kv_heads;
   const int64_t most = fit < kMaxSeqs ? fit : kMaxSeqs;
   return static_cast<int>(num_seqs < most ? num_seqs : most);
 }
@@ -894,16 +904,17 @@ int seqs_of(int num_seqs, int num_kv_heads, int group, int max_q_len, int max_co
 
 size_t fp4_prefill_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int max_q_len, int max_context_len) {
   const int G = num_q_heads / num_kv_heads;
-  const int seqs = seqs_of(num_seqs, num_kv_heads, G, max_q_len, max_context_len);
-  if (num_seqs > 0 && max_q_len > 0 && seqs == 0) return 0;
+  const int longest = longest_of(max_q_len, max_context_len);
+  if (num_seqs > 0 && max_q_len > 0 && seqs_of(num_seqs, num_kv_heads, G, longest, max_context_len) == 0) return 0;
   // header | counters | parts: the first two lie where they lie for every shape
-  return static_cast<size_t>(256 + fp4_counter_bytes() + 2 * device_sm_count() * rows_of(G, max_q_len) * (128 + 2) * 4);
+  return static_cast<size_t>(256 + fp4_counter_bytes() + 2 * device_sm_count() * rows_of(G, longest) * (128 + 2) * 4);
 }
 
 cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
   using namespace fp4_prefill_detail;
   const int G = p.num_q_heads / p.num_kv_heads;
-  const int seqs = seqs_of(p.num_seqs, p.num_kv_heads, G, p.max_q_len, p.max_context_len);
+  const int longest = longest_of(p.max_q_len, p.max_context_len);
+  const int seqs = seqs_of(p.num_seqs, p.num_kv_heads, G, longest, p.max_context_len);
   const int64_t sms = device_sm_count();
   CUtensorMap tm_q;
   if (!encode_q_tokens(&tm_q, p.q, static_cast<uint64_t>(p.num_tokens), static_cast<uint64_t>(p.num_q_heads) * 128,
@@ -916,7 +927,7 @@ cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
     L.p.cu_q += seq0;
     L.p.q_start += seq0;
     L.p.block_tables += static_cast<int64_t>(seq0) * p.max_blocks_per_seq;
-    L.rows = rows_of(G, p.max_q_len);
+    L.rows = rows_of(G, longest);
     L.tile_bytes = static_cast<uint32_t>(fp4_tile_bytes(p.block_size, 128));
     L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
     L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
@@ -928,7 +939,7 @@ cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
     cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
     if (e != cudaSuccess) return e;
     // every SM, while an item is not cut into too many parts to add up
-    const int64_t items = static_cast<int64_t>(L.p.num_seqs) * pairs_of(G, p.max_q_len) * p.num_kv_heads;
+    const int64_t items = static_cast<int64_t>(L.p.num_seqs) * pairs_of(G, longest) * p.num_kv_heads;
     const int64_t ctas = items * kMostParts < sms ? items * kMostParts : sms;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));

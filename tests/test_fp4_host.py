@@ -150,6 +150,21 @@ def test_binding_refuses_wrong_tensors(ops):
         ops.fp4_tile_bytes(16, 100)
 
 
+@pytest.mark.parametrize("group", [1, 2, 4, 8, 16])
+def test_prefill_workspace_never_shrinks_as_the_bound_grows(lib, group):
+    """max_q_len is a bound, however loose: every size up to the largest int
+    has room for the parts of the longest chunk that the context allows."""
+    for hkv in (1, 8):
+        for ctx in (1, 100, 4096, 1 << 20):
+            bounds = sorted({1, 2, 15, 16, 17, 255, 256, 257, *(1 << e for e in range(9, 31)), ctx, (1 << 31) - 1})
+            # a sequence's places, (2 + key tiles) for each tile pair and head, are numbered in 31 bits
+            fits = [mq for mq in bounds if (2 + -(-ctx // 128)) * -(-min(mq, ctx) // (256 // group)) * hkv < 1 << 31]
+            size = {mq: lib.pa_prefill_fp4_workspace_size(1, group * hkv, hkv, 128, 16, mq, ctx) for mq in bounds}
+            assert all(0 < size[a] <= size[b] < 1 << 40 for a, b in zip(fits, fits[1:])), (hkv, ctx, size)
+            assert all(size[mq] == 0 for mq in bounds if mq not in fits)
+            assert size[(1 << 31) - 1] == size[ctx]
+
+
 # ---------------------------------------------------------------------------
 # allocator
 # ---------------------------------------------------------------------------

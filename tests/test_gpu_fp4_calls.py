@@ -402,3 +402,28 @@ def test_calls_behind_one_another(ops):
         graph.replay()
     torch.cuda.synchronize()
     check()
+
+
+@pytest.mark.parametrize("G,hkv,max_q", [(4, 8, 1 << 30), (16, 1, 1 << 28), (8, 2, (1 << 31) - 1), (1, 3, 1 << 29)])
+def test_prefill_with_a_loose_bound_of_the_chunks(ops, G, hkv, max_q):
+    """max_q_len far above every chunk: the results of the tight bound, from a
+    workspace of the size asked for, nothing behind it written."""
+    rng = np.random.default_rng(G)
+    chunks, bs, d = [(3000, 70), (0, 300), (0, 0), (900, 1)], 16, 128
+    lens = [s + c for s, c in chunks]
+    tables, kc, vc = _attention_case(rng, lens, G, hkv, d, bs)
+    n = [c for _, c in chunks]
+    q = to_device(bf16(rng.standard_normal((sum(n), G * hkv, d))))
+    cu, start = _dev(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)), _dev(np.array([s for s, _ in chunks], np.int32))
+    kd, vd, td = _dev(kc), _dev(vc), _dev(tables)
+    outs = []
+    for mq in (max(n), max_q):
+        need = ops.make_prefill_workspace_fp4(4, G * hkv, hkv, d, bs, mq, max(lens)).numel()
+        room = torch.full((need + (1 << 22),), 0x5a, dtype=torch.uint8, device="cuda")
+        room[:need] = 0
+        out = torch.full(q.shape, float("nan"), device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ops.pa_prefill_fp4(out, q, kd, vd, cu, start, td, 0.1, hkv, bs, mq, max(lens), room[:need], KS, VS, status=st)
+        assert int(st.item()) == 0 and bool((room[need:] == 0x5a).all())
+        outs.append(out)
+    assert bool(torch.isfinite(outs[0]).all()) and torch.equal(outs[0], outs[1])
