@@ -543,10 +543,13 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       }
       aborted = __any_sync(0xffffffffu, aborted);
       const uint32_t item_no = ic++;
-      // Three items ahead the notes start afresh: a warp gets no further than two
-      // steps ahead of another, and the output of five items ago is read (the
-      // values stored by now waited for the products of two steps ago, and those
-      // for the output of the item before).
+      // Three items ahead the notes start afresh, in the place of those of five
+      // items ago.  A warp gets no further than two steps, so two items, ahead of
+      // another: nobody writes them yet.  And both tiles have read the old ones:
+      // the last value stored waited until both product warps had released the
+      // one of two steps before, of item J >= item_no - 3, and a product warp
+      // begins J only when its tile's outputs of the items before J, notes
+      // included, are read (kOFree, whether the tile has steps in J or not).
       if (tid >= 256 && tid < 264) first_nan[((item_no + 3) & 7u) * 8 + tid - 256] = 0x7fffffff;
       for (int t = 0; t < n && !aborted; ++t, ++kc) {
         const int slot = kc & 1u;
@@ -626,7 +629,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         if (lane == 0 && do_pv) bar = &bars[kPFull + i], parity = pc & 1u;
         if (lane == 1 && t >= 0) bar = &bars[kVFull + vslot], parity = ((kc + t) >> 1) & 1u;
         if (lane == 2 && next) bar = &bars[kKFull + kslot], parity = ((kc + t + 1) >> 1) & 1u;
-        if (lane == 3 && do_pv && t == 0) bar = &bars[kOFree + i], parity = (oc & 1u) ^ 1u;
+        if (lane == 3 && t == 0) bar = &bars[kOFree + i], parity = (oc & 1u) ^ 1u;  // also where P.V is none: see the notes
         if (lane == 4 && t == -1) bar = &bars[kQFull], parity = ic & 1u;
         if (bar) wait(bar, parity, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       if (steps > 0 && !aborted) {
         ptx::tc_fence_after();
         const float inv = l != 0.f ? p.v_scale / l : 0.f;
-        // the first key with a NaN in this lane's group (read before O is handed on)
+        // the first key with a NaN in this lane's group (read before O is handed on, which frees the notes)
         const int nan_key = first_nan[(item_no & 7u) * 8 + (lane & 7)];
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {

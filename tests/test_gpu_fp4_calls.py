@@ -427,3 +427,45 @@ def test_prefill_with_a_loose_bound_of_the_chunks(ops, G, hkv, max_q):
         assert int(st.item()) == 0 and bool((room[need:] == 0x5a).all())
         outs.append(out)
     assert bool(torch.isfinite(outs[0]).all()) and torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("G,hkv,S", [(16, 1, 4000), (8, 3, 3000), (16, 4, 2500)])
+def test_items_of_two_tiles_between_items_of_one(ops, G, hkv, S):
+    """Chunks that fill two tiles, with NaN values in some, in front of runs of
+    chunks that fill one: the notes of the former reach their rows and no
+    others, call after call."""
+    rng = np.random.default_rng(10 * G + hkv)
+    bs, d, nb, tile = 8, 128, 48, 128 // G
+    n = rng.integers(1, tile + 1, size=S)
+    two = rng.random(S) < 0.15
+    n[two] = rng.integers(tile + 1, 2 * tile + 1, size=int(two.sum()))
+    m = 2 * tile // bs
+    tables = rng.integers(0, nb, size=(S, m)).astype(np.int32)
+    kc, vc = pool(rng, nb, hkv, bs, d, KS), pool(rng, nb, hkv, bs, d, VS)
+    bad = [3, 17, 30, 31]
+    spoilt = {b: (int(rng.integers(0, bs)), int(rng.integers(0, hkv)), int(rng.integers(0, 8))) for b in bad}
+    for b, (tok, head, group) in spoilt.items():
+        vc[b, head, bs * 64 + tok * 8 + group] = 0x7f
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    q = bf16(rng.standard_normal((int(cu[-1]), G * hkv, d)))
+    want = np.zeros(q.shape, dtype=bool)
+    for i in range(S):
+        for j in range(m):
+            if int(tables[i, j]) in spoilt:
+                tok, head, group = spoilt[int(tables[i, j])]
+                want[cu[i] + j * bs + tok:cu[i + 1], head * G:(head + 1) * G, 16 * group:16 * group + 16] = True
+    rows = [(i, j + 1) for i in range(S) for j in range(n[i])]
+    pick = [r for r in sorted({0, len(rows) - 1, *rng.integers(0, len(rows), 150).tolist()}) if not want[r].any()
+            and not set(tables[rows[r][0]].tolist()) & set(bad)]
+    ref, tol = _reference(q.f32[pick], tables, kc, vc, bs, d, 0.1, [rows[r][0] for r in pick],
+                          [rows[r][1] for r in pick])
+    ws = ops.make_prefill_workspace_fp4(S, G * hkv, hkv, d, bs, 2 * tile, 2 * tile)
+    qd, kd, vd, cd, td = to_device(q), _dev(kc), _dev(vc), _dev(cu), _dev(tables)
+    zero = torch.zeros(S, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        out = torch.zeros(q.shape, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ops.pa_prefill_fp4(out, qd, kd, vd, cd, zero, td, 0.1, hkv, bs, 2 * tile, 2 * tile, ws, KS, VS, status=st)
+        assert int(st.item()) == 0
+        assert np.array_equal(np.isnan(to_f64(out)), want)
+        _check(out[torch.tensor(pick, device="cuda")], ref, tol)
