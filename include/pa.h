@@ -509,8 +509,9 @@ pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t n
  *                      PA_ERR_INVALID_ARG for positions that do not ascend,
  *                      lie before their destination or past the table, for a
  *                      table entry outside the pool (such a token is not
- *                      moved) and for a count outside [0, max_keep] (such a
- *                      sequence is left alone)
+ *                      moved), for a count outside [0, max_keep] and for a
+ *                      range of keep that ends behind cu_keep[num_seqs] (such
+ *                      a sequence is left alone)
  * Blocks that are written must belong to one sequence only
  * (pa_alloc_make_writable); afterwards pa_alloc_truncate frees the rest.
  * ---------------------------------------------------------------------- */
@@ -521,6 +522,16 @@ pa_status pa_compact_tokens(void* k_cache, void* v_cache, int64_t cache_layer_st
                             const int32_t* dst_start, const int32_t* keep,
                             const int32_t* cu_keep, int32_t num_seqs, int32_t max_keep,
                             int32_t* status, void* stream);
+/* The same with the number of entries that keep has: a sequence whose range
+ * ends behind them is reported and left alone, so no cu_keep makes the call
+ * read past keep. */
+pa_status pa_compact_tokens_checked(void* k_cache, void* v_cache, int64_t cache_layer_stride,
+                                    int32_t num_layers, int32_t num_blocks, int32_t block_size,
+                                    int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* dst_start, const int32_t* keep, int32_t num_keep,
+                                    const int32_t* cu_keep, int32_t num_seqs, int32_t max_keep,
+                                    int32_t* status, void* stream);
 
 /* ------------------------------------------------------------------------
  * Host block allocator -- [vLLM2] block-table section and [KV02] section 2:

@@ -69,6 +69,8 @@ SIGNATURES = {
                              f32, f32, f32, vp, vp, C.c_size_t, vp]),
     "pa_compact_tokens": (i32, [vp, vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, i32, vp,
                                 vp]),
+    "pa_compact_tokens_checked": (i32, [vp, vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, i32, i32,
+                                        vp, vp]),
     "pa_alloc_create": (i32, [i32, i32, P_i32, C.POINTER(vp)]),
     "pa_alloc_destroy": (None, [vp]),
     "pa_alloc_num_blocks": (i32, [vp]),

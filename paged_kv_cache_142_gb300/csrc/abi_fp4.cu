@@ -50,6 +50,55 @@ bool group_ok(int32_t num_q_heads, int32_t num_kv_heads) {
   return g == 1 || g == 2 || g == 4 || g == 8 || g == 16;
 }
 
+// num_keep: entries of keep, or -1 for what cu_keep says
+pa_status compact_impl(void* k_cache, void* v_cache, int64_t cache_layer_stride, int32_t num_layers,
+                       int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* dst_start,
+                       const int32_t* keep, int32_t num_keep, const int32_t* cu_keep, int32_t num_seqs,
+                       int32_t max_keep, int32_t* status, void* stream) {
+  if (num_blocks <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+      (dtype != PA_DTYPE_FP4 && !is_float(dtype)))
+    return PA_ERR_INVALID_ARG;
+  if ((block_size & (block_size - 1)) != 0 || block_size > 256) return PA_ERR_UNSUPPORTED;
+  if (dtype == PA_DTYPE_FP4 && check_pool(num_blocks, block_size, num_kv_heads, head_dim) != PA_OK)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t e = dtype == PA_DTYPE_F32 ? 4 : (dtype == PA_DTYPE_BF16 ? 2 : 1);
+  const int64_t row = dtype == PA_DTYPE_FP4 ? head_dim / 2 : head_dim * e;
+  if (dtype != PA_DTYPE_FP4 && (row % 16 != 0 || row > 8192)) return PA_ERR_UNSUPPORTED;
+  const int64_t tile = dtype == PA_DTYPE_FP4 ? pa::fp4_tile_bytes(block_size, head_dim) : row * block_size;
+  const int64_t layer = tile * num_kv_heads * num_blocks;
+  if (num_seqs < 0 || max_keep < 0 || num_keep < -1 || max_blocks_per_seq <= 0 || num_layers < 1 || num_layers > 32767)
+    return PA_ERR_INVALID_ARG;
+  if (num_layers > 1 && (cache_layer_stride * e < layer || (cache_layer_stride * e) % 16 != 0))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || max_keep == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !dst_start || !keep || !cu_keep) return PA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) || !aligned(dst_start, 4) ||
+      !aligned(keep, 4) || !aligned(cu_keep, 4) || !aligned(status, 4))
+    return PA_ERR_INVALID_ARG;
+  pa::CompactParams p{};
+  p.k_cache = static_cast<unsigned char*>(k_cache);
+  p.v_cache = static_cast<unsigned char*>(v_cache);
+  p.layer_bytes = num_layers > 1 ? cache_layer_stride * e : 0;
+  p.block_tables = block_tables;
+  p.dst_start = dst_start;
+  p.keep = keep;
+  p.cu_keep = cu_keep;
+  p.status = status;
+  p.num_layers = num_layers;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.max_keep = max_keep;
+  p.num_keep = num_keep;
+  p.row_bytes = static_cast<int32_t>(row);
+  p.scale_bytes = dtype == PA_DTYPE_FP4 ? head_dim / 16 : 0;
+  p.tile_bytes = tile;
+  return pa::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -203,46 +252,21 @@ pa_status pa_compact_tokens(void* k_cache, void* v_cache, int64_t cache_layer_st
                             pa_dtype dtype, const int32_t* block_tables, int32_t max_blocks_per_seq,
                             const int32_t* dst_start, const int32_t* keep, const int32_t* cu_keep, int32_t num_seqs,
                             int32_t max_keep, int32_t* status, void* stream) {
-  if (num_blocks <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
-      (dtype != PA_DTYPE_FP4 && !is_float(dtype)))
-    return PA_ERR_INVALID_ARG;
-  if ((block_size & (block_size - 1)) != 0 || block_size > 256) return PA_ERR_UNSUPPORTED;
-  if (dtype == PA_DTYPE_FP4 && check_pool(num_blocks, block_size, num_kv_heads, head_dim) != PA_OK)
-    return PA_ERR_UNSUPPORTED;
-  const int64_t e = dtype == PA_DTYPE_F32 ? 4 : (dtype == PA_DTYPE_BF16 ? 2 : 1);
-  const int64_t row = dtype == PA_DTYPE_FP4 ? head_dim / 2 : head_dim * e;
-  if (dtype != PA_DTYPE_FP4 && (row % 16 != 0 || row > 8192)) return PA_ERR_UNSUPPORTED;
-  const int64_t tile = dtype == PA_DTYPE_FP4 ? pa::fp4_tile_bytes(block_size, head_dim) : row * block_size;
-  const int64_t layer = tile * num_kv_heads * num_blocks;
-  if (num_seqs < 0 || max_keep < 0 || max_blocks_per_seq <= 0 || num_layers < 1 || num_layers > 32767)
-    return PA_ERR_INVALID_ARG;
-  if (num_layers > 1 && (cache_layer_stride * e < layer || (cache_layer_stride * e) % 16 != 0))
-    return PA_ERR_INVALID_ARG;
-  if (num_seqs == 0 || max_keep == 0) return PA_OK;
-  if (!k_cache || !v_cache || !block_tables || !dst_start || !keep || !cu_keep) return PA_ERR_INVALID_ARG;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) || !aligned(dst_start, 4) ||
-      !aligned(keep, 4) || !aligned(cu_keep, 4) || !aligned(status, 4))
-    return PA_ERR_INVALID_ARG;
-  pa::CompactParams p{};
-  p.k_cache = static_cast<unsigned char*>(k_cache);
-  p.v_cache = static_cast<unsigned char*>(v_cache);
-  p.layer_bytes = num_layers > 1 ? cache_layer_stride * e : 0;
-  p.block_tables = block_tables;
-  p.dst_start = dst_start;
-  p.keep = keep;
-  p.cu_keep = cu_keep;
-  p.status = status;
-  p.num_layers = num_layers;
-  p.num_blocks = num_blocks;
-  p.block_size = block_size;
-  p.num_kv_heads = num_kv_heads;
-  p.max_blocks_per_seq = max_blocks_per_seq;
-  p.num_seqs = num_seqs;
-  p.max_keep = max_keep;
-  p.row_bytes = static_cast<int32_t>(row);
-  p.scale_bytes = dtype == PA_DTYPE_FP4 ? head_dim / 16 : 0;
-  p.tile_bytes = tile;
-  return pa::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return compact_impl(k_cache, v_cache, cache_layer_stride, num_layers, num_blocks, block_size, num_kv_heads, head_dim,
+                      dtype, block_tables, max_blocks_per_seq, dst_start, keep, -1, cu_keep, num_seqs, max_keep, status,
+                      stream);
+}
+
+pa_status pa_compact_tokens_checked(void* k_cache, void* v_cache, int64_t cache_layer_stride, int32_t num_layers,
+                                    int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                                    pa_dtype dtype, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* dst_start, const int32_t* keep, int32_t num_keep,
+                                    const int32_t* cu_keep, int32_t num_seqs, int32_t max_keep, int32_t* status,
+                                    void* stream) {
+  if (num_keep < 0) return PA_ERR_INVALID_ARG;
+  return compact_impl(k_cache, v_cache, cache_layer_stride, num_layers, num_blocks, block_size, num_kv_heads, head_dim,
+                      dtype, block_tables, max_blocks_per_seq, dst_start, keep, num_keep, cu_keep, num_seqs, max_keep,
+                      status, stream);
 }
 
 }  // extern "C"

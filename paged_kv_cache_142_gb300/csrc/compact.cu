@@ -64,9 +64,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   const int dst0 = p.dst_start[seq];
   // positions are 32-bit numbers
   const int64_t table_tokens = min(static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size, int64_t(0x7fffffff));
+  const int num_keep = p.num_keep >= 0 ? p.num_keep : p.cu_keep[p.num_seqs];  // entries that may be read
   const bool report = p.status && blockIdx.y == 0 && blockIdx.z == 0;
   if (n == 0) return;
-  if (b < 0 || n < 0 || n > p.max_keep || dst0 < 0 || dst0 + static_cast<int64_t>(n) > table_tokens) {
+  if (b < 0 || n < 0 || n > p.max_keep || b + static_cast<int64_t>(n) > num_keep || dst0 < 0 ||
+      dst0 + static_cast<int64_t>(n) > table_tokens) {
     if (report && threadIdx.x == 0) atomicExch(p.status, kDevErrInvalidArg);
     return;
   }

@@ -86,6 +86,7 @@ struct CompactParams {
   const int32_t* cu_keep;
   int32_t* status;
   int32_t num_layers, num_blocks, block_size, num_kv_heads, max_blocks_per_seq, num_seqs, max_keep;
+  int32_t num_keep;     // entries of keep; -1: what cu_keep says
   int32_t row_bytes;    // one token's row of one head (4-bit pages: its codes)
   int32_t scale_bytes;  // 4-bit pages: its scales, else 0
   int64_t tile_bytes;

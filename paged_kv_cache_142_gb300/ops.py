@@ -504,7 +504,8 @@ def pa_compact_tokens(k_cache, v_cache, block_tables, dst_start, keep, cu_keep, 
     """Move each sequence's kept tokens ``keep[cu_keep[i]:cu_keep[i+1]]``
     (ascending positions) to positions ``dst_start[i]``, ``dst_start[i] + 1``,
     ...  Caches of one layer or with a leading layer dimension; 4-bit caches
-    (uint8): give ``block_size`` and ``head_dim``."""
+    (uint8): give ``block_size`` and ``head_dim``.  A sequence whose range ends
+    behind ``keep`` is reported in ``status`` and left alone."""
     layered = k_cache.dim() == (4 if k_cache.dtype == torch.uint8 else 5)
     if layered:
         Lyr, NB, Hkv, bs, D, dt = _any_layer_cache_dims(k_cache, v_cache, block_size, head_dim)
@@ -519,10 +520,11 @@ def pa_compact_tokens(k_cache, v_cache, block_tables, dst_start, keep, cu_keep, 
           and block_tables.shape[0] == S and block_tables.is_contiguous(),
           "block_tables must be contiguous int32 [num_seqs, max_blocks]")
     _on_current_device(k_cache, v_cache, block_tables, dst_start, keep, cu_keep, status)
-    L.check(_LIB.pa_compact_tokens(
+    L.check(_LIB.pa_compact_tokens_checked(
         k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0) if layered else 0, Lyr, NB, bs, Hkv, D, dt,
-        block_tables.data_ptr(), block_tables.shape[1], dst_start.data_ptr(), keep.data_ptr(), cu_keep.data_ptr(), S,
-        min(int(max_keep), keep.numel()), _status_ptr(status), _stream(stream)), "pa_compact_tokens")
+        block_tables.data_ptr(), block_tables.shape[1], dst_start.data_ptr(), keep.data_ptr(), keep.numel(),
+        cu_keep.data_ptr(), S, min(int(max_keep), keep.numel()), _status_ptr(status), _stream(stream)),
+        "pa_compact_tokens")
 
 
 # --------------------------------------------------------------------------

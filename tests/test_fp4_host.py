@@ -127,6 +127,15 @@ def test_compact_refusals(lib):
     assert call(n=0, kc=None) == L.PA_OK and call(mk=0, kc=None) == L.PA_OK
 
 
+def test_checked_compact_refusals(lib):
+    def call(kc=P, bs=16, d=128, dt=1, keep=P, num_keep=4, cu=P, n=2, mk=3, status=None):
+        return lib.pa_compact_tokens_checked(kc, P, 0, 1, 8, bs, 2, d, dt, P, 4, P, keep, num_keep, cu, n, mk, status, None)
+    assert call(num_keep=-1) == BAD and call(num_keep=-5) == BAD
+    assert call(bs=12) == UNSUP and call(d=3) == UNSUP and call(dt=5) == BAD and call(n=-1) == BAD and call(mk=-1) == BAD
+    assert call(kc=None) == BAD and call(keep=None) == BAD and call(cu=None) == BAD and call(status=P + 1) == BAD
+    assert call(n=0, num_keep=0, keep=None) == L.PA_OK and call(mk=0, num_keep=0) == L.PA_OK
+
+
 def test_copy_accepts_4bit_pools(lib):
     def call(bs=16, d=128, n=1, layers=1, stride=0):
         return lib.pa_copy_blocks_layers(None, None, stride, layers, 8, bs, 2, d, L.PA_DTYPE_FP4, None, n, None)

@@ -136,3 +136,43 @@ def test_compaction_replayed_from_a_graph(ops):
             want[(2 + j) // bs, :, (2 + j) % bs] = rows[p // bs, :, p % bs]
         rows = want
         assert np.array_equal(_rows(_bytes(kt).reshape(k.shape), "fp4", bs, d)[0], rows)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+def test_ranges_behind_keep_are_reported_and_left_alone(ops, lib, kind):
+    """cu_keep that points behind keep, with counts that are small: what lies
+    there (memory of the test's own, with positions that could be moved) is
+    not taken for a list; the sequences whose lists are whole are compacted."""
+    rng = np.random.default_rng(5)
+    hkv, bs, d, nb = 2, 16, 128, 8
+    k = _pool(rng, kind, 1, nb, hkv, bs, d)
+    tables = _dev(np.arange(8, dtype=np.int32).reshape(4, 2))
+    wide = _dev(np.array([4, 9, 5, 6, 7, 20, 3, 8], np.int32))
+    start = torch.zeros(4, dtype=torch.int32, device="cuda")
+    #        entries of keep, cu_keep, sequences that move
+    cases = [(4, [0, 2, 4, 4, 6], [0, 1]), (4, [0, 2, 5, 6, 8], [0]), (2, [0, 2, 1 << 30, (1 << 30) + 2, 2], [0]),
+             (8, [0, 2, 5, 6, 8], [0, 1, 2, 3])]
+    for entries, cu, moved in cases:
+        kt, vt = _tensor(k, kind, d), _tensor(k, kind, d)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ops.pa_compact_tokens(kt[0], vt[0], tables, start, wide[:entries], _dev(np.array(cu, np.int32)), 3, bs, d,
+                              status=status)
+        assert int(status.item()) == (0 if len(moved) == 4 else 1), cu
+        want = _rows(k, kind, bs, d).copy()
+        for i in moved:
+            for j, src in enumerate(wide[cu[i]:cu[i + 1]].tolist()):
+                want[:, 2 * i + j // bs, :, j % bs] = _rows(k, kind, bs, d)[:, 2 * i + src // bs, :, src % bs]
+        for t in (kt, vt):
+            assert np.array_equal(_rows(_bytes(t).reshape(k.shape), kind, bs, d), want), cu
+    # without keep's length the call goes by cu_keep[num_seqs]
+    kt, vt = _tensor(k, kind, d), _tensor(k, kind, d)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = _dev(np.array([0, 2, 5, 6, 4], np.int32))
+    st = lib.pa_compact_tokens(kt.data_ptr(), vt.data_ptr(), 0, 1, nb, bs, hkv, d, 1 if kind == "bf16" else 2,
+                               tables.data_ptr(), 2, start.data_ptr(), wide.data_ptr(), cu.data_ptr(), 4, 3,
+                               status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and int(status.item()) == 1
+    want = _rows(k, kind, bs, d).copy()
+    for j, src in enumerate((4, 9)):
+        want[:, 0, :, j] = _rows(k, kind, bs, d)[:, src // bs, :, src % bs]
+    assert np.array_equal(_rows(_bytes(kt).reshape(k.shape), kind, bs, d), want)
