@@ -299,7 +299,9 @@ pa_status pa_decode_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
  * tensor memory is freed, the output is left undefined, and
  * PA_ERR_DEVICE_TIMEOUT reaches the host through pa_workspace_error.  The
  * workspace must be zeroed again (pa_workspace_init) before its next use.
- * The same stop path serves any real wait that runs out its 2 s limit. */
+ * The same stop path serves any real wait that runs out its 2 s limit.
+ * pa_decode_fp4 takes the hook too: the warps of a CTA wait so before they join
+ * their sums, and the CTA then stops and reports in the same way. */
 void pa_test_stall_decode(uint64_t ns);
 
 /* Zero a decode workspace (enqueued on `stream`). */

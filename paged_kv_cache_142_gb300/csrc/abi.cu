@@ -42,6 +42,10 @@ int64_t device_sm_count() {
   }
   return n;
 }
+
+// Timeout-path test hook (pa_test_stall_decode): 0 = off.
+static std::atomic<uint64_t> g_test_stall_ns{0};
+uint64_t test_stall_ns() { return g_test_stall_ns.load(std::memory_order_relaxed); }
 }  // namespace pa
 
 namespace {
@@ -49,8 +53,6 @@ namespace {
 using pa::DecodeKernelInfo;
 using pa::DecodeParams;
 
-// Timeout-path test hook (pa_test_stall_decode): 0 = off.
-std::atomic<uint64_t> g_test_stall_ns{0};
 // kv heads per decode work item (pa_set_decode_kv_per_item): 0 = automatic.
 std::atomic<int> g_kv_per_item{0};
 
@@ -793,7 +795,7 @@ pa_status pa_decode(void* out, pa_dtype out_dtype, const void* q, int32_t num_se
   p.ws_counters = reinterpret_cast<int32_t*>(ws + pl.ws_counters);
   p.ws_ml = reinterpret_cast<float*>(ws + pl.ws_ml);
   p.ws_o = reinterpret_cast<float*>(ws + pl.ws_o);
-  p.test_stall_ns = g_test_stall_ns.load(std::memory_order_relaxed);
+  p.test_stall_ns = pa::test_stall_ns();
 
   cudaError_t e;
   if (pl.umma) {
@@ -842,7 +844,7 @@ pa_status pa_set_decode_kv_per_item(int32_t kv_per_item) {
 }
 
 void pa_test_stall_decode(uint64_t ns) {
-  g_test_stall_ns.store(ns < pa::kWaitLimitNs ? ns : pa::kWaitLimitNs, std::memory_order_relaxed);
+  pa::g_test_stall_ns.store(ns < pa::kWaitLimitNs ? ns : pa::kWaitLimitNs, std::memory_order_relaxed);
 }
 
 pa_status pa_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {

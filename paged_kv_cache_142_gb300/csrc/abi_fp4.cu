@@ -184,6 +184,7 @@ pa_status pa_decode_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t nu
   p.scale_log2 = scale * 1.4426950408889634f * k_scale;
   p.v_scale = v_scale;
   p.err = static_cast<int32_t*>(workspace);
+  p.test_stall_ns = pa::test_stall_ns();
   p.ws = static_cast<unsigned char*>(workspace);
   return pa::launch_fp4_decode(p, head_dim, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -59,6 +59,9 @@ struct DecodeParams {
   uint64_t test_stall_ns;
 };
 
+// pa_test_stall_decode's setting.
+uint64_t test_stall_ns();
+
 // SMs of the current device (152, the GB300's, when none can be queried).
 int64_t device_sm_count();
 

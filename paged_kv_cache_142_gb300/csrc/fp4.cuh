@@ -42,6 +42,7 @@ struct Fp4AttnParams {
   float scale_log2;  // softmax scale * log2(e) * k_scale
   float v_scale;
   int32_t* err;      // device error word (may be null in prefill)
+  uint64_t test_stall_ns;  // decode, timeout-path test hook (0 = off): a wait for what never comes, this long
   unsigned char* ws;
 };
 

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   float* qfac = reinterpret_cast<float*>(smem + L.off_qfac);               // [2][16] score factors
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L.off_bar);         // the next segment's queries
   uint64_t* merge_free = q_full + 1;  // the merge area and stat have been read
+  uint64_t* never = q_full + 2;       // no one arrives: for pa_test_stall_decode
   __shared__ int warp_sums[kWarps];
   __shared__ int last_flag;
 
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   if (tid == 0) {
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(merge_free, kWarps);
+    ptx::mbar_init(never, 1);
     ptx::mbar_init_fence();
   }
   for (int i = tid; i < 2 * NT * (D / 32) * 32; i += kThreads) qf16[i] = make_uint4(0, 0, 0, 0);  // heads past G
@@ -422,13 +424,12 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
       ptx::bulk_g2s(qraw, src, G * D * 2, q_full, ptx::policy_evict_first());
     }
   };
+  // A wait that gives up ends the whole CTA's work at its next barrier: no later
+  // wait begins, no query copy either, and the end reports it.
   bool aborted = false;
   uint32_t q_parity = 0;
   auto convert_q = [&](int b) {
-    if (!ptx::mbar_wait(q_full, q_parity, kWaitLimitNs)) {
-      aborted = true;  // the output is then undefined
-      atomicExch(p.err, kDevErrTimeout);
-    }
+    if (!ptx::mbar_wait(q_full, q_parity, kWaitLimitNs)) aborted = true;
     q_parity ^= 1u;
     for (int i0 = 0; i0 < q_chunks; i0 += kThreads) {
       const int i = i0 + tid;
@@ -467,10 +468,10 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
   if (s_begin >= c_end) return;
   fetch_q(sc);
   convert_q(0);
-  __syncthreads();
+  aborted = __syncthreads_or(aborted);
   int qb = 0;
   uint32_t merge_parity = 1;  // free at the start
-  for (int sb = s_begin; sb < c_end;) {
+  for (int sb = s_begin; sb < c_end && !aborted;) {
     const int item_b = sb - sc.st;                    // the item's first unit
     const int se = min(c_end, item_b + sc.nst);       // the segment's end
     Cursor next = sc;
@@ -688,11 +689,12 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
         if (heads <= 0) break;
         // the round before, of this segment or the last, is read
         if (!ptx::mbar_wait(merge_free, merge_parity, kWaitLimitNs)) aborted = true;
+        if (p.test_stall_ns && !ptx::mbar_wait(never, 0, p.test_stall_ns)) aborted = true;
         merge_parity ^= 1u;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int h = 2 * tig + c - h0;
-          if (h >= 0 && h < kHeads) {
+          if (!aborted && h >= 0 && h < kHeads) {
             if (g == 0) stat[warp * 8 + h] = active ? make_float2(m[nt][c], l[nt][c]) : make_float2(-CUDART_INF_F, 0.f);
             if (active && h < heads) {
               float* row = merge + warp * (gpairs * kPair) + (h >> 1) * kPair + c * D + g * kRow;
@@ -703,7 +705,8 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
             }
           }
         }
-        __syncthreads();
+        aborted = __syncthreads_or(aborted);
+        if (aborted) goto stop;
         for (int i = tid; i < heads * D / 4; i += kThreads) {
           const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
           float2 st[kWarps];
@@ -815,9 +818,14 @@ __global__ void __launch_bounds__(fp4_decode_detail::kThreads, (D <= 128 && NT =
     sc = next;
     qb ^= 1;
   }
-  // a query copy whose wait of 2 s gave up is given another 2 s to land
-  if (__syncthreads_or(aborted)) {
-    if (tid == 0) (void)ptx::mbar_wait(q_full, q_parity ^ 1u, kWaitLimitNs);
+stop:
+  if (aborted) {  // the whole CTA; the output is undefined, and the heads that it shares are left unjoined
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (tid == 0) {
+      atomicExch(p.err, kDevErrTimeout);
+      // a query copy whose wait of 2 s gave up is given another 2 s to land
+      (void)ptx::mbar_wait(q_full, q_parity ^ 1u, kWaitLimitNs);
+    }
     __syncthreads();
   }
 }
@@ -937,7 +945,7 @@ cudaError_t launch_fp4_decode(const Fp4AttnParams& p, int head_dim, cudaStream_t
     const int64_t held = round_up(L.nseq + 1, 64);  // few different sizes
     L.off_prefix = take(held * 4);
     L.off_lens = take(held * 4);
-    L.off_bar = take(2 * 8);
+    L.off_bar = take(3 * 8);
     L.counters = reinterpret_cast<int32_t*>(p.ws + 256);
     L.part = reinterpret_cast<float*>(p.ws + 256 + fp4_counter_bytes());
     // at least a unit for every warp, as far as the longest context allows

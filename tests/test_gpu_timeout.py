@@ -53,3 +53,41 @@ def test_expired_wait_is_reported_and_the_next_decode_is_correct(ops, lib, parti
     again = g.decode(partition_tokens=partition_tokens, workspace=ws)   # asserts status 0
     assert float(np.abs(to_f64(again) - ref).max()) <= TOL["bf16"]
     assert ops.pa_workspace_error(ws) == 0
+
+
+@pytest.mark.parametrize("lens,G,hkv,d,bs", [([9000, 3, 0, 700], 4, 2, 128, 16), ([40] * 300, 1, 4, 64, 8),
+                                             ([2500] * 3, 16, 1, 256, 32)])
+def test_expired_wait_of_the_4bit_decode_is_reported(ops, lib, lens, G, hkv, d, bs):
+    """The warps' wait before they join their sums runs out: the host reads it,
+    and over a zeroed workspace the next call gives what the one before gave."""
+    from fp4_case import bf16, pool
+    from paged_case import to_device
+
+    rng = np.random.default_rng(len(lens))
+    nb, m = 40, max(1, -(-max(lens) // bs))
+    dev = lambda x: torch.from_numpy(x).cuda()
+    kc, vc = dev(pool(rng, nb, hkv, bs, d, 1.0)), dev(pool(rng, nb, hkv, bs, d, 1.0))
+    tables = dev(rng.integers(0, nb, size=(len(lens), m)).astype(np.int32))
+    q = to_device(bf16(rng.standard_normal((len(lens), G * hkv, d))))
+    n = dev(np.array(lens, np.int32))
+    ws = ops.make_workspace_fp4(len(lens), G * hkv, hkv, d, bs, max(lens))
+
+    def decode():
+        out = torch.full(q.shape, float("nan"), device="cuda")
+        ops.pa_decode_fp4(out, q, kc, vc, tables, n, 0.1, hkv, bs, max(lens), ws)
+        t0 = time.perf_counter()
+        status = ops.pa_workspace_error(ws)  # synchronises the stream
+        return out, status, time.perf_counter() - t0
+
+    before, status, _ = decode()
+    assert status == 0 and bool(torch.isfinite(before).all())
+    lib.pa_test_stall_decode(100_000)
+    try:
+        _, status, elapsed = decode()
+    finally:
+        lib.pa_test_stall_decode(0)
+    assert status == 6  # PA_ERR_DEVICE_TIMEOUT
+    assert elapsed < 1.0, elapsed  # no wait of 2 s behind it
+    ops.pa_workspace_init(ws)
+    again, status, _ = decode()
+    assert status == 0 and torch.equal(again, before)
