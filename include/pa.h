@@ -599,7 +599,11 @@ pa_status pa_alloc_make_writable(pa_allocator* a, int32_t seq, int32_t from, int
                                  int64_t* cow_pairs, int32_t cap, int32_t* num_cow);
 /* Shorten `seq` to its first new_len tokens and release the blocks behind
  * them (in table order; last block first when prefix caching is on).  A
- * tracked sequence stays tracked.  PA_ERR_INVALID_ARG unless
+ * tracked sequence stays tracked; but if its last block is then partly used
+ * and shared, pa_alloc_append_token_ids refuses it as it does a fork, and the
+ * calls that copy the block (pa_alloc_append_slot, pa_alloc_make_writable) end
+ * the tracking.  A block that is partly used loses its prefix key, if shared
+ * not before it is written in place.  PA_ERR_INVALID_ARG unless
  * 0 <= new_len <= length. */
 pa_status pa_alloc_truncate(pa_allocator* a, int32_t seq, int32_t new_len);
 /* Release every block of `seq` in table order (last block first when

@@ -246,9 +246,10 @@ class BlockAllocator {
                                q->tokens.data() + static_cast<int64_t>(j) * block_size_, q->extra);
       }
     }
-    // a block that is no longer full will be filled with other tokens: no key
-    // may go on standing for it
-    if (pc_ && new_len % block_size_ != 0) drop_key(q->table[keep - 1]);
+    // a block of its own that is no longer full will be filled with other
+    // tokens: no key may go on standing for it.  A shared one is copied before
+    // this sequence writes, or gives up its key when it is written in place.
+    if (pc_ && new_len % block_size_ != 0 && ref_[q->table[keep - 1]] == 1) drop_key(q->table[keep - 1]);
     return PA_OK;
   }
 
@@ -368,6 +369,8 @@ class BlockAllocator {
         q->table[li] = nb;
         src = last;
         dst = nb;
+      } else if (pc_) {
+        drop_key(last);  // truncated while it was shared: its contents change now
       }
     }
     q->len = pos + 1;

@@ -271,3 +271,68 @@ def test_prefix_keys_follow_truncation_and_rewriting(ops):
     # another request for the first tokens still finds the block that was not touched
     s2, cached, _ = a.seq_create_prefix(ids[:8])
     assert cached == 4 and a.block_table(s2)[0] == table[0]
+
+
+def _two_holders(ops):
+    """Two requests of the same 12 tokens in three shared, keyed blocks; the
+    first cut to 10 tokens."""
+    a = ops.BlockAllocator(16, 4)
+    a.enable_prefix_cache()
+    ids = list(range(50, 62))
+    s1 = a.seq_create_prefix(ids)[0]
+    s2, cached, _ = a.seq_create_prefix(ids)
+    table = a.block_table(s1)
+    assert cached == 12 and a.block_table(s2) == table and a.num_cached() == 3
+    key = a.block_key(table[2])
+    a.truncate(s1, 10)
+    return a, ids, s1, s2, table, key
+
+
+def test_truncation_into_a_shared_block_keeps_its_key(ops):
+    """Its contents are another sequence's too, and do not change: a third
+    request finds all 12 tokens.  A copy for the writer leaves them alone."""
+    a, ids, s1, s2, table, key = _two_holders(ops)
+    assert a.block_key(table[2]) == key and a.num_cached() == 3
+    s3, cached, _ = a.seq_create_prefix(ids)
+    assert cached == 12 and a.block_table(s3) == table
+    with pytest.raises(ops.PAError):
+        a.append_token_ids(s1, [7])                      # the block would have to be copied first
+    slot, src, dst = a.append_slot(s1)
+    assert src == table[2] and slot == dst * 4 + 2 and a.block_key(dst) is None and a.block_key(table[2]) == key
+
+
+@pytest.mark.parametrize("how", ["ids", "slot", "slots", "tokens", "writable"])
+def test_the_key_goes_with_the_first_write_in_place(ops, how):
+    """The other holder leaves: the block is the truncated sequence's own, still
+    with its contents, until the sequence writes into it."""
+    a, ids, s1, s2, table, key = _two_holders(ops)
+    a.free_seq(s2)
+    assert a.refcount(table[2]) == 1 and a.block_key(table[2]) == key
+    s3, cached, _ = a.seq_create_prefix(ids)
+    assert cached == 12
+    a.free_seq(s3)
+    if how == "ids":
+        a.append_token_ids(s1, [7])
+    elif how == "slot":
+        a.append_slot(s1)
+    elif how == "slots":
+        assert len(a.append_slots([s1])[1]) == 0
+    elif how == "tokens":
+        a.append_tokens(s1, 2)
+    else:
+        assert len(a.make_writable(s1, 9, 10)) == 0
+    assert a.block_table(s1)[2] == table[2] and a.block_key(table[2]) is None and a.num_cached() == 2
+    assert a.seq_create_prefix(ids)[1] == 8
+    if how == "ids":
+        a.append_token_ids(s1, [8])                      # full again, with other tokens: keyed for those
+        k1 = oracle.block_key(a.block_key(table[1]), ids[8:10] + [7, 8], b"")
+        assert a.block_key(table[2]) == k1
+
+
+def test_a_truncated_holder_that_leaves_last_keeps_the_block_cached(ops):
+    a, ids, s1, s2, table, key = _two_holders(ops)
+    a.free_seq(s2)
+    a.free_seq(s1)
+    assert a.num_free() == 16 and a.block_key(table[2]) == key
+    s3, cached, _ = a.seq_create_prefix(ids + [1])
+    assert cached == 12 and a.block_table(s3)[:3] == table
