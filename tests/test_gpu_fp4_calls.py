@@ -469,3 +469,98 @@ def test_items_of_two_tiles_between_items_of_one(ops, G, hkv, S):
         assert int(st.item()) == 0
         assert np.array_equal(np.isnan(to_f64(out)), want)
         _check(out[torch.tensor(pick, device="cuda")], ref, tol)
+
+
+def test_single_keys_among_millions(ops):
+    """Every query is aligned with one of 60 keys planted among 6 million, so
+    its output is that key's value: at the first and last token, around the
+    chunk and past 5.9 million among them.  Rows in front of their key do not
+    see it, and average the others.
+
+    A planted key's score is 0.1 * 384 = 38.4 and no other key's comes near
+    it, so its weight is 1 - rest with a rest that the reference knows.  Then
+    the output is off by half a step of the weight's f16, 2^-12, the
+    exponential's 2^-21 and a few fp32 roundings (2^-20 together) and the rest's
+    own errors (at most 2 of each: as much again) of max |V|.  No other
+    addition counts: what came before the key is scaled by exp(-38) when the
+    reference is raised to it, and what comes after is 0 in f16."""
+    rng = np.random.default_rng(21)
+    nb, ns, bs, d, G, n, start, scale = 64, 60, 256, 128, 16, 40, 6_000_037, 0.1
+    end = start + n
+    m = -(-end // bs)
+    kc, vc = pool(rng, nb + ns, 1, bs, d, KS), pool(rng, nb + ns, 1, bs, d, VS)
+    # pages: shared ones, and one of its own for every planted key
+    last = (end - 1) // bs
+    own = np.unique(np.concatenate([[0, 1, start // bs - 1, start // bs, last],
+                                    rng.choice(np.arange(5_900_000 // bs, last - 2), 20, replace=False),
+                                    rng.choice(np.arange(2, 5_900_000 // bs), 45, replace=False)]))
+    own = np.concatenate([own[:2], rng.permutation(own[2:-3])[:ns - 5], own[-3:]])[:ns]
+    tables = np.resize(rng.permutation(nb), m).astype(np.int32)
+    tables[own] = nb + np.arange(len(own))
+    off = rng.integers(0, bs, size=len(own))
+    off[own == 0] = 0
+    off[own == last] = (end - 1) % bs
+    off[own == start // bs] = min(bs - 1, start % bs + n // 2)   # inside the chunk, if its page goes so far
+    place = own * bs + off
+    u = rng.choice([-1.0, 1.0], size=(len(own), d)).astype(np.float32)
+    val = rng.choice([-1.5, 1.5], size=(len(own), d)).astype(np.float32)
+    slots = (nb + np.arange(len(own), dtype=np.int64)) * bs + off
+    fp4.reshape_and_cache((3 * u)[:, None], kc, slots, bs, KS)
+    fp4.reshape_and_cache(val[:, None], vc, slots, bs, VS)
+    K, V = (fp4.values(c, bs, d, s)[:, 0].reshape(-1, d) for c, s in ((kc, KS), (vc, VS)))
+    assert np.array_equal(K[slots], 3 * u) and np.array_equal(V[slots], val)
+    uses = [np.flatnonzero(tables == b) for b in range(nb + ns)]   # the pages of every block, ascending
+    vmax = float(np.abs(V).max())
+
+    def reference(target, pos):
+        """The outputs of queries u[target] [H] at position pos, and their bounds."""
+        count = np.zeros((nb + ns, bs))
+        for b, pages in enumerate(uses):
+            whole = np.searchsorted(pages, (pos + 1) // bs)        # pages that end before pos
+            count[b] = whole
+            if whole < len(pages) and pages[whole] == (pos + 1) // bs:
+                count[b, :(pos + 1) % bs] += 1
+        count = count.reshape(-1)
+        assert count.sum() == pos + 1
+        s = scale * (u[target].astype(np.float64) @ K.T)
+        s[:, count == 0] = -np.inf
+        w = count * np.exp(s - s.max(axis=1, keepdims=True))
+        w /= w.sum(axis=1, keepdims=True)
+        seen = place[target] <= pos
+        rest = 1 - w[np.arange(len(target)), slots[target]]
+        assert (rest[seen] < 1e-6).all()
+        tight = vmax * (2.0 ** -12 + 2.0 ** -20 + 2 * rest)
+        # without the planted key: fp32 sums over a CTA's share of the keys, of which 100 CTAs or more have 3 tiles' rows
+        ds = (d + 4) * 2.0 ** -23 * scale * float(np.abs(K).sum(axis=1).max())  # a score's, as in attention_bound
+        loose = vmax * (2 * ds + 2.0 ** -21 + 2.0 ** -12 + 3 * end / 100 * 2.0 ** -23)
+        return w @ V, np.where(seen, tight, loose), seen
+
+    def check(out, target, pos):
+        ref, tol, seen = reference(target, pos)
+        # the bounds tell the outputs from zeros, from other keys' and from the key left out or let in
+        assert (np.abs(ref[seen]) > 1.4).all() and (tol < 0.1).all() and (np.abs(ref[~seen]) < 1.0).all()
+        for a, b in ((a, b) for a in range(len(target)) for b in range(a) if target[a] != target[b] and seen[a] and seen[b]):
+            assert np.abs(ref[a] - ref[b]).max() > 2.5
+        _check(out, ref, tol[:, None])
+        return int(seen.sum()), int((~seen).sum())
+
+    kd, vd = _dev(kc), _dev(vc)
+    # single tokens: four sequences over the same pages
+    lens = [end, end - 1, 5_900_003, start]
+    target = np.resize(rng.permutation(len(own)), (4, G))
+    target[0, :2] = [int(np.argmax(place)), int(np.argmin(place))]
+    got = _decode(ops, bf16(u[target]), np.tile(tables, (4, 1)), lens, kd, vd, bs, scale, 1)
+    for i in range(4):
+        check(got[i], target[i], lens[i] - 1)
+    # a chunk: every planted key is some row's, those inside the chunk several rows'
+    target = np.resize(rng.permutation(len(own)), (n, G))
+    inside = np.flatnonzero(place >= start)
+    target[:, :len(inside)] = inside
+    ws = ops.make_prefill_workspace_fp4(1, G, 1, d, bs, n, end)
+    out = torch.full((n, G, d), float("nan"), device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.pa_prefill_fp4(out, to_device(bf16(u[target])), kd, vd, _dev(np.array([0, n], np.int32)),
+                       _dev(np.array([start], np.int32)), _dev(tables[None]), scale, 1, bs, n, end, ws, KS, VS, status=st)
+    assert int(st.item()) == 0
+    done = [check(out[t], target[t], start + t) for t in range(n)]
+    assert len(inside) >= 1 and sum(b for _, b in done) >= n // 2 and sum(a for a, _ in done) > 400
