@@ -31,11 +31,6 @@ __device__ __forceinline__ void load32(uint32_t (&w)[8], const void* p) {
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p));
 }
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 
 // Walks this thread's groups, kUnroll tokens at a time: early(e, row) for
 // each, then early2(e, codes, scales) and last(e, row, codes, scales) for those
@@ -165,10 +160,10 @@ __global__ void __launch_bounds__(kThreads)
           uint32_t o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
-          store32(dst + row * 32, o);
+          fp4::store32(dst + row * 32, o);
         } else {
-          store32(dst + row * 64, reinterpret_cast<uint32_t(&)[8]>(w[0]));
-          store32(dst + row * 64 + 32, reinterpret_cast<uint32_t(&)[8]>(w[8]));
+          fp4::store32(dst + row * 64, reinterpret_cast<uint32_t(&)[8]>(w[0]));
+          fp4::store32(dst + row * 64 + 32, reinterpret_cast<uint32_t(&)[8]>(w[8]));
         }
       });
 }

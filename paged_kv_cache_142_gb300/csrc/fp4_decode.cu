@@ -90,16 +90,8 @@ struct Launch {
   float* part;             // [2 * CTAs][G * (D + 2)]
 };
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
+using fp4::fast_exp2;
+using fp4::pack_f16;
 // the 8 x 8 matrix of 16-bit elements spread over the warp, transposed
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;

@@ -86,7 +86,7 @@ constexpr uint32_t kColO = 256;  // tensor memory: S of the tiles at 0 and 128, 
 // as places before the item's first step.
 constexpr int kLead = 2;
 constexpr int kMaxSeqs = 4096;   // of one launch: their places lie in shared memory
-constexpr int kMostParts = 32;   // CTAs of an item
+constexpr int kMostParts = 32;   // CTAs for each item on the average, at most (a long one among short ones has more)
 
 struct Launch {
   Fp4AttnParams p;      // of this launch's sequences
@@ -222,16 +222,8 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
   return yes != 0;
 }
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
+using fp4::fast_exp2;
+using fp4::pack_f16;
 // kind::f16, f16 operands, fp32 accumulator, M = N = 128; b_mn: B is N-major
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (16u << 17) | (8u << 24);
@@ -325,14 +317,7 @@ struct Row {
   uint2 s;
 };
 
-}  // namespace fp4_prefill_detail
-
-namespace fp4_prefill_detail {
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
+using fp4::store32;
 // 16 outputs of a row, times inv, in whole 32-byte sectors
 __device__ __forceinline__ void store_out(const Fp4AttnParams& p, int64_t at, const uint32_t (&v)[16], float inv) {
   uint32_t h[8];
@@ -554,8 +539,8 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
       for (int t = 0; t < n && !aborted; ++t, ++kc) {
         const int slot = kc & 1u;
         const uint32_t ph = (kc >> 1) & 1u;
-        const bool more = t + 1 < n;
-        if (more) at = locate(it, table, it.t0 + t + 1);
+        const bool next = t + 1 < n;
+        if (next) at = locate(it, table, it.t0 + t + 1);
         wait(&bars[kKFree + slot], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
@@ -563,7 +548,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kKFull + slot]);
-        if (more) load(kx, p.k_cache, at, it.t0 + t + 1);
+        if (next) load(kx, p.k_cache, at, it.t0 + t + 1);
         wait(&bars[kVFree + slot], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
@@ -572,7 +557,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kVFull + slot]);
-        if (more) load(vx, p.v_cache, at, it.t0 + t + 1);
+        if (next) load(vx, p.v_cache, at, it.t0 + t + 1);
       }
     }
   } else if (warp >= 12) {
@@ -652,7 +637,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         } else if (next && leader) {
           ptx::mbar_arrive(&bars[kKFree + kslot]);
         }
-        if (!aborted && leader && (t == n - 2 || n == 0)) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
+        if (!aborted && leader && t == n - 2) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
         __syncwarp();
         asm volatile("bar.arrive %0, 64;" ::"r"(i ? 2 : 1) : "memory");
       }
@@ -941,7 +926,7 @@ cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream) {
     int per_sm = 0;
     cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
     if (e != cudaSuccess) return e;
-    // every SM, while an item is not cut into too many parts to add up
+    // every SM, while the items are not cut into too many parts to add up
     const int64_t items = static_cast<int64_t>(L.p.num_seqs) * pairs_of(G, longest) * p.num_kv_heads;
     const int64_t ctas = items * kMostParts < sms ? items * kMostParts : sms;
     cudaLaunchConfig_t cfg{};
