@@ -471,7 +471,9 @@ pa_status pa_decode_fp4(void* out, pa_dtype out_dtype,
 
 /* pa_prefill over a 4-bit cache (head_dim 128, any block size): causal
  * attention of each sequence's chunk of bf16 queries, rounded as in
- * pa_decode_fp4; out is 32-byte aligned.  max_context_len: host, >= every q_start[i] + chunk length
+ * pa_decode_fp4; out is 32-byte aligned.  scale is positive, as in pa_prefill
+ * (pa_decode and pa_decode_fp4 take any finite one).  max_q_len and
+ * max_context_len: host, bounds of every chunk's length and of every q_start[i] + length
  * (a longer one is reported in *status and its rows are not written).  The
  * workspace (256-byte aligned, zero-filled before its first use) holds the
  * partial results of a long history that is split over CTAs; calls that

@@ -15,9 +15,9 @@
 // registers allow (four pieces a thread, 512 threads for long lists), its
 // places serve several planes, the next plane's rows load before this one's
 // are written, and few kept tokens (accepted drafts) take all heads in one CTA.
-// 64 sequences x up to 8 tokens in 32 layers (81 MB): 23.4 us; 16 sequences x
-// 2000 of 4096 tokens in 4 bits (75 MB): 33 us (one piece a thread and a CTA a
-// plane and head: 49 and 104 us).
+// 64 sequences x up to 8 tokens in 32 layers (78 MB): 23.4 us; 16 sequences x
+// 2000 of 4096 tokens in 4 bits (74 MB): 27.6 us, call behind call (one piece a
+// thread and a CTA a plane and head: 49 and 104 us).
 #include "decode.cuh"
 #include "fp4.cuh"
 #include "ptx.cuh"
