@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(fp4_prefill_detail::kThreads, 1)
         } else if (next && leader) {
           ptx::mbar_arrive(&bars[kKFree + kslot]);
         }
-        if (!aborted && leader && t == n - 2) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
+        if (!aborted && leader && next && t + 2 == n) ptx::umma_commit(&bars[kQFree]);  // the last Q.K^T is issued
         __syncwarp();
         asm volatile("bar.arrive %0, 64;" ::"r"(i ? 2 : 1) : "memory");
       }
