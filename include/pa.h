@@ -538,6 +538,143 @@ pa_status pa_compact_tokens_checked(void* k_cache, void* v_cache, int64_t cache_
                                     int32_t* status, void* stream);
 
 /* ------------------------------------------------------------------------
+ * A latent cache -- [PA] "KV Cache 为什么难管理": a token's cache costs
+ * 2 * L * H_kv * d elements.  Where every head's key and value derive from one
+ * latent vector c and one position key r a token, the cache holds the two alone:
+ *   cache   [num_blocks][block_size][latent_dim + rope_dim] of dtype
+ * with blocks, tables, slots and lengths as everywhere.  The copies below take
+ * any latent_dim and rope_dim whose rows are whole 16-byte pieces (8192 bytes
+ * together at most), F32 or BF16; the attention calls take bf16 caches with
+ * latent_dim 512, rope_dim 64 and block_size 8 to 256.
+ * Contexts: up to 2^30 tokens.
+ *
+ * pa_reshape_and_cache_latent: for t < num_tokens with s = slot_mapping[t],
+ *   cache[s / block_size][s % block_size] = (latent[t], rope[t]).
+ *   latent, rope  device; rows latent_stride and rope_stride elements apart
+ *                 (slices of a wider tensor are fine), each stride a whole
+ *                 number of 16-byte pieces; bases 16-byte aligned
+ *   status        as in pa_reshape_and_cache_checked, or NULL.
+ * Negative slots are skipped, slots past the pool too.
+ * pa_copy_blocks_latent, pa_compact_tokens_latent: pa_copy_blocks (checked if
+ *   status is given) and pa_compact_tokens_checked over the one array, in every
+ *   layer (layer l at cache + l * cache_layer_stride elements; the stride is
+ *   ignored for one layer).
+ * ---------------------------------------------------------------------- */
+pa_status pa_reshape_and_cache_latent(const void* latent, int64_t latent_stride, const void* rope, int64_t rope_stride,
+                                      int32_t num_tokens, const int64_t* slot_mapping, void* cache, int32_t num_blocks,
+                                      int32_t block_size, int32_t latent_dim, int32_t rope_dim, pa_dtype dtype,
+                                      int32_t* status, void* stream);
+pa_status pa_copy_blocks_latent(void* cache, int64_t cache_layer_stride, int32_t num_layers, int32_t num_blocks,
+                                int32_t block_size, int32_t latent_dim, int32_t rope_dim, pa_dtype dtype,
+                                const int64_t* block_pairs, int32_t num_pairs, int32_t* status, void* stream);
+pa_status pa_compact_tokens_latent(void* cache, int64_t cache_layer_stride, int32_t num_layers, int32_t num_blocks,
+                                   int32_t block_size, int32_t latent_dim, int32_t rope_dim, pa_dtype dtype,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* dst_start,
+                                   const int32_t* keep, int32_t num_keep, const int32_t* cu_keep, int32_t num_seqs,
+                                   int32_t max_keep, int32_t* status, void* stream);
+
+/* Decode over a latent cache, absorbed form: the query of head h has been
+ * multiplied by the transpose of that head's key projection, so it meets the
+ * latent rows as they are, and the output is multiplied by the value projection
+ * afterwards.  Query j < q_len of sequence i is its token at position
+ * context_lens[i] - q_len + j (the q_len tokens are in the cache already):
+ *   s[t]         = scale * q[i][j][h] . row_t,   t <= that position
+ *   out[i][j][h] = sum_t softmax(s)[t] * row_t[0 : latent_dim]
+ * and 0 where there is no t (empty sequences; positions below 0).  Rows behind
+ * the context are never used, whatever they hold.
+ *   q    device, bf16 [num_seqs][q_len][num_heads][latent_dim + rope_dim], 16-byte aligned
+ *   out  device, [num_seqs][q_len][num_heads][latent_dim] of out_dtype, 32-byte aligned
+ *   num_heads 1 to 128, q_len any; scale any finite number.
+ *   workspace  pa_decode_latent_workspace_size bytes, 256-byte aligned, the
+ *              first 256 zeroed before its first use; calls that overlap on the
+ *              GPU use different ones (so do graphs that may)
+ * Every table entry read must be in [0, num_blocks) and every length in
+ * [0, max_context_len]: one outside is read as block 0, or as an empty
+ * sequence, and pa_workspace_error() reports PA_ERR_INVALID_ARG.  Probabilities
+ * enter the product with the values in bf16.
+ */
+size_t pa_decode_latent_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_heads, int32_t latent_dim,
+                                       int32_t rope_dim, int32_t block_size, int32_t max_context_len);
+pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t num_seqs, int32_t q_len,
+                           int32_t num_heads, const void* cache, int32_t num_blocks, int32_t block_size,
+                           int32_t latent_dim, int32_t rope_dim, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len,
+                           float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Causal attention of chunks over a latent cache, expanded form: keys and
+ * values of every head are formed from the cached rows (c, r) of the sequence,
+ *   k[h][t] = (w_k[h] c_t, r_t)     v[h][t] = w_v[h] c_t
+ * rounded to bf16 in the workspace, and the chunk's queries attend to them.
+ * Chunk i is q[cu_q[i] .. cu_q[i+1]) at positions q_start[i] + 0, 1, ..., whose
+ * rows are in the cache already; query j sees the positions up to its own.
+ *   q          device, bf16 [num_tokens][num_heads][head_dim + rope_dim], 16-byte aligned
+ *   w_k, w_v   device, bf16 [num_heads][head_dim][latent_dim], 16-byte aligned
+ *   out        device, [num_tokens][num_heads][head_dim] of out_dtype, 32-byte aligned
+ *   head_dim 128; num_heads 1 to 65535; scale positive
+ *   total_context  at least the sum of q_start[i] + chunk length over the
+ *              chunks that are not empty (host bound; it sizes the workspace)
+ *   status     device int32, caller-zeroed, or NULL: PA_ERR_INVALID_ARG for a
+ *              chunk that lies outside q, is longer than max_q_len, ends behind
+ *              its table or max_context_len, or whose context does not fit
+ *              total_context (its rows stay as they are), and for a table entry
+ *              outside the pool (read as block 0); PA_ERR_DEVICE_TIMEOUT
+ *   workspace  pa_prefill_latent_workspace_size bytes, 256-byte aligned, needs
+ *              no initialisation; calls that overlap on the GPU use different ones
+ */
+size_t pa_prefill_latent_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
+                                        int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                        int32_t max_context_len, int64_t total_context);
+pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_t num_tokens, const int32_t* cu_q,
+                            const int32_t* q_start, int32_t num_seqs, int32_t max_q_len, int32_t max_context_len,
+                            int64_t total_context, int32_t num_heads, const void* cache, int32_t num_blocks,
+                            int32_t block_size, int32_t latent_dim, int32_t rope_dim, const void* w_k, const void* w_v,
+                            int32_t head_dim, const int32_t* block_tables, int32_t max_blocks_per_seq, float scale,
+                            int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention weight: what a long context's tokens are
+ * worth to the queries that followed them, and which of them stay.  The kept
+ * positions go to pa_compact_tokens as they are.
+ *
+ * pa_accumulate_weights: the queries of a window (one for a decode step, the
+ * last ones of a prompt after a prefill) at positions context_lens[i] - window
+ * + j; for t < context_lens[i]
+ *   weights[i][t] += sum over j and query heads h of p[i][j][h][t],
+ *   p = softmax over t <= position of scale * q[i][j][h] . K_t (h's kv head).
+ * Queries at positions below 0 add nothing; entries from context_lens[i] on
+ * stay as they are.  The sum is taken in fp32 in a fixed order.
+ *   weights  device fp32, rows weights_stride (>= max_context_len) apart
+ *   q        device, bf16 [num_seqs][window][num_q_heads][head_dim], 16-byte aligned
+ *   k_cache  bf16 [num_blocks][num_kv_heads][block_size][head_dim]; head_dim 64,
+ *            128, 256, or 576 (a latent cache: one kv head); block_size 8 to
+ *            256; num_q_heads / num_kv_heads 1 to 128; up to 65535 sequences
+ *   workspace, tables and lengths: as in pa_decode_latent
+ *
+ * pa_select_tokens: of sequence i's positions [dst_start[i], context_lens[i])
+ * the n = cu_keep[i+1] - cu_keep[i] that stay: the last min(recent, n), and of
+ * the others those with the largest weights (equal weights: the lower position
+ * first; NaN: below every number).  keep[cu_keep[i] ..] receives them in
+ * ascending order, and the weights move along: weights[i][dst_start[i] + j] is
+ * that of the j-th kept position, the entries up to context_lens[i] become 0.
+ *   keep     device int32 [num_keep];  cu_keep  device int32 [num_seqs + 1]
+ *   status   device int32, caller-zeroed, or NULL: PA_ERR_INVALID_ARG for a
+ *            sequence whose range lies outside keep, is longer than its
+ *            positions, or whose length passes max_context_len; it is left alone
+ * ---------------------------------------------------------------------- */
+size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t window, int32_t num_q_heads,
+                                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                            int32_t max_context_len);
+pa_status pa_accumulate_weights(float* weights, int64_t weights_stride, const void* q, int32_t num_seqs,
+                                int32_t window, int32_t num_q_heads, const void* k_cache, int32_t num_blocks,
+                                int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                int32_t max_context_len, float scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
+pa_status pa_select_tokens(int32_t* keep, int32_t num_keep, const int32_t* cu_keep, float* weights,
+                           int64_t weights_stride, const int32_t* dst_start, const int32_t* context_lens,
+                           int32_t num_seqs, int32_t recent, int32_t max_context_len, int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------
  * Host block allocator -- [vLLM2] block-table section and [KV02] section 2:
  * fixed-size blocks handed out on demand from anywhere in the pool; [PA]
  * "Block Table 如何工作": full blocks trigger a new allocation, freed blocks

@@ -71,6 +71,20 @@ SIGNATURES = {
                                 vp]),
     "pa_compact_tokens_checked": (i32, [vp, vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, i32, i32,
                                         vp, vp]),
+    "pa_reshape_and_cache_latent": (i32, [vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+    "pa_copy_blocks_latent": (i32, [vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp]),
+    "pa_compact_tokens_latent": (i32, [vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, i32, i32, vp,
+                                       vp]),
+    "pa_decode_latent_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+    "pa_decode_latent": (i32, [vp, i32, vp, i32, i32, i32, vp, i32, i32, i32, i32, vp, i32, vp, i32, f32, vp,
+                               C.c_size_t, vp]),
+    "pa_prefill_latent_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32, i32, i64]),
+    "pa_prefill_latent": (i32, [vp, i32, vp, i32, vp, vp, i32, i32, i32, i64, i32, vp, i32, i32, i32, i32, vp, vp, i32,
+                                vp, i32, f32, vp, vp, C.c_size_t, vp]),
+    "pa_accumulate_weights_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+    "pa_accumulate_weights": (i32, [vp, i64, vp, i32, i32, i32, vp, i32, i32, i32, i32, vp, i32, vp, i32, f32, vp,
+                                    C.c_size_t, vp]),
+    "pa_select_tokens": (i32, [vp, i32, vp, vp, i64, vp, vp, i32, i32, i32, vp, vp]),
     "pa_alloc_create": (i32, [i32, i32, P_i32, C.POINTER(vp)]),
     "pa_alloc_destroy": (None, [vp]),
     "pa_alloc_num_blocks": (i32, [vp]),

@@ -275,6 +275,24 @@ bool encode_kv_groups(CUtensorMap* m, const void* base, uint64_t rows, uint32_t 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace pa {
+bool encode_bf16_tiles(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box, int swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc || rank < 1 || rank > 5) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i], es[i] = 1;
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace pa
+
+namespace {
 // Per-kernel dynamic shared memory attribute and occupancy, cached.
 struct KernelCache {
   const void* fn;
@@ -429,7 +447,7 @@ pa_status copy_blocks_impl(void* k_cache, void* v_cache, int64_t cache_layer_str
   if (status && !aligned4(status)) return PA_ERR_INVALID_ARG;
   const int64_t block_bytes = static_cast<int64_t>(num_kv_heads) * tile * e;
   cudaError_t err = pa::launch_copy_blocks(k_cache, v_cache,
-                                           num_layers > 1 ? cache_layer_stride * e : 0, num_layers,
+                                           num_layers > 1 ? cache_layer_stride * e : 0, 2 * num_layers,
                                            num_blocks, block_bytes, block_pairs, num_pairs, status,
                                            static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -85,7 +85,7 @@ pa_status compact_impl(void* k_cache, void* v_cache, int64_t cache_layer_stride,
   p.keep = keep;
   p.cu_keep = cu_keep;
   p.status = status;
-  p.num_layers = num_layers;
+  p.num_planes = 2 * num_layers;
   p.num_blocks = num_blocks;
   p.block_size = block_size;
   p.num_kv_heads = num_kv_heads;

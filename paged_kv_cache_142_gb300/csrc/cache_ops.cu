@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// blockIdx.x: pair; blockIdx.y: layer * 2 + (0 K, 1 V); blockIdx.z: slice of
+// blockIdx.x: pair; blockIdx.y: plane, layer * 2 + (0 K, 1 V) (latent caches:
+// the layer, even ones from k_cache on and odd ones from v_cache); blockIdx.z: slice of
 // the block.  gate (checked mode): nothing is copied while *gate != 0.
 __global__ void __launch_bounds__(256)
     copy_blocks_kernel(uint4* __restrict__ k_cache, uint4* __restrict__ v_cache,
@@ -149,7 +150,7 @@ cudaError_t launch_reshape_and_cache(const void* key, const void* value, int64_t
 }
 
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, int64_t cache_layer_bytes,
-                               int32_t num_layers, int32_t num_blocks, int64_t block_bytes,
+                               int32_t num_planes, int32_t num_blocks, int64_t block_bytes,
                                const int64_t* pairs, int32_t num_pairs, int32_t* status,
                                cudaStream_t stream) {
   if (status) {
@@ -164,7 +165,7 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, int64_t cache_layer
   int64_t split = (chunks + threads * 8 - 1) / (threads * 8);
   if (split < 1) split = 1;
   if (split > 64) split = 64;
-  dim3 grid(static_cast<unsigned>(num_pairs), static_cast<unsigned>(2 * num_layers),
+  dim3 grid(static_cast<unsigned>(num_pairs), static_cast<unsigned>(num_planes),
             static_cast<unsigned>(split));
   copy_blocks_kernel<<<grid, threads, 0, stream>>>(static_cast<uint4*>(k_cache),
                                                    static_cast<uint4*>(v_cache),

@@ -3,7 +3,7 @@
 //   position dst_start + j  :=  position keep[j],   keep[j] >= dst_start + j.
 //
 // One CTA owns the rows of one (sequence, head group) in a few planes (a plane:
-// the K or V cache of a layer), so no other CTA reads or writes them.  It walks
+// the K or V cache of a layer, or a layer of a latent cache), so no other CTA reads or writes them.  It walks
 // the kept tokens in chunks, and a chunk plane by plane: all of its rows are
 // read into registers, the CTA synchronises, then they are written.  keep
 // ascends, so every later source lies at or behind its own destination and so
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int seq = blockIdx.x;
-  const int plane0 = blockIdx.z * planes, plane1 = min(2 * p.num_layers, plane0 + planes);
+  const int plane0 = blockIdx.z * planes, plane1 = min(p.num_planes, plane0 + planes);
   auto cache_of = [&](int plane) {
     return ((plane & 1) ? p.v_cache : p.k_cache) + (plane >> 1) * p.layer_bytes;
   };
@@ -169,9 +169,9 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   // as few planes a CTA as let all CTAs run at once (an SM holds 1024 threads of them)
   const int64_t room = device_sm_count() * (1024 / threads), per_plane = static_cast<int64_t>(p.num_seqs) * groups;
   int planes = 1;
-  while (planes < 2 * p.num_layers && per_plane * ((2 * p.num_layers + planes - 1) / planes) > room) ++planes;
+  while (planes < p.num_planes && per_plane * ((p.num_planes + planes - 1) / planes) > room) ++planes;
   const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(groups),
-                  static_cast<unsigned>((2 * p.num_layers + planes - 1) / planes));
+                  static_cast<unsigned>((p.num_planes + planes - 1) / planes));
   return launch_early(planes > 1 ? compact_kernel<true> : compact_kernel<false>, grid, threads, stream, p, heads, units,
                       planes);
 }

@@ -127,8 +127,9 @@ cudaError_t launch_reshape_and_cache(const void* key, const void* value, int64_t
                                      int32_t block_size, int32_t num_kv_heads, int32_t row_bytes,
                                      int32_t* status, cudaStream_t stream);
 
+// plane i of the copy: (i even: k_cache, odd: v_cache) + i / 2 * cache_layer_bytes
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, int64_t cache_layer_bytes,
-                               int32_t num_layers, int32_t num_blocks, int64_t block_bytes,
+                               int32_t num_planes, int32_t num_blocks, int64_t block_bytes,
                                const int64_t* pairs, int32_t num_pairs, int32_t* status,
                                cudaStream_t stream);
 

@@ -78,6 +78,7 @@ size_t fp4_prefill_workspace(int num_seqs, int num_q_heads, int num_kv_heads, in
 cudaError_t launch_fp4_prefill(const Fp4AttnParams& p, cudaStream_t stream);
 
 struct CompactParams {
+  // plane i: (i even: k_cache, odd: v_cache) + i / 2 * layer_bytes
   unsigned char* k_cache;
   unsigned char* v_cache;
   int64_t layer_bytes;
@@ -86,7 +87,7 @@ struct CompactParams {
   const int32_t* keep;
   const int32_t* cu_keep;
   int32_t* status;
-  int32_t num_layers, num_blocks, block_size, num_kv_heads, max_blocks_per_seq, num_seqs, max_keep;
+  int32_t num_planes, num_blocks, block_size, num_kv_heads, max_blocks_per_seq, num_seqs, max_keep;
   int32_t num_keep;     // entries of keep; -1: what cu_keep says
   int32_t row_bytes;    // one token's row of one head (4-bit pages: its codes)
   int32_t scale_bytes;  // 4-bit pages: its scales, else 0

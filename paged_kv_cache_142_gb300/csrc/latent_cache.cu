@@ -1,0 +1,57 @@
+// Append to the latent cache: row slots[t] of the pool becomes (latent[t],
+// rope[t]).
+//
+// Pure data movement in 16-byte pieces.  A row is one run in the cache, so
+// consecutive threads write consecutive pieces of it; they read the latent part
+// and then the position part, whose rows may be slices of a wider tensor.
+#include "decode.cuh"
+#include "fp4.cuh"
+#include "latent.cuh"
+#include "ptx.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+
+__global__ void __launch_bounds__(kThreads)
+    latent_append_kernel(const unsigned char* latent, int64_t latent_stride, const unsigned char* rope,
+                         int64_t rope_stride, int32_t num_tokens, const int64_t* slots, uint4* cache,
+                         int64_t num_slots, int32_t latent_chunks, int32_t row_chunks, int32_t* status) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t total = static_cast<int64_t>(num_tokens) * row_chunks;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t t = i / row_chunks;
+    const int32_t c = static_cast<int32_t>(i - t * row_chunks);
+    const int64_t slot = slots[t];
+    if (slot < 0) continue;  // padding
+    if (slot >= num_slots) {  // past the pool: never written
+      if (status && c == 0) atomicExch(status, kDevErrInvalidArg);
+      continue;
+    }
+    const unsigned char* src = c < latent_chunks ? latent + t * latent_stride + static_cast<int64_t>(c) * 16
+                                                 : rope + t * rope_stride + static_cast<int64_t>(c - latent_chunks) * 16;
+    cache[slot * row_chunks + c] = *reinterpret_cast<const uint4*>(src);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const void* latent, int64_t latent_stride_bytes, const void* rope,
+                                 int64_t rope_stride_bytes, int32_t num_tokens, const int64_t* slots, void* cache,
+                                 int64_t num_slots, int32_t latent_bytes, int32_t rope_bytes, int32_t* status,
+                                 cudaStream_t stream) {
+  const int32_t row_chunks = (latent_bytes + rope_bytes) / 16;
+  const int64_t total = static_cast<int64_t>(num_tokens) * row_chunks;
+  int64_t blocks = (total + kThreads - 1) / kThreads;
+  const int64_t cap = device_sm_count() * 16;
+  if (blocks > cap) blocks = cap;
+  return launch_early(latent_append_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, stream,
+                      static_cast<const unsigned char*>(latent), latent_stride_bytes,
+                      static_cast<const unsigned char*>(rope), rope_stride_bytes, num_tokens, slots,
+                      static_cast<uint4*>(cache), num_slots, latent_bytes / 16, row_chunks, status);
+}
+
+}  // namespace pa

@@ -528,6 +528,246 @@ def pa_compact_tokens(k_cache, v_cache, block_tables, dst_start, keep, cu_keep, 
 
 
 # --------------------------------------------------------------------------
+# the latent cache
+# --------------------------------------------------------------------------
+def _latent_dims(cache):
+    """(layers, layer stride, NB, bs, row) of a latent cache [NB, bs, row], with a leading layer dimension or without."""
+    if cache.dim() not in (3, 4) or not (cache if cache.dim() == 3 else cache[0]).is_contiguous():
+        raise ValueError("a latent cache must be [NB, bs, latent + rope] or [L, NB, bs, latent + rope], each layer contiguous")
+    if cache.dim() == 3:
+        return (1, 0, *cache.shape)
+    return (cache.shape[0], cache.stride(0), *cache.shape[1:])
+
+
+def _tables_of(block_tables, num_seqs):
+    if not (block_tables.dtype is torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == num_seqs
+            and block_tables.is_contiguous()):
+        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks]")
+
+
+def _workspace(workspace):
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA uint8 tensor")
+
+
+def pa_reshape_and_cache_latent(latent, rope, slot_mapping, cache, stream=None, status=None) -> None:
+    """Write the rows ``(latent[t], rope[t])`` of ``[T, latent]`` and ``[T, rope]``
+    (slices of a wider tensor are fine) into the slots ``slot_mapping[T]`` of a
+    latent cache ``[NB, bs, latent + rope]``."""
+    if latent.dim() != 2 or rope.dim() != 2 or rope.shape[0] != latent.shape[0]:
+        raise ValueError("latent and rope must be [T, latent] and [T, rope]")
+    T, dl = latent.shape
+    dr = rope.shape[1]
+    if cache.dim() != 3 or not cache.is_contiguous() or cache.shape[2] != dl + dr:
+        raise ValueError("cache must be a contiguous [NB, bs, latent + rope]")
+    if latent.dtype is not cache.dtype or rope.dtype is not cache.dtype:
+        raise ValueError("latent, rope and cache must share a dtype")
+    if T and (latent.stride(1) != 1 or rope.stride(1) != 1):
+        raise ValueError("rows of latent and rope must be contiguous")
+    if not (slot_mapping.dtype is torch.int64 and slot_mapping.numel() == T and slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping must be a contiguous CUDA int64 tensor of num_tokens entries")
+    dev = torch.cuda.current_device()
+    _all_on(dev, latent, rope, slot_mapping, cache)
+    if status is not None:
+        _all_on(dev, status)
+    L.check(_LIB.pa_reshape_and_cache_latent(
+        latent.data_ptr(), latent.stride(0), rope.data_ptr(), rope.stride(0), T, slot_mapping.data_ptr(),
+        cache.data_ptr(), cache.shape[0], cache.shape[1], dl, dr, dtype_code(cache.dtype), _status_ptr(status),
+        _stream(stream, dev)), "pa_reshape_and_cache_latent")
+
+
+def pa_copy_blocks_latent(cache, block_pairs, rope_dim=64, stream=None, status=None) -> None:
+    """cache[dst] = cache[src] for every row (src, dst) of ``block_pairs``, in
+    every layer of a latent cache ``[NB, bs, row]`` or ``[L, NB, bs, row]``.
+    ``status``: the pairs are validated first, and nothing is copied if one is
+    invalid."""
+    layers, stride, NB, bs, row = _latent_dims(cache)
+    n = block_pairs.shape[0] if block_pairs.numel() else 0
+    dev = torch.cuda.current_device()
+    _all_on(dev, cache)
+    if n:
+        _need(block_pairs.dtype == torch.int64 and block_pairs.is_contiguous() and block_pairs.shape == (n, 2),
+              "block_pairs must be a contiguous CUDA int64 [n, 2]")
+        _all_on(dev, block_pairs)
+    if status is not None:
+        _all_on(dev, status)
+    L.check(_LIB.pa_copy_blocks_latent(
+        cache.data_ptr(), stride, layers, NB, bs, row - rope_dim, rope_dim, dtype_code(cache.dtype),
+        block_pairs.data_ptr() if n else None, n, _status_ptr(status), _stream(stream, dev)), "pa_copy_blocks_latent")
+
+
+def pa_compact_tokens_latent(cache, block_tables, dst_start, keep, cu_keep, max_keep, rope_dim=64, status=None,
+                             stream=None) -> None:
+    """pa_compact_tokens over a latent cache ``[NB, bs, row]`` or ``[L, NB, bs, row]``."""
+    layers, stride, NB, bs, row = _latent_dims(cache)
+    S = dst_start.numel()
+    _i32(dst_start, S, "dst_start")
+    _i32(cu_keep, S + 1, "cu_keep")
+    _i32(keep, keep.numel(), "keep")
+    _tables_of(block_tables, S)
+    dev = torch.cuda.current_device()
+    _all_on(dev, cache, block_tables, dst_start, keep, cu_keep)
+    if status is not None:
+        _all_on(dev, status)
+    L.check(_LIB.pa_compact_tokens_latent(
+        cache.data_ptr(), stride, layers, NB, bs, row - rope_dim, rope_dim, dtype_code(cache.dtype),
+        block_tables.data_ptr(), block_tables.shape[1], dst_start.data_ptr(), keep.data_ptr(), keep.numel(),
+        cu_keep.data_ptr(), S, min(int(max_keep), keep.numel()), _status_ptr(status), _stream(stream, dev)),
+        "pa_compact_tokens_latent")
+
+
+def make_workspace_latent(num_seqs, q_len, num_heads, latent_dim, rope_dim, block_size, max_context_len,
+                          device="cuda") -> torch.Tensor:
+    """A zero-filled pa_decode_latent workspace of the required size."""
+    n = _LIB.pa_decode_latent_workspace_size(num_seqs, q_len, num_heads, latent_dim, rope_dim, block_size,
+                                             int(max_context_len))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_decode_latent_workspace_size")
+    return torch.zeros(int(n), dtype=torch.uint8, device=device)
+
+
+def pa_decode_latent(out, q, cache, block_tables, context_lens, scale, max_context_len, workspace,
+                     stream=None) -> None:
+    """Absorbed attention of the last tokens of every sequence over a latent
+    cache: ``q`` (bf16) ``[B, H, latent + rope]``, or ``[B, Q, H, latent + rope]``
+    for the last Q tokens; ``out`` alike with ``latent`` columns."""
+    if q.dim() not in (3, 4) or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA bf16 tensor [B, H, row] or [B, Q, H, row]")
+    B, H, row = q.shape[0], q.shape[-2], q.shape[-1]
+    Q = q.shape[1] if q.dim() == 4 else 1
+    if cache.dim() != 3 or cache.dtype is not torch.bfloat16 or not cache.is_contiguous() or cache.shape[2] != row:
+        raise ValueError("cache must be a contiguous bf16 [NB, bs, row] with q's row")
+    if (out.shape[:-1] != q.shape[:-1] or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16)
+            or out.shape[-1] >= row):
+        raise ValueError("out must be a contiguous fp32 or bf16 tensor of q's shape with latent columns")
+    _tables_of(block_tables, B)
+    _i32(context_lens, B, "context_lens")
+    _workspace(workspace)
+    dev = torch.cuda.current_device()
+    _all_on(dev, out, q, cache, block_tables, context_lens, workspace)
+    latent = out.shape[-1]
+    L.check(_LIB.pa_decode_latent(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), B, Q, H, cache.data_ptr(), cache.shape[0], cache.shape[1],
+        latent, row - latent, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+        int(max_context_len), float(scale), workspace.data_ptr(), workspace.numel(), _stream(stream, dev)),
+        "pa_decode_latent")
+
+
+def make_prefill_workspace_latent(num_seqs, num_heads, latent_dim, rope_dim, head_dim, block_size, max_q_len,
+                                  max_context_len, total_context, device="cuda") -> torch.Tensor:
+    """A pa_prefill_latent workspace of the required size: it holds the expanded
+    keys and values of ``total_context`` tokens (the chunks' contexts together)."""
+    n = _LIB.pa_prefill_latent_workspace_size(num_seqs, num_heads, latent_dim, rope_dim, head_dim, block_size,
+                                              int(max_q_len), int(max_context_len), int(total_context))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_prefill_latent_workspace_size")
+    return torch.empty(int(n), dtype=torch.uint8, device=device)
+
+
+def pa_prefill_latent(out, q, cache, w_k, w_v, cu_q, q_start, block_tables, scale, max_q_len, max_context_len,
+                      total_context, workspace, status=None, stream=None) -> None:
+    """Causal attention of each sequence's chunk ``q[cu_q[i]:cu_q[i+1]]`` (bf16
+    ``[T, H, head + rope]``, positions from ``q_start[i]``) over keys and values
+    expanded from a latent cache by ``w_k`` and ``w_v`` ``[H, head, latent]``."""
+    if q.dim() != 3 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA bf16 tensor [T, H, head + rope]")
+    T, H, dq = q.shape
+    if w_k.dim() != 3 or w_v.shape != w_k.shape or w_k.shape[0] != H:
+        raise ValueError("w_k and w_v must be [H, head, latent] both")
+    _, head, latent = w_k.shape
+    if not (w_k.dtype is torch.bfloat16 and w_v.dtype is torch.bfloat16 and w_k.is_contiguous() and w_v.is_contiguous()):
+        raise ValueError("w_k and w_v must be contiguous CUDA bf16 tensors")
+    rope = dq - head
+    if cache.dim() != 3 or cache.dtype is not torch.bfloat16 or not cache.is_contiguous() or cache.shape[2] != latent + rope:
+        raise ValueError("cache must be a contiguous bf16 [NB, bs, latent + rope]")
+    if out.shape != (T, H, head) or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be a contiguous fp32 or bf16 [T, H, head]")
+    S = cu_q.numel() - 1
+    _i32(cu_q, S + 1, "cu_q")
+    _i32(q_start, S, "q_start")
+    _tables_of(block_tables, S)
+    _workspace(workspace)
+    dev = torch.cuda.current_device()
+    _all_on(dev, out, q, cache, w_k, w_v, cu_q, q_start, block_tables, workspace)
+    if status is not None:
+        _all_on(dev, status)
+    L.check(_LIB.pa_prefill_latent(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), T, cu_q.data_ptr(), q_start.data_ptr(), S, int(max_q_len),
+        int(max_context_len), int(total_context), H, cache.data_ptr(), cache.shape[0], cache.shape[1], latent, rope,
+        w_k.data_ptr(), w_v.data_ptr(), head, block_tables.data_ptr(), block_tables.shape[1], float(scale),
+        _status_ptr(status), workspace.data_ptr(), workspace.numel(), _stream(stream, dev)), "pa_prefill_latent")
+
+
+# --------------------------------------------------------------------------
+# eviction by accumulated attention weight
+# --------------------------------------------------------------------------
+def make_workspace_weights(num_seqs, window, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                           device="cuda") -> torch.Tensor:
+    """A zero-filled pa_accumulate_weights workspace of the required size."""
+    n = _LIB.pa_accumulate_weights_workspace_size(num_seqs, window, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                  int(max_context_len))
+    if n == 0:
+        raise PAError(L.PA_ERR_UNSUPPORTED, "pa_accumulate_weights_workspace_size")
+    return torch.zeros(int(n), dtype=torch.uint8, device=device)
+
+
+def _weights_rows(weights, num_seqs, max_context_len):
+    if not (weights.dtype is torch.float32 and weights.dim() == 2 and weights.shape[0] == num_seqs
+            and weights.stride(1) == 1 and weights.shape[1] >= max_context_len):
+        raise ValueError("weights must be fp32 [num_seqs, at least max_context_len] with contiguous rows")
+
+
+def pa_accumulate_weights(weights, q, k_cache, block_tables, context_lens, scale, num_kv_heads, max_context_len,
+                          workspace, stream=None) -> None:
+    """weights[i, t] += the attention that the queries ``q`` (bf16 ``[B, H, D]``,
+    or ``[B, W, H, D]`` for the last W tokens) pay token t, over queries and
+    heads.  ``k_cache`` bf16 ``[NB, Hkv, bs, D]`` or a latent cache ``[NB, bs, D]``."""
+    if q.dim() not in (3, 4) or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA bf16 tensor [B, H, D] or [B, W, H, D]")
+    B, H, D = q.shape[0], q.shape[-2], q.shape[-1]
+    W = q.shape[1] if q.dim() == 4 else 1
+    if k_cache.dim() == 3:
+        k_cache = k_cache.unsqueeze(1)
+    if k_cache.dim() != 4 or k_cache.dtype is not torch.bfloat16 or not k_cache.is_contiguous() or k_cache.shape[3] != D:
+        raise ValueError("k_cache must be a contiguous bf16 [NB, Hkv, bs, D] with q's head_dim")
+    NB, Hkv, bs, _ = k_cache.shape
+    if Hkv != num_kv_heads:
+        raise ValueError("num_kv_heads does not match the cache")
+    _weights_rows(weights, B, int(max_context_len))
+    _tables_of(block_tables, B)
+    _i32(context_lens, B, "context_lens")
+    _workspace(workspace)
+    dev = torch.cuda.current_device()
+    _all_on(dev, weights, q, k_cache, block_tables, context_lens, workspace)
+    L.check(_LIB.pa_accumulate_weights(
+        weights.data_ptr(), weights.stride(0), q.data_ptr(), B, W, H, k_cache.data_ptr(), NB, bs, Hkv, D,
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), float(scale),
+        workspace.data_ptr(), workspace.numel(), _stream(stream, dev)), "pa_accumulate_weights")
+
+
+def pa_select_tokens(keep, cu_keep, weights, dst_start, context_lens, recent, max_context_len, status=None,
+                     stream=None) -> None:
+    """Fill ``keep[cu_keep[i]:cu_keep[i+1]]`` with the positions of ``[dst_start[i],
+    context_lens[i])`` that stay: the last ``recent`` and those with the largest
+    ``weights[i]``, ascending; the weights move to the places that
+    pa_compact_tokens gives the tokens."""
+    S = dst_start.numel()
+    _i32(dst_start, S, "dst_start")
+    _i32(context_lens, S, "context_lens")
+    _i32(cu_keep, S + 1, "cu_keep")
+    _i32(keep, keep.numel(), "keep")
+    _weights_rows(weights, S, int(max_context_len))
+    dev = torch.cuda.current_device()
+    _all_on(dev, keep, cu_keep, weights, dst_start, context_lens)
+    if status is not None:
+        _all_on(dev, status)
+    L.check(_LIB.pa_select_tokens(
+        keep.data_ptr(), keep.numel(), cu_keep.data_ptr(), weights.data_ptr(), weights.stride(0), dst_start.data_ptr(),
+        context_lens.data_ptr(), S, int(recent), int(max_context_len), _status_ptr(status), _stream(stream, dev)),
+        "pa_select_tokens")
+
+
+# --------------------------------------------------------------------------
 # host allocator
 # --------------------------------------------------------------------------
 def _p32(a: np.ndarray):
