@@ -35,6 +35,9 @@ pa_status check_attention(int32_t num_blocks, int32_t block_size, int32_t latent
   return latent_dim == 512 && rope_dim == 64 && block_size >= 8 ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
+// a pool's rows are numbered in 32 bits by the tensor loads
+bool pool_ok(int64_t tiles, int32_t block_size) { return tiles * block_size < (int64_t(1) << 31); }
+
 bool table_ok(int32_t max_blocks_per_seq, int32_t block_size, int32_t max_context_len) {
   return max_blocks_per_seq > 0 && max_context_len >= 0 &&
          static_cast<int64_t>(max_blocks_per_seq) * block_size >= max_context_len;
@@ -135,7 +138,7 @@ size_t pa_decode_latent_workspace_size(int32_t num_seqs, int32_t q_len, int32_t 
       max_context_len > kMaxContext || check_attention(1, block_size, latent_dim, rope_dim) != PA_OK ||
       static_cast<int64_t>(num_seqs) * q_len * num_heads >= (int64_t(1) << 31))
     return 0;
-  return pa::latent_decode_workspace(num_seqs, q_len, num_heads, latent_dim);
+  return pa::latent_decode_workspace(num_seqs, q_len, num_heads, max_context_len);
 }
 
 pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t num_seqs, int32_t q_len,
@@ -149,7 +152,7 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
     return PA_ERR_INVALID_ARG;
   const size_t need = pa_decode_latent_workspace_size(num_seqs, q_len, num_heads, latent_dim, rope_dim, block_size,
                                                       max_context_len);
-  if (need == 0) return PA_ERR_UNSUPPORTED;
+  if (need == 0 || !pool_ok(num_blocks, block_size)) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!out || !q || !cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 32) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
@@ -202,7 +205,7 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
     return PA_ERR_INVALID_ARG;
   const size_t need = pa_prefill_latent_workspace_size(num_seqs, num_heads, latent_dim, rope_dim, head_dim, block_size,
                                                        max_q_len, max_context_len, total_context);
-  if (need == 0) return PA_ERR_UNSUPPORTED;
+  if (need == 0 || !pool_ok(num_blocks, block_size)) return PA_ERR_UNSUPPORTED;
   if (num_tokens == 0 || num_seqs == 0 || max_q_len == 0) return PA_OK;
   if (!out || !q || !cu_q || !q_start || !cache || !w_k || !w_v || !block_tables) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 32) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(w_k, 16) || !aligned(w_v, 16) ||
@@ -261,7 +264,7 @@ pa_status pa_accumulate_weights(float* weights, int64_t weights_stride, const vo
     return PA_ERR_INVALID_ARG;
   const size_t need = pa_accumulate_weights_workspace_size(num_seqs, window, num_q_heads, num_kv_heads, head_dim,
                                                            block_size, max_context_len);
-  if (need == 0) return PA_ERR_UNSUPPORTED;
+  if (need == 0 || !pool_ok(static_cast<int64_t>(num_blocks) * num_kv_heads, block_size)) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0 || max_context_len == 0) return PA_OK;
   if (!weights || !q || !k_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
   if (!aligned(weights, 4) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(block_tables, 4) ||

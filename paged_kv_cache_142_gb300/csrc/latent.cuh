@@ -73,7 +73,7 @@ cudaError_t launch_latent_append(const void* latent, int64_t latent_stride_bytes
                                  int64_t rope_stride_bytes, int32_t num_tokens, const int64_t* slots, void* cache,
                                  int64_t num_slots, int32_t latent_bytes, int32_t rope_bytes, int32_t* status,
                                  cudaStream_t stream);
-size_t latent_decode_workspace(int num_seqs, int q_len, int num_heads, int latent_dim);
+size_t latent_decode_workspace(int num_seqs, int q_len, int num_heads, int max_context_len);
 cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t stream);
 size_t latent_prefill_workspace(int num_seqs, int num_heads, int latent_dim, int rope_dim, int head_dim,
                                 int64_t total_context);

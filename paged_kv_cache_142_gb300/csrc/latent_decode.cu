@@ -1,6 +1,37 @@
-// Attention over the latent cache in its absorbed form.
-//   s[h,t] = scale q[h] . row[t],  out[h] = sum_t softmax(s)[t] row[t][:latent]
-// A warp for each query row; its lanes share the row's dims.
+// Attention over the latent cache in its absorbed form, on the 5th-generation
+// tensor cores; latent_dim 512, rope_dim 64.
+//
+//   S[128 rows x 64 tokens] = Q K^T,   P = 2^(S f - m),   O[128 x 512] += P V
+// A row is one head of one query token; K is the cached row (576 values), V its
+// first 512.  Every head shares the rows, so a step does 4.4 MFLOP a token for
+// 1152 bytes (128 heads): bytes and products are in balance, and both have to
+// stream.
+//
+// O alone is 256 KB in fp32, all of an SM's tensor memory, so a cluster of two
+// CTAs shares an item by columns: CTA c holds columns 256 c .. of the latent
+// part and half of the position part, of all rows and all tokens.  No byte of
+// the cache is loaded twice.
+//   S: each CTA forms the product over its own 288 columns and both add them up:
+//      a CTA finishes the rows 64 c .. 64 c + 63 and gets the other's partial
+//      sums of them through distributed shared memory (16 KB a tile).
+//   P: finished by the CTA that owns the row, written into its own shared
+//      memory and copied into the other's (8 KB), as both need all rows for
+//      their columns of O.  Maximum and sum of a row stay in one thread; the
+//      reference is raised only when the maximum passes it by 2^8, and then
+//      the other CTA gets the factor for its columns along with P.
+// The queries lie in tensor memory as the A operand (144 columns), so that
+// shared memory holds four tiles of K and V: three are in flight while one is
+// worked on.
+//
+// fp32 outputs take the probabilities in two bf16 parts, P and what its
+// rounding left (2^-17 in all); bf16 outputs take one (2^-8, as the output).
+//
+// The work is cut into equal runs of tiles, one for each cluster, across the
+// borders of sequences; a cluster that takes part of an item leaves its rows
+// unnormalised in the workspace, and a second kernel adds the parts up.
+//
+// One CTA per SM, 6 warps: 0-3 scores and outputs (a row a thread: two warps
+// finish rows, two ship partial sums), 4 loads, 5 issues products.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -8,63 +39,756 @@
 #include "fp4.cuh"
 #include "latent.cuh"
 #include "ptx.cuh"
+#include "umma.cuh"
 
 namespace pa {
-namespace {
+namespace latent_decode_detail {
 
-__global__ void __launch_bounds__(128) latent_decode_kernel(const LatentDecodeParams p) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t per_seq = static_cast<int64_t>(p.q_len) * p.num_heads;
-  if (row >= per_seq * p.num_seqs) return;
-  const int seq = static_cast<int>(row / per_seq);
-  const int j = static_cast<int>(row % per_seq) / p.num_heads;
-  const int dim = p.latent_dim + p.rope_dim, mine = dim / 32;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row * dim;
-  float qv[18], acc[18];
-  for (int i = 0; i < mine; ++i) qv[i] = __bfloat162float(q[i * 32 + lane]) * p.scale_log2, acc[i] = 0.f;
-  float m = -CUDART_INF_F, l = 0.f;
-  int len = p.context_lens[seq];
-  if (len > p.max_context_len || len < 0) {
-    if (lane == 0) atomicExch(p.err, kDevErrInvalidArg);
-    len = 0;
+using namespace um;
+
+constexpr int kThreads = 6 * 32;
+constexpr int kTile = 64;                      // tokens
+constexpr int kLatBytes = kTile * 512;         // [8-token group][4 chunks of 64 columns][8 rows x 128 bytes]
+constexpr int kRopeBytes = kTile * 64;         // [8-token group][8 rows x 64 bytes]
+constexpr int kStageBytes = kLatBytes + kRopeBytes;
+constexpr int kPBytes = 128 * 128;             // 128 rows x 64 bf16
+constexpr int kXBytes = 64 * kTile * 4;        // partial sums of 64 rows: [4-token group][row][4]
+constexpr uint32_t kColQ = 256, kColS = 400;   // tensor memory: O at 0
+constexpr float kSlack = 8.f;
+constexpr int kLead = 3;      // what starting and ending an item costs a cluster, in tiles
+constexpr int kMaxSeqs = 2048;  // of one launch: their places lie in shared memory
+constexpr int kMinTiles = 4;  // of a cluster's run, where there are enough clusters
+
+__host__ __device__ constexpr int stages_of(bool hi) { return hi ? 3 : 4; }
+
+// barriers ([2] or [4] each where they have a number)
+enum : int {
+  kFull = 0, kEmpty = 4, kQFull = 8, kSFull = 9, kSFree = 10, kXFull = 11, kXFree = 13, kPFull = 15, kPCopy = 17,
+  kPFree = 19, kODone = 21, kOFree = 22, kLFull = 23, kDrain = 24, kNumBars = 25
+};
+// shared memory, behind the stages: P slots, exchange slots, then
+constexpr int kOffBar = 0;
+constexpr int kOffAlpha = 256;                // [2 slots][own | other's][64]
+constexpr int kOffL = kOffAlpha + 1024;       // [64] the other CTA's 1 / sum
+constexpr int kOffPrefix = kOffL + 256;
+
+struct Launch {
+  LatentDecodeParams p;
+  int rows, row_tiles;   // of a sequence; tiles of 128
+  int bs_log, part_rows;
+  int num_clusters;
+  int4* desc;            // [clusters] the item that a cluster's run begins inside of: sequence (or -1), row tile, first and last cluster
+  float* ml;             // [2 * clusters][part_rows][2] maximum (log2), sum
+  float* o;              // [2 * clusters][part_rows][512]
+};
+
+// An item (a row tile of a sequence) and this cluster's part of it.
+struct Item {
+  int seq, rt, len, tiles;
+  int start, end;  // places: kLead, then the tiles
+  int t0, t1;
+  bool whole;
+};
+
+struct Walk {
+  const Launch& L;
+  const int* prefix;
+  int c_begin, c_end;
+  __device__ __forceinline__ int length(int seq) const {
+    const int n = L.p.context_lens[seq];
+    return n > 0 && n <= L.p.max_context_len ? n : 0;
   }
-  const int limit = len - p.q_len + 1 + j;
-  const int32_t* table = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq;
-  for (int t = 0; t < limit; ++t) {
-    int phys = table[t / p.block_size];
-    if (phys < 0 || phys >= p.num_blocks) {
-      if (lane == 0) atomicExch(p.err, kDevErrInvalidArg);
-      phys = 0;
+  __device__ __forceinline__ void derive(Item& it) const {
+    it.end = it.start + kLead + it.tiles;
+    const int first = it.start + kLead;
+    it.t0 = max(c_begin, first) - first;
+    it.t1 = min(c_end, it.end) - first;
+    it.whole = it.t0 == 0 && it.t1 == it.tiles;
+  }
+  __device__ __forceinline__ void open(Item& it) const {
+    it.len = length(it.seq);
+    it.tiles = (it.len + kTile - 1) / kTile;
+  }
+  // the item at c_begin
+  __device__ __noinline__ void find(Item& it) const {
+    int lo = 0, hi = L.p.num_seqs - 1;
+    while (lo < hi) {  // the last sequence that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= c_begin) lo = mid;
+      else hi = mid - 1;
     }
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.cache) +
-                             (static_cast<int64_t>(phys) * p.block_size + t % p.block_size) * dim;
-    float s = 0.f, kv[18];
-    for (int i = 0; i < mine; ++i) kv[i] = __bfloat162float(k[i * 32 + lane]), s = fmaf(qv[i], kv[i], s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s), ref = mn == -CUDART_INF_F ? 0.f : mn;
-    const float a = exp2f(m - ref), e = exp2f(s - ref);
-    l = l * a + e;
-    for (int i = 0; i < mine; ++i) acc[i] = fmaf(e, kv[i], acc[i] * a);
-    m = mn;
+    it.seq = lo;
+    open(it);
+    const int r = c_begin - prefix[lo];
+    it.rt = r / (kLead + it.tiles);
+    it.start = c_begin - r % (kLead + it.tiles);
+    derive(it);
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  for (int i = 0; i < p.latent_dim / 32; ++i) {
-    const int64_t at = row * p.latent_dim + i * 32 + lane;
-    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
-    else static_cast<float*>(p.out)[at] = acc[i] * inv;
+  __device__ __forceinline__ void next(Item& it) const {
+    it.start = it.end;
+    if (++it.rt == L.row_tiles) {
+      it.rt = 0;
+      do ++it.seq;
+      while (prefix[it.seq + 1] == it.start);  // sequences without places
+      open(it);
+    }
+    derive(it);
+  }
+  // calls f for every item with tiles of this cluster's
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    Item it;
+    it.end = c_begin;
+    for (bool more = c_begin < c_end; more;) {
+      if (it.end == c_begin) find(it);
+      else next(it);
+      more = it.end < c_end;
+      if (it.t1 > it.t0) f(it);
+    }
+  }
+};
+
+// keys that the last (first) row of a row tile sees
+__device__ __forceinline__ int seen_by(const Launch& L, const Item& it, int row) {
+  return it.len - L.p.q_len + 1 + row / L.p.num_heads;
+}
+
+// Sums over the parts, or zeros: outputs of 32 bytes and more
+__device__ __forceinline__ void store16(const LatentDecodeParams& p, int64_t at, const float (&v)[16]) {
+  uint32_t h[8];
+  if (p.out_bf16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    fp4::store32(static_cast<__nv_bfloat16*>(p.out) + at, h);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(v[8 * q + e]);
+      fp4::store32(static_cast<float*>(p.out) + at + 8 * q, h);
+    }
   }
 }
 
-}  // namespace
+template <bool HI>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_lat,
+                  const __grid_constant__ CUtensorMap tm_rope) {
+  constexpr int kStages = stages_of(HI), kParts = HI ? 2 : 1;
+  const LatentDecodeParams& p = L.p;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* smem_p = smem + kStages * kStageBytes;              // [2 slots][parts][128 rows]
+  unsigned char* smem_x = smem_p + 2 * kParts * kPBytes;             // [2 slots]
+  unsigned char* rest = smem_x + 2 * kXBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rest + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* alphas = reinterpret_cast<float*>(rest + kOffAlpha);
+  float* other_l = reinterpret_cast<float*>(rest + kOffL);
+  int* prefix = reinterpret_cast<int*>(rest + kOffPrefix);
+  __shared__ int warp_sums[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  const int cluster = blockIdx.x >> 1;
 
-size_t latent_decode_workspace(int, int, int, int) { return 256; }
+  ptx::griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&bars[kFull + i], 1);
+      ptx::mbar_init(&bars[kEmpty + i], 1);
+    }
+    ptx::mbar_init(&bars[kQFull], 4);
+    ptx::mbar_init(&bars[kSFull], 1);
+    ptx::mbar_init(&bars[kSFree], 4);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kXFull + i], 1);
+      ptx::mbar_init(&bars[kXFree + i], 2);
+      ptx::mbar_init(&bars[kPFull + i], 4);
+      ptx::mbar_init(&bars[kPCopy + i], 1);
+      ptx::mbar_init(&bars[kPFree + i], 2);
+    }
+    ptx::mbar_init(&bars[kODone], 1);
+    ptx::mbar_init(&bars[kOFree], 4);
+    ptx::mbar_init(&bars[kLFull], 1);
+    ptx::mbar_init(&bars[kDrain], 1);
+    *gave_up = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == 5) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool aborted = false;
+  ptx::griddep_wait();
+
+  // ---- places before every sequence; sequences without tokens: zeros ----
+  {
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int beg = min(p.num_seqs, tid * per), end = min(p.num_seqs, beg + per);
+    int local = 0;
+    for (int s = beg; s < end; ++s) {
+      const int n = p.context_lens[s];
+      int places = 0;
+      if (n > 0 && n <= p.max_context_len) places = (kLead + (n + kTile - 1) / kTile) * L.row_tiles;
+      else if (n != 0 && blockIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
+      prefix[s + 1] = places;
+      local += places;
+    }
+    int x = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int run = x - local;
+    for (int w = 0; w < warp; ++w) run += warp_sums[w];
+    if (tid == 0) prefix[0] = 0;
+    for (int s = beg; s < end; ++s) prefix[s + 1] = run += prefix[s + 1];
+    __syncthreads();
+    const float zero[16] = {};
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
+      if (prefix[s + 1] == prefix[s])
+        for (int64_t i = tid; i < static_cast<int64_t>(L.rows) * 32; i += kThreads)
+          store16(p, static_cast<int64_t>(s) * L.rows * 512 + i * 16, zero);
+  }
+  if (tid == 0 && rank == 0) L.desc[cluster] = make_int4(-1, 0, 0, 0);  // until it reports an item
+  cluster_sync();  // both CTAs' barriers are ready
+  const int total = prefix[p.num_seqs];
+  const int share = total / L.num_clusters, extra = total - share * L.num_clusters;
+  auto run_begin = [&](int c) { return c * share + min(c, extra); };
+  const Walk walk{L, prefix, run_begin(cluster), run_begin(cluster + 1)};
+
+  if (warp == 4) {
+    // ============================== loads ==============================
+    // lane i: the latent part of the tile's page i; lane 16 + i: its position part
+    const int page_rows = min(kTile, 1 << L.bs_log), pages = kTile / page_rows;
+    const int page = lane & 15;
+    const uint64_t policy = L.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+    uint32_t kt = 0;
+    if (lane == 0) {
+      ptx::prefetch_tensormap(&tm_lat);
+      ptx::prefetch_tensormap(&tm_rope);
+    }
+    walk.each([&](const Item& it) {
+      const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
+      const int kend = seen_by(L, it, min(L.rows, it.rt * 128 + 128) - 1);  // nobody sees what lies behind it
+      auto row_of = [&](int t) -> int {  // the page's first row in the pool, in 8-row groups; -1: nothing to load
+        const int tok = t * kTile + page * page_rows;
+        if (page >= pages || tok >= kend) return -1;
+        int phys = __ldg(table + (tok >> L.bs_log));
+        if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
+          atomicExch(p.err, kDevErrInvalidArg);
+          phys = 0;
+        }
+        return static_cast<int>((static_cast<int64_t>(phys) << L.bs_log) / 8) + (tok & ((1 << L.bs_log) - 1)) / 8;
+      };
+      int at = row_of(it.t0);
+      for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
+        const int now = at;
+        if (t + 1 < it.t1) at = row_of(t + 1);
+        const int slot = kt % kStages;
+        wait(&bars[kEmpty + slot], ((kt / kStages) & 1u) ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        const uint32_t have = __popc(__ballot_sync(0xffffffffu, now >= 0) & 0xffffu);
+        unsigned char* stage = smem + slot * kStageBytes;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kFull + slot], have * page_rows * (512 + 64));
+        __syncwarp();
+        if (now >= 0) {
+          if (lane < 16)
+            ptx::tma_load_4d(stage + page * page_rows * 512, &tm_lat, 0, 0, static_cast<int>(rank) * 4, now,
+                             &bars[kFull + slot], policy);
+          else
+            ptx::tma_load_2d(stage + kLatBytes + page * page_rows * 64, &tm_rope, static_cast<int>(rank) * 32, now * 8,
+                             &bars[kFull + slot], policy);
+        }
+        __syncwarp();
+      }
+    });
+  } else if (warp == 5) {
+    // ============================ products ============================
+    const bool leader = elect_one();
+    constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, kTile, 0, 0), kIdO = ptx::idesc_bf16_f32(128, 256, 0, 1);
+    const uint64_t desc_k = ptx::smem_desc(smem, 16, 4096, ptx::kLayoutSw128);
+    const uint64_t desc_r = ptx::smem_desc(smem + kLatBytes, 16, 512, kLayoutSw64);
+    const uint64_t desc_v = ptx::smem_desc(smem, 1024, 4096, ptx::kLayoutSw128);
+    const uint64_t desc_p = ptx::smem_desc(smem_p, 16, 1024, ptx::kLayoutSw128);
+    uint32_t kt = 0, items = 0;
+    auto values = [&](uint32_t k, bool first) {  // P V of tile k
+      wait(&bars[kPFull + (k & 1u)], (k >> 1) & 1u, aborted);
+      if (first) wait(&bars[kOFree], (items & 1u) ^ 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      ptx::tc_fence_after();
+      if (leader) {
+        const uint64_t dv = desc_v + (k % kStages) * (kStageBytes >> 4);
+        const uint64_t dp = desc_p + (k & 1u) * (kParts * kPBytes >> 4);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // 16 tokens each
+            ptx::umma_bf16(tmem, dp + h * (kPBytes >> 4) + j * 2, dv + j * (8192 >> 4), kIdO, h + j > 0 ? 1u : !first);
+        ptx::umma_commit(&bars[kEmpty + k % kStages]);
+        umma_commit_cluster(&bars[kPFree + (k & 1u)], 3);
+        ptx::umma_commit(&bars[kODone]);
+      }
+      __syncwarp();
+    };
+    walk.each([&](const Item& it) {
+      const int kend = seen_by(L, it, min(L.rows, it.rt * 128 + 128) - 1);
+      for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
+        const uint32_t slot = kt % kStages;
+        wait(&bars[kFull + slot], (kt / kStages) & 1u, aborted);
+        if (t == it.t0) wait(&bars[kQFull], items & 1u, aborted);
+        wait(&bars[kSFree], (kt & 1u) ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        unsigned char* stage = smem + slot * kStageBytes;
+        const int there = max(0, kend - t * kTile);
+        if (there < kTile) {
+          // rows behind the last token: zeros, whatever the page or an earlier
+          // tile left there (0 * NaN would reach O)
+          for (int i = there * 32 + lane; i < kTile * 32; i += 32) {
+            const int row = i >> 5, c = i & 31;
+            *reinterpret_cast<uint4*>(stage + (row >> 3) * 4096 + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ptx::tc_fence_after();
+        if (leader) {
+          const uint64_t dk = desc_k + slot * (kStageBytes >> 4), dr = desc_r + slot * (kStageBytes >> 4);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)  // chunks of 64 columns, 16 of them (32 bytes) each
+            umma_ts(tmem + kColS, tmem + kColQ + j * 8, dk + (j >> 2) * (1024 >> 4) + (j & 3) * 2, kIdS, j > 0);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) umma_ts(tmem + kColS, tmem + kColQ + 128 + j * 8, dr + j * 2, kIdS, 1);
+          ptx::umma_commit(&bars[kSFull]);
+        }
+        __syncwarp();
+        if (t > it.t0) values(kt - 1, t - 1 == it.t0);
+      }
+      if (!aborted) values(kt - 1, it.t1 - it.t0 == 1);
+      ++items;
+    });
+    // nothing may be in flight when tensor memory is freed
+    if (leader) {
+      ptx::umma_commit(&bars[kDrain]);
+      bool drain = false;
+      wait(&bars[kDrain], 0, drain);
+      if (drain) aborted = true;
+    }
+    aborted = __any_sync(0xffffffffu, aborted);
+  } else {
+    // ============ scores and outputs: one row per thread ============
+    const int r = tid;  // row of the tile, tensor-memory lane
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    const bool own = static_cast<uint32_t>(warp >> 1) == rank;
+    const int xr = r & 63;  // row among the 64 of a CTA
+    uint32_t kt = 0, items = 0;
+    const float f = p.scale_log2;
+    walk.each([&](const Item& it) {
+      const int row = it.rt * 128 + r;
+      const bool valid = row < L.rows;
+      const int last_row = min(L.rows, it.rt * 128 + 128) - 1;
+      const int limit = valid ? seen_by(L, it, row) : 0;
+      const int limit_min = seen_by(L, it, it.rt * 128), limit_max = seen_by(L, it, last_row);
+      const int64_t out_row = static_cast<int64_t>(it.seq) * L.rows + row;
+      // ---- queries into tensor memory: all products of the item before are complete ----
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + out_row * 576);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 x = valid ? __ldg(src + rank * 32 + c * 8 + e) : make_uint4(0, 0, 0, 0);
+            v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+          }
+          ptx::tmem_st32(tmem + lanes + kColQ + c * 32, v);
+        }
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 x = valid ? __ldg(src + 64 + rank * 4 + e) : make_uint4(0, 0, 0, 0);
+          v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+        }
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                tmem + lanes + kColQ + 128),
+            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+            "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+            : "memory");
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
+      }
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int t = it.t0; t < it.t1; ++t, ++kt) {
+        const uint32_t slot = kt & 1u, ph = (kt >> 1) & 1u;
+        // the columns of O, raised to a new reference once P V of the tile before is in them
+        auto rescale = [&](float alpha) {
+          wait(&bars[kODone], (kt - 1) & 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) return;
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[32];
+            ptx::TmemLd<32>::run(tmem + lanes + c * 32, v);
+            wait_ld32(v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+            ptx::tmem_st32(tmem + lanes + c * 32, v);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+        };
+        wait(&bars[kSFull], kt & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        ptx::tc_fence_after();
+        uint32_t s[64];
+        load64(tmem + lanes + kColS, s);
+        wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(s));
+        wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kSFree]);
+        // Tokens that some rows of the tile see and others do not: a value among
+        // this CTA's columns that is not finite makes every row's partial sum
+        // not finite.  It becomes zero, so that 0 * NaN does not reach the rows
+        // that do not see it; the others have the score.
+        if (warp == 0 && limit_min < limit_max && limit_min < (t + 1) * kTile) {
+          uint64_t odd = 0;
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= uint64_t(1) << j;
+          odd = __shfl_sync(0xffffffffu, odd, 0);
+          const int from = max(0, limit_min - t * kTile), upto = min(kTile, limit_max - t * kTile);
+          unsigned char* stage = smem + (kt % kStages) * kStageBytes;
+          for (int j = from; j < upto; ++j)
+            if ((odd >> j) & 1u)
+              *reinterpret_cast<uint4*>(stage + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          if (odd) ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!own) {
+          // ---- the other CTA's rows: its partial sums, then its probabilities ----
+          wait_cluster(&bars[kXFree + slot], ph ^ 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) return;
+          const uint32_t dst = remote(smem_x + slot * kXBytes, peer), bar = remote(&bars[kXFull + slot], peer);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            store_async4(dst + (j * 64 + xr) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
+                         __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
+          if (xr == 0) ptx::mbar_arrive_expect_tx(&bars[kPCopy + slot], kParts * kPBytes / 2 + 256);
+          wait_cluster(&bars[kPCopy + slot], ph, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) return;
+          const float alpha = alphas[slot * 128 + 64 + xr];
+          if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            rescale(alpha);
+            if (aborted) return;
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars[kPFull + slot]);
+          continue;
+        }
+        // ---- own rows: scores, probabilities ----
+        if (xr == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + slot], kXBytes);
+        wait_cluster(&bars[kXFull + slot], ph, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        float x[64];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float4 y = *reinterpret_cast<const float4*>(smem_x + slot * kXBytes + (j * 64 + xr) * 16);
+          x[4 * j] = (__uint_as_float(s[4 * j]) + y.x) * f;
+          x[4 * j + 1] = (__uint_as_float(s[4 * j + 1]) + y.y) * f;
+          x[4 * j + 2] = (__uint_as_float(s[4 * j + 2]) + y.z) * f;
+          x[4 * j + 3] = (__uint_as_float(s[4 * j + 3]) + y.w) * f;
+        }
+        __syncwarp();
+        if (lane == 0) remote_arrive(remote(&bars[kXFree + slot], peer));
+        const int nvis = limit - t * kTile;
+        if (!__all_sync(0xffffffffu, nvis >= kTile)) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j >= nvis) x[j] = -CUDART_INF_F;
+        }
+        float m0 = x[0], m1 = x[1];
+#pragma unroll
+        for (int j = 2; j < 64; j += 4) m0 = max3(m0, x[j], x[j + 1]), m1 = j + 3 < 64 ? max3(m1, x[j + 2], x[j + 3]) : m1;
+        const float top = fmaxf(m0, m1);
+        float alpha = 1.f;
+        if (top > m + kSlack || (m == -CUDART_INF_F && top > m)) {
+          if (t > it.t0) alpha = fp4::fast_exp2(m - top);
+          m = top;
+        }
+        l *= alpha;
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        wait_cluster(&bars[kPFree + slot], ph ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        unsigned char* prow = smem_p + slot * kParts * kPBytes + (r >> 3) * 1024 + (r & 7) * 128;
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[4], w2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = fp4::fast_exp2(x[8 * c + 2 * e] - ref), b = fp4::fast_exp2(x[8 * c + 2 * e + 1] - ref);
+            sum0 += a;
+            sum1 += b;
+            w[e] = pack_bf16(a, b);
+            if (HI) w2[e] = pack_bf16(a - __uint_as_float(w[e] << 16), b - __uint_as_float(w[e] & 0xffff0000u));
+          }
+          *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (HI) *reinterpret_cast<uint4*>(prow + kPBytes + ((c ^ (r & 7)) << 4)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        }
+        l += sum0 + sum1;
+        alphas[slot * 128 + xr] = alpha;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {  // this warp's 32 rows into the other CTA
+          const uint32_t bar = remote(&bars[kPCopy + slot], peer);
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) {
+            const unsigned char* src = smem_p + (slot * kParts + h) * kPBytes + (r >> 3) * 1024;
+            copy_to_cta(remote(src, peer), src, 4096, bar);
+          }
+          copy_to_cta(remote(alphas + slot * 128 + 64 + xr, peer), alphas + slot * 128 + xr, 128, bar);
+        }
+        if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          rescale(alpha);
+          if (aborted) return;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kPFull + slot]);
+      }
+      // ---- the rows' sums for the other CTA's columns, then the outputs ----
+      float inv = l != 0.f ? 1.f / l : 0.f;
+      if (own) store_async1(remote(other_l + xr, peer), inv, remote(&bars[kLFull], peer));
+      else {
+        if (xr == 0) ptx::mbar_arrive_expect_tx(&bars[kLFull], 256);
+        wait_cluster(&bars[kLFull], items & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        inv = other_l[xr];
+      }
+      wait(&bars[kODone], (kt - 1) & 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      ptx::tc_fence_after();
+      const int64_t part = (static_cast<int64_t>(cluster) * 2 + (it.t0 > 0 ? 0 : 1)) * L.part_rows + r;
+      const bool store = valid && r < L.part_rows;
+      if (!it.whole && own && store) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t v[32];
+        ptx::TmemLd<32>::run(tmem + lanes + c * 32, v);
+        wait_ld32(v);
+        if (c == 7) {  // O is read: the next item's P V may write it
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars[kOFree]);
+        }
+        if (!store) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float y[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[16 * h + j]);
+          const int64_t col = static_cast<int64_t>(rank) * 256 + c * 32 + h * 16;
+          if (it.whole) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = inv != 0.f ? y[j] * inv : 0.f;
+            store16(p, out_row * 512 + col, y);
+          } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
+              fp4::store32(L.o + part * 512 + col + 8 * q, w);
+            }
+          }
+        }
+      }
+      // a cluster that begins inside an item's tiles reports it
+      if (it.t0 > 0 && rank == 0 && tid == 0) {
+        const int wide = extra * (share + 1);
+        auto cluster_of = [&](int u) { return u < wide ? u / (share + 1) : extra + (u - wide) / share; };
+        L.desc[cluster] = make_int4(it.seq, it.rt, cluster_of(it.start + kLead), cluster_of(it.end - 1));
+      }
+      ++items;
+    });
+  }
+
+  if (aborted) *gave_up = 1;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 5) ptx::tmem_dealloc(tmem, 512);
+  if (tid == 0 && *gave_up) atomicExch(p.err, kDevErrTimeout);
+  cluster_sync();  // the other CTA may still signal this one's barriers
+}
+
+// Parts of items added up: a warp takes 128 columns of a row.  The first cluster
+// behind an item's start reports the item.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int units = (L.num_clusters - 1) * L.part_rows * 4;
+  for (int u = (blockIdx.x * kMergeThreads + threadIdx.x) >> 5; u < units; u += gridDim.x * kMergeThreads / 32) {
+    const int b = 1 + u / (L.part_rows * 4), r = (u >> 2) % L.part_rows, col = (u & 3) * 128 + lane * 4;
+    const int4 d = L.desc[b];
+    if (d.x < 0 || d.z != b - 1) continue;
+    const int row = d.y * 128 + r;
+    if (row >= L.rows) continue;
+    // the part that begins the item lies in its cluster's second place, the others in their first
+    auto part_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == d.z ? 1 : 0)) * L.part_rows + r; };
+    float M = -CUDART_INF_F;
+#pragma unroll 4
+    for (int c = d.z; c <= d.w; ++c) M = fmaxf(M, __ldcg(L.ml + part_of(c) * 2));
+    const float ref = M == -CUDART_INF_F ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 8
+    for (int c = d.z; c <= d.w; ++c) {
+      const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + part_of(c) * 2));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(L.o + part_of(c) * 512 + col));
+      if (e.y == 0.f) continue;  // a part that this row sees nothing of
+      const float w = fp4::fast_exp2(e.x - ref);
+      sum = fmaf(w, e.y, sum);
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const int64_t at = (static_cast<int64_t>(d.x) * L.rows + row) * 512 + col;
+    if (L.p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.p.out) + at) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(L.p.out) + at) =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
+}
+
+int smem_bytes(bool hi, int seqs) {
+  return 1024 + stages_of(hi) * kStageBytes + 2 * (hi ? 2 : 1) * kPBytes + 2 * kXBytes + kOffPrefix +
+         (seqs + 64) / 64 * 256;
+}
+
+// Sequences of one launch: their places fit an int.  0: not even one's do.
+int seqs_of(int num_seqs, int64_t row_tiles, int max_context_len) {
+  const int64_t places = (kLead + (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile) * row_tiles;
+  const int64_t fit = ((int64_t(1) << 31) - 1) / places;
+  const int64_t most = fit < kMaxSeqs ? fit : kMaxSeqs;
+  return static_cast<int>(num_seqs < most ? num_seqs : most);
+}
+
+int max_clusters() { return static_cast<int>(device_sm_count() / 2); }
+int part_rows_of(int64_t rows) { return static_cast<int>(rows < 128 ? rows : 128); }
+
+}  // namespace latent_decode_detail
+
+size_t latent_decode_workspace(int num_seqs, int q_len, int num_heads, int max_context_len) {
+  using namespace latent_decode_detail;
+  const int64_t rows = static_cast<int64_t>(q_len) * num_heads;
+  if (num_seqs > 0 && seqs_of(num_seqs, (rows + 127) / 128, max_context_len) == 0) return 0;
+  // header | reports | maxima and sums | parts
+  const int64_t n = max_clusters();
+  return static_cast<size_t>(256 + (n * 16 + 255) / 256 * 256 + 2 * n * part_rows_of(rows) * (512 + 2) * 4);
+}
 
 cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.q_len * p.num_heads;
-  return launch_early(latent_decode_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, stream, p);
+  using namespace latent_decode_detail;
+  const int64_t rows = static_cast<int64_t>(p.q_len) * p.num_heads, row_tiles = (rows + 127) / 128;
+  const int seqs = seqs_of(p.num_seqs, row_tiles, p.max_context_len);
+  const int n = max_clusters();
+  const bool hi = !p.out_bf16;
+  // the pool as groups of 8 rows of 8 chunks of 64 columns, and as rows of position columns
+  CUtensorMap tm_lat, tm_rope;
+  const uint64_t pool_rows = static_cast<uint64_t>(p.num_blocks) * p.block_size;
+  const uint32_t box_rows = p.block_size < kTile ? p.block_size : kTile;
+  {
+    const uint64_t dims[4] = {64, 8, 8, pool_rows / 8}, strides[3] = {1152, 128, 9216};
+    const uint32_t box[4] = {64, 8, 4, box_rows / 8};
+    if (!encode_bf16_tiles(&tm_lat, 4, p.cache, dims, strides, box, 128)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[2] = {64, pool_rows}, strides[1] = {1152};
+    const uint32_t box[2] = {32, box_rows};
+    if (!encode_bf16_tiles(&tm_rope, 2, static_cast<const __nv_bfloat16*>(p.cache) + 512, dims, strides, box, 64))
+      return cudaErrorInvalidValue;
+  }
+  for (int seq0 = 0; seq0 < p.num_seqs; seq0 += seqs) {
+    Launch L{};
+    L.p = p;
+    L.p.num_seqs = p.num_seqs - seq0 < seqs ? p.num_seqs - seq0 : seqs;
+    L.p.q = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(seq0) * rows * 576;
+    L.p.out = static_cast<unsigned char*>(p.out) + static_cast<int64_t>(seq0) * rows * 512 * (p.out_bf16 ? 2 : 4);
+    L.p.context_lens += seq0;
+    L.p.block_tables += static_cast<int64_t>(seq0) * p.max_blocks_per_seq;
+    L.rows = static_cast<int>(rows);
+    L.row_tiles = static_cast<int>(row_tiles);
+    L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
+    L.part_rows = part_rows_of(rows);
+    // every SM, while a cluster gets a few tiles
+    const int64_t tiles = static_cast<int64_t>(L.p.num_seqs) * row_tiles * ((static_cast<int64_t>(p.max_context_len) + kTile - 1) / kTile);
+    const int64_t want = (tiles + kMinTiles - 1) / kMinTiles;
+    L.num_clusters = static_cast<int>(want < 1 ? 1 : (want < n ? want : n));
+    L.desc = reinterpret_cast<int4*>(p.ws + 256);
+    L.ml = reinterpret_cast<float*>(p.ws + 256 + (static_cast<int64_t>(n) * 16 + 255) / 256 * 256);
+    L.o = L.ml + static_cast<int64_t>(2) * n * L.part_rows * 2;
+    const int smem = smem_bytes(hi, L.p.num_seqs);
+    const void* fn = hi ? reinterpret_cast<const void*>(&decode_kernel<true>) : reinterpret_cast<const void*>(&decode_kernel<false>);
+    int per_sm = 0;
+    cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * L.num_clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    void* args[] = {&L, &tm_lat, &tm_rope};
+    e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) return e;
+    if (L.num_clusters > 1) {
+      int64_t ctas = static_cast<int64_t>(L.num_clusters - 1) * L.part_rows * 4 / (kMergeThreads / 32);
+      const int64_t cap = device_sm_count() * 4;
+      ctas = ctas < 1 ? 1 : (ctas < cap ? ctas : cap);
+      e = launch_early(merge_kernel, dim3(static_cast<unsigned>(ctas)), kMergeThreads, stream, L);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pa

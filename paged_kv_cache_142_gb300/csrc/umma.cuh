@@ -1,0 +1,122 @@
+// Helpers of the tcgen05 kernels over latent rows: operands in tensor memory,
+// clusters, and waits that see what another CTA of the cluster wrote.
+#pragma once
+
+#include "decode.cuh"
+#include "ptx.cuh"
+
+namespace pa {
+namespace um {
+
+constexpr uint32_t kLayoutSw64 = 4;
+
+// one lane of the warp, the same each time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+// D (+)= A B with A in tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+// arrive on the barrier at this place in every CTA of the mask once the products issued so far are complete
+__device__ __forceinline__ void umma_commit_cluster(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          ptx::smem_addr(bar)),
+      "h"(mask)
+      : "memory");
+}
+// the place in CTA `rank` of the cluster that p has in this one
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// stores into another CTA's shared memory, counted by its barrier
+__device__ __forceinline__ void store_async4(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+      "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void store_async1(uint32_t dst, float a, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+               "r"(__float_as_uint(a)), "r"(bar)
+               : "memory");
+}
+// a run of this CTA's shared memory copied to another CTA's, counted by its barrier
+__device__ __forceinline__ void copy_to_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(ptx::smem_addr(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(ptx::smem_addr(bar)), "r"(parity), "r"(ptx::kSleepHintNs)
+      : "memory");
+  return done != 0;
+}
+// Bounded waits; one that gives up sets `aborted`, and no later one waits.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
+  if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
+}
+__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, bool& aborted) {
+  if (aborted || try_wait_cluster(bar, parity)) return;
+  const uint64_t t0 = ptx::global_ns();
+  while (!try_wait_cluster(bar, parity))
+    if (ptx::global_ns() - t0 > kWaitLimitNs) {
+      aborted = true;
+      return;
+    }
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// two values rounded to bf16, lo in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 64 columns of this warp's lanes
+__device__ __forceinline__ void load64(uint32_t at, uint32_t (&v)[64]) {
+  ptx::TmemLd<32>::run(at, *reinterpret_cast<uint32_t(*)[32]>(v));
+  ptx::TmemLd<32>::run(at + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+}
+// waits for this warp's tensor-memory loads; what uses v comes after it
+__device__ __forceinline__ void wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+}  // namespace um
+}  // namespace pa
