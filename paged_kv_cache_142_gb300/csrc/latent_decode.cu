@@ -30,8 +30,9 @@
 // borders of sequences; a cluster that takes part of an item leaves its rows
 // unnormalised in the workspace, and a second kernel adds the parts up.
 //
-// One CTA per SM, 6 warps: 0-3 scores and outputs (a row a thread: two warps
-// finish rows, two ship partial sums), 4 loads, 5 issues products.
+// One CTA per SM, 11 warps: 0-3 and 4-7 scores and outputs (half of a row's
+// tokens a thread; of each four warps two finish rows and two ship partial
+// sums), 8 loads, 9 and 10 issue the products of S and of O (one warp for both would hold back the next S while it waits for P).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -46,13 +47,13 @@ namespace latent_decode_detail {
 
 using namespace um;
 
-constexpr int kThreads = 6 * 32;
+constexpr int kThreads = 11 * 32;
 constexpr int kTile = 64;                      // tokens
 constexpr int kLatBytes = kTile * 512;         // [8-token group][4 chunks of 64 columns][8 rows x 128 bytes]
 constexpr int kRopeBytes = kTile * 64;         // [8-token group][8 rows x 64 bytes]
 constexpr int kStageBytes = kLatBytes + kRopeBytes;
-constexpr int kPBytes = 128 * 128;             // 128 rows x 64 bf16
-constexpr int kXBytes = 64 * kTile * 4;        // partial sums of 64 rows: [4-token group][row][4]
+constexpr int kPBytes = 128 * 128;             // [half of the tokens][128 rows x 32 bf16]
+constexpr int kXBytes = 64 * kTile * 4;        // partial sums of 64 rows: [half of the tokens][4-token group][row][4]
 constexpr uint32_t kColQ = 256, kColS = 400;   // tensor memory: O at 0
 constexpr float kSlack = 8.f;
 constexpr int kLead = 3;      // what starting and ending an item costs a cluster, in tiles
@@ -64,13 +65,14 @@ __host__ __device__ constexpr int stages_of(bool hi) { return hi ? 3 : 4; }
 // barriers ([2] or [4] each where they have a number)
 enum : int {
   kFull = 0, kEmpty = 4, kQFull = 8, kSFull = 9, kSFree = 10, kXFull = 11, kXFree = 13, kPFull = 15, kPCopy = 17,
-  kPFree = 19, kODone = 21, kOFree = 22, kLFull = 23, kDrain = 24, kNumBars = 25
+  kPFree = 19, kODone = 21, kOFree = 23, kLFull = 24, kFixed = 25, kDrain = 26, kNumBars = 28
 };
 // shared memory, behind the stages: P slots, exchange slots, then
 constexpr int kOffBar = 0;
 constexpr int kOffAlpha = 256;                // [2 slots][own | other's][64]
 constexpr int kOffL = kOffAlpha + 1024;       // [64] the other CTA's 1 / sum
-constexpr int kOffPrefix = kOffL + 256;
+constexpr int kOffTops = kOffL + 256;          // [2 slots][half][64] maxima of half a row
+constexpr int kOffPrefix = kOffTops + 1024;
 
 struct Launch {
   LatentDecodeParams p;
@@ -153,6 +155,11 @@ __device__ __forceinline__ int seen_by(const Launch& L, const Item& it, int row)
   return it.len - L.p.q_len + 1 + row / L.p.num_heads;
 }
 
+// whether any of 64 rows has a new reference
+__device__ __forceinline__ bool raised(const float* alpha, int lane) {
+  return __any_sync(0xffffffffu, alpha[lane] != 1.f || alpha[lane + 32] != 1.f);
+}
+
 // Sums over the parts, or zeros: outputs of 32 bytes and more
 __device__ __forceinline__ void store16(const LatentDecodeParams& p, int64_t at, const float (&v)[16]) {
   uint32_t h[8];
@@ -187,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* alphas = reinterpret_cast<float*>(rest + kOffAlpha);
   float* other_l = reinterpret_cast<float*>(rest + kOffL);
+  float* tops = reinterpret_cast<float*>(rest + kOffTops);
   int* prefix = reinterpret_cast<int*>(rest + kOffPrefix);
   __shared__ int warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -199,24 +207,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kFull + i], 1);
       ptx::mbar_init(&bars[kEmpty + i], 1);
     }
-    ptx::mbar_init(&bars[kQFull], 4);
+    ptx::mbar_init(&bars[kQFull], 8);
     ptx::mbar_init(&bars[kSFull], 1);
-    ptx::mbar_init(&bars[kSFree], 4);
+    ptx::mbar_init(&bars[kSFree], 8);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars[kXFull + i], 1);
-      ptx::mbar_init(&bars[kXFree + i], 2);
+      ptx::mbar_init(&bars[kXFree + i], 4);
       ptx::mbar_init(&bars[kPFull + i], 4);
       ptx::mbar_init(&bars[kPCopy + i], 1);
       ptx::mbar_init(&bars[kPFree + i], 2);
+      ptx::mbar_init(&bars[kODone + i], 1);
     }
-    ptx::mbar_init(&bars[kODone], 1);
-    ptx::mbar_init(&bars[kOFree], 4);
+    ptx::mbar_init(&bars[kOFree], 8);
     ptx::mbar_init(&bars[kLFull], 1);
     ptx::mbar_init(&bars[kDrain], 1);
+    ptx::mbar_init(&bars[kDrain + 1], 1);
+    ptx::mbar_init(&bars[kFixed], 4);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tc_fence_before();
   }
@@ -265,7 +275,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto run_begin = [&](int c) { return c * share + min(c, extra); };
   const Walk walk{L, prefix, run_begin(cluster), run_begin(cluster + 1)};
 
-  if (warp == 4) {
+  // no product may be in flight when tensor memory is freed
+  auto drain = [&](int bar, bool leader) {
+    if (leader) {
+      ptx::umma_commit(&bars[bar]);
+      bool late = false;
+      wait(&bars[bar], 0, late);
+      if (late) aborted = true;
+    }
+    aborted = __any_sync(0xffffffffu, aborted);
+  };
+
+  if (warp == 8) {
     // ============================== loads ==============================
     // lane i: the latent part of the tile's page i; lane 16 + i: its position part
     const int page_rows = min(kTile, 1 << L.bs_log), pages = kTile / page_rows;
@@ -312,35 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     });
-  } else if (warp == 5) {
-    // ============================ products ============================
+  } else if (warp == 9) {
+    // ===================== products of the scores =====================
     const bool leader = elect_one();
-    constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, kTile, 0, 0), kIdO = ptx::idesc_bf16_f32(128, 256, 0, 1);
+    constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, kTile, 0, 0);
     const uint64_t desc_k = ptx::smem_desc(smem, 16, 4096, ptx::kLayoutSw128);
     const uint64_t desc_r = ptx::smem_desc(smem + kLatBytes, 16, 512, kLayoutSw64);
-    const uint64_t desc_v = ptx::smem_desc(smem, 1024, 4096, ptx::kLayoutSw128);
-    const uint64_t desc_p = ptx::smem_desc(smem_p, 16, 1024, ptx::kLayoutSw128);
     uint32_t kt = 0, items = 0;
-    auto values = [&](uint32_t k, bool first) {  // P V of tile k
-      wait(&bars[kPFull + (k & 1u)], (k >> 1) & 1u, aborted);
-      if (first) wait(&bars[kOFree], (items & 1u) ^ 1u, aborted);
-      aborted = __any_sync(0xffffffffu, aborted);
-      if (aborted) return;
-      ptx::tc_fence_after();
-      if (leader) {
-        const uint64_t dv = desc_v + (k % kStages) * (kStageBytes >> 4);
-        const uint64_t dp = desc_p + (k & 1u) * (kParts * kPBytes >> 4);
-#pragma unroll
-        for (int h = 0; h < kParts; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)  // 16 tokens each
-            ptx::umma_bf16(tmem, dp + h * (kPBytes >> 4) + j * 2, dv + j * (8192 >> 4), kIdO, h + j > 0 ? 1u : !first);
-        ptx::umma_commit(&bars[kEmpty + k % kStages]);
-        umma_commit_cluster(&bars[kPFree + (k & 1u)], 3);
-        ptx::umma_commit(&bars[kODone]);
-      }
-      __syncwarp();
-    };
     walk.each([&](const Item& it) {
       const int kend = seen_by(L, it, min(L.rows, it.rt * 128 + 128) - 1);
       for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
@@ -374,25 +373,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::umma_commit(&bars[kSFull]);
         }
         __syncwarp();
-        if (t > it.t0) values(kt - 1, t - 1 == it.t0);
       }
-      if (!aborted) values(kt - 1, it.t1 - it.t0 == 1);
       ++items;
     });
-    // nothing may be in flight when tensor memory is freed
-    if (leader) {
-      ptx::umma_commit(&bars[kDrain]);
-      bool drain = false;
-      wait(&bars[kDrain], 0, drain);
-      if (drain) aborted = true;
-    }
-    aborted = __any_sync(0xffffffffu, aborted);
+    drain(kDrain + 1, leader);
+  } else if (warp == 10) {
+    // ===================== products with the values =====================
+    const bool leader = elect_one();
+    constexpr uint32_t kIdO = ptx::idesc_bf16_f32(128, 256, 0, 1);
+    const uint64_t desc_v = ptx::smem_desc(smem, 1024, 4096, ptx::kLayoutSw128);
+    const uint64_t desc_p = ptx::smem_desc(smem_p, 16, 512, kLayoutSw64);
+    uint32_t kt = 0, items = 0, fixes = 0;
+    walk.each([&](const Item& it) {
+      for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
+        const uint32_t slot = kt & 1u, ph = (kt >> 1) & 1u;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kPCopy + slot], kParts * kPBytes / 2 + 256);
+        if (t == it.t0) wait(&bars[kOFree], (items & 1u) ^ 1u, aborted);
+        wait(&bars[kPFull + slot], ph, aborted);
+        wait(&bars[kPCopy + slot], ph, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        if (t > it.t0 && raised(alphas + slot * 128 + 64, lane)) {  // then two warps bring O to the new references
+          wait(&bars[kFixed], fixes++ & 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) return;
+        }
+        ptx::tc_fence_after();
+        if (leader) {
+          const uint64_t dv = desc_v + (kt % kStages) * (kStageBytes >> 4);
+          const uint64_t dp = desc_p + slot * (kParts * kPBytes >> 4);
+#pragma unroll
+          for (int h = 0; h < kParts; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // 16 tokens each
+              ptx::umma_bf16(tmem, dp + h * (kPBytes >> 4) + (j >> 1) * (kPBytes / 2 >> 4) + (j & 1) * 2, dv + j * (8192 >> 4), kIdO,
+                             h + j > 0 || t > it.t0 ? 1u : 0u);
+          ptx::umma_commit(&bars[kEmpty + kt % kStages]);
+          umma_commit_cluster(&bars[kPFree + slot], 3);
+          ptx::umma_commit(&bars[kODone + slot]);
+        }
+        __syncwarp();
+      }
+      ++items;
+    });
+    drain(kDrain, leader);
   } else {
-    // ============ scores and outputs: one row per thread ============
-    const int r = tid;  // row of the tile, tensor-memory lane
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-    const bool own = static_cast<uint32_t>(warp >> 1) == rank;
+    // ============ scores and outputs: half of the tokens of a row per thread ============
+    const int r = tid & 127;  // row of the tile, tensor-memory lane
+    const int half = tid >> 7;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const bool own = static_cast<uint32_t>((warp & 3) >> 1) == rank;
     const int xr = r & 63;  // row among the 64 of a CTA
+    auto both_halves = [&]() { ptx::bar_sync(1 + (warp & 3), 64); };  // the two warps of these rows
     uint32_t kt = 0, items = 0;
     const float f = p.scale_log2;
     walk.each([&](const Item& it) {
@@ -406,132 +438,137 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + out_row * 576);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t v[32];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint4 x = valid ? __ldg(src + rank * 32 + c * 8 + e) : make_uint4(0, 0, 0, 0);
+            const uint4 x = valid ? __ldg(src + rank * 32 + half * 16 + c * 8 + e) : make_uint4(0, 0, 0, 0);
             v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
           }
-          ptx::tmem_st32(tmem + lanes + kColQ + c * 32, v);
+          ptx::tmem_st32(tmem + lanes + kColQ + half * 64 + c * 32, v);
         }
-        uint32_t v[16];
+        uint32_t v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 x = valid ? __ldg(src + 64 + rank * 4 + e) : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 2; ++e) {
+          const uint4 x = valid ? __ldg(src + 64 + rank * 4 + half * 2 + e) : make_uint4(0, 0, 0, 0);
           v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
         }
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-                tmem + lanes + kColQ + 128),
-            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-            "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-            : "memory");
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tmem + lanes + kColQ +
+                                                                                                  128 + half * 8),
+                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
       }
-      float m = -CUDART_INF_F, l = 0.f;
+      float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens
+      // this half's columns of O on a new reference, once P V of the tile before k
+      // is in them (a barrier for every other tile: with one, its phase could be two
+      // behind this row's, which looks like done)
+      auto rescale = [&](uint32_t k, float alpha) {
+        wait(&bars[kODone + ((k - 1) & 1u)], ((k - 1) >> 1) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          ptx::TmemLd<32>::run(tmem + lanes + half * 128 + c * 32, v);
+          wait_ld32(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+          ptx::tmem_st32(tmem + lanes + half * 128 + c * 32, v);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+      };
+      // the other CTA's rows of tile k: O on their new references, if there are any
+      auto received = [&](uint32_t k, bool later) {
+        const uint32_t slot = k & 1u;
+        wait(&bars[kPCopy + slot], (k >> 1) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted || !later || !raised(alphas + slot * 128 + 64, lane)) return;
+        rescale(k, alphas[slot * 128 + 64 + xr]);
+        __syncwarp();
+        if (lane == 0 && !aborted) ptx::mbar_arrive(&bars[kFixed]);
+      };
       for (int t = it.t0; t < it.t1; ++t, ++kt) {
         const uint32_t slot = kt & 1u, ph = (kt >> 1) & 1u;
-        // the columns of O, raised to a new reference once P V of the tile before is in them
-        auto rescale = [&](float alpha) {
-          wait(&bars[kODone], (kt - 1) & 1u, aborted);
-          aborted = __any_sync(0xffffffffu, aborted);
-          if (aborted) return;
-          ptx::tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t v[32];
-            ptx::TmemLd<32>::run(tmem + lanes + c * 32, v);
-            wait_ld32(v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
-            ptx::tmem_st32(tmem + lanes + c * 32, v);
-          }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-        };
         wait(&bars[kSFull], kt & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) return;
         ptx::tc_fence_after();
-        uint32_t s[64];
-        load64(tmem + lanes + kColS, s);
-        wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(s));
-        wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        uint32_t s[32];
+        ptx::TmemLd<32>::run(tmem + lanes + kColS + half * 32, s);
+        wait_ld32(s);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kSFree]);
+        if (!own) {
+          // ---- the other CTA's rows: its partial sums; the references of the tile before ----
+          wait(&bars[kXFree + slot], ph ^ 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) return;
+          const uint32_t dst = remote(smem_x + slot * kXBytes + half * (kXBytes / 2), peer);
+          const uint32_t bar = remote(&bars[kXFull + slot], peer);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            store_async4(dst + (j * 64 + xr) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
+                         __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
+          if (t > it.t0) received(kt - 1, t - 1 > it.t0);
+          if (aborted) return;
+          continue;
+        }
+        // ---- own rows: scores, probabilities ----
         // Tokens that some rows of the tile see and others do not: a value among
         // this CTA's columns that is not finite makes every row's partial sum
         // not finite.  It becomes zero, so that 0 * NaN does not reach the rows
         // that do not see it; the others have the score.
-        if (warp == 0 && limit_min < limit_max && limit_min < (t + 1) * kTile) {
-          uint64_t odd = 0;
+        if (xr < 32 && limit_min < limit_max && limit_min < (t + 1) * kTile) {
+          uint32_t odd = 0;
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= uint64_t(1) << j;
+          for (int j = 0; j < 32; ++j)
+            if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= 1u << j;
           odd = __shfl_sync(0xffffffffu, odd, 0);
-          const int from = max(0, limit_min - t * kTile), upto = min(kTile, limit_max - t * kTile);
-          unsigned char* stage = smem + (kt % kStages) * kStageBytes;
+          const int from = max(0, limit_min - t * kTile - half * 32), upto = min(32, limit_max - t * kTile - half * 32);
+          unsigned char* stage = smem + (kt % kStages) * kStageBytes + half * 4 * 4096;
           for (int j = from; j < upto; ++j)
             if ((odd >> j) & 1u)
               *reinterpret_cast<uint4*>(stage + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
-          if (odd) ptx::fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (!own) {
-          // ---- the other CTA's rows: its partial sums, then its probabilities ----
-          wait_cluster(&bars[kXFree + slot], ph ^ 1u, aborted);
-          aborted = __any_sync(0xffffffffu, aborted);
-          if (aborted) return;
-          const uint32_t dst = remote(smem_x + slot * kXBytes, peer), bar = remote(&bars[kXFull + slot], peer);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            store_async4(dst + (j * 64 + xr) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
-                         __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
-          if (xr == 0) ptx::mbar_arrive_expect_tx(&bars[kPCopy + slot], kParts * kPBytes / 2 + 256);
-          wait_cluster(&bars[kPCopy + slot], ph, aborted);
-          aborted = __any_sync(0xffffffffu, aborted);
-          if (aborted) return;
-          const float alpha = alphas[slot * 128 + 64 + xr];
-          if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            rescale(alpha);
-            if (aborted) return;
-          }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars[kPFull + slot]);
-          continue;
-        }
-        // ---- own rows: scores, probabilities ----
-        if (xr == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + slot], kXBytes);
-        wait_cluster(&bars[kXFull + slot], ph, aborted);
+        if (xr == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + slot], kXBytes);
+        wait(&bars[kXFull + slot], ph, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) return;
-        float x[64];
+        float x[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 y = *reinterpret_cast<const float4*>(smem_x + slot * kXBytes + (j * 64 + xr) * 16);
+        for (int j = 0; j < 8; ++j) {
+          const float4 y = *reinterpret_cast<const float4*>(smem_x + slot * kXBytes + half * (kXBytes / 2) + (j * 64 + xr) * 16);
           x[4 * j] = (__uint_as_float(s[4 * j]) + y.x) * f;
           x[4 * j + 1] = (__uint_as_float(s[4 * j + 1]) + y.y) * f;
           x[4 * j + 2] = (__uint_as_float(s[4 * j + 2]) + y.z) * f;
           x[4 * j + 3] = (__uint_as_float(s[4 * j + 3]) + y.w) * f;
         }
-        __syncwarp();
-        if (lane == 0) remote_arrive(remote(&bars[kXFree + slot], peer));
-        const int nvis = limit - t * kTile;
-        if (!__all_sync(0xffffffffu, nvis >= kTile)) {
+        const int nvis = limit - t * kTile - half * 32;
+        if (!__all_sync(0xffffffffu, nvis >= 32)) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
+          for (int j = 0; j < 32; ++j)
             if (j >= nvis) x[j] = -CUDART_INF_F;
         }
         float m0 = x[0], m1 = x[1];
 #pragma unroll
-        for (int j = 2; j < 64; j += 4) m0 = max3(m0, x[j], x[j + 1]), m1 = j + 3 < 64 ? max3(m1, x[j + 2], x[j + 3]) : m1;
-        const float top = fmaxf(m0, m1);
+        for (int j = 2; j < 32; j += 4) {
+          m0 = max3(m0, x[j], x[j + 1]);
+          if (j + 3 < 32) m1 = max3(m1, x[j + 2], x[j + 3]);
+        }
+        float top = fmaxf(m0, m1);
+        __syncwarp();  // every lane has read its sums
+        if (lane == 0) remote_arrive(remote(&bars[kXFree + slot], peer), top);
+        tops[(slot * 2 + half) * 64 + xr] = top;
+        both_halves();
+        top = fmaxf(top, tops[(slot * 2 + (half ^ 1)) * 64 + xr]);
         float alpha = 1.f;
         if (top > m + kSlack || (m == -CUDART_INF_F && top > m)) {
           if (t > it.t0) alpha = fp4::fast_exp2(m - top);
@@ -539,13 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l *= alpha;
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        wait_cluster(&bars[kPFree + slot], ph ^ 1u, aborted);
+        wait(&bars[kPFree + slot], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) return;
-        unsigned char* prow = smem_p + slot * kParts * kPBytes + (r >> 3) * 1024 + (r & 7) * 128;
+        // [half][128 rows x 64 bytes], 64-byte swizzle
+        unsigned char* prow = smem_p + slot * kParts * kPBytes + half * (kPBytes / 2) + (r >> 3) * 512 + (r & 7) * 64;
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t w[4], w2[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -555,52 +593,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e] = pack_bf16(a, b);
             if (HI) w2[e] = pack_bf16(a - __uint_as_float(w[e] << 16), b - __uint_as_float(w[e] & 0xffff0000u));
           }
-          *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          if (HI) *reinterpret_cast<uint4*>(prow + kPBytes + ((c ^ (r & 7)) << 4)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          const int at = (c ^ ((r >> 1) & 3)) << 4;
+          *reinterpret_cast<uint4*>(prow + at) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (HI) *reinterpret_cast<uint4*>(prow + kPBytes + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         }
         l += sum0 + sum1;
-        alphas[slot * 128 + xr] = alpha;
+        if (half == 0) alphas[slot * 128 + xr] = alpha;
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {  // this warp's 32 rows into the other CTA
           const uint32_t bar = remote(&bars[kPCopy + slot], peer);
 #pragma unroll
-          for (int h = 0; h < kParts; ++h) {
-            const unsigned char* src = smem_p + (slot * kParts + h) * kPBytes + (r >> 3) * 1024;
-            copy_to_cta(remote(src, peer), src, 4096, bar);
-          }
-          copy_to_cta(remote(alphas + slot * 128 + 64 + xr, peer), alphas + slot * 128 + xr, 128, bar);
+          for (int h = 0; h < kParts; ++h)
+            copy_to_cta(remote(prow + h * kPBytes, peer), prow + h * kPBytes, 2048, bar);
+          if (half == 0) copy_to_cta(remote(alphas + slot * 128 + 64 + xr, peer), alphas + slot * 128 + xr, 128, bar);
         }
         if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          rescale(alpha);
+          rescale(kt, alpha);
           if (aborted) return;
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kPFull + slot]);
       }
-      // ---- the rows' sums for the other CTA's columns, then the outputs ----
-      float inv = l != 0.f ? 1.f / l : 0.f;
-      if (own) store_async1(remote(other_l + xr, peer), inv, remote(&bars[kLFull], peer));
-      else {
-        if (xr == 0) ptx::mbar_arrive_expect_tx(&bars[kLFull], 256);
-        wait_cluster(&bars[kLFull], items & 1u, aborted);
+      if (!own) received(kt - 1, it.t1 - it.t0 > 1);
+      if (aborted) return;
+      // ---- the rows' sums, also for the other CTA's columns; then the outputs ----
+      float inv;
+      if (own) {
+        tops[((kt & 1u) * 2 + half) * 64 + xr] = l;
+        both_halves();
+        l += tops[((kt & 1u) * 2 + (half ^ 1)) * 64 + xr];
+        both_halves();  // read before the next tile writes there
+        inv = l != 0.f ? 1.f / l : 0.f;
+        if (half == 0) store_async1(remote(other_l + xr, peer), inv, remote(&bars[kLFull], peer));
+      } else {
+        if (xr == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kLFull], 256);
+        wait(&bars[kLFull], items & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) return;
         inv = other_l[xr];
       }
-      wait(&bars[kODone], (kt - 1) & 1u, aborted);
+      wait(&bars[kODone + ((kt - 1) & 1u)], ((kt - 1) >> 1) & 1u, aborted);
       aborted = __any_sync(0xffffffffu, aborted);
       if (aborted) return;
       ptx::tc_fence_after();
       const int64_t part = (static_cast<int64_t>(cluster) * 2 + (it.t0 > 0 ? 0 : 1)) * L.part_rows + r;
       const bool store = valid && r < L.part_rows;
-      if (!it.whole && own && store) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
+      if (!it.whole && own && store && half == 0) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
-        ptx::TmemLd<32>::run(tmem + lanes + c * 32, v);
+        ptx::TmemLd<32>::run(tmem + lanes + half * 128 + c * 32, v);
         wait_ld32(v);
-        if (c == 7) {  // O is read: the next item's P V may write it
+        if (c == 3) {  // O is read: the next item's P V may write it
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars[kOFree]);
@@ -611,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float y[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[16 * h + j]);
-          const int64_t col = static_cast<int64_t>(rank) * 256 + c * 32 + h * 16;
+          const int64_t col = static_cast<int64_t>(rank) * 256 + half * 128 + c * 32 + h * 16;
           if (it.whole) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) y[j] = inv != 0.f ? y[j] * inv : 0.f;
@@ -641,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 5) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 9) ptx::tmem_dealloc(tmem, 512);
   if (tid == 0 && *gave_up) atomicExch(p.err, kDevErrTimeout);
   cluster_sync();  // the other CTA may still signal this one's barriers
 }

@@ -1,5 +1,5 @@
 // Helpers of the tcgen05 kernels over latent rows: operands in tensor memory,
-// clusters, and waits that see what another CTA of the cluster wrote.
+// and what the CTAs of a cluster send one another.
 #pragma once
 
 #include "decode.cuh"
@@ -37,8 +37,11 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_addr(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void remote_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// after `used` has been formed (the arrival stands for what was read to form it)
+__device__ __forceinline__ void remote_arrive(uint32_t bar, float used) {
+  asm volatile("{\n\t.reg .f32 t;\n\tmov.f32 t, %1;\n\tmbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+               "f"(used)
+               : "memory");
 }
 // stores into another CTA's shared memory, counted by its barrier
 __device__ __forceinline__ void store_async4(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
@@ -58,29 +61,9 @@ __device__ __forceinline__ void copy_to_cta(uint32_t dst, const void* src, uint3
                "r"(ptx::smem_addr(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(ptx::smem_addr(bar)), "r"(parity), "r"(ptx::kSleepHintNs)
-      : "memory");
-  return done != 0;
-}
 // Bounded waits; one that gives up sets `aborted`, and no later one waits.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
   if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
-}
-__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, bool& aborted) {
-  if (aborted || try_wait_cluster(bar, parity)) return;
-  const uint64_t t0 = ptx::global_ns();
-  while (!try_wait_cluster(bar, parity))
-    if (ptx::global_ns() - t0 > kWaitLimitNs) {
-      aborted = true;
-      return;
-    }
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
