@@ -11,17 +11,13 @@
 // CTAs shares an item by columns: CTA c holds columns 256 c .. of the latent
 // part and half of the position part, of all rows and all tokens.  No byte of
 // the cache is loaded twice.
-//   S: each CTA forms the product over its own 288 columns and both add them up:
-//      a CTA finishes the rows 64 c .. 64 c + 63 and gets the other's partial
-//      sums of them through distributed shared memory (16 KB a tile).
-//   P: finished by the CTA that owns the row, written into its own shared
-//      memory and copied into the other's (8 KB), as both need all rows for
-//      their columns of O.  Maximum and sum of a row stay in one thread; the
-//      reference is raised only when the maximum passes it by 2^8, and then
-//      the other CTA gets the factor for its columns along with P.
+// Each forms S over its own 288 columns; the two add their partial sums up
+// through distributed shared memory (32 KB a tile each way at 128 rows), and both
+// form the same probabilities, each for its columns of O: handing P over instead
+// halves the exponentials, but puts a second exchange into a tile's chain.
+// A row's reference is raised only when its maximum passes it by 2^8.
 // The queries lie in tensor memory as the A operand (144 columns), so that
-// shared memory holds four tiles of K and V: three are in flight while one is
-// worked on.
+// shared memory holds four tiles of K and V.
 //
 // fp32 outputs take the probabilities in two bf16 parts, P and what its
 // rounding left (2^-17 in all); bf16 outputs take one (2^-8, as the output).
@@ -30,9 +26,13 @@
 // borders of sequences; a cluster that takes part of an item leaves its rows
 // unnormalised in the workspace, and a second kernel adds the parts up.
 //
-// One CTA per SM, 11 warps: 0-3 and 4-7 scores and outputs (half of a row's
-// tokens a thread; of each four warps two finish rows and two ship partial
-// sums), 8 loads, 9 and 10 issue the products of S and of O (one warp for both would hold back the next S while it waits for P).
+// One CTA per SM, 19 warps: 0-7 and 8-15 scores and outputs of every other tile
+// (half of a row's tokens a thread; warps without rows do nothing), 16 loads, 17
+// and 18 issue the products of S and of O (one warp for both would hold back the
+// next S while it waits for P).  A tile's chain (scores, exchange, maximum,
+// probabilities) takes 2000 clocks, nearly all of them latency, whatever the
+// width: so two tiles are in it at a time, and only the reference passes from one
+// group to the other.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -47,13 +47,13 @@ namespace latent_decode_detail {
 
 using namespace um;
 
-constexpr int kThreads = 11 * 32;
+constexpr int kThreads = 19 * 32;
 constexpr int kTile = 64;                      // tokens
 constexpr int kLatBytes = kTile * 512;         // [8-token group][4 chunks of 64 columns][8 rows x 128 bytes]
 constexpr int kRopeBytes = kTile * 64;         // [8-token group][8 rows x 64 bytes]
 constexpr int kStageBytes = kLatBytes + kRopeBytes;
 constexpr int kPBytes = 128 * 128;             // [half of the tokens][128 rows x 32 bf16]
-constexpr int kXBytes = 64 * kTile * 4;        // partial sums of 64 rows: [half of the tokens][4-token group][row][4]
+constexpr int kXBytes = 128 * kTile * 4;       // the other CTA's partial sums: [half of the tokens][4-token group][row][4]
 constexpr uint32_t kColQ = 256, kColS = 400;   // tensor memory: O at 0
 constexpr float kSlack = 8.f;
 constexpr int kLead = 3;      // what starting and ending an item costs a cluster, in tiles
@@ -64,19 +64,19 @@ __host__ __device__ constexpr int stages_of(bool hi) { return hi ? 3 : 4; }
 
 // barriers ([2] or [4] each where they have a number)
 enum : int {
-  kFull = 0, kEmpty = 4, kQFull = 8, kSFull = 9, kSFree = 10, kXFull = 11, kXFree = 13, kPFull = 15, kPCopy = 17,
-  kPFree = 19, kODone = 21, kOFree = 23, kLFull = 24, kFixed = 25, kDrain = 26, kNumBars = 28
+  kFull = 0, kEmpty = 4, kQFull = 8, kSFree = 9, kSFull = 10, kXFull = 12, kXFree = 14, kPFull = 16, kPFree = 18,
+  kODone = 20, kOFree = 22, kDrain = 23, kRef = 25, kNumBars = 33  // kRef: [group][quarter of the rows]
 };
-// shared memory, behind the stages: P slots, exchange slots, then
+// shared memory, behind the stages: P slots, the exchange, then
 constexpr int kOffBar = 0;
-constexpr int kOffAlpha = 256;                // [2 slots][own | other's][64]
-constexpr int kOffL = kOffAlpha + 1024;       // [64] the other CTA's 1 / sum
-constexpr int kOffTops = kOffL + 256;          // [2 slots][half][64] maxima of half a row
-constexpr int kOffPrefix = kOffTops + 1024;
+constexpr int kOffTops = 512;                  // [2 turns][group][half][128] maxima of half a row
+constexpr int kOffRefs = kOffTops + 4096;      // [group][128] the rows' references
+constexpr int kOffPrefix = kOffRefs + 1024;
 
 struct Launch {
   LatentDecodeParams p;
   int rows, row_tiles;   // of a sequence; tiles of 128
+  int quarters;          // of the 128 rows that any tile has
   int bs_log, part_rows;
   int num_clusters;
   int4* desc;            // [clusters] the item that a cluster's run begins inside of: sequence (or -1), row tile, first and last cluster
@@ -155,12 +155,7 @@ __device__ __forceinline__ int seen_by(const Launch& L, const Item& it, int row)
   return it.len - L.p.q_len + 1 + row / L.p.num_heads;
 }
 
-// whether any of 64 rows has a new reference
-__device__ __forceinline__ bool raised(const float* alpha, int lane) {
-  return __any_sync(0xffffffffu, alpha[lane] != 1.f || alpha[lane + 32] != 1.f);
-}
-
-// Sums over the parts, or zeros: outputs of 32 bytes and more
+// 16 outputs of a row
 __device__ __forceinline__ void store16(const LatentDecodeParams& p, int64_t at, const float (&v)[16]) {
   uint32_t h[8];
   if (p.out_bf16) {
@@ -187,14 +182,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* smem_p = smem + kStages * kStageBytes;              // [2 slots][parts][128 rows]
-  unsigned char* smem_x = smem_p + 2 * kParts * kPBytes;             // [2 slots]
-  unsigned char* rest = smem_x + 2 * kXBytes;
+  unsigned char* smem_x = smem_p + 2 * kParts * kPBytes;
+  unsigned char* rest = smem_x + kXBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(rest + kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* alphas = reinterpret_cast<float*>(rest + kOffAlpha);
-  float* other_l = reinterpret_cast<float*>(rest + kOffL);
   float* tops = reinterpret_cast<float*>(rest + kOffTops);
+  float* refs = reinterpret_cast<float*>(rest + kOffRefs);
   int* prefix = reinterpret_cast<int*>(rest + kOffPrefix);
   __shared__ int warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -207,26 +201,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kFull + i], 1);
       ptx::mbar_init(&bars[kEmpty + i], 1);
     }
-    ptx::mbar_init(&bars[kQFull], 8);
-    ptx::mbar_init(&bars[kSFull], 1);
-    ptx::mbar_init(&bars[kSFree], 8);
+    const int warps = 2 * L.quarters;  // of a group
+    ptx::mbar_init(&bars[kQFull], 2 * warps);
+    ptx::mbar_init(&bars[kSFree], warps);
     for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kSFull + i], 1);
       ptx::mbar_init(&bars[kXFull + i], 1);
-      ptx::mbar_init(&bars[kXFree + i], 4);
-      ptx::mbar_init(&bars[kPFull + i], 4);
-      ptx::mbar_init(&bars[kPCopy + i], 1);
-      ptx::mbar_init(&bars[kPFree + i], 2);
+      ptx::mbar_init(&bars[kXFree + i], warps);
+      ptx::mbar_init(&bars[kPFull + i], warps);
+      ptx::mbar_init(&bars[kPFree + i], 1);
       ptx::mbar_init(&bars[kODone + i], 1);
     }
-    ptx::mbar_init(&bars[kOFree], 8);
-    ptx::mbar_init(&bars[kLFull], 1);
+    ptx::mbar_init(&bars[kOFree], 2 * warps);
+    for (int i = 0; i < 8; ++i) ptx::mbar_init(&bars[kRef + i], 2);
     ptx::mbar_init(&bars[kDrain], 1);
     ptx::mbar_init(&bars[kDrain + 1], 1);
-    ptx::mbar_init(&bars[kFixed], 4);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tc_fence_before();
   }
@@ -286,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     aborted = __any_sync(0xffffffffu, aborted);
   };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ============================== loads ==============================
     // lane i: the latent part of the tile's page i; lane 16 + i: its position part
     const int page_rows = min(kTile, 1 << L.bs_log), pages = kTile / page_rows;
@@ -333,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     });
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ===================== products of the scores =====================
     const bool leader = elect_one();
     constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, kTile, 0, 0);
@@ -370,34 +363,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_ts(tmem + kColS, tmem + kColQ + j * 8, dk + (j >> 2) * (1024 >> 4) + (j & 3) * 2, kIdS, j > 0);
 #pragma unroll
           for (int j = 0; j < 2; ++j) umma_ts(tmem + kColS, tmem + kColQ + 128 + j * 8, dr + j * 2, kIdS, 1);
-          ptx::umma_commit(&bars[kSFull]);
+          ptx::umma_commit(&bars[kSFull + (kt & 1u)]);
         }
         __syncwarp();
       }
       ++items;
     });
     drain(kDrain + 1, leader);
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ===================== products with the values =====================
     const bool leader = elect_one();
     constexpr uint32_t kIdO = ptx::idesc_bf16_f32(128, 256, 0, 1);
     const uint64_t desc_v = ptx::smem_desc(smem, 1024, 4096, ptx::kLayoutSw128);
     const uint64_t desc_p = ptx::smem_desc(smem_p, 16, 512, kLayoutSw64);
-    uint32_t kt = 0, items = 0, fixes = 0;
+    uint32_t kt = 0, items = 0;
     walk.each([&](const Item& it) {
       for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
-        const uint32_t slot = kt & 1u, ph = (kt >> 1) & 1u;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kPCopy + slot], kParts * kPBytes / 2 + 256);
+        const uint32_t slot = kt & 1u;
         if (t == it.t0) wait(&bars[kOFree], (items & 1u) ^ 1u, aborted);
-        wait(&bars[kPFull + slot], ph, aborted);
-        wait(&bars[kPCopy + slot], ph, aborted);
+        wait(&bars[kPFull + slot], (kt >> 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) return;
-        if (t > it.t0 && raised(alphas + slot * 128 + 64, lane)) {  // then two warps bring O to the new references
-          wait(&bars[kFixed], fixes++ & 1u, aborted);
-          aborted = __any_sync(0xffffffffu, aborted);
-          if (aborted) return;
-        }
         ptx::tc_fence_after();
         if (leader) {
           const uint64_t dv = desc_v + (kt % kStages) * (kStageBytes >> 4);
@@ -406,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < kParts; ++h)
 #pragma unroll
             for (int j = 0; j < 4; ++j)  // 16 tokens each
-              ptx::umma_bf16(tmem, dp + h * (kPBytes >> 4) + (j >> 1) * (kPBytes / 2 >> 4) + (j & 1) * 2, dv + j * (8192 >> 4), kIdO,
-                             h + j > 0 || t > it.t0 ? 1u : 0u);
+              ptx::umma_bf16(tmem, dp + h * (kPBytes >> 4) + (j >> 1) * (kPBytes / 2 >> 4) + (j & 1) * 2,
+                             dv + j * (8192 >> 4), kIdO, h + j > 0 || t > it.t0 ? 1u : 0u);
           ptx::umma_commit(&bars[kEmpty + kt % kStages]);
-          umma_commit_cluster(&bars[kPFree + slot], 3);
+          ptx::umma_commit(&bars[kPFree + slot]);
           ptx::umma_commit(&bars[kODone + slot]);
         }
         __syncwarp();
@@ -417,15 +403,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
     });
     drain(kDrain, leader);
-  } else {
-    // ============ scores and outputs: half of the tokens of a row per thread ============
+  } else if ((warp & 3) < L.quarters) {
+    // ===== scores and outputs: every other tile, half of a row's tokens per thread =====
     const int r = tid & 127;  // row of the tile, tensor-memory lane
-    const int half = tid >> 7;
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const bool own = static_cast<uint32_t>((warp & 3) >> 1) == rank;
-    const int xr = r & 63;  // row among the 64 of a CTA
-    auto both_halves = [&]() { ptx::bar_sync(1 + (warp & 3), 64); };  // the two warps of these rows
-    uint32_t kt = 0, items = 0;
+    const int half = (warp >> 2) & 1;
+    const uint32_t group = warp >> 3;  // the tiles k = group mod 2
+    const int quarter = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    auto both_halves = [&]() { ptx::bar_sync(1 + 4 * static_cast<int>(group) + quarter, 64); };
+    auto everybody = [&]() { ptx::bar_sync(9, L.quarters * 128); };
+    const int quad = 2 * static_cast<int>(group) + half;  // a quarter of the columns of Q and O
+    uint32_t kt = 0;
     const float f = p.scale_log2;
     walk.each([&](const Item& it) {
       const int row = it.rt * 128 + r;
@@ -434,70 +422,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int limit = valid ? seen_by(L, it, row) : 0;
       const int limit_min = seen_by(L, it, it.rt * 128), limit_max = seen_by(L, it, last_row);
       const int64_t out_row = static_cast<int64_t>(it.seq) * L.rows + row;
+      const uint32_t k1 = kt + (it.t1 - it.t0);  // behind the last tile
       // ---- queries into tensor memory: all products of the item before are complete ----
       {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + out_row * 576);
+        uint32_t v[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 x = valid ? __ldg(src + rank * 32 + half * 16 + c * 8 + e) : make_uint4(0, 0, 0, 0);
-            v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
-          }
-          ptx::tmem_st32(tmem + lanes + kColQ + half * 64 + c * 32, v);
-        }
-        uint32_t v[8];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint4 x = valid ? __ldg(src + 64 + rank * 4 + half * 2 + e) : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = valid ? __ldg(src + rank * 32 + quad * 8 + e) : make_uint4(0, 0, 0, 0);
           v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
         }
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tmem + lanes + kColQ +
-                                                                                                  128 + half * 8),
-                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        const uint4 y = valid ? __ldg(src + 64 + rank * 4 + quad) : make_uint4(0, 0, 0, 0);
+        ptx::tmem_st32(tmem + lanes + kColQ + quad * 32, v);
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tmem + lanes + kColQ + 128 + quad * 4),
+                     "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                      : "memory");
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
       }
-      float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens
-      // this half's columns of O on a new reference, once P V of the tile before k
-      // is in them (a barrier for every other tile: with one, its phase could be two
-      // behind this row's, which looks like done)
-      auto rescale = [&](uint32_t k, float alpha) {
-        wait(&bars[kODone + ((k - 1) & 1u)], ((k - 1) >> 1) & 1u, aborted);
+      float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens, on the reference m
+      // (a warp that gave up goes on, without waiting, to meet the others at the named barriers)
+      for (uint32_t k = kt + ((kt ^ group) & 1u); k < k1; k += 2) {
+        const uint32_t ph = (k >> 1) & 1u;
+        const int t = it.t0 + static_cast<int>(k - kt);
+        wait(&bars[kSFull + group], ph, aborted);
+        if (k > 0) wait(&bars[kXFree + (group ^ 1u)], ((k - 1) >> 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted) return;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          ptx::TmemLd<32>::run(tmem + lanes + half * 128 + c * 32, v);
-          wait_ld32(v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
-          ptx::tmem_st32(tmem + lanes + half * 128 + c * 32, v);
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-      };
-      // the other CTA's rows of tile k: O on their new references, if there are any
-      auto received = [&](uint32_t k, bool later) {
-        const uint32_t slot = k & 1u;
-        wait(&bars[kPCopy + slot], (k >> 1) & 1u, aborted);
-        aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted || !later || !raised(alphas + slot * 128 + 64, lane)) return;
-        rescale(k, alphas[slot * 128 + 64 + xr]);
-        __syncwarp();
-        if (lane == 0 && !aborted) ptx::mbar_arrive(&bars[kFixed]);
-      };
-      for (int t = it.t0; t < it.t1; ++t, ++kt) {
-        const uint32_t slot = kt & 1u, ph = (kt >> 1) & 1u;
-        wait(&bars[kSFull], kt & 1u, aborted);
-        aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted) return;
         ptx::tc_fence_after();
         uint32_t s[32];
         ptx::TmemLd<32>::run(tmem + lanes + kColS + half * 32, s);
@@ -505,47 +457,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kSFree]);
-        if (!own) {
-          // ---- the other CTA's rows: its partial sums; the references of the tile before ----
-          wait(&bars[kXFree + slot], ph ^ 1u, aborted);
-          aborted = __any_sync(0xffffffffu, aborted);
-          if (aborted) return;
-          const uint32_t dst = remote(smem_x + slot * kXBytes + half * (kXBytes / 2), peer);
-          const uint32_t bar = remote(&bars[kXFull + slot], peer);
+        // ---- this CTA's partial sums to the other, and the other's ----
+        if (!aborted) {
+          const uint32_t dst = remote(smem_x + half * (kXBytes / 2), peer), bar = remote(&bars[kXFull + group], peer);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            store_async4(dst + (j * 64 + xr) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
+            store_async4(dst + (j * 128 + r) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
                          __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
-          if (t > it.t0) received(kt - 1, t - 1 > it.t0);
-          if (aborted) return;
-          continue;
         }
-        // ---- own rows: scores, probabilities ----
+        if (r == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], L.quarters * 32 * kTile * 4);
         // Tokens that some rows of the tile see and others do not: a value among
         // this CTA's columns that is not finite makes every row's partial sum
         // not finite.  It becomes zero, so that 0 * NaN does not reach the rows
         // that do not see it; the others have the score.
-        if (xr < 32 && limit_min < limit_max && limit_min < (t + 1) * kTile) {
+        if (quarter == 0 && limit_min < limit_max && limit_min < (t + 1) * kTile) {
           uint32_t odd = 0;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= 1u << j;
           odd = __shfl_sync(0xffffffffu, odd, 0);
           const int from = max(0, limit_min - t * kTile - half * 32), upto = min(32, limit_max - t * kTile - half * 32);
-          unsigned char* stage = smem + (kt % kStages) * kStageBytes + half * 4 * 4096;
+          unsigned char* stage = smem + (k % kStages) * kStageBytes + half * 4 * 4096;
           for (int j = from; j < upto; ++j)
             if ((odd >> j) & 1u)
               *reinterpret_cast<uint4*>(stage + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
         }
-        if (xr == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + slot], kXBytes);
-        wait(&bars[kXFull + slot], ph, aborted);
+        wait(&bars[kXFull + group], ph, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted) return;
         float x[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float4 y = *reinterpret_cast<const float4*>(smem_x + slot * kXBytes + half * (kXBytes / 2) + (j * 64 + xr) * 16);
+          const float4 y = *reinterpret_cast<const float4*>(smem_x + half * (kXBytes / 2) + (j * 128 + r) * 16);
           x[4 * j] = (__uint_as_float(s[4 * j]) + y.x) * f;
           x[4 * j + 1] = (__uint_as_float(s[4 * j + 1]) + y.y) * f;
           x[4 * j + 2] = (__uint_as_float(s[4 * j + 2]) + y.z) * f;
@@ -565,22 +508,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float top = fmaxf(m0, m1);
         __syncwarp();  // every lane has read its sums
-        if (lane == 0) remote_arrive(remote(&bars[kXFree + slot], peer), top);
-        tops[(slot * 2 + half) * 64 + xr] = top;
+        if (lane == 0 && !aborted) remote_arrive(remote(&bars[kXFree + group], peer), top);
+        float* pair = tops + ((ph * 2 + group) * 2) * 128 + r;
+        pair[half * 128] = top;
         both_halves();
-        top = fmaxf(top, tops[(slot * 2 + (half ^ 1)) * 64 + xr]);
-        float alpha = 1.f;
-        if (top > m + kSlack || (m == -CUDART_INF_F && top > m)) {
-          if (t > it.t0) alpha = fp4::fast_exp2(m - top);
-          m = top;
+        top = fmaxf(top, pair[(half ^ 1) * 128]);
+        // the reference of the tile before, which the other group had
+        float before = -CUDART_INF_F;
+        if (k > kt) {
+          wait(&bars[kRef + (group ^ 1u) * 4 + quarter], ((k - 1) >> 1) & 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          before = refs[(group ^ 1u) * 128 + r];
         }
-        l *= alpha;
+        const bool raise = top > before + kSlack || (before == -CUDART_INF_F && top > before);
+        const float now = raise ? top : before;
+        const float alpha = raise && k > kt ? fp4::fast_exp2(before - now) : 1.f;
+        if (half == 0) refs[group * 128 + r] = now;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kRef + group * 4 + quarter]);
+        if (m != now) l *= fp4::fast_exp2(m - now);
+        m = now;
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        wait(&bars[kPFree + slot], ph ^ 1u, aborted);
+        wait(&bars[kPFree + group], ph ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted) return;
+        if (aborted) continue;
         // [half][128 rows x 64 bytes], 64-byte swizzle
-        unsigned char* prow = smem_p + slot * kParts * kPBytes + half * (kPBytes / 2) + (r >> 3) * 512 + (r & 7) * 64;
+        unsigned char* prow = smem_p + group * kParts * kPBytes + half * (kPBytes / 2) + (r >> 3) * 512 + (r & 7) * 64;
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -598,54 +551,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (HI) *reinterpret_cast<uint4*>(prow + kPBytes + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         }
         l += sum0 + sum1;
-        if (half == 0) alphas[slot * 128 + xr] = alpha;
         ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {  // this warp's 32 rows into the other CTA
-          const uint32_t bar = remote(&bars[kPCopy + slot], peer);
+        if (k > kt && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // this half's columns of O on the new reference, once P V of the tile
+          // before is in them (a barrier for every other tile: with one, its
+          // phase could be two behind this row's, which looks like done)
+          wait(&bars[kODone + (group ^ 1u)], ((k - 1) >> 1) & 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            ptx::TmemLd<32>::run(tmem + lanes + half * 128 + c * 32, v);
+            wait_ld32(v);
 #pragma unroll
-          for (int h = 0; h < kParts; ++h)
-            copy_to_cta(remote(prow + h * kPBytes, peer), prow + h * kPBytes, 2048, bar);
-          if (half == 0) copy_to_cta(remote(alphas + slot * 128 + 64 + xr, peer), alphas + slot * 128 + xr, 128, bar);
-        }
-        if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          rescale(kt, alpha);
-          if (aborted) return;
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+            ptx::tmem_st32(tmem + lanes + half * 128 + c * 32, v);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars[kPFull + slot]);
+        if (lane == 0 && !aborted) ptx::mbar_arrive(&bars[kPFull + group]);
       }
-      if (!own) received(kt - 1, it.t1 - it.t0 > 1);
-      if (aborted) return;
-      // ---- the rows' sums, also for the other CTA's columns; then the outputs ----
-      float inv;
-      if (own) {
-        tops[((kt & 1u) * 2 + half) * 64 + xr] = l;
-        both_halves();
-        l += tops[((kt & 1u) * 2 + (half ^ 1)) * 64 + xr];
-        both_halves();  // read before the next tile writes there
-        inv = l != 0.f ? 1.f / l : 0.f;
-        if (half == 0) store_async1(remote(other_l + xr, peer), inv, remote(&bars[kLFull], peer));
-      } else {
-        if (xr == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kLFull], 256);
-        wait(&bars[kLFull], items & 1u, aborted);
-        aborted = __any_sync(0xffffffffu, aborted);
-        if (aborted) return;
-        inv = other_l[xr];
-      }
-      wait(&bars[kODone + ((kt - 1) & 1u)], ((kt - 1) >> 1) & 1u, aborted);
+      // ---- the rows' sums, then the outputs ----
+      everybody();
+      const uint32_t kl = k1 - 1;
+      const float last = refs[(kl & 1u) * 128 + r];
+      if (m != last) l *= fp4::fast_exp2(m - last);
+      m = last;
+      tops[quad * 128 + r] = l;
+      everybody();
+      l = (tops[r] + tops[128 + r]) + (tops[256 + r] + tops[384 + r]);
+      everybody();  // read before the next tile writes there
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      wait(&bars[kODone + (kl & 1u)], (kl >> 1) & 1u, aborted);
       aborted = __any_sync(0xffffffffu, aborted);
+      kt = k1;
       if (aborted) return;
       ptx::tc_fence_after();
       const int64_t part = (static_cast<int64_t>(cluster) * 2 + (it.t0 > 0 ? 0 : 1)) * L.part_rows + r;
       const bool store = valid && r < L.part_rows;
-      if (!it.whole && own && store && half == 0) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
+      if (!it.whole && rank == 0 && store && quad == 0) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t v[32];
-        ptx::TmemLd<32>::run(tmem + lanes + half * 128 + c * 32, v);
+        ptx::TmemLd<32>::run(tmem + lanes + quad * 64 + c * 32, v);
         wait_ld32(v);
-        if (c == 3) {  // O is read: the next item's P V may write it
+        if (c == 1) {  // O is read: the next item's P V may write it
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars[kOFree]);
@@ -656,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float y[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[16 * h + j]);
-          const int64_t col = static_cast<int64_t>(rank) * 256 + half * 128 + c * 32 + h * 16;
+          const int64_t col = static_cast<int64_t>(rank) * 256 + quad * 64 + c * 32 + h * 16;
           if (it.whole) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) y[j] = inv != 0.f ? y[j] * inv : 0.f;
@@ -678,7 +631,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto cluster_of = [&](int u) { return u < wide ? u / (share + 1) : extra + (u - wide) / share; };
         L.desc[cluster] = make_int4(it.seq, it.rt, cluster_of(it.start + kLead), cluster_of(it.end - 1));
       }
-      ++items;
     });
   }
 
@@ -686,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 17) ptx::tmem_dealloc(tmem, 512);
   if (tid == 0 && *gave_up) atomicExch(p.err, kDevErrTimeout);
   cluster_sync();  // the other CTA may still signal this one's barriers
 }
@@ -737,7 +689,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
 }
 
 int smem_bytes(bool hi, int seqs) {
-  return 1024 + stages_of(hi) * kStageBytes + 2 * (hi ? 2 : 1) * kPBytes + 2 * kXBytes + kOffPrefix +
+  return 1024 + stages_of(hi) * kStageBytes + 2 * (hi ? 2 : 1) * kPBytes + kXBytes + kOffPrefix +
          (seqs + 64) / 64 * 256;
 }
 
@@ -794,6 +746,7 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
     L.p.block_tables += static_cast<int64_t>(seq0) * p.max_blocks_per_seq;
     L.rows = static_cast<int>(rows);
     L.row_tiles = static_cast<int>(row_tiles);
+    L.quarters = row_tiles > 1 ? 4 : static_cast<int>((rows + 31) / 32);
     L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
     L.part_rows = part_rows_of(rows);
     // every SM, while a cluster gets a few tiles
