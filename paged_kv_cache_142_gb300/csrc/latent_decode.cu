@@ -643,48 +643,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // the other CTA may still signal this one's barriers
 }
 
-// Parts of items added up: a warp takes 128 columns of a row.  The first cluster
-// behind an item's start reports the item.
+// Parts of items added up: a warp takes a CS-th of a row's columns.  The first
+// cluster behind an item's start reports the item, and the rows of a cluster
+// that reports none, or a later one of an item, are nobody's.
 constexpr int kMergeThreads = 256;
+template <int CS>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  constexpr int N = 4 / CS;  // columns lane * 4 + 128 i
   const int lane = threadIdx.x & 31;
-  const int units = (L.num_clusters - 1) * L.part_rows * 4;
-  for (int u = (blockIdx.x * kMergeThreads + threadIdx.x) >> 5; u < units; u += gridDim.x * kMergeThreads / 32) {
-    const int b = 1 + u / (L.part_rows * 4), r = (u >> 2) % L.part_rows, col = (u & 3) * 128 + lane * 4;
-    const int4 d = L.desc[b];
-    if (d.x < 0 || d.z != b - 1) continue;
-    const int row = d.y * 128 + r;
-    if (row >= L.rows) continue;
-    // the part that begins the item lies in its cluster's second place, the others in their first
-    auto part_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == d.z ? 1 : 0)) * L.part_rows + r; };
-    float M = -CUDART_INF_F;
-#pragma unroll 4
-    for (int c = d.z; c <= d.w; ++c) M = fmaxf(M, __ldcg(L.ml + part_of(c) * 2));
-    const float ref = M == -CUDART_INF_F ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 8
-    for (int c = d.z; c <= d.w; ++c) {
-      const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + part_of(c) * 2));
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(L.o + part_of(c) * 512 + col));
-      if (e.y == 0.f) continue;  // a part that this row sees nothing of
-      const float w = fp4::fast_exp2(e.x - ref);
-      sum = fmaf(w, e.y, sum);
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
+  const int u = (blockIdx.x * kMergeThreads + threadIdx.x) >> 5;
+  const int b = 1 + u / (L.part_rows * CS), r = u / CS % L.part_rows, col = u % CS * 128 + lane * 4;
+  if (b >= L.num_clusters) return;
+  const int4 d = L.desc[b];
+  const int row = d.y * 128 + r;
+  if (d.x < 0 || d.z != b - 1 || row >= L.rows) return;
+  // the part that begins the item lies in its cluster's second place, the others in their first
+  auto part_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == d.z ? 1 : 0)) * L.part_rows + r; };
+  float4 acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float ref = -CUDART_INF_F, sum = 0.f;
+#pragma unroll CS == 1 ? 2 : 8
+  for (int c = d.z; c <= d.w; ++c) {
+    const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + part_of(c) * 2));
+    float4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(L.o + part_of(c) * 512 + col + 128 * i));
+    if (e.y == 0.f) continue;  // a part that this row sees nothing of
+    const float now = fmaxf(ref, e.x), w = fp4::fast_exp2(e.x - now), old = fp4::fast_exp2(ref - now);
+    ref = now;
+    sum = fmaf(w, e.y, sum * old);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      acc[i].x = fmaf(w, x[i].x, acc[i].x * old);
+      acc[i].y = fmaf(w, x[i].y, acc[i].y * old);
+      acc[i].z = fmaf(w, x[i].z, acc[i].z * old);
+      acc[i].w = fmaf(w, x[i].w, acc[i].w * old);
     }
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    const int64_t at = (static_cast<int64_t>(d.x) * L.rows + row) * 512 + col;
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t at = (static_cast<int64_t>(d.x) * L.rows + row) * 512 + col + 128 * i;
+    const float4 y = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
     if (L.p.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.p.out) + at) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.p.out) + at) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
     else
-      *reinterpret_cast<float4*>(static_cast<float*>(L.p.out) + at) =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      *reinterpret_cast<float4*>(static_cast<float*>(L.p.out) + at) = y;
   }
 }
 
@@ -779,10 +786,12 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
     e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess) return e;
     if (L.num_clusters > 1) {
-      int64_t ctas = static_cast<int64_t>(L.num_clusters - 1) * L.part_rows * 4 / (kMergeThreads / 32);
-      const int64_t cap = device_sm_count() * 4;
-      ctas = ctas < 1 ? 1 : (ctas < cap ? ctas : cap);
-      e = launch_early(merge_kernel, dim3(static_cast<unsigned>(ctas)), kMergeThreads, stream, L);
+      // few items have many parts each: more warps a row
+      const bool few = static_cast<int64_t>(L.p.num_seqs) * row_tiles < 16;
+      const int64_t warps = static_cast<int64_t>(L.num_clusters - 1) * L.part_rows * (few ? 4 : 1);
+      const dim3 ctas(static_cast<unsigned>((warps * 32 + kMergeThreads - 1) / kMergeThreads));
+      e = few ? launch_early(merge_kernel<4>, ctas, kMergeThreads, stream, L)
+              : launch_early(merge_kernel<1>, ctas, kMergeThreads, stream, L);
       if (e != cudaSuccess) return e;
     }
   }
