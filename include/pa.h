@@ -591,7 +591,8 @@ pa_status pa_compact_tokens_latent(void* cache, int64_t cache_layer_stride, int3
  * Every table entry read must be in [0, num_blocks) and every length in
  * [0, max_context_len]: one outside is read as block 0, or as an empty
  * sequence, and pa_workspace_error() reports PA_ERR_INVALID_ARG.  Probabilities
- * enter the product with the values in bf16.
+ * enter the product with the values in bf16; for fp32 outputs in two bf16 parts
+ * (2^-16 of the value).
  */
 size_t pa_decode_latent_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_heads, int32_t latent_dim,
                                        int32_t rope_dim, int32_t block_size, int32_t max_context_len);
@@ -604,7 +605,9 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
 /* Causal attention of chunks over a latent cache, expanded form: keys and
  * values of every head are formed from the cached rows (c, r) of the sequence,
  *   k[h][t] = (w_k[h] c_t, r_t)     v[h][t] = w_v[h] c_t
- * rounded to bf16 in the workspace, and the chunk's queries attend to them.
+ * and the chunk's queries attend to them.  bf16 outputs: keys, values and
+ * probabilities are rounded to bf16; fp32 outputs: they are held in two bf16
+ * parts each (2^-16 of the value).
  * Chunk i is q[cu_q[i] .. cu_q[i+1]) at positions q_start[i] + 0, 1, ..., whose
  * rows are in the cache already; query j sees the positions up to its own.
  *   q          device, bf16 [num_tokens][num_heads][head_dim + rope_dim], 16-byte aligned

@@ -8,6 +8,7 @@ import numpy as np
 
 CUT = 2.0 ** -23   # one fp32 addition
 BF16 = 2.0 ** -8   # one rounding to bf16
+TWO = 2.0 ** -16   # a value in two bf16 parts: the second rounds what the first left
 EXP = 2.0 ** -20   # the exponential, the logarithm and the products around them
 
 
@@ -34,10 +35,11 @@ def softmax(s):
     return e / np.where(total > 0, total, 1.0)
 
 
-def attend(q, k, v, scale, limit, dk=None, dv=None):
+def attend(q, k, v, scale, limit, dk=None, dv=None, dp=BF16):
     """out [R, Dv] and its bound in fp32, before a rounding of the output: q [R, D],
     k [T, D], v [T, Dv]; row r sees the first limit[r] keys.  dk, dv: by how
-    much the kernel's keys and values may differ from these."""
+    much the kernel's keys and values may differ from these; dp: the rounding of
+    the probabilities."""
     R, T = q.shape[0], k.shape[0]
     if T == 0:
         return np.zeros((R, v.shape[1])), np.zeros((R, v.shape[1]))
@@ -49,14 +51,14 @@ def attend(q, k, v, scale, limit, dk=None, dv=None):
     d = np.where(hide, 0.0, ds).max(1, keepdims=True)
     p = softmax(s)
     mass = p @ np.abs(v)
-    rel = 2 * np.expm1(2 * d) + EXP + BF16 + (T + 64) * CUT
+    rel = 2 * np.expm1(2 * d) + EXP + dp + (T + 64) * CUT
     tol = rel * mass
     if dv is not None:
         tol = tol + (1 + rel) * (p @ dv)
     return p @ v, tol
 
 
-def decode(q, cache, tables, lens, scale, latent):
+def decode(q, cache, tables, lens, scale, latent, dp=BF16):
     """q [B, Q, H, D] -> (out [B, Q, H, latent], bound)."""
     B, Q, H, _ = q.shape
     bs = cache.shape[1]
@@ -65,7 +67,7 @@ def decode(q, cache, tables, lens, scale, latent):
         x = rows(cache, tables[i], int(lens[i]), bs)
         for j in range(Q):
             limit = np.full(H, max(0, int(lens[i]) - Q + 1 + j))
-            out[i, j], tol[i, j] = attend(q[i, j].astype(np.float64), x, x[:, :latent], scale, limit)
+            out[i, j], tol[i, j] = attend(q[i, j].astype(np.float64), x, x[:, :latent], scale, limit, dp=dp)
     return out, tol
 
 
@@ -75,17 +77,21 @@ def to_bf16(x):
     return np.ldexp(np.rint(m * 256.0), e - 8)
 
 
-def expanded(c, w):
+def expanded(c, w, two=False):
     """c [T, L] by w [D, L]: bf16 values [T, D], and by how much a kernel's may
-    differ: a whole step where fp32 arithmetic may round to the other side."""
+    differ: a whole step where fp32 arithmetic may round to the other side.
+    two: the values themselves, and what two bf16 parts leave."""
     x = c @ w.T
     slack = (c.shape[1] + 4) * CUT * (np.abs(c) @ np.abs(w).T)
+    if two:
+        return x, slack + TWO * (np.abs(x) + slack)
     r = to_bf16(x)
     return r, np.maximum(np.abs(to_bf16(x + slack) - r), np.abs(to_bf16(x - slack) - r))
 
 
-def prefill(q, cache, w_k, w_v, cu, start, tables, scale):
-    """q [T, H, head + rope] -> (out [T, H, head], bound)."""
+def prefill(q, cache, w_k, w_v, cu, start, tables, scale, two=False):
+    """q [T, H, head + rope] -> (out [T, H, head], bound); two: keys, values and
+    probabilities in two bf16 parts instead of one."""
     T, H, _ = q.shape
     head, latent = w_k.shape[1:]
     bs = cache.shape[1]
@@ -96,11 +102,12 @@ def prefill(q, cache, w_k, w_v, cu, start, tables, scale):
             continue
         x = rows(cache, tables[i], a + n, bs)
         for h in range(H):
-            k, dk = expanded(x[:, :latent], w_k[h].astype(np.float64))
-            v, dv = expanded(x[:, :latent], w_v[h].astype(np.float64))
+            k, dk = expanded(x[:, :latent], w_k[h].astype(np.float64), two)
+            v, dv = expanded(x[:, :latent], w_v[h].astype(np.float64), two)
             k = np.concatenate([k, x[:, latent:]], 1)
             dk = np.concatenate([dk, np.zeros_like(x[:, latent:])], 1)
-            o, t = attend(q[cu[i]:cu[i + 1], h].astype(np.float64), k, v, scale, a + 1 + np.arange(n), dk, dv)
+            o, t = attend(q[cu[i]:cu[i + 1], h].astype(np.float64), k, v, scale, a + 1 + np.arange(n), dk, dv,
+                          TWO if two else BF16)
             out[cu[i]:cu[i + 1], h], tol[cu[i]:cu[i + 1], h] = o, t
     return out, tol
 

@@ -189,7 +189,7 @@ size_t pa_prefill_latent_workspace_size(int32_t num_seqs, int32_t num_heads, int
       total_context + static_cast<int64_t>(num_seqs) * 128 >= (int64_t(1) << 31) ||
       check_attention(1, block_size, latent_dim, rope_dim) != PA_OK)
     return 0;
-  return 256 + pa::latent_prefill_workspace(num_seqs, num_heads, latent_dim, rope_dim, head_dim, total_context);
+  return pa::latent_prefill_workspace(num_seqs, num_heads, latent_dim, rope_dim, head_dim, total_context);
 }
 
 pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_t num_tokens, const int32_t* cu_q,

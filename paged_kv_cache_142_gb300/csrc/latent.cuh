@@ -44,6 +44,39 @@ struct LatentPrefillParams {
   unsigned char* ws;
 };
 
+// What the kernels of one pa_prefill_latent call share, in its workspace.  Tokens
+// of the contexts lie one behind the other, each context from a multiple of 128 on.
+struct LatentExpanded {
+  int32_t* tile0;        // [num_seqs + 1] 128-token tiles before a sequence; one without any is empty or refused
+  int64_t* place0;       // [num_seqs + 1] places before a sequence, for one head (latent_prefill.cu)
+  int32_t* counters;     // [CTAs], zeroed by every call
+  float* parts;          // maxima, sums and rows that CTAs leave for one another
+  unsigned char* rope;   // [rows][64] bf16
+  unsigned char* k[2];   // [heads][rows][128] bf16; [1]: what the rounding of [0] left (fp32 outputs)
+  unsigned char* v[2];
+  int64_t rows;          // of a head: whole tiles
+  int32_t head0, heads;  // of this pass
+  bool hi;               // keys and values in two parts
+};
+
+// How the expanded attention's work is counted: an item is a pair of 128-token
+// tiles of a sequence for one head, and has kLatentLead places (what starting and
+// ending it costs a CTA, in steps) and one for each step of 128 keys.
+constexpr int kLatentLead = 2, kLatentPair = 256;
+// steps of pair j of n query tokens behind q0 others
+__host__ __device__ __forceinline__ int latent_steps(int n, int q0, int j) {
+  return (q0 + (n < (j + 1) * kLatentPair ? n : (j + 1) * kLatentPair) + 127) / 128;
+}
+// places of pairs 0 .. j - 1, all whole, for one head: two more steps for every pair
+__host__ __device__ __forceinline__ int64_t latent_places_before(int q0, int j) {
+  return static_cast<int64_t>(j) * (kLatentLead + (q0 + 127) / 128) + static_cast<int64_t>(j) * (j + 1);
+}
+__host__ __device__ __forceinline__ int64_t latent_places(int n, int q0) {
+  if (n <= 0) return 0;
+  const int j = (n + kLatentPair - 1) / kLatentPair - 1;
+  return latent_places_before(q0, j) + kLatentLead + latent_steps(n, q0, j);
+}
+
 struct WeightsParams {
   float* weights;  // [num_seqs], rows weights_stride apart
   int64_t weights_stride;
@@ -78,6 +111,8 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
 size_t latent_prefill_workspace(int num_seqs, int num_heads, int latent_dim, int rope_dim, int head_dim,
                                 int64_t total_context);
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t stream);
+cudaError_t launch_latent_plan(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);
+cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);
 size_t weights_workspace(int num_seqs, int window, int num_q_heads, int num_kv_heads, int head_dim,
                          int max_context_len);
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream);

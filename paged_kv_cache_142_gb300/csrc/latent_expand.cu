@@ -1,0 +1,379 @@
+// Keys and values of every head from the latent rows:
+//   K[h][t] = w_k[h] c_t,   V[h][t] = w_v[h] c_t,   D[128 x 256] = C[128 x 512] W[h]^T
+// for 128-token tiles of the contexts, and the position parts of the rows packed
+// beside them.  Rounded to bf16; where the outputs are fp32, to two bf16 parts
+// (2^-17 together).  Rows behind a context are zeros.  A token whose value is
+// not finite gets a value of zero and a key of NaN: whoever sees it puts out NaN,
+// and 0 * NaN does not reach the rows that do not.
+//
+// A CTA holds its tile's rows (128 KB, gathered through the block table by TMA)
+// and walks the heads; their weights stream.  4096 clocks of products need 256 KB
+// of weights, 64 bytes a clock, more than the second-level cache feeds every SM
+// with: so a cluster of two CTAs with two tiles takes the same heads, and each
+// loads half of the weights for both (multicast).
+// Six warps: 0-3 write out (a token a thread), 4 loads, 5 issues products; the
+// results of two heads alternate in tensor memory.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "decode.cuh"
+#include "fp4.cuh"
+#include "latent.cuh"
+#include "ptx.cuh"
+#include "umma.cuh"
+
+namespace pa {
+namespace latent_expand_detail {
+
+using namespace um;
+
+// ---------------------------------------------------------------- the plan
+// Tiles and places before every sequence; one CTA.  The contexts of the chunks
+// before count in 64 bits, and the counters of the attention start at zero.
+constexpr int kPlanThreads = 512;
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LatentPrefillParams p, const LatentExpanded x, int num_counters) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int64_t sums[3][kPlanThreads / 32];
+  const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+  int64_t seen = 0, tiles = 0, places = 0;  // before this round of kPlanThreads sequences
+  for (int i = tid; i < num_counters; i += kPlanThreads) x.counters[i] = 0;
+  if (tid == 0) x.tile0[0] = 0, x.place0[0] = 0;
+  for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int64_t n = 0, q0 = 0;
+    bool ok = false, bad = false;
+    if (s < p.num_seqs) {
+      const int64_t b = p.cu_q[s];
+      n = static_cast<int64_t>(p.cu_q[s + 1]) - b, q0 = p.q_start[s];
+      ok = n > 0 && n <= p.max_q_len && b >= 0 && b + n <= p.num_tokens && q0 >= 0 && q0 + n <= p.max_context_len &&
+           q0 + n <= table_tokens;
+      bad = n != 0 && !ok;
+    }
+    auto scan = [&](int64_t v, int which) {  // inclusive, over the block
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane == 31) sums[which][warp] = v;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) v += sums[which][w];
+      return v;
+    };
+    auto all = [&](int which) {
+      int64_t v = 0;
+      for (int w = 0; w < kPlanThreads / 32; ++w) v += sums[which][w];
+      return v;
+    };
+    const int64_t upto = seen + scan(ok ? q0 + n : 0, 0);
+    seen += all(0);
+    if (ok && upto > p.total_context) ok = false, bad = true;
+    const int64_t t = tiles + scan(ok ? (q0 + n + 127) / 128 : 0, 1);
+    const int64_t u = places + scan(ok ? latent_places(static_cast<int>(n), static_cast<int>(q0)) : 0, 2);
+    tiles += all(1);
+    places += all(2);
+    if (s < p.num_seqs) {
+      x.tile0[s + 1] = static_cast<int32_t>(t);
+      x.place0[s + 1] = u;
+      if (bad && p.status) atomicExch(p.status, kDevErrInvalidArg);
+    }
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------- the expansion
+constexpr int kThreads = 6 * 32;
+constexpr int kABytes = 8 * 16384;   // [8 chunks of 64 columns][128 rows x 128 bytes]
+constexpr int kBBytes = 32768;       // a chunk of a head's weights: 128 rows of w_k, 128 of w_v
+constexpr int kStages = 2;
+constexpr int kOffB = kABytes, kOffBar = kOffB + kStages * kBBytes;
+constexpr int kSmemBytes = 1024 + kOffBar + 256;
+enum : int { kAFull = 0, kAFree = 1, kBFull = 2, kBFree = 4, kDFull = 6, kDFree = 8, kDrain = 10, kNumBars = 11 };
+
+struct Launch {
+  LatentPrefillParams p;
+  LatentExpanded x;
+  int bs_log;
+};
+
+// 16 columns of a token's key or value, in one part or two
+__device__ __forceinline__ void store16(const LatentExpanded& x, unsigned char* const (&dst)[2], int64_t at, const float (&y)[16]) {
+  uint32_t h[8], l[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+    l[e] = pack_bf16(y[2 * e] - __uint_as_float(h[e] << 16), y[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
+  }
+  fp4::store32(dst[0] + at * 2, h);
+  if (x.hi) fp4::store32(dst[1] + at * 2, l);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    expand_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_pool,
+                  const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv) {
+  const LatentPrefillParams& p = L.p;
+  const LatentExpanded& x = L.x;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+
+  ptx::griddep_launch_dependents();
+  if (tid == 0) {
+    ptx::mbar_init(&bars[kAFull], 1);
+    ptx::mbar_init(&bars[kAFree], 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kBFull + i], 1);
+      ptx::mbar_init(&bars[kBFree + i], 2);
+      ptx::mbar_init(&bars[kDFull + i], 1);
+      ptx::mbar_init(&bars[kDFree + i], 4);
+    }
+    ptx::mbar_init(&bars[kDrain], 1);
+    *gave_up = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == 5) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool aborted = false;
+  ptx::griddep_wait();
+  cluster_sync();  // both CTAs' barriers are ready
+
+  // units (pair of tiles, head), equal runs of them for the clusters
+  const int tiles = x.tile0[p.num_seqs];
+  const int64_t units = static_cast<int64_t>((tiles + 1) / 2) * x.heads;
+  const int64_t clusters = gridDim.x / 2, c = blockIdx.x / 2;
+  const int64_t u0 = units * c / clusters, u1 = units * (c + 1) / clusters;
+
+  // a tile's sequence, first token and tokens (none for a tile behind the last)
+  struct Tile {
+    int seq, tok, n;
+  };
+  auto tile_of = [&](int64_t unit) {
+    Tile t{0, 0, 0};
+    const int i = static_cast<int>(unit / x.heads) * 2 + static_cast<int>(rank);
+    if (i >= tiles) return t;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {  // the last sequence that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (x.tile0[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    t.seq = lo;
+    t.tok = (i - x.tile0[lo]) * 128;
+    t.n = min(128, p.q_start[lo] + p.cu_q[lo + 1] - p.cu_q[lo] - t.tok);
+    return t;
+  };
+
+  if (warp == 4) {
+    // ============================== loads ==============================
+    const int page_rows = min(128, 1 << L.bs_log);
+    uint32_t kb = 0, ka = 0;
+    const uint64_t keep = ptx::policy_evict_last();
+    for (int64_t u = u0; u < u1 && !aborted; ++u) {
+      const int h = x.head0 + static_cast<int>(u % x.heads);
+      if (u == u0 || u % x.heads == 0) {
+        const Tile t = tile_of(u);
+        wait(&bars[kAFree], (ka & 1u) ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        ++ka;
+        const int pages = (t.n + page_rows - 1) / page_rows;
+        if (lane == 0) {
+          if (pages) ptx::mbar_arrive_expect_tx(&bars[kAFull], static_cast<uint32_t>(pages * page_rows) * 1024u);
+          else ptx::mbar_arrive(&bars[kAFull]);
+        }
+        __syncwarp();
+        if (lane < pages) {
+          const int tok = t.tok + lane * page_rows;
+          int phys = __ldg(p.block_tables + static_cast<int64_t>(t.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+          if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
+            if (p.status) atomicExch(p.status, kDevErrInvalidArg);
+            phys = 0;
+          }
+          const int at = static_cast<int>((static_cast<int64_t>(phys) << L.bs_log) + (tok & ((1 << L.bs_log) - 1)));
+          for (int ch = 0; ch < 8; ++ch)
+            ptx::tma_load_2d(smem + ch * 16384 + lane * page_rows * 128, &tm_pool, ch * 64, at, &bars[kAFull], keep);
+        }
+        __syncwarp();
+      }
+      for (int ch = 0; ch < 8 && !aborted; ++ch, ++kb) {
+        const uint32_t slot = kb % kStages;
+        wait(&bars[kBFree + slot], ((kb / kStages) & 1u) ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (!aborted && lane == 0) {
+          ptx::mbar_arrive_expect_tx(&bars[kBFull + slot], kBBytes);
+          tma_load_2d_cluster(smem + kOffB + slot * kBBytes + rank * 16384, rank ? &tm_wv : &tm_wk, ch * 64, h * 128,
+                              &bars[kBFull + slot], 3, keep);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 5) {
+    // ============================ products ============================
+    const bool leader = elect_one();
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, 256, 0, 0);
+    const uint64_t desc_a = ptx::smem_desc(smem, 16, 1024, ptx::kLayoutSw128);
+    const uint64_t desc_b = ptx::smem_desc(smem + kOffB, 16, 1024, ptx::kLayoutSw128);
+    uint32_t kb = 0, ka = 0, kd = 0;
+    for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
+      if (u == u0 || u % x.heads == 0) wait(&bars[kAFull], ka++ & 1u, aborted);
+      wait(&bars[kDFree + (kd & 1u)], ((kd >> 1) & 1u) ^ 1u, aborted);
+      const uint32_t d = tmem + (kd & 1u) * 256;
+      for (int ch = 0; ch < 8; ++ch, ++kb) {
+        const uint32_t slot = kb % kStages;
+        wait(&bars[kBFull + slot], (kb / kStages) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        ptx::tc_fence_after();
+        if (leader) {
+          const uint64_t da = desc_a + ch * (16384 >> 4), db = desc_b + slot * (kBBytes >> 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ptx::umma_bf16(d, da + j * 2, db + j * 2, kId, ch + j > 0);
+          umma_commit_cluster(&bars[kBFree + slot], 3);
+          if (ch == 7) {
+            ptx::umma_commit(&bars[kDFull + (kd & 1u)]);
+            if (u + 1 == u1 || (u + 1) % x.heads == 0) ptx::umma_commit(&bars[kAFree]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (leader) {  // nothing may be in flight when tensor memory is freed
+      ptx::umma_commit(&bars[kDrain]);
+      bool late = false;
+      wait(&bars[kDrain], 0, late);
+      if (late) aborted = true;
+    }
+    aborted = __any_sync(0xffffffffu, aborted);
+  } else {
+    // ===================== results: a token a thread =====================
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    uint32_t kd = 0;
+    Tile t{0, 0, 0};
+    for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
+      if (u == u0 || u % x.heads == 0) t = tile_of(u);
+      const int h = static_cast<int>(u % x.heads);
+      const int tile = static_cast<int>(u / x.heads) * 2 + static_cast<int>(rank);
+      const int64_t row = static_cast<int64_t>(tile) * 128 + tid;
+      const bool there = tile < tiles, valid = tid < t.n;
+      if (h == 0 && there) {  // the position part, packed
+        uint4 r[8];
+        const int tok = t.tok + tid;
+        if (valid) {
+          int phys = __ldg(p.block_tables + static_cast<int64_t>(t.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+          if (phys < 0 || phys >= p.num_blocks) phys = 0;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(p.cache) +
+              ((static_cast<int64_t>(phys) << L.bs_log) + (tok & ((1 << L.bs_log) - 1))) * 576 + 512);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[e] = __ldg(src + e);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<uint4*>(x.rope)[row * 8 + e] = valid ? r[e] : make_uint4(0, 0, 0, 0);
+      }
+      wait(&bars[kDFull + (kd & 1u)], (kd >> 1) & 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) break;
+      ptx::tc_fence_after();
+      const uint32_t d = tmem + lanes + (kd & 1u) * 256;
+      const int64_t at = (static_cast<int64_t>(h) * x.rows + row) * 128;
+      bool odd = false;  // the value is not finite somewhere
+#pragma unroll 1
+      for (int col = 0; col < 256; col += 32) {
+        const int from = (col + 128) & 255;  // values first
+        uint32_t v[32];
+        ptx::TmemLd<32>::run(d + from, v);
+        wait_ld32(v);
+        if (col == 224) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars[kDFree + (kd & 1u)]);
+        }
+        if (!there) continue;
+        if (from >= 128) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) odd |= (v[j] & 0x7fffffffu) >= 0x7f7f8000u;  // in bf16
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float y[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            y[j] = !valid ? 0.f : (from < 128 && odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(v[16 * q + j]));
+          store16(x, from < 128 ? x.k : x.v, at + (from & 127) + 16 * q, y);
+        }
+      }
+      if (odd && valid && there) {  // no value, in place of what was stored
+        const float none[16] = {};
+        for (int col = 0; col < 128; col += 16) store16(x, x.v, at + col, none);
+      }
+    }
+  }
+
+  if (aborted) *gave_up = 1;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 5) ptx::tmem_dealloc(tmem, 512);
+  if (tid == 0 && *gave_up && p.status) atomicExch(p.status, kDevErrTimeout);
+  cluster_sync();  // the other CTA may still load and signal here
+}
+
+}  // namespace latent_expand_detail
+
+cudaError_t launch_latent_plan(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream) {
+  using namespace latent_expand_detail;
+  return launch_early(plan_kernel, dim3(1), kPlanThreads, stream, p, x, static_cast<int>(device_sm_count()));
+}
+
+cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream) {
+  using namespace latent_expand_detail;
+  Launch L{};
+  L.p = p;
+  L.x = x;
+  L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
+  CUtensorMap tm_pool, tm_wk, tm_wv;
+  const uint64_t pool[2] = {576, static_cast<uint64_t>(p.num_blocks) * p.block_size}, pool_stride[1] = {1152};
+  const uint32_t pool_box[2] = {64, static_cast<uint32_t>(p.block_size < 128 ? p.block_size : 128)};
+  const uint64_t w[2] = {512, static_cast<uint64_t>(p.num_heads) * 128}, w_stride[1] = {1024};
+  const uint32_t w_box[2] = {64, 128};
+  if (!encode_bf16_tiles(&tm_pool, 2, p.cache, pool, pool_stride, pool_box, 128) ||
+      !encode_bf16_tiles(&tm_wk, 2, p.w_k, w, w_stride, w_box, 128) ||
+      !encode_bf16_tiles(&tm_wv, 2, p.w_v, w, w_stride, w_box, 128))
+    return cudaErrorInvalidValue;
+  const void* fn = reinterpret_cast<const void*>(&expand_kernel);
+  int per_sm = 0;
+  cudaError_t e = fp4_occupancy(fn, kThreads, kSmemBytes, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (x.rows / 128 + 1) / 2 * x.heads, most = device_sm_count() / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < 1 ? 1 : (units < most ? units : most))));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  void* args[] = {&L, &tm_pool, &tm_wk, &tm_wv};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace pa

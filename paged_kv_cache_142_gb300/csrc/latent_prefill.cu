@@ -1,6 +1,29 @@
 // Causal attention of chunks of queries over the latent cache in its expanded
-// form: k[h,t] = (w_k[h] c[t], rope[t]), v[h,t] = w_v[h] c[t], c the latent part
-// of a row.  First the keys and values of every head, then the attention.
+// form, on the 5th-generation tensor cores: keys of 128 + 64 dims, values of 128.
+//
+//   S[128 rows x 128 keys] = Q K^T,   P = 2^(S f - m),   O[128 x 128] += P V
+// The keys and values of every head are expanded first (latent_expand.cu), so
+// that a query and key pair costs 320 multiplications instead of the absorbed
+// form's 1088, and a key's 131072 for its two projections are shared by all
+// queries.  A row is one token of one head; a CTA takes two tiles of 128 tokens,
+// so that every key and value loaded serves 256 rows.  Accumulators are fp32 in
+// tensor memory: S of both tiles, O of both.  P is written over its S and read
+// from there as the A operand; bf16 outputs take it in bf16 (2^-8, as the output),
+// fp32 outputs take P, keys and values in two bf16 parts (2^-17 together).
+//
+// Queries take 96 KB of shared memory; the rest is a ring of eight 16 KB pieces (64
+// dims of a step's keys; 64 of its values' tokens), each freed as both tiles have
+// used it.
+//
+// The work is cut into equal runs of steps (128 keys of a tile pair), one for
+// each CTA, across the borders of heads, pairs and sequences; an item is a
+// (sequence, tile pair, head).  A CTA that takes part of an item's keys leaves its
+// rows unnormalised in the workspace with their maximum and sum, and the last CTA
+// of the item adds the parts up in the order of the keys.
+//
+// One CTA per SM, 11 warps, each role walking the same items: 0-3 and 4-7 the
+// softmax of the first and the second tile (a row a thread), 8 loads, 9 and 10
+// issue the products of the first and the second tile.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -8,156 +31,687 @@
 #include "fp4.cuh"
 #include "latent.cuh"
 #include "ptx.cuh"
+#include "umma.cuh"
 
 namespace pa {
-namespace {
+namespace latent_prefill_detail {
 
-// The first place of each chunk's context in the expanded arrays, a multiple of
-// 128; -1 for an empty chunk and for one that is refused.  One CTA; the contexts
-// of the chunks before count in 64 bits.
-constexpr int kPlanThreads = 512;
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LatentPrefillParams p, int32_t* base) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ int64_t sums[2][kPlanThreads / 32];
-  const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
-  int64_t seen = 0, place = 0;  // contexts and places of the sequences before this round of kPlanThreads
-  for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    int64_t len = 0;
-    bool bad = false;
-    if (s < p.num_seqs) {
-      const int64_t b = p.cu_q[s], n = static_cast<int64_t>(p.cu_q[s + 1]) - b, q0 = p.q_start[s];
-      bad = n != 0;
-      if (n > 0 && n <= p.max_q_len && b >= 0 && b + n <= p.num_tokens && q0 >= 0 && q0 + n <= p.max_context_len &&
-          q0 + n <= table_tokens)
-        len = q0 + n, bad = false;
+using namespace um;
+
+constexpr int kThreads = 11 * 32;
+constexpr int kPiece = 16384;
+constexpr int kSlots = 8;
+constexpr int kOffRing = 6 * kPiece;  // behind the queries: [tile][3 chunks of 64 dims][128 rows x 128 bytes]
+constexpr int kOffBar = kOffRing + kSlots * kPiece;
+constexpr int kSmemBytes = 1024 + kOffBar + 512;
+constexpr float kSlack = 8.f;  // the reference is raised past 2^8
+
+// barriers
+enum : int {
+  kFull = 0, kFree = kSlots, kQFull = 2 * kSlots, kQFree, kSFull, kPFull = kSFull + 2, kODone = kPFull + 2,
+  kOFree = kODone + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1
+};
+static_assert(kNumBars * 8 + 32 <= 512, "barrier area");
+constexpr uint32_t kColO = 256;  // tensor memory: S of the tiles at 0 and 128, then O of the tiles
+
+constexpr int kLead = kLatentLead, kPair = kLatentPair;
+
+struct Launch {
+  LatentPrefillParams p;
+  LatentExpanded x;
+};
+
+// A sequence's items, pair after pair with the heads inside.
+struct Chunk {
+  int b, n, q0;
+  int64_t row0;  // of its context in the expanded arrays
+  __device__ __forceinline__ int pairs() const { return (n + kPair - 1) / kPair; }
+  __device__ __forceinline__ int tiles(int j) const { return latent_steps(n, q0, j); }
+  __device__ __forceinline__ int64_t before(int j) const { return latent_places_before(q0, j); }
+};
+
+__device__ __forceinline__ Chunk chunk_of(const Launch& L, int seq) {
+  Chunk c;
+  c.b = L.p.cu_q[seq];
+  c.n = L.p.cu_q[seq + 1] - c.b;
+  c.q0 = L.p.q_start[seq];
+  c.row0 = static_cast<int64_t>(L.x.tile0[seq]) * 128;
+  return c;
+}
+
+// An item and this CTA's part of it.
+struct Item {
+  Chunk c;
+  int seq, pair, head;  // the head among this pass's
+  int64_t start, end;   // places: kLead, then the steps
+  int tok0, pos0, ntok; // first token in the chunk; its position; tokens of the two tiles
+  int t0, t1;           // this CTA's steps
+  int n0, n1;           // this CTA's steps of each tile
+  bool whole;
+  __device__ __forceinline__ int kend() const { return pos0 + ntok; }  // keys that the last token sees
+  __device__ __forceinline__ int steps_of(int tile) const { return tile ? n1 : n0; }
+};
+
+struct Walk {
+  const Launch& L;
+  int64_t c_begin, c_end;
+  __device__ __forceinline__ void derive(Item& it) const {
+    const int tiles = it.c.tiles(it.pair);
+    it.end = it.start + kLead + tiles;
+    it.tok0 = it.pair * kPair;
+    it.ntok = min(kPair, it.c.n - it.tok0);
+    it.pos0 = it.c.q0 + it.tok0;
+    const int64_t first = it.start + kLead;
+    it.t0 = static_cast<int>((c_begin > first ? c_begin : first) - first);
+    it.t1 = static_cast<int>((c_end < it.end ? c_end : it.end) - first);
+    it.whole = it.t0 == 0 && it.t1 == tiles;
+    // the first tile's last token may see fewer keys than the second's
+    const int seen0 = (it.pos0 + min(128, it.ntok) + 127) / 128;
+    it.n0 = max(0, min(it.t1, seen0) - it.t0);
+    it.n1 = it.ntok > 128 ? max(0, it.t1 - it.t0) : 0;
+  }
+  // the item at c_begin; one copy for every kind of warp
+  __device__ __noinline__ void find(Item& it) const {
+    const int heads = L.x.heads;
+    int lo = 0, hi = L.p.num_seqs - 1;
+    while (lo < hi) {  // the last sequence that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (L.x.place0[mid] * heads <= c_begin) lo = mid;
+      else hi = mid - 1;
     }
-    const int64_t padded = (len + 127) / 128 * 128;
-    int64_t x = len, y = padded;
+    it.seq = lo;
+    it.c = chunk_of(L, lo);
+    int64_t r = c_begin - L.x.place0[lo] * heads;
+    int a = 0, b = it.c.pairs() - 1;
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (heads * it.c.before(mid) <= r) a = mid;
+      else b = mid - 1;
+    }
+    r -= heads * it.c.before(a);
+    const int places = kLead + it.c.tiles(a);
+    it.pair = a;
+    it.head = static_cast<int>(r / places);
+    it.start = c_begin - r % places;
+    derive(it);
+  }
+  __device__ __forceinline__ void next(Item& it) const {
+    it.start = it.end;
+    if (++it.head == L.x.heads) {
+      it.head = 0;
+      if (++it.pair * kPair >= it.c.n) {
+        it.pair = 0;
+        do ++it.seq;
+        while (L.x.place0[it.seq + 1] * L.x.heads == it.start);  // sequences without places
+        it.c = chunk_of(L, it.seq);
+      }
+    }
+    derive(it);
+  }
+  // calls f for every item with steps of this CTA's
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    Item it;
+    it.end = c_begin;
+    for (bool more = c_begin < c_end; more;) {
+      if (it.end == c_begin) find(it);
+      else next(it);
+      more = it.end < c_end;
+      if (it.t1 > it.t0) f(it);
+    }
+  }
+};
+
+__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
+// A row's probabilities 2^(s f + bias) of a step's 128 keys as 64 bf16 pairs (HI:
+// and what their rounding left), their sum, and the largest s; MASK: keys from
+// nvis on do not count.  The next 16 scores load while 16 are worked on.
+template <bool MASK, bool HI>
+__device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&hi)[64],
+                                              uint32_t (&lo)[HI ? 64 : 1], float& top, float& sum) {
+  const uint64_t ff = fp4::pair(f, f), bb = fp4::pair(bias, bias);
+  uint64_t s0 = 0, s1 = 0;
+  float m0 = -CUDART_INF_F, m1 = m0;
+  uint32_t v[2][16];
+  ptx::TmemLd<16>::run(s_at, v[0]);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) x += u, y += v;
+  for (int c = 0; c < 8; ++c) {
+    wait_ld16(v[c & 1]);
+    if (c < 7) ptx::TmemLd<16>::run(s_at + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(v[c & 1][j + e]);
+        if (MASK && c * 16 + j + e >= nvis) x[e] = -CUDART_INF_F;
+      }
+      m0 = max3(m0, x[0], x[1]);
+      m1 = max3(m1, x[2], x[3]);
+      const float2 a = fp4::unpair(fp4::fma2(fp4::pair(x[0], x[1]), ff, bb));
+      const float2 b = fp4::unpair(fp4::fma2(fp4::pair(x[2], x[3]), ff, bb));
+      const float e0 = fp4::fast_exp2(a.x), e1 = fp4::fast_exp2(a.y), e2 = fp4::fast_exp2(b.x), e3 = fp4::fast_exp2(b.y);
+      s0 = fp4::add2(s0, fp4::pair(e0, e1));
+      s1 = fp4::add2(s1, fp4::pair(e2, e3));
+      const int at = (c * 16 + j) / 2;
+      hi[at] = pack_bf16(e0, e1);
+      hi[at + 1] = pack_bf16(e2, e3);
+      if (HI) {
+        lo[at] = pack_bf16(e0 - __uint_as_float(hi[at] << 16), e1 - __uint_as_float(hi[at] & 0xffff0000u));
+        lo[at + 1] = pack_bf16(e2 - __uint_as_float(hi[at + 1] << 16), e3 - __uint_as_float(hi[at + 1] & 0xffff0000u));
+      }
     }
-    if (lane == 31) sums[0][warp] = x, sums[1][warp] = y;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) x += sums[0][w], y += sums[1][w];
-    if (s < p.num_seqs) {
-      if (seen + x > p.total_context) bad = bad || len > 0, len = 0;
-      base[s] = len > 0 ? static_cast<int32_t>(place + y - padded) : -1;
-      if (bad && p.status) atomicExch(p.status, kDevErrInvalidArg);
+  }
+  top = fmaxf(m0, m1);
+  const float2 t = fp4::unpair(fp4::add2(s0, s1));
+  sum = t.x + t.y;
+}
+// the largest of a row's first nvis scores of a step
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t s_at, int nvis) {
+  float m0 = -CUDART_INF_F, m1 = m0;
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t v[32];
+    ptx::TmemLd<32>::run(s_at + c, v);
+    wait_ld32(v);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = MASK && c + j + e >= nvis ? -CUDART_INF_F : __uint_as_float(v[j + e]);
+      m0 = max3(m0, x[0], x[1]);
+      m1 = max3(m1, x[2], x[3]);
     }
-    for (int w = 0; w < kPlanThreads / 32; ++w) seen += sums[0][w], place += sums[1][w];
-    __syncthreads();
+  }
+  return fmaxf(m0, m1);
+}
+
+// 16 outputs of a row, times inv, in whole 32-byte sectors
+__device__ __forceinline__ void store_out(const LatentPrefillParams& p, int64_t at, const uint32_t (&v)[16], float inv) {
+  uint32_t h[8];
+  if (p.out_bf16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+    fp4::store32(static_cast<__nv_bfloat16*>(p.out) + at, h);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(__uint_as_float(v[8 * q + e]) * inv);
+      fp4::store32(static_cast<float*>(p.out) + at + 8 * q, h);
+    }
   }
 }
 
-// a block: 8 tokens of a sequence, a head; a thread: a dim of the head's key and value
-__global__ void __launch_bounds__(128) expand_kernel(const LatentPrefillParams p, const int32_t* bases, __nv_bfloat16* k, __nv_bfloat16* v) {
+template <bool HI>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_q,
+                  const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_v2) {
+  constexpr int kKeys = HI ? 5 : 3, kValues = HI ? 4 : 2;  // pieces of a step
+  const LatentPrefillParams& p = L.p;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* ring = smem + kOffRing;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = gave_up + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
   ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int seq = blockIdx.z, h = blockIdx.y, t0 = blockIdx.x * 8;
-  const int64_t base = bases[seq];
-  if (base < 0) return;
-  const int len = p.q_start[seq] + p.cu_q[seq + 1] - p.cu_q[seq];
-  if (t0 >= len) return;
-  __shared__ float c[8][512];
-  const int dim = p.latent_dim + p.rope_dim;
-  for (int i = threadIdx.x; i < 8 * p.latent_dim; i += 128) {
-    const int t = t0 + i / p.latent_dim;
-    float x = 0.f;
-    if (t < len) {
-      int phys = p.block_tables[static_cast<int64_t>(seq) * p.max_blocks_per_seq + t / p.block_size];
-      if (phys < 0 || phys >= p.num_blocks) {
-        if (p.status) atomicExch(p.status, kDevErrInvalidArg);
-        phys = 0;
-      }
-      x = __bfloat162float(static_cast<const __nv_bfloat16*>(
-          p.cache)[(static_cast<int64_t>(phys) * p.block_size + t % p.block_size) * dim + i % p.latent_dim]);
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(&bars[kFull + i], 1);
+      ptx::mbar_init(&bars[kFree + i], 2);
     }
-    c[i / p.latent_dim][i % p.latent_dim] = x;
+    ptx::mbar_init(&bars[kQFull], 1);
+    ptx::mbar_init(&bars[kQFree], 2);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kSFull + i], 1);
+      ptx::mbar_init(&bars[kPFull + i], 4);
+      ptx::mbar_init(&bars[kODone + i], 1);
+      ptx::mbar_init(&bars[kOFree + i], 4);
+    }
+    ptx::mbar_init(&bars[kDrain], 2);
+    *gave_up = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tc_fence_before();
   }
   __syncthreads();
-  const int64_t w_at = (static_cast<int64_t>(h) * p.head_dim + threadIdx.x) * p.latent_dim;
-  const __nv_bfloat16* wk = static_cast<const __nv_bfloat16*>(p.w_k) + w_at;
-  const __nv_bfloat16* wv = static_cast<const __nv_bfloat16*>(p.w_v) + w_at;
-  float ak[8] = {}, av[8] = {};
-  for (int i = 0; i < p.latent_dim; ++i) {
-    const float a = __bfloat162float(wk[i]), b = __bfloat162float(wv[i]);
-    for (int j = 0; j < 8; ++j) ak[j] = fmaf(a, c[j][i], ak[j]), av[j] = fmaf(b, c[j][i], av[j]);
-  }
-  for (int j = 0; j < 8 && t0 + j < len; ++j) {
-    const int64_t at = ((base + t0 + j) * p.num_heads + h) * 128 + threadIdx.x;
-    k[at] = __float2bfloat16(ak[j]);
-    v[at] = __float2bfloat16(av[j]);
-  }
-}
-
-// a warp: one query row
-__global__ void __launch_bounds__(128) attend_kernel(const LatentPrefillParams p, const int32_t* bases, const __nv_bfloat16* k,
-                                                     const __nv_bfloat16* v) {
-  ptx::griddep_launch_dependents();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool aborted = false;
   ptx::griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int seq = blockIdx.z, h = blockIdx.y, j = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int b = p.cu_q[seq], n = p.cu_q[seq + 1] - b;
-  const int64_t base = bases[seq];
-  if (base < 0 || j >= n) return;
-  const int limit = p.q_start[seq] + j + 1;
-  const int64_t row = static_cast<int64_t>(b + j) * p.num_heads + h;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row * 192;
-  float qv[6], acc[4] = {};
-  for (int i = 0; i < 6; ++i) qv[i] = __bfloat162float(q[i * 32 + lane]) * p.scale_log2;
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int t = 0; t < limit; ++t) {
-    int phys = p.block_tables[static_cast<int64_t>(seq) * p.max_blocks_per_seq + t / p.block_size];
-    if (phys < 0 || phys >= p.num_blocks) phys = 0;
-    const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.cache) +
-                             (static_cast<int64_t>(phys) * p.block_size + t % p.block_size) * 576 + 512;
-    const int64_t at = ((base + t) * p.num_heads + h) * 128;
-    float s = 0.f;
-    for (int i = 0; i < 4; ++i) s = fmaf(qv[i], __bfloat162float(k[at + i * 32 + lane]), s);
-    for (int i = 0; i < 2; ++i) s = fmaf(qv[4 + i], __bfloat162float(r[i * 32 + lane]), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s), ref = mn == -CUDART_INF_F ? 0.f : mn;
-    const float a = exp2f(m - ref), e = exp2f(s - ref);
-    l = l * a + e;
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(e, __bfloat162float(v[at + i * 32 + lane]), acc[i] * a);
-    m = mn;
+
+  const int64_t total = L.x.place0[p.num_seqs] * L.x.heads;
+  const int64_t share = total / gridDim.x, extra = total - share * gridDim.x;
+  auto cta_begin = [&](int64_t c) { return c * share + (c < extra ? c : extra); };
+  const Walk walk{L, cta_begin(blockIdx.x), cta_begin(blockIdx.x + 1)};
+
+  if (warp == 8) {
+    // ============================== loads ==============================
+    uint32_t ic = 0, uc = 0;  // items, pieces
+    const uint64_t first = ptx::policy_evict_first(), normal = ptx::policy_evict_normal();
+    auto piece = [&]() -> unsigned char* {  // the next piece's place, once it is free
+      const uint32_t slot = uc % kSlots;
+      wait(&bars[kFree + slot], ((uc / kSlots) & 1u) ^ 1u, aborted);
+      if (aborted) return nullptr;
+      ptx::mbar_arrive_expect_tx(&bars[kFull + slot], kPiece);
+      return ring + slot * kPiece;
+    };
+    if (lane == 0)
+      walk.each([&](const Item& it) {
+        if (aborted) return;
+        const int n = max(it.n0, it.n1);
+        const int row0 = static_cast<int>(it.c.row0), at0 = static_cast<int>(it.head * L.x.rows + it.c.row0);
+        // the queries; rows past the chunk are other rows' or zeros, and nobody's
+        wait(&bars[kQFree], (ic & 1u) ^ 1u, aborted);
+        if (aborted) return;
+        ++ic;
+        const int tiles = it.ntok > 128 ? 2 : 1;
+        ptx::mbar_arrive_expect_tx(&bars[kQFull], static_cast<uint32_t>(tiles * 3 * kPiece));
+        for (int i = 0; i < tiles; ++i)
+          for (int c = 0; c < 3; ++c)
+            ptx::tma_load_2d(smem + (i * 3 + c) * kPiece, &tm_q, (L.x.head0 + it.head) * 192 + c * 64,
+                             it.c.b + it.tok0 + i * 128, &bars[kQFull], first);
+        auto keys = [&](int t) {
+          for (int k = 0; k < kKeys; ++k, ++uc) {
+            unsigned char* dst = piece();
+            if (!dst) return;
+            uint64_t* bar = &bars[kFull + uc % kSlots];
+            if (k == kKeys - 1) ptx::tma_load_2d(dst, &tm_rope, 0, row0 + t * 128, bar, normal);
+            else ptx::tma_load_2d(dst, k < 2 ? &tm_k : &tm_k2, (k & 1) * 64, at0 + t * 128, bar, normal);
+          }
+        };
+        keys(it.t0);
+        for (int t = 0; t < n && !aborted; ++t) {
+          for (int k = 0; k < kValues; ++k, ++uc) {
+            unsigned char* dst = piece();
+            if (!dst) return;
+            uint64_t* bar = &bars[kFull + uc % kSlots];
+            const CUtensorMap* map = k < 2 ? &tm_v : &tm_v2;
+            const int y = at0 + (it.t0 + t) * 128 + (k & 1) * 64;
+            ptx::tma_load_2d(dst, map, 0, y, bar, normal);
+            ptx::tma_load_2d(dst + kPiece / 2, map, 64, y, bar, normal);
+          }
+          if (t + 1 < n) keys(it.t0 + t + 1);
+        }
+      });
+    aborted = __any_sync(0xffffffffu, aborted);
+  } else if (warp >= 9) {
+    // ============================ products ============================
+    // A warp for each tile, so that one's waits pass while the other's products
+    // run.  The whole warp runs this and descriptors stay in uniform registers;
+    // one elected lane issues.
+    const int i = warp - 9;
+    const bool leader = elect_one();
+    constexpr uint32_t kIdS = ptx::idesc_bf16_f32(128, 128, 0, 0), kIdO = ptx::idesc_bf16_f32(128, 128, 0, 1);
+    const uint64_t desc_q = ptx::smem_desc(smem + i * 3 * kPiece, 16, 1024, ptx::kLayoutSw128);
+    const uint64_t desc_k = ptx::smem_desc(ring, 16, 1024, ptx::kLayoutSw128);
+    const uint64_t desc_v = ptx::smem_desc(ring, kPiece / 2, 1024, ptx::kLayoutSw128);
+    const uint32_t s_at = tmem + i * 128, o_at = tmem + kColO + i * 128;
+    uint32_t ic = 0, uc = 0, pc = 0, oc = 0;  // items; pieces; steps and items of the tile
+    uint32_t turns = 0;
+    walk.each([&](const Item& it) {
+      const int n = max(it.n0, it.n1), mine = it.steps_of(i);
+      for (int t = -1; t < n; ++t) {
+        // P V of step t (none before the first), Q K^T of step t + 1
+        const bool do_pv = t >= 0 && t < mine, next = t + 1 < n, do_qk = t + 1 < mine;
+        uint64_t* bar = nullptr;
+        uint32_t parity = 0;
+        if (lane == 0 && do_pv) bar = &bars[kPFull + i], parity = pc & 1u;
+        if (lane == 1 && t == 0 && do_pv) bar = &bars[kOFree + i], parity = (oc & 1u) ^ 1u;
+        if (lane == 2 && t == -1) bar = &bars[kQFull], parity = ic & 1u;
+        if (bar) wait(bar, parity, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        // the tiles' turns: whole steps alternate, so that the tiles' softmaxes
+        // and products do too (a warp that gave up goes on taking turns).  Not
+        // where a step has more pieces than the ring: the tile ahead would wait
+        // for pieces that the other has to free first.
+        if (!HI) {
+          if (i) ptx::bar_sync(1, 64);
+          else if (turns++) ptx::bar_sync(2, 64);
+        }
+        ptx::tc_fence_after();
+        if (t >= 0) {
+#pragma unroll
+          for (int k = 0; k < kValues; ++k, ++uc) {
+            const uint32_t slot = uc % kSlots;
+            wait(&bars[kFull + slot], (uc / kSlots) & 1u, aborted);
+            aborted = __any_sync(0xffffffffu, aborted);
+            if (aborted) continue;
+            if (leader) {
+              if (do_pv) {
+                const uint64_t dv = desc_v + slot * (kPiece >> 4);
+#pragma unroll
+                for (int h = 0; h < (HI && k < 2 ? 2 : 1); ++h)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)  // 16 keys each
+                    umma_ts(o_at, s_at + h * 64 + (k & 1) * 32 + j * 8, dv + j * (2048 >> 4), kIdO, k + h + j > 0 || t > 0);
+                ptx::umma_commit(&bars[kFree + slot]);
+              } else {
+                ptx::mbar_arrive(&bars[kFree + slot]);  // a step of the other tile alone
+              }
+            }
+            __syncwarp();
+          }
+          if (do_pv && !aborted) {
+            if (leader) ptx::umma_commit(&bars[kODone + i]);
+            ++pc;
+            oc += t == 0;
+          }
+        }
+        if (next) {
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k, ++uc) {
+            const uint32_t slot = uc % kSlots;
+            wait(&bars[kFull + slot], (uc / kSlots) & 1u, aborted);
+            aborted = __any_sync(0xffffffffu, aborted);
+            if (aborted) continue;
+            if (leader) {
+              if (do_qk) {
+                const uint64_t dk = desc_k + slot * (kPiece >> 4);
+                const uint64_t dq = desc_q + (k == kKeys - 1 ? 2 : k & 1) * (kPiece >> 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ptx::umma_bf16(s_at, dq + j * 2, dk + j * 2, kIdS, k + j > 0);
+                ptx::umma_commit(&bars[kFree + slot]);
+              } else {
+                ptx::mbar_arrive(&bars[kFree + slot]);
+              }
+            }
+            __syncwarp();
+          }
+          if (leader && !aborted) {
+            if (do_qk) ptx::umma_commit(&bars[kSFull + i]);
+            if (t + 2 == n) ptx::umma_commit(&bars[kQFree]);  // the last Q K^T is issued
+          }
+        }
+        __syncwarp();
+        if (!HI) asm volatile("bar.arrive %0, 64;" ::"r"(i ? 2 : 1) : "memory");
+      }
+      ++ic;
+    });
+    if (!HI && i == 0 && turns) ptx::bar_sync(2, 64);
+    // nothing may be in flight when tensor memory is freed
+    if (leader) {
+      ptx::umma_commit(&bars[kDrain]);
+      bool late = false;
+      wait(&bars[kDrain], 0, late);
+      if (late) aborted = true;
+    }
+    aborted = __any_sync(0xffffffffu, aborted);
+  } else {
+    // ============ softmax and output: one query row per thread ============
+    const int i = warp >> 2;  // tile
+    const int r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + kColO + i * 128;
+    const int trow = i * 128 + r;
+    uint32_t sc = 0;  // steps of the tile
+    const float f = fmaxf(p.scale_log2, 1.2e-38f);  // not zero: a masked -inf times it stays -inf
+    walk.each([&](const Item& it) {  // a warp that gave up still meets the others below
+      const int64_t row = static_cast<int64_t>(it.c.b + it.tok0 + trow) * p.num_heads + L.x.head0 + it.head;
+      const bool valid = trow < it.ntok;
+      const int steps = it.steps_of(i);
+      // keys that this row sees (one that is nobody's: as the last, so that it needs no mask of its own)
+      const int limit = valid ? it.pos0 + trow + 1 : it.kend();
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int t = 0; t < steps && !aborted; ++t, ++sc) {
+        wait(&bars[kSFull + i], sc & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        ptx::tc_fence_after();
+        const int nvis = limit - (it.t0 + t) * 128;
+        const bool all = __all_sync(0xffffffffu, nvis >= 128);
+        // The probabilities are formed on the reference as it is; a row whose
+        // maximum turns out to pass it by more than 2^8 raises it, and the step
+        // is formed again (its scores are still there).  The first step starts
+        // from its own maximum.
+        if (t == 0) {
+          const float mx = (all ? row_max<false>(s_at, nvis) : row_max<true>(s_at, nvis)) * f;
+          if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
+        }
+        uint32_t hi[64], lo[HI ? 64 : 1];
+        float top, sum;
+        auto form = [&]() {
+          const float bias = m == -CUDART_INF_F ? 0.f : -m;
+          if (all) probabilities<false, HI>(s_at, nvis, f, bias, hi, lo, top, sum);
+          else probabilities<true, HI>(s_at, nvis, f, bias, hi, lo, top, sum);
+        };
+        form();
+        const bool raise = top * f > m + kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? fp4::fast_exp2(m - top * f) : 1.f;
+          if (raise) m = top * f;
+          l *= alpha;
+          if (t > 0) {  // O, once P V of the step before is in it
+            wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
+            aborted = __any_sync(0xffffffffu, aborted);
+            if (aborted) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              ptx::TmemLd<32>::run(o_at + c * 32, v);
+              wait_ld32(v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+              ptx::tmem_st32(o_at + c * 32, v);
+            }
+          }
+          form();
+        }
+        l += sum;
+        ptx::tmem_st32(s_at, *reinterpret_cast<uint32_t(*)[32]>(hi));
+        ptx::tmem_st32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(hi + 32));
+        if (HI) {
+          ptx::tmem_st32(s_at + 64, *reinterpret_cast<uint32_t(*)[32]>(lo));
+          ptx::tmem_st32(s_at + 96, *reinterpret_cast<uint32_t(*)[32]>(lo + (HI ? 32 : 0)));
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kPFull + i]);
+      }
+      // a part's place
+      auto part_of = [&](int64_t c) { return (c * 2 + (cta_begin(c) >= it.start ? 0 : 1)) * kPair; };
+      float* const ml = L.x.parts;
+      float* const po = L.x.parts + static_cast<int64_t>(gridDim.x) * 2 * kPair * 2;
+      const int64_t prow = part_of(blockIdx.x) + trow;
+      if (steps > 0 && !aborted) {
+        wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+      }
+      if (steps > 0 && !aborted) {
+        ptx::tc_fence_after();
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[2][16];
+          ptx::TmemLd<16>::run(o_at + c, v[0]);
+          ptx::TmemLd<16>::run(o_at + c + 16, v[1]);
+          wait_ld16(v[0]);
+          wait_ld16(v[1]);
+          if (c == 96) {  // O is read: the next item's P V may write it
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars[kOFree + i]);
+          }
+          if (!valid) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (it.whole) {
+              store_out(p, row * 128 + c + h * 16, v[h], inv);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(po + prow * 128 + c + h * 16);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                dst[q] = make_float4(__uint_as_float(v[h][4 * q]), __uint_as_float(v[h][4 * q + 1]),
+                                     __uint_as_float(v[h][4 * q + 2]), __uint_as_float(v[h][4 * q + 3]));
+            }
+          }
+        }
+      }
+      if (it.whole) return;
+      // the last CTA of the item adds its parts up
+      if (valid && !aborted) *reinterpret_cast<float2*>(ml + prow * 2) = make_float2(m, l);
+      auto cta_of = [&](int64_t u) {
+        const int64_t wide = extra * (share + 1);
+        return u < wide ? u / (share + 1) : extra + (u - wide) / share;
+      };
+      const int64_t c0 = cta_of(it.start + kLead), c1 = cta_of(it.end - 1);
+      __threadfence();
+      ptx::bar_sync(3, 256);
+      if (tid == 0) {
+        int32_t* counter = L.x.counters + c0;
+        const int before = atomicAdd(counter, 1);
+        *last_flag = before == c1 - c0;
+        if (before == c1 - c0) *counter = 0;
+        __threadfence();
+      }
+      ptx::bar_sync(3, 256);
+      if (*last_flag) {
+        // 16 outputs a thread, eight threads a row: a warp reads whole rows
+        for (int k = tid; k < it.ntok * 8; k += 256) {
+          const int pr = k >> 3, d = (k & 7) * 16;
+          float M = -CUDART_INF_F;
+#pragma unroll 4
+          for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(ml + (part_of(c) + pr) * 2));
+          const float ref = M == -CUDART_INF_F ? 0.f : M;
+          float acc[16], sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+#pragma unroll 2
+          for (int64_t c = c0; c <= c1; ++c) {
+            const int64_t at = part_of(c) + pr;
+            const float2 e = __ldcg(reinterpret_cast<const float2*>(ml + at * 2));
+            const float4* src = reinterpret_cast<const float4*>(po + at * 128 + d);
+            float4 y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = __ldcg(src + j);
+            if (e.y == 0.f) continue;  // a part that this row sees nothing of: its O may be anything
+            const float w = fp4::fast_exp2(e.x - ref);
+            sum = fmaf(w, e.y, sum);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[4 * j] = fmaf(w, y[j].x, acc[4 * j]);
+              acc[4 * j + 1] = fmaf(w, y[j].y, acc[4 * j + 1]);
+              acc[4 * j + 2] = fmaf(w, y[j].z, acc[4 * j + 2]);
+              acc[4 * j + 3] = fmaf(w, y[j].w, acc[4 * j + 3]);
+            }
+          }
+          const int64_t orow = static_cast<int64_t>(it.c.b + it.tok0 + pr) * p.num_heads + L.x.head0 + it.head;
+          store_out(p, orow * 128 + d, reinterpret_cast<uint32_t(&)[16]>(acc), sum != 0.f ? 1.f / sum : 0.f);
+        }
+      }
+      ptx::bar_sync(3, 256);  // the flag is free again
+    });
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = row * 128 + i * 32 + lane;
-    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
-    else static_cast<float*>(p.out)[at] = acc[i] * inv;
-  }
+
+  if (aborted) *gave_up = 1;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+  if (tid == 0 && *gave_up && p.status) atomicExch(p.status, kDevErrTimeout);
 }
 
-}  // namespace
+int64_t rows_of(int64_t num_seqs, int64_t total_context) { return (total_context + num_seqs * 127) / 128 * 128; }
+int64_t up(int64_t n) { return (n + 1023) / 1024 * 1024; }
+int64_t parts_bytes(int64_t ctas) { return ctas * 2 * kPair * (128 + 2) * 4; }
 
-namespace {
-int64_t padded_rows(int num_seqs, int64_t total_context) { return (total_context + static_cast<int64_t>(num_seqs) * 127) / 128 * 128; }
-int64_t plan_bytes(int num_seqs) { return (static_cast<int64_t>(num_seqs) * 4 + 255) / 256 * 256; }
-}  // namespace
+}  // namespace latent_prefill_detail
 
 size_t latent_prefill_workspace(int num_seqs, int num_heads, int, int, int head_dim, int64_t total_context) {
-  return static_cast<size_t>(plan_bytes(num_seqs) + padded_rows(num_seqs, total_context) * num_heads * head_dim * 4);
+  using namespace latent_prefill_detail;
+  const int64_t sms = device_sm_count(), rows = rows_of(num_seqs, total_context);
+  // tiles and places before the sequences | counters | parts | position parts | keys | values.  Room for an even number
+  // of heads: fp32 outputs take half of them at a time, in two parts.
+  const int64_t heads = (static_cast<int64_t>(num_heads) + 1) / 2 * 2;
+  if (rows * heads >= (int64_t(1) << 31)) return 0;  // rows are numbered in 32 bits by the tensor loads
+  return static_cast<size_t>(1024 + up((static_cast<int64_t>(num_seqs) + 1) * 12 + 8) + up(sms * 4) + up(parts_bytes(sms)) +
+                             up(rows * 128) + 2 * up(rows * heads * head_dim * 2));
 }
 
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t stream) {
-  int32_t* base = reinterpret_cast<int32_t*>(p.ws);
-  __nv_bfloat16* k = reinterpret_cast<__nv_bfloat16*>(p.ws + plan_bytes(p.num_seqs));
-  __nv_bfloat16* v = k + padded_rows(p.num_seqs, p.total_context) * p.num_heads * 128;
-  cudaError_t e = launch_early(plan_kernel, dim3(1), kPlanThreads, stream, p, base);
+  using namespace latent_prefill_detail;
+  const int64_t sms = device_sm_count();
+  const bool hi = !p.out_bf16;
+  const int all = (p.num_heads + 1) / 2 * 2, pass = hi ? all / 2 : p.num_heads;
+  LatentExpanded x{};
+  x.rows = rows_of(p.num_seqs, p.total_context);
+  x.hi = hi;
+  unsigned char* at = reinterpret_cast<unsigned char*>(up(reinterpret_cast<int64_t>(p.ws)));
+  auto take = [&](int64_t bytes) {
+    unsigned char* r = at;
+    at += up(bytes);
+    return r;
+  };
+  x.place0 = reinterpret_cast<int64_t*>(take((static_cast<int64_t>(p.num_seqs) + 1) * 12 + 8));
+  x.tile0 = reinterpret_cast<int32_t*>(x.place0 + p.num_seqs + 1);
+  x.counters = reinterpret_cast<int32_t*>(take(sms * 4));
+  x.parts = reinterpret_cast<float*>(take(parts_bytes(sms)));
+  x.rope = take(x.rows * 128);
+  x.k[0] = take(x.rows * all * 256);
+  x.v[0] = take(x.rows * all * 256);
+  x.k[1] = x.k[0] + x.rows * pass * 256;
+  x.v[1] = x.v[0] + x.rows * pass * 256;
+  cudaError_t e = launch_latent_plan(p, x, stream);
   if (e != cudaSuccess) return e;
-  e = launch_early(expand_kernel, dim3((p.max_context_len + 7) / 8, p.num_heads, p.num_seqs), 128, stream, p,
-                   static_cast<const int32_t*>(base), k, v);
-  if (e != cudaSuccess) return e;
-  return launch_early(attend_kernel, dim3((p.max_q_len + 3) / 4, p.num_heads, p.num_seqs), 128, stream, p,
-                      static_cast<const int32_t*>(base), static_cast<const __nv_bfloat16*>(k),
-                      static_cast<const __nv_bfloat16*>(v));
+  for (int h = 0; h < p.num_heads; h += pass) {
+    x.head0 = h;
+    x.heads = p.num_heads - h < pass ? p.num_heads - h : pass;
+    if (x.rows > 0 && (e = launch_latent_expand(p, x, stream)) != cudaSuccess) return e;
+    Launch L{};
+    L.p = p;
+    L.x = x;
+    CUtensorMap tq, tr, tk, tk2, tv, tv2;
+    const uint64_t q[2] = {static_cast<uint64_t>(p.num_heads) * 192, static_cast<uint64_t>(p.num_tokens)};
+    const uint64_t q_stride[1] = {static_cast<uint64_t>(p.num_heads) * 384};
+    const uint64_t rows = static_cast<uint64_t>(x.rows > 0 ? x.rows : 128);
+    const uint64_t r[2] = {64, rows}, r_stride[1] = {128};
+    const uint64_t k[2] = {128, rows * x.heads}, k_stride[1] = {256};
+    const uint32_t box[2] = {64, 128}, box_v[2] = {64, 64};
+    if (!encode_bf16_tiles(&tq, 2, p.q, q, q_stride, box, 128) || !encode_bf16_tiles(&tr, 2, x.rope, r, r_stride, box, 128) ||
+        !encode_bf16_tiles(&tk, 2, x.k[0], k, k_stride, box, 128) ||
+        !encode_bf16_tiles(&tk2, 2, x.k[hi], k, k_stride, box, 128) ||
+        !encode_bf16_tiles(&tv, 2, x.v[0], k, k_stride, box_v, 128) ||
+        !encode_bf16_tiles(&tv2, 2, x.v[hi], k, k_stride, box_v, 128))
+      return cudaErrorInvalidValue;
+    const void* fn = hi ? reinterpret_cast<const void*>(&attend_kernel<true>) : reinterpret_cast<const void*>(&attend_kernel<false>);
+    int per_sm = 0;
+    if ((e = fp4_occupancy(fn, kThreads, kSmemBytes, &per_sm)) != cudaSuccess) return e;
+    // every SM, while the items are not cut into too many parts to add up
+    const int64_t items = (static_cast<int64_t>(p.num_tokens) / kPair + p.num_seqs) * x.heads;
+    const int64_t ctas = items * 32 < sms ? items * 32 : sms;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&L, &tq, &tr, &tk, &tk2, &tv, &tv2};
+    if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pa

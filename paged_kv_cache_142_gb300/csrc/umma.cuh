@@ -101,5 +101,15 @@ __device__ __forceinline__ void wait_ld32(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// a box loaded into this place of every CTA in the mask, counted by the barrier at this place of each
+__device__ __forceinline__ void tma_load_2d_cluster(void* dst, const void* map, int x, int y, uint64_t* bar, uint16_t mask,
+                                                    uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(ptx::smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(ptx::smem_addr(bar)), "h"(mask), "l"(policy)
+      : "memory");
+}
+
 }  // namespace um
 }  // namespace pa

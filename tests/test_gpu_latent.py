@@ -105,11 +105,12 @@ def test_decode(ops, H, Q, bs):
     rng = np.random.default_rng(H * 100 + Q + bs)
     lens = [1, 0, 63, 64, 65, 17, 200, 129]
     tables, cache, q = decode_case(rng, lens, bs, H, Q, pad=-1)
-    ref, tol = O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT)
+    exact = O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT, O.TWO)
+    rounded = O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT)
     for fill in (0.0, float("nan"), float("inf")):
         pool = blank_unused(dev16(cache), tables, lens, bs, fill)
-        check(run_decode(ops, q, pool, tables, lens, bs, 0.07), ref, tol, False)
-    check(run_decode(ops, q, pool, tables, lens, bs, 0.07, torch.bfloat16), ref, tol, True)
+        check(run_decode(ops, q, pool, tables, lens, bs, 0.07), *exact, False)
+        check(run_decode(ops, q, pool, tables, lens, bs, 0.07, torch.bfloat16), *rounded, True)
 
 
 @pytest.mark.parametrize("B,H,top,bs", [(1, 16, 9000, 16), (1, 128, 5000, 32), (3, 128, 3000, 16), (90, 16, 400, 16),
@@ -120,8 +121,9 @@ def test_decode_lengths(ops, B, H, top, bs):
     lens = [int(x) for x in rng.integers(0, top, size=B)]
     lens[-1] = top
     tables, cache, q = decode_case(rng, lens, bs, H, 1)
-    ref, tol = O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT)
-    check(run_decode(ops, q, dev16(cache), tables, lens, bs, 0.07), ref, tol, False)
+    for dt, dp in ((torch.float32, O.TWO), (torch.bfloat16, O.BF16)):
+        ref, tol = O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT, dp)
+        check(run_decode(ops, q, dev16(cache), tables, lens, bs, 0.07, dt), ref, tol, dt == torch.bfloat16)
 
 
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30, 2.0])
@@ -201,17 +203,19 @@ def run_prefill(ops, q, pool, w_k, w_v, cu, start, tables, bs, scale, max_q, max
 
 @pytest.mark.parametrize("chunks,H,bs", [
     ([(0, 1)], 1, 16), ([(0, 5), (7, 0), (100, 30)], 3, 16), ([(0, 129), (200, 64)], 2, 8), ([(511, 1), (0, 128), (1, 256)], 4, 32),
-    ([(0, 300)], 5, 256), ([(130, 257), (3, 1), (0, 2)], 2, 64), ([(1000, 17)], 16, 128)])
+    ([(0, 300)], 5, 256), ([(130, 257), (3, 1), (0, 2)], 2, 64), ([(1000, 17)], 16, 128), ([(0, 700), (300, 513)], 6, 16),
+    ([(5, 3)] * 30, 2, 16), ([(5000, 40)], 1, 32)])
 def test_prefill(ops, chunks, H, bs):
     rng = np.random.default_rng(len(chunks) * 10 + H)
     lens, tables, cache, cu, q, w_k, w_v = prefill_case(rng, chunks, bs, H, pad=-1)
     start = [s for s, _ in chunks]
-    ref, tol = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.072)
+    exact = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.072, two=True)
+    rounded = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.072)
     args = (cu, start, tables, bs, 0.072, max(n for _, n in chunks), max(lens), sum(lens))
     for fill in (0.0, float("nan")):
         pool = blank_unused(dev16(cache), tables, lens, bs, fill)
-        check(run_prefill(ops, q, pool, w_k, w_v, *args), ref, tol, False)
-    check(run_prefill(ops, q, pool, w_k, w_v, *args, out_dtype=torch.bfloat16), ref, tol, True)
+        check(run_prefill(ops, q, pool, w_k, w_v, *args), *exact, False)
+        check(run_prefill(ops, q, pool, w_k, w_v, *args, out_dtype=torch.bfloat16), *rounded, True)
 
 
 def test_prefill_reports_what_lies_outside(ops):
@@ -219,7 +223,7 @@ def test_prefill_reports_what_lies_outside(ops):
     chunks, bs = [(20, 40), (0, 30), (64, 64)], 16
     lens, tables, cache, cu, q, w_k, w_v = prefill_case(rng, chunks, bs, 2)
     start = [s for s, _ in chunks]
-    ref, tol = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.072)
+    ref, tol = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.072, two=True)
     pool, total = dev16(cache), sum(lens)
     rest = np.r_[0:40, 70:134]
     # a chunk that starts below zero, ends behind max_context_len, is longer than max_q_len
