@@ -98,16 +98,16 @@ struct Launch {
   int bs_log;
 };
 
-// 16 columns of a token's key or value, in one part or two
-__device__ __forceinline__ void store16(const LatentExpanded& x, unsigned char* const (&dst)[2], int64_t at, const float (&y)[16]) {
+// 16 columns of a token's key or value, and what their rounding left where it is wanted
+__device__ __forceinline__ void store16(unsigned char* dst, unsigned char* rest, int64_t at, const float (&y)[16]) {
   uint32_t h[8], l[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     h[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
     l[e] = pack_bf16(y[2 * e] - __uint_as_float(h[e] << 16), y[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
   }
-  fp4::store32(dst[0] + at * 2, h);
-  if (x.hi) fp4::store32(dst[1] + at * 2, l);
+  fp4::store32(dst + at * 2, h);
+  if (rest) fp4::store32(rest + at * 2, l);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -219,6 +219,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    // The products of both CTAs signal these barriers when they complete, which
+    // no thread's order covers: a CTA stays until the last signals are here (one
+    // that arrives where its CTA has gone is a fault).
+    for (uint32_t k = kb > kStages ? kb - kStages : 0; k < kb; ++k)
+      wait(&bars[kBFree + k % kStages], (k / kStages) & 1u, aborted);
+    aborted = __any_sync(0xffffffffu, aborted);
   } else if (warp == 5) {
     // ============================ products ============================
     const bool leader = elect_one();
@@ -259,6 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ===================== results: a token a thread =====================
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    unsigned char *const k0 = x.k[0], *const v0 = x.v[0];
+    unsigned char *const k1 = x.hi ? x.k[1] : nullptr, *const v1 = x.hi ? x.v[1] : nullptr;
     uint32_t kd = 0;
     Tile t{0, 0, 0};
     for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
@@ -312,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             y[j] = !valid ? 0.f : (from < 128 && odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(v[16 * q + j]));
-          store16(x, from < 128 ? x.k : x.v, at + (from & 127) + 16 * q, y);
+          store16(from < 128 ? k0 : v0, from < 128 ? k1 : v1, at + (from & 127) + 16 * q, y);
         }
       }
       if (odd && valid && there) {  // no value, in place of what was stored
         const float none[16] = {};
-        for (int col = 0; col < 128; col += 16) store16(x, x.v, at + col, none);
+        for (int col = 0; col < 128; col += 16) store16(v0, v1, at + col, none);
       }
     }
   }
