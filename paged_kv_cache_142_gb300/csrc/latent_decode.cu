@@ -452,8 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         aborted = __any_sync(0xffffffffu, aborted);
         ptx::tc_fence_after();
         uint32_t s[32];
-        ptx::TmemLd<32>::run(tmem + lanes + kColS + half * 32, s);
-        wait_ld32(s);
+        load_now(tmem + lanes + kColS + half * 32, s);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars[kSFree]);
@@ -562,8 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
-            ptx::TmemLd<32>::run(tmem + lanes + half * 128 + c * 32, v);
-            wait_ld32(v);
+            load_now(tmem + lanes + half * 128 + c * 32, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
             ptx::tmem_st32(tmem + lanes + half * 128 + c * 32, v);
@@ -596,8 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t v[32];
-        ptx::TmemLd<32>::run(tmem + lanes + quad * 64 + c * 32, v);
-        wait_ld32(v);
+        load_now(tmem + lanes + quad * 64 + c * 32, v);
         if (c == 1) {  // O is read: the next item's P V may write it
           ptx::tc_fence_before();
           __syncwarp();

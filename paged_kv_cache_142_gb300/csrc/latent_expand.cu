@@ -32,8 +32,6 @@ using namespace um;
 // before count in 64 bits, and the counters of the attention start at zero.
 constexpr int kPlanThreads = 512;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LatentPrefillParams p, const LatentExpanded x, int num_counters) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int64_t sums[3][kPlanThreads / 32];
   const int64_t table_tokens = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
@@ -124,7 +122,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
 
-  ptx::griddep_launch_dependents();
   if (tid == 0) {
     ptx::mbar_init(&bars[kAFull], 1);
     ptx::mbar_init(&bars[kAFree], 1);
@@ -146,7 +143,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool aborted = false;
-  ptx::griddep_wait();
   cluster_sync();  // both CTAs' barriers are ready
 
   // units (pair of tiles, head), equal runs of them for the clusters
@@ -213,8 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         aborted = __any_sync(0xffffffffu, aborted);
         if (!aborted && lane == 0) {
           ptx::mbar_arrive_expect_tx(&bars[kBFull + slot], kBBytes);
-          tma_load_2d_cluster(smem + kOffB + slot * kBBytes + rank * 16384, rank ? &tm_wv : &tm_wk, ch * 64, h * 128,
-                              &bars[kBFull + slot], 3, keep);
+          unsigned char* dst = smem + kOffB + slot * kBBytes;
+          if (rank) tma_load_2d_cluster(dst + 16384, &tm_wv, ch * 64, h * 128, &bars[kBFull + slot], 3, keep);
+          else tma_load_2d_cluster(dst, &tm_wk, ch * 64, h * 128, &bars[kBFull + slot], 3, keep);
         }
         __syncwarp();
       }
@@ -302,8 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int col = 0; col < 256; col += 32) {
         const int from = (col + 128) & 255;  // values first
         uint32_t v[32];
-        ptx::TmemLd<32>::run(d + from, v);
-        wait_ld32(v);
+        load_now(d + from, v);
         if (col == 224) {
           ptx::tc_fence_before();
           __syncwarp();
@@ -343,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_latent_plan(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream) {
   using namespace latent_expand_detail;
-  return launch_early(plan_kernel, dim3(1), kPlanThreads, stream, p, x, static_cast<int>(device_sm_count()));
+  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, x, static_cast<int>(device_sm_count()));
+  return cudaGetLastError();
 }
 
 cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream) {
@@ -371,15 +368,13 @@ cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpan
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   void* args[] = {&L, &tm_pool, &tm_wk, &tm_wv};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }

@@ -79,6 +79,29 @@ __device__ __forceinline__ Chunk chunk_of(const Launch& L, int seq) {
   return c;
 }
 
+// The item at a place: its sequence, pair, head and how far behind its first place
+// it lies.  One copy for every kind of warp, its result in registers.
+__device__ __noinline__ int4 item_at(const int64_t* place0, const int32_t* cu_q, const int32_t* q_start, int num_seqs,
+                                     int heads, int64_t u) {
+  int lo = 0, hi = num_seqs - 1;
+  while (lo < hi) {  // the last sequence that starts at or before it
+    const int mid = (lo + hi + 1) >> 1;
+    if (place0[mid] * heads <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const Chunk c{0, cu_q[lo + 1] - cu_q[lo], q_start[lo], 0};
+  int64_t r = u - place0[lo] * heads;
+  int a = 0, b = c.pairs() - 1;
+  while (a < b) {
+    const int mid = (a + b + 1) >> 1;
+    if (heads * c.before(mid) <= r) a = mid;
+    else b = mid - 1;
+  }
+  r -= heads * c.before(a);
+  const int places = kLead + c.tiles(a);
+  return make_int4(lo, a, static_cast<int>(r / places), static_cast<int>(r % places));
+}
+
 // An item and this CTA's part of it.
 struct Item {
   Chunk c;
@@ -110,31 +133,7 @@ struct Walk {
     it.n0 = max(0, min(it.t1, seen0) - it.t0);
     it.n1 = it.ntok > 128 ? max(0, it.t1 - it.t0) : 0;
   }
-  // the item at c_begin; one copy for every kind of warp
-  __device__ __noinline__ void find(Item& it) const {
-    const int heads = L.x.heads;
-    int lo = 0, hi = L.p.num_seqs - 1;
-    while (lo < hi) {  // the last sequence that starts at or before it
-      const int mid = (lo + hi + 1) >> 1;
-      if (L.x.place0[mid] * heads <= c_begin) lo = mid;
-      else hi = mid - 1;
-    }
-    it.seq = lo;
-    it.c = chunk_of(L, lo);
-    int64_t r = c_begin - L.x.place0[lo] * heads;
-    int a = 0, b = it.c.pairs() - 1;
-    while (a < b) {
-      const int mid = (a + b + 1) >> 1;
-      if (heads * it.c.before(mid) <= r) a = mid;
-      else b = mid - 1;
-    }
-    r -= heads * it.c.before(a);
-    const int places = kLead + it.c.tiles(a);
-    it.pair = a;
-    it.head = static_cast<int>(r / places);
-    it.start = c_begin - r % places;
-    derive(it);
-  }
+  __device__ __forceinline__ void find(Item& it) const;
   __device__ __forceinline__ void next(Item& it) const {
     it.start = it.end;
     if (++it.head == L.x.heads) {
@@ -162,36 +161,33 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
+__device__ __forceinline__ void Walk::find(Item& it) const {
+  const int4 x = item_at(L.x.place0, L.p.cu_q, L.p.q_start, L.p.num_seqs, L.x.heads, c_begin);
+  it.seq = x.x, it.pair = x.y, it.head = x.z, it.start = c_begin - x.w;
+  it.c = chunk_of(L, it.seq);
+  derive(it);
 }
 
-// A row's probabilities 2^(s f + bias) of a step's 128 keys as 64 bf16 pairs (HI:
-// and what their rounding left), their sum, and the largest s; MASK: keys from
-// nvis on do not count.  The next 16 scores load while 16 are worked on.
-template <bool MASK, bool HI>
-__device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&hi)[64],
-                                              uint32_t (&lo)[HI ? 64 : 1], float& top, float& sum) {
+// A row's probabilities 2^(s f + bias) of N keys of a step, from its key FROM on, as
+// bf16 pairs (HI: and what their rounding left); their sum, and the largest s.
+// MASK: the step's keys from nvis on do not count.
+template <int FROM, int N, bool MASK, bool HI>
+__device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&hi)[N / 2],
+                                              uint32_t (&lo)[HI ? N / 2 : 1], float& top, float& sum) {
   const uint64_t ff = fp4::pair(f, f), bb = fp4::pair(bias, bias);
   uint64_t s0 = 0, s1 = 0;
   float m0 = -CUDART_INF_F, m1 = m0;
-  uint32_t v[2][16];
-  ptx::TmemLd<16>::run(s_at, v[0]);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    wait_ld16(v[c & 1]);
-    if (c < 7) ptx::TmemLd<16>::run(s_at + (c + 1) * 16, v[(c + 1) & 1]);
+  for (int c = 0; c < N; c += 16) {
+    uint32_t v[16];
+    load_now(s_at + FROM + c, v);
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[e] = __uint_as_float(v[c & 1][j + e]);
-        if (MASK && c * 16 + j + e >= nvis) x[e] = -CUDART_INF_F;
+        x[e] = __uint_as_float(v[j + e]);
+        if (MASK && FROM + c + j + e >= nvis) x[e] = -CUDART_INF_F;
       }
       m0 = max3(m0, x[0], x[1]);
       m1 = max3(m1, x[2], x[3]);
@@ -200,7 +196,7 @@ __device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, 
       const float e0 = fp4::fast_exp2(a.x), e1 = fp4::fast_exp2(a.y), e2 = fp4::fast_exp2(b.x), e3 = fp4::fast_exp2(b.y);
       s0 = fp4::add2(s0, fp4::pair(e0, e1));
       s1 = fp4::add2(s1, fp4::pair(e2, e3));
-      const int at = (c * 16 + j) / 2;
+      const int at = (c + j) / 2;
       hi[at] = pack_bf16(e0, e1);
       hi[at + 1] = pack_bf16(e2, e3);
       if (HI) {
@@ -220,8 +216,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, int nvis) {
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
     uint32_t v[32];
-    ptx::TmemLd<32>::run(s_at + c, v);
-    wait_ld32(v);
+    load_now(s_at + c, v);
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       float x[4];
@@ -269,7 +264,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* last_flag = gave_up + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  ptx::griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(&bars[kFull + i], 1);
@@ -295,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool aborted = false;
-  ptx::griddep_wait();
 
   const int64_t total = L.x.place0[p.num_seqs] * L.x.heads;
   const int64_t share = total / gridDim.x, extra = total - share * gridDim.x;
@@ -334,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!dst) return;
             uint64_t* bar = &bars[kFull + uc % kSlots];
             if (k == kKeys - 1) ptx::tma_load_2d(dst, &tm_rope, 0, row0 + t * 128, bar, normal);
-            else ptx::tma_load_2d(dst, k < 2 ? &tm_k : &tm_k2, (k & 1) * 64, at0 + t * 128, bar, normal);
+            else if (k < 2) ptx::tma_load_2d(dst, &tm_k, (k & 1) * 64, at0 + t * 128, bar, normal);
+            else ptx::tma_load_2d(dst, &tm_k2, (k & 1) * 64, at0 + t * 128, bar, normal);
           }
         };
         keys(it.t0);
@@ -343,10 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* dst = piece();
             if (!dst) return;
             uint64_t* bar = &bars[kFull + uc % kSlots];
-            const CUtensorMap* map = k < 2 ? &tm_v : &tm_v2;
             const int y = at0 + (it.t0 + t) * 128 + (k & 1) * 64;
-            ptx::tma_load_2d(dst, map, 0, y, bar, normal);
-            ptx::tma_load_2d(dst + kPiece / 2, map, 64, y, bar, normal);
+            for (int h = 0; h < 2; ++h) {
+              if (k < 2) ptx::tma_load_2d(dst + h * kPiece / 2, &tm_v, h * 64, y, bar, normal);
+              else ptx::tma_load_2d(dst + h * kPiece / 2, &tm_v2, h * 64, y, bar, normal);
+            }
           }
           if (t + 1 < n) keys(it.t0 + t + 1);
         }
@@ -477,51 +472,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const int nvis = limit - (it.t0 + t) * 128;
         const bool all = __all_sync(0xffffffffu, nvis >= 128);
-        // The probabilities are formed on the reference as it is; a row whose
-        // maximum turns out to pass it by more than 2^8 raises it, and the step
-        // is formed again (its scores are still there).  The first step starts
-        // from its own maximum.
-        if (t == 0) {
-          const float mx = (all ? row_max<false>(s_at, nvis) : row_max<true>(s_at, nvis)) * f;
-          if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
-        }
-        uint32_t hi[64], lo[HI ? 64 : 1];
-        float top, sum;
-        auto form = [&]() {
-          const float bias = m == -CUDART_INF_F ? 0.f : -m;
-          if (all) probabilities<false, HI>(s_at, nvis, f, bias, hi, lo, top, sum);
-          else probabilities<true, HI>(s_at, nvis, f, bias, hi, lo, top, sum);
-        };
-        form();
-        const bool raise = top * f > m + kSlack;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float alpha = raise ? fp4::fast_exp2(m - top * f) : 1.f;
-          if (raise) m = top * f;
+        // a row's new reference, for its sum and for its O once P V of the step before is in it
+        auto raise_to = [&](bool raise, float now) {
+          const float alpha = raise ? fp4::fast_exp2(m - now) : 1.f;
+          if (raise) m = now;
           l *= alpha;
-          if (t > 0) {  // O, once P V of the step before is in it
-            wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
-            aborted = __any_sync(0xffffffffu, aborted);
-            if (aborted) break;
-            ptx::tc_fence_after();
+          if (t == 0) return;
+          wait(&bars[kODone + i], (sc - 1) & 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) return;
+          ptx::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              ptx::TmemLd<32>::run(o_at + c * 32, v);
-              wait_ld32(v);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            load_now(o_at + c * 32, v);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
-              ptx::tmem_st32(o_at + c * 32, v);
-            }
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+            ptx::tmem_st32(o_at + c * 32, v);
           }
+        };
+        float top, sum;
+        if (HI || t == 0) {
+          const float mx = (all ? row_max<false>(s_at, nvis) : row_max<true>(s_at, nvis)) * f;
+          if (t == 0) {
+            if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
+          } else {
+            const bool raise = mx > m + kSlack;
+            if (__any_sync(0xffffffffu, raise)) raise_to(raise, mx);
+          }
+        }
+        const auto bias = [&]() { return m == -CUDART_INF_F ? 0.f : -m; };
+        if constexpr (HI) {
+          // in halves, each written as soon as its scores are read: both parts of
+          // all 128 at once do not fit the registers
+          uint32_t hi[32], lo[32], hi2[32], lo2[32];
+          float sum2;
+          if (all) probabilities<0, 64, false, true>(s_at, nvis, f, bias(), hi, lo, top, sum);
+          else probabilities<0, 64, true, true>(s_at, nvis, f, bias(), hi, lo, top, sum);
+          ptx::tmem_st32(s_at, hi);
+          if (all) probabilities<64, 64, false, true>(s_at, nvis, f, bias(), hi2, lo2, top, sum2);
+          else probabilities<64, 64, true, true>(s_at, nvis, f, bias(), hi2, lo2, top, sum2);
+          sum += sum2;
+          ptx::tmem_st32(s_at + 32, hi2);
+          ptx::tmem_st32(s_at + 64, lo);
+          ptx::tmem_st32(s_at + 96, lo2);
+        } else {
+          // The probabilities are formed on the reference as it is; a row whose
+          // maximum turns out to pass it by more than 2^8 raises it, and the step
+          // is formed again (its scores are still there).  The first step starts
+          // from its own maximum.
+          uint32_t hi[64], none[1];
+          auto form = [&]() {
+            if (all) probabilities<0, 128, false, false>(s_at, nvis, f, bias(), hi, none, top, sum);
+            else probabilities<0, 128, true, false>(s_at, nvis, f, bias(), hi, none, top, sum);
+          };
           form();
+          const bool raise = top * f > m + kSlack;
+          if (__any_sync(0xffffffffu, raise)) {
+            raise_to(raise, top * f);
+            form();
+          }
+          ptx::tmem_st32(s_at, *reinterpret_cast<uint32_t(*)[32]>(hi));
+          ptx::tmem_st32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(hi + 32));
         }
+        if (aborted) break;
         l += sum;
-        ptx::tmem_st32(s_at, *reinterpret_cast<uint32_t(*)[32]>(hi));
-        ptx::tmem_st32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(hi + 32));
-        if (HI) {
-          ptx::tmem_st32(s_at + 64, *reinterpret_cast<uint32_t(*)[32]>(lo));
-          ptx::tmem_st32(s_at + 96, *reinterpret_cast<uint32_t(*)[32]>(lo + (HI ? 32 : 0)));
-        }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -542,19 +557,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           uint32_t v[2][16];
-          ptx::TmemLd<16>::run(o_at + c, v[0]);
-          ptx::TmemLd<16>::run(o_at + c + 16, v[1]);
-          wait_ld16(v[0]);
-          wait_ld16(v[1]);
+          load_now(o_at + c, v[0]);
+          load_now(o_at + c + 16, v[1]);
           if (c == 96) {  // O is read: the next item's P V may write it
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars[kOFree + i]);
           }
-          if (!valid) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (it.whole) {
+            if (!valid) {
+            } else if (it.whole) {
               store_out(p, row * 128 + c + h * 16, v[h], inv);
             } else {
               float4* dst = reinterpret_cast<float4*>(po + prow * 128 + c + h * 16);
@@ -564,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      __uint_as_float(v[h][4 * q + 2]), __uint_as_float(v[h][4 * q + 3]));
             }
           }
+          __syncwarp();  // the next load is the whole warp's
         }
       }
       if (it.whole) return;
@@ -703,11 +717,6 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t str
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     void* args[] = {&L, &tq, &tr, &tk, &tk2, &tv, &tv2};
     if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess) return e;
   }
