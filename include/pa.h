@@ -606,8 +606,8 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
  * values of every head are formed from the cached rows (c, r) of the sequence,
  *   k[h][t] = (w_k[h] c_t, r_t)     v[h][t] = w_v[h] c_t
  * and the chunk's queries attend to them.  bf16 outputs: keys, values and
- * probabilities are rounded to bf16; fp32 outputs: they are held in two bf16
- * parts each (2^-16 of the value).
+ * probabilities are rounded to bf16, on the tensor cores; fp32 outputs: they stay
+ * in fp32, on the CUDA cores (about 30 times as slow).
  * Chunk i is q[cu_q[i] .. cu_q[i+1]) at positions q_start[i] + 0, 1, ..., whose
  * rows are in the cache already; query j sees the positions up to its own.
  *   q          device, bf16 [num_tokens][num_heads][head_dim + rope_dim], 16-byte aligned

@@ -52,11 +52,11 @@ struct LatentExpanded {
   int32_t* counters;     // [CTAs], zeroed by every call
   float* parts;          // maxima, sums and rows that CTAs leave for one another
   unsigned char* rope;   // [rows][64] bf16
-  unsigned char* k[2];   // [heads][rows][128] bf16; [1]: what the rounding of [0] left (fp32 outputs)
-  unsigned char* v[2];
+  unsigned char* k;      // [heads][rows][128]
+  unsigned char* v;
   int64_t rows;          // of a head: whole tiles
   int32_t head0, heads;  // of this pass
-  bool hi;               // keys and values in two parts
+  bool f32;              // keys and values in fp32 (fp32 outputs), else bf16
 };
 
 // How the expanded attention's work is counted: an item is a pair of 128-token
@@ -113,6 +113,7 @@ size_t latent_prefill_workspace(int num_seqs, int num_heads, int latent_dim, int
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t stream);
 cudaError_t launch_latent_plan(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);
 cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);
+cudaError_t launch_latent_attend_f32(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);
 size_t weights_workspace(int num_seqs, int window, int num_q_heads, int num_kv_heads, int head_dim,
                          int max_context_len);
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream);

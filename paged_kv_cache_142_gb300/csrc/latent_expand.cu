@@ -1,8 +1,7 @@
 // Keys and values of every head from the latent rows:
 //   K[h][t] = w_k[h] c_t,   V[h][t] = w_v[h] c_t,   D[128 x 256] = C[128 x 512] W[h]^T
 // for 128-token tiles of the contexts, and the position parts of the rows packed
-// beside them.  Rounded to bf16; where the outputs are fp32, to two bf16 parts
-// (2^-17 together).  Rows behind a context are zeros.  A token whose value is
+// beside them.  Rounded to bf16, or left in fp32 where the outputs are.  Rows behind a context are zeros.  A token whose value is
 // not finite gets a value of zero and a key of NaN: whoever sees it puts out NaN,
 // and 0 * NaN does not reach the rows that do not.
 //
@@ -96,16 +95,21 @@ struct Launch {
   int bs_log;
 };
 
-// 16 columns of a token's key or value, and what their rounding left where it is wanted
-__device__ __forceinline__ void store16(unsigned char* dst, unsigned char* rest, int64_t at, const float (&y)[16]) {
-  uint32_t h[8], l[8];
+// 16 columns of a token's key or value, `at` elements into dst
+__device__ __forceinline__ void store16(unsigned char* dst, bool f32, int64_t at, const float (&y)[16]) {
+  uint32_t h[8];
+  if (!f32) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    h[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-    l[e] = pack_bf16(y[2 * e] - __uint_as_float(h[e] << 16), y[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
+    for (int e = 0; e < 8; ++e) h[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+    fp4::store32(dst + at * 2, h);
+    return;
   }
-  fp4::store32(dst + at * 2, h);
-  if (rest) fp4::store32(rest + at * 2, l);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(y[8 * q + e]);
+    fp4::store32(dst + at * 4 + 32 * q, h);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -262,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ===================== results: a token a thread =====================
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-    unsigned char *const k0 = x.k[0], *const v0 = x.v[0];
-    unsigned char *const k1 = x.hi ? x.k[1] : nullptr, *const v1 = x.hi ? x.v[1] : nullptr;
+    unsigned char *const k = x.k, *const v0 = x.v;
+    const bool f32 = x.f32;
     uint32_t kd = 0;
     Tile t{0, 0, 0};
     for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
@@ -316,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             y[j] = !valid ? 0.f : (from < 128 && odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(v[16 * q + j]));
-          store16(from < 128 ? k0 : v0, from < 128 ? k1 : v1, at + (from & 127) + 16 * q, y);
+          store16(from < 128 ? k : v0, f32, at + (from & 127) + 16 * q, y);
         }
       }
       if (odd && valid && there) {  // no value, in place of what was stored
         const float none[16] = {};
-        for (int col = 0; col < 128; col += 16) store16(v0, v1, at + col, none);
+        for (int col = 0; col < 128; col += 16) store16(v0, f32, at + col, none);
       }
     }
   }

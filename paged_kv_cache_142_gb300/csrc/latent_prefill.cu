@@ -8,8 +8,8 @@
 // queries.  A row is one token of one head; a CTA takes two tiles of 128 tokens,
 // so that every key and value loaded serves 256 rows.  Accumulators are fp32 in
 // tensor memory: S of both tiles, O of both.  P is written over its S and read
-// from there as the A operand; bf16 outputs take it in bf16 (2^-8, as the output),
-// fp32 outputs take P, keys and values in two bf16 parts (2^-17 together).
+// from there as the A operand, in bf16 (2^-8, as the output).  fp32 outputs need
+// more than that and have a kernel of their own (latent_prefill_f32.cu).
 //
 // Queries take 96 KB of shared memory; the rest is a ring of eight 16 KB pieces (64
 // dims of a step's keys; 64 of its values' tokens), each freed as both tiles have
@@ -168,26 +168,25 @@ __device__ __forceinline__ void Walk::find(Item& it) const {
   derive(it);
 }
 
-// A row's probabilities 2^(s f + bias) of N keys of a step, from its key FROM on, as
-// bf16 pairs (HI: and what their rounding left); their sum, and the largest s.
-// MASK: the step's keys from nvis on do not count.
-template <int FROM, int N, bool MASK, bool HI>
-__device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&hi)[N / 2],
-                                              uint32_t (&lo)[HI ? N / 2 : 1], float& top, float& sum) {
+// A row's probabilities 2^(s f + bias) of a step's 128 keys as 64 bf16 pairs, their
+// sum, and the largest s; MASK: keys from nvis on do not count.
+template <bool MASK>
+__device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, float bias, uint32_t (&pk)[64], float& top,
+                                              float& sum) {
   const uint64_t ff = fp4::pair(f, f), bb = fp4::pair(bias, bias);
   uint64_t s0 = 0, s1 = 0;
   float m0 = -CUDART_INF_F, m1 = m0;
 #pragma unroll
-  for (int c = 0; c < N; c += 16) {
+  for (int c = 0; c < 128; c += 16) {
     uint32_t v[16];
-    load_now(s_at + FROM + c, v);
+    load_now(s_at + c, v);
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         x[e] = __uint_as_float(v[j + e]);
-        if (MASK && FROM + c + j + e >= nvis) x[e] = -CUDART_INF_F;
+        if (MASK && c + j + e >= nvis) x[e] = -CUDART_INF_F;
       }
       m0 = max3(m0, x[0], x[1]);
       m1 = max3(m1, x[2], x[3]);
@@ -196,13 +195,8 @@ __device__ __forceinline__ void probabilities(uint32_t s_at, int nvis, float f, 
       const float e0 = fp4::fast_exp2(a.x), e1 = fp4::fast_exp2(a.y), e2 = fp4::fast_exp2(b.x), e3 = fp4::fast_exp2(b.y);
       s0 = fp4::add2(s0, fp4::pair(e0, e1));
       s1 = fp4::add2(s1, fp4::pair(e2, e3));
-      const int at = (c + j) / 2;
-      hi[at] = pack_bf16(e0, e1);
-      hi[at + 1] = pack_bf16(e2, e3);
-      if (HI) {
-        lo[at] = pack_bf16(e0 - __uint_as_float(hi[at] << 16), e1 - __uint_as_float(hi[at] & 0xffff0000u));
-        lo[at + 1] = pack_bf16(e2 - __uint_as_float(hi[at + 1] << 16), e3 - __uint_as_float(hi[at + 1] & 0xffff0000u));
-      }
+      pk[(c + j) / 2] = pack_bf16(e0, e1);
+      pk[(c + j) / 2 + 1] = pack_bf16(e2, e3);
     }
   }
   top = fmaxf(m0, m1);
@@ -246,13 +240,11 @@ __device__ __forceinline__ void store_out(const LatentPrefillParams& p, int64_t 
   }
 }
 
-template <bool HI>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_v2) {
-  constexpr int kKeys = HI ? 5 : 3, kValues = HI ? 4 : 2;  // pieces of a step
+                  const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int kKeys = 3, kValues = 2;  // pieces of a step
   const LatentPrefillParams& p = L.p;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -327,8 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!dst) return;
             uint64_t* bar = &bars[kFull + uc % kSlots];
             if (k == kKeys - 1) ptx::tma_load_2d(dst, &tm_rope, 0, row0 + t * 128, bar, normal);
-            else if (k < 2) ptx::tma_load_2d(dst, &tm_k, (k & 1) * 64, at0 + t * 128, bar, normal);
-            else ptx::tma_load_2d(dst, &tm_k2, (k & 1) * 64, at0 + t * 128, bar, normal);
+            else ptx::tma_load_2d(dst, &tm_k, k * 64, at0 + t * 128, bar, normal);
           }
         };
         keys(it.t0);
@@ -337,11 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* dst = piece();
             if (!dst) return;
             uint64_t* bar = &bars[kFull + uc % kSlots];
-            const int y = at0 + (it.t0 + t) * 128 + (k & 1) * 64;
-            for (int h = 0; h < 2; ++h) {
-              if (k < 2) ptx::tma_load_2d(dst + h * kPiece / 2, &tm_v, h * 64, y, bar, normal);
-              else ptx::tma_load_2d(dst + h * kPiece / 2, &tm_v2, h * 64, y, bar, normal);
-            }
+            const int y = at0 + (it.t0 + t) * 128 + k * 64;
+            for (int h = 0; h < 2; ++h) ptx::tma_load_2d(dst + h * kPiece / 2, &tm_v, h * 64, y, bar, normal);
           }
           if (t + 1 < n) keys(it.t0 + t + 1);
         }
@@ -374,13 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bar) wait(bar, parity, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         // the tiles' turns: whole steps alternate, so that the tiles' softmaxes
-        // and products do too (a warp that gave up goes on taking turns).  Not
-        // where a step has more pieces than the ring: the tile ahead would wait
-        // for pieces that the other has to free first.
-        if (!HI) {
-          if (i) ptx::bar_sync(1, 64);
-          else if (turns++) ptx::bar_sync(2, 64);
-        }
+        // and products do too (a warp that gave up goes on taking turns).  The
+        // ring holds a step's pieces, so that the tile ahead never waits for one
+        // that the other has to free first.
+        if (i) ptx::bar_sync(1, 64);
+        else if (turns++) ptx::bar_sync(2, 64);
         ptx::tc_fence_after();
         if (t >= 0) {
 #pragma unroll
@@ -393,10 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (do_pv) {
                 const uint64_t dv = desc_v + slot * (kPiece >> 4);
 #pragma unroll
-                for (int h = 0; h < (HI && k < 2 ? 2 : 1); ++h)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)  // 16 keys each
-                    umma_ts(o_at, s_at + h * 64 + (k & 1) * 32 + j * 8, dv + j * (2048 >> 4), kIdO, k + h + j > 0 || t > 0);
+                for (int j = 0; j < 4; ++j)  // 16 keys each
+                  umma_ts(o_at, s_at + k * 32 + j * 8, dv + j * (2048 >> 4), kIdO, k + j > 0 || t > 0);
                 ptx::umma_commit(&bars[kFree + slot]);
               } else {
                 ptx::mbar_arrive(&bars[kFree + slot]);  // a step of the other tile alone
@@ -420,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
               if (do_qk) {
                 const uint64_t dk = desc_k + slot * (kPiece >> 4);
-                const uint64_t dq = desc_q + (k == kKeys - 1 ? 2 : k & 1) * (kPiece >> 4);
+                const uint64_t dq = desc_q + k * (kPiece >> 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) ptx::umma_bf16(s_at, dq + j * 2, dk + j * 2, kIdS, k + j > 0);
                 ptx::umma_commit(&bars[kFree + slot]);
@@ -436,11 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (!HI) asm volatile("bar.arrive %0, 64;" ::"r"(i ? 2 : 1) : "memory");
+        asm volatile("bar.arrive %0, 64;" ::"r"(i ? 2 : 1) : "memory");
       }
       ++ic;
     });
-    if (!HI && i == 0 && turns) ptx::bar_sync(2, 64);
+    if (i == 0 && turns) ptx::bar_sync(2, 64);
     // nothing may be in flight when tensor memory is freed
     if (leader) {
       ptx::umma_commit(&bars[kDrain]);
@@ -491,50 +475,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_st32(o_at + c * 32, v);
           }
         };
-        float top, sum;
-        if (HI || t == 0) {
+        // The probabilities are formed on the reference as it is; a row whose
+        // maximum turns out to pass it by more than 2^8 raises it, and the step
+        // is formed again (its scores are still there).  The first step starts
+        // from its own maximum.
+        if (t == 0) {
           const float mx = (all ? row_max<false>(s_at, nvis) : row_max<true>(s_at, nvis)) * f;
-          if (t == 0) {
-            if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
-          } else {
-            const bool raise = mx > m + kSlack;
-            if (__any_sync(0xffffffffu, raise)) raise_to(raise, mx);
-          }
+          if (nvis > 0 && mx > -CUDART_INF_F) m = mx;
         }
-        const auto bias = [&]() { return m == -CUDART_INF_F ? 0.f : -m; };
-        if constexpr (HI) {
-          // in halves, each written as soon as its scores are read: both parts of
-          // all 128 at once do not fit the registers
-          uint32_t hi[32], lo[32], hi2[32], lo2[32];
-          float sum2;
-          if (all) probabilities<0, 64, false, true>(s_at, nvis, f, bias(), hi, lo, top, sum);
-          else probabilities<0, 64, true, true>(s_at, nvis, f, bias(), hi, lo, top, sum);
-          ptx::tmem_st32(s_at, hi);
-          if (all) probabilities<64, 64, false, true>(s_at, nvis, f, bias(), hi2, lo2, top, sum2);
-          else probabilities<64, 64, true, true>(s_at, nvis, f, bias(), hi2, lo2, top, sum2);
-          sum += sum2;
-          ptx::tmem_st32(s_at + 32, hi2);
-          ptx::tmem_st32(s_at + 64, lo);
-          ptx::tmem_st32(s_at + 96, lo2);
-        } else {
-          // The probabilities are formed on the reference as it is; a row whose
-          // maximum turns out to pass it by more than 2^8 raises it, and the step
-          // is formed again (its scores are still there).  The first step starts
-          // from its own maximum.
-          uint32_t hi[64], none[1];
-          auto form = [&]() {
-            if (all) probabilities<0, 128, false, false>(s_at, nvis, f, bias(), hi, none, top, sum);
-            else probabilities<0, 128, true, false>(s_at, nvis, f, bias(), hi, none, top, sum);
-          };
+        uint32_t pk[64];
+        float top, sum;
+        auto form = [&]() {
+          const float bias = m == -CUDART_INF_F ? 0.f : -m;
+          if (all) probabilities<false>(s_at, nvis, f, bias, pk, top, sum);
+          else probabilities<true>(s_at, nvis, f, bias, pk, top, sum);
+        };
+        form();
+        const bool raise = top * f > m + kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+          raise_to(raise, top * f);
           form();
-          const bool raise = top * f > m + kSlack;
-          if (__any_sync(0xffffffffu, raise)) {
-            raise_to(raise, top * f);
-            form();
-          }
-          ptx::tmem_st32(s_at, *reinterpret_cast<uint32_t(*)[32]>(hi));
-          ptx::tmem_st32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(hi + 32));
         }
+        ptx::tmem_st32(s_at, *reinterpret_cast<uint32_t(*)[32]>(pk));
+        ptx::tmem_st32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
         if (aborted) break;
         l += sum;
         ptx::tmem_wait_st();
@@ -654,7 +617,7 @@ size_t latent_prefill_workspace(int num_seqs, int num_heads, int, int, int head_
   using namespace latent_prefill_detail;
   const int64_t sms = device_sm_count(), rows = rows_of(num_seqs, total_context);
   // tiles and places before the sequences | counters | parts | position parts | keys | values.  Room for an even number
-  // of heads: fp32 outputs take half of them at a time, in two parts.
+  // of heads: fp32 outputs take half of them at a time.
   const int64_t heads = (static_cast<int64_t>(num_heads) + 1) / 2 * 2;
   if (rows * heads >= (int64_t(1) << 31)) return 0;  // rows are numbered in 32 bits by the tensor loads
   return static_cast<size_t>(1024 + up((static_cast<int64_t>(num_seqs) + 1) * 12 + 8) + up(sms * 4) + up(parts_bytes(sms)) +
@@ -664,11 +627,10 @@ size_t latent_prefill_workspace(int num_seqs, int num_heads, int, int, int head_
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t stream) {
   using namespace latent_prefill_detail;
   const int64_t sms = device_sm_count();
-  const bool hi = !p.out_bf16;
-  const int all = (p.num_heads + 1) / 2 * 2, pass = hi ? all / 2 : p.num_heads;
+  const int all = (p.num_heads + 1) / 2 * 2, pass = p.out_bf16 ? p.num_heads : all / 2;
   LatentExpanded x{};
   x.rows = rows_of(p.num_seqs, p.total_context);
-  x.hi = hi;
+  x.f32 = !p.out_bf16;
   unsigned char* at = reinterpret_cast<unsigned char*>(up(reinterpret_cast<int64_t>(p.ws)));
   auto take = [&](int64_t bytes) {
     unsigned char* r = at;
@@ -680,47 +642,46 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t str
   x.counters = reinterpret_cast<int32_t*>(take(sms * 4));
   x.parts = reinterpret_cast<float*>(take(parts_bytes(sms)));
   x.rope = take(x.rows * 128);
-  x.k[0] = take(x.rows * all * 256);
-  x.v[0] = take(x.rows * all * 256);
-  x.k[1] = x.k[0] + x.rows * pass * 256;
-  x.v[1] = x.v[0] + x.rows * pass * 256;
+  x.k = take(x.rows * all * 256);
+  x.v = take(x.rows * all * 256);
+  x.heads = pass;
   cudaError_t e = launch_latent_plan(p, x, stream);
-  if (e != cudaSuccess) return e;
-  for (int h = 0; h < p.num_heads; h += pass) {
-    x.head0 = h;
-    x.heads = p.num_heads - h < pass ? p.num_heads - h : pass;
-    if (x.rows > 0 && (e = launch_latent_expand(p, x, stream)) != cudaSuccess) return e;
-    Launch L{};
-    L.p = p;
-    L.x = x;
-    CUtensorMap tq, tr, tk, tk2, tv, tv2;
-    const uint64_t q[2] = {static_cast<uint64_t>(p.num_heads) * 192, static_cast<uint64_t>(p.num_tokens)};
-    const uint64_t q_stride[1] = {static_cast<uint64_t>(p.num_heads) * 384};
-    const uint64_t rows = static_cast<uint64_t>(x.rows > 0 ? x.rows : 128);
-    const uint64_t r[2] = {64, rows}, r_stride[1] = {128};
-    const uint64_t k[2] = {128, rows * x.heads}, k_stride[1] = {256};
-    const uint32_t box[2] = {64, 128}, box_v[2] = {64, 64};
-    if (!encode_bf16_tiles(&tq, 2, p.q, q, q_stride, box, 128) || !encode_bf16_tiles(&tr, 2, x.rope, r, r_stride, box, 128) ||
-        !encode_bf16_tiles(&tk, 2, x.k[0], k, k_stride, box, 128) ||
-        !encode_bf16_tiles(&tk2, 2, x.k[hi], k, k_stride, box, 128) ||
-        !encode_bf16_tiles(&tv, 2, x.v[0], k, k_stride, box_v, 128) ||
-        !encode_bf16_tiles(&tv2, 2, x.v[hi], k, k_stride, box_v, 128))
-      return cudaErrorInvalidValue;
-    const void* fn = hi ? reinterpret_cast<const void*>(&attend_kernel<true>) : reinterpret_cast<const void*>(&attend_kernel<false>);
-    int per_sm = 0;
-    if ((e = fp4_occupancy(fn, kThreads, kSmemBytes, &per_sm)) != cudaSuccess) return e;
-    // every SM, while the items are not cut into too many parts to add up
-    const int64_t items = (static_cast<int64_t>(p.num_tokens) / kPair + p.num_seqs) * x.heads;
-    const int64_t ctas = items * 32 < sms ? items * 32 : sms;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = stream;
-    void* args[] = {&L, &tq, &tr, &tk, &tk2, &tv, &tv2};
-    if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess) return e;
+  if (e != cudaSuccess || x.rows == 0) return e;
+  if (x.f32) {
+    for (int h = 0; h < p.num_heads; h += pass) {
+      x.head0 = h;
+      x.heads = p.num_heads - h < pass ? p.num_heads - h : pass;
+      if ((e = launch_latent_expand(p, x, stream)) != cudaSuccess) return e;
+      if ((e = launch_latent_attend_f32(p, x, stream)) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
   }
-  return cudaSuccess;
+  if ((e = launch_latent_expand(p, x, stream)) != cudaSuccess) return e;
+  Launch L{};
+  L.p = p;
+  L.x = x;
+  CUtensorMap tq, tr, tk, tv;
+  const uint64_t q[2] = {static_cast<uint64_t>(p.num_heads) * 192, static_cast<uint64_t>(p.num_tokens)};
+  const uint64_t q_stride[1] = {static_cast<uint64_t>(p.num_heads) * 384};
+  const uint64_t r[2] = {64, static_cast<uint64_t>(x.rows)}, r_stride[1] = {128};
+  const uint64_t k[2] = {128, static_cast<uint64_t>(x.rows) * x.heads}, k_stride[1] = {256};
+  const uint32_t box[2] = {64, 128}, box_v[2] = {64, 64};
+  if (!encode_bf16_tiles(&tq, 2, p.q, q, q_stride, box, 128) || !encode_bf16_tiles(&tr, 2, x.rope, r, r_stride, box, 128) ||
+      !encode_bf16_tiles(&tk, 2, x.k, k, k_stride, box, 128) || !encode_bf16_tiles(&tv, 2, x.v, k, k_stride, box_v, 128))
+    return cudaErrorInvalidValue;
+  const void* fn = reinterpret_cast<const void*>(&attend_kernel);
+  int per_sm = 0;
+  if ((e = fp4_occupancy(fn, kThreads, kSmemBytes, &per_sm)) != cudaSuccess) return e;
+  // every SM, while the items are not cut into too many parts to add up
+  const int64_t items = (static_cast<int64_t>(p.num_tokens) / kPair + p.num_seqs) * x.heads;
+  const int64_t ctas = items * 32 < sms ? items * 32 : sms;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  void* args[] = {&L, &tq, &tr, &tk, &tv};
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace pa
