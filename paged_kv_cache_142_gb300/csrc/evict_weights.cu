@@ -1,6 +1,22 @@
 // Accumulated attention weights: weights[t] += sum over a window's queries and
-// heads of softmax_t(scale q . k[t]).  First each row's maximum and sum, then
-// each token's probabilities added up.
+// heads of softmax_t(scale q . k[t]).
+//
+// Three steps.  (1) scores: S = Q K^T on the 5th-generation tensor cores, written
+// out in fp32 (log2 domain, -inf where a row does not see a token) with each
+// tile's maximum and sum of exponentials per row.  (2) a row's logarithm of its
+// sum from its tiles'.  (3) a token's 2^(s - lse) added up over the rows in a
+// fixed order, and into its weight.
+//
+// Step 1 reads K once, which is what the whole cannot do without.  Its scores cost 8
+// bytes a row and token, written and read: 32 of a decode step's four rows against
+// 256 of the key, 1024 of a latent row's 128 against 1152.  Forming S a second time
+// instead would read K again.
+//
+// Step 1: a CTA walks an equal run of units (token tile of a sequence, kv head and
+// row tile).  The rows of a tile are the heads of a kv head's group, query after
+// query.  10 warps: 0-3 and 4-7 take the scores of every other unit (a row a
+// thread), 8 loads, 9 issues products.  A page is one TMA box: [8-token group]
+// [chunk of 64 dims][8 rows x 128 bytes] of its kv head.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -8,93 +24,502 @@
 #include "fp4.cuh"
 #include "latent.cuh"
 #include "ptx.cuh"
+#include "umma.cuh"
 
 namespace pa {
-namespace {
+namespace weights_detail {
 
-__device__ __forceinline__ const __nv_bfloat16* key_at(const WeightsParams& p, int seq, int kvh, int t, bool report) {
-  int phys = p.block_tables[static_cast<int64_t>(seq) * p.max_blocks_per_seq + t / p.block_size];
-  if (phys < 0 || phys >= p.num_blocks) {
-    if (report) atomicExch(p.err, kDevErrInvalidArg);
-    phys = 0;
-  }
-  return static_cast<const __nv_bfloat16*>(p.k_cache) +
-         ((static_cast<int64_t>(phys) * p.num_kv_heads + kvh) * p.block_size + t % p.block_size) * p.head_dim;
-}
+using namespace um;
+
+constexpr int kThreads = 10 * 32;
+constexpr int kMaxSeqs = 1024;  // of one launch: their units lie in shared memory
+constexpr int64_t kScoreBytes = int64_t(512) << 20;  // of one launch, where a sequence does not need more
+
+// NC: chunks of 64 dims; tokens of a tile, tiles and query tiles in shared memory
+template <int NC>
+struct Shape {
+  static constexpr int kTokens = NC <= 2 ? 128 : NC <= 4 ? 64 : 32;
+  static constexpr int kStageBytes = kTokens * NC * 128;
+  static constexpr int kStages = NC == 1 ? 8 : NC <= 4 ? 4 : 2;
+  static constexpr int kQBytes = NC * 16384;  // [chunk][128 rows x 128 bytes]
+  static constexpr int kQSlots = NC <= 2 ? 2 : 1;
+  static constexpr int kOffQ = kStages * kStageBytes;
+  static constexpr int kOffBar = kOffQ + kQSlots * kQBytes;
+  static constexpr int kOffPrefix = kOffBar + 256;
+};
+
+enum : int { kFull = 0, kFree = 8, kQFull = 16, kQFree = 18, kSFull = 20, kSFree = 22, kDrain = 24, kNumBars = 25 };
+
+struct Launch {
+  WeightsParams p;
+  int group;        // query heads of a kv head
+  int rows;         // of a kv head: window * group
+  int tile_queries; // queries of a row tile; its rows are tile_queries * group <= 128
+  int row_tiles;
+  int bs_log;
+  int64_t pitch;    // scores of a row
+  int tiles_pitch;  // tiles of a row
+  float* lse;       // [seqs][kv heads * rows]
+  float2* tile_ml;  // [seqs][kv heads * rows][tiles_pitch] maximum (log2), sum
+  float* scores;    // [seqs][kv heads * rows][pitch]
+};
+
 __device__ __forceinline__ int length_of(const WeightsParams& p, int seq) {
-  const int len = p.context_lens[seq];
-  if (len >= 0 && len <= p.max_context_len) return len;
-  atomicExch(p.err, kDevErrInvalidArg);
-  return 0;
+  const int n = p.context_lens[seq];
+  return n > 0 && n <= p.max_context_len ? n : 0;
 }
 
-// a warp: a query row's log2 of its sum of exponentials
-__global__ void __launch_bounds__(128) stats_kernel(const WeightsParams p, float* lse) {
+// A unit: a token tile of (sequence, kv head, row tile).
+struct Unit {
+  int seq, len, tiles;
+  int kvh, rt, tile;
+};
+
+template <int NC>
+struct Walk {
+  const Launch& L;
+  const int* prefix;
+  int u0, u1;
+  __device__ __forceinline__ void open(Unit& x) const {
+    x.len = length_of(L.p, x.seq);
+    x.tiles = (x.len + Shape<NC>::kTokens - 1) / Shape<NC>::kTokens;
+  }
+  __device__ __forceinline__ void find(Unit& x) const {
+    int lo = 0, hi = L.p.num_seqs - 1;
+    while (lo < hi) {  // the last sequence that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    x.seq = lo;
+    open(x);
+    const int r = u0 - prefix[lo], at = r / x.tiles;
+    x.tile = r - at * x.tiles;
+    x.kvh = at / L.row_tiles;
+    x.rt = at - x.kvh * L.row_tiles;
+  }
+  // f(unit, first of its queries here, last of its queries here)
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if (u0 >= u1) return;
+    Unit x;
+    find(x);
+    bool first = true;
+    for (int u = u0; u < u1; ++u) {
+      const bool last = x.tile + 1 == x.tiles;
+      f(x, first, last || u + 1 == u1);
+      first = last;
+      if (!last) {
+        ++x.tile;
+        continue;
+      }
+      x.tile = 0;
+      if (++x.rt < L.row_tiles) continue;
+      x.rt = 0;
+      if (++x.kvh < L.p.num_kv_heads) continue;
+      x.kvh = 0;
+      if (u + 1 == u1) continue;
+      do ++x.seq;
+      while (prefix[x.seq + 1] == u + 1);  // sequences without units
+      open(x);
+    }
+  }
+};
+
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1)
+    scores_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_q) {
+  using S = Shape<NC>;
+  const WeightsParams& p = L.p;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* prefix = reinterpret_cast<int*>(smem + S::kOffPrefix);
+  __shared__ int warp_sums[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  ptx::griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      ptx::mbar_init(&bars[kFull + i], 1);
+      ptx::mbar_init(&bars[kFree + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kQFull + i], 1);
+      ptx::mbar_init(&bars[kQFree + i], 1);
+      ptx::mbar_init(&bars[kSFull + i], 1);
+      ptx::mbar_init(&bars[kSFree + i], 4);
+    }
+    ptx::mbar_init(&bars[kDrain], 1);
+    *gave_up = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(tmem_slot, 256);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool aborted = false;
+  ptx::griddep_wait();
+
+  {  // ---- units before every sequence ----
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int beg = min(p.num_seqs, tid * per), end = min(p.num_seqs, beg + per);
+    int local = 0;
+    for (int s = beg; s < end; ++s) {
+      const int n = length_of(p, s);
+      if (n != p.context_lens[s] && blockIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
+      const int units = (n + S::kTokens - 1) / S::kTokens * p.num_kv_heads * L.row_tiles;
+      prefix[s + 1] = units;
+      local += units;
+    }
+    int x = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int run = x - local;
+    for (int w = 0; w < warp; ++w) run += warp_sums[w];
+    if (tid == 0) prefix[0] = 0;
+    for (int s = beg; s < end; ++s) prefix[s + 1] = run += prefix[s + 1];
+    __syncthreads();
+  }
+  const int total = prefix[p.num_seqs];
+  const int share = total / gridDim.x, extra = total - share * gridDim.x;
+  auto run_begin = [&](int c) { return c * share + min(c, extra); };
+  const Walk<NC> walk{L, prefix, run_begin(blockIdx.x), run_begin(blockIdx.x + 1)};
+
+  if (warp == 8) {
+    // ============================== loads ==============================
+    // lane i: the unit's page i (and i + 32 ..., where blocks are small)
+    const int page_rows = min(S::kTokens, 1 << L.bs_log), pages = S::kTokens / page_rows;  // at most 16
+    const uint64_t policy = L.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+    uint32_t k = 0, qk = 0;
+    walk.each([&](const Unit& x, bool first, bool) {
+      if (aborted) return;
+      if (first) {  // the row tile's queries; rows past them are nobody's
+        const uint32_t slot = qk % S::kQSlots;
+        wait(&bars[kQFree + slot], ((qk / S::kQSlots) & 1u) ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        ++qk;
+        if (lane == 0) {
+          const uint32_t rows = static_cast<uint32_t>(min(L.tile_queries, p.window) * L.group);
+          ptx::mbar_arrive_expect_tx(&bars[kQFull + slot], rows * 128u * NC);
+          for (int c = 0; c < NC; ++c)
+            tma_load_3d(smem + S::kOffQ + slot * S::kQBytes + c * 16384, &tm_q, c * 64, x.kvh * L.group,
+                        x.seq * p.window + x.rt * L.tile_queries, &bars[kQFull + slot], ptx::policy_evict_normal());
+        }
+        __syncwarp();
+      }
+      const int tok = x.tile * S::kTokens + lane * page_rows;
+      int at = -1;  // the page's first row in the pool, in 8-row groups
+      if (lane < pages && tok < x.len) {
+        int phys = __ldg(p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+        if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
+          atomicExch(p.err, kDevErrInvalidArg);
+          phys = 0;
+        }
+        at = static_cast<int>(((static_cast<int64_t>(phys) * p.num_kv_heads + x.kvh) << L.bs_log) / 8) +
+             (tok & ((1 << L.bs_log) - 1)) / 8;
+      }
+      const uint32_t slot = k % S::kStages;
+      wait(&bars[kFree + slot], ((k / S::kStages) & 1u) ^ 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      const uint32_t have = __popc(__ballot_sync(0xffffffffu, at >= 0));
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kFull + slot], have * page_rows * 128u * NC);
+      __syncwarp();
+      if (at >= 0)
+        ptx::tma_load_4d(smem + slot * S::kStageBytes + lane * page_rows * 128 * NC, &tm_k, 0, 0, 0, at,
+                         &bars[kFull + slot], policy);
+      __syncwarp();
+      ++k;
+    });
+  } else if (warp == 9) {
+    // ============================ products ============================
+    const bool leader = elect_one();
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, S::kTokens, 0, 0);
+    const uint64_t desc_k = ptx::smem_desc(smem, 16, 1024 * NC, ptx::kLayoutSw128);
+    const uint64_t desc_q = ptx::smem_desc(smem + S::kOffQ, 16, 1024, ptx::kLayoutSw128);
+    uint32_t k = 0, qk = 0;
+    walk.each([&](const Unit&, bool first, bool last) {
+      if (aborted) return;
+      const uint32_t slot = k % S::kStages, qslot = qk % S::kQSlots;
+      if (first) wait(&bars[kQFull + qslot], (qk / S::kQSlots) & 1u, aborted);
+      wait(&bars[kSFree + (k & 1u)], ((k >> 1) & 1u) ^ 1u, aborted);
+      wait(&bars[kFull + slot], (k / S::kStages) & 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      ptx::tc_fence_after();
+      if (leader) {
+        const uint64_t dk = desc_k + slot * (S::kStageBytes >> 4), dq = desc_q + qslot * (S::kQBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < 4 * NC; ++c)
+          ptx::umma_bf16(tmem + (k & 1u) * 128, dq + (c >> 2) * (16384 >> 4) + (c & 3) * 2,
+                         dk + (c >> 2) * (1024 >> 4) + (c & 3) * 2, kId, c > 0);
+        ptx::umma_commit(&bars[kSFull + (k & 1u)]);
+        ptx::umma_commit(&bars[kFree + slot]);
+        if (last) ptx::umma_commit(&bars[kQFree + qslot]);
+      }
+      __syncwarp();
+      ++k;
+      qk += last;
+    });
+    if (leader) {  // nothing may be in flight when tensor memory is freed
+      ptx::umma_commit(&bars[kDrain]);
+      bool late = false;
+      wait(&bars[kDrain], 0, late);
+      if (late) aborted = true;
+    }
+    aborted = __any_sync(0xffffffffu, aborted);
+  } else {
+    // ==================== scores: one row per thread ====================
+    const uint32_t buffer = warp >> 2;  // the units k = buffer mod 2
+    const int r = tid & 127;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + buffer * 128;
+    uint32_t k = 0;
+    const int64_t all_rows = static_cast<int64_t>(p.num_kv_heads) * L.rows;
+    walk.each([&](const Unit& x, bool, bool) {
+      const uint32_t mine = k++;
+      if (aborted || (mine & 1u) != buffer) return;
+      wait(&bars[kSFull + buffer], (mine >> 1) & 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      ptx::tc_fence_after();
+      const int tile_rows = min(L.tile_queries * L.group, L.rows - x.rt * L.tile_queries * L.group);
+      const int row = x.rt * L.tile_queries * L.group + r;
+      const bool valid = r < tile_rows;
+      if ((warp & 3) * 32 < tile_rows) {
+        const int seen = x.len - p.window + 1 + row / L.group;  // tokens that this row sees
+        const int nvis = seen - x.tile * S::kTokens;
+        const int64_t grow = x.seq * all_rows + static_cast<int64_t>(x.kvh) * L.rows + row;
+        float* dst = L.scores + grow * L.pitch + x.tile * S::kTokens;
+        float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < S::kTokens; c += 32) {
+          uint32_t v[32];
+          load_now(at + c, v);
+          float m0 = -CUDART_INF_F;
+          float y[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            y[j] = c + j < nvis ? __uint_as_float(v[j]) * p.scale_log2 : -CUDART_INF_F;
+            m0 = fmaxf(m0, y[j]);
+          }
+          const float now = fmaxf(top, m0), ref = now == -CUDART_INF_F ? 0.f : now;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) s0 += fp4::fast_exp2(y[j] - ref), s1 += fp4::fast_exp2(y[j + 1] - ref);
+          sum = fmaf(sum, fp4::fast_exp2(top - ref), s0 + s1);
+          top = now;
+          if (valid) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
+              fp4::store32(dst + c + 8 * q, w);
+            }
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+        if (valid) L.tile_ml[grow * L.tiles_pitch + x.tile] = make_float2(top, sum);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars[kSFree + buffer]);
+    });
+  }
+
+  if (aborted) *gave_up = 1;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 9) ptx::tmem_dealloc(tmem, 256);
+  if (tid == 0 && *gave_up) atomicExch(p.err, kDevErrTimeout);
+}
+
+// A warp: a row's log2 of its sum over its tiles (infinity where it sees nothing).
+__global__ void __launch_bounds__(256) lse_kernel(const Launch L, int tokens) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t per_seq = static_cast<int64_t>(p.window) * p.num_q_heads;
-  if (row >= per_seq * p.num_seqs) return;
-  const int seq = static_cast<int>(row / per_seq), r = static_cast<int>(row % per_seq);
-  const int w = r / p.num_q_heads, h = r % p.num_q_heads, kvh = h / (p.num_q_heads / p.num_kv_heads);
-  const int mine = p.head_dim / 32;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row * p.head_dim;
-  float qv[18];
-  for (int i = 0; i < mine; ++i) qv[i] = __bfloat162float(q[i * 32 + lane]) * p.scale_log2;
-  const int limit = length_of(p, seq) - p.window + 1 + w;
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int t = 0; t < limit; ++t) {
-    const __nv_bfloat16* k = key_at(p, seq, kvh, t, lane == 0);
-    float s = 0.f;
-    for (int i = 0; i < mine; ++i) s = fmaf(qv[i], __bfloat162float(k[i * 32 + lane]), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s), ref = mn == -CUDART_INF_F ? 0.f : mn;
-    l = l * exp2f(m - ref) + exp2f(s - ref);
-    m = mn;
+  const int64_t all_rows = static_cast<int64_t>(L.p.num_kv_heads) * L.rows;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  if (row >= all_rows * L.p.num_seqs) return;
+  const int len = length_of(L.p, static_cast<int>(row / all_rows));
+  const int seen = len - L.p.window + 1 + static_cast<int>(row % all_rows) % L.rows / L.group;
+  const int tiles = (len + tokens - 1) / tokens;
+  float m = -CUDART_INF_F, s = 0.f;
+  for (int i = lane; i < tiles; i += 32) {
+    const float2 e = __ldcg(L.tile_ml + row * L.tiles_pitch + i);
+    const float now = fmaxf(m, e.x), ref = now == -CUDART_INF_F ? 0.f : now;
+    s = fmaf(s, fp4::fast_exp2(m - ref), e.y * fp4::fast_exp2(e.x - ref));
+    m = now;
   }
-  if (lane == 0) lse[row] = limit > 0 ? m + log2f(l) : CUDART_INF_F;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float now = fmaxf(m, m2), ref = now == -CUDART_INF_F ? 0.f : now;
+    s = fmaf(s, fp4::fast_exp2(m - ref), s2 * fp4::fast_exp2(m2 - ref));
+    m = now;
+  }
+  if (lane == 0) L.lse[row] = seen > 0 ? m + log2f(s) : CUDART_INF_F;
 }
 
-// a warp: a token, row after row
-__global__ void __launch_bounds__(128) add_kernel(const WeightsParams p, const float* lse) {
+// A CTA: 128 tokens of a sequence; its warps share the rows, four tokens a lane.
+constexpr int kAddWarps = 8;
+__global__ void __launch_bounds__(32 * kAddWarps) add_kernel(const Launch L) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int lane = threadIdx.x & 31, seq = blockIdx.y, t = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int len = length_of(p, seq);
-  if (t >= len) return;
-  const int mine = p.head_dim / 32, group = p.num_q_heads / p.num_kv_heads;
-  float total = 0.f;
-  for (int kvh = 0; kvh < p.num_kv_heads; ++kvh) {
-    const __nv_bfloat16* k = key_at(p, seq, kvh, t, false);
-    float kv[18];
-    for (int i = 0; i < mine; ++i) kv[i] = __bfloat162float(k[i * 32 + lane]) * p.scale_log2;
-    for (int w = max(0, t + p.window - len); w < p.window; ++w)
-      for (int g = 0; g < group; ++g) {
-        const int64_t row = (static_cast<int64_t>(seq) * p.window + w) * p.num_q_heads + kvh * group + g;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row * p.head_dim;
-        float s = 0.f;
-        for (int i = 0; i < mine; ++i) s = fmaf(kv[i], __bfloat162float(q[i * 32 + lane]), s);
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        total += exp2f(s - lse[row]);
-      }
+  const int seq = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int len = length_of(L.p, seq), t0 = blockIdx.x * 128;
+  if (t0 >= len) return;
+  const int rows = L.p.num_kv_heads * L.rows;
+  const float* lse = L.lse + static_cast<int64_t>(seq) * rows;
+  const float* s = L.scores + static_cast<int64_t>(seq) * rows * L.pitch + t0 + lane * 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (t0 + lane * 4 < len) {
+#pragma unroll 8
+    for (int r = warp; r < rows; r += kAddWarps) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(s + r * L.pitch));
+      const float l = __ldcg(lse + r);
+      sum.x += fp4::fast_exp2(x.x - l);
+      sum.y += fp4::fast_exp2(x.y - l);
+      sum.z += fp4::fast_exp2(x.z - l);
+      sum.w += fp4::fast_exp2(x.w - l);
+    }
   }
-  if (lane == 0) p.weights[seq * p.weights_stride + t] += total;
+  __shared__ float4 part[kAddWarps][32];
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (threadIdx.x < 128 && t0 + static_cast<int>(threadIdx.x) < len) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAddWarps; ++w) v += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+    L.p.weights[seq * L.p.weights_stride + t0 + threadIdx.x] += v;
+  }
 }
 
-}  // namespace
+int tokens_of(int head_dim) {
+  return head_dim <= 128 ? 128 : head_dim <= 256 ? 64 : 32;
+}
+int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+// of one sequence: its rows' logarithms, tiles' statistics and scores
+int64_t seq_bytes(int64_t rows, int head_dim, int max_context_len) {
+  const int64_t tiles = up(max_context_len, 128) / tokens_of(head_dim);
+  return rows * (4 + tiles * 8 + up(max_context_len, 128) * 4);
+}
+// sequences of one launch; 0: not even one's units fit an int
+int seqs_of(int num_seqs, int64_t rows, int num_kv_heads, int head_dim, int max_context_len) {
+  const int64_t units = up(max_context_len, 128) / tokens_of(head_dim) * (rows < num_kv_heads ? num_kv_heads : rows);
+  const int64_t fit = units > 0 ? ((int64_t(1) << 31) - 1) / units : kMaxSeqs;
+  if (fit == 0) return 0;
+  int64_t n = kScoreBytes / (seq_bytes(rows, head_dim, max_context_len) + 1);
+  if (n < 1) n = 1;
+  if (n > fit) n = fit;
+  if (n > kMaxSeqs) n = kMaxSeqs;
+  return static_cast<int>(n < num_seqs ? n : num_seqs);
+}
 
-size_t weights_workspace(int num_seqs, int window, int num_q_heads, int, int, int) {
-  return 256 + static_cast<size_t>(num_seqs) * window * num_q_heads * 4;
+template <int NC>
+cudaError_t launch_scores(const Launch& L, const CUtensorMap& tm_k, const CUtensorMap& tm_q, int64_t most_units,
+                          cudaStream_t stream) {
+  using S = Shape<NC>;
+  const int smem = 1024 + S::kOffPrefix + (L.p.num_seqs + 64) / 64 * 256;
+  const void* fn = reinterpret_cast<const void*>(&scores_kernel<NC>);
+  int per_sm = 0;
+  const cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t sms = device_sm_count();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(most_units < 1 ? 1 : (most_units < sms ? most_units : sms)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<Launch*>(&L), const_cast<CUtensorMap*>(&tm_k), const_cast<CUtensorMap*>(&tm_q)};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace weights_detail
+
+size_t weights_workspace(int num_seqs, int window, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len) {
+  using namespace weights_detail;
+  const int64_t rows = static_cast<int64_t>(window) * num_q_heads;
+  if (num_seqs == 0) return 256;
+  const int seqs = seqs_of(num_seqs, rows, num_kv_heads, head_dim, max_context_len);
+  if (seqs == 0 || rows >= (int64_t(1) << 31)) return 0;
+  return static_cast<size_t>(256 + 3 * 256 + seqs * seq_bytes(rows, head_dim, max_context_len));
 }
 
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
-  float* lse = reinterpret_cast<float*>(p.ws + 256);
-  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.window * p.num_q_heads;
-  const cudaError_t e = launch_early(stats_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, stream, p, lse);
-  if (e != cudaSuccess) return e;
-  return launch_early(add_kernel, dim3((p.max_context_len + 3) / 4, p.num_seqs), 128, stream, p,
-                      static_cast<const float*>(lse));
+  using namespace weights_detail;
+  const int64_t rows = static_cast<int64_t>(p.window) * p.num_q_heads;
+  const int seqs = seqs_of(p.num_seqs, rows, p.num_kv_heads, p.head_dim, p.max_context_len);
+  const int NC = p.head_dim / 64, tokens = tokens_of(p.head_dim), group = p.num_q_heads / p.num_kv_heads;
+  Launch L{};
+  L.group = group;
+  L.rows = p.window * group;
+  L.tile_queries = 128 / group;
+  L.row_tiles = (p.window + L.tile_queries - 1) / L.tile_queries;
+  L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
+  L.pitch = up(p.max_context_len, 128);
+  L.tiles_pitch = static_cast<int>(L.pitch / tokens);
+  unsigned char* at = p.ws + 256;
+  L.scores = reinterpret_cast<float*>(at);
+  at += up(static_cast<int64_t>(seqs) * rows * L.pitch * 4, 256);
+  L.tile_ml = reinterpret_cast<float2*>(at);
+  at += up(static_cast<int64_t>(seqs) * rows * L.tiles_pitch * 8, 256);
+  L.lse = reinterpret_cast<float*>(at);
+  CUtensorMap tm_k, tm_q;
+  // K as groups of 8 rows of NC chunks of 64 dims; queries as (dims, heads, queries)
+  const uint64_t row = static_cast<uint64_t>(p.head_dim) * 2;
+  const uint64_t kd[4] = {64, 8, static_cast<uint64_t>(NC), static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size / 8};
+  const uint64_t ks[3] = {row, 128, 8 * row};
+  const uint32_t kb[4] = {64, 8, static_cast<uint32_t>(NC), static_cast<uint32_t>(p.block_size < tokens ? p.block_size : tokens) / 8};
+  if (!encode_bf16_tiles(&tm_k, 4, p.k_cache, kd, ks, kb, 128)) return cudaErrorInvalidValue;
+  const uint64_t qd[3] = {static_cast<uint64_t>(p.head_dim), static_cast<uint64_t>(p.num_q_heads),
+                          static_cast<uint64_t>(p.num_seqs) * p.window};
+  const uint64_t qs[2] = {row, row * p.num_q_heads};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(group), static_cast<uint32_t>(p.window < L.tile_queries ? p.window : L.tile_queries)};
+  for (int s0 = 0; s0 < p.num_seqs; s0 += seqs) {
+    L.p = p;
+    L.p.num_seqs = p.num_seqs - s0 < seqs ? p.num_seqs - s0 : seqs;
+    L.p.weights += s0 * p.weights_stride;
+    L.p.q = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(s0) * rows * p.head_dim;
+    L.p.block_tables += static_cast<int64_t>(s0) * p.max_blocks_per_seq;
+    L.p.context_lens += s0;
+    const uint64_t qn[3] = {qd[0], qd[1], static_cast<uint64_t>(L.p.num_seqs) * p.window};
+    if (!encode_bf16_tiles(&tm_q, 3, L.p.q, qn, qs, qb, 128)) return cudaErrorInvalidValue;
+    const int64_t units = L.pitch / tokens * p.num_kv_heads * L.row_tiles * L.p.num_seqs;
+    cudaError_t e = NC == 1   ? launch_scores<1>(L, tm_k, tm_q, units, stream)
+                    : NC == 2 ? launch_scores<2>(L, tm_k, tm_q, units, stream)
+                    : NC == 4 ? launch_scores<4>(L, tm_k, tm_q, units, stream)
+                              : launch_scores<9>(L, tm_k, tm_q, units, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t warps = rows * L.p.num_seqs;
+    e = launch_early(lse_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, stream, L, tokens);
+    if (e != cudaSuccess) return e;
+    e = launch_early(add_kernel, dim3(static_cast<unsigned>(L.pitch / 128), static_cast<unsigned>(L.p.num_seqs)),
+                     32 * kAddWarps, stream, L);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pa

@@ -106,6 +106,13 @@ __device__ __forceinline__ void load_now(uint32_t at, uint32_t (&v)[32]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(ptx::smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(ptx::smem_addr(bar)), "l"(policy)
+      : "memory");
+}
 // a box loaded into this place of every CTA in the mask, counted by the barrier at this place of each
 __device__ __forceinline__ void tma_load_2d_cluster(void* dst, const void* map, int x, int y, uint64_t* bar, uint16_t mask,
                                                     uint64_t policy) {
