@@ -200,13 +200,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 8) {
     // ============================== loads ==============================
-    // lane i: the unit's page i (and i + 32 ..., where blocks are small)
+    // lane i: the unit's page i
     const int page_rows = min(S::kTokens, 1 << L.bs_log), pages = S::kTokens / page_rows;  // at most 16
     const uint64_t policy = L.row_tiles == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
     uint32_t k = 0, qk = 0;
-    walk.each([&](const Unit& x, bool first, bool) {
+    // a unit's pages are looked up while the one before is loaded
+    struct {
+      int at, q_head, q_row;
+      bool first;
+    } ahead{-1, 0, 0, false};
+    auto issue = [&]() {
       if (aborted) return;
-      if (first) {  // the row tile's queries; rows past them are nobody's
+      if (ahead.first) {  // the row tile's queries; rows past them are nobody's
         const uint32_t slot = qk % S::kQSlots;
         wait(&bars[kQFree + slot], ((qk / S::kQSlots) & 1u) ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
@@ -216,35 +221,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t rows = static_cast<uint32_t>(min(L.tile_queries, p.window) * L.group);
           ptx::mbar_arrive_expect_tx(&bars[kQFull + slot], rows * 128u * NC);
           for (int c = 0; c < NC; ++c)
-            tma_load_3d(smem + S::kOffQ + slot * S::kQBytes + c * 16384, &tm_q, c * 64, x.kvh * L.group,
-                        x.seq * p.window + x.rt * L.tile_queries, &bars[kQFull + slot], ptx::policy_evict_normal());
+            tma_load_3d(smem + S::kOffQ + slot * S::kQBytes + c * 16384, &tm_q, c * 64, ahead.q_head, ahead.q_row,
+                        &bars[kQFull + slot], ptx::policy_evict_normal());
         }
         __syncwarp();
-      }
-      const int tok = x.tile * S::kTokens + lane * page_rows;
-      int at = -1;  // the page's first row in the pool, in 8-row groups
-      if (lane < pages && tok < x.len) {
-        int phys = __ldg(p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
-        if (phys < 0 || phys >= p.num_blocks) {  // never read outside the pool
-          atomicExch(p.err, kDevErrInvalidArg);
-          phys = 0;
-        }
-        at = static_cast<int>(((static_cast<int64_t>(phys) * p.num_kv_heads + x.kvh) << L.bs_log) / 8) +
-             (tok & ((1 << L.bs_log) - 1)) / 8;
       }
       const uint32_t slot = k % S::kStages;
       wait(&bars[kFree + slot], ((k / S::kStages) & 1u) ^ 1u, aborted);
       aborted = __any_sync(0xffffffffu, aborted);
       if (aborted) return;
-      const uint32_t have = __popc(__ballot_sync(0xffffffffu, at >= 0));
+      const uint32_t have = __popc(__ballot_sync(0xffffffffu, ahead.at >= 0));
       if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kFull + slot], have * page_rows * 128u * NC);
       __syncwarp();
-      if (at >= 0)
-        ptx::tma_load_4d(smem + slot * S::kStageBytes + lane * page_rows * 128 * NC, &tm_k, 0, 0, 0, at,
+      if (ahead.at >= 0)
+        ptx::tma_load_4d(smem + slot * S::kStageBytes + lane * page_rows * 128 * NC, &tm_k, 0, 0, 0, ahead.at,
                          &bars[kFull + slot], policy);
       __syncwarp();
       ++k;
+    };
+    bool any = false;
+    walk.each([&](const Unit& x, bool first, bool) {
+      const int tok = x.tile * S::kTokens + lane * page_rows;
+      int phys = -1;
+      const bool there = lane < pages && tok < x.len;
+      if (there) phys = __ldg(p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+      if (any) issue();
+      any = true;
+      if (there && (phys < 0 || phys >= p.num_blocks)) {  // never read outside the pool
+        atomicExch(p.err, kDevErrInvalidArg);
+        phys = 0;
+      }
+      // the page's first row in the pool, in 8-row groups
+      ahead.at = there ? static_cast<int>(((static_cast<int64_t>(phys) * p.num_kv_heads + x.kvh) << L.bs_log) / 8) +
+                             (tok & ((1 << L.bs_log) - 1)) / 8
+                       : -1;
+      ahead.q_head = x.kvh * L.group;
+      ahead.q_row = x.seq * p.window + x.rt * L.tile_queries;
+      ahead.first = first;
     });
+    if (any) issue();
   } else if (warp == 9) {
     // ============================ products ============================
     const bool leader = elect_one();

@@ -84,10 +84,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LatentPrefillP
 constexpr int kThreads = 6 * 32;
 constexpr int kABytes = 8 * 16384;   // [8 chunks of 64 columns][128 rows x 128 bytes]
 constexpr int kBBytes = 32768;       // a chunk of a head's weights: 128 rows of w_k, 128 of w_v
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr int kOffB = kABytes, kOffBar = kOffB + kStages * kBBytes;
 constexpr int kSmemBytes = 1024 + kOffBar + 256;
-enum : int { kAFull = 0, kAFree = 1, kBFull = 2, kBFree = 4, kDFull = 6, kDFree = 8, kDrain = 10, kNumBars = 11 };
+enum : int { kAFull = 0, kAFree = 1, kBFull = 2, kBFree = 5, kDFull = 8, kDFree = 10, kDrain = 12, kNumBars = 13 };
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct Launch {
   LatentPrefillParams p;
@@ -129,9 +130,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     ptx::mbar_init(&bars[kAFull], 1);
     ptx::mbar_init(&bars[kAFree], 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&bars[kBFull + i], 1);
       ptx::mbar_init(&bars[kBFree + i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars[kDFull + i], 1);
       ptx::mbar_init(&bars[kDFree + i], 4);
     }
