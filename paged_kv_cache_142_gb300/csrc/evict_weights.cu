@@ -126,7 +126,11 @@ struct Walk {
   }
 };
 
-template <int NC>
+// FEW: at most 16 rows.  Then tokens are the product's rows and queries its
+// columns: a thread has one token's scores of all rows instead of one row's of all
+// tokens, so that four warps share the exponentials that a quarter of the lanes
+// of one would form, and a row's maximum and sum go through shuffles.
+template <int NC, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
     scores_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_q) {
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ============================ products ============================
     const bool leader = elect_one();
-    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, S::kTokens, 0, 0);
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, FEW ? 16 : S::kTokens, 0, 0);
     const uint64_t desc_k = ptx::smem_desc(smem, 16, 1024 * NC, ptx::kLayoutSw128);
     const uint64_t desc_q = ptx::smem_desc(smem + S::kOffQ, 16, 1024, ptx::kLayoutSw128);
     uint32_t k = 0, qk = 0;
@@ -279,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) {
         const uint64_t dk = desc_k + slot * (S::kStageBytes >> 4), dq = desc_q + qslot * (S::kQBytes >> 4);
 #pragma unroll
-        for (int c = 0; c < 4 * NC; ++c)
-          ptx::umma_bf16(tmem + (k & 1u) * 128, dq + (c >> 2) * (16384 >> 4) + (c & 3) * 2,
-                         dk + (c >> 2) * (1024 >> 4) + (c & 3) * 2, kId, c > 0);
+        for (int c = 0; c < 4 * NC; ++c) {
+          const uint64_t q = dq + (c >> 2) * (16384 >> 4) + (c & 3) * 2, t = dk + (c >> 2) * (1024 >> 4) + (c & 3) * 2;
+          ptx::umma_bf16(tmem + (k & 1u) * 128, FEW ? t : q, FEW ? q : t, kId, c > 0);
+        }
         ptx::umma_commit(&bars[kSFull + (k & 1u)]);
         ptx::umma_commit(&bars[kFree + slot]);
         if (last) ptx::umma_commit(&bars[kQFree + qslot]);
@@ -311,44 +316,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       aborted = __any_sync(0xffffffffu, aborted);
       if (aborted) return;
       ptx::tc_fence_after();
-      const int tile_rows = min(L.tile_queries * L.group, L.rows - x.rt * L.tile_queries * L.group);
-      const int row = x.rt * L.tile_queries * L.group + r;
-      const bool valid = r < tile_rows;
-      if ((warp & 3) * 32 < tile_rows) {
-        const int seen = x.len - p.window + 1 + row / L.group;  // tokens that this row sees
-        const int nvis = seen - x.tile * S::kTokens;
-        const int64_t grow = x.seq * all_rows + static_cast<int64_t>(x.kvh) * L.rows + row;
-        float* dst = L.scores + grow * L.pitch + x.tile * S::kTokens;
-        float top = -CUDART_INF_F, sum = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < S::kTokens; c += 32) {
-          uint32_t v[32];
-          load_now(at + c, v);
-          float m0 = -CUDART_INF_F;
-          float y[32];
+      if constexpr (FEW) {
+        uint32_t v[16];
+        load_now(at, v);
+        const int64_t row0 = x.seq * all_rows + static_cast<int64_t>(x.kvh) * L.rows;
+        float* dst = L.scores + row0 * L.pitch + x.tile * S::kTokens + r;
+        const int tok = x.tile * S::kTokens + r;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            y[j] = c + j < nvis ? __uint_as_float(v[j]) * p.scale_log2 : -CUDART_INF_F;
-            m0 = fmaxf(m0, y[j]);
-          }
-          const float now = fmaxf(top, m0), ref = now == -CUDART_INF_F ? 0.f : now;
-          float s0 = 0.f, s1 = 0.f;
+        for (int j = 0; j < 16; ++j) {
+          if (j >= L.rows) break;
+          const int seen = x.len - p.window + 1 + j / L.group;  // tokens that this row sees
+          const float y = tok < seen ? __uint_as_float(v[j]) * p.scale_log2 : -CUDART_INF_F;
+          dst[j * L.pitch] = y;
+          float top = y;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) s0 += fp4::fast_exp2(y[j] - ref), s1 += fp4::fast_exp2(y[j + 1] - ref);
-          sum = fmaf(sum, fp4::fast_exp2(top - ref), s0 + s1);
-          top = now;
-          if (valid) {
+          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          float e = fp4::fast_exp2(y - (top == -CUDART_INF_F ? 0.f : top));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
-              fp4::store32(dst + c + 8 * q, w);
-            }
-          }
-          __syncwarp();  // the next load is the whole warp's
+          for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+          // a warp's 32 tokens have statistics of their own
+          if (lane == 0) L.tile_ml[(row0 + j) * L.tiles_pitch + x.tile * 4 + (warp & 3)] = make_float2(top, e);
         }
-        if (valid) L.tile_ml[grow * L.tiles_pitch + x.tile] = make_float2(top, sum);
+      } else {
+        const int tile_rows = min(L.tile_queries * L.group, L.rows - x.rt * L.tile_queries * L.group);
+        const int row = x.rt * L.tile_queries * L.group + r;
+        const bool valid = r < tile_rows;
+        if ((warp & 3) * 32 < tile_rows) {
+          const int seen = x.len - p.window + 1 + row / L.group;  // tokens that this row sees
+          const int nvis = seen - x.tile * S::kTokens;
+          const int64_t grow = x.seq * all_rows + static_cast<int64_t>(x.kvh) * L.rows + row;
+          float* dst = L.scores + grow * L.pitch + x.tile * S::kTokens;
+          float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < S::kTokens; c += 32) {
+            uint32_t v[32];
+            load_now(at + c, v);
+            float m0 = -CUDART_INF_F;
+            float y[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              y[j] = c + j < nvis ? __uint_as_float(v[j]) * p.scale_log2 : -CUDART_INF_F;
+              m0 = fmaxf(m0, y[j]);
+            }
+            const float now = fmaxf(top, m0), ref = now == -CUDART_INF_F ? 0.f : now;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) s0 += fp4::fast_exp2(y[j] - ref), s1 += fp4::fast_exp2(y[j + 1] - ref);
+            sum = fmaf(sum, fp4::fast_exp2(top - ref), s0 + s1);
+            top = now;
+            if (valid) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
+                fp4::store32(dst + c + 8 * q, w);
+              }
+            }
+            __syncwarp();  // the next load is the whole warp's
+          }
+          if (valid) L.tile_ml[grow * L.tiles_pitch + x.tile] = make_float2(top, sum);
+        }
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -374,7 +402,7 @@ __global__ void __launch_bounds__(256) lse_kernel(const Launch L, int tokens) {
   if (row >= all_rows * L.p.num_seqs) return;
   const int len = length_of(L.p, static_cast<int>(row / all_rows));
   const int seen = len - L.p.window + 1 + static_cast<int>(row % all_rows) % L.rows / L.group;
-  const int tiles = (len + tokens - 1) / tokens;
+  const int tiles = (len + tokens - 1) / tokens;  // (what a row's statistics stand for)
   float m = -CUDART_INF_F, s = 0.f;
   for (int i = lane; i < tiles; i += 32) {
     const float2 e = __ldcg(L.tile_ml + row * L.tiles_pitch + i);
@@ -429,30 +457,30 @@ __global__ void __launch_bounds__(32 * kAddWarps) add_kernel(const Launch L) {
 int tokens_of(int head_dim) {
   return head_dim <= 128 ? 128 : head_dim <= 256 ? 64 : 32;
 }
+constexpr int kStatTokens = 32;  // the least that a row's statistics stand for
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // of one sequence: its rows' logarithms, tiles' statistics and scores
-int64_t seq_bytes(int64_t rows, int head_dim, int max_context_len) {
-  const int64_t tiles = up(max_context_len, 128) / tokens_of(head_dim);
-  return rows * (4 + tiles * 8 + up(max_context_len, 128) * 4);
+int64_t seq_bytes(int64_t rows, int max_context_len) {
+  return rows * (4 + up(max_context_len, 128) / kStatTokens * 8 + up(max_context_len, 128) * 4);
 }
 // sequences of one launch; 0: not even one's units fit an int
 int seqs_of(int num_seqs, int64_t rows, int num_kv_heads, int head_dim, int max_context_len) {
   const int64_t units = up(max_context_len, 128) / tokens_of(head_dim) * (rows < num_kv_heads ? num_kv_heads : rows);
   const int64_t fit = units > 0 ? ((int64_t(1) << 31) - 1) / units : kMaxSeqs;
   if (fit == 0) return 0;
-  int64_t n = kScoreBytes / (seq_bytes(rows, head_dim, max_context_len) + 1);
+  int64_t n = kScoreBytes / (seq_bytes(rows, max_context_len) + 1);
   if (n < 1) n = 1;
   if (n > fit) n = fit;
   if (n > kMaxSeqs) n = kMaxSeqs;
   return static_cast<int>(n < num_seqs ? n : num_seqs);
 }
 
-template <int NC>
+template <int NC, bool FEW>
 cudaError_t launch_scores(const Launch& L, const CUtensorMap& tm_k, const CUtensorMap& tm_q, int64_t most_units,
                           cudaStream_t stream) {
   using S = Shape<NC>;
   const int smem = 1024 + S::kOffPrefix + (L.p.num_seqs + 64) / 64 * 256;
-  const void* fn = reinterpret_cast<const void*>(&scores_kernel<NC>);
+  const void* fn = reinterpret_cast<const void*>(&scores_kernel<NC, FEW>);
   int per_sm = 0;
   const cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
   if (e != cudaSuccess) return e;
@@ -479,7 +507,7 @@ size_t weights_workspace(int num_seqs, int window, int num_q_heads, int num_kv_h
   if (num_seqs == 0) return 256;
   const int seqs = seqs_of(num_seqs, rows, num_kv_heads, head_dim, max_context_len);
   if (seqs == 0 || rows >= (int64_t(1) << 31)) return 0;
-  return static_cast<size_t>(256 + 3 * 256 + seqs * seq_bytes(rows, head_dim, max_context_len));
+  return static_cast<size_t>(256 + 3 * 256 + seqs * seq_bytes(rows, max_context_len));
 }
 
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
@@ -494,7 +522,9 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
   L.row_tiles = (p.window + L.tile_queries - 1) / L.tile_queries;
   L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
   L.pitch = up(p.max_context_len, 128);
-  L.tiles_pitch = static_cast<int>(L.pitch / tokens);
+  const bool few = L.rows <= 16 && tokens == 128;
+  const int stat_tokens = few ? kStatTokens : tokens;
+  L.tiles_pitch = static_cast<int>(L.pitch / stat_tokens);
   unsigned char* at = p.ws + 256;
   L.scores = reinterpret_cast<float*>(at);
   at += up(static_cast<int64_t>(seqs) * rows * L.pitch * 4, 256);
@@ -522,13 +552,13 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
     const uint64_t qn[3] = {qd[0], qd[1], static_cast<uint64_t>(L.p.num_seqs) * p.window};
     if (!encode_bf16_tiles(&tm_q, 3, L.p.q, qn, qs, qb, 128)) return cudaErrorInvalidValue;
     const int64_t units = L.pitch / tokens * p.num_kv_heads * L.row_tiles * L.p.num_seqs;
-    cudaError_t e = NC == 1   ? launch_scores<1>(L, tm_k, tm_q, units, stream)
-                    : NC == 2 ? launch_scores<2>(L, tm_k, tm_q, units, stream)
-                    : NC == 4 ? launch_scores<4>(L, tm_k, tm_q, units, stream)
-                              : launch_scores<9>(L, tm_k, tm_q, units, stream);
+    cudaError_t e = NC == 1   ? (few ? launch_scores<1, true> : launch_scores<1, false>)(L, tm_k, tm_q, units, stream)
+                    : NC == 2 ? (few ? launch_scores<2, true> : launch_scores<2, false>)(L, tm_k, tm_q, units, stream)
+                    : NC == 4 ? launch_scores<4, false>(L, tm_k, tm_q, units, stream)
+                              : launch_scores<9, false>(L, tm_k, tm_q, units, stream);
     if (e != cudaSuccess) return e;
     const int64_t warps = rows * L.p.num_seqs;
-    e = launch_early(lse_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, stream, L, tokens);
+    e = launch_early(lse_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, stream, L, stat_tokens);
     if (e != cudaSuccess) return e;
     e = launch_early(add_kernel, dim3(static_cast<unsigned>(L.pitch / 128), static_cast<unsigned>(L.p.num_seqs)),
                      32 * kAddWarps, stream, L);
