@@ -61,12 +61,40 @@ struct Launch {
   int tiles_pitch;  // tiles of a row
   float* lse;       // [seqs][kv heads * rows]
   float2* tile_ml;  // [seqs][kv heads * rows][tiles_pitch] maximum (log2), sum
-  float* scores;    // [seqs][kv heads * rows][pitch]
+  float* scores;    // [seqs][kv heads * rows][pitch]; null: formed a second time instead
 };
 
 __device__ __forceinline__ int length_of(const WeightsParams& p, int seq) {
   const int n = p.context_lens[seq];
   return n > 0 && n <= p.max_context_len ? n : 0;
+}
+
+// prefix[s]: units before sequence s, `each` of them a tile of `tokens`
+__device__ __forceinline__ void count_units(const WeightsParams& p, int* prefix, int* warp_sums, int tokens, int each) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  const int beg = min(p.num_seqs, tid * per), end = min(p.num_seqs, beg + per);
+  int local = 0;
+  for (int s = beg; s < end; ++s) {
+    const int n = length_of(p, s);
+    if (n != p.context_lens[s] && blockIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
+    const int units = (n + tokens - 1) / tokens * each;
+    prefix[s + 1] = units;
+    local += units;
+  }
+  int x = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int run = x - local;
+  for (int w = 0; w < warp; ++w) run += warp_sums[w];
+  if (tid == 0) prefix[0] = 0;
+  for (int s = beg; s < end; ++s) prefix[s + 1] = run += prefix[s + 1];
+  __syncthreads();
 }
 
 // A unit: a token tile of (sequence, kv head, row tile).
@@ -172,31 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool aborted = false;
   ptx::griddep_wait();
 
-  {  // ---- units before every sequence ----
-    const int per = (p.num_seqs + kThreads - 1) / kThreads;
-    const int beg = min(p.num_seqs, tid * per), end = min(p.num_seqs, beg + per);
-    int local = 0;
-    for (int s = beg; s < end; ++s) {
-      const int n = length_of(p, s);
-      if (n != p.context_lens[s] && blockIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
-      const int units = (n + S::kTokens - 1) / S::kTokens * p.num_kv_heads * L.row_tiles;
-      prefix[s + 1] = units;
-      local += units;
-    }
-    int x = local;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int run = x - local;
-    for (int w = 0; w < warp; ++w) run += warp_sums[w];
-    if (tid == 0) prefix[0] = 0;
-    for (int s = beg; s < end; ++s) prefix[s + 1] = run += prefix[s + 1];
-    __syncthreads();
-  }
+  count_units(p, prefix, warp_sums, S::kTokens, p.num_kv_heads * L.row_tiles);
   const int total = prefix[p.num_seqs];
   const int share = total / gridDim.x, extra = total - share * gridDim.x;
   auto run_begin = [&](int c) { return c * share + min(c, extra); };
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; j += 2) s0 += fp4::fast_exp2(y[j] - ref), s1 += fp4::fast_exp2(y[j + 1] - ref);
             sum = fmaf(sum, fp4::fast_exp2(top - ref), s0 + s1);
             top = now;
-            if (valid) {
+            if (valid && L.scores) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 uint32_t w[8];
@@ -454,33 +458,238 @@ __global__ void __launch_bounds__(32 * kAddWarps) add_kernel(const Launch L) {
   }
 }
 
+// Step 3 without stored scores: a token tile's products with every row tile again,
+// tokens as the product's rows (128) and queries as its columns, so that a thread
+// adds up one token's probabilities of 128 rows and needs nobody else's.  Warps 0-3
+// add, 8 loads, 9 issues products.
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1)
+    again_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_q) {
+  using S = Shape<NC>;
+  static_assert(S::kTokens == 128 && S::kQSlots == 2, "a tile's tokens are the product's rows");
+  const WeightsParams& p = L.p;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* prefix = reinterpret_cast<int*>(smem + S::kOffPrefix);
+  __shared__ int warp_sums[kThreads / 32];
+  __shared__ __align__(16) float row_lse[2][128];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  ptx::griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      ptx::mbar_init(&bars[kFull + i], 1);
+      ptx::mbar_init(&bars[kFree + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars[kQFull + i], 1);
+      ptx::mbar_init(&bars[kQFree + i], 1);
+      ptx::mbar_init(&bars[kSFull + i], 1);
+      ptx::mbar_init(&bars[kSFree + i], 4);
+    }
+    ptx::mbar_init(&bars[kDrain], 1);
+    *gave_up = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(tmem_slot, 256);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool aborted = false;
+  ptx::griddep_wait();
+  count_units(p, prefix, warp_sums, S::kTokens, 1);
+  const int total = prefix[p.num_seqs];
+  const int share = total / gridDim.x, extra = total - share * gridDim.x;
+  auto run_begin = [&](int c) { return c * share + min(c, extra); };
+  const int u0 = run_begin(blockIdx.x), u1 = run_begin(blockIdx.x + 1);
+  const int inner = p.num_kv_heads * L.row_tiles;
+  const int64_t all_rows = static_cast<int64_t>(p.num_kv_heads) * L.rows;
+
+  // f(sequence, its length, tile) for the tiles of this CTA
+  auto tiles = [&](auto f) {
+    if (u0 >= u1) return;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {  // the last sequence that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    for (int u = u0; u < u1; ++u) {
+      while (prefix[lo + 1] == u) ++lo;  // the next sequence with tiles
+      f(lo, length_of(p, lo), u - prefix[lo]);
+    }
+  };
+
+  if (warp == 8) {
+    // ============================== loads ==============================
+    const int page_rows = min(128, 1 << L.bs_log), pages = 128 / page_rows;
+    const uint64_t normal = ptx::policy_evict_normal();
+    uint32_t k = 0;
+    tiles([&](int seq, int len, int tile) {
+      const int tok = tile * 128 + lane * page_rows;
+      int phys = -1;
+      if (lane < pages && tok < len) {
+        phys = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + (tok >> L.bs_log));
+        if (phys < 0 || phys >= p.num_blocks) phys = 0;  // (reported by the first step)
+      }
+      const uint32_t have = __popc(__ballot_sync(0xffffffffu, phys >= 0));
+      for (int i = 0; i < inner && !aborted; ++i, ++k) {
+        const int kvh = i / L.row_tiles, rt = i - kvh * L.row_tiles;
+        const uint32_t slot = k % S::kStages, qslot = k & 1u;
+        wait(&bars[kQFree + qslot], ((k >> 1) & 1u) ^ 1u, aborted);
+        wait(&bars[kFree + slot], ((k / S::kStages) & 1u) ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        if (lane == 0) {
+          const uint32_t rows = static_cast<uint32_t>(min(L.tile_queries, p.window) * L.group);
+          ptx::mbar_arrive_expect_tx(&bars[kQFull + qslot], rows * 128u * NC);
+          ptx::mbar_arrive_expect_tx(&bars[kFull + slot], have * page_rows * 128u * NC);
+          for (int c = 0; c < NC; ++c)
+            tma_load_3d(smem + S::kOffQ + qslot * S::kQBytes + c * 16384, &tm_q, c * 64, kvh * L.group,
+                        seq * p.window + rt * L.tile_queries, &bars[kQFull + qslot], normal);
+        }
+        __syncwarp();
+        if (phys >= 0)
+          ptx::tma_load_4d(smem + slot * S::kStageBytes + lane * page_rows * 128 * NC, &tm_k, 0, 0, 0,
+                           static_cast<int>(((static_cast<int64_t>(phys) * p.num_kv_heads + kvh) << L.bs_log) / 8) +
+                               (tok & ((1 << L.bs_log) - 1)) / 8,
+                           &bars[kFull + slot], normal);
+        __syncwarp();
+      }
+    });
+  } else if (warp == 9) {
+    // ============================ products ============================
+    const bool leader = elect_one();
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, 128, 0, 0);
+    const uint64_t desc_k = ptx::smem_desc(smem, 16, 1024 * NC, ptx::kLayoutSw128);
+    const uint64_t desc_q = ptx::smem_desc(smem + S::kOffQ, 16, 1024, ptx::kLayoutSw128);
+    uint32_t k = 0;
+    tiles([&](int, int, int) {
+      for (int i = 0; i < inner && !aborted; ++i, ++k) {
+        const uint32_t slot = k % S::kStages, two = k & 1u, ph = (k >> 1) & 1u;
+        wait(&bars[kQFull + two], ph, aborted);
+        wait(&bars[kFull + slot], (k / S::kStages) & 1u, aborted);
+        wait(&bars[kSFree + two], ph ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) return;
+        ptx::tc_fence_after();
+        if (leader) {
+          const uint64_t dk = desc_k + slot * (S::kStageBytes >> 4), dq = desc_q + two * (S::kQBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < 4 * NC; ++c)
+            ptx::umma_bf16(tmem + two * 128, dk + (c >> 2) * (1024 >> 4) + (c & 3) * 2,
+                           dq + (c >> 2) * (16384 >> 4) + (c & 3) * 2, kId, c > 0);
+          ptx::umma_commit(&bars[kSFull + two]);
+          ptx::umma_commit(&bars[kFree + slot]);
+          ptx::umma_commit(&bars[kQFree + two]);
+        }
+        __syncwarp();
+      }
+    });
+    if (leader) {  // nothing may be in flight when tensor memory is freed
+      ptx::umma_commit(&bars[kDrain]);
+      bool late = false;
+      wait(&bars[kDrain], 0, late);
+      if (late) aborted = true;
+    }
+    aborted = __any_sync(0xffffffffu, aborted);
+  } else if (warp < 4) {
+    // ==================== sums: one token per thread ====================
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    uint32_t k = 0;
+    tiles([&](int seq, int len, int tile) {
+      const int tok = tile * 128 + tid;
+      float s0 = 0.f, s1 = 0.f;
+      for (int i = 0; i < inner; ++i, ++k) {  // (a warp that gave up still meets the others at the barrier)
+        const int kvh = i / L.row_tiles, rt = i - kvh * L.row_tiles;
+        const uint32_t two = k & 1u;
+        const int row = rt * L.tile_queries * L.group + tid, rows = min(L.tile_queries * L.group, L.rows - (row - tid));
+        // rows that are nobody's, or see nothing: 2^(s - inf) = 0
+        row_lse[two][tid] =
+            tid < rows ? __ldcg(L.lse + seq * all_rows + static_cast<int64_t>(kvh) * L.rows + row) : CUDART_INF_F;
+        ptx::bar_sync(1, 128);
+        wait(&bars[kSFull + two], (k >> 1) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        ptx::tc_fence_after();
+        // queries from which on (by row of the tile) this token is seen: its first such query's first row
+        const int q0 = tok - (len - p.window) - rt * L.tile_queries;
+        const int from = q0 > 0 ? q0 * L.group : 0;
+        const bool all = __all_sync(0xffffffffu, from == 0) && rows == 128;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          load_now(at + two * 128 + c, v);
+          if (all) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(&row_lse[two][c + j]);
+              s0 += fp4::fast_exp2(fmaf(__uint_as_float(v[j]), p.scale_log2, -l.x));
+              s1 += fp4::fast_exp2(fmaf(__uint_as_float(v[j + 1]), p.scale_log2, -l.y));
+              s0 += fp4::fast_exp2(fmaf(__uint_as_float(v[j + 2]), p.scale_log2, -l.z));
+              s1 += fp4::fast_exp2(fmaf(__uint_as_float(v[j + 3]), p.scale_log2, -l.w));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              s0 += c + j >= from && c + j < rows
+                        ? fp4::fast_exp2(fmaf(__uint_as_float(v[j]), p.scale_log2, -row_lse[two][c + j]))
+                        : 0.f;
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !aborted) ptx::mbar_arrive(&bars[kSFree + two]);
+      }
+      if (tok < len && !aborted) p.weights[seq * p.weights_stride + tok] += s0 + s1;
+    });
+  }
+
+  if (aborted) *gave_up = 1;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 9) ptx::tmem_dealloc(tmem, 256);
+  if (tid == 0 && *gave_up) atomicExch(p.err, kDevErrTimeout);
+}
+
 int tokens_of(int head_dim) {
   return head_dim <= 128 ? 128 : head_dim <= 256 ? 64 : 32;
 }
 constexpr int kStatTokens = 32;  // the least that a row's statistics stand for
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+// Scores stored or formed again, by a kv head's rows.  Stored they cost 8 bytes a row
+// and token; again the key's 2 head_dim bytes once more (and its products, which
+// are free beside them): so from head_dim / 4 rows on, where a tile of tokens fills
+// the product's 128 rows.  32 queries of a group of 4 over 4 x 16384 tokens: stored
+// 132 us, again 75.
+bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > head_dim / 4; }
 // of one sequence: its rows' logarithms, tiles' statistics and scores
-int64_t seq_bytes(int64_t rows, int max_context_len) {
-  return rows * (4 + up(max_context_len, 128) / kStatTokens * 8 + up(max_context_len, 128) * 4);
+int64_t seq_bytes(int64_t rows, bool stored, int max_context_len) {
+  return rows * (4 + up(max_context_len, 128) / kStatTokens * 8 + (stored ? up(max_context_len, 128) * 4 : 0));
 }
 // sequences of one launch; 0: not even one's units fit an int
 int seqs_of(int num_seqs, int64_t rows, int num_kv_heads, int head_dim, int max_context_len) {
   const int64_t units = up(max_context_len, 128) / tokens_of(head_dim) * (rows < num_kv_heads ? num_kv_heads : rows);
   const int64_t fit = units > 0 ? ((int64_t(1) << 31) - 1) / units : kMaxSeqs;
   if (fit == 0) return 0;
-  int64_t n = kScoreBytes / (seq_bytes(rows, max_context_len) + 1);
+  int64_t n = kScoreBytes / (seq_bytes(rows, !again(rows / num_kv_heads, head_dim), max_context_len) + 1);
   if (n < 1) n = 1;
   if (n > fit) n = fit;
   if (n > kMaxSeqs) n = kMaxSeqs;
   return static_cast<int>(n < num_seqs ? n : num_seqs);
 }
 
-template <int NC, bool FEW>
-cudaError_t launch_scores(const Launch& L, const CUtensorMap& tm_k, const CUtensorMap& tm_q, int64_t most_units,
-                          cudaStream_t stream) {
-  using S = Shape<NC>;
-  const int smem = 1024 + S::kOffPrefix + (L.p.num_seqs + 64) / 64 * 256;
-  const void* fn = reinterpret_cast<const void*>(&scores_kernel<NC, FEW>);
+// one CTA per SM, launched while the kernel before drains
+cudaError_t launch_walk(const void* fn, int smem, const Launch& L, const CUtensorMap& tm_k, const CUtensorMap& tm_q,
+                        int64_t most_units, cudaStream_t stream) {
   int per_sm = 0;
   const cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
   if (e != cudaSuccess) return e;
@@ -498,6 +707,10 @@ cudaError_t launch_scores(const Launch& L, const CUtensorMap& tm_k, const CUtens
   void* args[] = {const_cast<Launch*>(&L), const_cast<CUtensorMap*>(&tm_k), const_cast<CUtensorMap*>(&tm_q)};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
+template <int NC>
+int smem_of(int num_seqs) {
+  return 1024 + Shape<NC>::kOffPrefix + (num_seqs + 64) / 64 * 256;
+}
 
 }  // namespace weights_detail
 
@@ -507,7 +720,7 @@ size_t weights_workspace(int num_seqs, int window, int num_q_heads, int num_kv_h
   if (num_seqs == 0) return 256;
   const int seqs = seqs_of(num_seqs, rows, num_kv_heads, head_dim, max_context_len);
   if (seqs == 0 || rows >= (int64_t(1) << 31)) return 0;
-  return static_cast<size_t>(256 + 3 * 256 + seqs * seq_bytes(rows, max_context_len));
+  return static_cast<size_t>(256 + 3 * 256 + seqs * seq_bytes(rows, !again(rows / num_kv_heads, head_dim), max_context_len));
 }
 
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
@@ -526,8 +739,11 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
   const int stat_tokens = few ? kStatTokens : tokens;
   L.tiles_pitch = static_cast<int>(L.pitch / stat_tokens);
   unsigned char* at = p.ws + 256;
-  L.scores = reinterpret_cast<float*>(at);
-  at += up(static_cast<int64_t>(seqs) * rows * L.pitch * 4, 256);
+  const bool twice = again(L.rows, p.head_dim);
+  if (!twice) {
+    L.scores = reinterpret_cast<float*>(at);
+    at += up(static_cast<int64_t>(seqs) * rows * L.pitch * 4, 256);
+  }
   L.tile_ml = reinterpret_cast<float2*>(at);
   at += up(static_cast<int64_t>(seqs) * rows * L.tiles_pitch * 8, 256);
   L.lse = reinterpret_cast<float*>(at);
@@ -551,16 +767,23 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
     L.p.context_lens += s0;
     const uint64_t qn[3] = {qd[0], qd[1], static_cast<uint64_t>(L.p.num_seqs) * p.window};
     if (!encode_bf16_tiles(&tm_q, 3, L.p.q, qn, qs, qb, 128)) return cudaErrorInvalidValue;
-    const int64_t units = L.pitch / tokens * p.num_kv_heads * L.row_tiles * L.p.num_seqs;
-    cudaError_t e = NC == 1   ? (few ? launch_scores<1, true> : launch_scores<1, false>)(L, tm_k, tm_q, units, stream)
-                    : NC == 2 ? (few ? launch_scores<2, true> : launch_scores<2, false>)(L, tm_k, tm_q, units, stream)
-                    : NC == 4 ? launch_scores<4, false>(L, tm_k, tm_q, units, stream)
-                              : launch_scores<9, false>(L, tm_k, tm_q, units, stream);
+    const int64_t tiles = L.pitch / tokens * L.p.num_seqs;
+    const void* fn = NC == 1   ? (few ? reinterpret_cast<const void*>(&scores_kernel<1, true>) : reinterpret_cast<const void*>(&scores_kernel<1, false>))
+                     : NC == 2 ? (few ? reinterpret_cast<const void*>(&scores_kernel<2, true>) : reinterpret_cast<const void*>(&scores_kernel<2, false>))
+                     : NC == 4 ? reinterpret_cast<const void*>(&scores_kernel<4, false>)
+                               : reinterpret_cast<const void*>(&scores_kernel<9, false>);
+    const int n = L.p.num_seqs;
+    const int smem = NC == 1 ? smem_of<1>(n) : NC == 2 ? smem_of<2>(n) : NC == 4 ? smem_of<4>(n) : smem_of<9>(n);
+    cudaError_t e = launch_walk(fn, smem, L, tm_k, tm_q, tiles * p.num_kv_heads * L.row_tiles, stream);
     if (e != cudaSuccess) return e;
     const int64_t warps = rows * L.p.num_seqs;
     e = launch_early(lse_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, stream, L, stat_tokens);
     if (e != cudaSuccess) return e;
-    e = launch_early(add_kernel, dim3(static_cast<unsigned>(L.pitch / 128), static_cast<unsigned>(L.p.num_seqs)),
+    if (twice)
+      e = launch_walk(NC == 1 ? reinterpret_cast<const void*>(&again_kernel<1>) : reinterpret_cast<const void*>(&again_kernel<2>), smem,
+                      L, tm_k, tm_q, tiles, stream);
+    else
+      e = launch_early(add_kernel, dim3(static_cast<unsigned>(L.pitch / 128), static_cast<unsigned>(L.p.num_seqs)),
                      32 * kAddWarps, stream, L);
     if (e != cudaSuccess) return e;
   }

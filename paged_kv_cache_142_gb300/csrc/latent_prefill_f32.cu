@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_f32_kernel(const LatentPre
   // the longest rows first
   const int q0 = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) * kQueries;
   if (x.tile0[seq + 1] == x.tile0[seq] || q0 >= n) return;
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   float* sq = smem;
   float* sk = sq + kQueries * 192;
   float* sv = sk + kKeys * kPitch;
