@@ -4,8 +4,8 @@
 // the weights moved to the places that token compaction gives their tokens.
 //
 // The threshold is found by radix selection on the weights' order-preserving
-// bit patterns: four passes, each counts the 8-bit digits of the candidates
-// that agree with the digits found so far.  Then one sweep in order of the
+// bit patterns: up to four passes, each counts the 8-bit digits of the candidates
+// that agree with the digits found so far, until all of those stay.  Then one sweep in order of the
 // positions numbers what is above it, and as many of what equals it as are
 // still wanted.  Counts are integers, so the result does not depend on the
 // order of anything.
@@ -61,12 +61,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
 
   extern __shared__ float slice[];
   __shared__ int hist[kCopies * kPitch];
-  __shared__ int total[2][256];
-  __shared__ int shared_digit[2];
+  __shared__ int total[2][256], sums[256];
+  __shared__ int shared_digit[3];
   __shared__ int2 counts;          // above, equal: of this CTA's slice
-  __shared__ int warp_gt[kWarps], warp_eq[kWarps];
+  __shared__ int2 warp_counts[kWarps];
+  // a warp's stretch of the slice
+  const int seg = (mine + kWarps * 32 - 1) / (kWarps * 32) * 32;
+  const int w0 = min(mine, warp * seg), w1 = min(mine, w0 + seg);
   if (cached)
-    for (int i = tid; i < mine; i += kThreads) slice[i] = row[lo + i];
+    for (int i = w0 + lane; i < w1; i += 32) slice[i] = row[lo + i];
   const float* w = cached ? slice : row + lo;
 
   // ---- the threshold, digit by digit ----
@@ -79,7 +82,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
       for (int i = tid; i < kCopies * kPitch; i += kThreads) hist[i] = 0;
       __syncthreads();
       int* mine_hist = hist + (lane & (kCopies - 1)) * kPitch;
-      for (int i = tid; i < mine; i += kThreads) {
+#pragma unroll 4
+      for (int i = w0 + lane; i < w1; i += 32) {
         const uint32_t k = order_of(w[i]);
         if ((k & mask) == prefix) atomicAdd(mine_hist + ((k >> shift) & 255u), 1);
       }
@@ -90,16 +94,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
         for (int c = 0; c < kCopies; ++c) s += hist[c * kPitch + tid];
         total[pass & 1][tid] = s;
       }
-      cluster.sync();
+      if (C > 1) cluster.sync();
+      if (tid < 256) {
+        int s = 0;
+        if (C > 1) {
+          int v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = c < C ? cluster.map_shared_rank(&total[pass & 1][0], c)[tid] : 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) s += v[c];
+        } else {
+          s = total[pass & 1][tid];
+        }
+        sums[255 - tid] = s;
+      }
+      __syncthreads();
       if (warp == 0) {
         // lane: digits 255 - 8 lane and the seven below
         int cnt[8], sum = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          cnt[e] = 0;
-          for (int c = 0; c < C; ++c) cnt[e] += cluster.map_shared_rank(&total[pass & 1][0], c)[255 - 8 * lane - e];
-          sum += cnt[e];
-        }
+        for (int e = 0; e < 8; ++e) sum += cnt[e] = sums[8 * lane + e];
         int above = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -113,6 +127,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
             if (want > above && want <= above + cnt[e]) {
               shared_digit[0] = 255 - 8 * lane - e;
               shared_digit[1] = want - above;
+              shared_digit[2] = cnt[e];
             }
             above += cnt[e];
           }
@@ -122,6 +137,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
       prefix |= static_cast<uint32_t>(shared_digit[0]) << shift;
       mask |= 255u << shift;
       want = shared_digit[1];
+      if (want == shared_digit[2] && prefix) {  // all that agree so far stay: they are what lies above prefix - 1
+        prefix -= 1;
+        want = 0;
+        break;
+      }
     }
   } else {
     prefix = 0xffffffffu;  // no weight is as large
@@ -129,53 +149,44 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
 
   // ---- how many of each slice stay ----
   int gt = 0, eq = 0;
-  for (int i = tid; i < mine; i += kThreads) {
+#pragma unroll 4
+  for (int i = w0 + lane; i < w1; i += 32) {
     const uint32_t k = order_of(w[i]);
     gt += k > prefix;
     eq += k == prefix;
   }
-  for (int o = 16; o; o >>= 1) gt += __shfl_xor_sync(0xffffffffu, gt, o), eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  if (lane == 0) warp_gt[warp] = gt, warp_eq[warp] = eq;
+  gt = __reduce_add_sync(0xffffffffu, gt), eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) warp_counts[warp] = make_int2(gt, eq);
   __syncthreads();
   if (tid == 0) {
     int2 s = make_int2(0, 0);
-    for (int i = 0; i < kWarps; ++i) s.x += warp_gt[i], s.y += warp_eq[i];
+    for (int i = 0; i < kWarps; ++i) s.x += warp_counts[i].x, s.y += warp_counts[i].y;
     counts = s;
   }
   cluster.sync();  // also: every slice has been read
-  int base = 0, take = want;  // places before this slice; of its equal ones the first `take` stay
-  for (int c = 0; c < rank; ++c) {
-    const int2 s = *cluster.map_shared_rank(&counts, c);
+  int base = 0, take = want;  // places before this stretch; of its equal ones the first `take` stay
+  auto pass_over = [&](int2 s) {
     base += s.x + min(s.y, take);
     take -= min(s.y, take);
-  }
+  };
+  for (int c = 0; c < rank; ++c) pass_over(*cluster.map_shared_rank(&counts, c));
+  for (int v = 0; v < warp; ++v) pass_over(warp_counts[v]);
 
   // ---- positions in order, and the weights behind them ----
-  for (int i0 = 0; i0 < mine; i0 += kThreads) {
-    const int i = i0 + tid;
-    const float x = i < mine ? w[i] : 0.f;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const float x = i < w1 ? w[i] : 0.f;
     const uint32_t k = order_of(x);
-    const bool is_gt = i < mine && k > prefix, is_eq = i < mine && k == prefix;
+    const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-    __syncthreads();  // the counts of the chunk before are read
-    if (lane == 0) warp_gt[warp] = __popc(bg), warp_eq[warp] = __popc(be);
-    __syncthreads();
-    int g0 = 0, e0 = 0, gs = 0, es = 0;
-#pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-      const int x0 = warp_gt[v], x1 = warp_eq[v];
-      if (v < warp) g0 += x0, e0 += x1;
-      gs += x0, es += x1;
-    }
     const uint32_t below = (1u << lane) - 1u;
-    const int g = g0 + __popc(bg & below), e = e0 + __popc(be & below);
+    const int g = __popc(bg & below), e = __popc(be & below);
     if (is_gt || (is_eq && e < take)) {
       const int at = base + g + min(e, take);
       p.keep[c0 + at] = lo + i;
       if (cached) row[a + at] = x;
     }
-    base += gs + min(es, take);
-    take -= min(es, take);
+    pass_over(make_int2(__popc(bg), __popc(be)));
   }
   for (int j = rank * kThreads + tid; j < late; j += C * kThreads) p.keep[c0 + need + j] = last + j;
   if (cached) {
