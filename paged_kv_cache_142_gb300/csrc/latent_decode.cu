@@ -52,20 +52,22 @@ constexpr int kTile = 64;                      // tokens
 constexpr int kLatBytes = kTile * 512;         // [8-token group][4 chunks of 64 columns][8 rows x 128 bytes]
 constexpr int kRopeBytes = kTile * 64;         // [8-token group][8 rows x 64 bytes]
 constexpr int kStageBytes = kLatBytes + kRopeBytes;
-constexpr int kPBytes = 128 * 128;             // [half of the tokens][128 rows x 32 bf16]
-constexpr int kXBytes = 128 * kTile * 4;       // the other CTA's partial sums: [half of the tokens][4-token group][row][4]
+__host__ __device__ constexpr int p_bytes(bool narrow) { return (narrow ? 32 : 128) * 128; }  // [half of the tokens][rows x 32 bf16]
+// the other CTA's partial sums: [half of the tokens][4-token group][row][4]
+__host__ __device__ constexpr int x_bytes(bool narrow) { return (narrow ? 32 : 128) * kTile * 4; }
 constexpr uint32_t kColQ = 256, kColS = 400;   // tensor memory: O at 0
 constexpr float kSlack = 8.f;
 constexpr int kLead = 3;      // what starting and ending an item costs a cluster, in tiles
 constexpr int kMaxSeqs = 2048;  // of one launch: their places lie in shared memory
 constexpr int kMinTiles = 4;  // of a cluster's run, where there are enough clusters
 
-__host__ __device__ constexpr int stages_of(bool hi) { return hi ? 3 : 4; }
+// narrow: at most 32 rows, whose probabilities and sums leave room for another tile
+__host__ __device__ constexpr int stages_of(bool hi, bool narrow) { return narrow ? 5 : hi ? 3 : 4; }
 
-// barriers ([2] or [4] each where they have a number)
+// barriers
 enum : int {
-  kFull = 0, kEmpty = 4, kQFull = 8, kSFree = 9, kSFull = 10, kXFull = 12, kXFree = 14, kPFull = 16, kPFree = 18,
-  kODone = 20, kOFree = 22, kDrain = 23, kRef = 25, kNumBars = 33  // kRef: [group][quarter of the rows]
+  kFull = 0, kEmpty = 5, kQFull = 10, kSFree = 11, kSFull = 12, kXFull = 14, kXFree = 16, kPFull = 18, kPFree = 20,
+  kODone = 22, kOFree = 24, kDrain = 25, kRef = 27, kNumBars = 35  // kRef: [group][quarter of the rows]
 };
 // shared memory, behind the stages: P slots, the exchange, then
 constexpr int kOffBar = 0;
@@ -136,16 +138,22 @@ struct Walk {
     }
     derive(it);
   }
-  // calls f for every item with tiles of this cluster's
+  // calls f(item, the one behind it, whether there is one) for every item with tiles of this cluster's
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    Item it;
-    it.end = c_begin;
-    for (bool more = c_begin < c_end; more;) {
-      if (it.end == c_begin) find(it);
-      else next(it);
-      more = it.end < c_end;
-      if (it.t1 > it.t0) f(it);
+    if (c_begin >= c_end) return;
+    Item it, nxt;
+    find(it);
+    for (;;) {
+      bool more = it.end < c_end;
+      nxt = it;
+      if (more) {
+        next(nxt);
+        more = nxt.t1 > nxt.t0;
+      }
+      if (it.t1 > it.t0) f(it, nxt, more);
+      if (!more) return;
+      it = nxt;
     }
   }
 };
@@ -172,16 +180,17 @@ __device__ __forceinline__ void store16(const LatentDecodeParams& p, int64_t at,
   }
 }
 
-template <bool HI>
+template <bool HI, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_lat,
                   const __grid_constant__ CUtensorMap tm_rope) {
-  constexpr int kStages = stages_of(HI), kParts = HI ? 2 : 1;
+  constexpr int kStages = stages_of(HI, NARROW), kParts = HI ? 2 : 1, kRows = NARROW ? 32 : 128;
+  constexpr int kPBytes = p_bytes(NARROW), kXBytes = x_bytes(NARROW);
   const LatentDecodeParams& p = L.p;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* smem_p = smem + kStages * kStageBytes;              // [2 slots][parts][128 rows]
+  unsigned char* smem_p = smem + kStages * kStageBytes;              // [2 slots][parts]; of fewer than 128 rows the products read on, into rows of nobody's
   unsigned char* smem_x = smem_p + 2 * kParts * kPBytes;
   unsigned char* rest = smem_x + kXBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(rest + kOffBar);
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::prefetch_tensormap(&tm_lat);
       ptx::prefetch_tensormap(&tm_rope);
     }
-    walk.each([&](const Item& it) {
+    walk.each([&](const Item& it, const Item&, bool) {
       const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
       const int kend = seen_by(L, it, min(L.rows, it.rt * 128 + 128) - 1);  // nobody sees what lies behind it
       auto row_of = [&](int t) -> int {  // the page's first row in the pool, in 8-row groups; -1: nothing to load
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc_k = ptx::smem_desc(smem, 16, 4096, ptx::kLayoutSw128);
     const uint64_t desc_r = ptx::smem_desc(smem + kLatBytes, 16, 512, kLayoutSw64);
     uint32_t kt = 0, items = 0;
-    walk.each([&](const Item& it) {
+    walk.each([&](const Item& it, const Item&, bool) {
       const int kend = seen_by(L, it, min(L.rows, it.rt * 128 + 128) - 1);
       for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
         const uint32_t slot = kt % kStages;
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc_v = ptx::smem_desc(smem, 1024, 4096, ptx::kLayoutSw128);
     const uint64_t desc_p = ptx::smem_desc(smem_p, 16, 512, kLayoutSw64);
     uint32_t kt = 0, items = 0;
-    walk.each([&](const Item& it) {
+    walk.each([&](const Item& it, const Item&, bool) {
       for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
         const uint32_t slot = kt & 1u;
         if (t == it.t0) wait(&bars[kOFree], (items & 1u) ^ 1u, aborted);
@@ -414,8 +423,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto everybody = [&]() { ptx::bar_sync(9, L.quarters * 128); };
     const int quad = 2 * static_cast<int>(group) + half;  // a quarter of the columns of Q and O
     uint32_t kt = 0;
+    bool first = true;
     const float f = p.scale_log2;
-    walk.each([&](const Item& it) {
+    // an item's queries into tensor memory, once all scores of the item before are formed
+    auto load_queries = [&](const Item& it) {
+      const int row = it.rt * 128 + r;
+      const bool valid = row < L.rows;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                        (static_cast<int64_t>(it.seq) * L.rows + row) * 576);
+      uint32_t v[32];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint4 x = valid ? __ldg(src + rank * 32 + quad * 8 + e) : make_uint4(0, 0, 0, 0);
+        v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+      }
+      const uint4 y = valid ? __ldg(src + 64 + rank * 4 + quad) : make_uint4(0, 0, 0, 0);
+      ptx::tmem_st32(tmem + lanes + kColQ + quad * 32, v);
+      asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tmem + lanes + kColQ + 128 + quad * 4),
+                   "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                   : "memory");
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
+    };
+    walk.each([&](const Item& it, const Item& nxt, bool more) {
       const int row = it.rt * 128 + r;
       const bool valid = row < L.rows;
       const int last_row = min(L.rows, it.rt * 128 + 128) - 1;
@@ -423,24 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int limit_min = seen_by(L, it, it.rt * 128), limit_max = seen_by(L, it, last_row);
       const int64_t out_row = static_cast<int64_t>(it.seq) * L.rows + row;
       const uint32_t k1 = kt + (it.t1 - it.t0);  // behind the last tile
-      // ---- queries into tensor memory: all products of the item before are complete ----
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + out_row * 576);
-        uint32_t v[32];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 x = valid ? __ldg(src + rank * 32 + quad * 8 + e) : make_uint4(0, 0, 0, 0);
-          v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+      if (first) load_queries(it);
+      first = false;
+      if (more) {  // the next item's queries, on their way
+        const int nrow = nxt.rt * 128 + r;
+        const char* src = static_cast<const char*>(p.q) + (static_cast<int64_t>(nxt.seq) * L.rows + nrow) * 1152;
+        if (nrow < L.rows) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + rank * 512 + quad * 128));
+          if (quad == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 1024 + rank * 64));
         }
-        const uint4 y = valid ? __ldg(src + 64 + rank * 4 + quad) : make_uint4(0, 0, 0, 0);
-        ptx::tmem_st32(tmem + lanes + kColQ + quad * 32, v);
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tmem + lanes + kColQ + 128 + quad * 4),
-                     "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                     : "memory");
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
       }
       float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens, on the reference m
       // (a warp that gave up goes on, without waiting, to meet the others at the named barriers)
@@ -461,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = remote(smem_x + half * (kXBytes / 2), peer), bar = remote(&bars[kXFull + group], peer);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            store_async4(dst + (j * 128 + r) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
+            store_async4(dst + (j * kRows + r) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
                          __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
         }
         if (r == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], L.quarters * 32 * kTile * 4);
@@ -487,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float x[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float4 y = *reinterpret_cast<const float4*>(smem_x + half * (kXBytes / 2) + (j * 128 + r) * 16);
+          const float4 y = *reinterpret_cast<const float4*>(smem_x + half * (kXBytes / 2) + (j * kRows + r) * 16);
           x[4 * j] = (__uint_as_float(s[4 * j]) + y.x) * f;
           x[4 * j + 1] = (__uint_as_float(s[4 * j + 1]) + y.y) * f;
           x[4 * j + 2] = (__uint_as_float(s[4 * j + 2]) + y.z) * f;
@@ -572,9 +595,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0 && !aborted) ptx::mbar_arrive(&bars[kPFull + group]);
       }
+      const uint32_t kl = k1 - 1;
+      if (more) {  // the next item's scores begin beside this one's last product and outputs
+        wait(&bars[kSFull + (kl & 1u)], (kl >> 1) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        ptx::tc_fence_after();
+        load_queries(nxt);
+      }
       // ---- the rows' sums, then the outputs ----
       everybody();
-      const uint32_t kl = k1 - 1;
       const float last = refs[(kl & 1u) * 128 + r];
       if (m != last) l *= fp4::fast_exp2(m - last);
       m = last;
@@ -692,8 +721,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
   }
 }
 
-int smem_bytes(bool hi, int seqs) {
-  return 1024 + stages_of(hi) * kStageBytes + 2 * (hi ? 2 : 1) * kPBytes + kXBytes + kOffPrefix +
+int smem_bytes(bool hi, bool narrow, int seqs) {
+  return 1024 + stages_of(hi, narrow) * kStageBytes + 2 * (hi ? 2 : 1) * p_bytes(narrow) + x_bytes(narrow) + kOffPrefix +
          (seqs + 64) / 64 * 256;
 }
 
@@ -760,8 +789,12 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
     L.desc = reinterpret_cast<int4*>(p.ws + 256);
     L.ml = reinterpret_cast<float*>(p.ws + 256 + (static_cast<int64_t>(n) * 16 + 255) / 256 * 256);
     L.o = L.ml + static_cast<int64_t>(2) * n * L.part_rows * 2;
-    const int smem = smem_bytes(hi, L.p.num_seqs);
-    const void* fn = hi ? reinterpret_cast<const void*>(&decode_kernel<true>) : reinterpret_cast<const void*>(&decode_kernel<false>);
+    const bool narrow = rows <= 32;
+    const int smem = smem_bytes(hi, narrow, L.p.num_seqs);
+    const void* fn = narrow ? (hi ? reinterpret_cast<const void*>(&decode_kernel<true, true>)
+                                  : reinterpret_cast<const void*>(&decode_kernel<false, true>))
+                            : (hi ? reinterpret_cast<const void*>(&decode_kernel<true, false>)
+                                  : reinterpret_cast<const void*>(&decode_kernel<false, false>));
     int per_sm = 0;
     cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
     if (e != cudaSuccess) return e;
