@@ -57,8 +57,8 @@ __host__ __device__ constexpr int p_bytes(bool narrow) { return (narrow ? 32 : 1
 __host__ __device__ constexpr int x_bytes(bool narrow) { return (narrow ? 32 : 128) * kTile * 4; }
 constexpr uint32_t kColQ = 256, kColS = 400;   // tensor memory: O at 0
 constexpr float kSlack = 8.f;
-constexpr int kLead = 3;      // what starting and ending an item costs a cluster, in tiles
 constexpr int kMaxSeqs = 2048;  // of one launch: their places lie in shared memory
+constexpr int kMostLead = 8;
 constexpr int kMinTiles = 4;  // of a cluster's run, where there are enough clusters
 
 // narrow: at most 32 rows, whose probabilities and sums leave room for another tile
@@ -81,6 +81,7 @@ struct Launch {
   int quarters;          // of the 128 rows that any tile has
   int bs_log, part_rows;
   int num_clusters;
+  int lead;              // what starting and ending an item costs a cluster, in tiles: places before its first
   int4* desc;            // [clusters] the item that a cluster's run begins inside of: sequence (or -1), row tile, first and last cluster
   float* ml;             // [2 * clusters][part_rows][2] maximum (log2), sum
   float* o;              // [2 * clusters][part_rows][512]
@@ -89,7 +90,7 @@ struct Launch {
 // An item (a row tile of a sequence) and this cluster's part of it.
 struct Item {
   int seq, rt, len, tiles;
-  int start, end;  // places: kLead, then the tiles
+  int start, end;  // places: the lead's, then the tiles'
   int t0, t1;
   bool whole;
 };
@@ -103,8 +104,8 @@ struct Walk {
     return n > 0 && n <= L.p.max_context_len ? n : 0;
   }
   __device__ __forceinline__ void derive(Item& it) const {
-    it.end = it.start + kLead + it.tiles;
-    const int first = it.start + kLead;
+    it.end = it.start + L.lead + it.tiles;
+    const int first = it.start + L.lead;
     it.t0 = max(c_begin, first) - first;
     it.t1 = min(c_end, it.end) - first;
     it.whole = it.t0 == 0 && it.t1 == it.tiles;
@@ -124,8 +125,8 @@ struct Walk {
     it.seq = lo;
     open(it);
     const int r = c_begin - prefix[lo];
-    it.rt = r / (kLead + it.tiles);
-    it.start = c_begin - r % (kLead + it.tiles);
+    it.rt = r / (L.lead + it.tiles);
+    it.start = c_begin - r % (L.lead + it.tiles);
     derive(it);
   }
   __device__ __forceinline__ void next(Item& it) const {
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = beg; s < end; ++s) {
       const int n = p.context_lens[s];
       int places = 0;
-      if (n > 0 && n <= p.max_context_len) places = (kLead + (n + kTile - 1) / kTile) * L.row_tiles;
+      if (n > 0 && n <= p.max_context_len) places = (L.lead + (n + kTile - 1) / kTile) * L.row_tiles;
       else if (n != 0 && blockIdx.x == 0) atomicExch(p.err, kDevErrInvalidArg);
       prefix[s + 1] = places;
       local += places;
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.t0 > 0 && rank == 0 && tid == 0) {
         const int wide = extra * (share + 1);
         auto cluster_of = [&](int u) { return u < wide ? u / (share + 1) : extra + (u - wide) / share; };
-        L.desc[cluster] = make_int4(it.seq, it.rt, cluster_of(it.start + kLead), cluster_of(it.end - 1));
+        L.desc[cluster] = make_int4(it.seq, it.rt, cluster_of(it.start + L.lead), cluster_of(it.end - 1));
       }
     });
   }
@@ -728,7 +729,7 @@ int smem_bytes(bool hi, bool narrow, int seqs) {
 
 // Sequences of one launch: their places fit an int.  0: not even one's do.
 int seqs_of(int num_seqs, int64_t row_tiles, int max_context_len) {
-  const int64_t places = (kLead + (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile) * row_tiles;
+  const int64_t places = (kMostLead + (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile) * row_tiles;
   const int64_t fit = ((int64_t(1) << 31) - 1) / places;
   const int64_t most = fit < kMaxSeqs ? fit : kMaxSeqs;
   return static_cast<int>(num_seqs < most ? num_seqs : most);
@@ -782,6 +783,9 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
     L.quarters = row_tiles > 1 ? 4 : static_cast<int>((rows + 31) / 32);
     L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
     L.part_rows = part_rows_of(rows);
+    // 16 rows: 4 tiles (71 us the batch of 256; 3: 71, 6: 73, 8: 75); 128 rows, whose outputs and queries are
+    // eight times as much: 7 (batch of 64: 74 us; 3: 81, 5: 75)
+    L.lead = 4 + 3 * L.part_rows / 128;
     // every SM, while a cluster gets a few tiles
     const int64_t tiles = static_cast<int64_t>(L.p.num_seqs) * row_tiles * ((static_cast<int64_t>(p.max_context_len) + kTile - 1) / kTile);
     const int64_t want = (tiles + kMinTiles - 1) / kMinTiles;

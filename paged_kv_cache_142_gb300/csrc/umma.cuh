@@ -84,11 +84,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Columns of this warp's lanes, loaded and waited for in one statement.  The load
-// writes its registers when it completes, not when it is issued: between it and a
-// wait of its own the compiler may spill them and use them for something else,
-// which the load then overwrites (in a kernel that spills, with addresses in
-// them, that has been a fault).
+// Columns of this warp's lanes, loaded and waited for in one statement: the load
+// writes its registers when it completes, not when it is issued, and nothing that
+// uses them may come between it and its wait.
 __device__ __forceinline__ void load_now(uint32_t at, uint32_t (&v)[16]) {
   asm volatile(
       "{\n\ttcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
