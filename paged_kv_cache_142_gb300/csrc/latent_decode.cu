@@ -26,13 +26,24 @@
 // borders of sequences; a cluster that takes part of an item leaves its rows
 // unnormalised in the workspace, and a second kernel adds the parts up.
 //
-// One CTA per SM, 19 warps: 0-7 and 8-15 scores and outputs of every other tile
-// (half of a row's tokens a thread; warps without rows do nothing), 16 loads, 17
-// and 18 issue the products of S and of O (one warp for both would hold back the
-// next S while it waits for P).  A tile's chain (scores, exchange, maximum,
-// probabilities) takes 2000 clocks, nearly all of them latency, whatever the
-// width: so two tiles are in it at a time, and only the reference passes from one
-// group to the other.
+// One CTA per SM, 19 warps: 0-15 scores and outputs, 16 loads, 17 and 18 issue
+// the products of S and of O (one warp for both would hold back the next S while
+// it waits for P).  A tile's chain (scores, exchange, maximum, probabilities)
+// takes 2000 clocks, nearly all of them latency, whatever the width: so several
+// tiles are in it at a time, and only the reference passes from one group of
+// warps to the next.  More than 32 rows: two groups of eight warps, half of a
+// row's tokens a thread; a warp whose rows nobody has does nothing.  At most 32
+// rows would leave three quarters of tensor memory, and so of the warps (a warp
+// reaches the lanes of its own quarter), without work: there the queries stand
+// in all four quarters, each of the last three has every third tile's scores, a
+// quarter of a row's tokens a thread, and the first's warps keep the outputs
+// (16 rows, batch of 256 with 900 tokens or so: 64 us; two groups of two warps: 71).
+//
+// Measured: the batch of 256 with 16 heads reads 259 MB in 64 us, 4.0 TB/s (60%
+// of a plain copy): what is left is the start and the end of an item, where the
+// chain has fewer tiles than it could.  The batch of 64 with 128 heads takes 73 us
+// (2.3 TB/s, 500 TFLOP/s): the exchange of 32 KB of partial sums a tile and the
+// merge of the parts (10 us) bound it.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -62,17 +73,19 @@ constexpr int kMostLead = 8;
 constexpr int kMinTiles = 4;  // of a cluster's run, where there are enough clusters
 
 // narrow: at most 32 rows, whose probabilities and sums leave room for another tile
+// and whose scores every quarter of tensor memory can have (see below)
+__host__ __device__ constexpr int groups_of(bool narrow) { return narrow ? 3 : 2; }
 __host__ __device__ constexpr int stages_of(bool hi, bool narrow) { return narrow ? 5 : hi ? 3 : 4; }
 
 // barriers
 enum : int {
-  kFull = 0, kEmpty = 5, kQFull = 10, kSFree = 11, kSFull = 12, kXFull = 14, kXFree = 16, kPFull = 18, kPFree = 20,
-  kODone = 22, kOFree = 24, kDrain = 25, kRef = 27, kNumBars = 35  // kRef: [group][quarter of the rows]
+  kFull = 0, kEmpty = 5, kQFull = 10, kSFree = 11, kSFull = 12, kXFull = 15, kXFree = 18, kPFull = 21, kPFree = 24,
+  kODone = 27, kOFree = 30, kDrain = 31, kLFull = 33, kLFree = 34, kRef = 35, kNumBars = 43
 };
 // shared memory, behind the stages: P slots, the exchange, then
 constexpr int kOffBar = 0;
-constexpr int kOffTops = 512;                  // [2 turns][group][half][128] maxima of half a row
-constexpr int kOffRefs = kOffTops + 4096;      // [group][128] the rows' references
+constexpr int kOffTops = 512;                  // [2 turns][group][part of the tokens][rows] maxima of a part of a row
+constexpr int kOffRefs = kOffTops + 4096;      // [group][rows] the rows' references
 constexpr int kOffPrefix = kOffRefs + 1024;
 
 struct Launch {
@@ -186,19 +199,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_lat,
                   const __grid_constant__ CUtensorMap tm_rope) {
   constexpr int kStages = stages_of(HI, NARROW), kParts = HI ? 2 : 1, kRows = NARROW ? 32 : 128;
+  constexpr uint32_t kGroups = groups_of(NARROW);  // tiles in the chain of scores and probabilities
   constexpr int kPBytes = p_bytes(NARROW), kXBytes = x_bytes(NARROW);
   const LatentDecodeParams& p = L.p;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* smem_p = smem + kStages * kStageBytes;              // [2 slots][parts]; of fewer than 128 rows the products read on, into rows of nobody's
-  unsigned char* smem_x = smem_p + 2 * kParts * kPBytes;
+  // [groups][parts]; of fewer than 128 rows the products read on, into rows of nobody's
+  unsigned char* smem_p = smem + kStages * kStageBytes;
+  unsigned char* smem_x = smem_p + kGroups * kParts * kPBytes;
   unsigned char* rest = smem_x + kXBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(rest + kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* tops = reinterpret_cast<float*>(rest + kOffTops);
-  float* refs = reinterpret_cast<float*>(rest + kOffRefs);
+  float* refs = NARROW ? tops + 768 : reinterpret_cast<float*>(rest + kOffRefs);
+  float* sums = tops + 864;  // narrow: [group][part of the tokens][32], up to kOffPrefix
   int* prefix = reinterpret_cast<int*>(rest + kOffPrefix);
   __shared__ int warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -211,19 +227,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kFull + i], 1);
       ptx::mbar_init(&bars[kEmpty + i], 1);
     }
-    const int warps = 2 * L.quarters;  // of a group
-    ptx::mbar_init(&bars[kQFull], 2 * warps);
+    const int warps = NARROW ? 4 : 2 * L.quarters;  // of a group
+    ptx::mbar_init(&bars[kQFull], kGroups * warps);
     ptx::mbar_init(&bars[kSFree], warps);
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < kGroups; ++i) {
       ptx::mbar_init(&bars[kSFull + i], 1);
       ptx::mbar_init(&bars[kXFull + i], 1);
       ptx::mbar_init(&bars[kXFree + i], warps);
-      ptx::mbar_init(&bars[kPFull + i], warps);
+      ptx::mbar_init(&bars[kPFull + i], NARROW ? 8 : warps);
       ptx::mbar_init(&bars[kPFree + i], 1);
       ptx::mbar_init(&bars[kODone + i], 1);
     }
-    ptx::mbar_init(&bars[kOFree], 2 * warps);
-    for (int i = 0; i < 8; ++i) ptx::mbar_init(&bars[kRef + i], 2);
+    ptx::mbar_init(&bars[kOFree], NARROW ? 4 : 2 * warps);
+    ptx::mbar_init(&bars[kLFull], 12);
+    ptx::mbar_init(&bars[kLFree], 4);
+    for (int i = 0; i < 8; ++i) ptx::mbar_init(&bars[kRef + i], NARROW ? 4 : 2);
     ptx::mbar_init(&bars[kDrain], 1);
     ptx::mbar_init(&bars[kDrain + 1], 1);
     *gave_up = 0;
@@ -287,6 +305,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (late) aborted = true;
     }
     aborted = __any_sync(0xffffffffu, aborted);
+  };
+
+  // a quarter of an item's queries into tensor memory, once all scores of the item before are formed
+  auto load_queries = [&](const Item& it, uint32_t lanes, int r, int quad) {
+    const int row = it.rt * 128 + r;
+    const bool valid = row < L.rows;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                      (static_cast<int64_t>(it.seq) * L.rows + row) * 576);
+    uint32_t v[32];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint4 x = valid ? __ldg(src + rank * 32 + quad * 8 + e) : make_uint4(0, 0, 0, 0);
+      v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+    }
+    const uint4 y = valid ? __ldg(src + 64 + rank * 4 + quad) : make_uint4(0, 0, 0, 0);
+    ptx::tmem_st32(tmem + lanes + kColQ + quad * 32, v);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tmem + lanes + kColQ + 128 + quad * 4),
+                 "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                 : "memory");
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
+  };
+  // the next item's queries, on their way
+  auto fetch_queries = [&](const Item& it, int r, int quad) {
+    const int row = it.rt * 128 + r;
+    const char* src = static_cast<const char*>(p.q) + (static_cast<int64_t>(it.seq) * L.rows + row) * 1152;
+    if (row < L.rows) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + rank * 512 + quad * 128));
+      if (quad == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 1024 + rank * 64));
+    }
+  };
+  // a quarter of the columns of a row's outputs: normalised, or as a part
+  auto put_out = [&](const Item& it, int r, int quad, float m, float l) {
+    const int row = it.rt * 128 + r;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t out_row = static_cast<int64_t>(it.seq) * L.rows + row;
+    const int64_t part = (static_cast<int64_t>(cluster) * 2 + (it.t0 > 0 ? 0 : 1)) * L.part_rows + r;
+    const bool store = row < L.rows && r < L.part_rows;
+    if (!it.whole && rank == 0 && store && quad == 0) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      uint32_t v[32];
+      load_now(tmem + lanes + quad * 64 + c * 32, v);
+      if (c == 1) {  // O is read: the next item's P V may write it
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kOFree]);
+      }
+      if (!store) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float y[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[16 * h + j]);
+        const int64_t col = static_cast<int64_t>(rank) * 256 + quad * 64 + c * 32 + h * 16;
+        if (it.whole) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = inv != 0.f ? y[j] * inv : 0.f;
+          store16(p, out_row * 512 + col, y);
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
+            fp4::store32(L.o + part * 512 + col + 8 * q, w);
+          }
+        }
+      }
+    }
+    // a cluster that begins inside an item's tiles reports it
+    if (it.t0 > 0 && rank == 0 && tid == 0) {
+      const int wide = extra * (share + 1);
+      auto cluster_of = [&](int u) { return u < wide ? u / (share + 1) : extra + (u - wide) / share; };
+      L.desc[cluster] = make_int4(it.seq, it.rt, cluster_of(it.start + L.lead), cluster_of(it.end - 1));
+    }
   };
 
   if (warp == 16) {
@@ -373,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_ts(tmem + kColS, tmem + kColQ + j * 8, dk + (j >> 2) * (1024 >> 4) + (j & 3) * 2, kIdS, j > 0);
 #pragma unroll
           for (int j = 0; j < 2; ++j) umma_ts(tmem + kColS, tmem + kColQ + 128 + j * 8, dr + j * 2, kIdS, 1);
-          ptx::umma_commit(&bars[kSFull + (kt & 1u)]);
+          ptx::umma_commit(&bars[kSFull + kt % kGroups]);
         }
         __syncwarp();
       }
@@ -389,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kt = 0, items = 0;
     walk.each([&](const Item& it, const Item&, bool) {
       for (int t = it.t0; t < it.t1 && !aborted; ++t, ++kt) {
-        const uint32_t slot = kt & 1u;
+        const uint32_t slot = kt % kGroups;
         if (t == it.t0) wait(&bars[kOFree], (items & 1u) ^ 1u, aborted);
-        wait(&bars[kPFull + slot], (kt >> 1) & 1u, aborted);
+        wait(&bars[kPFull + slot], (kt / kGroups) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) return;
         ptx::tc_fence_after();
@@ -413,7 +510,195 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
     });
     drain(kDrain, leader);
-  } else if ((warp & 3) < L.quarters) {
+  } else if (NARROW && (warp & 3) == 0) {
+    // ========= outputs of few rows: references, then a quarter of the columns =========
+    // Lanes 0-31 hold the rows' outputs; the lanes of the other quarters of tensor
+    // memory have the same rows' scores, a tile each.
+    const int part = warp >> 2;
+    uint32_t kt = 0, items = 0;
+    walk.each([&](const Item& it, const Item&, bool) {
+      const uint32_t k1 = kt + (it.t1 - it.t0);
+      float m = -CUDART_INF_F;
+      for (uint32_t k = kt; k < k1 && !aborted; ++k) {
+        const uint32_t g = k % kGroups;
+        wait(&bars[kRef + g], (k / kGroups) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (aborted) break;
+        const float now = refs[g * 32 + lane];
+        const float alpha = now != m ? fp4::fast_exp2(m - now) : 1.f;
+        m = now;
+        if (k > kt && __any_sync(0xffffffffu, alpha != 1.f)) {
+          const uint32_t b = (k - 1) % kGroups;
+          wait(&bars[kODone + b], ((k - 1) / kGroups) & 1u, aborted);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (aborted) break;
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32];
+            load_now(tmem + part * 64 + c * 32, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+            ptx::tmem_st32(tmem + part * 64 + c * 32, v);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kPFull + g]);
+      }
+      const uint32_t kl = k1 - 1;
+      kt = k1;
+      wait(&bars[kLFull], items & 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      float l = 0.f;
+#pragma unroll
+      for (int i = 0; i < 12; ++i) l += sums[i * 32 + lane];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars[kLFree]);
+      ++items;
+      wait(&bars[kODone + kl % kGroups], (kl / kGroups) & 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      if (aborted) return;
+      ptx::tc_fence_after();
+      put_out(it, lane, part, m, l);
+    });
+  } else if (NARROW && warp < 16) {
+    // ===== scores of few rows: every third tile, a quarter of a row's tokens per thread =====
+    const uint32_t group = static_cast<uint32_t>(warp & 3) - 1;  // the tiles k = group mod 3
+    const int part = warp >> 2, r = lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    auto all_parts = [&]() { ptx::bar_sync(1 + static_cast<int>(group), 128); };
+    uint32_t kt = 0, items = 0;
+    bool first = true;
+    const float f = p.scale_log2;
+    walk.each([&](const Item& it, const Item& nxt, bool more) {
+      const int row = it.rt * 128 + r;
+      const int limit = row < L.rows ? seen_by(L, it, row) : 0;
+      const int limit_min = seen_by(L, it, it.rt * 128), limit_max = seen_by(L, it, L.rows - 1);
+      const uint32_t k1 = kt + (it.t1 - it.t0);  // behind the last tile
+      if (first) load_queries(it, lanes, r, part);
+      first = false;
+      if (more) fetch_queries(nxt, r, part);
+      float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens, on the reference m
+      // (a warp that gave up goes on, without waiting, to meet the others at the named barriers)
+      for (uint32_t k = kt + (group + 2 * kt) % kGroups; k < k1; k += kGroups) {
+        const uint32_t ph = (k / kGroups) & 1u, before_g = (group + 2) % kGroups;
+        const int t = it.t0 + static_cast<int>(k - kt);
+        wait(&bars[kSFull + group], ph, aborted);
+        if (k > 0) wait(&bars[kXFree + before_g], ((k - 1) / kGroups) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        ptx::tc_fence_after();
+        uint32_t s[16];
+        load_now(tmem + lanes + kColS + part * 16, s);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kSFree]);
+        if (!aborted) {
+          const uint32_t dst = remote(smem_x + part * (kXBytes / 4), peer), bar = remote(&bars[kXFull + group], peer);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            store_async4(dst + (j * 32 + r) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
+                         __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
+        }
+        if (r == 0 && part == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], kXBytes);
+        if (limit_min < limit_max && limit_min < (t + 1) * kTile) {  // as below
+          uint32_t odd = 0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= 1u << j;
+          odd = __shfl_sync(0xffffffffu, odd, 0);
+          const int from = max(0, limit_min - t * kTile - part * 16), upto = min(16, limit_max - t * kTile - part * 16);
+          unsigned char* stage = smem + (k % kStages) * kStageBytes + part * 2 * 4096;
+          for (int j = from; j < upto; ++j)
+            if ((odd >> j) & 1u)
+              *reinterpret_cast<uint4*>(stage + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+        }
+        wait(&bars[kXFull + group], ph, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 y = *reinterpret_cast<const float4*>(smem_x + part * (kXBytes / 4) + (j * 32 + r) * 16);
+          x[4 * j] = (__uint_as_float(s[4 * j]) + y.x) * f;
+          x[4 * j + 1] = (__uint_as_float(s[4 * j + 1]) + y.y) * f;
+          x[4 * j + 2] = (__uint_as_float(s[4 * j + 2]) + y.z) * f;
+          x[4 * j + 3] = (__uint_as_float(s[4 * j + 3]) + y.w) * f;
+        }
+        const int nvis = limit - t * kTile - part * 16;
+        if (!__all_sync(0xffffffffu, nvis >= 16)) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j >= nvis) x[j] = -CUDART_INF_F;
+        }
+        float top = fmaxf(x[0], x[1]);
+#pragma unroll
+        for (int j = 2; j < 16; j += 2) top = max3(top, x[j], x[j + 1]);
+        __syncwarp();  // every lane has read its sums
+        if (lane == 0 && !aborted) remote_arrive(remote(&bars[kXFree + group], peer), top);
+        float* four = tops + ((ph * kGroups + group) * 4) * 32 + r;
+        four[part * 32] = top;
+        all_parts();
+        top = fmaxf(fmaxf(four[0], four[32]), fmaxf(four[64], four[96]));
+        float before = -CUDART_INF_F;  // the reference of the tile before, which another group had
+        if (k > kt) wait(&bars[kRef + before_g], ((k - 1) / kGroups) & 1u, aborted);
+        // this group's P, and its references, are free once P V of its tile before is complete
+        wait(&bars[kPFree + group], ph ^ 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        if (k > kt) before = refs[before_g * 32 + r];
+        const bool raise = top > before + kSlack || (before == -CUDART_INF_F && top > before);
+        const float now = raise ? top : before;
+        if (part == 0) refs[group * 32 + r] = now;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kRef + group]);
+        if (m != now) l *= fp4::fast_exp2(m - now);
+        m = now;
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        if (aborted) continue;
+        unsigned char* prow = smem_p + group * kParts * kPBytes + (part >> 1) * (kPBytes / 2) + (r >> 3) * 512 + (r & 7) * 64;
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[4], w2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = fp4::fast_exp2(x[8 * c + 2 * e] - ref), b = fp4::fast_exp2(x[8 * c + 2 * e + 1] - ref);
+            sum0 += a;
+            sum1 += b;
+            w[e] = pack_bf16(a, b);
+            if (HI) w2[e] = pack_bf16(a - __uint_as_float(w[e] << 16), b - __uint_as_float(w[e] & 0xffff0000u));
+          }
+          const int at = (((part & 1) * 2 + c) ^ ((r >> 1) & 3)) << 4;
+          *reinterpret_cast<uint4*>(prow + at) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (HI) *reinterpret_cast<uint4*>(prow + kPBytes + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        }
+        l += sum0 + sum1;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars[kPFull + group]);
+      }
+      const uint32_t kl = k1 - 1;
+      if (more) {  // the next item's scores begin beside this one's last product and outputs
+        wait(&bars[kSFull + kl % kGroups], (kl / kGroups) & 1u, aborted);
+        aborted = __any_sync(0xffffffffu, aborted);
+        ptx::tc_fence_after();
+        load_queries(nxt, lanes, r, part);
+      }
+      // ---- the rows' sums, on the last reference ----
+      wait(&bars[kRef + kl % kGroups], (kl / kGroups) & 1u, aborted);
+      wait(&bars[kLFree], (items & 1u) ^ 1u, aborted);
+      aborted = __any_sync(0xffffffffu, aborted);
+      const float last = refs[(kl % kGroups) * 32 + r];
+      if (m != last) l *= fp4::fast_exp2(m - last);
+      sums[(group * 4 + part) * 32 + r] = l;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars[kLFull]);
+      kt = k1;
+      ++items;
+    });
+  } else if (!NARROW && (warp & 3) < L.quarters) {
     // ===== scores and outputs: every other tile, half of a row's tokens per thread =====
     const int r = tid & 127;  // row of the tile, tensor-memory lane
     const int half = (warp >> 2) & 1;
@@ -426,46 +711,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kt = 0;
     bool first = true;
     const float f = p.scale_log2;
-    // an item's queries into tensor memory, once all scores of the item before are formed
-    auto load_queries = [&](const Item& it) {
-      const int row = it.rt * 128 + r;
-      const bool valid = row < L.rows;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                        (static_cast<int64_t>(it.seq) * L.rows + row) * 576);
-      uint32_t v[32];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint4 x = valid ? __ldg(src + rank * 32 + quad * 8 + e) : make_uint4(0, 0, 0, 0);
-        v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
-      }
-      const uint4 y = valid ? __ldg(src + 64 + rank * 4 + quad) : make_uint4(0, 0, 0, 0);
-      ptx::tmem_st32(tmem + lanes + kColQ + quad * 32, v);
-      asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tmem + lanes + kColQ + 128 + quad * 4),
-                   "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                   : "memory");
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bars[kQFull]);
-    };
     walk.each([&](const Item& it, const Item& nxt, bool more) {
       const int row = it.rt * 128 + r;
       const bool valid = row < L.rows;
       const int last_row = min(L.rows, it.rt * 128 + 128) - 1;
       const int limit = valid ? seen_by(L, it, row) : 0;
       const int limit_min = seen_by(L, it, it.rt * 128), limit_max = seen_by(L, it, last_row);
-      const int64_t out_row = static_cast<int64_t>(it.seq) * L.rows + row;
       const uint32_t k1 = kt + (it.t1 - it.t0);  // behind the last tile
-      if (first) load_queries(it);
+      if (first) load_queries(it, lanes, r, quad);
       first = false;
-      if (more) {  // the next item's queries, on their way
-        const int nrow = nxt.rt * 128 + r;
-        const char* src = static_cast<const char*>(p.q) + (static_cast<int64_t>(nxt.seq) * L.rows + nrow) * 1152;
-        if (nrow < L.rows) {
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + rank * 512 + quad * 128));
-          if (quad == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 1024 + rank * 64));
-        }
-      }
+      if (more) fetch_queries(nxt, r, quad);
       float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens, on the reference m
       // (a warp that gave up goes on, without waiting, to meet the others at the named barriers)
       for (uint32_t k = kt + ((kt ^ group) & 1u); k < k1; k += 2) {
@@ -601,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&bars[kSFull + (kl & 1u)], (kl >> 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         ptx::tc_fence_after();
-        load_queries(nxt);
+        load_queries(nxt, lanes, r, quad);
       }
       // ---- the rows' sums, then the outputs ----
       everybody();
@@ -612,52 +867,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       everybody();
       l = (tops[r] + tops[128 + r]) + (tops[256 + r] + tops[384 + r]);
       everybody();  // read before the next tile writes there
-      const float inv = l != 0.f ? 1.f / l : 0.f;
       wait(&bars[kODone + (kl & 1u)], (kl >> 1) & 1u, aborted);
       aborted = __any_sync(0xffffffffu, aborted);
       kt = k1;
       if (aborted) return;
       ptx::tc_fence_after();
-      const int64_t part = (static_cast<int64_t>(cluster) * 2 + (it.t0 > 0 ? 0 : 1)) * L.part_rows + r;
-      const bool store = valid && r < L.part_rows;
-      if (!it.whole && rank == 0 && store && quad == 0) *reinterpret_cast<float2*>(L.ml + part * 2) = make_float2(m, l);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        load_now(tmem + lanes + quad * 64 + c * 32, v);
-        if (c == 1) {  // O is read: the next item's P V may write it
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars[kOFree]);
-        }
-        if (!store) continue;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float y[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[16 * h + j]);
-          const int64_t col = static_cast<int64_t>(rank) * 256 + quad * 64 + c * 32 + h * 16;
-          if (it.whole) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = inv != 0.f ? y[j] * inv : 0.f;
-            store16(p, out_row * 512 + col, y);
-          } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
-              fp4::store32(L.o + part * 512 + col + 8 * q, w);
-            }
-          }
-        }
-      }
-      // a cluster that begins inside an item's tiles reports it
-      if (it.t0 > 0 && rank == 0 && tid == 0) {
-        const int wide = extra * (share + 1);
-        auto cluster_of = [&](int u) { return u < wide ? u / (share + 1) : extra + (u - wide) / share; };
-        L.desc[cluster] = make_int4(it.seq, it.rt, cluster_of(it.start + L.lead), cluster_of(it.end - 1));
-      }
+      put_out(it, r, quad, m, l);
     });
   }
 
@@ -723,7 +938,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
 }
 
 int smem_bytes(bool hi, bool narrow, int seqs) {
-  return 1024 + stages_of(hi, narrow) * kStageBytes + 2 * (hi ? 2 : 1) * p_bytes(narrow) + x_bytes(narrow) + kOffPrefix +
+  return 1024 + stages_of(hi, narrow) * kStageBytes + groups_of(narrow) * (hi ? 2 : 1) * p_bytes(narrow) + x_bytes(narrow) + kOffPrefix +
          (seqs + 64) / 64 * 256;
 }
 
@@ -783,9 +998,9 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
     L.quarters = row_tiles > 1 ? 4 : static_cast<int>((rows + 31) / 32);
     L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
     L.part_rows = part_rows_of(rows);
-    // 16 rows: 4 tiles (71 us the batch of 256; 3: 71, 6: 73, 8: 75); 128 rows, whose outputs and queries are
-    // eight times as much: 7 (batch of 64: 74 us; 3: 81, 5: 75)
-    L.lead = 4 + 3 * L.part_rows / 128;
+    // 16 rows: 2 tiles (64 us the batch of 256; 3: 64, 4: 66, 6: 70); 128 rows, whose outputs and queries are
+    // eight times as much: 7 (batch of 64: 73 us; 3: 81, 5: 75)
+    L.lead = 2 + 5 * L.part_rows / 128;
     // every SM, while a cluster gets a few tiles
     const int64_t tiles = static_cast<int64_t>(L.p.num_seqs) * row_tiles * ((static_cast<int64_t>(p.max_context_len) + kTile - 1) / kTile);
     const int64_t want = (tiles + kMinTiles - 1) / kMinTiles;
