@@ -61,7 +61,7 @@ struct Launch {
   LatentExpanded x;
 };
 
-// A sequence's items, pair after pair with the heads inside.
+// A sequence's items, head after head with the pairs inside.
 struct Chunk {
   int b, n, q0;
   int64_t row0;  // of its context in the expanded arrays
@@ -90,16 +90,17 @@ __device__ __noinline__ int4 item_at(const int64_t* place0, const int32_t* cu_q,
     else hi = mid - 1;
   }
   const Chunk c{0, cu_q[lo + 1] - cu_q[lo], q_start[lo], 0};
+  const int64_t of_head = place0[lo + 1] - place0[lo];
   int64_t r = u - place0[lo] * heads;
+  const int head = static_cast<int>(r / of_head);
+  r -= head * of_head;
   int a = 0, b = c.pairs() - 1;
   while (a < b) {
     const int mid = (a + b + 1) >> 1;
-    if (heads * c.before(mid) <= r) a = mid;
+    if (c.before(mid) <= r) a = mid;
     else b = mid - 1;
   }
-  r -= heads * c.before(a);
-  const int places = kLead + c.tiles(a);
-  return make_int4(lo, a, static_cast<int>(r / places), static_cast<int>(r % places));
+  return make_int4(lo, a, head, static_cast<int>(r - c.before(a)));
 }
 
 // An item and this CTA's part of it.
@@ -136,10 +137,10 @@ struct Walk {
   __device__ __forceinline__ void find(Item& it) const;
   __device__ __forceinline__ void next(Item& it) const {
     it.start = it.end;
-    if (++it.head == L.x.heads) {
-      it.head = 0;
-      if (++it.pair * kPair >= it.c.n) {
-        it.pair = 0;
+    if (++it.pair * kPair >= it.c.n) {
+      it.pair = 0;
+      if (++it.head == L.x.heads) {
+        it.head = 0;
         do ++it.seq;
         while (L.x.place0[it.seq + 1] * L.x.heads == it.start);  // sequences without places
         it.c = chunk_of(L, it.seq);

@@ -50,17 +50,6 @@ __device__ __forceinline__ void store_async4(uint32_t dst, float a, float b, flo
       "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void store_async1(uint32_t dst, float a, uint32_t bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
-               "r"(__float_as_uint(a)), "r"(bar)
-               : "memory");
-}
-// a run of this CTA's shared memory copied to another CTA's, counted by its barrier
-__device__ __forceinline__ void copy_to_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "r"(ptx::smem_addr(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
 // Bounded waits; one that gives up sets `aborted`, and no later one waits.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
   if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
