@@ -1,17 +1,23 @@
 // Keys and values of every head from the latent rows:
 //   K[h][t] = w_k[h] c_t,   V[h][t] = w_v[h] c_t,   D[128 x 256] = C[128 x 512] W[h]^T
 // for 128-token tiles of the contexts, and the position parts of the rows packed
-// beside them.  Rounded to bf16, or left in fp32 where the outputs are.  Rows behind a context are zeros.  A token whose value is
-// not finite gets a value of zero and a key of NaN: whoever sees it puts out NaN,
-// and 0 * NaN does not reach the rows that do not.
+// beside them.  Rounded to bf16 (the products that follow take bf16), or left in
+// fp32 where the outputs are.  Rows behind a context are zeros.  A token whose
+// value is not finite gets a value of zero and a key of NaN: whoever sees it puts
+// out NaN, and 0 * NaN does not reach the rows that do not.
 //
 // A CTA holds its tile's rows (128 KB, gathered through the block table by TMA)
 // and walks the heads; their weights stream.  4096 clocks of products need 256 KB
 // of weights, 64 bytes a clock, more than the second-level cache feeds every SM
-// with: so a cluster of two CTAs with two tiles takes the same heads, and each
-// loads half of the weights for both (multicast).
-// Six warps: 0-3 write out (a token a thread), 4 loads, 5 issues products; the
-// results of two heads alternate in tensor memory.
+// with: so two CTAs with two tiles form one product of 256 rows, for which each
+// holds half of the weights (the first the keys', the second the values').
+// Six warps: 0-3 write out (a token a thread; bf16 through shared memory by TMA),
+// 4 loads, 5 of the first CTA issues the pair's products; the results of two heads
+// alternate in tensor memory.
+// Measured, 4 x 2048 tokens of 128 heads (275 GFLOP, 0.5 GB written): 203 us, 1350
+// TFLOP/s; 228 with stores from registers, 32 bytes of its own row a lane.  The
+// weights' way from the second-level cache bounds it: 3 stages cost 20 us more
+// than 4, 5 with half the room for results gain nothing.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -83,11 +89,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LatentPrefillP
 // ----------------------------------------------------------- the expansion
 constexpr int kThreads = 6 * 32;
 constexpr int kABytes = 8 * 16384;   // [8 chunks of 64 columns][128 rows x 128 bytes]
-constexpr int kBBytes = 32768;       // a chunk of a head's weights: 128 rows of w_k, 128 of w_v
-constexpr int kStages = 3;
-constexpr int kOffB = kABytes, kOffBar = kOffB + kStages * kBBytes;
+constexpr int kBBytes = 16384;       // a chunk of a head's weights: 128 rows of w_k, or of w_v
+constexpr int kStages = 4;
+constexpr int kOutBytes = 4096;      // 64 columns of a warp's 32 tokens
+constexpr int kOffB = kABytes, kOffOut = kOffB + kStages * kBBytes, kOffBar = kOffOut + 4 * 2 * kOutBytes;
 constexpr int kSmemBytes = 1024 + kOffBar + 256;
-enum : int { kAFull = 0, kAFree = 1, kBFull = 2, kBFree = 5, kDFull = 8, kDFree = 10, kDrain = 12, kNumBars = 13 };
+enum : int {
+  kAFull = 0, kAFree = 1, kBFull = 2, kBFree = kBFull + kStages, kDFull = kBFree + kStages, kDFree = kDFull + 2,
+  kDrain = kDFree + 2, kNumBars = kDrain + 1
+};
+static_assert(kNumBars * 8 + 16 <= 256, "barrier area");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct Launch {
@@ -96,26 +107,31 @@ struct Launch {
   int bs_log;
 };
 
-// 16 columns of a token's key or value, `at` elements into dst
-__device__ __forceinline__ void store16(unsigned char* dst, bool f32, int64_t at, const float (&y)[16]) {
-  uint32_t h[8];
-  if (!f32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-    fp4::store32(dst + at * 2, h);
-    return;
-  }
+// 16 columns of a token's key or value in fp32
+__device__ __forceinline__ void store16(unsigned char* dst, int64_t at, const float (&y)[16]) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
+    uint32_t h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(y[8 * q + e]);
     fp4::store32(dst + at * 4 + 32 * q, h);
   }
 }
+// 128 columns of a row of the results as bf16 pairs
+__device__ __forceinline__ void load_row(uint32_t at, uint32_t (&w)[64]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    load_now(at + c * 32, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[c * 16 + j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_pool,
-                  const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv) {
+                  const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
+                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   const LatentPrefillParams& p = L.p;
   const LatentExpanded& x = L.x;
   extern __shared__ unsigned char smem_raw[];
@@ -132,18 +148,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&bars[kAFree], 1);
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&bars[kBFull + i], 1);
-      ptx::mbar_init(&bars[kBFree + i], 2);
+      ptx::mbar_init(&bars[kBFree + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars[kDFull + i], 1);
-      ptx::mbar_init(&bars[kDFree + i], 4);
+      ptx::mbar_init(&bars[kDFree + i], 8);
     }
     ptx::mbar_init(&bars[kDrain], 1);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
   if (warp == 5) {
-    ptx::tmem_alloc(tmem_slot, 512);
+    tmem_alloc_pair(tmem_slot, 512);
     ptx::tc_fence_before();
   }
   __syncthreads();
@@ -162,9 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   struct Tile {
     int seq, tok, n;
   };
-  auto tile_of = [&](int64_t unit) {
+  auto tile_of = [&](int64_t unit, uint32_t which) {
     Tile t{0, 0, 0};
-    const int i = static_cast<int>(unit / x.heads) * 2 + static_cast<int>(rank);
+    const int i = static_cast<int>(unit / x.heads) * 2 + static_cast<int>(which);
     if (i >= tiles) return t;
     int lo = 0, hi = p.num_seqs - 1;
     while (lo < hi) {  // the last sequence that starts at or before it
@@ -178,6 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return t;
   };
 
+  // the first CTA's barrier at this place: it issues the pair's products
+  auto first_of = [](uint64_t* bar) { return remote(bar, 0); };
+
   if (warp == 4) {
     // ============================== loads ==============================
     const int page_rows = min(128, 1 << L.bs_log);
@@ -186,15 +205,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t u = u0; u < u1 && !aborted; ++u) {
       const int h = x.head0 + static_cast<int>(u % x.heads);
       if (u == u0 || u % x.heads == 0) {
-        const Tile t = tile_of(u);
+        const Tile t = tile_of(u, rank);
         wait(&bars[kAFree], (ka & 1u) ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (aborted) break;
         ++ka;
-        const int pages = (t.n + page_rows - 1) / page_rows;
-        if (lane == 0) {
-          if (pages) ptx::mbar_arrive_expect_tx(&bars[kAFull], static_cast<uint32_t>(pages * page_rows) * 1024u);
-          else ptx::mbar_arrive(&bars[kAFull]);
+        auto pages_of = [&](const Tile& y) { return (y.n + page_rows - 1) / page_rows; };
+        const int pages = pages_of(t);
+        if (rank == 0) {
+          const int both = pages + pages_of(tile_of(u, 1));
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kAFull], static_cast<uint32_t>(both * page_rows) * 1024u);
         }
         __syncwarp();
         if (lane < pages) {
@@ -206,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int at = static_cast<int>((static_cast<int64_t>(phys) << L.bs_log) + (tok & ((1 << L.bs_log) - 1)));
           for (int ch = 0; ch < 8; ++ch)
-            ptx::tma_load_2d(smem + ch * 16384 + lane * page_rows * 128, &tm_pool, ch * 64, at, &bars[kAFull], keep);
+            tma_load_2d_pair(smem + ch * 16384 + lane * page_rows * 128, &tm_pool, ch * 64, at, first_of(&bars[kAFull]), keep);
         }
         __syncwarp();
       }
@@ -215,28 +235,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&bars[kBFree + slot], ((kb / kStages) & 1u) ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         if (!aborted && lane == 0) {
-          ptx::mbar_arrive_expect_tx(&bars[kBFull + slot], kBBytes);
-          unsigned char* dst = smem + kOffB + slot * kBBytes;
-          if (rank) tma_load_2d_cluster(dst + 16384, &tm_wv, ch * 64, h * 128, &bars[kBFull + slot], 3, keep);
-          else tma_load_2d_cluster(dst, &tm_wk, ch * 64, h * 128, &bars[kBFull + slot], 3, keep);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&bars[kBFull + slot], 2 * kBBytes);
+          tma_load_2d_pair(smem + kOffB + slot * kBBytes, rank ? &tm_wv : &tm_wk, ch * 64, h * 128,
+                           first_of(&bars[kBFull + slot]), keep);
         }
         __syncwarp();
       }
     }
-    // The products of both CTAs signal these barriers when they complete, which
+    // The products signal these barriers of both CTAs when they complete, which
     // no thread's order covers: a CTA stays until the last signals are here (one
     // that arrives where its CTA has gone is a fault).
     for (uint32_t k = kb > kStages ? kb - kStages : 0; k < kb; ++k)
       wait(&bars[kBFree + k % kStages], (k / kStages) & 1u, aborted);
+    if (ka) wait(&bars[kAFree], (ka - 1) & 1u, aborted);
     aborted = __any_sync(0xffffffffu, aborted);
   } else if (warp == 5) {
     // ============================ products ============================
     const bool leader = elect_one();
-    constexpr uint32_t kId = ptx::idesc_bf16_f32(128, 256, 0, 0);
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(256, 256, 0, 0);
     const uint64_t desc_a = ptx::smem_desc(smem, 16, 1024, ptx::kLayoutSw128);
     const uint64_t desc_b = ptx::smem_desc(smem + kOffB, 16, 1024, ptx::kLayoutSw128);
     uint32_t kb = 0, ka = 0, kd = 0;
-    for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
+    for (int64_t u = u0; u < u1 && !aborted && rank == 0; ++u, ++kd) {
       if (u == u0 || u % x.heads == 0) wait(&bars[kAFull], ka++ & 1u, aborted);
       wait(&bars[kDFree + (kd & 1u)], ((kd >> 1) & 1u) ^ 1u, aborted);
       const uint32_t d = tmem + (kd & 1u) * 256;
@@ -249,18 +269,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) {
           const uint64_t da = desc_a + ch * (16384 >> 4), db = desc_b + slot * (kBBytes >> 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ptx::umma_bf16(d, da + j * 2, db + j * 2, kId, ch + j > 0);
-          umma_commit_cluster(&bars[kBFree + slot], 3);
+          for (int j = 0; j < 4; ++j) umma_pair(d, da + j * 2, db + j * 2, kId, ch + j > 0);
+          umma_commit_pair(&bars[kBFree + slot]);
           if (ch == 7) {
-            ptx::umma_commit(&bars[kDFull + (kd & 1u)]);
-            if (u + 1 == u1 || (u + 1) % x.heads == 0) ptx::umma_commit(&bars[kAFree]);
+            umma_commit_pair(&bars[kDFull + (kd & 1u)]);
+            if (u + 1 == u1 || (u + 1) % x.heads == 0) umma_commit_pair(&bars[kAFree]);
           }
         }
         __syncwarp();
       }
     }
     if (leader) {  // nothing may be in flight when tensor memory is freed
-      ptx::umma_commit(&bars[kDrain]);
+      if (rank == 0) umma_commit_pair(&bars[kDrain]);
       bool late = false;
       wait(&bars[kDrain], 0, late);
       if (late) aborted = true;
@@ -269,12 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ===================== results: a token a thread =====================
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-    unsigned char *const k = x.k, *const v0 = x.v;
     const bool f32 = x.f32;
     uint32_t kd = 0;
     Tile t{0, 0, 0};
     for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
-      if (u == u0 || u % x.heads == 0) t = tile_of(u);
+      if (u == u0 || u % x.heads == 0) t = tile_of(u, rank);
       const int h = static_cast<int>(u % x.heads);
       const int tile = static_cast<int>(u / x.heads) * 2 + static_cast<int>(rank);
       const int64_t row = static_cast<int64_t>(tile) * 128 + tid;
@@ -300,22 +319,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (aborted) break;
       ptx::tc_fence_after();
       const uint32_t d = tmem + lanes + (kd & 1u) * 256;
-      const int64_t at = (static_cast<int64_t>(h) * x.rows + row) * 128;
+      auto all_read = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive(first_of(&bars[kDFree + (kd & 1u)]));
+      };
       bool odd = false;  // the value is not finite somewhere
+      if (!f32) {
+        // bf16 rows leave by TMA, 64 columns of the warp's 32 tokens at a time
+        // (stored from registers, 32 bytes of its own row a lane, they took longer than the products)
+        uint32_t w[64];
+        auto put = [&](const CUtensorMap* map) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            unsigned char* box = smem + kOffOut + (warp * 2 + half) * kOutBytes;
+            if (lane == 0) tma_stores_read<1>();  // the box before in the same place
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint32_t* y = w + half * 32 + c * 4;
+              *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(map, half * 64, static_cast<int>(h * x.rows + row), box);
+          }
+        };
+        load_row(d + 128, w);  // values first
+#pragma unroll
+        for (int j = 0; j < 64; ++j) odd |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+        if (odd || !valid) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) w[j] = 0u;
+        }
+        if (there) put(&tm_v);
+        load_row(d, w);
+        all_read();
+        if (odd || !valid) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) w[j] = valid ? 0x7fff7fffu : 0u;
+        }
+        if (there) put(&tm_k);
+        continue;
+      }
+      const int64_t at = (static_cast<int64_t>(h) * x.rows + row) * 128;
 #pragma unroll 1
       for (int col = 0; col < 256; col += 32) {
         const int from = (col + 128) & 255;  // values first
         uint32_t v[32];
         load_now(d + from, v);
-        if (col == 224) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars[kDFree + (kd & 1u)]);
-        }
+        if (col == 224) all_read();
         if (!there) continue;
         if (from >= 128) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) odd |= (v[j] & 0x7fffffffu) >= 0x7f7f8000u;  // in bf16
+          for (int j = 0; j < 32; ++j) odd |= (v[j] & 0x7f800000u) == 0x7f800000u;
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -323,23 +380,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             y[j] = !valid ? 0.f : (from < 128 && odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(v[16 * q + j]));
-          store16(from < 128 ? k : v0, f32, at + (from & 127) + 16 * q, y);
+          store16(from < 128 ? x.k : x.v, at + (from & 127) + 16 * q, y);
         }
       }
       if (odd && valid && there) {  // no value, in place of what was stored
         const float none[16] = {};
-        for (int col = 0; col < 128; col += 16) store16(v0, f32, at + col, none);
+        for (int col = 0; col < 128; col += 16) store16(x.v, at + col, none);
       }
     }
+    tma_stores_done();
   }
 
   if (aborted) *gave_up = 1;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 5) ptx::tmem_dealloc(tmem, 512);
+  cluster_sync();  // the other CTA may still load, read and signal here
+  if (warp == 5) tmem_dealloc_pair(tmem, 512);
   if (tid == 0 && *gave_up && p.status) atomicExch(p.status, kDevErrTimeout);
-  cluster_sync();  // the other CTA may still load and signal here
 }
 
 }  // namespace latent_expand_detail
@@ -356,14 +414,17 @@ cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpan
   L.p = p;
   L.x = x;
   L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
-  CUtensorMap tm_pool, tm_wk, tm_wv;
+  CUtensorMap tm_pool, tm_wk, tm_wv, tm_k, tm_v;
   const uint64_t pool[2] = {576, static_cast<uint64_t>(p.num_blocks) * p.block_size}, pool_stride[1] = {1152};
   const uint32_t pool_box[2] = {64, static_cast<uint32_t>(p.block_size < 128 ? p.block_size : 128)};
   const uint64_t w[2] = {512, static_cast<uint64_t>(p.num_heads) * 128}, w_stride[1] = {1024};
-  const uint32_t w_box[2] = {64, 128};
+  const uint32_t w_box[2] = {64, 128}, out_box[2] = {64, 32};
+  const uint64_t out[2] = {128, static_cast<uint64_t>(x.rows) * x.heads}, out_stride[1] = {256};
   if (!encode_bf16_tiles(&tm_pool, 2, p.cache, pool, pool_stride, pool_box, 128) ||
       !encode_bf16_tiles(&tm_wk, 2, p.w_k, w, w_stride, w_box, 128) ||
-      !encode_bf16_tiles(&tm_wv, 2, p.w_v, w, w_stride, w_box, 128))
+      !encode_bf16_tiles(&tm_wv, 2, p.w_v, w, w_stride, w_box, 128) ||
+      !encode_bf16_tiles(&tm_k, 2, x.k, out, out_stride, out_box, 128) ||
+      !encode_bf16_tiles(&tm_v, 2, x.v, out, out_stride, out_box, 128))
     return cudaErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&expand_kernel);
   int per_sm = 0;
@@ -382,7 +443,7 @@ cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpan
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* args[] = {&L, &tm_pool, &tm_wk, &tm_wv};
+  void* args[] = {&L, &tm_pool, &tm_wk, &tm_wv, &tm_k, &tm_v};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

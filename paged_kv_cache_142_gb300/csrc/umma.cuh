@@ -23,13 +23,30 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b,
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
-// arrive on the barrier at this place in every CTA of the mask once the products issued so far are complete
-__device__ __forceinline__ void umma_commit_cluster(uint64_t* bar, uint16_t mask) {
+// The same as a pair of CTAs' product, issued by its first: D's and A's rows are the first's 128, then the second's;
+// B's columns too.
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// arrive on the barrier at this place in both CTAs once the pair's products issued so far are complete
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           ptx::smem_addr(bar)),
-      "h"(mask)
+      "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+// tensor memory of both CTAs of a pair, by a warp of each
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 // the place in CTA `rank` of the cluster that p has in this one
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
@@ -42,6 +59,9 @@ __device__ __forceinline__ void remote_arrive(uint32_t bar, float used) {
   asm volatile("{\n\t.reg .f32 t;\n\tmov.f32 t, %1;\n\tmbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
                "f"(used)
                : "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // stores into another CTA's shared memory, counted by its barrier
 __device__ __forceinline__ void store_async4(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
@@ -100,15 +120,27 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(ptx::smem_addr(bar)), "l"(policy)
       : "memory");
 }
-// a box loaded into this place of every CTA in the mask, counted by the barrier at this place of each
-__device__ __forceinline__ void tma_load_2d_cluster(void* dst, const void* map, int x, int y, uint64_t* bar, uint16_t mask,
-                                                    uint64_t policy) {
+// a box loaded into this CTA, counted by a barrier of either CTA of its pair
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int x, int y, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(ptx::smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(ptx::smem_addr(bar)), "h"(mask), "l"(policy)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(ptx::smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
+
+// a box stored from this CTA's shared memory, in a group of its own
+__device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\tcp.async.bulk.commit_group;" ::"l"(map),
+               "r"(x), "r"(y), "r"(ptx::smem_addr(src))
+               : "memory");
+}
+// until all but the newest N of this thread's groups have read their boxes; until all are complete
+template <int N>
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace um
 }  // namespace pa
