@@ -5,16 +5,21 @@
 //
 // The threshold is found by radix selection on the weights' order-preserving
 // bit patterns: up to four passes, each counts the 8-bit digits of the candidates
-// that agree with the digits found so far, until all of those stay.  Then one sweep in order of the
-// positions numbers what is above it, and as many of what equals it as are
-// still wanted.  Counts are integers, so the result does not depend on the
-// order of anything.
+// that agree with the digits found so far, until all of those stay.  Then one sweep
+// in order of the positions numbers what is above it, and as many of what equals
+// it as are still wanted.  Counts are integers, so the result does not depend on
+// the order of anything.
 //
 // A cluster of 1 to 8 CTAs shares a sequence: each holds a slice of its weights
 // in shared memory, counts it there, and adds up the others' counts through
 // distributed shared memory.  A digit that many weights share (zeros, the
 // exponents of small numbers) would serialise a warp's additions, so every CTA
 // counts in 16 copies, by lane, each a bank further.
+//
+// The work is a chain of passes with a barrier of the cluster after each; its
+// bytes (8 a candidate) hardly count.  Measured: 32 sequences of 150 to 700 tokens
+// 7.5 us (14 with rounds of the whole CTA and always four passes), 8 of 20000 to
+// 32768 9.9 us (37 before).
 #include <cooperative_groups.h>
 
 #include "decode.cuh"
@@ -46,9 +51,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
   const int seq = blockIdx.x / C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c0 = p.cu_keep[seq], c1 = p.cu_keep[seq + 1];
   const int a = p.dst_start[seq], b = p.context_lens[seq], n = c1 - c0;
-  if (n == 0 && a >= 0 && a <= b && b <= p.max_context_len) {
+  // (every bound by comparison first: differences of values that are out of range may wrap)
+  if (c0 == c1 && a >= 0 && a <= b && b <= p.max_context_len) {
     // nothing stays: the weights are cleared below
-  } else if (c0 < 0 || n < 0 || c1 > p.num_keep || a < 0 || b > p.max_context_len || n > b - a) {
+  } else if (c0 < 0 || c1 < c0 || c1 > p.num_keep || a < 0 || b < a || b > p.max_context_len || n > b - a) {
     if (p.status && rank == 0 && tid == 0) atomicExch(p.status, kDevErrInvalidArg);
     return;  // the whole cluster
   }
@@ -226,7 +232,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
 }  // namespace
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
-  // CTAs a sequence: a slice of some 2048 weights each while they all run at once
+  // CTAs a sequence: a slice of some 2048 weights each while they all run at once, two an SM (one CTA
+  // alone sweeps 32768 weights 64 to a thread)
   int ctas = 1;
   while (ctas < 8 && static_cast<int64_t>(ctas) * 2048 < p.max_context_len &&
          static_cast<int64_t>(p.num_seqs) * ctas * 2 <= 2 * device_sm_count())

@@ -150,6 +150,19 @@ def test_select_reports_what_lies_outside(ops):
         assert np.array_equal(ww[[0, 2]], after) and np.array_equal(ww[1], w[1])
 
 
+def test_select_reports_bounds_whose_differences_wrap(ops):
+    top, least = 2 ** 31 - 1, -2 ** 31
+    w = np.arange(100, dtype=np.float32)[None]
+    for cu, start, length in (([0, 1], top, least), ([top, least], 0, 100), ([least, top], 0, 100), ([0, 1], least, 100),
+                              ([0, top], 0, 100), ([0, least], 0, 100), ([0, 1], 0, least), ([-1, 0], 0, 100)):
+        keep, ww = torch.full((4,), -1, dtype=torch.int32, device="cuda"), dev(w)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ops.pa_select_tokens(keep, dev(np.array(cu, np.int32)), ww, dev(np.array([start], np.int32)),
+                             dev(np.array([length], np.int32)), 0, 100, status=status)
+        assert int(status.item()) == 1, (cu, start, length)
+        assert (keep == -1).all() and np.array_equal(ww.cpu().numpy(), w)
+
+
 # ------------------------------------------------- the operators together
 def test_eviction_of_a_latent_history(ops):
     """Append, decode, weights, selection, compaction, truncation and the next

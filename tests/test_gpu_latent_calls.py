@@ -93,6 +93,43 @@ def test_two_streams_with_their_own_workspaces(ops):
         check(w, *O.weights(np.zeros(w.shape), q.f32, cache.f32[:, None], tables, lens, 0.07), False)
 
 
+def test_prefills_on_two_streams(ops):
+    """Overlapping prefills of different shapes and outputs, an odd number of
+    tiles and of heads among them, each with its own workspace."""
+    rng = np.random.default_rng(31)
+    cases = []
+    for chunks, H, dt in (([(0, 300), (40, 129)], 5, torch.bfloat16), ([(700, 20)], 16, torch.bfloat16), ([(128, 130)], 3, torch.float32)):
+        _, tables, cache, cu, q, w_k, w_v = prefill_case(rng, chunks, 16, H)
+        start = [s for s, _ in chunks]
+        most, total = max(s + n for s, n in chunks), sum(s + n for s, n in chunks)
+        wp = ops.make_prefill_workspace_latent(len(chunks), H, LATENT, ROPE, HEAD, 16, max(n for _, n in chunks), most, total)
+        out = torch.zeros(q.shape[0], H, HEAD, dtype=dt, device="cuda")
+        args = [dev16(q), dev16(cache), dev16(w_k), dev16(w_v), dev(np.asarray(cu, np.int32)), dev(np.asarray(start, np.int32)), dev(tables)]
+        ref = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.07)
+        cases.append((out, args, max(n for _, n in chunks), most, total, wp, torch.cuda.Stream(), ref))
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(6):
+        for out, args, longest, most, total, wp, stream, _ in cases:
+            ops.pa_prefill_latent(out, *args, 0.07, longest, most, total, wp, status=status, stream=stream)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for out, *_, ref in cases:
+        check(out, *ref, out.dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("H,dt", [(16, torch.float32), (32, torch.bfloat16), (17, torch.float32)])
+def test_few_rows_of_many_sequences(ops, H, dt):
+    """2048 sequences a launch, where the shared memory is fullest, with items of
+    one tile and of several."""
+    rng = np.random.default_rng(32 + H)
+    lens = [int(x) for x in rng.integers(0, 30, size=2048)]
+    lens[5], lens[-1], lens[1000] = 700, 500, 65
+    tables, cache, q = decode_case(rng, lens, 16, H, 1)
+    ref, tol = O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT)
+    check(run_decode(ops, q, dev16(cache), tables, lens, 16, 0.07, dt), ref, tol, dt == torch.bfloat16)
+
+
 def test_pool_past_2_to_the_31_bytes(ops):
     """Blocks at the far end of a pool of more than 2^32 bytes."""
     rng = np.random.default_rng(4)
