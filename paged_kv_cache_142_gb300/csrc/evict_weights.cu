@@ -1,16 +1,21 @@
 // Accumulated attention weights: weights[t] += sum over a window's queries and
 // heads of softmax_t(scale q . k[t]).
 //
-// Three steps.  (1) scores: S = Q K^T on the 5th-generation tensor cores, written
-// out in fp32 (log2 domain, -inf where a row does not see a token) with each
-// tile's maximum and sum of exponentials per row.  (2) a row's logarithm of its
-// sum from its tiles'.  (3) a token's 2^(s - lse) added up over the rows in a
-// fixed order, and into its weight.
+// Three steps.  (1) scores: S = Q K^T on the 5th-generation tensor cores, with each
+// tile's maximum and sum of exponentials per row; of few rows written out in fp32
+// (log2 domain, -inf where a row does not see a token).  (2) a row's logarithm of
+// its sum from its tiles'.  (3) a token's 2^(s - lse) added up over the rows in a
+// fixed order, and into its weight: from the stored scores, or of many rows from
+// scores formed a second time.
 //
-// Step 1 reads K once, which is what the whole cannot do without.  Its scores cost 8
-// bytes a row and token, written and read: 32 of a decode step's four rows against
-// 256 of the key, 1024 of a latent row's 128 against 1152.  Forming S a second time
-// instead would read K again.
+// Stored scores cost 8 bytes a row and token, written and read: 32 of a decode
+// step's four rows against 256 of the key, but 1024 of 128 rows, four times the key.
+//
+// Measured: a decode step of 256 sequences, 32 q / 8 kv heads (448 MB of keys) 96 us,
+// of them the scores 78 (5.8 TB/s, 85% of a plain copy), the sums 6, the tokens 12;
+// a window of 32 queries over 4 x 9000 to 16384 tokens 74 us (34 and 40 for the two
+// times that the scores are formed: the exponentials of 128 rows a token bound
+// both; stored 132); a step of 128 heads over 44 MB of latent rows 33 us.
 //
 // Step 1: a CTA walks an equal run of units (token tile of a sequence, kv head and
 // row tile).  The rows of a tile are the heads of a kv head's group, query after
@@ -666,11 +671,11 @@ int tokens_of(int head_dim) {
 constexpr int kStatTokens = 32;  // the least that a row's statistics stand for
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // Scores stored or formed again, by a kv head's rows.  Stored they cost 8 bytes a row
-// and token; again the key's 2 head_dim bytes once more (and its products, which
-// are free beside them): so from head_dim / 4 rows on, where a tile of tokens fills
-// the product's 128 rows.  32 queries of a group of 4 over 4 x 16384 tokens: stored
-// 132 us, again 75.
-bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > head_dim / 4; }
+// and token, and an exponential; again a product of 128 rows, whatever number of
+// them there are, and the keys once more.  4 x 8192 tokens, 8 kv heads of 128 dims,
+// stored and again: 64 rows 58 and 64 us, 72 rows 63 and 65, 80 rows 67 and 65, 128
+// rows 101 and 58 (64 dims: 64 rows 50 and 60, 80 rows 66 and 60).
+bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > 76; }
 // of one sequence: its rows' logarithms, tiles' statistics and scores
 int64_t seq_bytes(int64_t rows, bool stored, int max_context_len) {
   return rows * (4 + up(max_context_len, 128) / kStatTokens * 8 + (stored ? up(max_context_len, 128) * 4 : 0));
