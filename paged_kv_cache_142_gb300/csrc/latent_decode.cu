@@ -885,18 +885,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // the other CTA may still signal this one's barriers
 }
 
-// Parts of items added up: a warp takes a CS-th of a row's columns.  The first
-// cluster behind an item's start reports the item, and the rows of a cluster
-// that reports none, or a later one of an item, are nobody's.
+// Parts of items added up.  The first cluster behind an item's start reports the
+// item, and the rows of a cluster that reports none, or a later one of an item, are
+// nobody's.  A warp takes a row, or (MANY parts each: few items) a quarter of its
+// columns and every eighth part, and the CTA's warps join; there a CTA looks for its
+// item's report, since hardly any cluster has one.
 constexpr int kMergeThreads = 256;
-template <int CS>
+template <bool MANY>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  constexpr int N = 4 / CS;  // columns lane * 4 + 128 i
-  const int lane = threadIdx.x & 31;
-  const int u = (blockIdx.x * kMergeThreads + threadIdx.x) >> 5;
-  const int b = 1 + u / (L.part_rows * CS), r = u / CS % L.part_rows, col = u % CS * 128 + lane * 4;
+  constexpr int N = MANY ? 1 : 4, kStep = MANY ? 8 : 1;  // columns lane * 4 + 128 i; parts of a warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = MANY ? blockIdx.x >> 2 : blockIdx.x * (kMergeThreads / 32) + warp;
+  const int r = u % L.part_rows, col = (MANY ? (blockIdx.x & 3) * 128 : 0) + lane * 4;
+  int b = 1 + u / L.part_rows;
+  if (MANY) {  // the report of this rank
+    int left = u / L.part_rows;
+    b = L.num_clusters;
+    for (int i = 1 + lane; i - lane < L.num_clusters && b == L.num_clusters; i += 32) {
+      const int4 d = i < L.num_clusters ? L.desc[i] : make_int4(-1, 0, 0, 0);
+      const uint32_t those = __ballot_sync(0xffffffffu, d.x >= 0 && d.z == i - 1);
+      const int n = __popc(those);
+      if (left < n) b = i - lane + static_cast<int>(__fns(those, 0, left + 1));
+      left -= n;
+    }
+  }
   if (b >= L.num_clusters) return;
   const int4 d = L.desc[b];
   const int row = d.y * 128 + r;
@@ -907,13 +921,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float ref = -CUDART_INF_F, sum = 0.f;
-#pragma unroll CS == 1 ? 2 : 8
-  for (int c = d.z; c <= d.w; ++c) {
-    const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + part_of(c) * 2));
-    float4 x[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(L.o + part_of(c) * 512 + col + 128 * i));
-    if (e.y == 0.f) continue;  // a part that this row sees nothing of
+  auto add = [&](float2 e, const float4 (&x)[N]) {
+    if (e.y == 0.f) return;  // a part that this row sees nothing of
     const float now = fmaxf(ref, e.x), w = fp4::fast_exp2(e.x - now), old = fp4::fast_exp2(ref - now);
     ref = now;
     sum = fmaf(w, e.y, sum * old);
@@ -923,6 +932,27 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Launch L) {
       acc[i].y = fmaf(w, x[i].y, acc[i].y * old);
       acc[i].z = fmaf(w, x[i].z, acc[i].z * old);
       acc[i].w = fmaf(w, x[i].w, acc[i].w * old);
+    }
+  };
+#pragma unroll MANY ? 4 : 2
+  for (int c = d.z + (MANY ? warp : 0); c <= d.w; c += kStep) {
+    const float2 e = __ldcg(reinterpret_cast<const float2*>(L.ml + part_of(c) * 2));
+    float4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(L.o + part_of(c) * 512 + col + 128 * i));
+    add(e, x);
+  }
+  if (MANY) {
+    __shared__ float2 ml[8];
+    __shared__ float4 rows[8][32];
+    if (lane == 0) ml[warp] = make_float2(ref, sum);
+    rows[warp][lane] = acc[0];
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const float4 x[1] = {rows[w][lane]};
+      add(ml[w], reinterpret_cast<const float4(&)[N]>(x));
     }
   }
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
@@ -1035,12 +1065,15 @@ cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t strea
     e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess) return e;
     if (L.num_clusters > 1) {
-      // few items have many parts each: more warps a row
-      const bool few = static_cast<int64_t>(L.p.num_seqs) * row_tiles < 16;
-      const int64_t warps = static_cast<int64_t>(L.num_clusters - 1) * L.part_rows * (few ? 4 : 1);
-      const dim3 ctas(static_cast<unsigned>((warps * 32 + kMergeThreads - 1) / kMergeThreads));
-      e = few ? launch_early(merge_kernel<4>, ctas, kMergeThreads, stream, L)
-              : launch_early(merge_kernel<1>, ctas, kMergeThreads, stream, L);
+      // Parts of a row spread over warps, and a warp a row: 1 x 30000 tokens with 16 heads 31 and 62 us, with
+      // 128 heads 39 and 76; 4 x 8192 with 128 heads 43 and 45, 8 x 4096 45 and 41 (its CTAs are too many);
+      // with 16 heads 8 x 4096 29 and 31, 15 x 4000 the same
+      const int64_t items = static_cast<int64_t>(L.p.num_seqs) * row_tiles;
+      const bool many = items < 16 && items * L.part_rows <= 512;
+      const dim3 ctas(static_cast<unsigned>(
+          many ? items * L.part_rows * 4 : (static_cast<int64_t>(L.num_clusters - 1) * L.part_rows + 7) / 8));
+      e = many ? launch_early(merge_kernel<true>, ctas, kMergeThreads, stream, L)
+               : launch_early(merge_kernel<false>, ctas, kMergeThreads, stream, L);
       if (e != cudaSuccess) return e;
     }
   }

@@ -24,6 +24,14 @@
 // One CTA per SM, 11 warps, each role walking the same items: 0-3 and 4-7 the
 // softmax of the first and the second tile (a row a thread), 8 loads, 9 and 10
 // issue the products of the first and the second tile.
+//
+// A row's reference is raised only when its maximum passes it by 2^8, so that O is
+// rarely rescaled.  Measured, 4 x 2048 tokens of 128 heads (687 GFLOP): 630 us, 1090
+// TFLOP/s (57% of the products' rate); 2 x 200 to 512 tokens over 8000 to 16000, 32
+// heads: 267 us.  A tile's softmax (tensor memory, 128 exponentials a thread, P)
+// bounds it: two tiles' products fill half of the time that it takes.  A head's
+// pairs follow one another, so that some of its keys come from the second-level
+// cache (heads inside pairs: 16 us more).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 

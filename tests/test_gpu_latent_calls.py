@@ -130,6 +130,15 @@ def test_few_rows_of_many_sequences(ops, H, dt):
     check(run_decode(ops, q, dev16(cache), tables, lens, 16, 0.07, dt), ref, tol, dt == torch.bfloat16)
 
 
+@pytest.mark.parametrize("lens,H,Q", [([5000], 16, 1), ([5000], 128, 1), ([3000, 0, 7, 2500], 128, 1), ([900] * 15, 16, 1), ([900] * 16, 16, 1),
+                                      ([2000] * 5, 128, 1), ([0, 4000], 3, 1), ([3000, 40], 100, 3), ([6000], 1, 300)])
+def test_few_long_sequences(ops, lens, H, Q):
+    """Items in many parts, beside ones in one."""
+    rng = np.random.default_rng(len(lens) + H)
+    tables, cache, q = decode_case(rng, lens, 32, H, Q)
+    check(run_decode(ops, q, dev16(cache), tables, lens, 32, 0.07), *O.decode(q.f32, cache.f32, tables, lens, 0.07, LATENT), False)
+
+
 def test_pool_past_2_to_the_31_bytes(ops):
     """Blocks at the far end of a pool of more than 2^32 bytes."""
     rng = np.random.default_rng(4)
