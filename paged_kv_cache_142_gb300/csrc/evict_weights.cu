@@ -13,14 +13,15 @@
 //
 // Measured: a decode step of 256 sequences, 32 q / 8 kv heads (448 MB of keys) 96 us,
 // of them the scores 78 (5.8 TB/s, 85% of a plain copy), the sums 6, the tokens 12;
-// a window of 32 queries over 4 x 9000 to 16384 tokens 74 us (34 and 40 for the two
-// times that the scores are formed: the exponentials of 128 rows a token bound
-// both; stored 132); a step of 128 heads over 44 MB of latent rows 33 us.
+// a window of 32 queries over 4 x 9000 to 16384 tokens 64 us (the exponentials of
+// 128 rows a token bound both times that the scores are formed; with four warps
+// for them in the place of eight, and eight in that of sixteen, 74; stored 132); a step of 128 heads over 44 MB of latent rows 33 us.
 //
 // Step 1: a CTA walks an equal run of units (token tile of a sequence, kv head and
 // row tile).  The rows of a tile are the heads of a kv head's group, query after
-// query.  10 warps: 0-3 and 4-7 take the scores of every other unit (a row a
-// thread), 8 loads, 9 issues products.  A page is one TMA box: [8-token group]
+// query.  Warps 0-3 and 4-7 take the scores of every other unit (a row a thread), 8
+// loads, 9 issues products; where a tile has 64 tokens or more, eight further warps
+// take its second half.  A page is one TMA box: [8-token group]
 // [chunk of 64 dims][8 rows x 128 bytes] of its kv head.
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -37,6 +38,9 @@ namespace weights_detail {
 using namespace um;
 
 constexpr int kThreads = 10 * 32;
+// warps that take scores: a row's tokens in two halves where a tile has two of 32
+__host__ __device__ constexpr int halves_of(int nc, bool few) { return !few && nc <= 4 ? 2 : 1; }
+__host__ __device__ constexpr int threads_of(int nc, bool few) { return (2 + 8 * halves_of(nc, few)) * 32; }
 constexpr int kMaxSeqs = 1024;  // of one launch: their units lie in shared memory
 constexpr int64_t kScoreBytes = int64_t(512) << 20;  // of one launch, where a sequence does not need more
 
@@ -75,9 +79,10 @@ __device__ __forceinline__ int length_of(const WeightsParams& p, int seq) {
 }
 
 // prefix[s]: units before sequence s, `each` of them a tile of `tokens`
+template <int THREADS>
 __device__ __forceinline__ void count_units(const WeightsParams& p, int* prefix, int* warp_sums, int tokens, int each) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  const int per = (p.num_seqs + THREADS - 1) / THREADS;
   const int beg = min(p.num_seqs, tid * per), end = min(p.num_seqs, beg + per);
   int local = 0;
   for (int s = beg; s < end; ++s) {
@@ -164,10 +169,11 @@ struct Walk {
 // tokens, so that four warps share the exponentials that a quarter of the lanes
 // of one would form, and a row's maximum and sum go through shuffles.
 template <int NC, bool FEW>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(NC, FEW), 1)
     scores_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_q) {
   using S = Shape<NC>;
+  constexpr int kHalves = halves_of(NC, FEW);
   const WeightsParams& p = L.p;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* prefix = reinterpret_cast<int*>(smem + S::kOffPrefix);
-  __shared__ int warp_sums[kThreads / 32];
+  __shared__ int warp_sums[threads_of(NC, FEW) / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   ptx::griddep_launch_dependents();
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kQFull + i], 1);
       ptx::mbar_init(&bars[kQFree + i], 1);
       ptx::mbar_init(&bars[kSFull + i], 1);
-      ptx::mbar_init(&bars[kSFree + i], 4);
+      ptx::mbar_init(&bars[kSFree + i], 4 * kHalves);
     }
     ptx::mbar_init(&bars[kDrain], 1);
     *gave_up = 0;
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool aborted = false;
   ptx::griddep_wait();
 
-  count_units(p, prefix, warp_sums, S::kTokens, p.num_kv_heads * L.row_tiles);
+  count_units<threads_of(NC, FEW)>(p, prefix, warp_sums, S::kTokens, p.num_kv_heads * L.row_tiles);
   const int total = prefix[p.num_seqs];
   const int share = total / gridDim.x, extra = total - share * gridDim.x;
   auto run_begin = [&](int c) { return c * share + min(c, extra); };
@@ -313,8 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     aborted = __any_sync(0xffffffffu, aborted);
   } else {
     // ==================== scores: one row per thread ====================
-    const uint32_t buffer = warp >> 2;  // the units k = buffer mod 2
-    const int r = tid & 127;
+    // warps 0-7 the first half of a tile's tokens, 10-17 the second; lanes by the warp's number mod 4
+    const uint32_t buffer = warp < 8 ? warp >> 2 : (warp - 10) >> 2;  // the units k = buffer mod 2
+    const int half = warp < 8 ? 0 : 1;
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + buffer * 128;
     uint32_t k = 0;
     const int64_t all_rows = static_cast<int64_t>(p.num_kv_heads) * L.rows;
@@ -352,39 +360,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = r < tile_rows;
         if ((warp & 3) * 32 < tile_rows) {
           const int seen = x.len - p.window + 1 + row / L.group;  // tokens that this row sees
-          const int nvis = seen - x.tile * S::kTokens;
+          const int from = half * (S::kTokens / kHalves);
+          const int nvis = seen - x.tile * S::kTokens - from;
           const int64_t grow = x.seq * all_rows + static_cast<int64_t>(x.kvh) * L.rows + row;
-          float* dst = L.scores + grow * L.pitch + x.tile * S::kTokens;
+          float* dst = L.scores + grow * L.pitch + x.tile * S::kTokens + from;
+          const uint64_t ff = fp4::pair(p.scale_log2, p.scale_log2);
           float top = -CUDART_INF_F, sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < S::kTokens; c += 32) {
+          for (int c = 0; c < S::kTokens / kHalves; c += 32) {
             uint32_t v[32];
-            load_now(at + c, v);
-            float m0 = -CUDART_INF_F;
-            float y[32];
+            load_now(at + from + c, v);
+            uint64_t y[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              y[j] = c + j < nvis ? __uint_as_float(v[j]) * p.scale_log2 : -CUDART_INF_F;
-              m0 = fmaxf(m0, y[j]);
+            for (int j = 0; j < 16; ++j)
+              y[j] = fp4::mul2(fp4::pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), ff);
+            if (!__all_sync(0xffffffffu, nvis >= c + 32)) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 t = fp4::unpair(y[j]);
+                y[j] = fp4::pair(c + 2 * j < nvis ? t.x : -CUDART_INF_F, c + 2 * j + 1 < nvis ? t.y : -CUDART_INF_F);
+              }
             }
-            const float now = fmaxf(top, m0), ref = now == -CUDART_INF_F ? 0.f : now;
-            float s0 = 0.f, s1 = 0.f;
+            float m0 = top, m1 = -CUDART_INF_F;
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) s0 += fp4::fast_exp2(y[j] - ref), s1 += fp4::fast_exp2(y[j + 1] - ref);
-            sum = fmaf(sum, fp4::fast_exp2(top - ref), s0 + s1);
+            for (int j = 0; j < 16; j += 2) {
+              const float2 t = fp4::unpair(y[j]), u = fp4::unpair(y[j + 1]);
+              m0 = max3(m0, t.x, t.y);
+              m1 = max3(m1, u.x, u.y);
+            }
+            const float now = fmaxf(m0, m1), ref = now == -CUDART_INF_F ? 0.f : now;
+            const uint64_t less = fp4::pair(-ref, -ref);
+            uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float2 t = fp4::unpair(fp4::add2(y[j], less)), u = fp4::unpair(fp4::add2(y[j + 1], less));
+              s0 = fp4::add2(s0, fp4::pair(fp4::fast_exp2(t.x), fp4::fast_exp2(t.y)));
+              s1 = fp4::add2(s1, fp4::pair(fp4::fast_exp2(u.x), fp4::fast_exp2(u.y)));
+            }
+            const float2 t = fp4::unpair(fp4::add2(s0, s1));
+            sum = fmaf(sum, fp4::fast_exp2(top - ref), t.x + t.y);
             top = now;
             if (valid && L.scores) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * q + e]);
+                for (int e = 0; e < 4; ++e) {
+                  const float2 z = fp4::unpair(y[4 * q + e]);
+                  w[2 * e] = __float_as_uint(z.x), w[2 * e + 1] = __float_as_uint(z.y);
+                }
                 fp4::store32(dst + c + 8 * q, w);
               }
             }
             __syncwarp();  // the next load is the whole warp's
           }
-          if (valid) L.tile_ml[grow * L.tiles_pitch + x.tile] = make_float2(top, sum);
+          if (valid) L.tile_ml[grow * L.tiles_pitch + x.tile * kHalves + half] = make_float2(top, sum);
         }
       }
       ptx::tc_fence_before();
@@ -465,8 +495,9 @@ __global__ void __launch_bounds__(32 * kAddWarps) add_kernel(const Launch L) {
 
 // Step 3 without stored scores: a token tile's products with every row tile again,
 // tokens as the product's rows (128) and queries as its columns, so that a thread
-// adds up one token's probabilities of 128 rows and needs nobody else's.  Warps 0-3
-// add, 8 loads, 9 issues products.
+// adds up one token's probabilities of half a row tile and needs only its partner's
+// in the end.  Warps 0-3 add the first halves, 4-7 the second ones, 8 loads, 9
+// issues products.
 template <int NC>
 __global__ void __launch_bounds__(kThreads, 1)
     again_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_k,
@@ -483,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* prefix = reinterpret_cast<int*>(smem + S::kOffPrefix);
   __shared__ int warp_sums[kThreads / 32];
   __shared__ __align__(16) float row_lse[2][128];
+  __shared__ float other[128];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   ptx::griddep_launch_dependents();
@@ -495,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kQFull + i], 1);
       ptx::mbar_init(&bars[kQFree + i], 1);
       ptx::mbar_init(&bars[kSFull + i], 1);
-      ptx::mbar_init(&bars[kSFree + i], 4);
+      ptx::mbar_init(&bars[kSFree + i], 8);
     }
     ptx::mbar_init(&bars[kDrain], 1);
     *gave_up = 0;
@@ -510,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   bool aborted = false;
   ptx::griddep_wait();
-  count_units(p, prefix, warp_sums, S::kTokens, 1);
+  count_units<kThreads>(p, prefix, warp_sums, S::kTokens, 1);
   const int total = prefix[p.num_seqs];
   const int share = total / gridDim.x, extra = total - share * gridDim.x;
   auto run_begin = [&](int c) { return c * share + min(c, extra); };
@@ -606,21 +638,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (late) aborted = true;
     }
     aborted = __any_sync(0xffffffffu, aborted);
-  } else if (warp < 4) {
-    // ==================== sums: one token per thread ====================
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  } else {
+    // ============ sums: one token and half of a row tile per thread ============
+    const int half = warp >> 2, r = tid & 127;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     uint32_t k = 0;
     tiles([&](int seq, int len, int tile) {
-      const int tok = tile * 128 + tid;
+      const int tok = tile * 128 + r;
       float s0 = 0.f, s1 = 0.f;
+      // rows that are nobody's, or see nothing: 2^(s - inf) = 0
+      auto lse_of = [&](int i) {
+        const int kvh = i / L.row_tiles, first = (i - kvh * L.row_tiles) * L.tile_queries * L.group;
+        const int rows = min(L.tile_queries * L.group, L.rows - first);
+        return half == 0 && r < rows ? __ldcg(L.lse + seq * all_rows + static_cast<int64_t>(kvh) * L.rows + first + r)
+                                     : CUDART_INF_F;
+      };
+      float ahead = lse_of(0);
       for (int i = 0; i < inner; ++i, ++k) {  // (a warp that gave up still meets the others at the barrier)
-        const int kvh = i / L.row_tiles, rt = i - kvh * L.row_tiles;
+        const int rt = i % L.row_tiles;
         const uint32_t two = k & 1u;
-        const int row = rt * L.tile_queries * L.group + tid, rows = min(L.tile_queries * L.group, L.rows - (row - tid));
-        // rows that are nobody's, or see nothing: 2^(s - inf) = 0
-        row_lse[two][tid] =
-            tid < rows ? __ldcg(L.lse + seq * all_rows + static_cast<int64_t>(kvh) * L.rows + row) : CUDART_INF_F;
-        ptx::bar_sync(1, 128);
+        const int rows = min(L.tile_queries * L.group, L.rows - rt * L.tile_queries * L.group);
+        if (half == 0) row_lse[two][r] = ahead;
+        ptx::bar_sync(1, 256);
+        if (i + 1 < inner) ahead = lse_of(i + 1);
         wait(&bars[kSFull + two], (k >> 1) & 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
         ptx::tc_fence_after();
@@ -629,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int from = q0 > 0 ? q0 * L.group : 0;
         const bool all = __all_sync(0xffffffffu, from == 0) && rows == 128;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = half * 64; c < half * 64 + 64; c += 32) {
           uint32_t v[32];
           load_now(at + two * 128 + c, v);
           if (all) {
@@ -653,7 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0 && !aborted) ptx::mbar_arrive(&bars[kSFree + two]);
       }
-      if (tok < len && !aborted) p.weights[seq * p.weights_stride + tok] += s0 + s1;
+      if (half) other[r] = s0 + s1;
+      ptx::bar_sync(1, 256);
+      if (!half && tok < len && !aborted) p.weights[seq * p.weights_stride + tok] += s0 + s1 + other[r];
     });
   }
 
@@ -673,9 +715,9 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // Scores stored or formed again, by a kv head's rows.  Stored they cost 8 bytes a row
 // and token, and an exponential; again a product of 128 rows, whatever number of
 // them there are, and the keys once more.  4 x 8192 tokens, 8 kv heads of 128 dims,
-// stored and again: 64 rows 58 and 64 us, 72 rows 63 and 65, 80 rows 67 and 65, 128
-// rows 101 and 58 (64 dims: 64 rows 50 and 60, 80 rows 66 and 60).
-bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > 76; }
+// stored and again: 48 rows 52 and 54 us, 64 rows 60 and 54, 128 rows 101 and 52 (64
+// dims: 48 rows 45 and 50, 64 rows 52 and 50; 64 x 1000 tokens, 64 rows: 101 and 99).
+bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > 56; }
 // of one sequence: its rows' logarithms, tiles' statistics and scores
 int64_t seq_bytes(int64_t rows, bool stored, int max_context_len) {
   return rows * (4 + up(max_context_len, 128) / kStatTokens * 8 + (stored ? up(max_context_len, 128) * 4 : 0));
@@ -693,15 +735,15 @@ int seqs_of(int num_seqs, int64_t rows, int num_kv_heads, int head_dim, int max_
 }
 
 // one CTA per SM, launched while the kernel before drains
-cudaError_t launch_walk(const void* fn, int smem, const Launch& L, const CUtensorMap& tm_k, const CUtensorMap& tm_q,
+cudaError_t launch_walk(const void* fn, int threads, int smem, const Launch& L, const CUtensorMap& tm_k, const CUtensorMap& tm_q,
                         int64_t most_units, cudaStream_t stream) {
   int per_sm = 0;
-  const cudaError_t e = fp4_occupancy(fn, kThreads, smem, &per_sm);
+  const cudaError_t e = fp4_occupancy(fn, threads, smem, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count();
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(most_units < 1 ? 1 : (most_units < sms ? most_units : sms)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -741,7 +783,7 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
   L.bs_log = __builtin_ctz(static_cast<unsigned>(p.block_size));
   L.pitch = up(p.max_context_len, 128);
   const bool few = L.rows <= 16 && tokens == 128;
-  const int stat_tokens = few ? kStatTokens : tokens;
+  const int stat_tokens = few ? kStatTokens : tokens / halves_of(NC, false);
   L.tiles_pitch = static_cast<int>(L.pitch / stat_tokens);
   unsigned char* at = p.ws + 256;
   const bool twice = again(L.rows, p.head_dim);
@@ -779,14 +821,14 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
                                : reinterpret_cast<const void*>(&scores_kernel<9, false>);
     const int n = L.p.num_seqs;
     const int smem = NC == 1 ? smem_of<1>(n) : NC == 2 ? smem_of<2>(n) : NC == 4 ? smem_of<4>(n) : smem_of<9>(n);
-    cudaError_t e = launch_walk(fn, smem, L, tm_k, tm_q, tiles * p.num_kv_heads * L.row_tiles, stream);
+    cudaError_t e = launch_walk(fn, threads_of(NC, few), smem, L, tm_k, tm_q, tiles * p.num_kv_heads * L.row_tiles, stream);
     if (e != cudaSuccess) return e;
     const int64_t warps = rows * L.p.num_seqs;
     e = launch_early(lse_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, stream, L, stat_tokens);
     if (e != cudaSuccess) return e;
     if (twice)
-      e = launch_walk(NC == 1 ? reinterpret_cast<const void*>(&again_kernel<1>) : reinterpret_cast<const void*>(&again_kernel<2>), smem,
-                      L, tm_k, tm_q, tiles, stream);
+      e = launch_walk(NC == 1 ? reinterpret_cast<const void*>(&again_kernel<1>) : reinterpret_cast<const void*>(&again_kernel<2>),
+                      kThreads, smem, L, tm_k, tm_q, tiles, stream);
     else
       e = launch_early(add_kernel, dim3(static_cast<unsigned>(L.pitch / 128), static_cast<unsigned>(L.p.num_seqs)),
                      32 * kAddWarps, stream, L);
