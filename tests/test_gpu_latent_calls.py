@@ -105,7 +105,7 @@ def test_prefills_on_two_streams(ops):
         wp = ops.make_prefill_workspace_latent(len(chunks), H, LATENT, ROPE, HEAD, 16, max(n for _, n in chunks), most, total)
         out = torch.zeros(q.shape[0], H, HEAD, dtype=dt, device="cuda")
         args = [dev16(q), dev16(cache), dev16(w_k), dev16(w_v), dev(np.asarray(cu, np.int32)), dev(np.asarray(start, np.int32)), dev(tables)]
-        ref = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.07)
+        ref = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.07, two=dt == torch.float32)
         cases.append((out, args, max(n for _, n in chunks), most, total, wp, torch.cuda.Stream(), ref))
     torch.cuda.synchronize()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -116,6 +116,17 @@ def test_prefills_on_two_streams(ops):
     assert int(status.item()) == 0
     for out, *_, ref in cases:
         check(out, *ref, out.dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("chunks,H", [([(4000, 3)], 2), ([(1500, 70), (0, 2)], 3), ([(0, 100)], 1), ([(900, 65), (0, 0), (31, 1)], 5), ([(0, 1)] * 3, 1)])
+def test_fp32_prefill_with_split_keys(ops, chunks, H):
+    """Few queries: their keys are shared among CTAs, some of which see nothing
+    of a row's, and rows of nobody stay."""
+    rng = np.random.default_rng(41 + H)
+    lens, tables, cache, cu, q, w_k, w_v = prefill_case(rng, chunks, 16, H, pad=-1)
+    start = [s for s, _ in chunks]
+    out = run_prefill(ops, q, dev16(cache), w_k, w_v, cu, start, tables, 16, 0.07, max(n for _, n in chunks) + 40, max(lens), sum(lens) + 5)
+    check(out, *O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.07, two=True), False)
 
 
 @pytest.mark.parametrize("H,dt", [(16, torch.float32), (32, torch.bfloat16), (17, torch.float32)])
