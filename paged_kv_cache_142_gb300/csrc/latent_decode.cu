@@ -194,6 +194,18 @@ __device__ __forceinline__ void store16(const LatentDecodeParams& p, int64_t at,
   }
 }
 
+// Of the tokens from .. upto - 1 of a stretch of staged rows, those of `odd` whose
+// latent columns are not all finite become zero.  By a whole warp, 8 columns a lane.
+__device__ __forceinline__ void clear_odd(unsigned char* rows, uint32_t odd, int from, int upto, int lane) {
+  for (int j = from; j < upto; ++j) {
+    if (!((odd >> j) & 1u)) continue;
+    uint4* at = reinterpret_cast<uint4*>(rows + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16);
+    const uint4 x = *at;
+    auto bad = [](uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; };
+    if (__any_sync(0xffffffffu, bad(x.x) || bad(x.y) || bad(x.z) || bad(x.w))) *at = make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <bool HI, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ Launch L, const __grid_constant__ CUtensorMap tm_lat,
@@ -610,11 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= 1u << j;
           odd = __shfl_sync(0xffffffffu, odd, 0);
           const int from = max(0, limit_min - t * kTile - part * 16), upto = min(16, limit_max - t * kTile - part * 16);
-          unsigned char* stage = smem + (k % kStages) * kStageBytes + part * 2 * 4096;
-          for (int j = from; j < upto; ++j)
-            if ((odd >> j) & 1u)
-              *reinterpret_cast<uint4*>(stage + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+          if (odd) wait(&bars[kFull + k % kStages], (k / kStages) & 1u, aborted);
+          clear_odd(smem + (k % kStages) * kStageBytes + part * 2 * 4096, odd, from, upto, lane);
         }
         wait(&bars[kXFull + group], ph, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
@@ -745,9 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (r == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], L.quarters * 32 * kTile * 4);
         // Tokens that some rows of the tile see and others do not: a value among
-        // this CTA's columns that is not finite makes every row's partial sum
-        // not finite.  It becomes zero, so that 0 * NaN does not reach the rows
-        // that do not see it; the others have the score.
+        // this CTA's columns that is not finite becomes zero, so that 0 * NaN does
+        // not reach the rows that do not see it; the others have the score.  Such a
+        // value makes every row's partial sum not finite, so row 0's says which
+        // tokens to look at (its query may be what is not finite, or its sum may
+        // have overflowed: the value itself decides).
         if (quarter == 0 && limit_min < limit_max && limit_min < (t + 1) * kTile) {
           uint32_t odd = 0;
 #pragma unroll
@@ -755,11 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((s[j] & 0x7f800000u) == 0x7f800000u) odd |= 1u << j;
           odd = __shfl_sync(0xffffffffu, odd, 0);
           const int from = max(0, limit_min - t * kTile - half * 32), upto = min(32, limit_max - t * kTile - half * 32);
-          unsigned char* stage = smem + (k % kStages) * kStageBytes + half * 4 * 4096;
-          for (int j = from; j < upto; ++j)
-            if ((odd >> j) & 1u)
-              *reinterpret_cast<uint4*>(stage + (j >> 3) * 4096 + (lane >> 3) * 1024 + (j & 7) * 128 + (lane & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+          if (odd) wait(&bars[kFull + k % kStages], (k / kStages) & 1u, aborted);
+          clear_odd(smem + (k % kStages) * kStageBytes + half * 4 * 4096, odd, from, upto, lane);
         }
         wait(&bars[kXFull + group], ph, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
