@@ -687,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               s0 += c + j >= from && c + j < rows
                         ? fp4::fast_exp2(fmaf(__uint_as_float(v[j]), p.scale_log2, -row_lse[two][c + j]))
                         : 0.f;
+            __syncwarp();  // the next load is the whole warp's
           }
         }
         ptx::tc_fence_before();

@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
     }
     const uint4 y = valid ? __ldg(src + 64 + rank * 4 + quad) : make_uint4(0, 0, 0, 0);
+    __syncwarp();  // the stores are the whole warp's
     ptx::tmem_st32(tmem + lanes + kColQ + quad * 32, v);
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tmem + lanes + kColQ + 128 + quad * 4),
                  "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
       uint32_t v[32];
+      __syncwarp();  // the load is the whole warp's, lanes without a row among it
       load_now(tmem + lanes + quad * 64 + c * 32, v);
       if (c == 1) {  // O is read: the next item's P V may write it
         ptx::tc_fence_before();

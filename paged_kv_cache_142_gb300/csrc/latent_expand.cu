@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tma_store_2d(map, half * 64, static_cast<int>(h * x.rows + row), box);
+            __syncwarp();  // loads of tensor memory are the whole warp's
           }
         };
         load_row(d + 128, w);  // values first
