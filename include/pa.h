@@ -651,7 +651,9 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
  *   k_cache  bf16 [num_blocks][num_kv_heads][block_size][head_dim]; head_dim 64,
  *            128, 256, or 576 (a latent cache: one kv head); block_size 8 to
  *            256; num_q_heads / num_kv_heads 1 to 128; up to 65535 sequences
- *   workspace, tables and lengths: as in pa_decode_latent
+ *   workspace, tables and lengths: as in pa_decode_latent; the size grows with
+ *            each argument, so that one made for the longest window and context
+ *            serves every smaller call
  *
  * pa_select_tokens: of sequence i's positions [dst_start[i], context_lens[i])
  * the n = cu_keep[i+1] - cu_keep[i] that stay: the last min(recent, n), and of

@@ -718,7 +718,8 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // them there are, and the keys once more.  4 x 8192 tokens, 8 kv heads of 128 dims,
 // stored and again: 48 rows 52 and 54 us, 64 rows 60 and 54, 128 rows 101 and 52 (64
 // dims: 48 rows 45 and 50, 64 rows 52 and 50; 64 x 1000 tokens, 64 rows: 101 and 99).
-bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > 56; }
+constexpr int kStoredRows = 56;
+bool again(int64_t rows, int head_dim) { return head_dim <= 128 && rows > kStoredRows; }
 // of one sequence: its rows' logarithms, tiles' statistics and scores
 int64_t seq_bytes(int64_t rows, bool stored, int max_context_len) {
   return rows * (4 + up(max_context_len, 128) / kStatTokens * 8 + (stored ? up(max_context_len, 128) * 4 : 0));
@@ -762,13 +763,24 @@ int smem_of(int num_seqs) {
 
 }  // namespace weights_detail
 
+// What a launch needs grows and shrinks with the window and the context: many rows
+// store no scores, and fewer long sequences fit one launch.  The size grows with
+// each argument, so that a workspace serves every smaller call: at least what any
+// launch of as many rows or fewer takes, which is one sequence or kScoreBytes.
 size_t weights_workspace(int num_seqs, int window, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len) {
   using namespace weights_detail;
   const int64_t rows = static_cast<int64_t>(window) * num_q_heads;
   if (num_seqs == 0) return 256;
-  const int seqs = seqs_of(num_seqs, rows, num_kv_heads, head_dim, max_context_len);
-  if (seqs == 0 || rows >= (int64_t(1) << 31)) return 0;
-  return static_cast<size_t>(256 + 3 * 256 + seqs * seq_bytes(rows, !again(rows / num_kv_heads, head_dim), max_context_len));
+  if (rows >= (int64_t(1) << 31) || seqs_of(num_seqs, rows, num_kv_heads, head_dim, max_context_len) == 0) return 0;
+  auto bound = [&](int64_t n, bool stored) {
+    const int64_t one = seq_bytes(n, stored, max_context_len), all = one * num_seqs;
+    const int64_t most = one > kScoreBytes ? one : kScoreBytes;
+    return all < most ? all : most;
+  };
+  const int64_t store = head_dim <= 128 ? static_cast<int64_t>(kStoredRows) * num_kv_heads : rows;
+  int64_t bytes = bound(rows < store ? rows : store, true);
+  if (rows > store && bound(rows, false) > bytes) bytes = bound(rows, false);
+  return static_cast<size_t>(256 + 3 * 256 + bytes);
 }
 
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {

@@ -703,7 +703,8 @@ def pa_prefill_latent(out, q, cache, w_k, w_v, cu_q, q_start, block_tables, scal
 # --------------------------------------------------------------------------
 def make_workspace_weights(num_seqs, window, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                            device="cuda") -> torch.Tensor:
-    """A zero-filled pa_accumulate_weights workspace of the required size."""
+    """A zero-filled pa_accumulate_weights workspace; made for the longest window
+    and context, it serves every smaller call."""
     n = _LIB.pa_accumulate_weights_workspace_size(num_seqs, window, num_q_heads, num_kv_heads, head_dim, block_size,
                                                   int(max_context_len))
     if n == 0:
