@@ -665,6 +665,8 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
  *   status   device int32, caller-zeroed, or NULL: PA_ERR_INVALID_ARG for a
  *            sequence whose range lies outside keep, is longer than its
  *            positions, or whose length passes max_context_len; it is left alone
+ *   With max_context_len 0 nothing stays and weights may be NULL; the call then
+ *   only reports, to a status that is given.
  * ---------------------------------------------------------------------- */
 size_t pa_accumulate_weights_workspace_size(int32_t num_seqs, int32_t window, int32_t num_q_heads,
                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,

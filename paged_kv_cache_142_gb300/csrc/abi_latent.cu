@@ -301,8 +301,11 @@ pa_status pa_select_tokens(int32_t* keep, int32_t num_keep, const int32_t* cu_ke
     return PA_ERR_INVALID_ARG;
   if (max_context_len > kMaxContext || static_cast<int64_t>(num_seqs) * 8 >= (int64_t(1) << 31))
     return PA_ERR_UNSUPPORTED;
-  if (num_seqs == 0 || max_context_len == 0) return PA_OK;
-  if ((!keep && num_keep > 0) || !cu_keep || !weights || !dst_start || !context_lens) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  // no sequence may have a token: a launch writes nothing and only reports those that do
+  if (max_context_len == 0 && !status) return PA_OK;
+  if ((!keep && num_keep > 0) || !cu_keep || (!weights && max_context_len > 0) || !dst_start || !context_lens)
+    return PA_ERR_INVALID_ARG;
   if (!aligned(keep, 4) || !aligned(cu_keep, 4) || !aligned(weights, 4) || !aligned(dst_start, 4) ||
       !aligned(context_lens, 4) || !aligned(status, 4))
     return PA_ERR_INVALID_ARG;
