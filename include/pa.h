@@ -654,6 +654,8 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
  *   workspace, tables and lengths: as in pa_decode_latent; the size grows with
  *            each argument, so that one made for the longest window and context
  *            serves every smaller call
+ *   With max_context_len 0 the call only reports lengths above it, and with
+ *   weights NULL beside that does nothing.
  *
  * pa_select_tokens: of sequence i's positions [dst_start[i], context_lens[i])
  * the n = cu_keep[i+1] - cu_keep[i] that stay: the last min(recent, n), and of

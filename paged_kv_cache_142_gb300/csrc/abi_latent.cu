@@ -265,7 +265,8 @@ pa_status pa_accumulate_weights(float* weights, int64_t weights_stride, const vo
   const size_t need = pa_accumulate_weights_workspace_size(num_seqs, window, num_q_heads, num_kv_heads, head_dim,
                                                            block_size, max_context_len);
   if (need == 0 || !pool_ok(static_cast<int64_t>(num_blocks) * num_kv_heads, block_size)) return PA_ERR_UNSUPPORTED;
-  if (num_seqs == 0 || max_context_len == 0) return PA_OK;
+  // (bounds of 0: nothing is added, and the call only reports lengths that pass them)
+  if (num_seqs == 0 || (max_context_len == 0 && !weights)) return PA_OK;
   if (!weights || !q || !k_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
   if (!aligned(weights, 4) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(block_tables, 4) ||
       !aligned(context_lens, 4))

@@ -836,6 +836,7 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
     const int smem = NC == 1 ? smem_of<1>(n) : NC == 2 ? smem_of<2>(n) : NC == 4 ? smem_of<4>(n) : smem_of<9>(n);
     cudaError_t e = launch_walk(fn, threads_of(NC, few), smem, L, tm_k, tm_q, tiles * p.num_kv_heads * L.row_tiles, stream);
     if (e != cudaSuccess) return e;
+    if (p.max_context_len == 0) continue;  // it has reported the lengths; no token has a weight
     const int64_t warps = rows * L.p.num_seqs;
     e = launch_early(lse_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, stream, L, stat_tokens);
     if (e != cudaSuccess) return e;

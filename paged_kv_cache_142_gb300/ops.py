@@ -740,8 +740,9 @@ def pa_accumulate_weights(weights, q, k_cache, block_tables, context_lens, scale
     _workspace(workspace)
     dev = torch.cuda.current_device()
     _all_on(dev, weights, q, k_cache, block_tables, context_lens, workspace)
+    # (weights without columns have no address, and nothing of them is touched; the lengths are looked at all the same)
     L.check(_LIB.pa_accumulate_weights(
-        weights.data_ptr(), weights.stride(0), q.data_ptr(), B, W, H, k_cache.data_ptr(), NB, bs, Hkv, D,
+        weights.data_ptr() or workspace.data_ptr(), weights.stride(0), q.data_ptr(), B, W, H, k_cache.data_ptr(), NB, bs, Hkv, D,
         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), float(scale),
         workspace.data_ptr(), workspace.numel(), _stream(stream, dev)), "pa_accumulate_weights")
 

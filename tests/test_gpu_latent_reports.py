@@ -31,3 +31,18 @@ def test_selection_bounded_by_no_tokens(ops, cu, start, lens, bad, width):
     assert (keep == -1).all() and (w == 5).all()
     ops.pa_select_tokens(keep, ints(*cu), w, ints(*start), ints(*lens), 1, 0)  # nobody to tell
     assert (keep == -1).all() and (w == 5).all()
+
+
+@pytest.mark.parametrize("width", [0, 4])
+@pytest.mark.parametrize("window,heads,d", [(1, 8, 128), (40, 8, 64), (2, 4, 576), (3, 2, 256)])
+def test_weights_bounded_by_no_tokens(ops, window, heads, d, width):
+    hkv = 1 if d == 576 else 2
+    q = torch.randn(3, window, heads, d, device="cuda").bfloat16()
+    cache = torch.randn(4, hkv, 16, d, device="cuda").bfloat16()
+    tables = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    w = torch.full((3, width), 5.0, device="cuda")
+    for lens, error in (((0, 0, 0), 0), ((0, 1, 0), 1), ((0, 0, -1), 1), ((2 ** 31 - 1, 0, 0), 1)):
+        ws = ops.make_workspace_weights(3, window, heads, hkv, d, 16, 0)
+        ops.pa_accumulate_weights(w, q, cache, tables, ints(*lens), 0.1, hkv, 0, ws)
+        assert ops.pa_workspace_error(ws) == error
+        assert (w == 5).all()
