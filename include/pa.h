@@ -620,7 +620,9 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
  *              chunk that lies outside q, is longer than max_q_len, ends behind
  *              its table or max_context_len, or whose context does not fit
  *              total_context (its rows stay as they are), and for a table entry
- *              outside the pool (read as block 0); PA_ERR_DEVICE_TIMEOUT
+ *              outside the pool (read as block 0); PA_ERR_DEVICE_TIMEOUT.  With
+ *              num_tokens or max_q_len 0 the call only reports, to a status
+ *              that is given
  *   workspace  pa_prefill_latent_workspace_size bytes, 256-byte aligned, needs
  *              no initialisation; calls that overlap on the GPU use different ones
  */

@@ -206,8 +206,12 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
   const size_t need = pa_prefill_latent_workspace_size(num_seqs, num_heads, latent_dim, rope_dim, head_dim, block_size,
                                                        max_q_len, max_context_len, total_context);
   if (need == 0 || !pool_ok(num_blocks, block_size)) return PA_ERR_UNSUPPORTED;
-  if (num_tokens == 0 || num_seqs == 0 || max_q_len == 0) return PA_OK;
-  if (!out || !q || !cu_q || !q_start || !cache || !w_k || !w_v || !block_tables) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  // no chunk may have a token: the plan alone runs, and reports those that do
+  const bool nothing = num_tokens == 0 || max_q_len == 0;
+  if (nothing && !status) return PA_OK;
+  if (!cu_q || !q_start || (!nothing && (!out || !q || !cache || !w_k || !w_v || !block_tables)))
+    return PA_ERR_INVALID_ARG;
   if (!aligned(out, 32) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(w_k, 16) || !aligned(w_v, 16) ||
       !aligned(cu_q, 4) || !aligned(q_start, 4) || !aligned(block_tables, 4) || !aligned(status, 4))
     return PA_ERR_INVALID_ARG;

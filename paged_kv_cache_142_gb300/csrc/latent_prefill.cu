@@ -655,7 +655,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t str
   x.v = take(x.rows * all * 256);
   x.heads = pass;
   cudaError_t e = launch_latent_plan(p, x, stream);
-  if (e != cudaSuccess || x.rows == 0) return e;
+  if (e != cudaSuccess || x.rows == 0 || p.num_tokens == 0 || p.max_q_len == 0) return e;
   if (x.f32) {
     for (int h = 0; h < p.num_heads; h += pass) {
       x.head0 = h;

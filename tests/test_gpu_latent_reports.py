@@ -46,3 +46,22 @@ def test_weights_bounded_by_no_tokens(ops, window, heads, d, width):
         ops.pa_accumulate_weights(w, q, cache, tables, ints(*lens), 0.1, hkv, 0, ws)
         assert ops.pa_workspace_error(ws) == error
         assert (w == 5).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,longest,cu,bad", [
+    (0, 4, (0, 3), True), (0, 4, (0, 0), False), (5, 0, (0, 5), True), (5, 0, (0, 0), False), (0, 0, (0, 0, 1, 1), True),
+    (0, 4, (0, -1), True), (5, 4, (0, 5), True), (5, 0, (5, 5), False)])
+def test_prefill_bounded_by_no_queries(ops, tokens, longest, cu, bad, dt):
+    S, H = len(cu) - 1, 2
+    e = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((tokens, H, 128), -7.0, dtype=dt, device="cuda")
+    ws = ops.make_prefill_workspace_latent(S, H, 512, 64, 128, 16, longest, 16, 16)
+    tables, start = torch.zeros(S, 1, dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    args = (out, e(tokens, H, 192), e(4, 16, 576), e(H, 128, 512), e(H, 128, 512), ints(*cu), start, tables, 0.1, longest, 16, 16, ws)
+    status = new_status()
+    ops.pa_prefill_latent(*args, status=status)
+    assert int(status.item()) == int(bad)
+    assert (out == -7).all()
+    ops.pa_prefill_latent(*args)  # nobody to tell
+    assert (out == -7).all()
