@@ -515,7 +515,8 @@ pa_status pa_prefill_fp4(void* out, pa_dtype out_dtype, const void* q, int32_t n
  *                      table entry outside the pool (such a token is not
  *                      moved), for a count outside [0, max_keep] and for a
  *                      range of keep that ends behind cu_keep[num_seqs] (such
- *                      a sequence is left alone)
+ *                      a sequence is left alone); with max_keep 0 the call
+ *                      only reports, to a status that is given
  * Blocks that are written must belong to one sequence only
  * (pa_alloc_make_writable); afterwards pa_alloc_truncate frees the rest.
  * ---------------------------------------------------------------------- */

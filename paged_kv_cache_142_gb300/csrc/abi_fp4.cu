@@ -71,8 +71,12 @@ pa_status compact_impl(void* k_cache, void* v_cache, int64_t cache_layer_stride,
     return PA_ERR_INVALID_ARG;
   if (num_layers > 1 && (cache_layer_stride * e < layer || (cache_layer_stride * e) % 16 != 0))
     return PA_ERR_INVALID_ARG;
-  if (num_seqs == 0 || max_keep == 0) return PA_OK;
-  if (!k_cache || !v_cache || !block_tables || !dst_start || !keep || !cu_keep) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  // no sequence may keep a token: a launch moves nothing and only reports those that do
+  const bool nothing = max_keep == 0;
+  if (nothing && !status) return PA_OK;
+  if (!dst_start || !cu_keep || (!nothing && (!k_cache || !v_cache || !block_tables || !keep)))
+    return PA_ERR_INVALID_ARG;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) || !aligned(dst_start, 4) ||
       !aligned(keep, 4) || !aligned(cu_keep, 4) || !aligned(status, 4))
     return PA_ERR_INVALID_ARG;

@@ -104,8 +104,11 @@ pa_status pa_compact_tokens_latent(void* cache, int64_t cache_layer_stride, int3
     return PA_ERR_INVALID_ARG;
   if (num_layers > 1 && (cache_layer_stride * e < row * block_size * num_blocks || cache_layer_stride * e % 16 != 0))
     return PA_ERR_INVALID_ARG;
-  if (num_seqs == 0 || max_keep == 0) return PA_OK;
-  if (!cache || !block_tables || !dst_start || !keep || !cu_keep) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  // no sequence may keep a token: a launch moves nothing and only reports those that do
+  const bool nothing = max_keep == 0;
+  if (nothing && !status) return PA_OK;
+  if (!dst_start || !cu_keep || (!nothing && (!cache || !block_tables || !keep))) return PA_ERR_INVALID_ARG;
   if (!aligned(cache, 16) || !aligned(block_tables, 4) || !aligned(dst_start, 4) || !aligned(keep, 4) ||
       !aligned(cu_keep, 4) || !aligned(status, 4))
     return PA_ERR_INVALID_ARG;

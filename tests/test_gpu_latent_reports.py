@@ -65,3 +65,23 @@ def test_prefill_bounded_by_no_queries(ops, tokens, longest, cu, bad, dt):
     assert (out == -7).all()
     ops.pa_prefill_latent(*args)  # nobody to tell
     assert (out == -7).all()
+
+
+@pytest.mark.parametrize("latent", [True, False])
+@pytest.mark.parametrize("entries,most,cu,bad", [(0, 5, (0, 2), True), (0, 5, (0, 0), False), (4, 0, (0, 2), True),
+                                                 (4, 0, (0, 0, 0), False), (4, 0, (0, 0, -1), True)])
+def test_compaction_bounded_by_no_tokens(ops, entries, most, cu, bad, latent):
+    S = len(cu) - 1
+    shape = (4, 16, 576) if latent else (4, 2, 16, 64)
+    cache = torch.randn(shape, device="cuda").bfloat16()
+    before = cache.clone()
+    tables = torch.tensor([[0, 1]] * S, dtype=torch.int32, device="cuda")
+    keep, start = torch.arange(entries, dtype=torch.int32, device="cuda") + 3, torch.zeros(S, dtype=torch.int32, device="cuda")
+    args = (tables, start, keep, ints(*cu), most)
+    call = (lambda **kw: ops.pa_compact_tokens_latent(cache, *args, **kw)) if latent else (
+        lambda **kw: ops.pa_compact_tokens(cache, cache, *args, **kw))
+    status = new_status()
+    call(status=status)
+    assert int(status.item()) == int(bad)
+    call()  # nobody to tell
+    assert torch.equal(cache, before)
