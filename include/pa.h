@@ -301,7 +301,12 @@ pa_status pa_decode_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
  * workspace must be zeroed again (pa_workspace_init) before its next use.
  * The same stop path serves any real wait that runs out its 2 s limit.
  * pa_decode_fp4 takes the hook too: the warps of a CTA wait so before they join
- * their sums, and the CTA then stops and reports in the same way. */
+ * their sums, and the CTA then stops and reports in the same way.
+ * pa_decode_latent, pa_prefill_latent and pa_accumulate_weights take it too:
+ * the warps that take scores or results give up at their first tile.  There
+ * the other roles have no stop word and run out their own 2 s limits, a few
+ * seconds a call; the outputs (the weights) are left undefined, and the report
+ * is in the workspace, of the prefill in its status. */
 void pa_test_stall_decode(uint64_t ns);
 
 /* Zero a decode workspace (enqueued on `stream`). */

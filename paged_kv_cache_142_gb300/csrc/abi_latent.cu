@@ -181,6 +181,7 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
   p.scale_log2 = scale * kLog2e;
   p.err = static_cast<int32_t*>(workspace);
   p.ws = static_cast<unsigned char*>(workspace);
+  p.test_stall_ns = pa::test_stall_ns();
   return pa::launch_latent_decode(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -244,6 +245,7 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
   p.scale_log2 = scale * kLog2e;
   p.status = status;
   p.ws = static_cast<unsigned char*>(workspace);
+  p.test_stall_ns = pa::test_stall_ns();
   return pa::launch_latent_prefill(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -298,6 +300,7 @@ pa_status pa_accumulate_weights(float* weights, int64_t weights_stride, const vo
   p.scale_log2 = scale * kLog2e;
   p.err = static_cast<int32_t*>(workspace);
   p.ws = static_cast<unsigned char*>(workspace);
+  p.test_stall_ns = pa::test_stall_ns();
   return pa::launch_weights(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -57,7 +57,7 @@ struct Shape {
   static constexpr int kOffPrefix = kOffBar + 256;
 };
 
-enum : int { kFull = 0, kFree = 8, kQFull = 16, kQFree = 18, kSFull = 20, kSFree = 22, kDrain = 24, kNumBars = 25 };
+enum : int { kFull = 0, kFree = 8, kQFull = 16, kQFree = 18, kSFull = 20, kSFree = 22, kDrain = 24, kNever = 25, kNumBars = 26 };
 
 struct Launch {
   WeightsParams p;
@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(threads_of(NC, FEW), 1)
       ptx::mbar_init(&bars[kSFree + i], 4 * kHalves);
     }
     ptx::mbar_init(&bars[kDrain], 1);
+    ptx::mbar_init(&bars[kNever], 1);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
@@ -279,6 +280,10 @@ __global__ void __launch_bounds__(threads_of(NC, FEW), 1)
       ahead.first = first;
     });
     if (any) issue();
+    if (aborted) {
+      wait_for_loads(&bars[kFull], S::kStages, k);
+      wait_for_loads(&bars[kQFull], S::kQSlots, qk);
+    }
   } else if (warp == 9) {
     // ============================ products ============================
     const bool leader = elect_one();
@@ -326,6 +331,8 @@ __global__ void __launch_bounds__(threads_of(NC, FEW), 1)
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + buffer * 128;
     uint32_t k = 0;
     const int64_t all_rows = static_cast<int64_t>(p.num_kv_heads) * L.rows;
+    if (p.test_stall_ns && !ptx::mbar_wait(&bars[kNever], 0, p.test_stall_ns)) aborted = true;  // pa_test_stall_decode
+    __syncwarp();
     walk.each([&](const Unit& x, bool, bool) {
       const uint32_t mine = k++;
       if (aborted || (mine & 1u) != buffer) return;
@@ -530,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kSFree + i], 8);
     }
     ptx::mbar_init(&bars[kDrain], 1);
+    ptx::mbar_init(&bars[kNever], 1);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
@@ -602,6 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     });
+    if (aborted) {
+      wait_for_loads(&bars[kFull], S::kStages, k);
+      wait_for_loads(&bars[kQFull], 2, k);
+    }
   } else if (warp == 9) {
     // ============================ products ============================
     const bool leader = elect_one();
@@ -643,6 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, r = tid & 127;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     uint32_t k = 0;
+    if (p.test_stall_ns && !ptx::mbar_wait(&bars[kNever], 0, p.test_stall_ns)) aborted = true;  // pa_test_stall_decode
+    __syncwarp();
     tiles([&](int seq, int len, int tile) {
       const int tok = tile * 128 + r;
       float s0 = 0.f, s1 = 0.f;

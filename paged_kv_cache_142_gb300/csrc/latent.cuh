@@ -24,6 +24,7 @@ struct LatentDecodeParams {
   float scale_log2;  // softmax scale * log2(e)
   int32_t* err;      // the workspace's error word
   unsigned char* ws;
+  uint64_t test_stall_ns;  // timeout-path test hook (0 = off): scores begin with a wait for what never comes, this long
 };
 
 struct LatentPrefillParams {
@@ -42,6 +43,7 @@ struct LatentPrefillParams {
   float scale_log2;
   int32_t* status;  // may be null
   unsigned char* ws;
+  uint64_t test_stall_ns;  // as in decode, in the expansion's and the attention's results
 };
 
 // What the kernels of one pa_prefill_latent call share, in its workspace.  Tokens
@@ -89,6 +91,7 @@ struct WeightsParams {
   float scale_log2;
   int32_t* err;
   unsigned char* ws;
+  uint64_t test_stall_ns;  // as in decode
 };
 
 struct SelectParams {

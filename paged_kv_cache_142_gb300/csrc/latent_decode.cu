@@ -80,7 +80,7 @@ __host__ __device__ constexpr int stages_of(bool hi, bool narrow) { return narro
 // barriers
 enum : int {
   kFull = 0, kEmpty = 5, kQFull = 10, kSFree = 11, kSFull = 12, kXFull = 15, kXFree = 18, kPFull = 21, kPFree = 24,
-  kODone = 27, kOFree = 30, kDrain = 31, kLFull = 33, kLFree = 34, kRef = 35, kNumBars = 43
+  kODone = 27, kOFree = 30, kDrain = 31, kLFull = 33, kLFree = 34, kRef = 35, kNever = 43, kNumBars = 44
 };
 // shared memory, behind the stages: P slots, the exchange, then
 constexpr int kOffBar = 0;
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 8; ++i) ptx::mbar_init(&bars[kRef + i], NARROW ? 4 : 2);
     ptx::mbar_init(&bars[kDrain], 1);
     ptx::mbar_init(&bars[kDrain + 1], 1);
+    ptx::mbar_init(&bars[kNever], 1);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
@@ -319,6 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     aborted = __any_sync(0xffffffffu, aborted);
   };
 
+  auto stall = [&]() {  // pa_test_stall_decode
+    if (p.test_stall_ns && !ptx::mbar_wait(&bars[kNever], 0, p.test_stall_ns)) aborted = true;
+    __syncwarp();
+  };
   // a quarter of an item's queries into tensor memory, once all scores of the item before are formed
   auto load_queries = [&](const Item& it, uint32_t lanes, int r, int quad) {
     const int row = it.rt * 128 + r;
@@ -447,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     });
+    if (aborted) wait_for_loads(&bars[kFull], kStages, kt);
   } else if (warp == 17) {
     // ===================== products of the scores =====================
     const bool leader = elect_one();
@@ -587,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kt = 0, items = 0;
     bool first = true;
     const float f = p.scale_log2;
+    stall();
     walk.each([&](const Item& it, const Item& nxt, bool more) {
       const int row = it.rt * 128 + r;
       const int limit = row < L.rows ? seen_by(L, it, row) : 0;
@@ -616,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_async4(dst + (j * 32 + r) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
                          __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
         }
-        if (r == 0 && part == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], kXBytes);
+        // (not once this warp gave up: the bytes of a tile that never comes would be added to the next one's)
+        if (r == 0 && part == 0 && !aborted) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], kXBytes);
         if (limit_min < limit_max && limit_min < (t + 1) * kTile) {  // as below
           uint32_t odd = 0;
 #pragma unroll
@@ -722,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kt = 0;
     bool first = true;
     const float f = p.scale_log2;
+    stall();
     walk.each([&](const Item& it, const Item& nxt, bool more) {
       const int row = it.rt * 128 + r;
       const bool valid = row < L.rows;
@@ -754,7 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_async4(dst + (j * kRows + r) * 16, __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]),
                          __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), bar);
         }
-        if (r == 0 && half == 0) ptx::mbar_arrive_expect_tx(&bars[kXFull + group], L.quarters * 32 * kTile * 4);
+        if (r == 0 && half == 0 && !aborted)
+          ptx::mbar_arrive_expect_tx(&bars[kXFull + group], L.quarters * 32 * kTile * 4);
         // Tokens that some rows of the tile see and others do not: a value among
         // this CTA's columns that is not finite becomes zero, so that 0 * NaN does
         // not reach the rows that do not see it; the others have the score.  Such a
@@ -893,6 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) ptx::tmem_dealloc(tmem, 512);
   if (tid == 0 && *gave_up) atomicExch(p.err, kDevErrTimeout);
   cluster_sync();  // the other CTA may still signal this one's barriers
+  if (*gave_up) let_arrive();
 }
 
 // Parts of items added up.  The first cluster behind an item's start reports the

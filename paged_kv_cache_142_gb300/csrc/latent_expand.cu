@@ -96,7 +96,7 @@ constexpr int kOffB = kABytes, kOffOut = kOffB + kStages * kBBytes, kOffBar = kO
 constexpr int kSmemBytes = 1024 + kOffBar + 256;
 enum : int {
   kAFull = 0, kAFree = 1, kBFull = 2, kBFree = kBFull + kStages, kDFull = kBFree + kStages, kDFree = kDFull + 2,
-  kDrain = kDFree + 2, kNumBars = kDrain + 1
+  kDrain = kDFree + 2, kNever, kNumBars
 };
 static_assert(kNumBars * 8 + 16 <= 256, "barrier area");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kDFree + i], 8);
     }
     ptx::mbar_init(&bars[kDrain], 1);
+    ptx::mbar_init(&bars[kNever], 1);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
@@ -234,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t slot = kb % kStages;
         wait(&bars[kBFree + slot], ((kb / kStages) & 1u) ^ 1u, aborted);
         aborted = __any_sync(0xffffffffu, aborted);
-        if (!aborted && lane == 0) {
+        if (aborted) break;
+        if (lane == 0) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(&bars[kBFull + slot], 2 * kBBytes);
           tma_load_2d_pair(smem + kOffB + slot * kBBytes, rank ? &tm_wv : &tm_wk, ch * 64, h * 128,
                            first_of(&bars[kBFull + slot]), keep);
@@ -249,6 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&bars[kBFree + k % kStages], (k / kStages) & 1u, aborted);
     if (ka) wait(&bars[kAFree], (ka - 1) & 1u, aborted);
     aborted = __any_sync(0xffffffffu, aborted);
+    if (aborted && rank == 0) {  // (both CTAs' loads are counted here)
+      wait_for_loads(&bars[kAFull], 1, ka);
+      wait_for_loads(&bars[kBFull], kStages, kb);
+    }
   } else if (warp == 5) {
     // ============================ products ============================
     const bool leader = elect_one();
@@ -292,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool f32 = x.f32;
     uint32_t kd = 0;
     Tile t{0, 0, 0};
+    if (p.test_stall_ns && !ptx::mbar_wait(&bars[kNever], 0, p.test_stall_ns)) aborted = true;  // pa_test_stall_decode
+    aborted = __any_sync(0xffffffffu, aborted);
     for (int64_t u = u0; u < u1 && !aborted; ++u, ++kd) {
       if (u == u0 || u % x.heads == 0) t = tile_of(u, rank);
       const int h = static_cast<int>(u % x.heads);
@@ -397,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   cluster_sync();  // the other CTA may still load, read and signal here
+  if (*gave_up) let_arrive();
+  __syncwarp();
   if (warp == 5) tmem_dealloc_pair(tmem, 512);
   if (tid == 0 && *gave_up && p.status) atomicExch(p.status, kDevErrTimeout);
 }

@@ -57,7 +57,7 @@ constexpr float kSlack = 8.f;  // the reference is raised past 2^8
 // barriers
 enum : int {
   kFull = 0, kFree = kSlots, kQFull = 2 * kSlots, kQFree, kSFull, kPFull = kSFull + 2, kODone = kPFull + 2,
-  kOFree = kODone + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1
+  kOFree = kODone + 2, kDrain = kOFree + 2, kNever, kNumBars
 };
 static_assert(kNumBars * 8 + 32 <= 512, "barrier area");
 constexpr uint32_t kColO = 256;  // tensor memory: S of the tiles at 0 and 128, then O of the tiles
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kOFree + i], 4);
     }
     ptx::mbar_init(&bars[kDrain], 2);
+    ptx::mbar_init(&bars[kNever], 1);
     *gave_up = 0;
     ptx::mbar_init_fence();
   }
@@ -343,6 +344,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t + 1 < n) keys(it.t0 + t + 1);
         }
       });
+    if (aborted) {  // (lane 0)
+      wait_for_loads(&bars[kFull], kSlots, uc);
+      wait_for_loads(&bars[kQFull], 1, ic);
+    }
+    __syncwarp();
     aborted = __any_sync(0xffffffffu, aborted);
   } else if (warp >= 9) {
     // ============================ products ============================
@@ -451,6 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int trow = i * 128 + r;
     uint32_t sc = 0;  // steps of the tile
     const float f = fmaxf(p.scale_log2, 1.2e-38f);  // not zero: a masked -inf times it stays -inf
+    if (p.test_stall_ns && !ptx::mbar_wait(&bars[kNever], 0, p.test_stall_ns)) aborted = true;  // pa_test_stall_decode
+    aborted = __any_sync(0xffffffffu, aborted);
     walk.each([&](const Item& it) {  // a warp that gave up still meets the others below
       const int64_t row = static_cast<int64_t>(it.c.b + it.tok0 + trow) * p.num_heads + L.x.head0 + it.head;
       const bool valid = trow < it.ntok;

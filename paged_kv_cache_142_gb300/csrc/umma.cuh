@@ -74,6 +74,19 @@ __device__ __forceinline__ void store_async4(uint32_t dst, float a, float b, flo
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& aborted) {
   if (!aborted && !ptx::mbar_wait(bar, parity, kWaitLimitNs)) aborted = true;
 }
+// Loads that a giving-up warp issued and nobody waited for, `count` of them so far on a
+// ring of barriers: until the last of each are here.  Shared memory must not pass to
+// another CTA under them.
+__device__ __forceinline__ void wait_for_loads(uint64_t* bars, uint32_t ring, uint32_t count) {
+  bool late = false;
+  for (uint32_t k = count > ring ? count - ring : 0; k < count; ++k) wait(&bars[k % ring], (k / ring) & 1u, late);
+}
+// What a CTA that gave up may still get from its pair (sums, signals), which no
+// barrier counts once the two are out of step: time to arrive.
+__device__ __forceinline__ void let_arrive() {
+  const uint64_t t0 = ptx::global_ns();
+  while (ptx::global_ns() - t0 < 100000u) __nanosleep(1000);
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
