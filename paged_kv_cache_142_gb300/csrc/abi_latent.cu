@@ -175,8 +175,6 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
   p.block_size = block_size;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.max_context_len = max_context_len;
-  p.latent_dim = latent_dim;
-  p.rope_dim = rope_dim;
   p.out_bf16 = out_dtype == PA_DTYPE_BF16 ? 1 : 0;
   p.scale_log2 = scale * kLog2e;
   p.err = static_cast<int32_t*>(workspace);
@@ -193,7 +191,7 @@ size_t pa_prefill_latent_workspace_size(int32_t num_seqs, int32_t num_heads, int
       total_context + static_cast<int64_t>(num_seqs) * 128 >= (int64_t(1) << 31) ||
       check_attention(1, block_size, latent_dim, rope_dim) != PA_OK)
     return 0;
-  return pa::latent_prefill_workspace(num_seqs, num_heads, latent_dim, rope_dim, head_dim, total_context);
+  return pa::latent_prefill_workspace(num_seqs, num_heads, head_dim, total_context);
 }
 
 pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_t num_tokens, const int32_t* cu_q,
@@ -238,9 +236,6 @@ pa_status pa_prefill_latent(void* out, pa_dtype out_dtype, const void* q, int32_
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.max_q_len = max_q_len;
   p.max_context_len = max_context_len;
-  p.latent_dim = latent_dim;
-  p.rope_dim = rope_dim;
-  p.head_dim = head_dim;
   p.out_bf16 = out_dtype == PA_DTYPE_BF16 ? 1 : 0;
   p.scale_log2 = scale * kLog2e;
   p.status = status;

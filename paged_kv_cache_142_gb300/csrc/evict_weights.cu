@@ -828,8 +828,6 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
   const uint64_t ks[3] = {row, 128, 8 * row};
   const uint32_t kb[4] = {64, 8, static_cast<uint32_t>(NC), static_cast<uint32_t>(p.block_size < tokens ? p.block_size : tokens) / 8};
   if (!encode_bf16_tiles(&tm_k, 4, p.k_cache, kd, ks, kb, 128)) return cudaErrorInvalidValue;
-  const uint64_t qd[3] = {static_cast<uint64_t>(p.head_dim), static_cast<uint64_t>(p.num_q_heads),
-                          static_cast<uint64_t>(p.num_seqs) * p.window};
   const uint64_t qs[2] = {row, row * p.num_q_heads};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(group), static_cast<uint32_t>(p.window < L.tile_queries ? p.window : L.tile_queries)};
   for (int s0 = 0; s0 < p.num_seqs; s0 += seqs) {
@@ -839,8 +837,9 @@ cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
     L.p.q = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(s0) * rows * p.head_dim;
     L.p.block_tables += static_cast<int64_t>(s0) * p.max_blocks_per_seq;
     L.p.context_lens += s0;
-    const uint64_t qn[3] = {qd[0], qd[1], static_cast<uint64_t>(L.p.num_seqs) * p.window};
-    if (!encode_bf16_tiles(&tm_q, 3, L.p.q, qn, qs, qb, 128)) return cudaErrorInvalidValue;
+    const uint64_t qd[3] = {static_cast<uint64_t>(p.head_dim), static_cast<uint64_t>(p.num_q_heads),
+                            static_cast<uint64_t>(L.p.num_seqs) * p.window};
+    if (!encode_bf16_tiles(&tm_q, 3, L.p.q, qd, qs, qb, 128)) return cudaErrorInvalidValue;
     const int64_t tiles = L.pitch / tokens * L.p.num_seqs;
     const void* fn = NC == 1   ? (few ? reinterpret_cast<const void*>(&scores_kernel<1, true>) : reinterpret_cast<const void*>(&scores_kernel<1, false>))
                      : NC == 2 ? (few ? reinterpret_cast<const void*>(&scores_kernel<2, true>) : reinterpret_cast<const void*>(&scores_kernel<2, false>))

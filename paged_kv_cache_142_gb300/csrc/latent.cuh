@@ -19,7 +19,6 @@ struct LatentDecodeParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   int32_t num_seqs, q_len, num_heads, num_blocks, block_size, max_blocks_per_seq, max_context_len;
-  int32_t latent_dim, rope_dim;
   int32_t out_bf16;
   float scale_log2;  // softmax scale * log2(e)
   int32_t* err;      // the workspace's error word
@@ -38,7 +37,6 @@ struct LatentPrefillParams {
   const int32_t* block_tables;
   int64_t total_context;
   int32_t num_tokens, num_seqs, num_heads, num_blocks, block_size, max_blocks_per_seq, max_q_len, max_context_len;
-  int32_t latent_dim, rope_dim, head_dim;
   int32_t out_bf16;
   float scale_log2;
   int32_t* status;  // may be null
@@ -111,8 +109,7 @@ cudaError_t launch_latent_append(const void* latent, int64_t latent_stride_bytes
                                  cudaStream_t stream);
 size_t latent_decode_workspace(int num_seqs, int q_len, int num_heads, int max_context_len);
 cudaError_t launch_latent_decode(const LatentDecodeParams& p, cudaStream_t stream);
-size_t latent_prefill_workspace(int num_seqs, int num_heads, int latent_dim, int rope_dim, int head_dim,
-                                int64_t total_context);
+size_t latent_prefill_workspace(int num_seqs, int num_heads, int head_dim, int64_t total_context);
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t stream);
 cudaError_t launch_latent_plan(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);
 cudaError_t launch_latent_expand(const LatentPrefillParams& p, const LatentExpanded& x, cudaStream_t stream);

@@ -232,21 +232,12 @@ __device__ __forceinline__ float row_max(uint32_t s_at, int nvis) {
   return fmaxf(m0, m1);
 }
 
-// 16 outputs of a row, times inv, in whole 32-byte sectors
+// 16 outputs of a row, times inv, in a whole 32-byte sector
 __device__ __forceinline__ void store_out(const LatentPrefillParams& p, int64_t at, const uint32_t (&v)[16], float inv) {
   uint32_t h[8];
-  if (p.out_bf16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-    fp4::store32(static_cast<__nv_bfloat16*>(p.out) + at, h);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = __float_as_uint(__uint_as_float(v[8 * q + e]) * inv);
-      fp4::store32(static_cast<float*>(p.out) + at + 8 * q, h);
-    }
-  }
+  for (int e = 0; e < 8; ++e) h[e] = pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+  fp4::store32(static_cast<__nv_bfloat16*>(p.out) + at, h);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -630,7 +621,7 @@ int64_t parts_bytes(int64_t ctas) { return ctas * 2 * kPair * (128 + 2) * 4; }
 
 }  // namespace latent_prefill_detail
 
-size_t latent_prefill_workspace(int num_seqs, int num_heads, int, int, int head_dim, int64_t total_context) {
+size_t latent_prefill_workspace(int num_seqs, int num_heads, int head_dim, int64_t total_context) {
   using namespace latent_prefill_detail;
   const int64_t sms = device_sm_count(), rows = rows_of(num_seqs, total_context);
   // tiles and places before the sequences | counters | parts | position parts | keys | values.  Room for an even number
