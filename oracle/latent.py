@@ -7,6 +7,7 @@ fp32 2^-24, and tensor cores may cut an fp32 sum instead of rounding it, 2^-23.
 import numpy as np
 
 CUT = 2.0 ** -23   # one fp32 addition
+F32 = 2.0 ** -24   # one rounding to fp32
 BF16 = 2.0 ** -8   # one rounding to bf16
 TWO = 2.0 ** -16   # a value in two bf16 parts: the second rounds what the first left
 EXP = 2.0 ** -20   # the exponential, the logarithm and the products around them
@@ -77,21 +78,25 @@ def to_bf16(x):
     return np.ldexp(np.rint(m * 256.0), e - 8)
 
 
-def expanded(c, w, two=False):
+def expanded(c, w, two=False, f32=False):
     """c [T, L] by w [D, L]: bf16 values [T, D], and by how much a kernel's may
     differ: a whole step where fp32 arithmetic may round to the other side.
-    two: the values themselves, and what two bf16 parts leave."""
+    f32: the values themselves, and what fp32 sums leave; two: a wider bound, with
+    room for a second part of 8 bits."""
     x = c @ w.T
     slack = (c.shape[1] + 4) * CUT * (np.abs(c) @ np.abs(w).T)
+    if f32:
+        return x, slack
     if two:
         return x, slack + TWO * (np.abs(x) + slack)
     r = to_bf16(x)
     return r, np.maximum(np.abs(to_bf16(x + slack) - r), np.abs(to_bf16(x - slack) - r))
 
 
-def prefill(q, cache, w_k, w_v, cu, start, tables, scale, two=False):
-    """q [T, H, head + rope] -> (out [T, H, head], bound); two: keys, values and
-    probabilities in two bf16 parts instead of one."""
+def prefill(q, cache, w_k, w_v, cu, start, tables, scale, two=False, f32=False):
+    """q [T, H, head + rope] -> (out [T, H, head], bound); keys, values and
+    probabilities rounded to bf16, or (f32) to nothing below fp32; two: as f32 with
+    the bound of 16 bits."""
     T, H, _ = q.shape
     head, latent = w_k.shape[1:]
     bs = cache.shape[1]
@@ -102,12 +107,12 @@ def prefill(q, cache, w_k, w_v, cu, start, tables, scale, two=False):
             continue
         x = rows(cache, tables[i], a + n, bs)
         for h in range(H):
-            k, dk = expanded(x[:, :latent], w_k[h].astype(np.float64), two)
-            v, dv = expanded(x[:, :latent], w_v[h].astype(np.float64), two)
+            k, dk = expanded(x[:, :latent], w_k[h].astype(np.float64), two, f32)
+            v, dv = expanded(x[:, :latent], w_v[h].astype(np.float64), two, f32)
             k = np.concatenate([k, x[:, latent:]], 1)
             dk = np.concatenate([dk, np.zeros_like(x[:, latent:])], 1)
             o, t = attend(q[cu[i]:cu[i + 1], h].astype(np.float64), k, v, scale, a + 1 + np.arange(n), dk, dv,
-                          TWO if two else BF16)
+                          F32 if f32 else TWO if two else BF16)
             out[cu[i]:cu[i + 1], h], tol[cu[i]:cu[i + 1], h] = o, t
     return out, tol
 

@@ -1,12 +1,13 @@
-"""Decode over the latent cache with query rows that are not finite, or that
-nobody has: every other row is what the 64-bit definition gives."""
+"""Query rows that are not finite, or that nobody has, over the latent cache (and in
+the weights): every other row is what the 64-bit definition gives."""
 import numpy as np
 import pytest
 import torch
 
-from latent_case import LATENT, ROW, check, dev, dev16
+from latent_case import LATENT, ROW, check, dev16
 from oracle import latent as O
-from test_gpu_latent import decode_case, run_decode
+from test_gpu_evict import run_weights, weights_case
+from test_gpu_latent import decode_case, prefill_case, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,36 @@ def test_values_and_queries_that_are_not_finite_together(ops, H, Q):
             keep = lambda x: x[:, :-1].reshape(3, -1, LATENT)[:, 1:]
             check(*(keep(x) for x in (out, ref, tol)), dt == torch.bfloat16)
             assert not torch.isfinite(out[:, -1]).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_prefill_beside_a_query_that_is_not_finite(ops, value, dt):
+    rng = np.random.default_rng(21)
+    chunks, H = [(100, 200), (0, 130), (900, 3)], 3
+    lens, tables, cache, cu, q, w_k, w_v = prefill_case(rng, chunks, 16, H)
+    start = [s for s, _ in chunks]
+    x = q.f32.copy()
+    bad = [(0, 0), (130, 2), (200, 1), (331, 0)]
+    for t, h in bad:
+        x[t, h] = value
+    ref, tol = O.prefill(q.f32, cache.f32, w_k.f32, w_v.f32, cu, start, tables, 0.07, f32=dt == torch.float32)
+    out = run_prefill(ops, type(q).from_f32(x, "bf16"), dev16(cache), w_k, w_v, cu, start, tables, 16, 0.07, 200, max(lens), sum(lens), dt)
+    keep = np.ones(x.shape[:2], bool)
+    for t, h in bad:
+        assert torch.isnan(out[t, h]).all()
+        keep[t, h] = False
+    check(out[torch.from_numpy(keep).cuda()], ref[keep], tol[keep], dt == torch.bfloat16)
+
+
+@pytest.mark.parametrize("W,H,hkv,d", [(1, 8, 2, 128), (40, 8, 2, 64), (3, 16, 1, ROW), (12, 4, 2, 256), (30, 8, 2, 128)])
+def test_weights_beside_queries_before_the_first_token(ops, W, H, hkv, d):
+    """Rows at positions below zero add nothing, whatever their queries hold."""
+    rng = np.random.default_rng(W)
+    lens = [max(1, W // 2), 300, 0, 1]
+    tables, k, q, before = weights_case(rng, lens, 16, W, H, hkv, d)
+    x = q.f32.copy()
+    for i, n in enumerate(lens):
+        x[i, : max(0, W - n)] = np.nan
+    ref, tol = O.weights(before, q.f32, k.f32, tables, lens, 0.1)
+    check(run_weights(ops, before, type(q).from_f32(x, "bf16"), dev16(k), tables, lens, 16, 0.1), ref, tol, False)
