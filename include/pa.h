@@ -586,8 +586,9 @@ pa_status pa_compact_tokens_latent(void* cache, int64_t cache_layer_stride, int3
  * context_lens[i] - q_len + j (the q_len tokens are in the cache already):
  *   s[t]         = scale * q[i][j][h] . row_t,   t <= that position
  *   out[i][j][h] = sum_t softmax(s)[t] * row_t[0 : latent_dim]
- * and 0 where there is no t (empty sequences; positions below 0).  Rows behind
- * the context are never used, whatever they hold.
+ * and 0 where there is no t (empty sequences; positions below 0), whatever their
+ * queries hold.  Rows behind the context are never used, and a value that is not
+ * finite, cached or in a query, changes no output whose sum it is not part of.
  *   q    device, bf16 [num_seqs][q_len][num_heads][latent_dim + rope_dim], 16-byte aligned
  *   out  device, [num_seqs][q_len][num_heads][latent_dim] of out_dtype, 32-byte aligned
  *   num_heads 1 to 128, q_len any; scale any finite number.
@@ -613,7 +614,9 @@ pa_status pa_decode_latent(void* out, pa_dtype out_dtype, const void* q, int32_t
  *   k[h][t] = (w_k[h] c_t, r_t)     v[h][t] = w_v[h] c_t
  * and the chunk's queries attend to them.  bf16 outputs: keys, values and
  * probabilities are rounded to bf16, on the tensor cores; fp32 outputs: they stay
- * in fp32, on the CUDA cores (about 30 times as slow).
+ * in fp32, on the CUDA cores (about 30 times as slow).  A token whose value v[h][t]
+ * is not finite in some dim, in bf16 for bf16 outputs, makes all head_dim outputs of
+ * head h NaN for the queries that see it; others take nothing of it.
  * Chunk i is q[cu_q[i] .. cu_q[i+1]) at positions q_start[i] + 0, 1, ..., whose
  * rows are in the cache already; query j sees the positions up to its own.
  *   q          device, bf16 [num_tokens][num_heads][head_dim + rope_dim], 16-byte aligned

@@ -13,9 +13,16 @@
 //
 // Measured: a decode step of 256 sequences, 32 q / 8 kv heads (448 MB of keys) 96 us,
 // of them the scores 78 (5.8 TB/s, 85% of a plain copy), the sums 6, the tokens 12;
-// a window of 32 queries over 4 x 9000 to 16384 tokens 64 us (the exponentials of
-// 128 rows a token bound both times that the scores are formed; with four warps
-// for them in the place of eight, and eight in that of sixteen, 74; stored 132); a step of 128 heads over 44 MB of latent rows 33 us.
+// a window of 32 queries over 4 x 9000 to 16384 tokens 64 us, 29 and 33 of them the
+// two times that the scores are formed.  No unit bounds those (special functions 28
+// and 25% busy, issue slots 49 and 37%, tensor pipe 21 and 19%, memory 52 and 46%):
+// a tile's chain does, product, tensor-memory load, maximum, exponentials, with two
+// tiles in it (half of the warps for the scores: 74; stored scores: 132).  A step of
+// 128 heads over 44 MB of latent rows 33 us, 21 of them the scores: 147 KB of
+// queries leave room for two tiles of 32 tokens, whose loads, products and scores
+// hardly overlap (special functions 4%, memory 26%); the rest is the two kernels
+// behind.  Windows of many rows over latent rows or heads of 256 store all scores:
+// 32 queries of 128 heads over 4 x 16384 latent rows 1.2 ms, a sequence a launch.
 //
 // Step 1: a CTA walks an equal run of units (token tile of a sequence, kv head and
 // row tile).  The rows of a tile are the heads of a kv head's group, query after
