@@ -20,7 +20,10 @@
 // shared memory holds four tiles of K and V.
 //
 // fp32 outputs take the probabilities in two bf16 parts, P and what its
-// rounding left (2^-17 in all); bf16 outputs take one (2^-8, as the output).
+// rounding left (2^-16 in all); bf16 outputs take one (2^-8, as the output): off by
+// 0.0020 relative against 64 bits, where one rounding of the output gives 0.0017.
+// Two parts would give that, for 13% of the time (the fp32 form takes 79.5 us where
+// this one takes 70, batch of 256, and 90 where it takes 79.5, 128 heads).
 //
 // The work is cut into equal runs of tiles, one for each cluster, across the
 // borders of sequences; a cluster that takes part of an item leaves its rows

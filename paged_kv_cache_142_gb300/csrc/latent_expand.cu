@@ -1,8 +1,12 @@
 // Keys and values of every head from the latent rows:
 //   K[h][t] = w_k[h] c_t,   V[h][t] = w_v[h] c_t,   D[128 x 256] = C[128 x 512] W[h]^T
 // for 128-token tiles of the contexts, and the position parts of the rows packed
-// beside them.  Rounded to bf16 (the products that follow take bf16), or left in
-// fp32 where the outputs are.  Rows behind a context are zeros.  A token whose
+// beside them.  Rounded to bf16 (the products that follow take bf16; 2^-8, as the
+// output: a row that sees few keys is then a value rounded twice, 0.0027 relative
+// against 64 bits with its probabilities', where one rounding gives 0.0017, and over
+// a long history 0.0018; a second part of the values would be two pieces of a step
+// more beside five and 128 multiplications beside 320), or left in fp32 where the
+// outputs are.  Rows behind a context are zeros.  A token whose
 // value is not finite gets a value of zero and a key of NaN: whoever sees it puts
 // out NaN, and 0 * NaN does not reach the rows that do not.
 //
