@@ -52,7 +52,7 @@ def test_prefill_workspace_grows(lib, argument):
 
 
 def test_a_prompt_windows_workspace_serves_the_steps_behind_it(lib):
-    """The calls of the finding: a window of 14 under one of 15, 8192 tokens under 16384."""
+    """A window of 14 under one of 15, which stores no scores; 8192 tokens under 16384, of which fewer sequences fit a launch."""
     size = lib.pa_accumulate_weights_workspace_size
     assert size(8, 14, 32, 8, 128, 16, 16384) <= size(8, 15, 32, 8, 128, 16, 16384) <= size(8, 32, 32, 8, 128, 16, 16384)
     assert size(4, 32, 128, 1, 576, 16, 8192) <= size(4, 32, 128, 1, 576, 16, 16384)
